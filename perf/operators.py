@@ -51,33 +51,33 @@ def _tables(name, **kw):
 def listed():
     return [
         # One decode step of a mid-sized batch: a token for every sequence.
-        _tables("tables: decode step, 64", seqs=64, ctx=4096),
+        _tables("tables decode 64", seqs=64, ctx=4096),
         # Continuous batching: decodes, prompt chunks, requests that leave and
         # requests that start behind a shared prefix, in one step.
-        _tables("tables: mixed step, 517", seqs=517, ctx=8192, chunk=700, prefill=0.12, leave=0.05, prefix_blocks=64),
+        _tables("tables mixed 517", seqs=517, ctx=8192, chunk=700, prefill=0.12, leave=0.05, prefix_blocks=64),
         # The largest: thousands of sequences, half a million new tokens.
-        _tables("tables: prompt step, 4096", seqs=4096, ctx=8192, chunk=1024, prefill=0.125, leave=0.03,
+        _tables("tables prompt 4096", seqs=4096, ctx=8192, chunk=1024, prefill=0.125, leave=0.03,
                 prefix_blocks=16),
         # A few chat requests behind a short system prompt: latency.
-        _prefix("prefix: 5 seqs on 1k", seqs=5, prefix=1024, own_lo=1, own_hi=300),
+        _prefix("prefix 5 on 1k", seqs=5, prefix=1024, own_lo=1, own_hi=300),
         # A serving batch behind a long system prompt.
-        _prefix("prefix: 64 seqs on 4k", seqs=64, prefix=4096, own_lo=16, own_hi=1024),
+        _prefix("prefix 64 on 4k", seqs=64, prefix=4096, own_lo=16, own_hi=1024),
         # Verification of 4 drafted tokens behind a document that few requests share.
-        _prefix("prefix: 9 seqs x 4 on 32k", seqs=9, queries=4, heads=64, kv_heads=8, prefix=32768, own_lo=5,
+        _prefix("prefix 9x4 on 32k", seqs=9, queries=4, heads=64, kv_heads=8, prefix=32768, own_lo=5,
                 own_hi=777, block=32),
         # The largest: many samples of one long prompt.
-        _prefix("prefix: 256 seqs on 16k", seqs=256, prefix=16384, own_lo=1, own_hi=2048),
+        _prefix("prefix 256 on 16k", seqs=256, prefix=16384, own_lo=1, own_hi=2048),
         # The smallest batch in 32 bits: one short sequence, capped scores.
-        _mod("mod: f32 cap, 1 seq", dtype="f32", heads=8, kv_heads=8, head=64, ctx_lo=200, ctx_hi=200, cap=30.0),
+        _mod("mod f32 cap 1", dtype="f32", heads=8, kv_heads=8, head=64, ctx_lo=200, ctx_hi=200, cap=30.0),
         # Capped scores with a sliding window, the ordinary serving batch.
-        _mod("mod: cap+window, 64", seqs=64, ctx_lo=512, ctx_hi=8192, cap=50.0, window=4096),
+        _mod("mod cap window 64", seqs=64, ctx_lo=512, ctx_hi=8192, cap=50.0, window=4096),
         # Distance bias over long contexts, one KV head per query head.
-        _mod("mod: alibi, 4 x 32k", seqs=4, heads=16, kv_heads=16, ctx_lo=30000, ctx_hi=32768, alibi=True),
+        _mod("mod alibi 4 on 32k", seqs=4, heads=16, kv_heads=16, ctx_lo=30000, ctx_hi=32768, alibi=True),
         # Drafted tokens verified over an FP8 pool: cap, window and 128 tokens kept in sight.
-        _mod("mod: fp8 verify, 48", dtype="fp8", seqs=48, queries=4, ctx_lo=300, ctx_hi=12000, cap=50.0, window=2048,
+        _mod("mod fp8 verify 48x4", dtype="fp8", seqs=48, queries=4, ctx_lo=300, ctx_hi=12000, cap=50.0, window=2048,
              prefix=128),
         # Packed documents with a bidirectional prefix, several queries each.
-        _mod("mod: documents, 96 x 3", seqs=96, queries=3, heads=24, kv_heads=4, head=64, block=8, ctx_lo=40,
+        _mod("mod documents 96x3", seqs=96, queries=3, heads=24, kv_heads=4, head=64, block=8, ctx_lo=40,
              ctx_hi=5000, docs=True, prefix=700, alibi=True),
     ]
 
