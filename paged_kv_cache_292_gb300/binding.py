@@ -31,6 +31,8 @@ PA_DEVERR_BLOCK_ID = 1
 PA_DEVERR_CONTEXT_LEN = 2
 PA_DEVERR_SLOT = 4
 PA_DEVERR_TIMEOUT = 8
+PA_DEVERR_NO_BLOCKS = 16
+PA_TABLES_RELEASE = -1
 
 INCLUDE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
 HEADER = os.path.join(INCLUDE, "pagedattn.h")
@@ -106,6 +108,7 @@ _SIGS = {
     "pa_bm_free": (_I, [_P, _I]),
     "pa_bm_export": (_I, [_P, _P, _P]),
     "pa_copy_blocks": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I]),
+    "pa_tables_step": (_I, [_P] * 10 + [_I] * 6 + [_P, _P]),
     "pa_version": (_I, []),
     "pa_test_stall_copy": (_I, [ctypes.c_longlong, ctypes.c_uint]),
 }
@@ -522,3 +525,93 @@ def decode_fp8_multi_append(query, k_new, v_new, k_cache, v_cache, block_tables,
                                           _stream(stream), NB if check_block_ids else 0, _ptr(workspace), ws_bytes,
                                           num_ranges, _ptr(error_flag)))
     return out
+
+
+# ---- operators beyond plain decode ---------------------------------------------
+
+
+def _on_device(first, *ts):
+    """All tensors contiguous and on one CUDA device, which becomes the current one for the call."""
+    dev = first.device
+    for t in (first, *ts):
+        if t is not None and (t.device != dev or not t.is_cuda or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous CUDA tensors on one device")
+    return dev.index
+
+
+class _call_on:
+    """Make a device current for one library call (nothing to do when it is)."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _require_stream(stream, index):
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+        raise ValueError("the stream belongs to another device than the tensors")
+
+
+def _used_on(stream, *ts):
+    """Tensors made here for a call on another stream than the allocating one outlive that call."""
+    if isinstance(stream, torch.cuda.Stream):
+        for t in ts:
+            t.record_stream(stream)
+
+
+def _require_dtype(dtype, **ts):
+    for name, t in ts.items():
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def pa_tables_step(block_tables, context_lens_out, seq_starts, slot_mapping, free_blocks, free_count_out,
+                   context_lens, new_lens, free_count, prefix_table, num_prefix_blocks, num_seqs,
+                   max_blocks_per_seq, block_size, num_physical_blocks, max_tokens, stream=None, error_flag=None):
+    _check(load().pa_tables_step(_ptr(block_tables), _ptr(context_lens_out), _ptr(seq_starts), _ptr(slot_mapping),
+                                 _ptr(free_blocks), _ptr(free_count_out), _ptr(context_lens), _ptr(new_lens),
+                                 _ptr(free_count), _ptr(prefix_table), num_prefix_blocks, num_seqs,
+                                 max_blocks_per_seq, block_size, num_physical_blocks, max_tokens, _stream(stream),
+                                 _ptr(error_flag)))
+
+
+def tables_step(block_tables, context_lens, new_lens, free_blocks, free_count, block_size, slot_mapping, *,
+                prefix_table=None, context_lens_out=None, free_count_out=None, seq_starts=None, stream=None,
+                error_flag=None):
+    """One step's block tables and slots from the requests' lengths (as in ``pa_tables_step``).
+
+    ``block_tables[S, MB]``, ``free_blocks[NB]`` and ``slot_mapping[T]`` (int64) are written in place; returns
+    ``(context_lens_out[S], free_count_out[1], seq_starts[S + 1])``, which are not the inputs' buffers."""
+    index = _on_device(block_tables, context_lens, new_lens, free_blocks, free_count, slot_mapping, prefix_table,
+                       context_lens_out, free_count_out, seq_starts, error_flag)
+    _require_dtype(torch.int32, block_tables=block_tables, context_lens=context_lens, new_lens=new_lens,
+                   free_blocks=free_blocks, free_count=free_count, prefix_table=prefix_table,
+                   context_lens_out=context_lens_out, free_count_out=free_count_out, seq_starts=seq_starts,
+                   error_flag=error_flag)
+    _require_dtype(torch.int64, slot_mapping=slot_mapping)
+    S, MB = block_tables.shape
+    outs = (context_lens_out, free_count_out, seq_starts)
+    want = (S, 1, S + 1)
+    if context_lens.numel() != S or new_lens.numel() != S or free_count.numel() != 1:
+        raise ValueError("context_lens and new_lens must have one entry per table row, free_count one entry")
+    if any(o is not None and o.numel() != n for o, n in zip(outs, want)):
+        raise ValueError("context_lens_out, free_count_out and seq_starts must have S, 1 and S + 1 entries")
+    _require_stream(stream, index)
+    with _call_on(index):
+        made = tuple(context_lens.new_empty(n) if o is None else o for o, n in zip(outs, want))
+        _used_on(stream, *(m for m, o in zip(made, outs) if o is None))
+        outs = made
+        pa_tables_step(block_tables, outs[0], outs[2], slot_mapping, free_blocks, outs[1], context_lens, new_lens,
+                       free_count, prefix_table, 0 if prefix_table is None else prefix_table.numel(), S, MB,
+                       block_size, free_blocks.numel(), slot_mapping.numel(), stream, error_flag)
+    return outs
