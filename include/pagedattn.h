@@ -222,6 +222,59 @@ int pa_decode_mq_append(void* out, const void* query, const void* k_new, const v
                         int32_t* error_flag);
 
 /*
+ * pa_decode_mod - decode with modified scores, one or several query tokens
+ * per sequence: the masks and biases models put on the same gather as
+ * pa_decode_mq.  With pos = context_lens[s] - num_queries + i the position of
+ * query i and c = context_lens[s], token t of sequence s has the score
+ *
+ *   score = softcap * tanh(scale * <q, k_t> / softcap) - alibi_slopes[h] * |pos - t|
+ *
+ * (softcap 0: scale * <q, k_t>; alibi_slopes NULL: no distance term), and query i
+ * sees it if 0 <= pos, t < c, t >= first_tokens[s], and
+ *
+ *   t < prefix_lens[s]   or   ( t <= pos  and  (window == 0 or pos - t < window) )
+ *
+ * softcap      >= 0, finite (tanh cap of the scores; 0: none)
+ * alibi_slopes [num_heads] float or NULL (any finite values)
+ * window       >= 0: tokens a query sees back, its own included (0: all)
+ * first_tokens [num_seqs] int32 or NULL: first token a sequence's queries see
+ *              (the start of their document); below 0 counts as 0
+ * prefix_lens  [num_seqs] int32 or NULL: tokens before this one are seen by every
+ *              query, also behind its position and its window (a
+ *              bidirectional prefix, or first tokens kept in sight); clamped
+ *              to [0, context_lens[s]]
+ * query, out   [num_seqs, num_queries, num_heads, head_size]
+ * A query that sees nothing gets a zero row.  Tokens no query of their sequence
+ * sees are not attended whatever the pool holds there (even NaN), and the table
+ * entries of blocks without a seen token may be stale: the blocks a window has
+ * left behind can be freed.  A token that some query of the sequence sees must
+ * be finite for the others too.
+ * Types: PA_F32 (num_queries == 1) or PA_BF16; (num_heads / num_kv_heads) *
+ * num_queries <= 32.  Scratch as in pa_decode_mq (pa_decode_mq_workspace_size),
+ * except that a caller's scratch may hold anything before a call, and that
+ * scratch of the library's own (workspace NULL) is refused while `stream` is
+ * being captured (PA_ERR_INVALID_ARG).  Two calls that may overlap in time need
+ * scratch of their own.  Other arguments as in pa_decode_mq.
+ *
+ * pa_decode_fp8_mod - the same over FP8 pools: keys and values as in
+ * pa_decode_fp8, query and out bf16.
+ */
+int pa_decode_mod(void* out, const void* query, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                  int num_queries, int num_heads, int num_kv_heads, int head_size, int block_size,
+                  int max_blocks_per_seq, float scale, float softcap, const float* alibi_slopes,
+                  int window, const int32_t* first_tokens, const int32_t* prefix_lens, void* stream,
+                  int dtype, int num_physical_blocks, void* workspace, size_t workspace_bytes,
+                  int num_ranges, int32_t* error_flag);
+int pa_decode_fp8_mod(void* out, const void* query, const void* k_cache, const void* v_cache,
+                      const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                      int num_queries, int num_heads, int num_kv_heads, int head_size, int block_size,
+                      int max_blocks_per_seq, float scale, float k_scale, float v_scale, float softcap,
+                      const float* alibi_slopes, int window, const int32_t* first_tokens,
+                      const int32_t* prefix_lens, void* stream, int num_physical_blocks, void* workspace,
+                      size_t workspace_bytes, int num_ranges, int32_t* error_flag);
+
+/*
  * pa_write_cache - scatter one step's new K/V rows into the paged pool
  * (the "reshape_and_cache" step).  For every token i with slot_mapping[i] >= 0:
  *   k_cache[slot / block_size, slot % block_size, :, :] = k_new[i, :, :]  (bit copy)

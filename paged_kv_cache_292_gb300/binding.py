@@ -108,6 +108,16 @@ _SIGS = {
     "pa_bm_free": (_I, [_P, _I]),
     "pa_bm_export": (_I, [_P, _P, _P]),
     "pa_copy_blocks": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I]),
+    "pa_decode_mod": (
+        _I,
+        [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, ctypes.c_float, _P, _I, _P, _P, _P, _I,
+         _I, _P, _SZ, _I, _P],
+    ),
+    "pa_decode_fp8_mod": (
+        _I,
+        [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+         ctypes.c_float, _P, _I, _P, _P, _P, _I, _P, _SZ, _I, _P],
+    ),
     "pa_tables_step": (_I, [_P] * 10 + [_I] * 6 + [_P, _P]),
     "pa_version": (_I, []),
     "pa_test_stall_copy": (_I, [ctypes.c_longlong, ctypes.c_uint]),
@@ -615,3 +625,90 @@ def tables_step(block_tables, context_lens, new_lens, free_blocks, free_count, b
                        free_count, prefix_table, 0 if prefix_table is None else prefix_table.numel(), S, MB,
                        block_size, free_blocks.numel(), slot_mapping.numel(), stream, error_flag)
     return outs
+
+
+def pa_decode_mod(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries, num_heads,
+                  num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, softcap=0.0, alibi_slopes=None,
+                  window=0, first_tokens=None, prefix_lens=None, stream=None, dtype=None, num_physical_blocks=0,
+                  workspace=None, workspace_bytes=0, num_ranges=0, error_flag=None):
+    dtype = dtype_code(query.dtype) if dtype is None else dtype
+    _check(load().pa_decode_mod(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                                _ptr(context_lens), num_seqs, num_queries, num_heads, num_kv_heads, head_size,
+                                block_size, max_blocks_per_seq, scale, softcap, _ptr(alibi_slopes), window,
+                                _ptr(first_tokens), _ptr(prefix_lens), _stream(stream), dtype, num_physical_blocks,
+                                _ptr(workspace), workspace_bytes, num_ranges, _ptr(error_flag)))
+
+
+def pa_decode_fp8_mod(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries, num_heads,
+                      num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, k_scale, v_scale, softcap=0.0,
+                      alibi_slopes=None, window=0, first_tokens=None, prefix_lens=None, stream=None,
+                      num_physical_blocks=0, workspace=None, workspace_bytes=0, num_ranges=0, error_flag=None):
+    _check(load().pa_decode_fp8_mod(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                                    _ptr(context_lens), num_seqs, num_queries, num_heads, num_kv_heads, head_size,
+                                    block_size, max_blocks_per_seq, scale, k_scale, v_scale, softcap,
+                                    _ptr(alibi_slopes), window, _ptr(first_tokens), _ptr(prefix_lens),
+                                    _stream(stream), num_physical_blocks, _ptr(workspace), workspace_bytes,
+                                    num_ranges, _ptr(error_flag)))
+
+
+def _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out):
+    """(S, Q, H, D, NB, bs, Hk, MB) of a step over paged pools, query [S, H, D] or [S, Q, H, D]."""
+    if query.dim() == 4:
+        S, Q, H, D = query.shape
+    else:
+        (S, H, D), Q = query.shape, 1
+    NB, bs, Hk, Dk = k_cache.shape
+    if Dk != D or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or block_tables.shape[0] != S or \
+            context_lens.numel() != S or (out is not None and out.shape != query.shape):
+        raise ValueError("shapes of query, pools, block_tables, context_lens and out do not go together")
+    _require_dtype(torch.int32, block_tables=block_tables, context_lens=context_lens)
+    return S, Q, H, D, NB, bs, Hk, block_tables.shape[1]
+
+
+def _decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, scales, out, stream, softcap,
+                alibi_slopes, window, first_tokens, prefix_lens, num_ranges, workspace, error_flag, check_block_ids):
+    index = _on_device(query, k_cache, v_cache, block_tables, context_lens, out, alibi_slopes, first_tokens,
+                       prefix_lens, workspace, error_flag)
+    S, Q, H, D, NB, bs, Hk, MB = _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out)
+    pool = torch.uint8 if scales else query.dtype
+    _require_dtype(pool, k_cache=k_cache, v_cache=v_cache)
+    _require_dtype(torch.bfloat16 if scales else query.dtype, query=query, out=out)
+    _require_dtype(torch.int32, first_tokens=first_tokens, prefix_lens=prefix_lens, error_flag=error_flag)
+    _require_dtype(torch.float32, alibi_slopes=alibi_slopes)
+    if (alibi_slopes is not None and alibi_slopes.numel() != H) or any(
+            t is not None and t.numel() != S for t in (first_tokens, prefix_lens)):
+        raise ValueError("alibi_slopes has one entry per query head, first_tokens and prefix_lens one per sequence")
+    _require_stream(stream, index)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    blocks = NB if check_block_ids else 0
+    with _call_on(index):
+        if out is None:
+            out = torch.empty_like(query)
+            _used_on(stream, out)
+        if scales:
+            pa_decode_fp8_mod(out, query, k_cache, v_cache, block_tables, context_lens, S, Q, H, Hk, D, bs, MB, scale,
+                              scales[0], scales[1], softcap, alibi_slopes, window, first_tokens, prefix_lens, stream,
+                              blocks, workspace, ws_bytes, num_ranges, error_flag)
+        else:
+            pa_decode_mod(out, query, k_cache, v_cache, block_tables, context_lens, S, Q, H, Hk, D, bs, MB, scale,
+                          softcap, alibi_slopes, window, first_tokens, prefix_lens, stream, None, blocks, workspace,
+                          ws_bytes, num_ranges, error_flag)
+    return out
+
+
+def decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, out=None, stream=None, *, softcap=0.0,
+               alibi_slopes=None, window=0, first_tokens=None, prefix_lens=None, num_ranges=0, workspace=None,
+               error_flag=None, check_block_ids=False):
+    """Decode with capped, biased and masked scores (as in ``pa_decode_mod``); query and out [S, H, D] or [S, Q, H, D]."""
+    return _decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, None, out, stream, softcap,
+                       alibi_slopes, window, first_tokens, prefix_lens, num_ranges, workspace, error_flag,
+                       check_block_ids)
+
+
+def decode_fp8_mod(query, k_cache, v_cache, block_tables, context_lens, scale, k_scale, v_scale, out=None,
+                   stream=None, *, softcap=0.0, alibi_slopes=None, window=0, first_tokens=None, prefix_lens=None,
+                   num_ranges=0, workspace=None, error_flag=None, check_block_ids=False):
+    """``decode_mod`` over uint8 E4M3 pools (as in ``pa_decode_fp8_mod``)."""
+    return _decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, (k_scale, v_scale), out, stream,
+                       softcap, alibi_slopes, window, first_tokens, prefix_lens, num_ranges, workspace, error_flag,
+                       check_block_ids)

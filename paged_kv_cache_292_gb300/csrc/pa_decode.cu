@@ -11,8 +11,10 @@
 #include <type_traits>
 
 #include "../../include/pagedattn.h"
+#include "pa_decode_impl.h"
 #include "pa_decode_kernel.cuh"
 #include "pa_internal.h"
+#include "pa_launch.cuh"
 #include "pa_schedule.h"
 
 namespace pa {
@@ -21,13 +23,6 @@ namespace pa {
 // Host side
 // ---------------------------------------------------------------------------
 namespace {
-
-struct Plan {
-  int Hg, HG, R, stages, q_slots, split;
-  uint32_t row_bytes, pitch, q_bytes, stage_bytes, smem;
-  uint32_t lines, box_rows, box_bytes;  // tensor-core paths (see DecodeParams)
-  size_t ws_ml, ws_o, ws_partials, ws_counters, ws_total;
-};
 
 // Scratch layout: partial (m, l) and O at the start, then the merge tickets
 // (num_seqs * num_kv_heads int32).  In a caller's buffer the tickets occupy
@@ -170,25 +165,6 @@ int validate(const void* out, const void* query, const void* k_cache, const void
   return PA_OK;
 }
 
-// Launch with programmatic stream serialisation: the kernel may become
-// resident while its predecessor on the stream finishes; it calls
-// griddepcontrol.wait before touching anything that predecessor produces.
-template <typename Kernel, typename Params>
-cudaError_t launch_pdl(Kernel kern, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                       const Params& prm) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, prm);
-}
-
 // The pools seen by the tensor copies: 4-D byte tensors (byte within a
 // 128-byte chunk, chunk within a head group's row, head group, token row)
 // with strides (1, 128, group row bytes, token row bytes).  A box is
@@ -273,28 +249,6 @@ int make_tensor_maps(DecodeParams* prm, const Plan& pl, int num_kv_heads, int he
   return PA_OK;
 }
 
-template <typename T, int D, int GMAX, int QMODE = 0, bool KV8 = false>
-int launch_typed(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream) {
-  // Devices whose shared-memory limit is already raised for this kernel
-  // (setting it again is harmless, so concurrent first calls may both set it).
-  constexpr int kTrackedDevices = 64;
-  static std::atomic<bool> configured[kTrackedDevices];
-  auto kern = pa_decode_kernel<T, D, GMAX, QMODE, KV8>;
-  if (dev < 0 || dev >= kTrackedDevices || !configured[dev].load(std::memory_order_acquire)) {
-    DeviceInfo info{};
-    int rc = current_device_info(&info);
-    if (rc != PA_OK) return rc;
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, info.max_smem_optin);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode smem)");
-    if (dev >= 0 && dev < kTrackedDevices) configured[dev].store(true, std::memory_order_release);
-  }
-  cudaError_t e =
-      launch_pdl(kern, dim3(pl.R * pl.HG), dim3(32 * (pl.Hg * pl.split + kProducers)), pl.smem, stream, prm);
-  if (e != cudaSuccess) return cuda_fail(e, "launch pa_decode_kernel");
-  return PA_OK;
-}
-
 template <typename T, int D>
 int launch_dtype(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream,
                  bool kv_fp8 = false) {
@@ -329,9 +283,9 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
                   int num_queries, int num_heads, int num_kv_heads, int head_size, int block_size,
                   int max_blocks_per_seq, float scale, void* stream, int dtype,
                   int num_physical_blocks, void* workspace, size_t workspace_bytes, int num_ranges,
-                  int32_t* error_flag, bool kv_fp8 = false, float k_scale = 1.f,
-                  float v_scale = 1.f, const void* k_new = nullptr, const void* v_new = nullptr,
-                  ScratchProvider fixed_scratch = nullptr) {
+                  int32_t* error_flag, bool kv_fp8, float k_scale,
+                  float v_scale, const void* k_new, const void* v_new,
+                  ScratchProvider fixed_scratch, const DecodeExtras* extras) {
   clear_error();
   if (k_new != nullptr || v_new != nullptr) {
     if (k_new == nullptr || v_new == nullptr)
@@ -364,13 +318,17 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
                  num_queries, elt, block_size);
   if (rc != PA_OK) return rc;
   int32_t* counters = nullptr;
-  const bool clear_tickets = workspace == nullptr && fixed_scratch != nullptr;
-  if (clear_tickets) {
+  bool clear_tickets = workspace == nullptr && fixed_scratch != nullptr;
+  if (extras != nullptr && workspace == nullptr) {
+    rc = kept_scratch(pl.ws_partials, pl.ws_counters, stream, &workspace, &counters);
+    if (rc != PA_OK) return rc;
+  } else if (clear_tickets) {
     rc = fixed_scratch(pl.ws_total, &workspace);
     if (rc != PA_OK) return rc;
     workspace_bytes = pl.ws_total;
   }
-  if (workspace == nullptr) {
+  if (counters != nullptr) {
+  } else if (workspace == nullptr) {
     rc = library_workspace(pl.ws_partials, &workspace);
     if (rc != PA_OK) return rc;
     rc = library_counters(pl.ws_counters, &counters);
@@ -383,6 +341,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
     const size_t cnt_bytes = sizeof(int32_t) * (size_t)num_seqs * num_kv_heads;
     counters = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) +
                                           ((workspace_bytes - cnt_bytes) & ~(size_t)255));
+    if (extras != nullptr) clear_tickets = true;  // the caller's scratch may hold anything
   }
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   DecodeParams prm{};
@@ -427,6 +386,22 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   prm.k_scale = k_scale;
   prm.k_new = k_new;
   prm.v_new = v_new;
+  prm.window = kNoWindow;
+  if (extras != nullptr && extras->walk == kWalkMod) {
+    const double log2e = 1.4426950408889634;
+    const double per_cap = extras->softcap > 0.f ? (double)scale * k_scale / extras->softcap : 0.0;
+    // The tensor-core consumers take tanh from a power of two, fp32 calls tanhf.
+    prm.cap_in = (float)(dtype == PA_F32 ? per_cap : 2.0 * log2e * per_cap);
+    prm.cap_out = (float)(extras->softcap * log2e);
+    prm.slopes = extras->alibi_slopes;
+    prm.first_tokens = extras->first_tokens;
+    prm.prefix_lens = extras->prefix_lens;
+    if (extras->window > 0 && extras->window < kNoWindow) prm.window = extras->window;
+  } else if (extras != nullptr) {
+    prm.prefix_tokens = extras->prefix_tokens;
+    prm.rest_ml = extras->rest_ml;
+    prm.rest_o = extras->rest_o;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (clear_tickets) {
     const cudaError_t e =
@@ -444,6 +419,9 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
     if (rc != PA_OK) return rc;
     prm.k_new = prm.v_new = nullptr;
   }
+  if (extras != nullptr)
+    return extras->walk == kWalkMod ? launch_mod(prm, pl, dev.device, st, head_size, dtype == PA_F32, kv_fp8)
+                                    : launch_rest(prm, pl, dev.device, st, head_size);
   if (dtype == PA_BF16) {
     return head_size == 64 ? launch_dtype<__nv_bfloat16, 64>(prm, pl, dev.device, st, kv_fp8)
                            : launch_dtype<__nv_bfloat16, 128>(prm, pl, dev.device, st, kv_fp8);

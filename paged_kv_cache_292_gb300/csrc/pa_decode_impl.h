@@ -1,0 +1,35 @@
+// The general decode call behind the C entry points of several translation units.
+#pragma once
+
+#include "pa_internal.h"
+
+namespace pa {
+
+// What a call asks of the decode kernel beyond the plain step.
+struct DecodeExtras {
+  int walk;  // kWalkMod or kWalkRest
+  // kWalkMod: modified scores
+  float softcap = 0.f;
+  const float* alibi_slopes = nullptr;
+  int window = 0;
+  const int32_t* first_tokens = nullptr;
+  const int32_t* prefix_lens = nullptr;
+  // kWalkRest: the tokens behind a shared prefix, left as (m, l, O) rows
+  int prefix_tokens = 0;
+  float* rest_ml = nullptr;
+  float* rest_o = nullptr;
+};
+
+int decode_impl_q(void* out, const void* query, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                  int num_queries, int num_heads, int num_kv_heads, int head_size, int block_size,
+                  int max_blocks_per_seq, float scale, void* stream, int dtype,
+                  int num_physical_blocks, void* workspace, size_t workspace_bytes, int num_ranges,
+                  int32_t* error_flag, bool kv_fp8 = false, float k_scale = 1.f,
+                  float v_scale = 1.f, const void* k_new = nullptr, const void* v_new = nullptr,
+                  ScratchProvider fixed_scratch = nullptr, const DecodeExtras* extras = nullptr);
+
+size_t decode_workspace_size_q(int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                               int num_ranges, int num_queries);
+
+}  // namespace pa

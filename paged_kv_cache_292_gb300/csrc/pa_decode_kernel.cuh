@@ -80,16 +80,25 @@ constexpr int kMaxRanges = 4096;    // bounds the partial-result scratch
 
 enum : int { kSegBegin = 1, kSegEnd = 2 };
 
+// Which tiles of a sequence a kernel walks, and what becomes of its rows.
+enum : int {
+  kWalkAll = 0,   // every token, plain scores, output rows
+  kWalkMod = 1,   // the tiles some query sees, modified scores, output rows
+  kWalkRest = 2,  // the tokens behind a shared prefix, plain scores, (m, l, O) rows
+};
+constexpr int kNoWindow = 1 << 30;  // longer than any context
+
 struct StageMeta {
   int seq;     // sequence index
   int tok0;    // first token of the tile within the sequence
-  int nvalid;  // valid tokens in the tile (1..16)
+  int nvalid;  // valid tokens in the tile (1..16); kWalkMod: bit mask of the rows some query sees
   int flags;   // kSegBegin | kSegEnd | (output slot + 1) << 2 | (slot of range r0) << 4
   int r0, r1;  // first and last range touching the sequence (cut sequences only)
   int ctx;     // the sequence's context length (causal limits of several queries)
   int newfirst;  // appending calls: first tile row holding one of the step's new
                  // tokens (rows newfirst .. nvalid-1; their pool rows are in the
-                 // stage's row list); -1 when the tile holds none
+                 // stage's row list); -1 when the tile holds none.  kWalkMod:
+                 // tokens before this one are seen by every query
 };
 
 struct DecodeParams {
@@ -125,6 +134,21 @@ struct DecodeParams {
   uint32_t box_rows;   // token rows per tensor copy: gcd(block_size, 16)
   uint32_t box_bytes;  // bytes one tensor copy lands (box_rows * lines * 128)
   float scale_log2;    // scale * log2(e)
+  // Modified scores (kWalkMod): s = cap * tanh(scale * q.k / cap), then
+  // - slope * |distance|; visibility by window, first token and prefix.
+  float cap_in;   // tensor-core paths: 2 * log2(e) * scale / cap, the base-2 exponent of
+                  // tanh's e^2x; fp32: scale / cap
+  float cap_out;  // cap * log2(e); 0: scores are not capped
+  const float* slopes;          // [num_heads] or nullptr
+  const int32_t* first_tokens;  // [num_seqs] or nullptr
+  const int32_t* prefix_lens;   // [num_seqs] or nullptr
+  int window;                   // tokens a query sees back from its own position (kNoWindow: all)
+  // Rest of a shared prefix (kWalkRest): sequences of at least
+  // prefix_tokens + num_queries - 1 tokens are walked from prefix_tokens on, the others
+  // whole; (m, l) and un-normalised O of every row go to rest_ml / rest_o.
+  int prefix_tokens;
+  float* rest_ml;  // [num_seqs * num_queries * num_heads][2]
+  float* rest_o;   // [num_seqs * num_queries * num_heads][D]
   unsigned long long wait_limit_ns;  // bound of every pipeline wait
   long long stall_tile;  // tests of the bounded waits: flattened tile whose copies are withheld (-1: none)
 };
@@ -168,6 +192,46 @@ __device__ __forceinline__ int clamp_context(const DecodeParams& p, int s, bool 
   }
   return c;
 }
+
+// The tiles one sequence contributes.  kWalkMod: `nh` tiles from token h0 (the
+// prefix every query sees), then the tiles from token t0 (what the window
+// leaves, from the first query's); kWalkRest: tiles from token t0.  A token is
+// seen by some query if it is in [first, pre) or in [max(first, lo), c).
+template <int WALK>
+struct SeqWalk {
+  int c = 0, n = 0;
+  int nh = 0, h0 = 0, t0 = 0, first = 0, pre = 0, lo = 0;
+
+  __device__ __forceinline__ SeqWalk() {}
+  __device__ __forceinline__ SeqWalk(const DecodeParams& p, int s, bool report_it) {
+    c = clamp_context(p, s, report_it);
+    if constexpr (WALK == kWalkAll) {
+      n = tiles_of(c);
+    } else if constexpr (WALK == kWalkRest) {
+      t0 = c >= p.prefix_tokens + p.num_queries - 1 ? p.prefix_tokens : 0;
+      n = tiles_of(c - t0);
+    } else {
+      first = p.first_tokens != nullptr ? max(0, __ldg(p.first_tokens + s)) : 0;
+      pre = p.prefix_lens != nullptr ? max(0, min(c, __ldg(p.prefix_lens + s))) : 0;
+      // The first query that exists sees back to its position - window + 1.
+      lo = max(max(first, pre), max(0, c - p.num_queries) - p.window + 1);
+      if (first < c) {
+        h0 = first & ~(kTile - 1);
+        nh = pre > first ? tiles_of(pre - h0) : 0;
+        t0 = max(lo & ~(kTile - 1), nh > 0 ? h0 + nh * kTile : 0);
+        n = nh + (c > t0 ? tiles_of(c - t0) : 0);
+      }
+    }
+  }
+  __device__ __forceinline__ int token(int j) const {
+    if constexpr (WALK == kWalkAll) return j * kTile;
+    if constexpr (WALK == kWalkRest) return t0 + j * kTile;
+    return j < nh ? h0 + j * kTile : t0 + (j - nh) * kTile;
+  }
+  __device__ __forceinline__ bool sees(int tok) const {  // kWalkMod
+    return tok < c && tok >= first && (tok < pre || tok >= lo);
+  }
+};
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
@@ -214,6 +278,82 @@ struct RowPtr {
   }
   __device__ __forceinline__ uint32_t at(int j) const { return a[j >> 2] ^ ((uint32_t)(j & 3) << 5); }
 };
+
+// Modified scores of one 16-token tile.  A lane holds rows r0 and r0 + 8 of
+// columns a and b, as (row r0: a, b; row r0 + 8: a, b).
+struct ModTile {
+  uint32_t vis;  // rows some query of the sequence sees
+  int tok0, ctx;
+  int pre;  // tokens before this one are seen by every query
+};
+
+struct ModCols {
+  int qa = 0, qb = 0;        // query index of each column (padding columns: any)
+  float sa = 0.f, sb = 0.f;  // log2(e) * slope of each column's head
+
+  // n: column a of (query, head) columns n = query * G + head, column b the next.
+  __device__ __forceinline__ void setup(const DecodeParams& p, int kv_head, int n) {
+    const int G = p.group, Q = p.num_queries;
+    qa = n < G * Q ? n / G : 0;
+    qb = n + 1 < G * Q ? (n + 1) / G : 0;
+    if (p.slopes != nullptr) {
+      if (n < G * Q) sa = 1.4426950408889634f * __ldg(p.slopes + kv_head * G + n % G);
+      if (n + 1 < G * Q) sb = 1.4426950408889634f * __ldg(p.slopes + kv_head * G + (n + 1) % G);
+    }
+  }
+};
+
+// x -> scores in log2 units.  The cap's tanh(y) = 1 - 2 / (1 + e^2y) runs on the
+// SFU (one 2^x, one reciprocal): its absolute error of about 2^-23 times the cap
+// is far below the rounding of the bf16 output.
+__device__ __forceinline__ float mod_cap(const DecodeParams& p, float x) {
+  const float e = ex2_ftz(x * p.cap_in);
+  return p.cap_out - 2.f * p.cap_out * rcp_ftz(1.f + e);
+}
+
+__device__ __forceinline__ void mod_scores(const DecodeParams& p, const ModCols& mc, const ModTile& t, int r0,
+                                           float& s0, float& s1, float& s2, float& s3) {
+  if (p.cap_out != 0.f) {
+    s0 = mod_cap(p, s0);
+    s1 = mod_cap(p, s1);
+    s2 = mod_cap(p, s2);
+    s3 = mod_cap(p, s3);
+  } else {
+    s0 *= p.scale_log2;
+    s1 *= p.scale_log2;
+    s2 *= p.scale_log2;
+    s3 *= p.scale_log2;
+  }
+  const int base = t.ctx - p.num_queries, row = t.tok0 + r0;
+  if (p.slopes != nullptr) {
+    const float da = static_cast<float>(base + mc.qa - row), db = static_cast<float>(base + mc.qb - row);
+    s0 -= mc.sa * fabsf(da);
+    s1 -= mc.sb * fabsf(db);
+    s2 -= mc.sa * fabsf(da - 8.f);
+    s3 -= mc.sb * fabsf(db - 8.f);
+  }
+  // Do all queries see all rows?  (The same answer for the whole warp.)
+  const bool split = base < 0 || (t.tok0 + kTile > t.pre &&
+                                  (t.tok0 + kTile - 1 > base || t.tok0 <= t.ctx - 1 - p.window));
+  if (split) {
+    const int pa = base + mc.qa, pb = base + mc.qb;
+    const int la = pa - p.window, lb = pb - p.window;
+    const bool pre0 = row < t.pre, pre1 = row + 8 < t.pre;
+    if (pa < 0 || !(pre0 || (row <= pa && row > la))) s0 = -INFINITY;
+    if (pb < 0 || !(pre0 || (row <= pb && row > lb))) s1 = -INFINITY;
+    if (pa < 0 || !(pre1 || (row + 8 <= pa && row + 8 > la))) s2 = -INFINITY;
+    if (pb < 0 || !(pre1 || (row + 8 <= pb && row + 8 > lb))) s3 = -INFINITY;
+  }
+  if (t.vis != 0xffffu) {
+    if (!((t.vis >> r0) & 1u)) s0 = s1 = -INFINITY;
+    if (!((t.vis >> (r0 + 8)) & 1u)) s2 = s3 = -INFINITY;
+  }
+}
+
+// Halves of a V fragment register (tokens t2, t2 + 1) to keep.
+__device__ __forceinline__ uint32_t keep_pair(uint32_t vis, int t2) {
+  return ((vis >> t2) & 1u ? 0x0000ffffu : 0u) | ((vis >> (t2 + 1)) & 1u ? 0xffff0000u : 0u);
+}
 
 // bf16 tensor-core consumer.  Lane l owns query heads hA = 2*(l%4), hB = hA+1
 // (columns of the score fragment) and, per 16-wide slice mt of the head
@@ -326,7 +466,8 @@ struct MmaConsumer {
     }
   }
 
-  // slot < 0: final output; else partial slot of range r.
+  // slot < 0: final output (REST: the row's (m, l, O)); else partial slot of range r.
+  template <bool REST = false>
   __device__ __forceinline__ void finish(const DecodeParams& p, int seq, int kv_head, int slot,
                                          int r, int lane) {
     float la = l_a, lb = l_b;
@@ -338,7 +479,7 @@ struct MmaConsumer {
     const int G = p.group, H = p.num_heads;
     const int ha = 2 * (lane & 3), hb = ha + 1, d0 = lane >> 2;
     const int qa = kv_head * G + ha, qb_ = kv_head * G + hb;
-    if (slot < 0) {
+    if (!REST && slot < 0) {
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + (size_t)seq * H * D;
       const float ia = 1.f / la, ib = 1.f / lb;
 #pragma unroll
@@ -354,8 +495,9 @@ struct MmaConsumer {
         }
       }
     } else {
-      const size_t base = ((size_t)r * 2 + slot) * H;
-      float* po = p.part_o + base * D;
+      const bool whole = REST && slot < 0;
+      const size_t base = whole ? (size_t)seq * H : ((size_t)r * 2 + slot) * H;
+      float* po = (whole ? p.rest_o : p.part_o) + base * D;
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) {
         const int d = mt * 16 + d0;
@@ -369,7 +511,7 @@ struct MmaConsumer {
         }
       }
       if (d0 == 0) {
-        float* pm = p.part_ml + base * 2;
+        float* pm = (whole ? p.rest_ml : p.part_ml) + base * 2;
         if (ha < G) {
           pm[(size_t)qa * 2 + 0] = m_a;
           pm[(size_t)qa * 2 + 1] = la;
@@ -387,13 +529,16 @@ struct MmaConsumer {
 // The N extent of the score fragment holds (query, head) columns: column
 // n = qi * G + g for query qi < Q and group head g < G, NT tiles of 8 columns.
 // Query qi sits at position ctx - Q + qi and sees tokens up to that position.
-template <int D, int NT>
+// MOD: modified scores (mod_scores) instead of the causal mask alone; `mo` is
+// the tile's mask and position.
+template <int D, int NT, bool MOD = false>
 struct MmaConsumerMQ {
   static constexpr int KS = D / 16;
   uint32_t qb[NT][KS][2];
   float acc[NT][KS][4];
   float m_a[NT], m_b[NT], l_a[NT], l_b[NT];
   int col0 = 0;  // first (query, head) column this warp owns
+  ModCols mc;    // MOD
 
   // w: KV head within the CTA's group; col_base: first column of this warp.
   __device__ __forceinline__ void begin_segment(const unsigned char* qslot, int w, int G, int Q,
@@ -439,7 +584,8 @@ struct MmaConsumerMQ {
 
   __device__ __forceinline__ void tile(uint32_t k_half, uint32_t v_half, uint32_t lines, int uh,
                                        int nvalid, int tok0, int ctx, int G, int Q,
-                                       float scale_log2, int lane) {
+                                       float scale_log2, int lane, const DecodeParams* mod = nullptr,
+                                       const ModTile& mo = ModTile()) {
     // Scores accumulate in two independent chains (even / odd k-steps) that
     // are added at the end: with one 8-column tile per warp, a single chain
     // would serialise all KS MMAs.
@@ -466,21 +612,28 @@ struct MmaConsumerMQ {
     float alpha_a[NT], alpha_b[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float s0 = c[nt][0] * scale_log2, s1 = c[nt][1] * scale_log2;
-      float s2 = c[nt][2] * scale_log2, s3 = c[nt][3] * scale_log2;
-      if (r0 >= nvalid) s0 = s1 = -INFINITY;
-      if (r0 + 8 >= nvalid) s2 = s3 = -INFINITY;
-      // Causal limits matter only on tiles that reach the queries' own
-      // positions (ctx - Q ..); the test is the same for the whole warp.
-      if (tok0 + kTile > ctx - Q) {
-        const int na = col0 + nt * 8 + 2 * (lane & 3), nb = na + 1;
-        // Last visible position of each column's query (-1: padding column).
-        const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
-        const int lim_b = nb < G * Q ? ctx - Q + nb / G : -1;
-        if (t0 > lim_a) s0 = -INFINITY;
-        if (t0 > lim_b) s1 = -INFINITY;
-        if (t1 > lim_a) s2 = -INFINITY;
-        if (t1 > lim_b) s3 = -INFINITY;
+      float s0 = c[nt][0], s1 = c[nt][1], s2 = c[nt][2], s3 = c[nt][3];
+      if constexpr (MOD) {
+        mod_scores(*mod, mc, mo, r0, s0, s1, s2, s3);
+      } else {
+        s0 *= scale_log2;
+        s1 *= scale_log2;
+        s2 *= scale_log2;
+        s3 *= scale_log2;
+        if (r0 >= nvalid) s0 = s1 = -INFINITY;
+        if (r0 + 8 >= nvalid) s2 = s3 = -INFINITY;
+        // Causal limits matter only on tiles that reach the queries' own
+        // positions (ctx - Q ..); the test is the same for the whole warp.
+        if (tok0 + kTile > ctx - Q) {
+          const int na = col0 + nt * 8 + 2 * (lane & 3), nb = na + 1;
+          // Last visible position of each column's query (-1: padding column).
+          const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
+          const int lim_b = nb < G * Q ? ctx - Q + nb / G : -1;
+          if (t0 > lim_a) s0 = -INFINITY;
+          if (t0 > lim_b) s1 = -INFINITY;
+          if (t1 > lim_a) s2 = -INFINITY;
+          if (t1 > lim_b) s3 = -INFINITY;
+        }
       }
       float mx_a = fmaxf(s0, s2), mx_b = fmaxf(s1, s3);
 #pragma unroll
@@ -512,7 +665,12 @@ struct MmaConsumerMQ {
     const RowPtr<NC> vp(v_half, (lane & 7) + (lane >> 4) * 8, uh + ((lane >> 3) & 1), lines);
     const int t2 = 2 * (lane & 3);
     uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
-    if (nvalid < kTile) {
+    if constexpr (MOD) {
+      if (mo.vis != 0xffffu) {
+        keep_lo = keep_pair(mo.vis, t2);
+        keep_hi = keep_pair(mo.vis, t2 + 8);
+      }
+    } else if (nvalid < kTile) {
       keep_lo = (t2 < nvalid ? 0x0000ffffu : 0u) | (t2 + 1 < nvalid ? 0xffff0000u : 0u);
       keep_hi = (t2 + 8 < nvalid ? 0x0000ffffu : 0u) | (t2 + 9 < nvalid ? 0xffff0000u : 0u);
     }
@@ -552,7 +710,8 @@ struct MmaConsumerMQ {
   // columns are split over several warps, where it measured faster).
   __device__ __forceinline__ void tile_hoisted(uint32_t k_half, uint32_t v_half, uint32_t lines, int uh,
                                                int nvalid, int tok0, int ctx, int G, int Q,
-                                       float scale_log2, int lane) {
+                                               float scale_log2, int lane, const DecodeParams* mod = nullptr,
+                                               const ModTile& mo = ModTile()) {
     // All K fragments are loaded first, then the scores accumulate in four
     // independent chains (k-step mod 4) added at the end: with one 8-column
     // tile per warp a single chain would serialise all KS MMAs.  The V
@@ -592,21 +751,28 @@ struct MmaConsumerMQ {
     float alpha_a[NT], alpha_b[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float s0 = c[nt][0] * scale_log2, s1 = c[nt][1] * scale_log2;
-      float s2 = c[nt][2] * scale_log2, s3 = c[nt][3] * scale_log2;
-      if (r0 >= nvalid) s0 = s1 = -INFINITY;
-      if (r0 + 8 >= nvalid) s2 = s3 = -INFINITY;
-      // Causal limits matter only on tiles that reach the queries' own
-      // positions (ctx - Q ..); the test is the same for the whole warp.
-      if (tok0 + kTile > ctx - Q) {
-        const int na = col0 + nt * 8 + 2 * (lane & 3), nb = na + 1;
-        // Last visible position of each column's query (-1: padding column).
-        const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
-        const int lim_b = nb < G * Q ? ctx - Q + nb / G : -1;
-        if (t0 > lim_a) s0 = -INFINITY;
-        if (t0 > lim_b) s1 = -INFINITY;
-        if (t1 > lim_a) s2 = -INFINITY;
-        if (t1 > lim_b) s3 = -INFINITY;
+      float s0 = c[nt][0], s1 = c[nt][1], s2 = c[nt][2], s3 = c[nt][3];
+      if constexpr (MOD) {
+        mod_scores(*mod, mc, mo, r0, s0, s1, s2, s3);
+      } else {
+        s0 *= scale_log2;
+        s1 *= scale_log2;
+        s2 *= scale_log2;
+        s3 *= scale_log2;
+        if (r0 >= nvalid) s0 = s1 = -INFINITY;
+        if (r0 + 8 >= nvalid) s2 = s3 = -INFINITY;
+        // Causal limits matter only on tiles that reach the queries' own
+        // positions (ctx - Q ..); the test is the same for the whole warp.
+        if (tok0 + kTile > ctx - Q) {
+          const int na = col0 + nt * 8 + 2 * (lane & 3), nb = na + 1;
+          // Last visible position of each column's query (-1: padding column).
+          const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
+          const int lim_b = nb < G * Q ? ctx - Q + nb / G : -1;
+          if (t0 > lim_a) s0 = -INFINITY;
+          if (t0 > lim_b) s1 = -INFINITY;
+          if (t1 > lim_a) s2 = -INFINITY;
+          if (t1 > lim_b) s3 = -INFINITY;
+        }
       }
       float mx_a = fmaxf(s0, s2), mx_b = fmaxf(s1, s3);
 #pragma unroll
@@ -637,7 +803,12 @@ struct MmaConsumerMQ {
     }
     const int t2 = 2 * (lane & 3);
     uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
-    if (nvalid < kTile) {
+    if constexpr (MOD) {
+      if (mo.vis != 0xffffu) {
+        keep_lo = keep_pair(mo.vis, t2);
+        keep_hi = keep_pair(mo.vis, t2 + 8);
+      }
+    } else if (nvalid < kTile) {
       keep_lo = (t2 < nvalid ? 0x0000ffffu : 0u) | (t2 + 1 < nvalid ? 0xffff0000u : 0u);
       keep_hi = (t2 + 8 < nvalid ? 0x0000ffffu : 0u) | (t2 + 9 < nvalid ? 0xffff0000u : 0u);
     }
@@ -676,7 +847,8 @@ struct MmaConsumerMQ {
   // score chains interleave and one softmax update covers all 32 tokens.
   __device__ __forceinline__ void tile2(uint32_t k_half0, uint32_t v_half0, uint32_t k_half1, uint32_t v_half1,
                                         uint32_t lines, int uh, int nvalid1, int tok0, int ctx, int G, int Q,
-                                        float scale_log2, int lane) {
+                                        float scale_log2, int lane, const DecodeParams* mod = nullptr,
+                                        const ModTile& mo0 = ModTile(), const ModTile& mo1 = ModTile()) {
     const RowPtr<NC> kp0(k_half0, (lane & 7) + ((lane >> 3) & 1) * 8, uh + (lane >> 4), lines);
     const RowPtr<NC> kp1(k_half1, (lane & 7) + ((lane >> 3) & 1) * 8, uh + (lane >> 4), lines);
     float cc[2][2][NT][4];
@@ -707,13 +879,19 @@ struct MmaConsumerMQ {
       float sv[2][4];
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt) {
-        const int nv = tt ? nvalid1 : kTile;
+        if constexpr (MOD) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sv[tt][i] = (cc[tt][0][nt][i] + cc[tt][1][nt][i]) * scale_log2;
-        if (r0 >= nv) sv[tt][0] = sv[tt][1] = -INFINITY;
-        if (r0 + 8 >= nv) sv[tt][2] = sv[tt][3] = -INFINITY;
+          for (int i = 0; i < 4; ++i) sv[tt][i] = cc[tt][0][nt][i] + cc[tt][1][nt][i];
+          mod_scores(*mod, mc, tt ? mo1 : mo0, r0, sv[tt][0], sv[tt][1], sv[tt][2], sv[tt][3]);
+        } else {
+          const int nv = tt ? nvalid1 : kTile;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sv[tt][i] = (cc[tt][0][nt][i] + cc[tt][1][nt][i]) * scale_log2;
+          if (r0 >= nv) sv[tt][0] = sv[tt][1] = -INFINITY;
+          if (r0 + 8 >= nv) sv[tt][2] = sv[tt][3] = -INFINITY;
+        }
       }
-      if (tok0 + 2 * kTile > ctx - Q) {  // the pair reaches the queries' own positions
+      if (!MOD && tok0 + 2 * kTile > ctx - Q) {  // the pair reaches the queries' own positions
         const int na = col0 + nt * 8 + 2 * (lane & 3), nb = na + 1;
         const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
         const int lim_b = nb < G * Q ? ctx - Q + nb / G : -1;
@@ -760,7 +938,15 @@ struct MmaConsumerMQ {
     }
     const int t2 = 2 * (lane & 3);
     uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
-    if (nvalid1 < kTile) {
+    uint32_t keep_lo0 = 0xffffffffu, keep_hi0 = 0xffffffffu;  // MOD: the first tile's
+    if constexpr (MOD) {
+      if ((mo0.vis & mo1.vis) != 0xffffu) {
+        keep_lo0 = keep_pair(mo0.vis, t2);
+        keep_hi0 = keep_pair(mo0.vis, t2 + 8);
+        keep_lo = keep_pair(mo1.vis, t2);
+        keep_hi = keep_pair(mo1.vis, t2 + 8);
+      }
+    } else if (nvalid1 < kTile) {
       keep_lo = (t2 < nvalid1 ? 0x0000ffffu : 0u) | (t2 + 1 < nvalid1 ? 0xffff0000u : 0u);
       keep_hi = (t2 + 8 < nvalid1 ? 0x0000ffffu : 0u) | (t2 + 9 < nvalid1 ? 0xffff0000u : 0u);
     }
@@ -785,6 +971,12 @@ struct MmaConsumerMQ {
       uint32_t v0[4], v1[4];
       ldmatrix_x4_trans(v0, vp0.at(mt));
       ldmatrix_x4_trans(v1, vp1.at(mt));
+      if constexpr (MOD) {
+        v0[0] &= keep_lo0;
+        v0[1] &= keep_lo0;
+        v0[2] &= keep_hi0;
+        v0[3] &= keep_hi0;
+      }
       v1[0] &= keep_lo;
       v1[1] &= keep_lo;
       v1[2] &= keep_hi;
@@ -800,6 +992,7 @@ struct MmaConsumerMQ {
   }
 
   // Output rows are [seq][query][head]; partial rows are [query][head].
+  template <bool REST = false>
   __device__ __forceinline__ void finish(const DecodeParams& p, int seq, int kv_head, int slot,
                                          int r, int lane) {
     const int G = p.group, H = p.num_heads, Q = p.num_queries;
@@ -819,7 +1012,7 @@ struct MmaConsumerMQ {
         const int qi = n / G, g = n % G;
         const int row = qi * H + kv_head * G + g;
         const float l = half ? lb : la, m = half ? m_b[nt] : m_a[nt];
-        if (slot < 0) {
+        if (!REST && slot < 0) {
           __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + ((size_t)seq * Q * H + row) * D;
           const float inv = l > 0.f ? 1.f / l : 0.f;  // a query with no keys gives zeros
 #pragma unroll
@@ -828,16 +1021,18 @@ struct MmaConsumerMQ {
             out[mt * 16 + d0 + 8] = __float2bfloat16_rn(acc[nt][mt][2 + half] * inv);
           }
         } else {
-          const size_t base = ((size_t)r * 2 + slot) * Q * H + row;
-          float* po = p.part_o + base * D;
+          const bool whole = REST && slot < 0;
+          const size_t base = (whole ? (size_t)seq : (size_t)r * 2 + slot) * Q * H + row;
+          float* po = (whole ? p.rest_o : p.part_o) + base * D;
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt) {
             po[mt * 16 + d0] = acc[nt][mt][half];
             po[mt * 16 + d0 + 8] = acc[nt][mt][2 + half];
           }
           if (d0 == 0) {
-            p.part_ml[base * 2 + 0] = m;
-            p.part_ml[base * 2 + 1] = l;
+            float* pm = (whole ? p.rest_ml : p.part_ml) + base * 2;
+            pm[0] = m;
+            pm[1] = l;
           }
         }
       }
@@ -862,7 +1057,8 @@ struct MmaConsumerMQ {
 // MQ: several query tokens per sequence with a causal mask, as in
 // MmaConsumerMQ: column n = col0 + (lane / 4) holds (query n / G, head n % G),
 // query qi sits at position ctx - Q + qi and sees tokens up to it.
-template <int D, bool MQ = false>
+// MOD (with MQ): modified scores, as in MmaConsumerMQ.
+template <int D, bool MQ = false, bool MOD = false>
 struct MmaConsumerF8 {
   static constexpr int KS = D / 16;
   uint32_t qb[KS][2];
@@ -870,6 +1066,7 @@ struct MmaConsumerF8 {
   float m_a, m_b, l_a, l_b;
   uint32_t lane_off = 0;  // this lane's ldmatrix row address within a half-stage (K and V alike)
   int col0 = 0;           // MQ: first (query, head) column of this warp
+  ModCols mc;             // MOD
 
   // Once per kernel: uh is the head's first 16-byte unit in the group's row.
   __device__ __forceinline__ void setup(uint32_t lines, int uh, int lane) {
@@ -926,7 +1123,8 @@ struct MmaConsumerF8 {
 
   // MQ: tok0 (first token of the tile), ctx, G and Q give the causal limits.
   __device__ __forceinline__ void tile(uint32_t k_half, uint32_t v_half, int nvalid, float scale_log2,
-                                       int lane, int tok0 = 0, int ctx = 0, int G = 1, int Q = 1) {
+                                       int lane, int tok0 = 0, int ctx = 0, int G = 1, int Q = 1,
+                                       const DecodeParams* mod = nullptr, const ModTile& mo = ModTile()) {
     // Matrices of one ldmatrix.x4: (rows 0-7, bytes 0-15), (rows 8-15, 0-15),
     // (rows 0-7, 16-31), (rows 8-15, 16-31) - two k-steps / m-tiles of 16 dims.
     // Half-stages are 1 KiB aligned, so adding the lane offset keeps the
@@ -958,11 +1156,18 @@ struct MmaConsumerF8 {
 #pragma unroll
       for (int i = 0; i < 4; ++i) cc[0][i] += cc[ch][i];
     const int g = lane >> 2, t2 = 2 * (lane & 3);
-    float s0 = cc[0][0] * scale_log2, s1 = cc[0][1] * scale_log2;
-    float s2 = cc[0][2] * scale_log2, s3 = cc[0][3] * scale_log2;
-    if (g >= nvalid) s0 = s1 = -INFINITY;
-    if (g + 8 >= nvalid) s2 = s3 = -INFINITY;
-    if (MQ && tok0 + kTile > ctx - Q) {  // only tiles reaching the queries' own positions
+    float s0 = cc[0][0], s1 = cc[0][1], s2 = cc[0][2], s3 = cc[0][3];
+    if constexpr (MOD) {
+      mod_scores(*mod, mc, mo, g, s0, s1, s2, s3);
+    } else {
+      s0 *= scale_log2;
+      s1 *= scale_log2;
+      s2 *= scale_log2;
+      s3 *= scale_log2;
+      if (g >= nvalid) s0 = s1 = -INFINITY;
+      if (g + 8 >= nvalid) s2 = s3 = -INFINITY;
+    }
+    if (MQ && !MOD && tok0 + kTile > ctx - Q) {  // only tiles reaching the queries' own positions
       // Last visible position of each column's query (-1: padding column).
       const int na = col0 + t2, nb = na + 1;
       const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
@@ -997,9 +1202,11 @@ struct MmaConsumerF8 {
     // Each V register holds bytes (tok 2t: dim 2g, 2g+1 | tok 2t+1: dim 2g, 2g+1);
     // on the last tile of a segment, tokens past the end are zeroed (code 0
     // is +0.0) before they meet a weight.
-    if (nvalid < kTile) {
-      const uint32_t keep_lo = (t2 < nvalid ? 0x0000ffffu : 0u) | (t2 + 1 < nvalid ? 0xffff0000u : 0u);
-      const uint32_t keep_hi = (t2 + 8 < nvalid ? 0x0000ffffu : 0u) | (t2 + 9 < nvalid ? 0xffff0000u : 0u);
+    if (MOD ? mo.vis != 0xffffu : nvalid < kTile) {
+      const uint32_t keep_lo = MOD ? keep_pair(mo.vis, t2)
+                                   : (t2 < nvalid ? 0x0000ffffu : 0u) | (t2 + 1 < nvalid ? 0xffff0000u : 0u);
+      const uint32_t keep_hi = MOD ? keep_pair(mo.vis, t2 + 8)
+                                   : (t2 + 8 < nvalid ? 0x0000ffffu : 0u) | (t2 + 9 < nvalid ? 0xffff0000u : 0u);
 #pragma unroll
       for (int j = 0; j < KS / 2; ++j) {
         vr[j][0] &= keep_lo;
@@ -1038,7 +1245,8 @@ struct MmaConsumerF8 {
   // exponentials, rescale) run once per pair.
   __device__ __forceinline__ void tile2(uint32_t k_half0, uint32_t v_half0, uint32_t k_half1, uint32_t v_half1,
                                         int nvalid1, float scale_log2, int lane, int tok0 = 0, int ctx = 0,
-                                        int G = 1, int Q = 1) {
+                                        int G = 1, int Q = 1, const DecodeParams* mod = nullptr,
+                                        const ModTile& mo0 = ModTile(), const ModTile& mo1 = ModTile()) {
     const uint32_t ka[2] = {k_half0 + lane_off, k_half1 + lane_off};
     const uint32_t va[2] = {v_half0 + lane_off, v_half1 + lane_off};
     uint32_t kr[2][KS / 2][4];
@@ -1073,10 +1281,18 @@ struct MmaConsumerF8 {
 #pragma unroll
     for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[tt][i] = (cc[tt][0][i] + cc[tt][1][i]) * scale_log2;
-    if (g >= nvalid1) sc[1][0] = sc[1][1] = -INFINITY;
-    if (g + 8 >= nvalid1) sc[1][2] = sc[1][3] = -INFINITY;
-    if (MQ && tok0 + 2 * kTile > ctx - Q) {  // the pair reaches the queries' own positions
+      for (int i = 0; i < 4; ++i) {
+        sc[tt][i] = cc[tt][0][i] + cc[tt][1][i];
+        if constexpr (!MOD) sc[tt][i] *= scale_log2;
+      }
+    if constexpr (MOD) {
+      mod_scores(*mod, mc, mo0, g, sc[0][0], sc[0][1], sc[0][2], sc[0][3]);
+      mod_scores(*mod, mc, mo1, g, sc[1][0], sc[1][1], sc[1][2], sc[1][3]);
+    } else {
+      if (g >= nvalid1) sc[1][0] = sc[1][1] = -INFINITY;
+      if (g + 8 >= nvalid1) sc[1][2] = sc[1][3] = -INFINITY;
+    }
+    if (MQ && !MOD && tok0 + 2 * kTile > ctx - Q) {  // the pair reaches the queries' own positions
       const int na = col0 + t2, nb = na + 1;
       const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
       const int lim_b = nb < G * Q ? ctx - Q + nb / G : -1;
@@ -1118,7 +1334,22 @@ struct MmaConsumerF8 {
       pb[tt][0] = movmatrix_trans(pack_f16x2(pw[tt][0], pw[tt][1]));
       pb[tt][1] = movmatrix_trans(pack_f16x2(pw[tt][2], pw[tt][3]));
     }
-    if (nvalid1 < kTile) {
+    if constexpr (MOD) {
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        const uint32_t vis = tt ? mo1.vis : mo0.vis;
+        if (vis != 0xffffu) {
+          const uint32_t keep_lo = keep_pair(vis, t2), keep_hi = keep_pair(vis, t2 + 8);
+#pragma unroll
+          for (int j = 0; j < KS / 2; ++j) {
+            vr[tt][j][0] &= keep_lo;
+            vr[tt][j][1] &= keep_hi;
+            vr[tt][j][2] &= keep_lo;
+            vr[tt][j][3] &= keep_hi;
+          }
+        }
+      }
+    } else if (nvalid1 < kTile) {
       const uint32_t keep_lo = (t2 < nvalid1 ? 0x0000ffffu : 0u) | (t2 + 1 < nvalid1 ? 0xffff0000u : 0u);
       const uint32_t keep_hi = (t2 + 8 < nvalid1 ? 0x0000ffffu : 0u) | (t2 + 9 < nvalid1 ? 0xffff0000u : 0u);
 #pragma unroll
@@ -1228,7 +1459,8 @@ struct MmaConsumerF8 {
 
 // fp32 CUDA-core consumer.  Lane l owns head dims [l*DC, l*DC+DC) of every
 // query head; after the butterfly reduction lane l holds the score of token l/2.
-template <int D, int GMAX>
+// MOD: modified scores (one query, at position ctx - 1; a row is seen or not).
+template <int D, int GMAX, bool MOD = false>
 struct SimtConsumer {
   static constexpr int DC = D / 32;
   float qv[GMAX][DC];
@@ -1252,7 +1484,8 @@ struct SimtConsumer {
 
   __device__ __forceinline__ void tile(const unsigned char* k_base, const unsigned char* v_base,
                                        uint32_t pitch, int nvalid, float scale_log2, int G,
-                                       int lane) {
+                                       int lane, const DecodeParams* mod = nullptr,
+                                       const ModTile& mo = ModTile(), int kv_head = 0) {
     const int my_tok = lane >> 1;
 #pragma unroll
     for (int h = 0; h < GMAX; ++h) {
@@ -1295,8 +1528,17 @@ struct SimtConsumer {
         sc = mine + __shfl_xor_sync(0xffffffffu, give, 2);
       }
       sc += __shfl_xor_sync(0xffffffffu, sc, 1);
-      sc *= scale_log2;
-      if (my_tok >= nvalid) sc = -INFINITY;
+      if constexpr (MOD) {
+        // fp32 outputs keep the cap's full precision: tanhf, not the SFU form.
+        sc = mod->cap_out != 0.f ? mod->cap_out * tanhf(sc * mod->cap_in) : sc * scale_log2;
+        if (mod->slopes != nullptr)
+          sc -= 1.4426950408889634f * __ldg(mod->slopes + kv_head * G + h) *
+                fabsf(static_cast<float>(mo.ctx - 1 - mo.tok0 - my_tok));
+        if (!((mo.vis >> my_tok) & 1u)) sc = -INFINITY;
+      } else {
+        sc *= scale_log2;
+        if (my_tok >= nvalid) sc = -INFINITY;
+      }
       float mx = sc;
 #pragma unroll
       for (int o = 2; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -1308,7 +1550,8 @@ struct SimtConsumer {
       l[h] = l[h] * alpha + pw;
 #pragma unroll
       for (int i = 0; i < DC; ++i) acc[h][i] *= alpha;
-      for (int t = 0; t < nvalid; ++t) {
+      for (int t = 0; t < (MOD ? kTile : nvalid); ++t) {
+        if (MOD && !((mo.vis >> t) & 1u)) continue;
         const float pt = __shfl_sync(0xffffffffu, pw, 2 * t);
         const float* vr = reinterpret_cast<const float*>(v_base + t * pitch) + lane * DC;
 #pragma unroll
@@ -1356,6 +1599,13 @@ __device__ void zero_row(const DecodeParams& p, int s) {
   for (size_t i = 0; i < n16; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// kWalkRest: an empty sequence leaves (m, l) = (-inf, 0) for all its rows.
+__device__ inline void empty_rest(const DecodeParams& p, int s) {
+  const size_t n = (size_t)p.num_queries * p.num_heads;
+  float2* ml = reinterpret_cast<float2*>(p.rest_ml) + (size_t)s * n;
+  for (size_t i = 0; i < n; ++i) ml[i] = make_float2(-INFINITY, 0.f);
+}
+
 __device__ __forceinline__ float warp_max_f(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -1374,7 +1624,8 @@ __device__ __forceinline__ float warp_sum_f(float v) {
 // writes the output rows, and resets the ticket counter.  Nobody waits.
 // `arrivals`: warps writing partials per range and KV head (two to four when
 // the (query, head) columns of a KV head are split across several warps).
-template <typename T, int D, bool kMQ>
+// kRest: the merged (m, l, O) go to the rest buffers instead of the output.
+template <typename T, int D, bool kMQ, bool kRest = false>
 __device__ void arrive_and_merge(const DecodeParams& p, int seq, int kv_head, int r0, int r1,
                                  int slot0, int lane, int arrivals = 1) {
   // Release: the warp barrier orders every lane's partial stores before lane
@@ -1460,6 +1711,18 @@ __device__ void arrive_and_merge(const DecodeParams& p, int seq, int kv_head, in
           for (int i = 0; i < DL; ++i) acc[g][i] = acc[g][i] * a_old + co[g][i] * a_new;
         }
       }
+    }
+    if constexpr (kRest) {
+      const size_t row = (size_t)seq * H + h0;
+#pragma unroll
+      for (int g = 0; g < GM; ++g) {
+        if (g < gn) {
+#pragma unroll
+          for (int i = 0; i < DL; ++i) p.rest_o[(row + g) * D + lane * DL + i] = acc[g][i];
+          if (lane == 0) *reinterpret_cast<float2*>(p.rest_ml + (row + g) * 2) = make_float2(run_m[g], run_l[g]);
+        }
+      }
+      continue;
     }
     T* out = reinterpret_cast<T*>(p.out) + ((size_t)seq * H + h0) * D + lane * DL;
 #pragma unroll
@@ -1566,7 +1829,9 @@ __device__ __forceinline__ void append_new_rows_fp8(const DecodeParams& p, const
 // sequence with a causal mask, (query, head) columns in one 8-wide MMA N-tile
 // per warp: one warp per KV head (up to 8 columns) or p.split warps (2 to 4,
 // up to 32 columns).
-template <typename T, int D, int GMAX, int QMODE, bool KV8 = false>
+// WALK: which tiles, and what becomes of the rows (kWalkMod on the tensor-core
+// paths: QMODE 1 or 2, also for one query).
+template <typename T, int D, int GMAX, int QMODE, bool KV8 = false, int WALK = kWalkAll>
 __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
     pa_decode_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -1588,8 +1853,13 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
   long long total = 0;
   for (int base = 0; base < S; base += nthreads) {
     const int s = base + tid;
-    long long n = (s < S) ? tiles_of(clamp_context(p, s, true)) : 0;
-    if (s < S && n == 0 && s % gridDim.x == blockIdx.x) zero_row<T, D>(p, s);
+    long long n = (s < S) ? SeqWalk<WALK>(p, s, true).n : 0;
+    if (s < S && n == 0 && s % gridDim.x == blockIdx.x) {
+      if constexpr (WALK == kWalkRest)
+        empty_rest(p, s);
+      else
+        zero_row<T, D>(p, s);
+    }
     n = warp_sum_ll(n);
     if (lane == 0) misc[warp] = n;
     __syncthreads();
@@ -1605,7 +1875,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
   long long run = 0;
   for (int base = 0; base < S; base += nthreads) {
     const int s = base + tid;
-    const long long n = (s < S) ? tiles_of(clamp_context(p, s, false)) : 0;
+    const long long n = (s < S) ? SeqWalk<WALK>(p, s, false).n : 0;
     const long long incl = warp_incl_scan_ll(n, lane);
     if (lane == 31) misc[warp] = incl;
     __syncthreads();
@@ -1670,10 +1940,12 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
     const T* qg = reinterpret_cast<const T*>(p.q);
     int s = s_first;
     long long ps = p_first;
-    int c = clamp_context(p, s, false);
-    long long ns = tiles_of(c);
+    SeqWalk<WALK> sw(p, s, false);
+    int c = sw.c;
+    long long ns = sw.n;
     // The next sequence's length is fetched one sequence ahead.
-    int c_next = (s + 1 < S) ? clamp_context(p, s + 1, false) : 0;
+    SeqWalk<WALK> sw_next;
+    if (s + 1 < S) sw_next = SeqWalk<WALK>(p, s + 1, false);
     int slot = 0, seg_r0 = 0, seg_r1 = 0, seg_slot0 = 0;
     int st = 0, qi = 0;
     uint32_t ph = 0, qph = 0;
@@ -1709,14 +1981,17 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
       while (x >= ps + ns) {
         ps += ns;
         ++s;
-        c = c_next;
-        ns = tiles_of(c);
-        c_next = (s + 1 < S) ? clamp_context(p, s + 1, false) : 0;
+        sw = sw_next;
+        c = sw.c;
+        ns = sw.n;
+        sw_next = SeqWalk<WALK>();
+        if (s + 1 < S) sw_next = SeqWalk<WALK>(p, s + 1, false);
         new_seq = true;
       }
       const int j = static_cast<int>(x - ps);
-      const int tok0 = j * kTile;
-      const int nvalid = min(kTile, c - tok0);
+      const int tok0 = sw.token(j);
+      int nvalid = min(kTile, c - tok0);
+      if constexpr (WALK == kWalkMod) nvalid = __ballot_sync(0xffffffffu, sw.sees(tok0 + t)) & 0xffff;
       const int blk0 = blk_of(tok0);
       if (new_seq) {
         slot = segment_slot(a, b, ps, ps + ns);
@@ -1732,6 +2007,12 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
         nxt = table_entry(cb + 32 + lane);
       }
       while (blk0 >= cb + 32) {
+        if (WALK == kWalkMod && blk0 >= cb + 96) {  // from the prefix to the window: start afresh
+          cb = blk0;
+          cur = table_entry(cb + lane);
+          nxt = table_entry(cb + 32 + lane);
+          break;
+        }
         cur = nxt;
         cb += 32;
         nxt = table_entry(cb + 32 + lane);
@@ -1781,6 +2062,9 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
       const int e_nxt = __shfl_sync(0xffffffffu, nxt, rel & 31);
       const int phys = rel < 32 ? e_cur : e_nxt;
       bool ok = t < nvalid;
+      // A box is copied if some query sees one of its rows.
+      if constexpr (WALK == kWalkMod)
+        ok = lead && ((nvalid >> t) & (kMmaPath ? (1 << p.box_rows) - 1 : 1)) != 0;
       if (ok && p.num_physical_blocks > 0 && (phys < 0 || phys >= p.num_physical_blocks)) {
         report(p.error_flag, PA_DEVERR_BLOCK_ID);
         ok = false;
@@ -1796,7 +2080,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
                             (unsigned)off_of(tok));
       // Appending calls: the step's new tokens are positions c - Q .. c - 1.
       int newfirst = -1;
-      if (kMmaPath && p.k_new != nullptr && tok0 + nvalid > c - p.num_queries) {
+      if (WALK == kWalkAll && kMmaPath && p.k_new != nullptr && tok0 + nvalid > c - p.num_queries) {
         newfirst = max(0, c - p.num_queries - tok0);
       }
       if (!mbar_wait_warp(empty_bar(st), ph ^ 1u, p.wait_limit_ns)) {
@@ -1806,14 +2090,14 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
       // Tests of the bounded waits: this tile's stage is never armed or
       // filled, so the consumers' wait on it runs out.
       const bool stall = x == p.stall_tile;
-      if (newfirst >= 0 && !is_v && t >= newfirst && t < nvalid) {
+      if (WALK == kWalkAll && newfirst >= 0 && !is_v && t >= newfirst && t < nvalid) {
         // Pool row of this tile row's new token; a failed block check leaves it unwritten.
         const bool bad = p.num_physical_blocks > 0 && (phys < 0 || phys >= p.num_physical_blocks);
         stage_rows[st * kTile + t] = bad ? -1 : row;
       }
       __syncwarp();
       if (lane == 0 && !stall) {
-        meta[st] = StageMeta{s, tok0, nvalid, flags, seg_r0, seg_r1, c, newfirst};
+        meta[st] = StageMeta{s, tok0, nvalid, flags, seg_r0, seg_r1, c, WALK == kWalkMod ? sw.pre : newfirst};
         mbar_arrive_expect_tx(full_bar(st), __popc(copies) * (kMmaPath ? p.box_bytes : p.row_bytes));
       }
       __syncwarp();
@@ -1854,11 +2138,13 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
     int st = 0, qi = 0;
     uint32_t ph = 0, qph = 0;
     constexpr bool kMma = (sizeof(T) == 2);
+    constexpr bool kMod = WALK == kWalkMod;
     using Mma = typename std::conditional<
-        KV8, MmaConsumerF8<D, (QMODE > 0)>,
-        typename std::conditional<QMODE == 0, MmaConsumer<D>, MmaConsumerMQ<D, 1>>::type>::type;
-    typename std::conditional<kMma, Mma, SimtConsumer<D, GMAX>>::type cons;
+        KV8, MmaConsumerF8<D, (QMODE > 0), kMod>,
+        typename std::conditional<QMODE == 0, MmaConsumer<D>, MmaConsumerMQ<D, 1, kMod>>::type>::type;
+    typename std::conditional<kMma, Mma, SimtConsumer<D, GMAX, kMod>>::type cons;
     if constexpr (KV8) cons.setup(p.lines, w * D / 16, lane);
+    if constexpr (kMod && kMma) cons.mc.setup(p, kv_head, col_base + 2 * (lane & 3));
     // FP8 consumers, and bf16 ones that split a KV head's columns over
     // several warps, take two stages at a time when both hold the same
     // segment (tile pairing: tile2), if the ring has four or more stages.
@@ -1895,7 +2181,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
       const uint32_t k_half = stages + st * p.stage_bytes;
       const uint32_t v_half = k_half + kTile * p.lines * kLine;
       const int uh = w * D * kKVBytes / 16;  // this head's first 16-byte unit in the row
-      if constexpr (kMma && QMODE < 2) {
+      if constexpr (kMma && QMODE < 2 && WALK == kWalkAll) {
         if (mt.newfirst >= 0) {
           const int* rows = stage_rows + st * kTile;
           if constexpr (KV8)
@@ -1922,7 +2208,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
           me = meta[st2];
           const uint32_t k_half2 = stages + st2 * p.stage_bytes;
           const uint32_t v_half2 = k_half2 + kTile * p.lines * kLine;
-          if constexpr (QMODE < 2) {
+          if constexpr (QMODE < 2 && WALK == kWalkAll) {
             if (me.newfirst >= 0) {
               if constexpr (KV8)
                 append_new_rows_fp8<D>(p, me, stage_rows + st2 * kTile, kv_head, w, k_half2, v_half2, lane);
@@ -1930,7 +2216,15 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
                 append_new_rows<D>(p, me, stage_rows + st2 * kTile, kv_head, w, k_half2, v_half2, lane);
             }
           }
-          if constexpr (KV8 && QMODE > 0)
+          const ModTile mo0{(uint32_t)mt.nvalid, mt.tok0, mt.ctx, mt.newfirst};
+          const ModTile mo1{(uint32_t)me.nvalid, me.tok0, me.ctx, me.newfirst};
+          if constexpr (kMod && KV8)
+            cons.tile2(k_half, v_half, k_half2, v_half2, 0, p.scale_log2, lane, mt.tok0, mt.ctx, G,
+                       p.num_queries, &p, mo0, mo1);
+          else if constexpr (kMod)
+            cons.tile2(k_half, v_half, k_half2, v_half2, p.lines, uh, 0, mt.tok0, mt.ctx, G, p.num_queries,
+                       p.scale_log2, lane, &p, mo0, mo1);
+          else if constexpr (KV8 && QMODE > 0)
             cons.tile2(k_half, v_half, k_half2, v_half2, me.nvalid, p.scale_log2, lane, mt.tok0, mt.ctx, G,
                        p.num_queries);
           else if constexpr (KV8)
@@ -1943,7 +2237,18 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
           ++x;
         }
       }
+      const ModTile mo{(uint32_t)mt.nvalid, mt.tok0, mt.ctx, mt.newfirst};
       if (paired) {
+      } else if constexpr (kMod && KV8) {
+        cons.tile(k_half, v_half, 0, p.scale_log2, lane, mt.tok0, mt.ctx, G, p.num_queries, &p, mo);
+      } else if constexpr (kMod && kMma && QMODE == 2) {
+        cons.tile_hoisted(k_half, v_half, p.lines, uh, 0, mt.tok0, mt.ctx, G, p.num_queries, p.scale_log2, lane,
+                          &p, mo);
+      } else if constexpr (kMod && kMma) {
+        cons.tile(k_half, v_half, p.lines, uh, 0, mt.tok0, mt.ctx, G, p.num_queries, p.scale_log2, lane, &p, mo);
+      } else if constexpr (kMod) {
+        const unsigned char* kb = smem + L.stage + st * p.stage_bytes + w * D * sizeof(T);
+        cons.tile(kb, kb + kTile * p.pitch, p.pitch, 0, p.scale_log2, G, lane, &p, mo, kv_head);
       } else if constexpr (KV8 && QMODE > 0) {
         cons.tile(k_half, v_half, mt.nvalid, p.scale_log2, lane, mt.tok0, mt.ctx, G, p.num_queries);
       } else if constexpr (KV8) {
@@ -1967,9 +2272,12 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
       }
       if (me.flags & kSegEnd) {
         const int slot = ((me.flags >> 2) & 3) - 1;
-        cons.finish(p, me.seq, kv_head, slot, r, lane);
+        if constexpr (WALK == kWalkRest)
+          cons.template finish<true>(p, me.seq, kv_head, slot, r, lane);
+        else
+          cons.finish(p, me.seq, kv_head, slot, r, lane);
         if (slot >= 0)
-          arrive_and_merge<T, D, (QMODE > 0)>(p, me.seq, kv_head, me.r0, me.r1, (me.flags >> 4) & 1, lane,
+          arrive_and_merge<T, D, (QMODE > 0), WALK == kWalkRest>(p, me.seq, kv_head, me.r0, me.r1, (me.flags >> 4) & 1, lane,
                                               kSplit);
         // Split-column kernels sit at the register cap: writing the state here
         // (the next segment's begin_segment rewrites it anyway) frees its

@@ -22,6 +22,13 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return y;
 }
 
+// 1 / x on the special-function unit (relative error below 2^-23; 0 for inf).
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -1,0 +1,67 @@
+// Launching the decode kernel, shared by the translation units that
+// instantiate it (one per kind of walk, compiled in parallel).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "pa_decode_kernel.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+struct Plan {
+  int Hg, HG, R, stages, q_slots, split;
+  uint32_t row_bytes, pitch, q_bytes, stage_bytes, smem;
+  uint32_t lines, box_rows, box_bytes;  // tensor-core paths (see DecodeParams)
+  size_t ws_ml, ws_o, ws_partials, ws_counters, ws_total;
+};
+
+// Launch with programmatic stream serialisation: the kernel may become
+// resident while its predecessor on the stream finishes; it calls
+// griddepcontrol.wait before touching anything that predecessor produces.
+template <typename Kernel, typename Params>
+cudaError_t launch_pdl(Kernel kern, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                       const Params& prm) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, prm);
+}
+
+template <typename T, int D, int GMAX, int QMODE = 0, bool KV8 = false, int WALK = kWalkAll>
+int launch_typed(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream) {
+  // Devices whose shared-memory limit is already raised for this kernel
+  // (setting it again is harmless, so concurrent first calls may both set it).
+  constexpr int kTrackedDevices = 64;
+  static std::atomic<bool> configured[kTrackedDevices];
+  auto kern = pa_decode_kernel<T, D, GMAX, QMODE, KV8, WALK>;
+  if (dev < 0 || dev >= kTrackedDevices || !configured[dev].load(std::memory_order_acquire)) {
+    DeviceInfo info{};
+    int rc = current_device_info(&info);
+    if (rc != PA_OK) return rc;
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, info.max_smem_optin);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode smem)");
+    if (dev >= 0 && dev < kTrackedDevices) configured[dev].store(true, std::memory_order_release);
+  }
+  cudaError_t e =
+      launch_pdl(kern, dim3(pl.R * pl.HG), dim3(32 * (pl.Hg * pl.split + kProducers)), pl.smem, stream, prm);
+  if (e != cudaSuccess) return cuda_fail(e, "launch pa_decode_kernel");
+  return PA_OK;
+}
+
+// The kernel variants of the other translation units.
+int launch_mod(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool f32,
+               bool kv_fp8);
+int launch_rest(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size);
+
+}  // namespace pa

@@ -19,19 +19,12 @@
 #include <mutex>
 
 #include "../../include/pagedattn.h"
+#include "pa_decode_impl.h"
 #include "pa_internal.h"
 
 static __device__ __align__(256) unsigned char g_static_scratch[PA_STATIC_SCRATCH_BYTES];
 
 namespace pa {
-
-int decode_impl_q(void* out, const void* query, const void* k_cache, const void* v_cache,
-                  const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
-                  int num_queries, int num_heads, int num_kv_heads, int head_size, int block_size,
-                  int max_blocks_per_seq, float scale, void* stream, int dtype,
-                  int num_physical_blocks, void* workspace, size_t workspace_bytes, int num_ranges,
-                  int32_t* error_flag, bool kv_fp8, float k_scale, float v_scale, const void* k_new,
-                  const void* v_new, ScratchProvider fixed_scratch);
 
 namespace {
 constexpr int kMaxDevices = 64;

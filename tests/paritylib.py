@@ -79,3 +79,14 @@ def assert_close(got: torch.Tensor, want: np.ndarray, dtype: str, what: str = ""
     if mean_tol is not None:
         assert err.mean() <= mean_tol, f"{what}: mean abs err {err.mean():.3e} > {mean_tol}"
     return float(err.max()), float(err.mean())
+
+
+def assert_rounded(got: torch.Tensor, want: np.ndarray, spread: np.ndarray, weight_error: float, what: str = ""):
+    """|got - want| within half a step of the output type plus ``weight_error`` times ``spread``: the weighted sum
+    of |v|, by which a relative error of each softmax weight shows in the output."""
+    g = got.double().cpu().numpy()
+    assert np.all(np.isfinite(g)), f"{what}: non-finite output"
+    half_step = torch.finfo(got.dtype).eps / 2
+    room = half_step * np.abs(want) + weight_error * spread
+    over = np.abs(g - want) - room
+    assert np.all(over <= 0), f"{what}: {np.max(over):.3e} beyond its bound, error {np.abs(g - want).max():.3e}"
