@@ -275,6 +275,47 @@ int pa_decode_fp8_mod(void* out, const void* query, const void* k_cache, const v
                       size_t workspace_bytes, int num_ranges, int32_t* error_flag);
 
 /*
+ * pa_decode_prefix - pa_decode_mq for a batch whose sequences share a long
+ * prefix (a system prompt, a document, samples of one prompt), attended once
+ * for all of them: the prefix's K/V are read once per call instead of once per
+ * sequence, and its scores are one matrix product per KV head.
+ *
+ * prefix_table [num_prefix_blocks] int32: the physical blocks of the prefix's
+ *              P = num_prefix_blocks * block_size tokens (may be NULL for 0)
+ * block_tables [num_seqs, max_blocks_per_seq]: the sequences' whole tables, as
+ *              for pa_decode_mq
+ * A sequence of context_lens[s] >= P + num_queries - 1 tokens has the prefix as its
+ * first P tokens; the entries of its row before num_prefix_blocks are not read.
+ * A shorter one (a padding row of context 0, a request that has not reached the
+ * end of the prompt) is attended through its own row alone.  So out is that of
+ * pa_decode_mq wherever the rows of the longer sequences begin with
+ * prefix_table, as pa_bm_share_prefix and pa_tables_step make them.
+ * Requires PA_BF16; block_size a multiple of 8 (PA_ERR_UNSUPPORTED otherwise);
+ * num_prefix_blocks <= max_blocks_per_seq; (num_heads / num_kv_heads) *
+ * num_queries <= 32.  num_physical_blocks > 0 checks the prefix's block ids
+ * too; tokens of a bad one count as zeros.
+ * The softmax weights of the prefix enter its second product rounded to bf16
+ * (relative error <= 2^-8 each; sums and statistics stay fp32).
+ * workspace    256-byte aligned device scratch of at least
+ *              pa_decode_prefix_workspace_size(...) bytes, of any content; NULL:
+ *              the library's own, refused while `stream` is being captured
+ *              (PA_ERR_INVALID_ARG).  Two calls that may overlap in time need
+ *              scratch of their own.
+ * Other arguments as in pa_decode_mq.  The call makes up to three launches.
+ */
+int pa_decode_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,
+                     const int32_t* prefix_table, const int32_t* block_tables,
+                     const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
+                     int num_kv_heads, int head_size, int block_size, int num_prefix_blocks,
+                     int max_blocks_per_seq, float scale, void* stream, int dtype,
+                     int num_physical_blocks, void* workspace, size_t workspace_bytes,
+                     int32_t* error_flag);
+
+/* Scratch bytes pa_decode_prefix needs on the current device (0 for invalid sizes). */
+size_t pa_decode_prefix_workspace_size(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
+                                       int head_size);
+
+/*
  * pa_write_cache - scatter one step's new K/V rows into the paged pool
  * (the "reshape_and_cache" step).  For every token i with slot_mapping[i] >= 0:
  *   k_cache[slot / block_size, slot % block_size, :, :] = k_new[i, :, :]  (bit copy)

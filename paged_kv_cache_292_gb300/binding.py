@@ -118,6 +118,11 @@ _SIGS = {
         [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, ctypes.c_float, ctypes.c_float,
          ctypes.c_float, _P, _I, _P, _P, _P, _I, _P, _SZ, _I, _P],
     ),
+    "pa_decode_prefix": (
+        _I,
+        [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _I, _I, _P, _SZ, _P],
+    ),
+    "pa_decode_prefix_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "pa_tables_step": (_I, [_P] * 10 + [_I] * 6 + [_P, _P]),
     "pa_version": (_I, []),
     "pa_test_stall_copy": (_I, [ctypes.c_longlong, ctypes.c_uint]),
@@ -712,3 +717,38 @@ def decode_fp8_mod(query, k_cache, v_cache, block_tables, context_lens, scale, k
     return _decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, (k_scale, v_scale), out, stream,
                        softcap, alibi_slopes, window, first_tokens, prefix_lens, num_ranges, workspace, error_flag,
                        check_block_ids)
+
+
+def pa_decode_prefix(out, query, k_cache, v_cache, prefix_table, block_tables, context_lens, num_seqs, num_queries,
+                     num_heads, num_kv_heads, head_size, block_size, num_prefix_blocks, max_blocks_per_seq, scale,
+                     stream=None, dtype=None, num_physical_blocks=0, workspace=None, workspace_bytes=0,
+                     error_flag=None):
+    dtype = dtype_code(query.dtype) if dtype is None else dtype
+    _check(load().pa_decode_prefix(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_table),
+                                   _ptr(block_tables), _ptr(context_lens), num_seqs, num_queries, num_heads,
+                                   num_kv_heads, head_size, block_size, num_prefix_blocks, max_blocks_per_seq, scale,
+                                   _stream(stream), dtype, num_physical_blocks, _ptr(workspace), workspace_bytes,
+                                   _ptr(error_flag)))
+
+
+def pa_decode_prefix_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads, head_size) -> int:
+    return int(load().pa_decode_prefix_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads, head_size))
+
+
+def decode_prefix(query, k_cache, v_cache, prefix_table, block_tables, context_lens, scale, out=None, stream=None, *,
+                  workspace=None, error_flag=None, check_block_ids=False):
+    """Decode of a batch that shares the prefix in the blocks ``prefix_table[NP]``, attended once for all (as in
+    ``pa_decode_prefix``); query and out [S, H, D] or [S, Q, H, D]."""
+    index = _on_device(query, k_cache, v_cache, prefix_table, block_tables, context_lens, out, workspace, error_flag)
+    S, Q, H, D, NB, bs, Hk, MB = _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out)
+    _require_dtype(query.dtype, k_cache=k_cache, v_cache=v_cache, out=out)
+    _require_dtype(torch.int32, prefix_table=prefix_table, error_flag=error_flag)
+    _require_stream(stream, index)
+    with _call_on(index):
+        if out is None:
+            out = torch.empty_like(query)
+            _used_on(stream, out)
+        pa_decode_prefix(out, query, k_cache, v_cache, prefix_table, block_tables, context_lens, S, Q, H, Hk, D, bs,
+                         prefix_table.numel(), MB, scale, stream, None, NB if check_block_ids else 0, workspace,
+                         workspace.numel() * workspace.element_size() if workspace is not None else 0, error_flag)
+    return out

@@ -22,6 +22,21 @@ namespace pa {
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+EncodeTiledFn encode_tiled_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      return static_cast<EncodeTiledFn>(nullptr);
+    }
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
 namespace {
 
 // Scratch layout: partial (m, l) and O at the start, then the merge tickets
@@ -170,23 +185,7 @@ int validate(const void* out, const void* query, const void* k_cache, const void
 // with strides (1, 128, group row bytes, token row bytes).  A box is
 // (128, lines, 1, box_rows); its lines past the group's row are outside the
 // tensor, so they arrive zero-filled without touching memory.
-using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
-
-EncodeTiledFn encode_tiled_fn() {
-  static const EncodeTiledFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      (void)cudaGetLastError();
-      return static_cast<EncodeTiledFn>(nullptr);
-    }
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
-
+//
 // Encoded maps of the last few pools this thread decoded over.  A map is a
 // pure function of the pool's address, extents, strides and box, which form
 // the key, so a hit is exactly what a fresh encode would give; repeated
@@ -273,6 +272,23 @@ int launch_dtype(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t 
 
 }  // namespace
 
+int decode_validate(const void* out, const void* query, const void* k_cache, const void* v_cache,
+                    const int32_t* block_tables, const int32_t* context_lens, int num_seqs, int num_queries,
+                    int num_heads, int num_kv_heads, int head_size, int block_size, int max_blocks_per_seq,
+                    float scale, int dtype, int num_physical_blocks, int num_ranges) {
+  int rc = validate(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_heads,
+                    num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, dtype,
+                    num_physical_blocks, num_ranges);
+  if (rc != PA_OK) return rc;
+  if (num_queries < 1) return fail(PA_ERR_INVALID_ARG, "pa_decode_mq: num_queries %d < 1", num_queries);
+  if (num_queries > 1 && dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_mq: several queries need bf16");
+  if (num_queries > 1 && (num_heads / num_kv_heads) * num_queries > kMaxColumns)
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_mq: group size x queries = %d > %d",
+                (num_heads / num_kv_heads) * num_queries, kMaxColumns);
+  return PA_OK;
+}
+
 // fixed_scratch: when set and `workspace` is NULL, the scratch comes from this
 // provider (given the plan's byte count, it returns a device buffer that keeps
 // earlier contents, or an error) instead of the library's growable buffer;
@@ -299,16 +315,10 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
     if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale <= 0.f || v_scale <= 0.f)
       return fail(PA_ERR_INVALID_ARG, "pa_decode_fp8: scales must be finite and positive");
   }
-  int rc = validate(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_heads,
-                    num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, dtype,
-                    num_physical_blocks, num_ranges);
+  int rc = decode_validate(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries,
+                           num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, dtype,
+                           num_physical_blocks, num_ranges);
   if (rc != PA_OK) return rc;
-  if (num_queries < 1) return fail(PA_ERR_INVALID_ARG, "pa_decode_mq: num_queries %d < 1", num_queries);
-  if (num_queries > 1 && dtype != PA_BF16)
-    return fail(PA_ERR_UNSUPPORTED, "pa_decode_mq: several queries need bf16");
-  if (num_queries > 1 && (num_heads / num_kv_heads) * num_queries > kMaxColumns)
-    return fail(PA_ERR_UNSUPPORTED, "pa_decode_mq: group size x queries = %d > %d",
-                (num_heads / num_kv_heads) * num_queries, kMaxColumns);
   DeviceInfo dev{};
   rc = current_device_info(&dev);
   if (rc != PA_OK) return rc;
@@ -341,7 +351,10 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
     const size_t cnt_bytes = sizeof(int32_t) * (size_t)num_seqs * num_kv_heads;
     counters = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) +
                                           ((workspace_bytes - cnt_bytes) & ~(size_t)255));
-    if (extras != nullptr) clear_tickets = true;  // the caller's scratch may hold anything
+    if (extras != nullptr && extras->tickets != nullptr)
+      counters = extras->tickets;
+    else if (extras != nullptr)
+      clear_tickets = true;  // the caller's scratch may hold anything
   }
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   DecodeParams prm{};

@@ -18,7 +18,15 @@ struct DecodeExtras {
   int prefix_tokens = 0;
   float* rest_ml = nullptr;
   float* rest_o = nullptr;
+  // Merge tickets that are zero between calls, when the scratch has none of its own.
+  int32_t* tickets = nullptr;
 };
+
+// The argument checks every decode call makes.
+int decode_validate(const void* out, const void* query, const void* k_cache, const void* v_cache,
+                    const int32_t* block_tables, const int32_t* context_lens, int num_seqs, int num_queries,
+                    int num_heads, int num_kv_heads, int head_size, int block_size, int max_blocks_per_seq,
+                    float scale, int dtype, int num_physical_blocks, int num_ranges = 0);
 
 int decode_impl_q(void* out, const void* query, const void* k_cache, const void* v_cache,
                   const int32_t* block_tables, const int32_t* context_lens, int num_seqs,

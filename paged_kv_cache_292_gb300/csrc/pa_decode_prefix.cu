@@ -1,20 +1,739 @@
-// The tokens of a batch's sequences behind their shared prefix: the decode
-// kernel with kWalkRest.
+// Decode attention of a batch that shares a long prefix (pa_decode_prefix).
+//
+// The softmax over a sequence's tokens splits into the prefix's P tokens and
+// the rest.  For the prefix, K and V are the same for all sequences, so the
+// (sequence, query, group head) rows of one KV head are the rows of two matrix
+// products, S = Q K^T and O = P V, that read the prefix once:
+//
+//   m_r = max_t s_rt, l_r = sum_t 2^(s_rt - m_r), O_r = sum_t 2^(s_rt - m_r) v_t
+//
+// (s in log2 units).  The rest is the decode kernel's walk behind the prefix
+// (kWalkRest), and the join adds the parts of a row by their maxima.
+//
+// Prefix kernel: one persistent CTA per SM, equal shares of the (KV head, pair
+// of 128-row tiles, 128-token tile) list (pa_prefix_work.h).  Per CTA:
+//   warps 0-3, 4-7  softmax groups 0 and 1: thread = row; scores come from
+//                   tensor memory, weights go back there as bf16
+//   warp 8          loads K and V tiles by TMA: boxes of gcd(block_size, 128)
+//                   token rows x 64 elements, into 128-byte swizzled panels
+//   warp 9          issues the products (tcgen05.mma, one thread): S from Q and K in
+//                   shared memory, O from the weights in tensor memory and V
+// With two row tiles each group has one and both use every K/V tile; with a
+// single row tile the groups take alternate K/V tiles and leave a partial
+// each.  While one group exponentiates, the tensor core works for the other.
+// Tensor memory: S0, S1 (128 columns each; the weights overwrite the first 64),
+// O0, O1 (D columns each).
 #include "pa_launch.cuh"
 
-namespace pa {
+#include <cmath>
+#include <cstring>
 
-int launch_rest(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size) {
-  using T = __nv_bfloat16;
-  const int columns = prm.group * prm.num_queries;
-  if (head_size == 64) {
-    if (prm.num_queries == 1) return launch_typed<T, 64, 8, 0, false, kWalkRest>(prm, pl, dev, stream);
-    return columns <= 8 ? launch_typed<T, 64, 8, 1, false, kWalkRest>(prm, pl, dev, stream)
-                        : launch_typed<T, 64, 8, 2, false, kWalkRest>(prm, pl, dev, stream);
+#include "pa_decode_impl.h"
+#include "pa_prefix_work.h"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kPrefixThreads = 320;
+constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
+// A running maximum is kept until a tile exceeds it by this factor (log2): until
+// then weights are at most 2^8, which bf16 and the fp32 sums hold as well as 1.
+constexpr float kSlack = 8.f;
+
+struct PrefixParams {
+  CUtensorMap tm_k, tm_v;  // (64 elements, chunk of 64 within a token row, token row)
+  const __nv_bfloat16* q;
+  const int32_t* table;
+  int32_t* error_flag;
+  float* part_ml;  // [slots][2][128][2]
+  float* part_o;   // [slots][2][128][D]
+  PrefixWork work;
+  int rows;  // query rows per KV head
+  int group, num_heads, block_size, prefix_tokens, num_physical_blocks, box_rows;
+  // Scores are scale_log2 * <(q & q_keep) ^ q_flip, k>: a negative scale changes the
+  // queries' signs and a scale of zero makes them zero, so that scale_log2 > 0
+  // and the largest product is the largest score.
+  float scale_log2;
+  uint32_t q_keep, q_flip;
+  unsigned long long wait_limit_ns;
+  long long stall_tile;  // tests of the bounded waits: item * tiles + tile whose copies are withheld
+};
+
+template <int D>
+struct PrefixLayout {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kTileBytes = kPanels * kPanel;  // a Q, K or V tile
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr uint32_t kQ = 1024;  // from a 1 KiB boundary; barriers before it
+  static constexpr uint32_t kRing = kQ + 2 * kTileBytes;
+  static constexpr uint32_t kBytes = kRing + kStages * kTileBytes + 1024;
+};
+
+// mbar_wait that also gives up when another warp has.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, unsigned long long limit,
+                                              const volatile int* abort_flag) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t spin = 1;; ++spin) {
+      if ((ok = mbar_try_wait(bar, parity))) break;
+      if ((spin & 63u) == 0 && (*abort_flag != 0 || global_timer_ns() - t0 > limit)) break;
+    }
   }
-  if (prm.num_queries == 1) return launch_typed<T, 128, 8, 0, false, kWalkRest>(prm, pl, dev, stream);
-  return columns <= 8 ? launch_typed<T, 128, 8, 1, false, kWalkRest>(prm, pl, dev, stream)
-                      : launch_typed<T, 128, 8, 2, false, kWalkRest>(prm, pl, dev, stream);
+  return __all_sync(0xffffffffu, ok);
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// Position in the ring of stages.
+struct Ring {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __grid_constant__ PrefixParams p) {
+  using L = PrefixLayout<D>;
+  constexpr int NS = L::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t bars = base;
+  auto full = [&](int i) { return bars + 8u * i; };
+  auto empty = [&](int i) { return bars + 8u * (NS + i); };
+  const uint32_t q_full = bars + 8u * (2 * NS);
+  auto s_full = [&](int w) { return bars + 8u * (2 * NS + 1 + w); };
+  auto p_full = [&](int w) { return bars + 8u * (2 * NS + 3 + w); };
+  auto o_full = [&](int w) { return bars + 8u * (2 * NS + 5 + w); };
+  const uint32_t drained = bars + 8u * (2 * NS + 7);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 512);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + 516);
+  auto timed_out = [&]() {
+    if (lane == 0) {
+      report(p.error_flag, PA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  };
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 1);
+    }
+    mbar_init(q_full, 256);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(s_full(w), 1);
+      mbar_init(p_full(w), 4);
+      mbar_init(o_full(w), 1);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(smem_addr(smem + 516), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const PrefixWork wk = p.work;
+  const int cta = blockIdx.x;
+  const int64_t ua = wk.cta_start(cta), ub = wk.cta_start(cta + 1);
+  const int first_item = wk.item_of(ua);
+
+  if (warp < 8) {
+    // ---------------- softmax ----------------
+    const int w = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the TMEM lanes
+    const uint32_t s_addr = tmem + lanes + 128u * w, o_addr = tmem + lanes + 256u + (uint32_t)D * w;
+    uint32_t s_phase = 0, o_phase = 0;
+    for (int item = first_item; item < wk.items() && wk.item_start(item) < ub; ++item) {
+      const int t0 = wk.tile_at(item, ua), t1 = wk.tile_at(item, ub);
+      if (t0 >= t1) continue;
+      const bool two = wk.weight(item) == 2;
+      const int head = item / wk.pairs, row0 = (item % wk.pairs) * 2 * kPrefixRows;
+      // The row's queries into the swizzled Q tile: with two row tiles a whole
+      // row per thread, with one a half row.
+      {
+        const int r = row0 + (two ? w * kPrefixRows : 0) + row;
+        constexpr int kUnits = D / 8;  // 16-byte units of a row
+        const int u0 = two ? 0 : w * (kUnits / 2), u1 = two ? kUnits : u0 + kUnits / 2;
+        const uint4* src = nullptr;
+        if (r < p.rows) {
+          const int tok = r / p.group, g = r - tok * p.group;
+          src = reinterpret_cast<const uint4*>(p.q + ((size_t)tok * p.num_heads + head * p.group + g) * D);
+        }
+        unsigned char* dst = smem + L::kQ + (two ? w * L::kTileBytes : 0) + row * 128;
+#pragma unroll 8
+        for (int u = u0; u < u1; ++u) {
+          uint4 v = src != nullptr ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+          v.x = (v.x & p.q_keep) ^ p.q_flip;
+          v.y = (v.y & p.q_keep) ^ p.q_flip;
+          v.z = (v.z & p.q_keep) ^ p.q_flip;
+          v.w = (v.w & p.q_keep) ^ p.q_flip;
+          *reinterpret_cast<uint4*>(dst + (u >> 3) * kPanel + (((u & 7) ^ (row & 7)) << 4)) = v;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        mbar_arrive(q_full);
+      }
+      const int step = two ? 1 : 2;
+      float m = -INFINITY, l = 0.f;
+      bool alive = true;
+      for (int x = t0 + (two ? 0 : w); x < t1; x += step) {
+        if (!wait_or_abort(s_full(w), s_phase, p.wait_limit_ns, abort_flag)) {
+          timed_out();
+          alive = false;
+          break;
+        }
+        s_phase ^= 1u;
+        tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]), s_addr + 32u * c);
+        tmem_wait_load();
+        const int nvalid = p.prefix_tokens - x * kPrefixTokens;
+        if (nvalid < kPrefixTokens) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= nvalid) s[i] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < 128; i += 4)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[i + j]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (m == -INFINITY) {
+          m = top;  // nothing but zero weights so far
+        }
+        const bool moves = (top - m) * p.scale_log2 > kSlack;
+        if (__any_sync(0xffffffffu, moves)) {
+          // The products of the group's earlier tiles are done (the scores were
+          // issued behind them), so O can be scaled here.
+          const float f = moves ? ex2_ftz((m - top) * p.scale_log2) : 1.f;
+          if (moves) m = top;
+          l *= f;
+          if (x >= t0 + step) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_load32(o, o_addr + 32u * c);
+              tmem_wait_load();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_store32(o_addr + 32u * c, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int e = 64 * c + 2 * i;
+            const float a = ex2_ftz(fmaf(s[e], p.scale_log2, neg)), b = ex2_ftz(fmaf(s[e + 1], p.scale_log2, neg));
+            sum[(2 * i) & 3] += a;
+            sum[(2 * i + 1) & 3] += b;
+            // The weights enter the product as bf16: half a step (2^-8 at most,
+            // both signs alike); the sum keeps them in fp32.
+            pk[i] = pack_bf16x2(a, b);
+          }
+          tmem_store32(s_addr + 32u * c, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(w));
+      }
+      if (!alive) break;
+      if (!wait_or_abort(o_full(w), o_phase, p.wait_limit_ns, abort_flag)) {
+        timed_out();
+        break;
+      }
+      o_phase ^= 1u;
+      tc_fence_after();
+      const size_t at = ((size_t)(cta + item) * 2 + w) * kPrefixRows + row;
+      *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m * p.scale_log2, l);
+      if (t0 + (two ? 0 : w) < t1) {  // this group had a tile
+        float4* dst = reinterpret_cast<float4*>(p.part_o + at * D);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_load32(o, o_addr + 32u * c);
+          tmem_wait_load();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[8 * c + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ---------------- loads ----------------
+    if (lane == 0) {
+      prefetch_tensormap(&p.tm_k);
+      prefetch_tensormap(&p.tm_v);
+    }
+    const int boxes = kPrefixTokens / p.box_rows;
+    const int box = lane / L::kPanels, panel = lane % L::kPanels;
+    const bool mine = box < boxes;
+    const uint32_t dst0 = panel * kPanel + box * p.box_rows * 128u;
+    Ring ring;
+    uint32_t armed = 0, armed_phase = 0;  // stages armed, with the parity of their last phase
+    bool alive = true;
+    for (int item = first_item; alive && item < wk.items() && wk.item_start(item) < ub; ++item) {
+      const int t0 = wk.tile_at(item, ua), t1 = wk.tile_at(item, ub);
+      if (t0 >= t1) continue;
+      const int head = item / wk.pairs;
+      // Token row of this lane's box in tile x, -1 for none (zeros then).
+      auto box_row = [&](int x) -> int {
+        const int tok = x * kPrefixTokens + box * p.box_rows;
+        if (!mine || x >= t1 || tok >= p.prefix_tokens) return -1;
+        const int blk = tok / p.block_size, phys = __ldg(p.table + blk);
+        if (p.num_physical_blocks > 0 && (phys < 0 || phys >= p.num_physical_blocks)) {
+          report(p.error_flag, PA_DEVERR_BLOCK_ID);
+          return -1;
+        }
+        return phys * p.block_size + (tok - blk * p.block_size);
+      };
+      auto load = [&](const void* tmap, int row, bool withhold) -> bool {
+        if (!wait_or_abort(empty(ring.i), ring.phase ^ 1u, p.wait_limit_ns, abort_flag)) {
+          timed_out();
+          return false;
+        }
+        if (!withhold) {
+          if (lane == 0) mbar_arrive_expect_tx(full(ring.i), L::kTileBytes);
+          __syncwarp();
+          // A chunk beyond the row's last is outside the tensor: zeros, without a read.
+          if (mine)
+            tma_load_3d(base + L::kRing + ring.i * L::kTileBytes + dst0, tmap, 0,
+                        (row < 0 ? wk.kv_heads : head) * L::kPanels + panel, row < 0 ? 0 : row, full(ring.i));
+          armed |= 1u << ring.i;
+          armed_phase = (armed_phase & ~(1u << ring.i)) | (ring.phase << ring.i);
+        }
+        ring.next(NS);
+        return true;
+      };
+      const int ahead = wk.weight(item) == 2 ? 1 : 2;  // K tiles ahead of the V tile
+      auto stalls = [&](int x) { return (long long)item * wk.tiles + x == p.stall_tile; };
+      int row_v = box_row(t0), row_v1 = box_row(t0 + 1), row_k;
+      alive = load(&p.tm_k, row_v, stalls(t0));
+      if (alive && ahead == 2 && t0 + 1 < t1) alive = load(&p.tm_k, row_v1, stalls(t0 + 1));
+      row_k = ahead == 2 ? box_row(t0 + 2) : row_v1;
+      for (int x = t0; alive && x < t1; ++x) {
+        const int row_next = box_row(x + ahead + 1);
+        alive = load(&p.tm_v, row_v, stalls(x));
+        if (alive && x + ahead < t1) alive = load(&p.tm_k, row_k, stalls(x + ahead));
+        row_v = row_v1;
+        row_v1 = ahead == 2 ? row_k : row_next;
+        row_k = row_next;
+      }
+    }
+    named_barrier_sync(1, kPrefixThreads);
+    if (*abort_flag != 0) {
+      // Copies that were started may still be landing: wait for them (again
+      // bounded) before the CTA's shared memory goes.
+      for (int i = 0; i < NS; ++i)
+        if ((armed >> i) & 1u) (void)mbar_wait(full(i), (armed_phase >> i) & 1u, p.wait_limit_ns);
+    }
+  } else {
+    // ---------------- products ----------------
+    constexpr uint32_t kScores = bf16_product(128, 128, false), kValues = bf16_product(128, D, true);
+    Ring ring;
+    uint32_t q_phase = 0, p_phase[2] = {0u, 0u};
+    bool alive = true;
+    const uint64_t q_op = smem_operand(base + L::kQ, kPanel);
+    for (int item = first_item; alive && item < wk.items() && wk.item_start(item) < ub; ++item) {
+      const int t0 = wk.tile_at(item, ua), t1 = wk.tile_at(item, ub);
+      if (t0 >= t1) continue;
+      const bool two = wk.weight(item) == 2;
+      const int ahead = two ? 1 : 2;
+      auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (wait_or_abort(bar, parity, p.wait_limit_ns, abort_flag)) return true;
+        timed_out();
+        return false;
+      };
+      // S of group w from the K tile in stage `st`.
+      auto scores = [&](int w, int st) {
+        if (lane == 0) {
+          const uint64_t a = q_op + (two ? (w * L::kTileBytes) >> 4 : 0u);
+          const uint64_t b = smem_operand(base + L::kRing + st * L::kTileBytes, kPanel);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * kPanel + (k & 3) * 32u) >> 4;
+            mma_ss(tmem + 128u * w, a + off, b + off, kScores, k > 0);
+          }
+          mma_commit(s_full(w));
+        }
+        __syncwarp();
+      };
+      auto release = [&](int st) {
+        if (lane == 0) mma_commit(empty(st));
+        __syncwarp();
+      };
+      if (!(alive = wait(q_full, q_phase))) break;
+      q_phase ^= 1u;
+      tc_fence_after();
+      // The first K tiles.
+      for (int x = t0; x < t0 + ahead && x < t1; ++x) {
+        if (!(alive = wait(full(ring.i), ring.phase))) break;
+        tc_fence_after();
+        scores(two ? 0 : x - t0, ring.i);
+        if (two) scores(1, ring.i);
+        release(ring.i);
+        ring.next(NS);
+      }
+      for (int x = t0; alive && x < t1; ++x) {
+        const Ring v = ring;
+        ring.next(NS);
+        const Ring k = ring;
+        const bool more = x + ahead < t1;
+        if (more) ring.next(NS);
+        for (int j = 0; j < (two ? 2 : 1); ++j) {
+          const int w = two ? j : (x - t0) & 1;
+          if (j == 0 && !(alive = wait(full(v.i), v.phase))) break;
+          if (!(alive = wait(p_full(w), p_phase[w]))) break;
+          p_phase[w] ^= 1u;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t b = smem_operand(base + L::kRing + v.i * L::kTileBytes, kPanel);
+#pragma unroll
+            for (int kk = 0; kk < kPrefixTokens / 16; ++kk)
+              mma_ts(tmem + 256u + (uint32_t)D * w, tmem + 128u * w + 8u * kk, b + ((kk * 2048u) >> 4), kValues,
+                     kk > 0 || x >= t0 + (two ? 1 : 2));
+          }
+          __syncwarp();
+          if (more) {
+            if (j == 0 && !(alive = wait(full(k.i), k.phase))) break;
+            tc_fence_after();
+            scores(w, k.i);
+          }
+        }
+        if (!alive) break;
+        release(v.i);
+        if (more) release(k.i);
+      }
+      if (!alive) break;
+      if (lane == 0) {
+        mma_commit(o_full(0));
+        mma_commit(o_full(1));
+      }
+      __syncwarp();
+    }
+    // Everything issued is done before tensor memory is freed.
+    if (lane == 0) mma_commit(drained);
+    __syncwarp();
+    (void)mbar_wait_warp(drained, 0, p.wait_limit_ns);
+    named_barrier_sync(1, kPrefixThreads);
+    tc_fence_after();
+    tmem_free(tmem, 512);
+    return;
+  }
+  if (warp < 8) {
+    tc_fence_before();
+    named_barrier_sync(1, kPrefixThreads);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Join: one warp per output row adds the row's partials (of the prefix, when
+// its sequence shares it, and the rest) by log-sum-exp.
+// ---------------------------------------------------------------------------
+struct JoinParams {
+  __nv_bfloat16* out;
+  const int32_t* context_lens;
+  const float* part_ml;
+  const float* part_o;
+  const float* rest_ml;
+  const float* rest_o;
+  PrefixWork work;
+  long long rows;  // num_seqs * num_queries * num_heads
+  int num_queries, num_heads, group, prefix_tokens, max_tokens;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ JoinParams p) {
+  constexpr int DL = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int token = (int)(row / p.num_heads), h = (int)(row - (long long)token * p.num_heads);
+  const int c = min(__ldg(p.context_lens + token / p.num_queries), p.max_tokens);
+  float m = -INFINITY, l = 0.f, acc[DL];
+#pragma unroll
+  for (int i = 0; i < DL; ++i) acc[i] = 0.f;
+  auto add = [&](float w, const float* o) {
+    float v[DL];
+    if constexpr (DL == 4) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(o) + lane);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(o) + lane);
+      v[0] = x.x, v[1] = x.y;
+    }
+#pragma unroll
+    for (int i = 0; i < DL; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+  };
+  {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rest_ml) + row);
+    if (ml.y > 0.f) {
+      m = ml.x;
+      l = ml.y;
+      add(1.f, p.rest_o + row * D);
+    }
+  }
+  if (c >= p.prefix_tokens + p.num_queries - 1) {
+    const int kv = h / p.group;
+    const long long r = (long long)token * p.group + (h - kv * p.group);  // row of the KV head
+    const int pair = (int)(r / (2 * kPrefixRows)), in_pair = (int)(r - (long long)pair * 2 * kPrefixRows);
+    const int item = kv * p.work.pairs + pair;
+    const bool two = p.work.weight(item) == 2;
+    const int c0 = p.work.cta_of(item, 0), c1 = p.work.cta_of(item, p.work.tiles - 1);
+    const int parts = (c1 - c0 + 1) * (two ? 1 : 2);
+    for (int j0 = 0; j0 < parts; j0 += 32) {
+      const int j = j0 + lane, cta = c0 + (two ? j : j >> 1);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      size_t at = 0;
+      if (j < parts) {
+        // A CTA whose range holds no first unit of the item has no partial.
+        const int ta = p.work.tile_at(item, p.work.cta_start(cta)), tb = p.work.tile_at(item, p.work.cta_start(cta + 1));
+        at = ((size_t)(cta + item) * 2 + (two ? in_pair >> 7 : j & 1)) * kPrefixRows + (in_pair & 127);
+        if (ta < tb) ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at);
+      }
+      float top = ml.y > 0.f ? ml.x : -INFINITY;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mn = fmaxf(m, top);
+      if (mn == -INFINITY) continue;
+      const float keep = ex2_ftz(m - mn), w = ml.y > 0.f ? ex2_ftz(ml.x - mn) : 0.f;
+      m = mn;
+      float lw = w * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+      l = l * keep + lw;
+#pragma unroll
+      for (int i = 0; i < DL; ++i) acc[i] *= keep;
+      const int n = min(32, parts - j0);
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const unsigned long long ak = __shfl_sync(0xffffffffu, (unsigned long long)at, k);
+        if (wk != 0.f) add(wk, p.part_o + ak * D);
+      }
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  __nv_bfloat16* out = p.out + row * D + lane * DL;
+  if constexpr (DL == 4) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  } else {
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Scratch: the rest's (m, l) and O rows, the prefix's partials, then what the
+// rest's walk needs.
+struct PrefixScratch {
+  size_t rest_ml, rest_o, part_ml, part_o, walk, total;
+};
+
+PrefixScratch prefix_scratch(int num_seqs, int num_queries, int num_heads, int num_kv_heads, int head_size,
+                             int slots, size_t walk_bytes) {
+  const size_t rows = (size_t)num_seqs * num_queries * num_heads;
+  const size_t part_rows = (size_t)slots * 2 * kPrefixRows;
+  PrefixScratch s;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes, 256);
+    return at;
+  };
+  (void)num_kv_heads;
+  s.rest_ml = take(rows * 8);
+  s.rest_o = take(rows * head_size * 4);
+  s.part_ml = take(part_rows * 8);
+  s.part_o = take(part_rows * head_size * 4);
+  s.walk = take(walk_bytes);
+  s.total = o;
+  return s;
+}
+
+// The slots of the longest list a batch can have: one CTA per SM.
+int most_slots(int num_seqs, int num_queries, int num_heads, int num_kv_heads, int sm_count) {
+  const int64_t rows = (int64_t)num_seqs * num_queries * (num_heads / num_kv_heads);
+  const int64_t pairs = (rows + 2 * kPrefixRows - 1) / (2 * kPrefixRows);
+  return (int)(sm_count + pairs * num_kv_heads);
+}
+
+int make_map(CUtensorMap* tm, const void* pool, int num_kv_heads, int head_size, uint64_t rows, int box_rows) {
+  const EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr) return fail(PA_ERR_CUDA, "pa_decode_prefix: the driver has no cuTensorMapEncodeTiled");
+  const cuuint64_t dims[3] = {64, (cuuint64_t)num_kv_heads * head_size / 64, rows};
+  const cuuint64_t strides[2] = {128, (cuuint64_t)num_kv_heads * head_size * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, estride[3] = {1, 1, 1};
+  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box,
+                         estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(PA_ERR_CUDA, "pa_decode_prefix: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  return PA_OK;
+}
+
+template <int D>
+int launch_prefix(const PrefixParams& prm, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(pa_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       PrefixLayout<D>::kBytes);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(prefix smem)");
+  e = launch_pdl(pa_prefix_kernel<D>, dim3(prm.work.ctas), dim3(kPrefixThreads), PrefixLayout<D>::kBytes, stream,
+                 prm);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefix_kernel");
+}
+
+}  // namespace
 }  // namespace pa
+
+extern "C" size_t pa_decode_prefix_workspace_size(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
+                                                  int head_size) {
+  using namespace pa;
+  const size_t walk = decode_workspace_size_q(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries);
+  DeviceInfo dev{};
+  if (walk == 0 || current_device_info(&dev) != PA_OK) return 0;
+  return prefix_scratch(num_seqs, num_queries, num_heads, num_kv_heads, head_size,
+                        most_slots(num_seqs, num_queries, num_heads, num_kv_heads, dev.sm_count), walk)
+      .total;
+}
+
+extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,
+                                const int32_t* prefix_table, const int32_t* block_tables,
+                                const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
+                                int num_kv_heads, int head_size, int block_size, int num_prefix_blocks,
+                                int max_blocks_per_seq, float scale, void* stream, int dtype,
+                                int num_physical_blocks, void* workspace, size_t workspace_bytes,
+                                int32_t* error_flag) {
+  using namespace pa;
+  clear_error();
+  if (num_prefix_blocks < 0 || (num_prefix_blocks > 0 && prefix_table == nullptr))
+    return fail(PA_ERR_INVALID_ARG, "pa_decode_prefix: %d prefix blocks without a table", num_prefix_blocks);
+  if (num_prefix_blocks > max_blocks_per_seq)
+    return fail(PA_ERR_INVALID_ARG, "pa_decode_prefix: prefix of %d blocks in tables of %d", num_prefix_blocks,
+                max_blocks_per_seq);
+  if (!aligned(prefix_table, 4)) return fail(PA_ERR_INVALID_ARG, "pa_decode_prefix: misaligned prefix_table");
+  if (dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: bf16 only");
+  if (block_size > 0 && block_size % 8 != 0)
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: block_size %d is not a multiple of 8", block_size);
+  int rc = decode_validate(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries,
+                           num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, dtype,
+                           num_physical_blocks);
+  if (rc != PA_OK) return rc;
+  DeviceInfo dev{};
+  rc = current_device_info(&dev);
+  if (rc != PA_OK) return rc;
+  const size_t walk_bytes =
+      decode_workspace_size_q(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries);
+  const PrefixScratch sc = prefix_scratch(num_seqs, num_queries, num_heads, num_kv_heads, head_size,
+                                          most_slots(num_seqs, num_queries, num_heads, num_kv_heads, dev.sm_count),
+                                          walk_bytes);
+  const bool own = workspace == nullptr;
+  int32_t* tickets = nullptr;
+  if (own) {
+    rc = kept_scratch(sc.total, sizeof(int32_t) * (size_t)num_seqs * num_kv_heads, stream, &workspace, &tickets);
+    if (rc != PA_OK) return rc;
+  } else {
+    if (workspace_bytes < sc.total)
+      return fail(PA_ERR_WORKSPACE, "pa_decode_prefix: workspace of %zu bytes, %zu needed", workspace_bytes,
+                  sc.total);
+    if (!aligned(workspace, 256))
+      return fail(PA_ERR_INVALID_ARG, "pa_decode_prefix: workspace not 256-byte aligned");
+  }
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int prefix_tokens = num_prefix_blocks * block_size;
+  const int group = num_heads / num_kv_heads;
+  const int64_t rows = (int64_t)num_seqs * num_queries * group;
+  PrefixParams prm{};
+  if (num_prefix_blocks > 0) {
+    const uint64_t pool_rows = num_physical_blocks > 0 ? (uint64_t)num_physical_blocks * block_size : 1ull << 31;
+    if (pool_rows > 1ull << 31 || rows > 1 << 30)
+      return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %llu token rows in the pool (at most 2^31)",
+                  (unsigned long long)pool_rows);
+    prm.box_rows = block_size & -block_size;
+    if (prm.box_rows > kPrefixTokens) prm.box_rows = kPrefixTokens;
+    rc = make_map(&prm.tm_k, k_cache, num_kv_heads, head_size, pool_rows, prm.box_rows);
+    if (rc == PA_OK) rc = make_map(&prm.tm_v, v_cache, num_kv_heads, head_size, pool_rows, prm.box_rows);
+    if (rc != PA_OK) return rc;
+    prm.q = static_cast<const __nv_bfloat16*>(query);
+    prm.table = prefix_table;
+    prm.error_flag = error_flag;
+    prm.part_ml = reinterpret_cast<float*>(ws + sc.part_ml);
+    prm.part_o = reinterpret_cast<float*>(ws + sc.part_o);
+    prm.work = make_prefix_work(rows, num_kv_heads, prefix_tokens, dev.sm_count);
+    prm.rows = (int)rows;
+    prm.group = group;
+    prm.num_heads = num_heads;
+    prm.block_size = block_size;
+    prm.prefix_tokens = prefix_tokens;
+    prm.num_physical_blocks = num_physical_blocks;
+    prm.scale_log2 = scale != 0.f ? (float)(std::fabs((double)scale) * 1.4426950408889634) : 1.f;
+    prm.q_keep = scale != 0.f ? 0xffffffffu : 0u;
+    prm.q_flip = scale < 0.f ? 0x80008000u : 0u;
+    take_wait_test(&prm.stall_tile, &prm.wait_limit_ns);
+    rc = head_size == 64 ? launch_prefix<64>(prm, st) : launch_prefix<128>(prm, st);
+    if (rc != PA_OK) return rc;
+  }
+  DecodeExtras ex{};
+  ex.walk = kWalkRest;
+  ex.prefix_tokens = prefix_tokens;
+  ex.rest_ml = reinterpret_cast<float*>(ws + sc.rest_ml);
+  ex.rest_o = reinterpret_cast<float*>(ws + sc.rest_o);
+  ex.tickets = tickets;
+  rc = decode_impl_q(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries, num_heads,
+                     num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, stream, dtype,
+                     num_physical_blocks, ws + sc.walk, walk_bytes, 0, error_flag, false, 1.f, 1.f, nullptr, nullptr,
+                     nullptr, &ex);
+  if (rc != PA_OK) return rc;
+  JoinParams jp{};
+  jp.out = static_cast<__nv_bfloat16*>(out);
+  jp.context_lens = context_lens;
+  jp.part_ml = prm.part_ml;
+  jp.part_o = prm.part_o;
+  jp.rest_ml = ex.rest_ml;
+  jp.rest_o = ex.rest_o;
+  jp.work = prm.work;
+  jp.rows = (long long)num_seqs * num_queries * num_heads;
+  jp.num_queries = num_queries;
+  jp.num_heads = num_heads;
+  jp.group = group;
+  jp.prefix_tokens = num_prefix_blocks > 0 ? prefix_tokens : 1 << 30;  // without one nobody shares it
+  jp.max_tokens = max_blocks_per_seq * block_size;
+  const dim3 grid((unsigned)((jp.rows + 7) / 8));
+  const cudaError_t e = head_size == 64 ? launch_pdl(pa_prefix_join<64>, grid, dim3(256), 0, st, jp)
+                                        : launch_pdl(pa_prefix_join<128>, grid, dim3(256), 0, st, jp);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefix_join");
+}

@@ -2,6 +2,8 @@
 // instantiate it (one per kind of walk, compiled in parallel).
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -58,6 +60,10 @@ int launch_typed(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t 
   if (e != cudaSuccess) return cuda_fail(e, "launch pa_decode_kernel");
   return PA_OK;
 }
+
+// The driver's encoder of tensor maps (nullptr if it has none).
+using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
+EncodeTiledFn encode_tiled_fn();
 
 // The kernel variants of the other translation units.
 int launch_mod(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool f32,
