@@ -35,7 +35,11 @@
 namespace pa {
 namespace {
 
-constexpr int kPrefixThreads = 320;
+constexpr int kPrefixThreads = 384;
+// Registers per thread: 168 at launch (65536 / 384, rounded down); the softmax
+// groups hold a row of 128 scores each, the third warpgroup issues copies and
+// products.  2 * 128 * 216 + 128 * 72 = 384 * 168.
+constexpr int kSoftmaxRegisters = 216, kIssueRegisters = 72;
 constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
 // A running maximum is kept until a tile exceeds it by this factor (log2): until
 // then weights are at most 2^8, which bf16 and the fp32 sums hold as well as 1.
@@ -47,7 +51,7 @@ struct PrefixParams {
   const int32_t* table;
   int32_t* error_flag;
   float* part_ml;  // [slots][2][128][2]
-  float* part_o;   // [slots][2][128][D]
+  float* part_o;   // [slots][2][D / 4][128][4]: a thread's row side by side with its neighbours'
   PrefixWork work;
   int rows;  // query rows per KV head
   int group, num_heads, block_size, prefix_tokens, num_physical_blocks, box_rows;
@@ -156,6 +160,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   const int64_t ua = wk.cta_start(cta), ub = wk.cta_start(cta + 1);
   const int first_item = wk.item_of(ua);
 
+  if (warp < 8)
+    registers_up<kSoftmaxRegisters>();
+  else
+    registers_down<kIssueRegisters>();
+
   if (warp < 8) {
     // ---------------- softmax ----------------
     const int w = warp >> 2, row = tid & 127;
@@ -203,22 +212,38 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
         }
         s_phase ^= 1u;
         tc_fence_after();
+        // Two halves, so that the second one's load runs under the first one's maximum.
         float s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
+        auto fetch = [&](int c) {
           tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]), s_addr + 32u * c);
+        };
+        fetch(0);
+        fetch(1);
         tmem_wait_load();
+        fetch(2);
+        fetch(3);
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < 64; i += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mx[j] = i + 4 < 64 ? fmaxf(fmaxf(mx[j], s[i + j]), s[i + 4 + j]) : fmaxf(mx[j], s[i + j]);
+        tmem_wait_load();
+#pragma unroll
+        for (int i = 64; i < 128; i += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], s[i + j]), s[i + 4 + j]);
         const int nvalid = p.prefix_tokens - x * kPrefixTokens;
-        if (nvalid < kPrefixTokens) {
+        if (nvalid < kPrefixTokens) {  // the prefix's last tile
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (i >= nvalid) s[i] = -INFINITY;
+          mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 128; i += 4)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[i + j]);
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int i = 4; i < 128; i += 4)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[i + j]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (m == -INFINITY) {
           m = top;  // nothing but zero weights so far
@@ -243,23 +268,30 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
           }
         }
         const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), neg2 = pair(neg, neg);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int e = 64 * c + 2 * i;
-            const float a = ex2_ftz(fmaf(s[e], p.scale_log2, neg)), b = ex2_ftz(fmaf(s[e + 1], p.scale_log2, neg));
-            sum[(2 * i) & 3] += a;
-            sum[(2 * i + 1) & 3] += b;
+            float a, b;
+            unpair(fma_pair(pair(s[e], s[e + 1]), scale2, neg2), a, b);
+            a = ex2_ftz(a);
+            b = ex2_ftz(b);
+            sum[i & 1] = add_pair(sum[i & 1], pair(a, b));
             // The weights enter the product as bf16: half a step (2^-8 at most,
             // both signs alike); the sum keeps them in fp32.
             pk[i] = pack_bf16x2(a, b);
           }
           tmem_store32(s_addr + 32u * c, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        {
+          float a, b;
+          unpair(add_pair(sum[0], sum[1]), a, b);
+          l += a + b;
+        }
         tmem_wait_store();
         tc_fence_before();
         __syncwarp();
@@ -275,7 +307,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
       const size_t at = ((size_t)(cta + item) * 2 + w) * kPrefixRows + row;
       *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m * p.scale_log2, l);
       if (t0 + (two ? 0 : w) < t1) {  // this group had a tile
-        float4* dst = reinterpret_cast<float4*>(p.part_o + at * D);
+        float4* dst = reinterpret_cast<float4*>(p.part_o) + (at - row) * (D / 4) + row;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -283,7 +315,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
           tmem_wait_load();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[8 * c + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+            dst[(8 * c + i) * kPrefixRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                          __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
       }
@@ -356,7 +388,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
       for (int i = 0; i < NS; ++i)
         if ((armed >> i) & 1u) (void)mbar_wait(full(i), (armed_phase >> i) & 1u, p.wait_limit_ns);
     }
-  } else {
+  } else if (warp == 9) {
     // ---------------- products ----------------
     constexpr uint32_t kScores = bf16_product(128, 128, false), kValues = bf16_product(128, D, true);
     Ring ring;
@@ -449,15 +481,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
     tmem_free(tmem, 512);
     return;
   }
-  if (warp < 8) {
+  if (warp < 8 || warp > 9) {  // (warps 10 and 11 only fill their warpgroup)
     tc_fence_before();
     named_barrier_sync(1, kPrefixThreads);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Join: one warp per output row adds the row's partials (of the prefix, when
-// its sequence shares it, and the rest) by log-sum-exp.
+// Join: a warp adds the partials of two neighbouring rows of a KV head (of the
+// prefix, when their sequences share it, and the rest) by log-sum-exp.  Two,
+// because a partial's rows lie side by side, four dims of each: a lane reads both
+// rows' dims as one 32-byte sector.
 // ---------------------------------------------------------------------------
 struct JoinParams {
   __nv_bfloat16* out;
@@ -467,90 +501,108 @@ struct JoinParams {
   const float* rest_ml;
   const float* rest_o;
   PrefixWork work;
-  long long rows;  // num_seqs * num_queries * num_heads
-  int num_queries, num_heads, group, prefix_tokens, max_tokens;
+  int rows;   // query rows per KV head
+  int pairs;  // of them, rounded up
+  int num_kv_heads, num_queries, num_heads, group, prefix_tokens, max_tokens;
 };
 
 template <int D>
 __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ JoinParams p) {
-  constexpr int DL = D / 32;
+  constexpr int kLanes = D / 4;  // lanes that hold four dims of each row
   const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
+  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (unit >= (long long)p.pairs * p.num_kv_heads) return;
   griddep_wait();
   griddep_launch_dependents();
-  const int token = (int)(row / p.num_heads), h = (int)(row - (long long)token * p.num_heads);
-  const int c = min(__ldg(p.context_lens + token / p.num_queries), p.max_tokens);
-  float m = -INFINITY, l = 0.f, acc[DL];
+  const int kv = (int)(unit / p.pairs), r0 = 2 * (int)(unit - (long long)kv * p.pairs);
+  const int n = min(2, p.rows - r0);
+  const bool holds = lane < kLanes;
+  long long row[2];  // output row
+  bool shares[2];
+  float m[2], l[2], acc[2][4];
 #pragma unroll
-  for (int i = 0; i < DL; ++i) acc[i] = 0.f;
-  auto add = [&](float w, const float* o) {
-    float v[DL];
-    if constexpr (DL == 4) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(o) + lane);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(o) + lane);
-      v[0] = x.x, v[1] = x.y;
-    }
-#pragma unroll
-    for (int i = 0; i < DL; ++i) acc[i] = fmaf(w, v[i], acc[i]);
-  };
-  {
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rest_ml) + row);
-    if (ml.y > 0.f) {
-      m = ml.x;
-      l = ml.y;
-      add(1.f, p.rest_o + row * D);
-    }
+  for (int i = 0; i < 2; ++i) {
+    const int r = min(r0 + i, p.rows - 1), token = r / p.group;
+    row[i] = (long long)token * p.num_heads + kv * p.group + (r - token * p.group);
+    const int c = min(__ldg(p.context_lens + token / p.num_queries), p.max_tokens);
+    shares[i] = c >= p.prefix_tokens + p.num_queries - 1;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rest_ml) + row[i]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ml.y > 0.f && holds) o = __ldcg(reinterpret_cast<const float4*>(p.rest_o + row[i] * D) + lane);
+    m[i] = ml.y > 0.f ? ml.x : -INFINITY;
+    l[i] = ml.y > 0.f ? ml.y : 0.f;
+    acc[i][0] = o.x, acc[i][1] = o.y, acc[i][2] = o.z, acc[i][3] = o.w;
   }
-  if (c >= p.prefix_tokens + p.num_queries - 1) {
-    const int kv = h / p.group;
-    const long long r = (long long)token * p.group + (h - kv * p.group);  // row of the KV head
-    const int pair = (int)(r / (2 * kPrefixRows)), in_pair = (int)(r - (long long)pair * 2 * kPrefixRows);
+  if (shares[0] || shares[1]) {
+    const int pair = r0 / (2 * kPrefixRows), in_pair = r0 - pair * 2 * kPrefixRows;
     const int item = kv * p.work.pairs + pair;
     const bool two = p.work.weight(item) == 2;
     const int c0 = p.work.cta_of(item, 0), c1 = p.work.cta_of(item, p.work.tiles - 1);
     const int parts = (c1 - c0 + 1) * (two ? 1 : 2);
     for (int j0 = 0; j0 < parts; j0 += 32) {
       const int j = j0 + lane, cta = c0 + (two ? j : j >> 1);
-      float2 ml = make_float2(-INFINITY, 0.f);
-      size_t at = 0;
+      float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);  // (m, l) of both rows
+      int at = 0;  // partial: slot and softmax group
       if (j < parts) {
         // A CTA whose range holds no first unit of the item has no partial.
         const int ta = p.work.tile_at(item, p.work.cta_start(cta)), tb = p.work.tile_at(item, p.work.cta_start(cta + 1));
-        at = ((size_t)(cta + item) * 2 + (two ? in_pair >> 7 : j & 1)) * kPrefixRows + (in_pair & 127);
-        if (ta < tb) ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at);
+        at = (cta + item) * 2 + (two ? in_pair >> 7 : j & 1);
+        if (ta < tb)
+          ml = __ldcg(reinterpret_cast<const float4*>(
+              p.part_ml + ((size_t)at * kPrefixRows + (in_pair & 127)) * 2));
       }
-      float top = ml.y > 0.f ? ml.x : -INFINITY;
+      float w[2];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float mn = fmaxf(m, top);
-      if (mn == -INFINITY) continue;
-      const float keep = ex2_ftz(m - mn), w = ml.y > 0.f ? ex2_ftz(ml.x - mn) : 0.f;
-      m = mn;
-      float lw = w * ml.y;
+      for (int i = 0; i < 2; ++i) {
+        const float pm = i ? ml.z : ml.x, pl = i ? ml.w : ml.y;
+        const bool some = shares[i] && pl > 0.f;
+        float top = some ? pm : -INFINITY;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-      l = l * keep + lw;
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float mn = fmaxf(m[i], top), ref = mn == -INFINITY ? 0.f : mn;
+        const float keep = ex2_ftz(m[i] - ref);
+        w[i] = some ? ex2_ftz(pm - ref) : 0.f;
+        m[i] = mn;
+        float lw = some ? w[i] * pl : 0.f;
 #pragma unroll
-      for (int i = 0; i < DL; ++i) acc[i] *= keep;
-      const int n = min(32, parts - j0);
+        for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+        l[i] = l[i] * keep + lw;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] *= keep;
+      }
+      const int here = min(32, parts - j0);
 #pragma unroll 4
-      for (int k = 0; k < n; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const unsigned long long ak = __shfl_sync(0xffffffffu, (unsigned long long)at, k);
-        if (wk != 0.f) add(wk, p.part_o + ak * D);
+      for (int k = 0; k < here; ++k) {
+        const float w0 = __shfl_sync(0xffffffffu, w[0], k), w1 = __shfl_sync(0xffffffffu, w[1], k);
+        const int ak = __shfl_sync(0xffffffffu, at, k);
+        // A partial without weight may hold anything.
+        if (holds && (w0 != 0.f || w1 != 0.f)) {
+          const float4* o = reinterpret_cast<const float4*>(p.part_o) +
+                            ((size_t)ak * (D / 4) + lane) * kPrefixRows + (in_pair & 127);
+          const float4 a = __ldcg(o), b = __ldcg(o + 1);
+          if (w0 != 0.f) {
+            acc[0][0] = fmaf(w0, a.x, acc[0][0]);
+            acc[0][1] = fmaf(w0, a.y, acc[0][1]);
+            acc[0][2] = fmaf(w0, a.z, acc[0][2]);
+            acc[0][3] = fmaf(w0, a.w, acc[0][3]);
+          }
+          if (w1 != 0.f) {
+            acc[1][0] = fmaf(w1, b.x, acc[1][0]);
+            acc[1][1] = fmaf(w1, b.y, acc[1][1]);
+            acc[1][2] = fmaf(w1, b.z, acc[1][2]);
+            acc[1][3] = fmaf(w1, b.w, acc[1][3]);
+          }
+        }
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  __nv_bfloat16* out = p.out + row * D + lane * DL;
-  if constexpr (DL == 4) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  } else {
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i < n && holds) {
+      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+      *reinterpret_cast<uint2*>(p.out + row[i] * D + 4 * lane) =
+          make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
+    }
   }
 }
 
@@ -678,9 +730,10 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   const int group = num_heads / num_kv_heads;
   const int64_t rows = (int64_t)num_seqs * num_queries * group;
   PrefixParams prm{};
+  if (rows > 1 << 30) return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %lld query rows", (long long)rows);
   if (num_prefix_blocks > 0) {
     const uint64_t pool_rows = num_physical_blocks > 0 ? (uint64_t)num_physical_blocks * block_size : 1ull << 31;
-    if (pool_rows > 1ull << 31 || rows > 1 << 30)
+    if (pool_rows > 1ull << 31)
       return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %llu token rows in the pool (at most 2^31)",
                   (unsigned long long)pool_rows);
     prm.box_rows = block_size & -block_size;
@@ -726,13 +779,15 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   jp.rest_ml = ex.rest_ml;
   jp.rest_o = ex.rest_o;
   jp.work = prm.work;
-  jp.rows = (long long)num_seqs * num_queries * num_heads;
+  jp.rows = (int)rows;
+  jp.pairs = (int)((rows + 1) / 2);
+  jp.num_kv_heads = num_kv_heads;
   jp.num_queries = num_queries;
   jp.num_heads = num_heads;
   jp.group = group;
   jp.prefix_tokens = num_prefix_blocks > 0 ? prefix_tokens : 1 << 30;  // without one nobody shares it
   jp.max_tokens = max_blocks_per_seq * block_size;
-  const dim3 grid((unsigned)((jp.rows + 7) / 8));
+  const dim3 grid((unsigned)(((long long)jp.pairs * num_kv_heads + 7) / 8));
   const cudaError_t e = head_size == 64 ? launch_pdl(pa_prefix_join<64>, grid, dim3(256), 0, st, jp)
                                         : launch_pdl(pa_prefix_join<128>, grid, dim3(256), 0, st, jp);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefix_join");
