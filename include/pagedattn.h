@@ -250,11 +250,14 @@ int pa_decode_mq_append(void* out, const void* query, const void* k_new, const v
  * left behind can be freed.  A token that some query of the sequence sees must
  * be finite for the others too.
  * Types: PA_F32 (num_queries == 1) or PA_BF16; (num_heads / num_kv_heads) *
- * num_queries <= 32.  Scratch as in pa_decode_mq (pa_decode_mq_workspace_size),
- * except that a caller's scratch may hold anything before a call, and that
- * scratch of the library's own (workspace NULL) is refused while `stream` is
- * being captured (PA_ERR_INVALID_ARG).  Two calls that may overlap in time need
- * scratch of their own.  Other arguments as in pa_decode_mq.
+ * num_queries <= 32.
+ * workspace    256-byte aligned device scratch of at least
+ *              pa_decode_mod_workspace_size(...) bytes, of any content; NULL: the
+ *              library's own, refused while `stream` is being captured
+ *              (PA_ERR_INVALID_ARG).  Two calls that may overlap in time need
+ *              scratch of their own.
+ * Other arguments as in pa_decode_mq.  The call makes two launches: the walk, and
+ * a merge of the sequences that range boundaries cut.
  *
  * pa_decode_fp8_mod - the same over FP8 pools: keys and values as in
  * pa_decode_fp8, query and out bf16.
@@ -273,6 +276,11 @@ int pa_decode_fp8_mod(void* out, const void* query, const void* k_cache, const v
                       const float* alibi_slopes, int window, const int32_t* first_tokens,
                       const int32_t* prefix_lens, void* stream, int num_physical_blocks, void* workspace,
                       size_t workspace_bytes, int num_ranges, int32_t* error_flag);
+
+/* Scratch bytes pa_decode_mod (kv_dtype PA_F32 or PA_BF16) or pa_decode_fp8_mod
+ * (PA_FP8_E4M3) needs on the current device (0 for invalid sizes). */
+size_t pa_decode_mod_workspace_size(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
+                                    int head_size, int kv_dtype, int num_ranges);
 
 /*
  * pa_decode_prefix - pa_decode_mq for a batch whose sequences share a long

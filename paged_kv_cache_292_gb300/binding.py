@@ -118,6 +118,7 @@ _SIGS = {
         [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, ctypes.c_float, ctypes.c_float,
          ctypes.c_float, _P, _I, _P, _P, _P, _I, _P, _SZ, _I, _P],
     ),
+    "pa_decode_mod_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "pa_decode_prefix": (
         _I,
         [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _I, _I, _P, _SZ, _P],
@@ -654,6 +655,12 @@ def pa_decode_fp8_mod(out, query, k_cache, v_cache, block_tables, context_lens, 
                                     _ptr(alibi_slopes), window, _ptr(first_tokens), _ptr(prefix_lens),
                                     _stream(stream), num_physical_blocks, _ptr(workspace), workspace_bytes,
                                     num_ranges, _ptr(error_flag)))
+
+
+def pa_decode_mod_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads, head_size, kv_dtype,
+                                 num_ranges=0) -> int:
+    return int(load().pa_decode_mod_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads, head_size,
+                                                   kv_dtype, num_ranges))
 
 
 def _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out):

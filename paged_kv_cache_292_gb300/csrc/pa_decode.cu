@@ -72,6 +72,10 @@ int heads_per_cta(int num_kv_heads, int head_size, int elt, int max_heads = kMax
 // per warp, so ceil(columns / 8) (at most 4: 32 columns).
 int column_split(int group, int num_queries) { return (group * num_queries + 7) / 8; }
 
+// CTAs of this many warps that fit on an SM's registers at 168 a thread (three
+// warps per quarter).
+int ctas_per_sm(int warps) { return warps <= 12 ? 12 / warps : 1; }
+
 int default_ranges(const DeviceInfo& dev, int HG) {
   const int r = dev.sm_count / HG;
   return r < 1 ? 1 : r;
@@ -88,16 +92,18 @@ int gcd_int(int a, int b) {
 
 // elt: bytes of a pool element; q_elt: bytes of a query element (bf16 queries
 // select the tensor-core consumers, whose stages are swizzled tensor boxes).
+// spread: CTAs of few warps (few KV heads, or few per group) get as many ranges
+// per SM as fit there: their consumers wait on latency, not on HBM.
 int make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int elt,
               int num_ranges, const DeviceInfo& dev, Plan* pl, int num_queries = 1,
-              int q_elt = 0, int block_size = 16) {
+              int q_elt = 0, int block_size = 16, bool spread = false) {
   if (q_elt == 0) q_elt = elt;
   const int G = num_heads / num_kv_heads;
   const bool mma = q_elt == 2;
   pl->split = column_split(G, num_queries);
   pl->Hg = heads_per_cta(num_kv_heads, head_size, elt, kMaxGroupHeads / pl->split);
   pl->HG = num_kv_heads / pl->Hg;
-  pl->R = num_ranges > 0 ? num_ranges : default_ranges(dev, pl->HG);
+  int per_sm = spread ? ctas_per_sm(pl->Hg * pl->split + kProducers) : 1;
   pl->row_bytes = (uint32_t)(pl->Hg * head_size * elt);
   pl->q_bytes = (uint32_t)(num_queries * pl->Hg * G * head_size * q_elt);
   pl->lines = pl->box_rows = pl->box_bytes = 0;
@@ -125,13 +131,19 @@ int make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int 
   pl->stage_bytes = 2u * kTile * pl->pitch;
   pl->stages = 0;
   const int pref[][2] = {{6, 2}, {5, 2}, {4, 2}, {3, 2}, {3, 1}, {2, 2}, {2, 1}};
-  for (auto& c : pref) {
-    const Layout L = make_layout(c[0], c[1], pl->q_bytes, pl->stage_bytes, mma);
-    if ((int)L.total <= dev.max_smem_optin) {
-      pl->stages = c[0];
-      pl->q_slots = c[1];
-      pl->smem = L.total;
-      break;
+  for (; per_sm > 0 && pl->stages == 0; --per_sm) {
+    // An SM has 228 KiB, of which each of its CTAs takes 1 KiB besides its own.
+    const int room = per_sm > 1 ? (228 << 10) / per_sm - 1024 : dev.max_smem_optin;
+    const int least = per_sm > 1 ? 4 : 0;  // fewer CTAs rather than a shorter ring
+    for (auto& c : pref) {
+      const Layout L = make_layout(c[0], c[1], pl->q_bytes, pl->stage_bytes, mma);
+      if ((int)L.total <= room && c[0] >= least) {
+        pl->stages = c[0];
+        pl->q_slots = c[1];
+        pl->smem = L.total;
+        pl->R = num_ranges > 0 ? num_ranges : default_ranges(dev, pl->HG) * per_sm;
+        break;
+      }
     }
   }
   if (pl->stages == 0)
@@ -301,7 +313,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
                   int num_physical_blocks, void* workspace, size_t workspace_bytes, int num_ranges,
                   int32_t* error_flag, bool kv_fp8, float k_scale,
                   float v_scale, const void* k_new, const void* v_new,
-                  ScratchProvider fixed_scratch, const DecodeExtras* extras) {
+                  ScratchProvider fixed_scratch, DecodeExtras* extras) {
   clear_error();
   if (k_new != nullptr || v_new != nullptr) {
     if (k_new == nullptr || v_new == nullptr)
@@ -325,19 +337,26 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   const int elt = dtype == PA_F32 ? 4 : 2;
   Plan pl{};
   rc = make_plan(num_seqs, num_heads, num_kv_heads, head_size, kv_fp8 ? 1 : elt, num_ranges, dev, &pl,
-                 num_queries, elt, block_size);
+                 num_queries, elt, block_size, extras != nullptr);
   if (rc != PA_OK) return rc;
   int32_t* counters = nullptr;
-  bool clear_tickets = workspace == nullptr && fixed_scratch != nullptr;
-  if (extras != nullptr && workspace == nullptr) {
-    rc = kept_scratch(pl.ws_partials, pl.ws_counters, stream, &workspace, &counters);
-    if (rc != PA_OK) return rc;
+  const bool clear_tickets = workspace == nullptr && fixed_scratch != nullptr;
+  if (extras != nullptr) {
+    const size_t need = pl.ws_partials + sizeof(int4) * (size_t)num_seqs;
+    if (workspace == nullptr) {
+      rc = kept_scratch(need, stream, &workspace);
+      if (rc != PA_OK) return rc;
+    } else if (workspace_bytes < need) {
+      return fail(PA_ERR_WORKSPACE, "pa_decode: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    } else if (!aligned(workspace, 256)) {
+      return fail(PA_ERR_INVALID_ARG, "pa_decode: workspace not 256-byte aligned");
+    }
   } else if (clear_tickets) {
     rc = fixed_scratch(pl.ws_total, &workspace);
     if (rc != PA_OK) return rc;
     workspace_bytes = pl.ws_total;
   }
-  if (counters != nullptr) {
+  if (extras != nullptr) {
   } else if (workspace == nullptr) {
     rc = library_workspace(pl.ws_partials, &workspace);
     if (rc != PA_OK) return rc;
@@ -351,10 +370,6 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
     const size_t cnt_bytes = sizeof(int32_t) * (size_t)num_seqs * num_kv_heads;
     counters = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) +
                                           ((workspace_bytes - cnt_bytes) & ~(size_t)255));
-    if (extras != nullptr && extras->tickets != nullptr)
-      counters = extras->tickets;
-    else if (extras != nullptr)
-      clear_tickets = true;  // the caller's scratch may hold anything
   }
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   DecodeParams prm{};
@@ -399,6 +414,13 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   prm.k_scale = k_scale;
   prm.k_new = k_new;
   prm.v_new = v_new;
+  if (extras != nullptr) {
+    prm.sm_count = dev.sm_count;
+    prm.cuts = reinterpret_cast<int4*>(ws + pl.ws_partials);
+    extras->cuts = prm.cuts;
+    extras->part_ml = prm.part_ml;
+    extras->part_o = prm.part_o;
+  }
   prm.window = kNoWindow;
   if (extras != nullptr && extras->walk == kWalkMod) {
     const double log2e = 1.4426950408889634;
@@ -412,6 +434,8 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
     if (extras->window > 0 && extras->window < kNoWindow) prm.window = extras->window;
   } else if (extras != nullptr) {
     prm.prefix_tokens = extras->prefix_tokens;
+    prm.beside = extras->prefix_units > 0.f;
+    prm.prefix_units = extras->prefix_units;
     prm.rest_ml = extras->rest_ml;
     prm.rest_o = extras->rest_o;
   }
@@ -471,6 +495,29 @@ size_t decode_workspace_size_q(int num_seqs, int num_heads, int num_kv_heads, in
     R = default_ranges(dev, num_kv_heads / heads_per_cta(num_kv_heads, head_size, 2, kMaxGroupHeads / split));
   }
   return workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, R, nullptr, num_queries);
+}
+
+size_t walk_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size, int num_ranges,
+                           int num_queries, int elt) {
+  if (num_queries < 1 || num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+      num_ranges < 0 || num_heads % num_kv_heads != 0)
+    return 0;
+  int R = num_ranges;
+  if (R == 0) {
+    DeviceInfo dev{};
+    if (current_device_info(&dev) != PA_OK) return 0;
+    const WalkShape w = walk_shape(num_heads, num_kv_heads, head_size, num_queries, elt);
+    R = default_ranges(dev, w.groups) * ctas_per_sm(w.warps);
+  }
+  Plan pl{};
+  workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, R, &pl, num_queries);
+  return pl.ws_partials + sizeof(int4) * (size_t)num_seqs;
+}
+
+WalkShape walk_shape(int num_heads, int num_kv_heads, int head_size, int num_queries, int elt) {
+  const int split = column_split(num_heads / num_kv_heads, num_queries);
+  const int hg = split > kMaxGroupHeads ? 1 : heads_per_cta(num_kv_heads, head_size, elt, kMaxGroupHeads / split);
+  return WalkShape{num_kv_heads / hg, hg * split + kProducers, hg * head_size * elt};
 }
 
 size_t decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,

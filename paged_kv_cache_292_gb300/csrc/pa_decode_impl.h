@@ -1,6 +1,8 @@
 // The general decode call behind the C entry points of several translation units.
 #pragma once
 
+#include <vector_types.h>
+
 #include "pa_internal.h"
 
 namespace pa {
@@ -16,11 +18,25 @@ struct DecodeExtras {
   const int32_t* prefix_lens = nullptr;
   // kWalkRest: the tokens behind a shared prefix, left as (m, l, O) rows
   int prefix_tokens = 0;
+  float prefix_units = 0.f;  // work of the prefix kernel launched just before (0: none)
   float* rest_ml = nullptr;
   float* rest_o = nullptr;
-  // Merge tickets that are zero between calls, when the scratch has none of its own.
-  int32_t* tickets = nullptr;
+  // Set by the call, inside its scratch: how sequences were cut, and the partials.
+  int4* cuts = nullptr;
+  const float* part_ml = nullptr;
+  const float* part_o = nullptr;
 };
+
+// Shape of a walk's CTAs: KV-head groups, warps, bytes of a staged K row.
+struct WalkShape {
+  int groups, warps, row_bytes;
+};
+WalkShape walk_shape(int num_heads, int num_kv_heads, int head_size, int num_queries, int elt);
+
+// Scratch of a call with extras (num_ranges 0: the default; elt: bytes of a pool
+// element).  0 for invalid sizes.
+size_t walk_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size, int num_ranges,
+                           int num_queries, int elt);
 
 // The argument checks every decode call makes.
 int decode_validate(const void* out, const void* query, const void* k_cache, const void* v_cache,
@@ -35,9 +51,6 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
                   int num_physical_blocks, void* workspace, size_t workspace_bytes, int num_ranges,
                   int32_t* error_flag, bool kv_fp8 = false, float k_scale = 1.f,
                   float v_scale = 1.f, const void* k_new = nullptr, const void* v_new = nullptr,
-                  ScratchProvider fixed_scratch = nullptr, const DecodeExtras* extras = nullptr);
-
-size_t decode_workspace_size_q(int num_seqs, int num_heads, int num_kv_heads, int head_size,
-                               int num_ranges, int num_queries);
+                  ScratchProvider fixed_scratch = nullptr, DecodeExtras* extras = nullptr);
 
 }  // namespace pa

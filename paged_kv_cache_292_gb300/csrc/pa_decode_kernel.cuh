@@ -88,6 +88,10 @@ enum : int {
 };
 constexpr int kNoWindow = 1 << 30;  // longer than any context
 
+// SeqCut, what the walks other than kWalkAll leave per sequence: (first range,
+// last range, slot of the first range's partial, state).
+enum : int { kCutEmpty = 0, kCutWhole = 1, kCutMerge = 2 };
+
 struct StageMeta {
   int seq;     // sequence index
   int tok0;    // first token of the tile within the sequence
@@ -147,6 +151,15 @@ struct DecodeParams {
   // prefix_tokens + num_queries - 1 tokens are walked from prefix_tokens on, the others
   // whole; (m, l) and un-normalised O of every row go to rest_ml / rest_o.
   int prefix_tokens;
+  // Both: how each sequence was cut (see SeqCut); the partials are merged by a
+  // kernel behind this one, all rows at once.
+  int4* cuts;
+  int sm_count;
+  // kWalkRest behind the prefix kernel: the grid starts beside it (its CTAs have
+  // let this one go, so what came before both is complete) and only its end
+  // waits for it.  prefix_units: that kernel's work, for sharing out the SMs.
+  bool beside;
+  float prefix_units;
   float* rest_ml;  // [num_seqs * num_queries * num_heads][2]
   float* rest_o;   // [num_seqs * num_queries * num_heads][D]
   unsigned long long wait_limit_ns;  // bound of every pipeline wait
@@ -232,6 +245,19 @@ struct SeqWalk {
     return tok < c && tok >= first && (tok < pre || tok >= lo);
   }
 };
+
+// SMs for the prefix kernel of `units` units (pa_prefix_work.h) beside a walk of
+// `tiles` tiles by `groups` CTAs each, in proportion to the SM time of either: a
+// unit takes about 0.9 us (D = 128: 128 x 128 x 128 x 4 flops), a tile about 0.35
+// us + 0.18 us per KiB of K row.  The walk is bound by HBM from about 80 SMs on.
+__device__ __forceinline__ int prefix_share(float units, long long tiles, int groups, float tile_us, int head_size,
+                                            int sm_count) {
+  if (tiles == 0) return sm_count;
+  const float a = units * (head_size == 128 ? 0.9f : 0.6f), b = static_cast<float>(tiles) * groups * tile_us;
+  const int n = __float2int_rn(sm_count * (a / (a + b)));
+  return max(1, min(n, sm_count - groups));
+}
+__device__ __forceinline__ float walk_tile_us(uint32_t row_bytes) { return 0.35f + 0.18f / 1024.f * row_bytes; }
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
@@ -1599,13 +1625,6 @@ __device__ void zero_row(const DecodeParams& p, int s) {
   for (size_t i = 0; i < n16; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// kWalkRest: an empty sequence leaves (m, l) = (-inf, 0) for all its rows.
-__device__ inline void empty_rest(const DecodeParams& p, int s) {
-  const size_t n = (size_t)p.num_queries * p.num_heads;
-  float2* ml = reinterpret_cast<float2*>(p.rest_ml) + (size_t)s * n;
-  for (size_t i = 0; i < n; ++i) ml[i] = make_float2(-INFINITY, 0.f);
-}
-
 __device__ __forceinline__ float warp_max_f(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -1624,8 +1643,7 @@ __device__ __forceinline__ float warp_sum_f(float v) {
 // writes the output rows, and resets the ticket counter.  Nobody waits.
 // `arrivals`: warps writing partials per range and KV head (two to four when
 // the (query, head) columns of a KV head are split across several warps).
-// kRest: the merged (m, l, O) go to the rest buffers instead of the output.
-template <typename T, int D, bool kMQ, bool kRest = false>
+template <typename T, int D, bool kMQ>
 __device__ void arrive_and_merge(const DecodeParams& p, int seq, int kv_head, int r0, int r1,
                                  int slot0, int lane, int arrivals = 1) {
   // Release: the warp barrier orders every lane's partial stores before lane
@@ -1712,18 +1730,6 @@ __device__ void arrive_and_merge(const DecodeParams& p, int seq, int kv_head, in
         }
       }
     }
-    if constexpr (kRest) {
-      const size_t row = (size_t)seq * H + h0;
-#pragma unroll
-      for (int g = 0; g < GM; ++g) {
-        if (g < gn) {
-#pragma unroll
-          for (int i = 0; i < DL; ++i) p.rest_o[(row + g) * D + lane * DL + i] = acc[g][i];
-          if (lane == 0) *reinterpret_cast<float2*>(p.rest_ml + (row + g) * 2) = make_float2(run_m[g], run_l[g]);
-        }
-      }
-      continue;
-    }
     T* out = reinterpret_cast<T*>(p.out) + ((size_t)seq * H + h0) * D + lane * DL;
 #pragma unroll
     for (int g = 0; g < GM; ++g) {
@@ -1736,6 +1742,61 @@ __device__ void arrive_and_merge(const DecodeParams& p, int seq, int kv_head, in
   }
   __syncwarp();
   if (lane == 0) *cnt = 0;  // leave the counter zeroed for the next call
+}
+
+// One row of a cut sequence (kCutMerge), its partials added by log-sum-exp by a
+// warp: lane i holds dims [i * D / 32, (i + 1) * D / 32).  The maxima and sums of up
+// to 32 partials are read at once, one per lane, so that the loads of their O
+// parts do not wait for one another.
+template <int DL>
+struct MergedRow {
+  float m, l;
+  float o[DL];
+};
+
+template <int D>
+__device__ __forceinline__ MergedRow<D / 32> merge_row(const float* part_ml, const float* part_o, const int4& cut,
+                                                       int seq_rows, int in_seq, int lane) {
+  constexpr int DL = D / 32;
+  MergedRow<DL> r;
+  r.m = -INFINITY;
+  r.l = 0.f;
+#pragma unroll
+  for (int i = 0; i < DL; ++i) r.o[i] = 0.f;
+  // Range rr left its partial in slot 0, the first range in slot cut.z.
+  auto at = [&](int rr) { return ((size_t)rr * 2 + (rr == cut.x ? cut.z : 0)) * seq_rows + in_seq; };
+  for (int r0 = cut.x; r0 <= cut.y; r0 += 32) {
+    const int rr = r0 + lane;
+    const float2 ml = rr <= cut.y ? __ldcg(reinterpret_cast<const float2*>(part_ml) + at(rr))
+                                  : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float m = fmaxf(r.m, top), ref = m == -INFINITY ? 0.f : m;  // -inf: no token seen so far
+    const float keep = ex2_ftz(r.m - ref), w = ex2_ftz(ml.x - ref);
+    r.m = m;
+    float l = w * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    r.l = r.l * keep + l;
+#pragma unroll
+    for (int i = 0; i < DL; ++i) r.o[i] *= keep;
+    const int n = min(32, cut.y - r0 + 1);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float* po = part_o + at(r0 + k) * D + lane * DL;
+      if constexpr (DL == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(po));
+        r.o[0] = fmaf(wk, v.x, r.o[0]), r.o[1] = fmaf(wk, v.y, r.o[1]);
+        r.o[2] = fmaf(wk, v.z, r.o[2]), r.o[3] = fmaf(wk, v.w, r.o[3]);
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(po));
+        r.o[0] = fmaf(wk, v.x, r.o[0]), r.o[1] = fmaf(wk, v.y, r.o[1]);
+      }
+    }
+  }
+  return r;
 }
 
 // Appending calls: a tile holding some of the step's new tokens (tile rows
@@ -1847,7 +1908,8 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
   constexpr bool kMmaPath = (sizeof(T) == 2);  // tensor-core consumers, swizzled stages
   const Layout L = make_layout(p.stages, p.q_slots, p.q_bytes, p.stage_bytes, kMmaPath);
   long long* misc = reinterpret_cast<long long*>(smem + L.misc);  // [0,32) scratch, [32..] results
-  griddep_wait();  // inputs may come from the kernel just before (e.g. the cache write)
+  if (WALK != kWalkRest || !p.beside)
+    griddep_wait();  // inputs may come from the kernel just before (e.g. the cache write)
 
   // ---- Prologue: total tile count, this range, and its first sequence. ----
   long long total = 0;
@@ -1855,10 +1917,8 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
     const int s = base + tid;
     long long n = (s < S) ? SeqWalk<WALK>(p, s, true).n : 0;
     if (s < S && n == 0 && s % gridDim.x == blockIdx.x) {
-      if constexpr (WALK == kWalkRest)
-        empty_rest(p, s);
-      else
-        zero_row<T, D>(p, s);
+      if constexpr (WALK != kWalkAll) p.cuts[s] = make_int4(0, -1, 0, kCutEmpty);
+      if constexpr (WALK != kWalkRest) zero_row<T, D>(p, s);
     }
     n = warp_sum_ll(n);
     if (lane == 0) misc[warp] = n;
@@ -1868,8 +1928,19 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
   }
   // Never more ranges than tiles, so no range is empty and a cut sequence
   // has exactly r1 - r0 + 1 partials.
-  const long long Reff = total < R ? total : R;
-  if (r >= Reff) return;
+  long long Reff = total < R ? total : R;
+  if constexpr (WALK == kWalkRest) {
+    // The SMs the prefix kernel leaves.
+    if (p.beside) {
+      const int left = p.sm_count - prefix_share(p.prefix_units, total, HG, walk_tile_us(p.row_bytes), D, p.sm_count);
+      const long long most = static_cast<long long>(left) * R / p.sm_count;
+      Reff = min(Reff, max(most, 1ll));
+    }
+  }
+  if (r >= Reff) {
+    if (WALK == kWalkRest && p.beside) griddep_wait();
+    return;
+  }
   const long long a = range_start(r, total, Reff), b = range_start(r + 1, total, Reff);
 
   long long run = 0;
@@ -1887,6 +1958,13 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
     if (s < S && n > 0 && excl <= a && a < excl + n) {
       misc[32] = s;
       misc[33] = excl;
+    }
+    if constexpr (WALK != kWalkAll) {
+      if (s < S && n > 0 && s % (Reff * HG) == blockIdx.x) {
+        const int r0 = static_cast<int>(range_of_tile(excl, total, Reff));
+        const int r1 = static_cast<int>(range_of_tile(excl + n - 1, total, Reff));
+        p.cuts[s] = make_int4(r0, r1, partial_slot_of_range(r0, excl, total, Reff), r0 == r1 ? kCutWhole : kCutMerge);
+      }
     }
     run += chunk;
     __syncthreads();
@@ -2276,8 +2354,8 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
           cons.template finish<true>(p, me.seq, kv_head, slot, r, lane);
         else
           cons.finish(p, me.seq, kv_head, slot, r, lane);
-        if (slot >= 0)
-          arrive_and_merge<T, D, (QMODE > 0), WALK == kWalkRest>(p, me.seq, kv_head, me.r0, me.r1, (me.flags >> 4) & 1, lane,
+        if (WALK == kWalkAll && slot >= 0)
+          arrive_and_merge<T, D, (QMODE > 0)>(p, me.seq, kv_head, me.r0, me.r1, (me.flags >> 4) & 1, lane,
                                               kSplit);
         // Split-column kernels sit at the register cap: writing the state here
         // (the next segment's begin_segment rewrites it anyway) frees its
@@ -2295,6 +2373,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
     }
     named_barrier_sync(1, nthreads);  // lets the producers drain their copies after a timeout
   }
+  if (WALK == kWalkRest && p.beside) griddep_wait();
   (void)Hk;
 }
 

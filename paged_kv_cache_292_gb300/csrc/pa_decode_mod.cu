@@ -9,6 +9,12 @@
 // then those from the first query's window on (SeqWalk), both cut into the same
 // equal ranges.  Inside a tile, rows nobody sees are neither copied (whole boxes)
 // nor used (their scores are -inf and their V entries zeroed in registers).
+//
+// Sequences cut by range boundaries leave partials, which a second kernel merges,
+// a warp per output row.  (In plain decode the last warp to finish a KV head
+// merges all its rows; with 32 columns per KV head and sequences cut over tens of
+// ranges that took longer than the walk: 48 sequences x 4 queries over FP8 pools
+// 79 us with it.)
 #include "pa_launch.cuh"
 
 #include <cmath>
@@ -16,9 +22,63 @@
 #include "pa_decode_impl.h"
 
 namespace pa {
+namespace {
+
+struct MergeParams {
+  void* out;
+  const int4* cuts;
+  const float* part_ml;
+  const float* part_o;
+  long long rows;    // num_seqs * seq_rows
+  int seq_rows;      // num_queries * num_heads
+  float v_scale;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) pa_merge_kernel(const __grid_constant__ MergeParams p) {
+  constexpr int DL = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int s = static_cast<int>(row / p.seq_rows), in_seq = static_cast<int>(row - (long long)s * p.seq_rows);
+  const int4 cut = __ldcg(p.cuts + s);
+  if (cut.w != kCutMerge) return;
+  const MergedRow<DL> m = merge_row<D>(p.part_ml, p.part_o, cut, p.seq_rows, in_seq, lane);
+  const float inv = m.l > 0.f ? p.v_scale / m.l : 0.f;
+  T* out = static_cast<T*>(p.out) + row * D + lane * DL;
+#pragma unroll
+  for (int i = 0; i < DL; ++i) out[i] = T(m.o[i] * inv);
+}
+
+template <typename T, int D>
+int launch_merge(const DecodeParams& prm, cudaStream_t stream) {
+  MergeParams mp{prm.out, prm.cuts, prm.part_ml, prm.part_o, 0, prm.num_queries * prm.num_heads, prm.v_scale};
+  mp.rows = (long long)prm.num_seqs * mp.seq_rows;
+  const cudaError_t e =
+      launch_pdl(pa_merge_kernel<T, D>, dim3((unsigned)((mp.rows + 7) / 8)), dim3(256), 0, stream, mp);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_merge_kernel");
+}
+
+int launch_walk(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool f32,
+                bool kv_fp8);
+
+}  // namespace
 
 int launch_mod(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool f32,
                bool kv_fp8) {
+  const int rc = launch_walk(prm, pl, dev, stream, head_size, f32, kv_fp8);
+  if (rc != PA_OK || pl.R == 1) return rc;  // one range cuts nothing
+  if (f32) return head_size == 64 ? launch_merge<float, 64>(prm, stream) : launch_merge<float, 128>(prm, stream);
+  return head_size == 64 ? launch_merge<__nv_bfloat16, 64>(prm, stream)
+                         : launch_merge<__nv_bfloat16, 128>(prm, stream);
+}
+
+namespace {
+
+int launch_walk(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool f32,
+                bool kv_fp8) {
   const bool wide = prm.group * prm.num_queries > 8;  // two to four warps per KV head
   if (f32) {
     if (head_size == 64)
@@ -42,8 +102,6 @@ int launch_mod(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t st
   return wide ? launch_typed<T, 128, 8, 2, false, kWalkMod>(prm, pl, dev, stream)
               : launch_typed<T, 128, 8, 1, false, kWalkMod>(prm, pl, dev, stream);
 }
-
-namespace {
 
 int make_extras(DecodeExtras* ex, float softcap, const float* alibi_slopes, int window,
                 const int32_t* first_tokens, const int32_t* prefix_lens) {
@@ -96,4 +154,11 @@ extern "C" int pa_decode_fp8_mod(void* out, const void* query, const void* k_cac
                            num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, stream,
                            PA_BF16, num_physical_blocks, workspace, workspace_bytes, num_ranges, error_flag, true,
                            k_scale, v_scale, nullptr, nullptr, nullptr, &ex);
+}
+
+extern "C" size_t pa_decode_mod_workspace_size(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
+                                               int head_size, int kv_dtype, int num_ranges) {
+  if (kv_dtype != PA_F32 && kv_dtype != PA_BF16 && kv_dtype != PA_FP8_E4M3) return 0;
+  return pa::walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, num_ranges, num_queries,
+                                 kv_dtype == PA_F32 ? 4 : kv_dtype == PA_BF16 ? 2 : 1);
 }

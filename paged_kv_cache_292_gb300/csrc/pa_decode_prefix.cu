@@ -52,7 +52,12 @@ struct PrefixParams {
   int32_t* error_flag;
   float* part_ml;  // [slots][2][128][2]
   float* part_o;   // [slots][2][D / 4][128][4]: a thread's row side by side with its neighbours'
-  PrefixWork work;
+  PrefixWork work;  // `ctas`: at most; what the walk behind the prefix leaves is taken (prefix_share)
+  int32_t* ctas_out;
+  const int32_t* context_lens;
+  int num_seqs, num_queries, max_tokens;  // of the walk: its tiles,
+  int walk_groups, walk_row_bytes;        // and the shape of its CTAs
+  int sm_count;
   int rows;  // query rows per KV head
   int group, num_heads, block_size, prefix_tokens, num_physical_blocks, box_rows;
   // Scores are scale_log2 * <(q & q_keep) ^ q_flip, k>: a negative scale changes the
@@ -132,6 +137,29 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
       *abort_flag = 1;
     }
   };
+  griddep_wait();
+  griddep_launch_dependents();  // the walk behind the prefix runs on the SMs left to it
+
+  // This kernel's share of the SMs, the same in every CTA.
+  PrefixWork wk = p.work;
+  {
+    long long* sums = reinterpret_cast<long long*>(smem + 640);
+    long long walk = 0;
+    for (int s = tid; s < p.num_seqs; s += kPrefixThreads) {
+      const int c = max(0, min(__ldg(p.context_lens + s), p.max_tokens));
+      walk += tiles_of(c >= p.prefix_tokens + p.num_queries - 1 ? c - p.prefix_tokens : c);
+    }
+    walk = warp_sum_ll(walk);
+    if (lane == 0) sums[warp] = walk;
+    __syncthreads();
+    walk = 0;
+    for (int i = 0; i < kPrefixThreads / 32; ++i) walk += sums[i];
+    wk.ctas = min(wk.ctas, prefix_share(static_cast<float>(wk.total()), walk, p.walk_groups,
+                                        walk_tile_us(p.walk_row_bytes), D, p.sm_count));
+  }
+  const int cta = blockIdx.x;
+  if (cta >= wk.ctas) return;
+  if (cta == 0 && tid == 0) *p.ctas_out = wk.ctas;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full(i), 1);
@@ -152,11 +180,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_wait();
-  griddep_launch_dependents();
-
-  const PrefixWork wk = p.work;
-  const int cta = blockIdx.x;
   const int64_t ua = wk.cta_start(cta), ub = wk.cta_start(cta + 1);
   const int first_item = wk.item_of(ua);
 
@@ -500,6 +523,10 @@ struct JoinParams {
   const float* part_o;
   const float* rest_ml;
   const float* rest_o;
+  const int4* cuts;  // the walk's, and its partials
+  const float* walk_ml;
+  const float* walk_o;
+  const int32_t* ctas;  // of the prefix kernel
   PrefixWork work;
   int rows;   // query rows per KV head
   int pairs;  // of them, rounded up
@@ -526,30 +553,58 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
     row[i] = (long long)token * p.num_heads + kv * p.group + (r - token * p.group);
     const int c = min(__ldg(p.context_lens + token / p.num_queries), p.max_tokens);
     shares[i] = c >= p.prefix_tokens + p.num_queries - 1;
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rest_ml) + row[i]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ml.y > 0.f && holds) o = __ldcg(reinterpret_cast<const float4*>(p.rest_o + row[i] * D) + lane);
-    m[i] = ml.y > 0.f ? ml.x : -INFINITY;
-    l[i] = ml.y > 0.f ? ml.y : 0.f;
-    acc[i][0] = o.x, acc[i][1] = o.y, acc[i][2] = o.z, acc[i][3] = o.w;
+    // The rest: nothing, a row the walk finished, or partials of several ranges.
+    const int seq = token / p.num_queries;
+    const int4 cut = __ldcg(p.cuts + seq);
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
+    if (cut.w == kCutWhole) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rest_ml) + row[i]);
+      if (ml.y > 0.f) {
+        m[i] = ml.x;
+        l[i] = ml.y;
+        if (holds) {
+          const float4 o = __ldcg(reinterpret_cast<const float4*>(p.rest_o + row[i] * D) + lane);
+          acc[i][0] = o.x, acc[i][1] = o.y, acc[i][2] = o.z, acc[i][3] = o.w;
+        }
+      }
+    } else if (cut.w == kCutMerge) {
+      const int seq_rows = p.num_queries * p.num_heads;
+      const MergedRow<D / 32> r = merge_row<D>(p.walk_ml, p.walk_o, cut, seq_rows,
+                                               static_cast<int>(row[i] - (long long)seq * seq_rows), lane);
+      m[i] = r.l > 0.f ? r.m : -INFINITY;
+      l[i] = r.l;
+      if constexpr (D == 128) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] = r.o[k];
+      } else {
+        // Two dims a lane there, four here.
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = __shfl_sync(0xffffffffu, r.o[k & 1], (2 * lane + (k >> 1)) & 31);
+          acc[i][k] = holds ? x : 0.f;
+        }
+      }
+    }
   }
   if (shares[0] || shares[1]) {
     const int pair = r0 / (2 * kPrefixRows), in_pair = r0 - pair * 2 * kPrefixRows;
-    const int item = kv * p.work.pairs + pair;
-    const bool two = p.work.weight(item) == 2;
-    const int c0 = p.work.cta_of(item, 0), c1 = p.work.cta_of(item, p.work.tiles - 1);
+    PrefixWork wk = p.work;
+    wk.ctas = __ldcg(p.ctas);
+    const int item = kv * wk.pairs + pair;
+    const bool two = wk.weight(item) == 2;
+    // Every CTA between the two has a partial: a range holds two units or more.
+    const int c0 = wk.cta_of(item, 0), c1 = wk.cta_of(item, wk.tiles - 1);
     const int parts = (c1 - c0 + 1) * (two ? 1 : 2);
     for (int j0 = 0; j0 < parts; j0 += 32) {
       const int j = j0 + lane, cta = c0 + (two ? j : j >> 1);
       float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);  // (m, l) of both rows
       int at = 0;  // partial: slot and softmax group
       if (j < parts) {
-        // A CTA whose range holds no first unit of the item has no partial.
-        const int ta = p.work.tile_at(item, p.work.cta_start(cta)), tb = p.work.tile_at(item, p.work.cta_start(cta + 1));
         at = (cta + item) * 2 + (two ? in_pair >> 7 : j & 1);
-        if (ta < tb)
-          ml = __ldcg(reinterpret_cast<const float4*>(
-              p.part_ml + ((size_t)at * kPrefixRows + (in_pair & 127)) * 2));
+        ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + ((size_t)at * kPrefixRows + (in_pair & 127)) * 2));
       }
       float w[2];
 #pragma unroll
@@ -613,11 +668,11 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
 // Scratch: the rest's (m, l) and O rows, the prefix's partials, then what the
 // rest's walk needs.
 struct PrefixScratch {
-  size_t rest_ml, rest_o, part_ml, part_o, walk, total;
+  size_t ctas, rest_ml, rest_o, part_ml, part_o, walk, total;
 };
 
-PrefixScratch prefix_scratch(int num_seqs, int num_queries, int num_heads, int num_kv_heads, int head_size,
-                             int slots, size_t walk_bytes) {
+PrefixScratch prefix_scratch(int num_seqs, int num_queries, int num_heads, int head_size, int slots,
+                             size_t walk_bytes) {
   const size_t rows = (size_t)num_seqs * num_queries * num_heads;
   const size_t part_rows = (size_t)slots * 2 * kPrefixRows;
   PrefixScratch s;
@@ -627,7 +682,7 @@ PrefixScratch prefix_scratch(int num_seqs, int num_queries, int num_heads, int n
     o += align_up(bytes, 256);
     return at;
   };
-  (void)num_kv_heads;
+  s.ctas = take(4);
   s.rest_ml = take(rows * 8);
   s.rest_o = take(rows * head_size * 4);
   s.part_ml = take(part_rows * 8);
@@ -674,10 +729,10 @@ int launch_prefix(const PrefixParams& prm, cudaStream_t stream) {
 extern "C" size_t pa_decode_prefix_workspace_size(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
                                                   int head_size) {
   using namespace pa;
-  const size_t walk = decode_workspace_size_q(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries);
+  const size_t walk = walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 2);
   DeviceInfo dev{};
   if (walk == 0 || current_device_info(&dev) != PA_OK) return 0;
-  return prefix_scratch(num_seqs, num_queries, num_heads, num_kv_heads, head_size,
+  return prefix_scratch(num_seqs, num_queries, num_heads, head_size,
                         most_slots(num_seqs, num_queries, num_heads, num_kv_heads, dev.sm_count), walk)
       .total;
 }
@@ -708,14 +763,13 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   rc = current_device_info(&dev);
   if (rc != PA_OK) return rc;
   const size_t walk_bytes =
-      decode_workspace_size_q(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries);
-  const PrefixScratch sc = prefix_scratch(num_seqs, num_queries, num_heads, num_kv_heads, head_size,
+      walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 2);
+  const PrefixScratch sc = prefix_scratch(num_seqs, num_queries, num_heads, head_size,
                                           most_slots(num_seqs, num_queries, num_heads, num_kv_heads, dev.sm_count),
                                           walk_bytes);
   const bool own = workspace == nullptr;
-  int32_t* tickets = nullptr;
   if (own) {
-    rc = kept_scratch(sc.total, sizeof(int32_t) * (size_t)num_seqs * num_kv_heads, stream, &workspace, &tickets);
+    rc = kept_scratch(sc.total, stream, &workspace);
     if (rc != PA_OK) return rc;
   } else {
     if (workspace_bytes < sc.total)
@@ -747,6 +801,15 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
     prm.part_ml = reinterpret_cast<float*>(ws + sc.part_ml);
     prm.part_o = reinterpret_cast<float*>(ws + sc.part_o);
     prm.work = make_prefix_work(rows, num_kv_heads, prefix_tokens, dev.sm_count);
+    const WalkShape shape = walk_shape(num_heads, num_kv_heads, head_size, num_queries, 2);
+    prm.ctas_out = reinterpret_cast<int32_t*>(ws + sc.ctas);
+    prm.context_lens = context_lens;
+    prm.num_seqs = num_seqs;
+    prm.num_queries = num_queries;
+    prm.max_tokens = max_blocks_per_seq * block_size;
+    prm.walk_groups = shape.groups;
+    prm.walk_row_bytes = shape.row_bytes;
+    prm.sm_count = dev.sm_count;
     prm.rows = (int)rows;
     prm.group = group;
     prm.num_heads = num_heads;
@@ -765,7 +828,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   ex.prefix_tokens = prefix_tokens;
   ex.rest_ml = reinterpret_cast<float*>(ws + sc.rest_ml);
   ex.rest_o = reinterpret_cast<float*>(ws + sc.rest_o);
-  ex.tickets = tickets;
+  ex.prefix_units = num_prefix_blocks > 0 ? (float)prm.work.total() : 0.f;
   rc = decode_impl_q(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries, num_heads,
                      num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, stream, dtype,
                      num_physical_blocks, ws + sc.walk, walk_bytes, 0, error_flag, false, 1.f, 1.f, nullptr, nullptr,
@@ -778,6 +841,10 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   jp.part_o = prm.part_o;
   jp.rest_ml = ex.rest_ml;
   jp.rest_o = ex.rest_o;
+  jp.cuts = ex.cuts;
+  jp.walk_ml = ex.part_ml;
+  jp.walk_o = ex.part_o;
+  jp.ctas = prm.ctas_out;
   jp.work = prm.work;
   jp.rows = (int)rows;
   jp.pairs = (int)((rows + 1) / 2);
@@ -785,7 +852,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   jp.num_queries = num_queries;
   jp.num_heads = num_heads;
   jp.group = group;
-  jp.prefix_tokens = num_prefix_blocks > 0 ? prefix_tokens : 1 << 30;  // without one nobody shares it
+  jp.prefix_tokens = num_prefix_blocks > 0 ? prefix_tokens : (1 << 30) + 1;  // beyond any context: nobody shares
   jp.max_tokens = max_blocks_per_seq * block_size;
   const dim3 grid((unsigned)(((long long)jp.pairs * num_kv_heads + 7) / 8));
   const cudaError_t e = head_size == 64 ? launch_pdl(pa_prefix_join<64>, grid, dim3(256), 0, st, jp)

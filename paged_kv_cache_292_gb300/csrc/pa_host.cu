@@ -25,8 +25,8 @@ void* g_ws_ptr[kMaxDevices] = {nullptr};
 size_t g_ws_bytes[kMaxDevices] = {0};
 void* g_cnt_ptr[kMaxDevices] = {nullptr};
 size_t g_cnt_bytes[kMaxDevices] = {0};
-void* g_kept_ptr[kMaxDevices][2] = {};  // kept_scratch: partials, tickets
-size_t g_kept_bytes[kMaxDevices][2] = {};
+void* g_kept_ptr[kMaxDevices] = {nullptr};  // kept_scratch
+size_t g_kept_bytes[kMaxDevices] = {0};
 }  // namespace
 
 int fail(int code, const char* fmt, ...) {
@@ -123,7 +123,7 @@ int library_counters(size_t bytes, int32_t** ptr) {
   return PA_OK;
 }
 
-int kept_scratch(size_t bytes, size_t ticket_bytes, void* stream, void** ptr, int32_t** tickets) {
+int kept_scratch(size_t bytes, void* stream, void** ptr) {
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &status);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
@@ -133,27 +133,16 @@ int kept_scratch(size_t bytes, size_t ticket_bytes, void* stream, void** ptr, in
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   std::lock_guard<std::mutex> lock(g_mutex);
-  const size_t need[2] = {bytes, ticket_bytes};
-  for (int i = 0; i < 2; ++i) {
-    if (g_kept_bytes[dev][i] >= need[i] && g_kept_ptr[dev][i] != nullptr) continue;
-    size_t want = i == 0 ? (size_t)8 << 20 : (size_t)64 << 10;
-    while (want < need[i]) want *= 2;
+  if (g_kept_bytes[dev] < bytes) {
+    size_t want = (size_t)16 << 20;
+    while (want < bytes) want *= 2;
     void* p = nullptr;
     e = cudaMalloc(&p, want);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(scratch)");
-    if (i == 1) {
-      e = cudaMemset(p, 0, want);
-      if (e == cudaSuccess) e = cudaDeviceSynchronize();
-      if (e != cudaSuccess) {
-        cudaFree(p);
-        return cuda_fail(e, "cudaMemset(tickets)");
-      }
-    }
-    g_kept_ptr[dev][i] = p;
-    g_kept_bytes[dev][i] = want;
+    g_kept_ptr[dev] = p;
+    g_kept_bytes[dev] = want;
   }
-  *ptr = g_kept_ptr[dev][0];
-  *tickets = static_cast<int32_t*>(g_kept_ptr[dev][1]);
+  *ptr = g_kept_ptr[dev];
   return PA_OK;
 }
 

@@ -32,12 +32,11 @@ int library_workspace(size_t bytes, void** ptr);
 int library_counters(size_t bytes, int32_t** ptr);
 
 // Library-owned scratch of the operators beyond plain decode: at least `bytes`
-// of any content and `ticket_bytes` of merge tickets that are zero between
-// calls.  Apart from the two buffers above, and never freed: a buffer that got
-// too small stays allocated (sizes double, so all of them together are below
-// twice the largest).  Refused while `stream` is being captured, where a graph
-// would keep the address beyond this call: captured calls bring their own.
-int kept_scratch(size_t bytes, size_t ticket_bytes, void* stream, void** ptr, int32_t** tickets);
+// of any content.  Apart from the two buffers above, and never freed: a buffer
+// that got too small stays allocated (sizes double, so all of them together are
+// below twice the largest).  Refused while `stream` is being captured, where a
+// graph would keep the address beyond this call: captured calls bring their own.
+int kept_scratch(size_t bytes, void* stream, void** ptr);
 
 // Writes the new rows of a multi-query appending call into the pools (token
 // i of sequence s at position context_lens[s] - num_queries + i), as its own

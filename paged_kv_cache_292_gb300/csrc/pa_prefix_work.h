@@ -58,8 +58,10 @@ PA_HD PrefixWork make_prefix_work(int64_t rows, int kv_heads, int prefix_tokens,
   w.pairs = (int)((rows + 2 * kPrefixRows - 1) / (2 * kPrefixRows));
   w.last_weight = rows - (int64_t)(w.pairs - 1) * 2 * kPrefixRows > kPrefixRows ? 2 : 1;
   w.kv_heads = kv_heads;
-  const int64_t all = (int64_t)w.tiles * w.pairs * kv_heads;
-  w.ctas = (int)(all < max_ctas ? all : max_ctas);
+  // Two units at least, so that every range holds a tile's first unit.
+  w.ctas = 1;
+  const int64_t most = w.total() / 2;
+  if (most > 1) w.ctas = (int)(most < max_ctas ? most : max_ctas);
   return w;
 }
 

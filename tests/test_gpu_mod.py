@@ -198,8 +198,9 @@ def test_workspace_of_any_content_capture_and_streams(dtype, Q):
     """A caller's scratch filled with ones, shared by two captured graphs of different shapes on one stream."""
     a = Batch(dtype, CTX, Q, **_mods("all", 8))
     b = Batch(dtype, [700, 5], Q, seed=4, **dict(window=300))
-    size = binding.pa_decode_mq_workspace_size(S, Q, 8, 2, 128)
-    ws = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+    kv = {"f32": binding.PA_F32, "bf16": binding.PA_BF16, "fp8": binding.PA_FP8_E4M3}[dtype]
+    size = binding.pa_decode_mod_workspace_size(S, Q, 8, 2, 128, kv)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
     parts = [(x, *x.gpu()) for x in (a, b)]
     outs = [torch.full_like(args[0], float("nan")) for _, args, _ in parts]
     graphs = []
@@ -223,12 +224,18 @@ def test_workspace_of_any_content_capture_and_streams(dtype, Q):
         want, spread = x.want()
         assert_rounded(out.view(want.shape), want, spread, WEIGHT_ERROR[dtype], "captured")
         assert torch.equal(out, e)
+    with pytest.raises(binding.PagedAttnError) as err:
+        a.call(*parts[0][1:], workspace=ws[: size // 64 // 256 * 256])
+    assert err.value.code == binding.PA_ERR_WORKSPACE
 
 
 def test_plain_modification_equals_decode():
     b = Batch("bf16", CTX, 1)
     args, kw = b.gpu()
-    assert torch.equal(b.call(args, kw), binding.decode(*args))
+    want, spread = b.want()
+    for got in (b.call(args, kw, num_ranges=1), b.call(args, kw)):
+        assert_rounded(got, binding.decode(*args).double().cpu().numpy(), spread[:, 0], WEIGHT_ERROR["bf16"] + 2.0**-8,
+                       "against decode")
 
 
 def test_python_layer_refuses_mismatched_arguments():

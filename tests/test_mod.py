@@ -135,3 +135,12 @@ def test_restatement_ignores_what_nobody_sees():
         t2[s, :4] = -1
     got, _ = modified.decode_mod(q, k2, v2, t2, lens, 0.5, bs, window=3)
     assert np.array_equal(got, want)
+
+
+def test_workspace_size(lib):
+    size = binding.pa_decode_mod_workspace_size
+    for bad in ((0, 1, 8, 8, 128, 1), (1, 0, 8, 8, 128, 1), (1, 1, 9, 8, 128, 1), (1, 1, 8, 0, 128, 1),
+                (1, 1, 8, 8, 0, 1), (1, 1, 8, 8, 128, 3), (1, 1, 8, 8, 128, 1, -1)):
+        assert size(*bad) == 0
+    # num_ranges partials of (m, l) and O for two slots, and 16 bytes per sequence.
+    assert size(5, 3, 8, 2, 64, binding.PA_BF16, 7) >= 7 * 2 * 24 * (8 + 4 * 64) + 16 * 5
