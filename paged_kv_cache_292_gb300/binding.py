@@ -544,38 +544,37 @@ def decode_fp8_multi_append(query, k_new, v_new, k_cache, v_cache, block_tables,
 
 
 # ---- operators beyond plain decode ---------------------------------------------
+#
+# A step's small operators take a few microseconds on the GPU, so these
+# functions check their tensors with few attribute reads and pass them on directly.
 
 
-def _on_device(first, *ts):
-    """All tensors contiguous and on one CUDA device, which becomes the current one for the call."""
-    dev = first.device
-    for t in (first, *ts):
-        if t is not None and (t.device != dev or not t.is_cuda or not t.is_contiguous()):
+def _device_of(first, *ts):
+    """The CUDA device index of contiguous tensors that all live on one device."""
+    index = first.get_device()
+    if index < 0 or not first.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors on one device")
+    for t in ts:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors on one device")
-    return dev.index
+    return index
 
 
-class _call_on:
-    """Make a device current for one library call (nothing to do when it is)."""
-
-    __slots__ = ("index", "before")
-
-    def __init__(self, index):
-        self.index = index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _require_dtype(dtype, what, *ts):
+    for t in ts:
+        if t is not None and t.dtype is not dtype:
+            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
 
 
-def _require_stream(stream, index):
-    if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
-        raise ValueError("the stream belongs to another device than the tensors")
+def _stream_on(stream, index):
+    """cudaStream_t of ``stream`` (None: device ``index``'s current stream)."""
+    if stream is None:
+        return torch.cuda.current_stream(index).cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != index:
+            raise ValueError("the stream belongs to another device than the tensors")
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _used_on(stream, *ts):
@@ -585,10 +584,23 @@ def _used_on(stream, *ts):
             t.record_stream(stream)
 
 
-def _require_dtype(dtype, **ts):
-    for name, t in ts.items():
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+def _call_on(index, fn, *args):
+    """One library call with the tensors' device current."""
+    if torch.cuda.current_device() == index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args)
+    if rc != PA_OK:
+        _check(rc)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _size(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def pa_tables_step(block_tables, context_lens_out, seq_starts, slot_mapping, free_blocks, free_count_out,
@@ -608,29 +620,31 @@ def tables_step(block_tables, context_lens, new_lens, free_blocks, free_count, b
 
     ``block_tables[S, MB]``, ``free_blocks[NB]`` and ``slot_mapping[T]`` (int64) are written in place; returns
     ``(context_lens_out[S], free_count_out[1], seq_starts[S + 1])``, which are not the inputs' buffers."""
-    index = _on_device(block_tables, context_lens, new_lens, free_blocks, free_count, slot_mapping, prefix_table,
+    index = _device_of(block_tables, context_lens, new_lens, free_blocks, free_count, slot_mapping, prefix_table,
                        context_lens_out, free_count_out, seq_starts, error_flag)
-    _require_dtype(torch.int32, block_tables=block_tables, context_lens=context_lens, new_lens=new_lens,
-                   free_blocks=free_blocks, free_count=free_count, prefix_table=prefix_table,
-                   context_lens_out=context_lens_out, free_count_out=free_count_out, seq_starts=seq_starts,
-                   error_flag=error_flag)
-    _require_dtype(torch.int64, slot_mapping=slot_mapping)
+    _require_dtype(torch.int32, "tables, lengths and the free list", block_tables, context_lens, new_lens,
+                   free_blocks, free_count, prefix_table, context_lens_out, free_count_out, seq_starts, error_flag)
+    _require_dtype(torch.int64, "slot_mapping", slot_mapping)
     S, MB = block_tables.shape
-    outs = (context_lens_out, free_count_out, seq_starts)
-    want = (S, 1, S + 1)
     if context_lens.numel() != S or new_lens.numel() != S or free_count.numel() != 1:
         raise ValueError("context_lens and new_lens must have one entry per table row, free_count one entry")
-    if any(o is not None and o.numel() != n for o, n in zip(outs, want)):
+    if context_lens_out is None:
+        context_lens_out = context_lens.new_empty(S)
+        _used_on(stream, context_lens_out)
+    if free_count_out is None:
+        free_count_out = context_lens.new_empty(1)
+        _used_on(stream, free_count_out)
+    if seq_starts is None:
+        seq_starts = context_lens.new_empty(S + 1)
+        _used_on(stream, seq_starts)
+    if context_lens_out.numel() != S or free_count_out.numel() != 1 or seq_starts.numel() != S + 1:
         raise ValueError("context_lens_out, free_count_out and seq_starts must have S, 1 and S + 1 entries")
-    _require_stream(stream, index)
-    with _call_on(index):
-        made = tuple(context_lens.new_empty(n) if o is None else o for o, n in zip(outs, want))
-        _used_on(stream, *(m for m, o in zip(made, outs) if o is None))
-        outs = made
-        pa_tables_step(block_tables, outs[0], outs[2], slot_mapping, free_blocks, outs[1], context_lens, new_lens,
-                       free_count, prefix_table, 0 if prefix_table is None else prefix_table.numel(), S, MB,
-                       block_size, free_blocks.numel(), slot_mapping.numel(), stream, error_flag)
-    return outs
+    _call_on(index, load().pa_tables_step, block_tables.data_ptr(), context_lens_out.data_ptr(),
+             seq_starts.data_ptr(), slot_mapping.data_ptr(), free_blocks.data_ptr(), free_count_out.data_ptr(),
+             context_lens.data_ptr(), new_lens.data_ptr(), free_count.data_ptr(), _at(prefix_table),
+             0 if prefix_table is None else prefix_table.numel(), S, MB, block_size, free_blocks.numel(),
+             slot_mapping.numel(), _stream_on(stream, index), _at(error_flag))
+    return context_lens_out, free_count_out, seq_starts
 
 
 def pa_decode_mod(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries, num_heads,
@@ -665,46 +679,49 @@ def pa_decode_mod_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads,
 
 def _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out):
     """(S, Q, H, D, NB, bs, Hk, MB) of a step over paged pools, query [S, H, D] or [S, Q, H, D]."""
-    if query.dim() == 4:
-        S, Q, H, D = query.shape
+    shape = query.shape
+    if len(shape) == 4:
+        S, Q, H, D = shape
     else:
-        (S, H, D), Q = query.shape, 1
-    NB, bs, Hk, Dk = k_cache.shape
-    if Dk != D or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or block_tables.shape[0] != S or \
-            context_lens.numel() != S or (out is not None and out.shape != query.shape):
+        (S, H, D), Q = shape, 1
+    pool = k_cache.shape
+    NB, bs, Hk, Dk = pool
+    SB, MB = block_tables.shape
+    if Dk != D or v_cache.shape != pool or SB != S or context_lens.numel() != S or (
+            out is not None and out.shape != shape):
         raise ValueError("shapes of query, pools, block_tables, context_lens and out do not go together")
-    _require_dtype(torch.int32, block_tables=block_tables, context_lens=context_lens)
-    return S, Q, H, D, NB, bs, Hk, block_tables.shape[1]
+    _require_dtype(torch.int32, "block_tables and context_lens", block_tables, context_lens)
+    return S, Q, H, D, NB, bs, Hk, MB
 
 
 def _decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, scales, out, stream, softcap,
                 alibi_slopes, window, first_tokens, prefix_lens, num_ranges, workspace, error_flag, check_block_ids):
-    index = _on_device(query, k_cache, v_cache, block_tables, context_lens, out, alibi_slopes, first_tokens,
+    index = _device_of(query, k_cache, v_cache, block_tables, context_lens, out, alibi_slopes, first_tokens,
                        prefix_lens, workspace, error_flag)
     S, Q, H, D, NB, bs, Hk, MB = _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out)
-    pool = torch.uint8 if scales else query.dtype
-    _require_dtype(pool, k_cache=k_cache, v_cache=v_cache)
-    _require_dtype(torch.bfloat16 if scales else query.dtype, query=query, out=out)
-    _require_dtype(torch.int32, first_tokens=first_tokens, prefix_lens=prefix_lens, error_flag=error_flag)
-    _require_dtype(torch.float32, alibi_slopes=alibi_slopes)
-    if (alibi_slopes is not None and alibi_slopes.numel() != H) or any(
-            t is not None and t.numel() != S for t in (first_tokens, prefix_lens)):
+    dtype = query.dtype
+    if scales:
+        _require_dtype(torch.bfloat16, "query", query)
+    _require_dtype(torch.uint8 if scales else dtype, "k_cache and v_cache", k_cache, v_cache)
+    _require_dtype(dtype, "out", out)
+    _require_dtype(torch.int32, "first_tokens, prefix_lens and error_flag", first_tokens, prefix_lens, error_flag)
+    _require_dtype(torch.float32, "alibi_slopes", alibi_slopes)
+    if (alibi_slopes is not None and alibi_slopes.numel() != H) or (
+            first_tokens is not None and first_tokens.numel() != S) or (
+            prefix_lens is not None and prefix_lens.numel() != S):
         raise ValueError("alibi_slopes has one entry per query head, first_tokens and prefix_lens one per sequence")
-    _require_stream(stream, index)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    blocks = NB if check_block_ids else 0
-    with _call_on(index):
-        if out is None:
-            out = torch.empty_like(query)
-            _used_on(stream, out)
-        if scales:
-            pa_decode_fp8_mod(out, query, k_cache, v_cache, block_tables, context_lens, S, Q, H, Hk, D, bs, MB, scale,
-                              scales[0], scales[1], softcap, alibi_slopes, window, first_tokens, prefix_lens, stream,
-                              blocks, workspace, ws_bytes, num_ranges, error_flag)
-        else:
-            pa_decode_mod(out, query, k_cache, v_cache, block_tables, context_lens, S, Q, H, Hk, D, bs, MB, scale,
-                          softcap, alibi_slopes, window, first_tokens, prefix_lens, stream, None, blocks, workspace,
-                          ws_bytes, num_ranges, error_flag)
+    raw = _stream_on(stream, index)
+    if out is None:
+        out = torch.empty_like(query)
+        _used_on(stream, out)
+    tensors = (out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+               context_lens.data_ptr(), S, Q, H, Hk, D, bs, MB, scale)
+    mods = (softcap, _at(alibi_slopes), window, _at(first_tokens), _at(prefix_lens), raw)
+    rest = (NB if check_block_ids else 0, _at(workspace), _size(workspace), num_ranges, _at(error_flag))
+    if scales:
+        _call_on(index, load().pa_decode_fp8_mod, *tensors, *scales, *mods, *rest)
+    else:
+        _call_on(index, load().pa_decode_mod, *tensors, *mods, dtype_code(dtype), *rest)
     return out
 
 
@@ -746,16 +763,17 @@ def decode_prefix(query, k_cache, v_cache, prefix_table, block_tables, context_l
                   workspace=None, error_flag=None, check_block_ids=False):
     """Decode of a batch that shares the prefix in the blocks ``prefix_table[NP]``, attended once for all (as in
     ``pa_decode_prefix``); query and out [S, H, D] or [S, Q, H, D]."""
-    index = _on_device(query, k_cache, v_cache, prefix_table, block_tables, context_lens, out, workspace, error_flag)
+    index = _device_of(query, k_cache, v_cache, prefix_table, block_tables, context_lens, out, workspace, error_flag)
     S, Q, H, D, NB, bs, Hk, MB = _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out)
-    _require_dtype(query.dtype, k_cache=k_cache, v_cache=v_cache, out=out)
-    _require_dtype(torch.int32, prefix_table=prefix_table, error_flag=error_flag)
-    _require_stream(stream, index)
-    with _call_on(index):
-        if out is None:
-            out = torch.empty_like(query)
-            _used_on(stream, out)
-        pa_decode_prefix(out, query, k_cache, v_cache, prefix_table, block_tables, context_lens, S, Q, H, Hk, D, bs,
-                         prefix_table.numel(), MB, scale, stream, None, NB if check_block_ids else 0, workspace,
-                         workspace.numel() * workspace.element_size() if workspace is not None else 0, error_flag)
+    dtype = query.dtype
+    _require_dtype(dtype, "k_cache, v_cache and out", k_cache, v_cache, out)
+    _require_dtype(torch.int32, "prefix_table and error_flag", prefix_table, error_flag)
+    raw = _stream_on(stream, index)
+    if out is None:
+        out = torch.empty_like(query)
+        _used_on(stream, out)
+    _call_on(index, load().pa_decode_prefix, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
+             v_cache.data_ptr(), prefix_table.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H,
+             Hk, D, bs, prefix_table.numel(), MB, scale, raw, dtype_code(dtype), NB if check_block_ids else 0,
+             _at(workspace), _size(workspace), _at(error_flag))
     return out

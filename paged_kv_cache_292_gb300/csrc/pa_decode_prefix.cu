@@ -699,27 +699,63 @@ int most_slots(int num_seqs, int num_queries, int num_heads, int num_kv_heads, i
   return (int)(sm_count + pairs * num_kv_heads);
 }
 
-int make_map(CUtensorMap* tm, const void* pool, int num_kv_heads, int head_size, uint64_t rows, int box_rows) {
+// The pools' tensor maps.  A map is a pure function of the fields of its key, so
+// the last few are kept per thread and a step over the same pools skips the
+// driver's encoder.
+struct MapKey {
+  const void* k;
+  const void* v;
+  uint64_t rows;
+  int num_kv_heads, head_size, box_rows;
+};
+struct KeptMaps {
+  MapKey key;
+  CUtensorMap tm_k, tm_v;
+};
+constexpr int kKeptMaps = 4;
+thread_local KeptMaps g_maps[kKeptMaps];
+thread_local int g_maps_used = 0, g_maps_next = 0;
+
+int make_maps(PrefixParams* prm, const MapKey& key) {
+  for (int i = 0; i < g_maps_used; ++i) {
+    const MapKey& o = g_maps[i].key;
+    if (o.k == key.k && o.v == key.v && o.rows == key.rows && o.num_kv_heads == key.num_kv_heads &&
+        o.head_size == key.head_size && o.box_rows == key.box_rows) {
+      prm->tm_k = g_maps[i].tm_k;
+      prm->tm_v = g_maps[i].tm_v;
+      return PA_OK;
+    }
+  }
   const EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return fail(PA_ERR_CUDA, "pa_decode_prefix: the driver has no cuTensorMapEncodeTiled");
-  const cuuint64_t dims[3] = {64, (cuuint64_t)num_kv_heads * head_size / 64, rows};
-  const cuuint64_t strides[2] = {128, (cuuint64_t)num_kv_heads * head_size * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, estride[3] = {1, 1, 1};
-  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box,
-                         estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    return fail(PA_ERR_CUDA, "pa_decode_prefix: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  const cuuint64_t row = (cuuint64_t)key.num_kv_heads * key.head_size;
+  const cuuint64_t dims[3] = {64, row / 64, key.rows}, strides[2] = {128, row * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)key.box_rows}, estride[3] = {1, 1, 1};
+  for (int i = 0; i < 2; ++i) {
+    const CUresult r = enc(i ? &prm->tm_v : &prm->tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                           const_cast<void*>(i ? key.v : key.k), dims, strides, box, estride,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+      return fail(PA_ERR_CUDA, "pa_decode_prefix: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  }
+  KeptMaps& m = g_maps[g_maps_next];
+  m.key = key;
+  m.tm_k = prm->tm_k;
+  m.tm_v = prm->tm_v;
+  g_maps_next = (g_maps_next + 1) % kKeptMaps;
+  if (g_maps_used < kKeptMaps) ++g_maps_used;
   return PA_OK;
 }
 
 template <int D>
-int launch_prefix(const PrefixParams& prm, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(pa_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       PrefixLayout<D>::kBytes);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(prefix smem)");
-  e = launch_pdl(pa_prefix_kernel<D>, dim3(prm.work.ctas), dim3(kPrefixThreads), PrefixLayout<D>::kBytes, stream,
-                 prm);
+int launch_prefix(const PrefixParams& prm, int device, cudaStream_t stream) {
+  static RaisedDevices raised;
+  const int rc = raise_smem_limit(reinterpret_cast<const void*>(pa_prefix_kernel<D>), PrefixLayout<D>::kBytes, device,
+                                  &raised);
+  if (rc != PA_OK) return rc;
+  const cudaError_t e = launch_pdl(pa_prefix_kernel<D>, dim3(prm.work.ctas), dim3(kPrefixThreads),
+                                   PrefixLayout<D>::kBytes, stream, prm);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefix_kernel");
 }
 
@@ -792,8 +828,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
                   (unsigned long long)pool_rows);
     prm.box_rows = block_size & -block_size;
     if (prm.box_rows > kPrefixTokens) prm.box_rows = kPrefixTokens;
-    rc = make_map(&prm.tm_k, k_cache, num_kv_heads, head_size, pool_rows, prm.box_rows);
-    if (rc == PA_OK) rc = make_map(&prm.tm_v, v_cache, num_kv_heads, head_size, pool_rows, prm.box_rows);
+    rc = make_maps(&prm, MapKey{k_cache, v_cache, pool_rows, num_kv_heads, head_size, prm.box_rows});
     if (rc != PA_OK) return rc;
     prm.q = static_cast<const __nv_bfloat16*>(query);
     prm.table = prefix_table;
@@ -820,7 +855,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
     prm.q_keep = scale != 0.f ? 0xffffffffu : 0u;
     prm.q_flip = scale < 0.f ? 0x80008000u : 0u;
     take_wait_test(&prm.stall_tile, &prm.wait_limit_ns);
-    rc = head_size == 64 ? launch_prefix<64>(prm, st) : launch_prefix<128>(prm, st);
+    rc = head_size == 64 ? launch_prefix<64>(prm, dev.device, st) : launch_prefix<128>(prm, dev.device, st);
     if (rc != PA_OK) return rc;
   }
   DecodeExtras ex{};

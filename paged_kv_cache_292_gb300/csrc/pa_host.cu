@@ -123,6 +123,15 @@ int library_counters(size_t bytes, int32_t** ptr) {
   return PA_OK;
 }
 
+int raise_smem_limit(const void* kernel, int bytes, int device, RaisedDevices* raised) {
+  const uint64_t bit = 1ull << (device & 63);
+  if (raised->done.load(std::memory_order_acquire) & bit) return PA_OK;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(shared memory)");
+  raised->done.fetch_or(bit, std::memory_order_release);
+  return PA_OK;
+}
+
 int kept_scratch(size_t bytes, void* stream, void** ptr) {
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &status);

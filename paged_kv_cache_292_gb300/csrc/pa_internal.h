@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace pa {
 
 // Record a message for pa_last_error() and return `code`.
@@ -13,6 +15,13 @@ int fail(int code, const char* fmt, ...);
 int cuda_fail(cudaError_t err, const char* what);
 // Clear the calling thread's message.
 void clear_error();
+
+// Raises a kernel's dynamic shared-memory limit on a device, once per device
+// (again on a race of first calls, which is harmless).
+struct RaisedDevices {
+  std::atomic<uint64_t> done{0};
+};
+int raise_smem_limit(const void* kernel, int bytes, int device, RaisedDevices* raised);
 
 struct DeviceInfo {
   int device;

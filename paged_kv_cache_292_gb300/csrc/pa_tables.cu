@@ -27,6 +27,8 @@
 namespace pa {
 namespace {
 
+RaisedDevices g_tables_raised;
+
 constexpr int kTablesThreads = 512;
 constexpr int kTablesMaxSeqs = 12288;  // four int32 per sequence in shared memory
 
@@ -309,9 +311,9 @@ extern "C" int pa_tables_step(int32_t* block_tables, int32_t* context_lens_out, 
                    context_lens, new_lens, free_count, prefix_table, error_flag,
                    num_seqs, num_prefix_blocks, max_blocks_per_seq, block_size, num_physical_blocks, max_tokens};
   const size_t smem = 16 * S;
-  cudaError_t e = cudaFuncSetAttribute(pa_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       16 * kTablesMaxSeqs);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(tables smem)");
+  rc = raise_smem_limit(reinterpret_cast<const void*>(pa_tables_kernel), 16 * kTablesMaxSeqs, dev.device,
+                        &g_tables_raised);
+  if (rc != PA_OK) return rc;
   const long long work = (long long)max_tokens + num_seqs;
   const long long want = (work + 4 * kTablesThreads - 1) / (4 * kTablesThreads);
   cudaLaunchConfig_t cfg = {};
@@ -324,7 +326,7 @@ extern "C" int pa_tables_step(int32_t* block_tables, int32_t* context_lens_out, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, pa_tables_kernel, prm);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, pa_tables_kernel, prm);
   if (e != cudaSuccess) return cuda_fail(e, "launch pa_tables_kernel");
   return PA_OK;
 }
