@@ -549,27 +549,29 @@ def decode_fp8_multi_append(query, k_new, v_new, k_cache, v_cache, block_tables,
 # functions check their tensors with few attribute reads and pass them on directly.
 
 
-def _device_of(first, *ts):
-    """The CUDA device index of contiguous tensors that all live on one device."""
-    index = first.get_device()
-    if index < 0 or not first.is_contiguous():
-        raise ValueError("tensors must be contiguous CUDA tensors on one device")
+def _on(index, dtype, what, *ts):
+    """Contiguous tensors of one type on CUDA device ``index`` (None: an argument left out)."""
     for t in ts:
-        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+        if t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()):
+            if t.dtype is not dtype:
+                raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
             raise ValueError("tensors must be contiguous CUDA tensors on one device")
+
+
+def _device_of(t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must be contiguous CUDA tensors on one device")
     return index
 
 
-def _require_dtype(dtype, what, *ts):
-    for t in ts:
-        if t is not None and t.dtype is not dtype:
-            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_on(stream, index):
     """cudaStream_t of ``stream`` (None: device ``index``'s current stream)."""
     if stream is None:
-        return torch.cuda.current_stream(index).cuda_stream
+        return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         if stream.device.index != index:
             raise ValueError("the stream belongs to another device than the tensors")
@@ -620,11 +622,10 @@ def tables_step(block_tables, context_lens, new_lens, free_blocks, free_count, b
 
     ``block_tables[S, MB]``, ``free_blocks[NB]`` and ``slot_mapping[T]`` (int64) are written in place; returns
     ``(context_lens_out[S], free_count_out[1], seq_starts[S + 1])``, which are not the inputs' buffers."""
-    index = _device_of(block_tables, context_lens, new_lens, free_blocks, free_count, slot_mapping, prefix_table,
-                       context_lens_out, free_count_out, seq_starts, error_flag)
-    _require_dtype(torch.int32, "tables, lengths and the free list", block_tables, context_lens, new_lens,
-                   free_blocks, free_count, prefix_table, context_lens_out, free_count_out, seq_starts, error_flag)
-    _require_dtype(torch.int64, "slot_mapping", slot_mapping)
+    index = _device_of(block_tables)
+    _on(index, torch.int32, "tables, lengths and the free list", block_tables, context_lens, new_lens, free_blocks,
+        free_count, prefix_table, context_lens_out, free_count_out, seq_starts, error_flag)
+    _on(index, torch.int64, "slot_mapping", slot_mapping)
     S, MB = block_tables.shape
     if context_lens.numel() != S or new_lens.numel() != S or free_count.numel() != 1:
         raise ValueError("context_lens and new_lens must have one entry per table row, free_count one entry")
@@ -677,8 +678,11 @@ def pa_decode_mod_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads,
                                                    kv_dtype, num_ranges))
 
 
-def _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out):
+def _step_shapes(index, query, k_cache, v_cache, block_tables, context_lens, out, pool_dtype):
     """(S, Q, H, D, NB, bs, Hk, MB) of a step over paged pools, query [S, H, D] or [S, Q, H, D]."""
+    _on(index, query.dtype, "query and out", query, out)
+    _on(index, pool_dtype, "k_cache and v_cache", k_cache, v_cache)
+    _on(index, torch.int32, "block_tables and context_lens", block_tables, context_lens)
     shape = query.shape
     if len(shape) == 4:
         S, Q, H, D = shape
@@ -690,26 +694,28 @@ def _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out):
     if Dk != D or v_cache.shape != pool or SB != S or context_lens.numel() != S or (
             out is not None and out.shape != shape):
         raise ValueError("shapes of query, pools, block_tables, context_lens and out do not go together")
-    _require_dtype(torch.int32, "block_tables and context_lens", block_tables, context_lens)
     return S, Q, H, D, NB, bs, Hk, MB
 
 
 def _decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, scales, out, stream, softcap,
                 alibi_slopes, window, first_tokens, prefix_lens, num_ranges, workspace, error_flag, check_block_ids):
-    index = _device_of(query, k_cache, v_cache, block_tables, context_lens, out, alibi_slopes, first_tokens,
-                       prefix_lens, workspace, error_flag)
-    S, Q, H, D, NB, bs, Hk, MB = _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out)
-    dtype = query.dtype
-    if scales:
-        _require_dtype(torch.bfloat16, "query", query)
-    _require_dtype(torch.uint8 if scales else dtype, "k_cache and v_cache", k_cache, v_cache)
-    _require_dtype(dtype, "out", out)
-    _require_dtype(torch.int32, "first_tokens, prefix_lens and error_flag", first_tokens, prefix_lens, error_flag)
-    _require_dtype(torch.float32, "alibi_slopes", alibi_slopes)
-    if (alibi_slopes is not None and alibi_slopes.numel() != H) or (
-            first_tokens is not None and first_tokens.numel() != S) or (
-            prefix_lens is not None and prefix_lens.numel() != S):
-        raise ValueError("alibi_slopes has one entry per query head, first_tokens and prefix_lens one per sequence")
+    index, dtype = _device_of(query), query.dtype
+    if scales and dtype is not torch.bfloat16:
+        raise ValueError(f"query must be {torch.bfloat16}, got {dtype}")
+    S, Q, H, D, NB, bs, Hk, MB = _step_shapes(index, query, k_cache, v_cache, block_tables, context_lens, out,
+                                              torch.uint8 if scales else dtype)
+    if alibi_slopes is not None:
+        _on(index, torch.float32, "alibi_slopes", alibi_slopes)
+        if alibi_slopes.numel() != H:
+            raise ValueError("alibi_slopes must have one entry per query head")
+    if first_tokens is not None or prefix_lens is not None:
+        _on(index, torch.int32, "first_tokens and prefix_lens", first_tokens, prefix_lens)
+        if any(t is not None and t.numel() != S for t in (first_tokens, prefix_lens)):
+            raise ValueError("first_tokens and prefix_lens must have one entry per sequence")
+    if error_flag is not None:
+        _on(index, torch.int32, "error_flag", error_flag)
+    if workspace is not None:
+        _on(index, workspace.dtype, "workspace", workspace)
     raw = _stream_on(stream, index)
     if out is None:
         out = torch.empty_like(query)
@@ -763,11 +769,11 @@ def decode_prefix(query, k_cache, v_cache, prefix_table, block_tables, context_l
                   workspace=None, error_flag=None, check_block_ids=False):
     """Decode of a batch that shares the prefix in the blocks ``prefix_table[NP]``, attended once for all (as in
     ``pa_decode_prefix``); query and out [S, H, D] or [S, Q, H, D]."""
-    index = _device_of(query, k_cache, v_cache, prefix_table, block_tables, context_lens, out, workspace, error_flag)
-    S, Q, H, D, NB, bs, Hk, MB = _step_shapes(query, k_cache, v_cache, block_tables, context_lens, out)
-    dtype = query.dtype
-    _require_dtype(dtype, "k_cache, v_cache and out", k_cache, v_cache, out)
-    _require_dtype(torch.int32, "prefix_table and error_flag", prefix_table, error_flag)
+    index, dtype = _device_of(query), query.dtype
+    S, Q, H, D, NB, bs, Hk, MB = _step_shapes(index, query, k_cache, v_cache, block_tables, context_lens, out, dtype)
+    _on(index, torch.int32, "prefix_table and error_flag", prefix_table, error_flag)
+    if workspace is not None:
+        _on(index, workspace.dtype, "workspace", workspace)
     raw = _stream_on(stream, index)
     if out is None:
         out = torch.empty_like(query)

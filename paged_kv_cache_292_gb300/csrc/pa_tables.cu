@@ -27,9 +27,12 @@
 namespace pa {
 namespace {
 
-RaisedDevices g_tables_raised;
+RaisedDevices g_raised_small, g_raised_large;
 
-constexpr int kTablesThreads = 512;
+// Small steps take one CTA whose few warps synchronise quickly, large ones as
+// many threads as an SM's share of slots keeps busy.
+constexpr int kSmallThreads = 256, kLargeThreads = 1024;
+constexpr int kRun = 4;  // consecutive slots a thread writes
 constexpr int kTablesMaxSeqs = 12288;  // four int32 per sequence in shared memory
 
 struct TablesParams {
@@ -47,26 +50,34 @@ struct TablesParams {
   int num_seqs, num_prefix_blocks, max_blocks, block_size, num_physical_blocks, max_tokens;
 };
 
-__device__ __forceinline__ long long block_sum_before(long long v, long long* scratch, int lane, int warp,
-                                                      long long* total) {
-  long long incl = v;
+// Sums of v[0..2] over the threads before this one and over all (THREADS / 32 <= 32 warps).
+template <int THREADS>
+__device__ __forceinline__ void block_sums(long long (&v)[3], long long (&total)[3], long long (&scratch)[3][32],
+                                           int lane, int warp) {
+  long long incl[3];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long n = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += n;
-  }
-  if (lane == 31) scratch[warp] = incl;
-  __syncthreads();
-  long long before = incl - v, sum = 0;
+  for (int q = 0; q < 3; ++q) {
+    incl[q] = v[q];
 #pragma unroll
-  for (int w = 0; w < kTablesThreads / 32; ++w) {
-    const long long x = scratch[w];
-    if (w < warp) before += x;
-    sum += x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long n = __shfl_up_sync(0xffffffffu, incl[q], o);
+      if (lane >= o) incl[q] += n;
+    }
+    if (lane == 31) scratch[q][warp] = incl[q];
   }
   __syncthreads();
-  *total = sum;
-  return before;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const long long mine = lane < THREADS / 32 ? scratch[q][lane] : 0;
+    long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long n = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += n;
+    }
+    v[q] = __shfl_sync(0xffffffffu, sum - mine, warp) + incl[q] - v[q];
+    total[q] = __shfl_sync(0xffffffffu, sum, 31);
+  }
 }
 
 // First index s with ends[s] > x (ends is non-decreasing and its last entry is > x).
@@ -82,9 +93,10 @@ __device__ __forceinline__ int owner_of(const int* ends, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kTablesThreads) pa_tables_kernel(const TablesParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ long long scratch[kTablesThreads / 32];
+  __shared__ long long scratch[3][32], reduce[2][32];
   const int S = p.num_seqs, bs = p.block_size, np = p.num_prefix_blocks;
   int* grow_end = reinterpret_cast<int*>(smem);
   int* need_end = grow_end + S;
@@ -97,7 +109,8 @@ __global__ void __launch_bounds__(kTablesThreads) pa_tables_kernel(const TablesP
   // Per sequence: what it returns, takes and gets, were the pool without end.
   const long long width_tokens = (long long)p.max_blocks * bs;
   int bad = 0;
-  for (int s = tid; s < S; s += kTablesThreads) {
+#pragma unroll 4
+  for (int s = tid; s < S; s += THREADS) {
     const int c = __ldg(p.context_lens + s);
     int n = __ldg(p.new_lens + s);
     const long long first_own = (long long)np * bs;
@@ -128,7 +141,7 @@ __global__ void __launch_bounds__(kTablesThreads) pa_tables_kernel(const TablesP
   __syncthreads();
 
   // Running sums: thread t owns the sequences [t * per, (t + 1) * per).
-  const int per = (S + kTablesThreads - 1) / kTablesThreads;
+  const int per = (S + THREADS - 1) / THREADS;
   const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
   long long grow = 0, need = 0, back = 0;
   for (int s = s0; s < s1; ++s) {
@@ -136,10 +149,10 @@ __global__ void __launch_bounds__(kTablesThreads) pa_tables_kernel(const TablesP
     need += need_end[s];
     back += back_end[s];
   }
-  long long total_grow, total_need, total_back;
-  grow = block_sum_before(grow, scratch, lane, warp, &total_grow);
-  need = block_sum_before(need, scratch, lane, warp, &total_need);
-  back = block_sum_before(back, scratch, lane, warp, &total_back);
+  long long sums[3] = {grow, need, back}, total[3];
+  block_sums<THREADS>(sums, total, scratch, lane, warp);
+  grow = sums[0], need = sums[1], back = sums[2];
+  const long long total_back = total[2];
   const int NB = p.num_physical_blocks;
   int count = __ldg(p.free_count);
   if (count < 0 || count > NB) {
@@ -168,23 +181,22 @@ __global__ void __launch_bounds__(kTablesThreads) pa_tables_kernel(const TablesP
     back_end[s] = (int)(back < NB ? back : NB);
   }
   // The sums at the last sequence served: the largest over the threads.
-  long long last = served_grow;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
-  if (lane == 0) scratch[warp] = last;
+  for (int o = 16; o > 0; o >>= 1) {
+    served_grow = max(served_grow, __shfl_xor_sync(0xffffffffu, served_grow, o));
+    served_need = max(served_need, __shfl_xor_sync(0xffffffffu, served_need, o));
+  }
+  if (lane == 0) {
+    reduce[0][warp] = served_grow;
+    reduce[1][warp] = served_need;
+  }
   __syncthreads();
+  long long total_grow = lane < THREADS / 32 ? reduce[0][lane] : 0, total_need = lane < THREADS / 32 ? reduce[1][lane] : 0;
 #pragma unroll
-  for (int w = 0; w < kTablesThreads / 32; ++w) last = max(last, scratch[w]);
-  __syncthreads();
-  total_grow = last;
-  last = served_need;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
-  if (lane == 0) scratch[warp] = last;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kTablesThreads / 32; ++w) last = max(last, scratch[w]);
-  total_need = last;
+  for (int o = 16; o > 0; o >>= 1) {
+    total_grow = max(total_grow, __shfl_xor_sync(0xffffffffu, total_grow, o));
+    total_need = max(total_need, __shfl_xor_sync(0xffffffffu, total_need, o));
+  }
   for (int s = s0; s < s1; ++s) {
     if (grow_end[s] < 0) {
       grow_end[s] = (int)total_grow;
@@ -195,7 +207,7 @@ __global__ void __launch_bounds__(kTablesThreads) pa_tables_kernel(const TablesP
   griddep_launch_dependents();
   if (first_cta && bad) report(p.error_flag, bad);
 
-  const int gtid = blockIdx.x * kTablesThreads + tid, gthreads = gridDim.x * kTablesThreads;
+  const int gtid = blockIdx.x * THREADS + tid, gthreads = gridDim.x * THREADS;
   const int n_back = (int)(total_back < NB - count ? total_back : NB - count);
   // The block at position i of the free list once the returned ones are on it.
   auto free_block = [&](int i) -> int {
@@ -237,18 +249,46 @@ __global__ void __launch_bounds__(kTablesThreads) pa_tables_kernel(const TablesP
     const int j = (base_of[s] + bs - 1) / bs + k - (s ? need_end[s - 1] : 0);
     p.block_tables[(size_t)s * p.max_blocks + j] = free_block(top - 1 - k);
   }
-  // Slots.
-  for (int i = gtid; i < p.max_tokens; i += gthreads) {
-    long long slot = -1;
-    if (i < (int)total_grow) {
-      const int s = owner_of(grow_end, S, i);
-      const int pos = base_of[s] + i - (s ? grow_end[s - 1] : 0);
-      const int j = pos / bs, held = (base_of[s] + bs - 1) / bs;
-      const int b = j < held ? p.block_tables[(size_t)s * p.max_blocks + j]
-                             : free_block(top - 1 - ((s ? need_end[s - 1] : 0) + j - held));
-      slot = (long long)b * bs + pos % bs;
+  // Slots: a thread writes kRun neighbours, which mostly lie in one block of one
+  // sequence, so that it searches and looks a block up once.
+  const bool wide = (reinterpret_cast<uintptr_t>(p.slot_mapping) & 15u) == 0;
+  for (long long i0 = (long long)gtid * kRun; i0 < p.max_tokens; i0 += (long long)gthreads * kRun) {
+    long long slot[kRun];
+    int s = -1, end = 0, pos = 0, held = 0, need0 = 0, row_block = -1;
+    long long first = 0;  // slot of the current block's token 0
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const long long i = i0 + k;
+      slot[k] = -1;
+      if (i < total_grow) {
+        if (i >= end) {  // another sequence
+          s = owner_of(grow_end, S, static_cast<int>(i));
+          end = grow_end[s];
+          pos = base_of[s] + static_cast<int>(i) - (s ? grow_end[s - 1] : 0);
+          held = (base_of[s] + bs - 1) / bs;
+          need0 = s ? need_end[s - 1] : 0;
+          row_block = -1;
+        }
+        const int j = pos / bs;
+        if (j != row_block) {
+          row_block = j;
+          const int b = j < held ? p.block_tables[(size_t)s * p.max_blocks + j]
+                                 : free_block(top - 1 - (need0 + j - held));
+          first = (long long)b * bs;
+        }
+        slot[k] = first + (pos - j * bs);
+        ++pos;
+      }
     }
-    p.slot_mapping[i] = slot;
+    int64_t* dst = p.slot_mapping + i0;
+    if (wide && i0 + kRun <= p.max_tokens) {
+#pragma unroll
+      for (int k = 0; k < kRun; k += 2) *reinterpret_cast<longlong2*>(dst + k) = make_longlong2(slot[k], slot[k + 1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kRun; ++k)
+        if (i0 + k < p.max_tokens) dst[k] = slot[k];
+    }
   }
 }
 
@@ -311,14 +351,18 @@ extern "C" int pa_tables_step(int32_t* block_tables, int32_t* context_lens_out, 
                    context_lens, new_lens, free_count, prefix_table, error_flag,
                    num_seqs, num_prefix_blocks, max_blocks_per_seq, block_size, num_physical_blocks, max_tokens};
   const size_t smem = 16 * S;
-  rc = raise_smem_limit(reinterpret_cast<const void*>(pa_tables_kernel), 16 * kTablesMaxSeqs, dev.device,
-                        &g_tables_raised);
+  const bool small = num_seqs <= 1024 && max_tokens <= 4096;
+  const int threads = small ? kSmallThreads : kLargeThreads;
+  rc = small ? raise_smem_limit(reinterpret_cast<const void*>(pa_tables_kernel<kSmallThreads>), 16 * kTablesMaxSeqs,
+                                dev.device, &g_raised_small)
+             : raise_smem_limit(reinterpret_cast<const void*>(pa_tables_kernel<kLargeThreads>), 16 * kTablesMaxSeqs,
+                                dev.device, &g_raised_large);
   if (rc != PA_OK) return rc;
   const long long work = (long long)max_tokens + num_seqs;
-  const long long want = (work + 4 * kTablesThreads - 1) / (4 * kTablesThreads);
+  const long long want = (work + kRun * threads - 1) / (kRun * threads);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(want < dev.sm_count ? want : dev.sm_count));
-  cfg.blockDim = dim3(kTablesThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -326,7 +370,8 @@ extern "C" int pa_tables_step(int32_t* block_tables, int32_t* context_lens_out, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, pa_tables_kernel, prm);
+  const cudaError_t e = small ? cudaLaunchKernelEx(&cfg, pa_tables_kernel<kSmallThreads>, prm)
+                              : cudaLaunchKernelEx(&cfg, pa_tables_kernel<kLargeThreads>, prm);
   if (e != cudaSuccess) return cuda_fail(e, "launch pa_tables_kernel");
   return PA_OK;
 }

@@ -3,6 +3,8 @@ device, run the fp64 oracle on (a sample of) its sequences, compare."""
 
 from __future__ import annotations
 
+import gc
+
 import numpy as np
 import torch
 
@@ -90,3 +92,26 @@ def assert_rounded(got: torch.Tensor, want: np.ndarray, spread: np.ndarray, weig
     room = half_step * np.abs(want) + weight_error * spread
     over = np.abs(g - want) - room
     assert np.all(over <= 0), f"{what}: {np.max(over):.3e} beyond its bound, error {np.abs(g - want).max():.3e}"
+
+
+def captured(call):
+    """``call`` captured into a CUDA graph (graphs that are no longer used go before, not in the middle of it)."""
+    gc.collect()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    return graph
+
+
+def refused_under_capture(call, error):
+    """Whether ``call`` raises ``error`` while a stream is being captured."""
+    said = []
+
+    def attempt():
+        try:
+            call()
+        except error as e:
+            said.append(e)
+
+    captured(attempt)
+    return bool(said)

@@ -16,7 +16,7 @@ from oracle import fp8 as ofp8
 from oracle import modified
 from paged_kv_cache_292_gb300 import binding, workloads
 
-from paritylib import assert_rounded
+from paritylib import assert_rounded, captured, refused_under_capture
 
 pytestmark = pytest.mark.gpu
 
@@ -205,14 +205,9 @@ def test_workspace_of_any_content_capture_and_streams(dtype, Q):
     outs = [torch.full_like(args[0], float("nan")) for _, args, _ in parts]
     graphs = []
     for (x, args, kw), out in zip(parts, outs):
-        with pytest.raises(binding.PagedAttnError):  # scratch of the library's own does not go into a graph
-            g = torch.cuda.CUDAGraph()
-            with torch.cuda.graph(g):
-                x.call(args, kw, out=out)
-        g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
-            x.call(args, kw, out=out, workspace=ws)
-        graphs.append(g)
+        # Scratch of the library's own does not go into a graph.
+        assert refused_under_capture(lambda: x.call(args, kw, out=out), binding.PagedAttnError)
+        graphs.append(captured(lambda: x.call(args, kw, out=out, workspace=ws)))
     for _ in range(2):
         for g in graphs:
             g.replay()

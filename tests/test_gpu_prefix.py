@@ -12,7 +12,7 @@ import torch
 from oracle import modified
 from paged_kv_cache_292_gb300 import binding
 
-from paritylib import assert_rounded
+from paritylib import assert_rounded, captured, refused_under_capture
 
 pytestmark = pytest.mark.gpu
 
@@ -197,13 +197,9 @@ def test_workspace_of_any_content_capture_and_streams():
     outs = [torch.full_like(args[0], float("nan")) for _, args in parts]
     graphs = []
     for (b, args), out in zip(parts, outs):
-        g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
-            binding.decode_prefix(*args, out=out, workspace=ws)
-        graphs.append(g)
-    with pytest.raises(binding.PagedAttnError):  # scratch of the library's own does not go into a graph
-        with torch.cuda.graph(torch.cuda.CUDAGraph()):
-            binding.decode_prefix(*parts[0][1])
+        graphs.append(captured(lambda: binding.decode_prefix(*args, out=out, workspace=ws)))
+    # Scratch of the library's own does not go into a graph.
+    assert refused_under_capture(lambda: binding.decode_prefix(*parts[0][1]), binding.PagedAttnError)
     for _ in range(2):
         for g in graphs:
             g.replay()

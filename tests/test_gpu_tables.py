@@ -7,6 +7,8 @@ import torch
 from oracle import tables as oracle_tables
 from paged_kv_cache_292_gb300 import binding
 
+from paritylib import captured
+
 pytestmark = pytest.mark.gpu
 
 
@@ -164,10 +166,12 @@ def test_captured_steps_swap_two_buffers():
     la, lb, ca, cb = t(lens), t(lens), t([count]), t([count])
     starts, slots = t(np.zeros(65)), torch.zeros(64, dtype=torch.int64, device="cuda")
     kw = dict(prefix_table=d_prefix, seq_starts=starts)
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
+
+    def two_steps():
         binding.tables_step(d_tables, la, d_new, d_free, ca, 16, slots, context_lens_out=lb, free_count_out=cb, **kw)
         binding.tables_step(d_tables, lb, d_new, d_free, cb, 16, slots, context_lens_out=la, free_count_out=ca, **kw)
+
+    graph = captured(two_steps)
     state = (tables, lens, free, count)
     for _ in range(3):
         graph.replay()
@@ -177,3 +181,19 @@ def test_captured_steps_swap_two_buffers():
     torch.cuda.synchronize()
     assert np.array_equal(d_tables.cpu().numpy(), state[0]) and np.array_equal(la.cpu().numpy(), state[1])
     assert int(ca) == state[3] and np.array_equal(slots.cpu().numpy(), r[3])
+
+
+@pytest.mark.parametrize("offset, tokens", [(0, 5001), (1, 5001), (1, 8), (1, 1), (3, 4098)])
+def test_slot_buffers_of_any_alignment_and_length(offset, tokens):
+    """A buffer that starts between 16-byte boundaries and ends inside a thread's run; nothing beyond it is written."""
+    rng = np.random.default_rng([12, offset, tokens])
+    tables, lens, free, count, prefix = _state(rng, 90, 8, 100, 1, 60, 2000)
+    new = rng.choice([-1, 0, 1, 3, 60], 90)
+    want = oracle_tables.tables_step(tables, lens, new, free, count, 8, tokens, prefix)
+    t = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()  # noqa: E731
+    room = torch.full((offset + tokens + 3,), -99, dtype=torch.int64, device="cuda")
+    binding.tables_step(t(tables), t(lens), t(new), t(free), t([count]), 8, room[offset : offset + tokens],
+                        prefix_table=t(prefix))
+    got = room.cpu().numpy()
+    assert np.array_equal(got[offset : offset + tokens], want[3])
+    assert np.all(got[:offset] == -99) and np.all(got[offset + tokens :] == -99)
