@@ -27,12 +27,9 @@
 namespace pa {
 namespace {
 
-RaisedDevices g_raised_small, g_raised_large;
-
-// Small steps take one CTA whose few warps synchronise quickly, large ones as
-// many threads as an SM's share of slots keeps busy.
+// Small steps take CTAs whose few warps synchronise quickly, large ones as many
+// threads as an SM's share of slots keeps busy.
 constexpr int kSmallThreads = 256, kLargeThreads = 1024;
-constexpr int kRun = 4;  // consecutive slots a thread writes
 constexpr int kTablesMaxSeqs = 12288;  // four int32 per sequence in shared memory
 
 struct TablesParams {
@@ -93,7 +90,10 @@ __device__ __forceinline__ int owner_of(const int* ends, int n, int x) {
   return lo;
 }
 
-template <int THREADS>
+// RUN: consecutive slots a thread writes.  Prompt chunks mostly lie in one block of
+// one sequence, which a run searches and looks up once; with more threads than
+// slots a thread per slot has the shorter chain of loads.
+template <int THREADS, int RUN>
 __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ long long scratch[3][32], reduce[2][32];
@@ -238,26 +238,29 @@ __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p
     p.seq_starts[S] = (int)total_grow;
     *p.free_count_out = top - (int)total_need;
   }
-  // Returned blocks onto the free list.
-  for (int k = gtid; k < n_back; k += gthreads) {
-    const int s = owner_of(back_end, S, k);
-    p.free_blocks[count + k] = p.block_tables[(size_t)s * p.max_blocks + np + k - (s ? back_end[s - 1] : 0)];
-  }
-  // Taken blocks into the tables.
-  for (int k = gtid; k < (int)total_need; k += gthreads) {
-    const int s = owner_of(need_end, S, k);
-    const int j = (base_of[s] + bs - 1) / bs + k - (s ? need_end[s - 1] : 0);
-    p.block_tables[(size_t)s * p.max_blocks + j] = free_block(top - 1 - k);
-  }
-  // Slots: a thread writes kRun neighbours, which mostly lie in one block of one
-  // sequence, so that it searches and looks a block up once.
+  // One list of work for all threads, each entry a chain of searches and loads of
+  // its own: the slots in runs, the taken blocks into the tables, the returned ones
+  // onto the free list.
+  const long long runs = ((long long)p.max_tokens + RUN - 1) / RUN, takes = runs + total_need, all = takes + n_back;
   const bool wide = (reinterpret_cast<uintptr_t>(p.slot_mapping) & 15u) == 0;
-  for (long long i0 = (long long)gtid * kRun; i0 < p.max_tokens; i0 += (long long)gthreads * kRun) {
-    long long slot[kRun];
+  for (long long entry = gtid; entry < all; entry += gthreads) {
+    if (entry >= takes) {
+      const int k = static_cast<int>(entry - takes), s = owner_of(back_end, S, k);
+      p.free_blocks[count + k] = p.block_tables[(size_t)s * p.max_blocks + np + k - (s ? back_end[s - 1] : 0)];
+      continue;
+    }
+    if (entry >= runs) {
+      const int k = static_cast<int>(entry - runs), s = owner_of(need_end, S, k);
+      const int j = (base_of[s] + bs - 1) / bs + k - (s ? need_end[s - 1] : 0);
+      p.block_tables[(size_t)s * p.max_blocks + j] = free_block(top - 1 - k);
+      continue;
+    }
+    const long long i0 = entry * RUN;
+    long long slot[RUN];
     int s = -1, end = 0, pos = 0, held = 0, need0 = 0, row_block = -1;
     long long first = 0;  // slot of the current block's token 0
 #pragma unroll
-    for (int k = 0; k < kRun; ++k) {
+    for (int k = 0; k < RUN; ++k) {
       const long long i = i0 + k;
       slot[k] = -1;
       if (i < total_grow) {
@@ -281,15 +284,38 @@ __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p
       }
     }
     int64_t* dst = p.slot_mapping + i0;
-    if (wide && i0 + kRun <= p.max_tokens) {
+    if (RUN > 1 && wide && i0 + RUN <= p.max_tokens) {
 #pragma unroll
-      for (int k = 0; k < kRun; k += 2) *reinterpret_cast<longlong2*>(dst + k) = make_longlong2(slot[k], slot[k + 1]);
+      for (int k = 0; k + 1 < RUN; k += 2)
+        *reinterpret_cast<longlong2*>(dst + k) = make_longlong2(slot[k], slot[k + 1]);
     } else {
 #pragma unroll
-      for (int k = 0; k < kRun; ++k)
+      for (int k = 0; k < RUN; ++k)
         if (i0 + k < p.max_tokens) dst[k] = slot[k];
     }
   }
+}
+
+template <int THREADS, int RUN>
+int launch_tables(const TablesParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
+  static RaisedDevices raised;
+  const int rc = raise_smem_limit(reinterpret_cast<const void*>(pa_tables_kernel<THREADS, RUN>), 16 * kTablesMaxSeqs,
+                                  dev.device, &raised);
+  if (rc != PA_OK) return rc;
+  const long long work = (long long)prm.max_tokens / RUN + prm.num_seqs;
+  const long long want = (work + THREADS - 1) / THREADS;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(want < dev.sm_count ? want : dev.sm_count));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = 16 * (size_t)prm.num_seqs;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, pa_tables_kernel<THREADS, RUN>, prm);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_tables_kernel");
 }
 
 bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
@@ -351,27 +377,8 @@ extern "C" int pa_tables_step(int32_t* block_tables, int32_t* context_lens_out, 
                    context_lens, new_lens, free_count, prefix_table, error_flag,
                    num_seqs, num_prefix_blocks, max_blocks_per_seq, block_size, num_physical_blocks, max_tokens};
   const size_t smem = 16 * S;
-  const bool small = num_seqs <= 1024 && max_tokens <= 4096;
-  const int threads = small ? kSmallThreads : kLargeThreads;
-  rc = small ? raise_smem_limit(reinterpret_cast<const void*>(pa_tables_kernel<kSmallThreads>), 16 * kTablesMaxSeqs,
-                                dev.device, &g_raised_small)
-             : raise_smem_limit(reinterpret_cast<const void*>(pa_tables_kernel<kLargeThreads>), 16 * kTablesMaxSeqs,
-                                dev.device, &g_raised_large);
-  if (rc != PA_OK) return rc;
-  const long long work = (long long)max_tokens + num_seqs;
-  const long long want = (work + kRun * threads - 1) / (kRun * threads);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(want < dev.sm_count ? want : dev.sm_count));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = small ? cudaLaunchKernelEx(&cfg, pa_tables_kernel<kSmallThreads>, prm)
-                              : cudaLaunchKernelEx(&cfg, pa_tables_kernel<kLargeThreads>, prm);
-  if (e != cudaSuccess) return cuda_fail(e, "launch pa_tables_kernel");
-  return PA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (num_seqs <= 1024 && max_tokens <= 4096) return launch_tables<kSmallThreads, 1>(prm, dev, st);
+  if (max_tokens <= dev.sm_count * kLargeThreads) return launch_tables<kLargeThreads, 1>(prm, dev, st);
+  return launch_tables<kLargeThreads, 4>(prm, dev, st);
 }
