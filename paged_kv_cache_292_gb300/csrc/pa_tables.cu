@@ -104,6 +104,10 @@ __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p
   int* base_of = back_end + S;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool first_cta = blockIdx.x == 0;
+  // Blocks that hold t tokens, and the block of token t (t < 2^30 + 4096).
+  const int shift = (bs & (bs - 1)) == 0 ? __ffs(bs) - 1 : -1;
+  auto block_of = [&](int t) { return shift >= 0 ? t >> shift : t / bs; };
+  auto blocks_for = [&](int t) { return block_of(t + bs - 1); };
   griddep_wait();
 
   // Per sequence: what it returns, takes and gets, were the pool without end.
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p
     }
     int back = 0, need = 0, base = c;
     if (n == PA_TABLES_RELEASE) {
-      back = c > 0 ? (c + bs - 1) / bs - np : 0;
+      back = c > 0 ? blocks_for(c) - np : 0;
       n = 0;
     } else if (n > 0) {
       if (c == 0) base = (int)first_own;
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p
         bad |= PA_DEVERR_CONTEXT_LEN;
         n = 0;
       } else {
-        need = (int)((end + bs - 1) / bs) - (base + bs - 1) / bs;
+        need = blocks_for((int)end) - blocks_for(base);
       }
     }
     grow_end[s] = n;
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p
     }
     if (entry >= runs) {
       const int k = static_cast<int>(entry - runs), s = owner_of(need_end, S, k);
-      const int j = (base_of[s] + bs - 1) / bs + k - (s ? need_end[s - 1] : 0);
+      const int j = blocks_for(base_of[s]) + k - (s ? need_end[s - 1] : 0);
       p.block_tables[(size_t)s * p.max_blocks + j] = free_block(top - 1 - k);
       continue;
     }
@@ -268,11 +272,11 @@ __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p
           s = owner_of(grow_end, S, static_cast<int>(i));
           end = grow_end[s];
           pos = base_of[s] + static_cast<int>(i) - (s ? grow_end[s - 1] : 0);
-          held = (base_of[s] + bs - 1) / bs;
+          held = blocks_for(base_of[s]);
           need0 = s ? need_end[s - 1] : 0;
           row_block = -1;
         }
-        const int j = pos / bs;
+        const int j = block_of(pos);
         if (j != row_block) {
           row_block = j;
           const int b = j < held ? p.block_tables[(size_t)s * p.max_blocks + j]
