@@ -248,16 +248,18 @@ struct SeqWalk {
 
 // SMs for the prefix kernel of `units` units (pa_prefix_work.h) beside a walk of
 // `tiles` tiles by `groups` CTAs each, in proportion to the SM time of either: a
-// unit takes about 0.9 us (D = 128: 128 x 128 x 128 x 4 flops), a tile about 0.35
-// us + 0.18 us per KiB of K row.  The walk is bound by HBM from about 80 SMs on.
+// unit takes about 0.7 us (D = 128: 128 x 128 x 128 x 4 flops), a tile about 0.35
+// us + 0.18 us per KiB of K row, or 0.65 us with several warps per KV head.  The walk is bound by HBM from about 80 SMs on.
 __device__ __forceinline__ int prefix_share(float units, long long tiles, int groups, float tile_us, int head_size,
                                             int sm_count) {
   if (tiles == 0) return sm_count;
-  const float a = units * (head_size == 128 ? 0.9f : 0.6f), b = static_cast<float>(tiles) * groups * tile_us;
+  const float a = units * (head_size == 128 ? 0.7f : 0.5f), b = static_cast<float>(tiles) * groups * tile_us;
   const int n = __float2int_rn(sm_count * (a / (a + b)));
   return max(1, min(n, sm_count - groups));
 }
-__device__ __forceinline__ float walk_tile_us(uint32_t row_bytes) { return 0.35f + 0.18f / 1024.f * row_bytes; }
+__device__ __forceinline__ float walk_tile_us(uint32_t row_bytes, int columns) {
+  return columns > 8 ? 0.65f : 0.35f + 0.18f / 1024.f * row_bytes;
+}
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
@@ -1932,7 +1934,8 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
   if constexpr (WALK == kWalkRest) {
     // The SMs the prefix kernel leaves.
     if (p.beside) {
-      const int left = p.sm_count - prefix_share(p.prefix_units, total, HG, walk_tile_us(p.row_bytes), D, p.sm_count);
+      const int left = p.sm_count - prefix_share(p.prefix_units, total, HG, walk_tile_us(p.row_bytes, p.group * p.num_queries), D,
+                                                  p.sm_count);
       const long long most = static_cast<long long>(left) * R / p.sm_count;
       Reff = min(Reff, max(most, 1ll));
     }
@@ -2185,7 +2188,9 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
       }
       if (ok && !stall) {
         const uint32_t dst = stages + st * p.stage_bytes + lane_dst;
-        if constexpr (kMmaPath) {
+        if constexpr (WALK == kWalkRest) {  // read once: leave L2 to the prefix
+          tma_load_4d_hint(dst, tmap, 0, 0, hg, row, full_bar(st), l2_policy<false>());
+        } else if constexpr (kMmaPath) {
           tma_load_4d(dst, tmap, 0, 0, hg, row, full_bar(st));
         } else {
           const KV* src = (is_v ? vc : kc) + ((size_t)row * Hk + (size_t)hg * Hg) * D;

@@ -12,11 +12,12 @@
 //
 // Prefix kernel: one persistent CTA per SM, equal shares of the (KV head, pair
 // of 128-row tiles, 128-token tile) list (pa_prefix_work.h).  Per CTA:
-//   warps 0-3, 4-7  softmax groups 0 and 1: thread = row; scores come from
-//                   tensor memory, weights go back there as bf16
-//   warp 8          loads K and V tiles by TMA: boxes of gcd(block_size, 128)
+//   warps 0-7, 8-15 softmax groups 0 and 1: two threads per row, 64 tokens each,
+//                   which exchange their maxima; scores come from tensor memory,
+//                   weights go back there as bf16
+//   warp 16         loads K and V tiles by TMA: boxes of gcd(block_size, 128)
 //                   token rows x 64 elements, into 128-byte swizzled panels
-//   warp 9          issues the products (tcgen05.mma, one thread): S from Q and K in
+//   warp 17         issues the products (tcgen05.mma, one thread): S from Q and K in
 //                   shared memory, O from the weights in tensor memory and V
 // With two row tiles each group has one and both use every K/V tile; with a
 // single row tile the groups take alternate K/V tiles and leave a partial
@@ -35,11 +36,12 @@
 namespace pa {
 namespace {
 
-constexpr int kPrefixThreads = 384;
-// Registers per thread: 168 at launch (65536 / 384, rounded down); the softmax
-// groups hold a row of 128 scores each, the third warpgroup issues copies and
-// products.  2 * 128 * 216 + 128 * 72 = 384 * 168.
-constexpr int kSoftmaxRegisters = 216, kIssueRegisters = 72;
+constexpr int kPrefixThreads = 640;
+// Registers per thread: 96 at launch (65536 / 640, rounded down); a softmax thread
+// holds 64 scores, the fifth warpgroup issues copies and products.
+// 4 * 128 * 104 + 128 * 64 = 640 * 96.
+constexpr int kSoftmaxRegisters = 104, kIssueRegisters = 64;
+constexpr int kSoftmaxWarps = 16, kLoadWarp = 16, kProductWarp = 17;
 constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
 // A running maximum is kept until a tile exceeds it by this factor (log2): until
 // then weights are at most 2^8, which bf16 and the fp32 sums hold as well as 1.
@@ -74,9 +76,10 @@ struct PrefixLayout {
   static constexpr int kPanels = D / 64;
   static constexpr uint32_t kTileBytes = kPanels * kPanel;  // a Q, K or V tile
   static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr uint32_t kQ = 1024;  // from a 1 KiB boundary; barriers before it
+  static constexpr uint32_t kExchange = 1024;  // [2 groups][2 halves][128] floats; barriers before it
+  static constexpr uint32_t kQ = 3 * 1024;
   static constexpr uint32_t kRing = kQ + 2 * kTileBytes;
-  static constexpr uint32_t kBytes = kRing + kStages * kTileBytes + 1024;
+  static constexpr uint32_t kBytes = kRing + kStages * kTileBytes;
 };
 
 // mbar_wait that also gives up when another warp has.
@@ -93,11 +96,12 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uns
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar) {
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar,
+                                            uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -117,9 +121,12 @@ template <int D>
 __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __grid_constant__ PrefixParams p) {
   using L = PrefixLayout<D>;
   constexpr int NS = L::kStages;
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
+  extern __shared__ __align__(1024) unsigned char smem[];  // swizzled panels start on 1 KiB boundaries
+  const uint32_t base = smem_addr(smem);
+  if ((base & 1023u) != 0) {  // cannot be: the array asks for it
+    if (threadIdx.x == 0) report(p.error_flag, PA_DEVERR_TIMEOUT);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t bars = base;
   auto full = [&](int i) { return bars + 8u * i; };
@@ -129,6 +136,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   auto p_full = [&](int w) { return bars + 8u * (2 * NS + 3 + w); };
   auto o_full = [&](int w) { return bars + 8u * (2 * NS + 5 + w); };
   const uint32_t drained = bars + 8u * (2 * NS + 7);
+  auto exchanged = [&](int w) { return bars + 8u * (2 * NS + 8 + w); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 512);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + 516);
   auto timed_out = [&]() {
@@ -155,7 +163,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
     walk = 0;
     for (int i = 0; i < kPrefixThreads / 32; ++i) walk += sums[i];
     wk.ctas = min(wk.ctas, prefix_share(static_cast<float>(wk.total()), walk, p.walk_groups,
-                                        walk_tile_us(p.walk_row_bytes), D, p.sm_count));
+                                        walk_tile_us(p.walk_row_bytes, p.group * p.num_queries), D, p.sm_count));
   }
   const int cta = blockIdx.x;
   if (cta >= wk.ctas) return;
@@ -165,17 +173,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
       mbar_init(full(i), 1);
       mbar_init(empty(i), 1);
     }
-    mbar_init(q_full, 256);
+    mbar_init(q_full, kSoftmaxWarps);
     for (int w = 0; w < 2; ++w) {
+      mbar_init(exchanged(w), kSoftmaxWarps / 2);
       mbar_init(s_full(w), 1);
-      mbar_init(p_full(w), 4);
+      mbar_init(p_full(w), kSoftmaxWarps / 2);
       mbar_init(o_full(w), 1);
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == 9) tmem_alloc(smem_addr(smem + 516), 512);
+  if (warp == kProductWarp) tmem_alloc(smem_addr(smem + 516), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -183,110 +192,122 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   const int64_t ua = wk.cta_start(cta), ub = wk.cta_start(cta + 1);
   const int first_item = wk.item_of(ua);
 
-  if (warp < 8)
+  if (warp < kSoftmaxWarps)
     registers_up<kSoftmaxRegisters>();
   else
     registers_down<kIssueRegisters>();
 
-  if (warp < 8) {
+  if (warp < kSoftmaxWarps) {
     // ---------------- softmax ----------------
-    const int w = warp >> 2, row = tid & 127;
+    const int w = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the TMEM lanes
-    const uint32_t s_addr = tmem + lanes + 128u * w, o_addr = tmem + lanes + 256u + (uint32_t)D * w;
-    uint32_t s_phase = 0, o_phase = 0;
+    const uint32_t s_addr = tmem + lanes + 128u * w, o_addr = tmem + lanes + 256u + (uint32_t)D * w + (D / 2) * half;
+    float* mine = reinterpret_cast<float*>(smem + L::kExchange) + (w * 2 + half) * 128 + row;
+    const float* other = reinterpret_cast<const float*>(smem + L::kExchange) + (w * 2 + (half ^ 1)) * 128 + row;
+    uint32_t s_phase = 0, o_phase = 0, x_phase = 0;
+    // Give the row's other thread `v` and get its value.  (What it gave before has
+    // been read: either the weights of the tile in between, which the tensor core
+    // waits for, or the next queries came after that.)
+    auto exchange = [&](float v, float* got) -> bool {
+      *mine = v;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(exchanged(w));
+      if (!wait_or_abort(exchanged(w), x_phase, p.wait_limit_ns, abort_flag)) return false;
+      x_phase ^= 1u;
+      tc_fence_after();
+      *got = *other;
+      return true;
+    };
     for (int item = first_item; item < wk.items() && wk.item_start(item) < ub; ++item) {
       const int t0 = wk.tile_at(item, ua), t1 = wk.tile_at(item, ub);
       if (t0 >= t1) continue;
       const bool two = wk.weight(item) == 2;
       const int head = item / wk.pairs, row0 = (item % wk.pairs) * 2 * kPrefixRows;
-      // The row's queries into the swizzled Q tile: with two row tiles a whole
-      // row per thread, with one a half row.
+      // The row's queries into the swizzled Q tile: half a row per thread with
+      // two row tiles, a quarter with one.
       {
         const int r = row0 + (two ? w * kPrefixRows : 0) + row;
         constexpr int kUnits = D / 8;  // 16-byte units of a row
-        const int u0 = two ? 0 : w * (kUnits / 2), u1 = two ? kUnits : u0 + kUnits / 2;
+        const int n = two ? kUnits / 2 : kUnits / 4, u0 = n * (two ? half : 2 * w + half);
         const uint4* src = nullptr;
         if (r < p.rows) {
           const int tok = r / p.group, g = r - tok * p.group;
           src = reinterpret_cast<const uint4*>(p.q + ((size_t)tok * p.num_heads + head * p.group + g) * D);
         }
         unsigned char* dst = smem + L::kQ + (two ? w * L::kTileBytes : 0) + row * 128;
-#pragma unroll 8
-        for (int u = u0; u < u1; ++u) {
-          uint4 v = src != nullptr ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
-          v.x = (v.x & p.q_keep) ^ p.q_flip;
-          v.y = (v.y & p.q_keep) ^ p.q_flip;
-          v.z = (v.z & p.q_keep) ^ p.q_flip;
-          v.w = (v.w & p.q_keep) ^ p.q_flip;
-          *reinterpret_cast<uint4*>(dst + (u >> 3) * kPanel + (((u & 7) ^ (row & 7)) << 4)) = v;
+        uint4 v[kUnits / 2];
+#pragma unroll
+        for (int i = 0; i < kUnits / 2; ++i)
+          v[i] = src != nullptr && i < n ? __ldg(src + u0 + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < kUnits / 2; ++i) {
+          if (i < n) {
+            const int u = u0 + i;
+            v[i].x = (v[i].x & p.q_keep) ^ p.q_flip;
+            v[i].y = (v[i].y & p.q_keep) ^ p.q_flip;
+            v[i].z = (v[i].z & p.q_keep) ^ p.q_flip;
+            v[i].w = (v[i].w & p.q_keep) ^ p.q_flip;
+            *reinterpret_cast<uint4*>(dst + (u >> 3) * kPanel + (((u & 7) ^ (row & 7)) << 4)) = v[i];
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
-        mbar_arrive(q_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
       }
       const int step = two ? 1 : 2;
       float m = -INFINITY, l = 0.f;
       bool alive = true;
       for (int x = t0 + (two ? 0 : w); x < t1; x += step) {
         if (!wait_or_abort(s_full(w), s_phase, p.wait_limit_ns, abort_flag)) {
-          timed_out();
           alive = false;
           break;
         }
         s_phase ^= 1u;
         tc_fence_after();
-        // Two halves, so that the second one's load runs under the first one's maximum.
-        float s[128];
-        auto fetch = [&](int c) {
-          tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]), s_addr + 32u * c);
-        };
-        fetch(0);
-        fetch(1);
+        float s[64];
+        tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[0]), s_addr + 64u * half);
+        tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[32]), s_addr + 64u * half + 32u);
         tmem_wait_load();
-        fetch(2);
-        fetch(3);
+        const int nvalid = p.prefix_tokens - x * kPrefixTokens - 64 * half;
+        if (nvalid < 64) {  // the prefix's last tile
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i >= nvalid) s[i] = -INFINITY;
+        }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < 64; i += 8)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mx[j] = i + 4 < 64 ? fmaxf(fmaxf(mx[j], s[i + j]), s[i + 4 + j]) : fmaxf(mx[j], s[i + j]);
-        tmem_wait_load();
-#pragma unroll
-        for (int i = 64; i < 128; i += 8)
+        for (int i = 4; i < 60; i += 8)
 #pragma unroll
           for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], s[i + j]), s[i + 4 + j]);
-        const int nvalid = p.prefix_tokens - x * kPrefixTokens;
-        if (nvalid < kPrefixTokens) {  // the prefix's last tile
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= nvalid) s[i] = -INFINITY;
-          mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 128; i += 4)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[i + j]);
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[60 + j]);
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), theirs;
+        // Behind the exchange both threads of every row have read their scores,
+        // which the weights may now overwrite.
+        if (!exchange(top, &theirs)) {
+          alive = false;
+          break;
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (m == -INFINITY) {
-          m = top;  // nothing but zero weights so far
-        }
+        top = fmaxf(top, theirs);
+        if (m == -INFINITY) m = top;  // nothing but zero weights so far
         const bool moves = (top - m) * p.scale_log2 > kSlack;
         if (__any_sync(0xffffffffu, moves)) {
           // The products of the group's earlier tiles are done (the scores were
-          // issued behind them), so O can be scaled here.
+          // issued behind them), so O can be scaled here, half its columns each.
           const float f = moves ? ex2_ftz((m - top) * p.scale_log2) : 1.f;
           if (moves) m = top;
           l *= f;
           if (x >= t0 + step) {
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_load32(o, o_addr + 32u * c);
+              uint32_t o[16];
+              tmem_load16(o, o_addr + 16u * c);
               tmem_wait_load();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_store32(o_addr + 32u * c, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_store16(o_addr + 16u * c, o);
             }
           }
         }
@@ -295,10 +316,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int e = 64 * c + 2 * i;
+          for (int i = 0; i < 16; ++i) {
+            const int e = 32 * c + 2 * i;
             float a, b;
             unpair(fma_pair(pair(s[e], s[e + 1]), scale2, neg2), a, b);
             a = ex2_ftz(a);
@@ -308,7 +329,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
             // both signs alike); the sum keeps them in fp32.
             pk[i] = pack_bf16x2(a, b);
           }
-          tmem_store32(s_addr + 32u * c, pk);
+          tmem_store16(s_addr + 32u * half + 16u * c, pk);
         }
         {
           float a, b;
@@ -320,35 +341,42 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(w));
       }
-      if (!alive) break;
-      if (!wait_or_abort(o_full(w), o_phase, p.wait_limit_ns, abort_flag)) {
+      if (alive) alive = wait_or_abort(o_full(w), o_phase, p.wait_limit_ns, abort_flag);
+      float theirs = 0.f;
+      if (alive) {
+        o_phase ^= 1u;
+        tc_fence_after();
+        alive = exchange(l, &theirs);
+      }
+      if (!alive) {
         timed_out();
         break;
       }
-      o_phase ^= 1u;
-      tc_fence_after();
       const size_t at = ((size_t)(cta + item) * 2 + w) * kPrefixRows + row;
-      *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m * p.scale_log2, l);
+      if (half == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m * p.scale_log2, l + theirs);
       if (t0 + (two ? 0 : w) < t1) {  // this group had a tile
-        float4* dst = reinterpret_cast<float4*>(p.part_o) + (at - row) * (D / 4) + row;
+        float4* dst = reinterpret_cast<float4*>(p.part_o) + (at - row) * (D / 4) + (D / 8) * half * kPrefixRows + row;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
           uint32_t o[32];
           tmem_load32(o, o_addr + 32u * c);
           tmem_wait_load();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             dst[(8 * c + i) * kPrefixRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == kLoadWarp) {
     // ---------------- loads ----------------
     if (lane == 0) {
       prefetch_tensormap(&p.tm_k);
       prefetch_tensormap(&p.tm_v);
     }
+    // The prefix's rows are read by every pair of row tiles, the walk's beside this
+    // kernel only once: keep these in L2.
+    const uint64_t policy = l2_policy<true>();
     const int boxes = kPrefixTokens / p.box_rows;
     const int box = lane / L::kPanels, panel = lane % L::kPanels;
     const bool mine = box < boxes;
@@ -382,7 +410,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
           // A chunk beyond the row's last is outside the tensor: zeros, without a read.
           if (mine)
             tma_load_3d(base + L::kRing + ring.i * L::kTileBytes + dst0, tmap, 0,
-                        (row < 0 ? wk.kv_heads : head) * L::kPanels + panel, row < 0 ? 0 : row, full(ring.i));
+                        (row < 0 ? wk.kv_heads : head) * L::kPanels + panel, row < 0 ? 0 : row, full(ring.i), policy);
           armed |= 1u << ring.i;
           armed_phase = (armed_phase & ~(1u << ring.i)) | (ring.phase << ring.i);
         }
@@ -411,7 +439,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
       for (int i = 0; i < NS; ++i)
         if ((armed >> i) & 1u) (void)mbar_wait(full(i), (armed_phase >> i) & 1u, p.wait_limit_ns);
     }
-  } else if (warp == 9) {
+  } else if (warp == kProductWarp) {
     // ---------------- products ----------------
     constexpr uint32_t kScores = bf16_product(128, 128, false), kValues = bf16_product(128, D, true);
     Ring ring;
@@ -504,17 +532,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
     tmem_free(tmem, 512);
     return;
   }
-  if (warp < 8 || warp > 9) {  // (warps 10 and 11 only fill their warpgroup)
+  if (warp < kSoftmaxWarps || warp > kProductWarp) {  // (the last two warps only fill their warpgroup)
     tc_fence_before();
     named_barrier_sync(1, kPrefixThreads);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Join: a warp adds the partials of two neighbouring rows of a KV head (of the
-// prefix, when their sequences share it, and the rest) by log-sum-exp.  Two,
-// because a partial's rows lie side by side, four dims of each: a lane reads both
-// rows' dims as one 32-byte sector.
+// Join: a warp per output row adds the row's partials by log-sum-exp: those of
+// the prefix, when its sequence shares it, and those of the rest.  The maxima and
+// sums of up to 32 partials of either kind are read at once, one per lane; what
+// bounds it is the chain of dependent loads, so the lists go side by side.
 // ---------------------------------------------------------------------------
 struct JoinParams {
   __nv_bfloat16* out;
@@ -528,136 +556,93 @@ struct JoinParams {
   const float* walk_o;
   const int32_t* ctas;  // of the prefix kernel
   PrefixWork work;
-  int rows;   // query rows per KV head
-  int pairs;  // of them, rounded up
-  int num_kv_heads, num_queries, num_heads, group, prefix_tokens, max_tokens;
+  long long rows;  // num_seqs * num_queries * num_heads
+  int num_queries, num_heads, group, prefix_tokens, max_tokens;
 };
 
 template <int D>
 __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ JoinParams p) {
-  constexpr int kLanes = D / 4;  // lanes that hold four dims of each row
+  constexpr int kLanes = D / 4;  // lanes that hold four dims
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (unit >= (long long)p.pairs * p.num_kv_heads) return;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  const int token = static_cast<int>(row / p.num_heads), h = static_cast<int>(row - (long long)token * p.num_heads);
+  const int seq = token / p.num_queries, kv = h / p.group;
+  const long long r = (long long)token * p.group + (h - kv * p.group);  // row of the KV head
+  PrefixWork wk = p.work;
+  const bool prefix = wk.tiles > 0;
+  const int item = prefix ? kv * wk.pairs + static_cast<int>(r / (2 * kPrefixRows)) : 0;
+  const int in_pair = static_cast<int>(r % (2 * kPrefixRows));
+  const bool two = prefix && wk.weight(item) == 2;
   griddep_wait();
   griddep_launch_dependents();
-  const int kv = (int)(unit / p.pairs), r0 = 2 * (int)(unit - (long long)kv * p.pairs);
-  const int n = min(2, p.rows - r0);
-  const bool holds = lane < kLanes;
-  long long row[2];  // output row
-  bool shares[2];
-  float m[2], l[2], acc[2][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = min(r0 + i, p.rows - 1), token = r / p.group;
-    row[i] = (long long)token * p.num_heads + kv * p.group + (r - token * p.group);
-    const int c = min(__ldg(p.context_lens + token / p.num_queries), p.max_tokens);
-    shares[i] = c >= p.prefix_tokens + p.num_queries - 1;
-    // The rest: nothing, a row the walk finished, or partials of several ranges.
-    const int seq = token / p.num_queries;
-    const int4 cut = __ldcg(p.cuts + seq);
-    m[i] = -INFINITY;
-    l[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
-    if (cut.w == kCutWhole) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.rest_ml) + row[i]);
-      if (ml.y > 0.f) {
-        m[i] = ml.x;
-        l[i] = ml.y;
-        if (holds) {
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(p.rest_o + row[i] * D) + lane);
-          acc[i][0] = o.x, acc[i][1] = o.y, acc[i][2] = o.z, acc[i][3] = o.w;
-        }
-      }
-    } else if (cut.w == kCutMerge) {
-      const int seq_rows = p.num_queries * p.num_heads;
-      const MergedRow<D / 32> r = merge_row<D>(p.walk_ml, p.walk_o, cut, seq_rows,
-                                               static_cast<int>(row[i] - (long long)seq * seq_rows), lane);
-      m[i] = r.l > 0.f ? r.m : -INFINITY;
-      l[i] = r.l;
-      if constexpr (D == 128) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][k] = r.o[k];
-      } else {
-        // Two dims a lane there, four here.
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = __shfl_sync(0xffffffffu, r.o[k & 1], (2 * lane + (k >> 1)) & 31);
-          acc[i][k] = holds ? x : 0.f;
-        }
-      }
-    }
+  const int4 cut = __ldcg(p.cuts + seq);
+  const int c = min(__ldg(p.context_lens + seq), p.max_tokens);
+  wk.ctas = prefix ? __ldcg(p.ctas) : 1;
+  // Prefix partials: every CTA between the first and the last tile's has one (a
+  // range holds two units or more), with a single row tile one per group.
+  int np = 0, c0 = 0;
+  if (prefix && c >= p.prefix_tokens + p.num_queries - 1) {
+    c0 = wk.cta_of(item, 0);
+    np = (wk.cta_of(item, wk.tiles - 1) - c0 + 1) * (two ? 1 : 2);
   }
-  if (shares[0] || shares[1]) {
-    const int pair = r0 / (2 * kPrefixRows), in_pair = r0 - pair * 2 * kPrefixRows;
-    PrefixWork wk = p.work;
-    wk.ctas = __ldcg(p.ctas);
-    const int item = kv * wk.pairs + pair;
-    const bool two = wk.weight(item) == 2;
-    // Every CTA between the two has a partial: a range holds two units or more.
-    const int c0 = wk.cta_of(item, 0), c1 = wk.cta_of(item, wk.tiles - 1);
-    const int parts = (c1 - c0 + 1) * (two ? 1 : 2);
-    for (int j0 = 0; j0 < parts; j0 += 32) {
-      const int j = j0 + lane, cta = c0 + (two ? j : j >> 1);
-      float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);  // (m, l) of both rows
-      int at = 0;  // partial: slot and softmax group
-      if (j < parts) {
-        at = (cta + item) * 2 + (two ? in_pair >> 7 : j & 1);
-        ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + ((size_t)at * kPrefixRows + (in_pair & 127)) * 2));
-      }
-      float w[2];
+  // Partials of the rest: none, the walk's finished row, or one per range.
+  const bool whole = cut.w == kCutWhole;
+  const int nr = cut.w == kCutEmpty ? 0 : whole ? 1 : cut.y - cut.x + 1;
+  const float* ml_r = whole ? p.rest_ml : p.walk_ml;
+  const float* o_r = whole ? p.rest_o : p.walk_o;
+  const int seq_rows = p.num_queries * p.num_heads, in_seq = static_cast<int>(row - (long long)seq * seq_rows);
+  auto rest_at = [&](int k) -> size_t {
+    return whole ? (size_t)row : ((size_t)(cut.x + k) * 2 + (k == 0 ? cut.z : 0)) * seq_rows + in_seq;
+  };
+  auto part_at = [&](int k) -> int { return (c0 + (two ? k : k >> 1) + item) * 2 + (two ? in_pair >> 7 : k & 1); };
+  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < max(nr, np); k0 += 32) {
+    const int k = k0 + lane;
+    float2 a = make_float2(-INFINITY, 0.f), b = a;
+    if (k < nr) a = __ldcg(reinterpret_cast<const float2*>(ml_r) + rest_at(k));
+    if (k < np) b = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)part_at(k) * kPrefixRows + (in_pair & 127));
+    if (!(a.y > 0.f)) a = make_float2(-INFINITY, a.y == 0.f ? 0.f : a.y);  // no token seen: no weight (NaN stays)
+    if (!(b.y > 0.f)) b = make_float2(-INFINITY, b.y == 0.f ? 0.f : b.y);
+    float top = fmaxf(a.x, b.x);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float pm = i ? ml.z : ml.x, pl = i ? ml.w : ml.y;
-        const bool some = shares[i] && pl > 0.f;
-        float top = some ? pm : -INFINITY;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+    const float keep = ex2_ftz(m - ref);
+    const float wa = ex2_ftz(a.x - ref), wb = ex2_ftz(b.x - ref);
+    m = mn;
+    float lw = (a.y != 0.f ? wa * a.y : 0.f) + (b.y != 0.f ? wb * b.y : 0.f);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float mn = fmaxf(m[i], top), ref = mn == -INFINITY ? 0.f : mn;
-        const float keep = ex2_ftz(m[i] - ref);
-        w[i] = some ? ex2_ftz(pm - ref) : 0.f;
-        m[i] = mn;
-        float lw = some ? w[i] * pl : 0.f;
+    for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    l = l * keep + lw;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-        l[i] = l[i] * keep + lw;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][k] *= keep;
-      }
-      const int here = min(32, parts - j0);
+    for (int i = 0; i < 4; ++i) acc[i] *= keep;
+    const int here_r = min(32, nr - k0), here_p = min(32, np - k0);
 #pragma unroll 4
-      for (int k = 0; k < here; ++k) {
-        const float w0 = __shfl_sync(0xffffffffu, w[0], k), w1 = __shfl_sync(0xffffffffu, w[1], k);
-        const int ak = __shfl_sync(0xffffffffu, at, k);
-        // A partial without weight may hold anything.
-        if (holds && (w0 != 0.f || w1 != 0.f)) {
-          const float4* o = reinterpret_cast<const float4*>(p.part_o) +
-                            ((size_t)ak * (D / 4) + lane) * kPrefixRows + (in_pair & 127);
-          const float4 a = __ldcg(o), b = __ldcg(o + 1);
-          if (w0 != 0.f) {
-            acc[0][0] = fmaf(w0, a.x, acc[0][0]);
-            acc[0][1] = fmaf(w0, a.y, acc[0][1]);
-            acc[0][2] = fmaf(w0, a.z, acc[0][2]);
-            acc[0][3] = fmaf(w0, a.w, acc[0][3]);
-          }
-          if (w1 != 0.f) {
-            acc[1][0] = fmaf(w1, b.x, acc[1][0]);
-            acc[1][1] = fmaf(w1, b.y, acc[1][1]);
-            acc[1][2] = fmaf(w1, b.z, acc[1][2]);
-            acc[1][3] = fmaf(w1, b.w, acc[1][3]);
-          }
-        }
+    for (int i = 0; i < here_r; ++i) {
+      const float w = __shfl_sync(0xffffffffu, wa, i);
+      if (w != 0.f && lane < kLanes) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(o_r + rest_at(k0 + i) * D) + lane);
+        acc[0] = fmaf(w, o.x, acc[0]), acc[1] = fmaf(w, o.y, acc[1]);
+        acc[2] = fmaf(w, o.z, acc[2]), acc[3] = fmaf(w, o.w, acc[3]);
+      }
+    }
+#pragma unroll 4
+    for (int i = 0; i < here_p; ++i) {
+      const float w = __shfl_sync(0xffffffffu, wb, i);
+      // A partial without weight may hold anything.
+      if (w != 0.f && lane < kLanes) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o) +
+                                ((size_t)part_at(k0 + i) * (D / 4) + lane) * kPrefixRows + (in_pair & 127));
+        acc[0] = fmaf(w, o.x, acc[0]), acc[1] = fmaf(w, o.y, acc[1]);
+        acc[2] = fmaf(w, o.z, acc[2]), acc[3] = fmaf(w, o.w, acc[3]);
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (i < n && holds) {
-      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-      *reinterpret_cast<uint2*>(p.out + row[i] * D + 4 * lane) =
-          make_uint2(pack_bf16x2(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
-    }
+  if (lane < kLanes) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2*>(p.out + row * D + 4 * lane) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   }
 }
 
@@ -881,15 +866,13 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   jp.walk_o = ex.part_o;
   jp.ctas = prm.ctas_out;
   jp.work = prm.work;
-  jp.rows = (int)rows;
-  jp.pairs = (int)((rows + 1) / 2);
-  jp.num_kv_heads = num_kv_heads;
+  jp.rows = (long long)num_seqs * num_queries * num_heads;
   jp.num_queries = num_queries;
   jp.num_heads = num_heads;
   jp.group = group;
-  jp.prefix_tokens = num_prefix_blocks > 0 ? prefix_tokens : (1 << 30) + 1;  // beyond any context: nobody shares
+  jp.prefix_tokens = prefix_tokens;
   jp.max_tokens = max_blocks_per_seq * block_size;
-  const dim3 grid((unsigned)(((long long)jp.pairs * num_kv_heads + 7) / 8));
+  const dim3 grid((unsigned)((jp.rows + 7) / 8));
   const cudaError_t e = head_size == 64 ? launch_pdl(pa_prefix_join<64>, grid, dim3(256), 0, st, jp)
                                         : launch_pdl(pa_prefix_join<128>, grid, dim3(256), 0, st, jp);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefix_join");
