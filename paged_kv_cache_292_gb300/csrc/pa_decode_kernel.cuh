@@ -249,11 +249,12 @@ struct SeqWalk {
 // SMs for the prefix kernel of `units` units (pa_prefix_work.h) beside a walk of
 // `tiles` tiles by `groups` CTAs each, in proportion to the SM time of either: a
 // unit takes about 0.7 us (D = 128: 128 x 128 x 128 x 4 flops), a tile about 0.35
-// us + 0.18 us per KiB of K row, or 0.65 us with several warps per KV head.  The walk is bound by HBM from about 80 SMs on.
-__device__ __forceinline__ int prefix_share(float units, long long tiles, int groups, float tile_us, int head_size,
-                                            int sm_count) {
+// us + 0.18 us per KiB of K row, or 0.65 us with several warps per KV head, and a
+// sequence another 0.8 us (its queries, its row).  The walk is bound by HBM from about 80 SMs on.
+__device__ __forceinline__ int prefix_share(float units, long long tiles, int seqs, int groups, float tile_us,
+                                            int head_size, int sm_count) {
   if (tiles == 0) return sm_count;
-  const float a = units * (head_size == 128 ? 0.7f : 0.5f), b = static_cast<float>(tiles) * groups * tile_us;
+  const float a = units * (head_size == 128 ? 0.7f : 0.5f), b = (tiles * tile_us + seqs * 0.8f) * groups;
   const int n = __float2int_rn(sm_count * (a / (a + b)));
   return max(1, min(n, sm_count - groups));
 }
@@ -1934,7 +1935,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
   if constexpr (WALK == kWalkRest) {
     // The SMs the prefix kernel leaves.
     if (p.beside) {
-      const int left = p.sm_count - prefix_share(p.prefix_units, total, HG, walk_tile_us(p.row_bytes, p.group * p.num_queries), D,
+      const int left = p.sm_count - prefix_share(p.prefix_units, total, S, HG, walk_tile_us(p.row_bytes, p.group * p.num_queries), D,
                                                   p.sm_count);
       const long long most = static_cast<long long>(left) * R / p.sm_count;
       Reff = min(Reff, max(most, 1ll));
@@ -2189,7 +2190,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
       if (ok && !stall) {
         const uint32_t dst = stages + st * p.stage_bytes + lane_dst;
         if constexpr (WALK == kWalkRest) {  // read once: leave L2 to the prefix
-          tma_load_4d_hint(dst, tmap, 0, 0, hg, row, full_bar(st), l2_policy<false>());
+          tma_load_4d_hint(dst, tmap, 0, 0, hg, row, full_bar(st), l2_evict_first());
         } else if constexpr (kMmaPath) {
           tma_load_4d(dst, tmap, 0, 0, hg, row, full_bar(st));
         } else {

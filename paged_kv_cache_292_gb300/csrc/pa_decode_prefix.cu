@@ -55,7 +55,7 @@ struct PrefixParams {
   float* part_ml;  // [slots][2][128][2]
   float* part_o;   // [slots][2][D / 4][128][4]: a thread's row side by side with its neighbours'
   PrefixWork work;  // `ctas`: at most; what the walk behind the prefix leaves is taken (prefix_share)
-  int32_t* ctas_out;
+  int2* item_ctas;  // [items]: first and last CTA with a partial
   const int32_t* context_lens;
   int num_seqs, num_queries, max_tokens;  // of the walk: its tiles,
   int walk_groups, walk_row_bytes;        // and the shape of its CTAs
@@ -96,12 +96,11 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uns
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar,
-                                            uint64_t policy) {
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
 
@@ -162,12 +161,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
     __syncthreads();
     walk = 0;
     for (int i = 0; i < kPrefixThreads / 32; ++i) walk += sums[i];
-    wk.ctas = min(wk.ctas, prefix_share(static_cast<float>(wk.total()), walk, p.walk_groups,
+    wk.ctas = min(wk.ctas, prefix_share(static_cast<float>(wk.total()), walk, p.num_seqs, p.walk_groups,
                                         walk_tile_us(p.walk_row_bytes, p.group * p.num_queries), D, p.sm_count));
   }
   const int cta = blockIdx.x;
   if (cta >= wk.ctas) return;
-  if (cta == 0 && tid == 0) *p.ctas_out = wk.ctas;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full(i), 1);
@@ -354,6 +352,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
       }
       const size_t at = ((size_t)(cta + item) * 2 + w) * kPrefixRows + row;
       if (half == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m * p.scale_log2, l + theirs);
+      if (tid == 0) {
+        if (t0 == 0) p.item_ctas[item].x = cta;
+        if (t1 == wk.tiles) p.item_ctas[item].y = cta;
+      }
       if (t0 + (two ? 0 : w) < t1) {  // this group had a tile
         float4* dst = reinterpret_cast<float4*>(p.part_o) + (at - row) * (D / 4) + (D / 8) * half * kPrefixRows + row;
 #pragma unroll
@@ -374,9 +376,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
       prefetch_tensormap(&p.tm_k);
       prefetch_tensormap(&p.tm_v);
     }
-    // The prefix's rows are read by every pair of row tiles, the walk's beside this
-    // kernel only once: keep these in L2.
-    const uint64_t policy = l2_policy<true>();
     const int boxes = kPrefixTokens / p.box_rows;
     const int box = lane / L::kPanels, panel = lane % L::kPanels;
     const bool mine = box < boxes;
@@ -410,7 +409,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
           // A chunk beyond the row's last is outside the tensor: zeros, without a read.
           if (mine)
             tma_load_3d(base + L::kRing + ring.i * L::kTileBytes + dst0, tmap, 0,
-                        (row < 0 ? wk.kv_heads : head) * L::kPanels + panel, row < 0 ? 0 : row, full(ring.i), policy);
+                        (row < 0 ? wk.kv_heads : head) * L::kPanels + panel, row < 0 ? 0 : row, full(ring.i));
           armed |= 1u << ring.i;
           armed_phase = (armed_phase & ~(1u << ring.i)) | (ring.phase << ring.i);
         }
@@ -554,9 +553,9 @@ struct JoinParams {
   const int4* cuts;  // the walk's, and its partials
   const float* walk_ml;
   const float* walk_o;
-  const int32_t* ctas;  // of the prefix kernel
+  const int2* item_ctas;
   PrefixWork work;
-  long long rows;  // num_seqs * num_queries * num_heads
+  int rows;  // num_seqs * num_queries * num_heads
   int num_queries, num_heads, group, prefix_tokens, max_tokens;
 };
 
@@ -564,34 +563,31 @@ template <int D>
 __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ JoinParams p) {
   constexpr int kLanes = D / 4;  // lanes that hold four dims
   const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= p.rows) return;
-  const int token = static_cast<int>(row / p.num_heads), h = static_cast<int>(row - (long long)token * p.num_heads);
+  const int token = row / p.num_heads, h = row - token * p.num_heads;
   const int seq = token / p.num_queries, kv = h / p.group;
-  const long long r = (long long)token * p.group + (h - kv * p.group);  // row of the KV head
-  PrefixWork wk = p.work;
-  const bool prefix = wk.tiles > 0;
-  const int item = prefix ? kv * wk.pairs + static_cast<int>(r / (2 * kPrefixRows)) : 0;
-  const int in_pair = static_cast<int>(r % (2 * kPrefixRows));
-  const bool two = prefix && wk.weight(item) == 2;
+  const int r = token * p.group + (h - kv * p.group);  // row of the KV head
+  const bool prefix = p.work.tiles > 0;
+  const int item = prefix ? kv * p.work.pairs + r / (2 * kPrefixRows) : 0;
+  const int in_pair = r % (2 * kPrefixRows);
+  const bool two = prefix && p.work.weight(item) == 2;
   griddep_wait();
   griddep_launch_dependents();
   const int4 cut = __ldcg(p.cuts + seq);
   const int c = min(__ldg(p.context_lens + seq), p.max_tokens);
-  wk.ctas = prefix ? __ldcg(p.ctas) : 1;
+  const int2 ctas = prefix ? __ldcg(p.item_ctas + item) : make_int2(0, -1);
   // Prefix partials: every CTA between the first and the last tile's has one (a
   // range holds two units or more), with a single row tile one per group.
-  int np = 0, c0 = 0;
-  if (prefix && c >= p.prefix_tokens + p.num_queries - 1) {
-    c0 = wk.cta_of(item, 0);
-    np = (wk.cta_of(item, wk.tiles - 1) - c0 + 1) * (two ? 1 : 2);
-  }
+  const int c0 = ctas.x;
+  const int np =
+      prefix && c >= p.prefix_tokens + p.num_queries - 1 ? (ctas.y - ctas.x + 1) * (two ? 1 : 2) : 0;
   // Partials of the rest: none, the walk's finished row, or one per range.
   const bool whole = cut.w == kCutWhole;
   const int nr = cut.w == kCutEmpty ? 0 : whole ? 1 : cut.y - cut.x + 1;
   const float* ml_r = whole ? p.rest_ml : p.walk_ml;
   const float* o_r = whole ? p.rest_o : p.walk_o;
-  const int seq_rows = p.num_queries * p.num_heads, in_seq = static_cast<int>(row - (long long)seq * seq_rows);
+  const int seq_rows = p.num_queries * p.num_heads, in_seq = row - seq * seq_rows;
   auto rest_at = [&](int k) -> size_t {
     return whole ? (size_t)row : ((size_t)(cut.x + k) * 2 + (k == 0 ? cut.z : 0)) * seq_rows + in_seq;
   };
@@ -641,7 +637,7 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
   }
   if (lane < kLanes) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(p.out + row * D + 4 * lane) =
+    *reinterpret_cast<uint2*>(p.out + (size_t)row * D + 4 * lane) =
         make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   }
 }
@@ -653,11 +649,11 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
 // Scratch: the rest's (m, l) and O rows, the prefix's partials, then what the
 // rest's walk needs.
 struct PrefixScratch {
-  size_t ctas, rest_ml, rest_o, part_ml, part_o, walk, total;
+  size_t item_ctas, rest_ml, rest_o, part_ml, part_o, walk, total;
 };
 
 PrefixScratch prefix_scratch(int num_seqs, int num_queries, int num_heads, int head_size, int slots,
-                             size_t walk_bytes) {
+                             int items, size_t walk_bytes) {
   const size_t rows = (size_t)num_seqs * num_queries * num_heads;
   const size_t part_rows = (size_t)slots * 2 * kPrefixRows;
   PrefixScratch s;
@@ -667,7 +663,7 @@ PrefixScratch prefix_scratch(int num_seqs, int num_queries, int num_heads, int h
     o += align_up(bytes, 256);
     return at;
   };
-  s.ctas = take(4);
+  s.item_ctas = take(sizeof(int2) * (size_t)items);
   s.rest_ml = take(rows * 8);
   s.rest_o = take(rows * head_size * 4);
   s.part_ml = take(part_rows * 8);
@@ -677,11 +673,11 @@ PrefixScratch prefix_scratch(int num_seqs, int num_queries, int num_heads, int h
   return s;
 }
 
-// The slots of the longest list a batch can have: one CTA per SM.
-int most_slots(int num_seqs, int num_queries, int num_heads, int num_kv_heads, int sm_count) {
+// Items of the list; its slots are at most these and one per SM.
+int count_items(int num_seqs, int num_queries, int num_heads, int num_kv_heads) {
   const int64_t rows = (int64_t)num_seqs * num_queries * (num_heads / num_kv_heads);
   const int64_t pairs = (rows + 2 * kPrefixRows - 1) / (2 * kPrefixRows);
-  return (int)(sm_count + pairs * num_kv_heads);
+  return (int)(pairs * num_kv_heads);
 }
 
 // The pools' tensor maps.  A map is a pure function of the fields of its key, so
@@ -753,9 +749,8 @@ extern "C" size_t pa_decode_prefix_workspace_size(int num_seqs, int num_queries,
   const size_t walk = walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 2);
   DeviceInfo dev{};
   if (walk == 0 || current_device_info(&dev) != PA_OK) return 0;
-  return prefix_scratch(num_seqs, num_queries, num_heads, head_size,
-                        most_slots(num_seqs, num_queries, num_heads, num_kv_heads, dev.sm_count), walk)
-      .total;
+  const int items = count_items(num_seqs, num_queries, num_heads, num_kv_heads);
+  return prefix_scratch(num_seqs, num_queries, num_heads, head_size, dev.sm_count + items, items, walk).total;
 }
 
 extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,
@@ -785,9 +780,12 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   if (rc != PA_OK) return rc;
   const size_t walk_bytes =
       walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 2);
-  const PrefixScratch sc = prefix_scratch(num_seqs, num_queries, num_heads, head_size,
-                                          most_slots(num_seqs, num_queries, num_heads, num_kv_heads, dev.sm_count),
-                                          walk_bytes);
+  const int64_t rows = (int64_t)num_seqs * num_queries * (num_heads / num_kv_heads);
+  if (rows * num_kv_heads > 1 << 30)
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %lld output rows", (long long)(rows * num_kv_heads));
+  const int items = count_items(num_seqs, num_queries, num_heads, num_kv_heads);
+  const PrefixScratch sc =
+      prefix_scratch(num_seqs, num_queries, num_heads, head_size, dev.sm_count + items, items, walk_bytes);
   const bool own = workspace == nullptr;
   if (own) {
     rc = kept_scratch(sc.total, stream, &workspace);
@@ -803,9 +801,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int prefix_tokens = num_prefix_blocks * block_size;
   const int group = num_heads / num_kv_heads;
-  const int64_t rows = (int64_t)num_seqs * num_queries * group;
   PrefixParams prm{};
-  if (rows > 1 << 30) return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %lld query rows", (long long)rows);
   if (num_prefix_blocks > 0) {
     const uint64_t pool_rows = num_physical_blocks > 0 ? (uint64_t)num_physical_blocks * block_size : 1ull << 31;
     if (pool_rows > 1ull << 31)
@@ -822,7 +818,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
     prm.part_o = reinterpret_cast<float*>(ws + sc.part_o);
     prm.work = make_prefix_work(rows, num_kv_heads, prefix_tokens, dev.sm_count);
     const WalkShape shape = walk_shape(num_heads, num_kv_heads, head_size, num_queries, 2);
-    prm.ctas_out = reinterpret_cast<int32_t*>(ws + sc.ctas);
+    prm.item_ctas = reinterpret_cast<int2*>(ws + sc.item_ctas);
     prm.context_lens = context_lens;
     prm.num_seqs = num_seqs;
     prm.num_queries = num_queries;
@@ -864,9 +860,9 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   jp.cuts = ex.cuts;
   jp.walk_ml = ex.part_ml;
   jp.walk_o = ex.part_o;
-  jp.ctas = prm.ctas_out;
+  jp.item_ctas = prm.item_ctas;
   jp.work = prm.work;
-  jp.rows = (long long)num_seqs * num_queries * num_heads;
+  jp.rows = num_seqs * num_queries * num_heads;
   jp.num_queries = num_queries;
   jp.num_heads = num_heads;
   jp.group = group;

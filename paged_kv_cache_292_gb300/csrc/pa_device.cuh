@@ -124,15 +124,10 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
-// L2 policies for the copies: lines that are read again stay, lines that are read
-// once go first.
-template <bool KEEP>
-__device__ __forceinline__ uint64_t l2_policy() {
+// L2 policy for copies of lines that are read once: they go first.
+__device__ __forceinline__ uint64_t l2_evict_first() {
   uint64_t p;
-  if constexpr (KEEP)
-    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-  else
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 
