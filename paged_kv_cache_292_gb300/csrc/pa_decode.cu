@@ -22,6 +22,30 @@ namespace pa {
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+// Of the shapes whose staged rows fit, the one with the most consumer warps per SM;
+// among equals the most KV heads per CTA (the longest copies).  An SM holds 12
+// warps at 168 registers a thread, 16 at the 128 that 64-dim walks keep to.  One
+// producer warp for few consumers: every warp of the other kind hides latency.
+WalkShape walk_shape(int num_heads, int num_kv_heads, int head_size, int num_queries, int elt) {
+  const int columns = (num_heads / num_kv_heads) * num_queries;
+  const int split = elt == 4 || columns <= 8 ? 1 : (columns + 15) / 16;
+  const int warps = head_size == 64 && elt != 4 ? 16 : 12;
+  WalkShape best{num_kv_heads, split, 1, 1, head_size * elt};
+  int most = 0;
+  for (int hg = 1; hg * split <= kMaxGroupHeads; ++hg) {
+    const int row = hg * head_size * elt, consumers = hg * split;
+    if (num_kv_heads % hg != 0 || row > kMaxRowBytes || (elt != 4 && row % kLine != 0)) continue;
+    const int producers = consumers >= 6 ? kProducers : 1;
+    int per_sm = warps / (consumers + producers);
+    if (per_sm < 1) per_sm = 1;
+    if (consumers * per_sm >= most) {
+      most = consumers * per_sm;
+      best = WalkShape{num_kv_heads / hg, split, producers, per_sm, row};
+    }
+  }
+  return best;
+}
+
 EncodeTiledFn encode_tiled_fn() {
   static const EncodeTiledFn fn = [] {
     void* f = nullptr;
@@ -72,10 +96,6 @@ int heads_per_cta(int num_kv_heads, int head_size, int elt, int max_heads = kMax
 // per warp, so ceil(columns / 8) (at most 4: 32 columns).
 int column_split(int group, int num_queries) { return (group * num_queries + 7) / 8; }
 
-// CTAs of this many warps that fit on an SM's registers at 168 a thread (three
-// warps per quarter).
-int ctas_per_sm(int warps) { return warps <= 12 ? 12 / warps : 1; }
-
 int default_ranges(const DeviceInfo& dev, int HG) {
   const int r = dev.sm_count / HG;
   return r < 1 ? 1 : r;
@@ -92,18 +112,26 @@ int gcd_int(int a, int b) {
 
 // elt: bytes of a pool element; q_elt: bytes of a query element (bf16 queries
 // select the tensor-core consumers, whose stages are swizzled tensor boxes).
-// spread: CTAs of few warps (few KV heads, or few per group) get as many ranges
-// per SM as fit there: their consumers wait on latency, not on HBM.
+// walk: the CTA shape of the walks other than kWalkAll (walk_shape), several
+// ranges per SM where they fit.
 int make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int elt,
               int num_ranges, const DeviceInfo& dev, Plan* pl, int num_queries = 1,
-              int q_elt = 0, int block_size = 16, bool spread = false) {
+              int q_elt = 0, int block_size = 16, bool walk = false) {
   if (q_elt == 0) q_elt = elt;
   const int G = num_heads / num_kv_heads;
   const bool mma = q_elt == 2;
   pl->split = column_split(G, num_queries);
   pl->Hg = heads_per_cta(num_kv_heads, head_size, elt, kMaxGroupHeads / pl->split);
+  pl->producers = kProducers;
+  int per_sm = 1;
+  if (walk) {
+    const WalkShape w = walk_shape(num_heads, num_kv_heads, head_size, num_queries, elt);
+    pl->split = w.split;
+    pl->Hg = num_kv_heads / w.groups;
+    pl->producers = w.producers;
+    per_sm = w.per_sm;
+  }
   pl->HG = num_kv_heads / pl->Hg;
-  int per_sm = spread ? ctas_per_sm(pl->Hg * pl->split + kProducers) : 1;
   pl->row_bytes = (uint32_t)(pl->Hg * head_size * elt);
   pl->q_bytes = (uint32_t)(num_queries * pl->Hg * G * head_size * q_elt);
   pl->lines = pl->box_rows = pl->box_bytes = 0;
@@ -152,7 +180,7 @@ int make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int 
   // Consumers that take two tiles per pass (FP8 pools; bf16 with a KV head's
   // columns split over several warps) hold two stages at once: they need four
   // or more.  Their rows are at most 1 KiB, so every shape they accept has.
-  const bool pairs = mma && (elt == 1 || pl->split >= 2);
+  const bool pairs = mma && (elt == 1 || G * num_queries > 8);
   if (pairs && pl->stages < 4)
     return fail(PA_ERR_UNSUPPORTED, "decode: %d stages of %u bytes, four needed", pl->stages, pl->stage_bytes);
   workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, pl->R, pl, num_queries);
@@ -507,17 +535,11 @@ size_t walk_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int he
     DeviceInfo dev{};
     if (current_device_info(&dev) != PA_OK) return 0;
     const WalkShape w = walk_shape(num_heads, num_kv_heads, head_size, num_queries, elt);
-    R = default_ranges(dev, w.groups) * ctas_per_sm(w.warps);
+    R = default_ranges(dev, w.groups) * w.per_sm;
   }
   Plan pl{};
   workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, R, &pl, num_queries);
   return pl.ws_partials + sizeof(int4) * (size_t)num_seqs;
-}
-
-WalkShape walk_shape(int num_heads, int num_kv_heads, int head_size, int num_queries, int elt) {
-  const int split = column_split(num_heads / num_kv_heads, num_queries);
-  const int hg = split > kMaxGroupHeads ? 1 : heads_per_cta(num_kv_heads, head_size, elt, kMaxGroupHeads / split);
-  return WalkShape{num_kv_heads / hg, hg * split + kProducers, hg * head_size * elt};
 }
 
 size_t decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,

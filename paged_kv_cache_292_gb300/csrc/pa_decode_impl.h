@@ -27,9 +27,10 @@ struct DecodeExtras {
   const float* part_o = nullptr;
 };
 
-// Shape of a walk's CTAs: KV-head groups, warps, bytes of a staged K row.
+// Shape of a walk's CTAs: KV-head groups, consumer warps per KV head, producer
+// warps, CTAs per SM, bytes of a staged K row.
 struct WalkShape {
-  int groups, warps, row_bytes;
+  int groups, split, producers, per_sm, row_bytes;
 };
 WalkShape walk_shape(int num_heads, int num_kv_heads, int head_size, int num_queries, int elt);
 

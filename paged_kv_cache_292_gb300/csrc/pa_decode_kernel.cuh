@@ -379,6 +379,61 @@ __device__ __forceinline__ void mod_scores(const DecodeParams& p, const ModCols&
   }
 }
 
+// The same for the row form (RowsConsumer): a lane holds columns t2, t2 + 1, t2 + 8,
+// t2 + 9 (tokens) of rows a (s[0..3]) and b (s[4..7]).  Without MOD: plain scores
+// under the causal mask.
+template <bool MOD>
+__device__ __forceinline__ void row_scores(const DecodeParams& p, const ModCols& mc, const ModTile& t, int t2,
+                                           float (&s)[8]) {
+  const int base = t.ctx - p.num_queries, col = t.tok0 + t2;
+  const int pa = base + mc.qa, pb = base + mc.qb;
+  if constexpr (MOD) {
+    if (p.cap_out != 0.f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = mod_cap(p, s[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] *= p.scale_log2;
+    }
+    if (p.slopes != nullptr) {
+      const float da = static_cast<float>(pa - col), db = static_cast<float>(pb - col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float d = static_cast<float>((i & 1) + 8 * (i >> 1));
+        s[i] -= mc.sa * fabsf(da - d);
+        s[4 + i] -= mc.sb * fabsf(db - d);
+      }
+    }
+    // Do all queries see all tokens?  (The same answer for the whole warp.)
+    if (base < 0 || (t.tok0 + kTile > t.pre && (t.tok0 + kTile - 1 > base || t.tok0 <= t.ctx - 1 - p.window))) {
+      const int la = pa - p.window, lb = pb - p.window;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = col + (i & 1) + 8 * (i >> 1);
+        const bool pre = c < t.pre;
+        if (pa < 0 || !(pre || (c <= pa && c > la))) s[i] = -INFINITY;
+        if (pb < 0 || !(pre || (c <= pb && c > lb))) s[4 + i] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] *= p.scale_log2;
+    if (t.tok0 + kTile > base) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = col + (i & 1) + 8 * (i >> 1);
+        if (c > pa) s[i] = -INFINITY;
+        if (c > pb) s[4 + i] = -INFINITY;
+      }
+    }
+  }
+  if (t.vis != 0xffffu) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!((t.vis >> (t2 + (i & 1) + 8 * (i >> 1))) & 1u)) s[i] = s[4 + i] = -INFINITY;
+  }
+}
+
 // Halves of a V fragment register (tokens t2, t2 + 1) to keep.
 __device__ __forceinline__ uint32_t keep_pair(uint32_t vis, int t2) {
   return ((vis >> t2) & 1u ? 0x0000ffffu : 0u) | ((vis >> (t2 + 1)) & 1u ? 0xffff0000u : 0u);
@@ -739,8 +794,7 @@ struct MmaConsumerMQ {
   // columns are split over several warps, where it measured faster).
   __device__ __forceinline__ void tile_hoisted(uint32_t k_half, uint32_t v_half, uint32_t lines, int uh,
                                                int nvalid, int tok0, int ctx, int G, int Q,
-                                               float scale_log2, int lane, const DecodeParams* mod = nullptr,
-                                               const ModTile& mo = ModTile()) {
+                                       float scale_log2, int lane) {
     // All K fragments are loaded first, then the scores accumulate in four
     // independent chains (k-step mod 4) added at the end: with one 8-column
     // tile per warp a single chain would serialise all KS MMAs.  The V
@@ -780,28 +834,21 @@ struct MmaConsumerMQ {
     float alpha_a[NT], alpha_b[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float s0 = c[nt][0], s1 = c[nt][1], s2 = c[nt][2], s3 = c[nt][3];
-      if constexpr (MOD) {
-        mod_scores(*mod, mc, mo, r0, s0, s1, s2, s3);
-      } else {
-        s0 *= scale_log2;
-        s1 *= scale_log2;
-        s2 *= scale_log2;
-        s3 *= scale_log2;
-        if (r0 >= nvalid) s0 = s1 = -INFINITY;
-        if (r0 + 8 >= nvalid) s2 = s3 = -INFINITY;
-        // Causal limits matter only on tiles that reach the queries' own
-        // positions (ctx - Q ..); the test is the same for the whole warp.
-        if (tok0 + kTile > ctx - Q) {
-          const int na = col0 + nt * 8 + 2 * (lane & 3), nb = na + 1;
-          // Last visible position of each column's query (-1: padding column).
-          const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
-          const int lim_b = nb < G * Q ? ctx - Q + nb / G : -1;
-          if (t0 > lim_a) s0 = -INFINITY;
-          if (t0 > lim_b) s1 = -INFINITY;
-          if (t1 > lim_a) s2 = -INFINITY;
-          if (t1 > lim_b) s3 = -INFINITY;
-        }
+      float s0 = c[nt][0] * scale_log2, s1 = c[nt][1] * scale_log2;
+      float s2 = c[nt][2] * scale_log2, s3 = c[nt][3] * scale_log2;
+      if (r0 >= nvalid) s0 = s1 = -INFINITY;
+      if (r0 + 8 >= nvalid) s2 = s3 = -INFINITY;
+      // Causal limits matter only on tiles that reach the queries' own
+      // positions (ctx - Q ..); the test is the same for the whole warp.
+      if (tok0 + kTile > ctx - Q) {
+        const int na = col0 + nt * 8 + 2 * (lane & 3), nb = na + 1;
+        // Last visible position of each column's query (-1: padding column).
+        const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
+        const int lim_b = nb < G * Q ? ctx - Q + nb / G : -1;
+        if (t0 > lim_a) s0 = -INFINITY;
+        if (t0 > lim_b) s1 = -INFINITY;
+        if (t1 > lim_a) s2 = -INFINITY;
+        if (t1 > lim_b) s3 = -INFINITY;
       }
       float mx_a = fmaxf(s0, s2), mx_b = fmaxf(s1, s3);
 #pragma unroll
@@ -832,12 +879,7 @@ struct MmaConsumerMQ {
     }
     const int t2 = 2 * (lane & 3);
     uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
-    if constexpr (MOD) {
-      if (mo.vis != 0xffffu) {
-        keep_lo = keep_pair(mo.vis, t2);
-        keep_hi = keep_pair(mo.vis, t2 + 8);
-      }
-    } else if (nvalid < kTile) {
+    if (nvalid < kTile) {
       keep_lo = (t2 < nvalid ? 0x0000ffffu : 0u) | (t2 + 1 < nvalid ? 0xffff0000u : 0u);
       keep_hi = (t2 + 8 < nvalid ? 0x0000ffffu : 0u) | (t2 + 9 < nvalid ? 0xffff0000u : 0u);
     }
@@ -876,8 +918,7 @@ struct MmaConsumerMQ {
   // score chains interleave and one softmax update covers all 32 tokens.
   __device__ __forceinline__ void tile2(uint32_t k_half0, uint32_t v_half0, uint32_t k_half1, uint32_t v_half1,
                                         uint32_t lines, int uh, int nvalid1, int tok0, int ctx, int G, int Q,
-                                        float scale_log2, int lane, const DecodeParams* mod = nullptr,
-                                        const ModTile& mo0 = ModTile(), const ModTile& mo1 = ModTile()) {
+                                        float scale_log2, int lane) {
     const RowPtr<NC> kp0(k_half0, (lane & 7) + ((lane >> 3) & 1) * 8, uh + (lane >> 4), lines);
     const RowPtr<NC> kp1(k_half1, (lane & 7) + ((lane >> 3) & 1) * 8, uh + (lane >> 4), lines);
     float cc[2][2][NT][4];
@@ -908,19 +949,13 @@ struct MmaConsumerMQ {
       float sv[2][4];
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt) {
-        if constexpr (MOD) {
+        const int nv = tt ? nvalid1 : kTile;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sv[tt][i] = cc[tt][0][nt][i] + cc[tt][1][nt][i];
-          mod_scores(*mod, mc, tt ? mo1 : mo0, r0, sv[tt][0], sv[tt][1], sv[tt][2], sv[tt][3]);
-        } else {
-          const int nv = tt ? nvalid1 : kTile;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sv[tt][i] = (cc[tt][0][nt][i] + cc[tt][1][nt][i]) * scale_log2;
-          if (r0 >= nv) sv[tt][0] = sv[tt][1] = -INFINITY;
-          if (r0 + 8 >= nv) sv[tt][2] = sv[tt][3] = -INFINITY;
-        }
+        for (int i = 0; i < 4; ++i) sv[tt][i] = (cc[tt][0][nt][i] + cc[tt][1][nt][i]) * scale_log2;
+        if (r0 >= nv) sv[tt][0] = sv[tt][1] = -INFINITY;
+        if (r0 + 8 >= nv) sv[tt][2] = sv[tt][3] = -INFINITY;
       }
-      if (!MOD && tok0 + 2 * kTile > ctx - Q) {  // the pair reaches the queries' own positions
+      if (tok0 + 2 * kTile > ctx - Q) {  // the pair reaches the queries' own positions
         const int na = col0 + nt * 8 + 2 * (lane & 3), nb = na + 1;
         const int lim_a = na < G * Q ? ctx - Q + na / G : -1;
         const int lim_b = nb < G * Q ? ctx - Q + nb / G : -1;
@@ -967,15 +1002,7 @@ struct MmaConsumerMQ {
     }
     const int t2 = 2 * (lane & 3);
     uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
-    uint32_t keep_lo0 = 0xffffffffu, keep_hi0 = 0xffffffffu;  // MOD: the first tile's
-    if constexpr (MOD) {
-      if ((mo0.vis & mo1.vis) != 0xffffu) {
-        keep_lo0 = keep_pair(mo0.vis, t2);
-        keep_hi0 = keep_pair(mo0.vis, t2 + 8);
-        keep_lo = keep_pair(mo1.vis, t2);
-        keep_hi = keep_pair(mo1.vis, t2 + 8);
-      }
-    } else if (nvalid1 < kTile) {
+    if (nvalid1 < kTile) {
       keep_lo = (t2 < nvalid1 ? 0x0000ffffu : 0u) | (t2 + 1 < nvalid1 ? 0xffff0000u : 0u);
       keep_hi = (t2 + 8 < nvalid1 ? 0x0000ffffu : 0u) | (t2 + 9 < nvalid1 ? 0xffff0000u : 0u);
     }
@@ -1000,12 +1027,6 @@ struct MmaConsumerMQ {
       uint32_t v0[4], v1[4];
       ldmatrix_x4_trans(v0, vp0.at(mt));
       ldmatrix_x4_trans(v1, vp1.at(mt));
-      if constexpr (MOD) {
-        v0[0] &= keep_lo0;
-        v0[1] &= keep_lo0;
-        v0[2] &= keep_hi0;
-        v0[3] &= keep_hi0;
-      }
       v1[0] &= keep_lo;
       v1[1] &= keep_lo;
       v1[2] &= keep_hi;
@@ -1486,6 +1507,245 @@ struct MmaConsumerF8 {
   }
 };
 
+// Consumer for more than 8 (query, head) columns per KV head in the walks other
+// than kWalkAll: 16 of them per warp, as the rows of the products.  S[16 x tokens] =
+// Q K^T with Q as the A operand, and the weights are A again for O[16 x D] += P V
+// straight from the score registers.  Against 8 columns per warp (S^T = K Q^T) it
+// reads, and for FP8 pools widens, every K and V fragment once for 16 rows, needs
+// two shuffles per reduction instead of three and no transpose of P.
+//   bf16: P as a high and a low bf16 part (about 2^-16).  FP8 pools: codes widened
+//   to f16, head dims inside a 16-wide k-step in the order 4t .. 4t + 3 per lane
+//   (see MmaConsumerF8), P rounded to f16.
+// Lane l holds rows l / 4 and l / 4 + 8 and, of a tile's scores, tokens 2 (l % 4),
+// + 1, + 8, + 9.
+template <int D, bool KV8, bool MOD>
+struct RowsConsumer {
+  static constexpr int KS = D / 16;
+  static constexpr int NC = D * 2 > 128 ? D * 2 / 128 : 1;
+  uint32_t qf[KS][4];
+  float acc[D / 8][4];  // KV8: tiles 2j and 2j + 1 are the even and odd dims of slice j
+  float m[2], l[2];
+  int row0 = 0;
+  uint32_t lane_off = 0;  // KV8: this lane's ldmatrix row address within a half-stage
+  ModCols mc;             // rows l / 4 and l / 4 + 8
+
+  __device__ __forceinline__ void setup(const DecodeParams& p, int kv_head, int first_row, int w, int lane) {
+    row0 = first_row;
+    const int G = p.group, n = G * p.num_queries, a = row0 + (lane >> 2), b = a + 8;
+    mc.qa = a < n ? a / G : 0;
+    mc.qb = b < n ? b / G : 0;
+    if (MOD && p.slopes != nullptr) {
+      if (a < n) mc.sa = 1.4426950408889634f * __ldg(p.slopes + kv_head * G + a % G);
+      if (b < n) mc.sb = 1.4426950408889634f * __ldg(p.slopes + kv_head * G + b % G);
+    }
+    if constexpr (KV8)
+      lane_off = RowPtr<1>(0u, (lane & 7) + ((lane >> 3) & 1) * 8, w * D / 16 + (lane >> 4), p.lines).a[0];
+  }
+
+  __device__ __forceinline__ void begin_segment(const DecodeParams& p, const unsigned char* qslot, int w, int lane) {
+    const int G = p.group, n = G * p.num_queries, Hg = p.heads_per_cta, t = lane & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = row0 + (lane >> 2) + 8 * half;
+      const bool real = r < n;
+      const int qi = real ? r / G : 0, g = real ? r % G : 0;
+      const __nv_bfloat16* q =
+          reinterpret_cast<const __nv_bfloat16*>(qslot) + ((size_t)qi * Hg * G + w * G + g) * D;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if constexpr (KV8) {
+          const uint2 v = real ? *reinterpret_cast<const uint2*>(q + ks * 16 + 4 * t) : make_uint2(0u, 0u);
+          qf[ks][half] = pack_f16x2(bf16_lo(v.x), bf16_hi(v.x));
+          qf[ks][2 + half] = pack_f16x2(bf16_lo(v.y), bf16_hi(v.y));
+        } else {
+          qf[ks][half] = real ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 2 * t) : 0u;
+          qf[ks][2 + half] = real ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + 2 * t) : 0u;
+        }
+      }
+      m[half] = -INFINITY;
+      l[half] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  }
+
+  // N tiles (1 or 2) of one segment in one pass.
+  template <int N>
+  __device__ __forceinline__ void tiles(const DecodeParams& p, const uint32_t (&kh)[N], const uint32_t (&vh)[N], int uh,
+                                        const ModTile (&mo)[N], int lane) {
+    const int t2 = 2 * (lane & 3);
+    float s[N][8];
+#pragma unroll
+    for (int tt = 0; tt < N; ++tt) {
+      float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // tokens 0-7, 8-15
+      if constexpr (KV8) {
+        const uint32_t ka = kh[tt] + lane_off;
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) {
+          uint32_t kr[4];
+          ldmatrix_x4(kr, ka ^ ((uint32_t)(j & 3) << 5));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // k-step 2j + i / 2, tokens 8 (i % 2) ..
+            uint32_t b0, b1;
+            e4m3x4_to_f16x2x2(kr[i], b0, b1);
+            mma_f16_16816(c[i & 1], qf[2 * j + (i >> 1)], b0, b1);
+          }
+        }
+      } else {
+        const RowPtr<NC> kp(kh[tt], (lane & 7) + ((lane >> 4) & 1) * 8, uh + ((lane >> 3) & 1), p.lines);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t b[4];
+          ldmatrix_x4(b, kp.at(ks));
+          mma_bf16_16816(c[0], qf[ks], b[0], b[1]);
+          mma_bf16_16816(c[1], qf[ks], b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s[tt][2 * i] = c[i][0], s[tt][2 * i + 1] = c[i][1];
+        s[tt][4 + 2 * i] = c[i][2], s[tt][5 + 2 * i] = c[i][3];
+      }
+      row_scores<MOD>(p, mc, mo[tt], t2, s[tt]);
+    }
+    float alpha[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float mx = s[0][4 * half];
+#pragma unroll
+      for (int tt = 0; tt < N; ++tt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[tt][4 * half + i]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[half], mx);
+      // A row may see no token of these tiles (or none yet): keep -inf out of the exponent base.
+      const float base = mn == -INFINITY ? 0.f : mn;
+      alpha[half] = ex2_ftz(m[half] - base);
+      m[half] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int tt = 0; tt < N; ++tt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[tt][4 * half + i] = ex2_ftz(s[tt][4 * half + i] - base);
+          sum += s[tt][4 * half + i];
+        }
+      l[half] = l[half] * alpha[half] + sum;
+    }
+    // Rescale the accumulators only when some running maximum moved.
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        acc[i][0] *= alpha[0];
+        acc[i][1] *= alpha[0];
+        acc[i][2] *= alpha[1];
+        acc[i][3] *= alpha[1];
+      }
+    }
+#pragma unroll
+    for (int tt = 0; tt < N; ++tt) {
+      const float (&w)[8] = s[tt];
+      uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
+      if (mo[tt].vis != 0xffffu) {
+        // V entries of rows nobody sees may be non-finite: zero them.
+        keep_lo = keep_pair(mo[tt].vis, t2);
+        keep_hi = keep_pair(mo[tt].vis, t2 + 8);
+      }
+      if constexpr (KV8) {
+        const uint32_t a[4] = {pack_f16x2(w[0], w[1]), pack_f16x2(w[4], w[5]), pack_f16x2(w[2], w[3]),
+                               pack_f16x2(w[6], w[7])};
+        const uint32_t va = vh[tt] + lane_off;
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) {
+          uint32_t vr[4];
+          ldmatrix_x4_trans(vr, va ^ ((uint32_t)(j & 3) << 5));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {  // slice 2j + i
+            uint32_t e0, o0, e1, o1;     // even and odd dims, tokens 0-7 and 8-15
+            e4m3x4_to_f16x2x2(__byte_perm(vr[2 * i] & keep_lo, 0u, 0x3120), e0, o0);
+            e4m3x4_to_f16x2x2(__byte_perm(vr[2 * i + 1] & keep_hi, 0u, 0x3120), e1, o1);
+            mma_f16_16816(acc[2 * (2 * j + i)], a, e0, e1);
+            mma_f16_16816(acc[2 * (2 * j + i) + 1], a, o0, o1);
+          }
+        }
+      } else {
+        const uint32_t a[4] = {pack_bf16x2(w[0], w[1]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[2], w[3]),
+                               pack_bf16x2(w[6], w[7])};
+        const uint32_t r[4] = {pack_bf16x2(w[0] - bf16_lo(a[0]), w[1] - bf16_hi(a[0])),
+                               pack_bf16x2(w[4] - bf16_lo(a[1]), w[5] - bf16_hi(a[1])),
+                               pack_bf16x2(w[2] - bf16_lo(a[2]), w[3] - bf16_hi(a[2])),
+                               pack_bf16x2(w[6] - bf16_lo(a[3]), w[7] - bf16_hi(a[3]))};
+        const RowPtr<NC> vp(vh[tt], (lane & 7) + ((lane >> 3) & 1) * 8, uh + (lane >> 4), p.lines);
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+          uint32_t b[4];
+          ldmatrix_x4_trans(b, vp.at(mt));
+          b[0] &= keep_lo;
+          b[1] &= keep_hi;
+          b[2] &= keep_lo;
+          b[3] &= keep_hi;
+          mma_bf16_16816(acc[2 * mt], a, b[0], b[1]);
+          mma_bf16_16816(acc[2 * mt + 1], a, b[2], b[3]);
+          mma_bf16_16816(acc[2 * mt], r, b[0], b[1]);
+          mma_bf16_16816(acc[2 * mt + 1], r, b[2], b[3]);
+        }
+      }
+    }
+  }
+
+  // slot < 0: final output (REST: the row's (m, l, O)); else partial slot of range r.
+  template <bool REST = false>
+  __device__ __forceinline__ void finish(const DecodeParams& p, int seq, int kv_head, int slot, int r, int lane) {
+    const int G = p.group, H = p.num_heads, Q = p.num_queries, t = lane & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float sum = l[half];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int n = row0 + (lane >> 2) + 8 * half;
+      if (n >= G * Q) continue;
+      const int row = (n / G) * H + kv_head * G + n % G;
+      const bool whole = slot < 0;
+      if (!REST && whole) {
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + ((size_t)seq * Q * H + row) * D;
+        const float inv = sum > 0.f ? p.v_scale / sum : 0.f;  // a query that sees nothing gives zeros
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const float (&a)[4] = acc[2 * j], (&b)[4] = acc[2 * j + 1];
+          if constexpr (KV8) {
+            *reinterpret_cast<uint2*>(out + 16 * j + 4 * t) =
+                make_uint2(pack_bf16x2(a[2 * half] * inv, b[2 * half] * inv),
+                           pack_bf16x2(a[2 * half + 1] * inv, b[2 * half + 1] * inv));
+          } else {
+            *reinterpret_cast<uint32_t*>(out + 16 * j + 2 * t) = pack_bf16x2(a[2 * half] * inv, a[2 * half + 1] * inv);
+            *reinterpret_cast<uint32_t*>(out + 16 * j + 8 + 2 * t) =
+                pack_bf16x2(b[2 * half] * inv, b[2 * half + 1] * inv);
+          }
+        }
+      } else {
+        const size_t at = (whole ? (size_t)seq : (size_t)r * 2 + slot) * Q * H + row;
+        float* po = (whole ? p.rest_o : p.part_o) + at * D;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const float (&a)[4] = acc[2 * j], (&b)[4] = acc[2 * j + 1];
+          if constexpr (KV8) {
+            *reinterpret_cast<float4*>(po + 16 * j + 4 * t) =
+                make_float4(a[2 * half], b[2 * half], a[2 * half + 1], b[2 * half + 1]);
+          } else {
+            *reinterpret_cast<float2*>(po + 16 * j + 2 * t) = make_float2(a[2 * half], a[2 * half + 1]);
+            *reinterpret_cast<float2*>(po + 16 * j + 8 + 2 * t) = make_float2(b[2 * half], b[2 * half + 1]);
+          }
+        }
+        if (t == 0)
+          *reinterpret_cast<float2*>((whole ? p.rest_ml : p.part_ml) + at * 2) = make_float2(m[half], sum);
+      }
+    }
+  }
+};
+
 // fp32 CUDA-core consumer.  Lane l owns head dims [l*DC, l*DC+DC) of every
 // query head; after the butterfly reduction lane l holds the score of token l/2.
 // MOD: modified scores (one query, at position ctx - 1; a row is seen or not).
@@ -1895,8 +2155,14 @@ __device__ __forceinline__ void append_new_rows_fp8(const DecodeParams& p, const
 // up to 32 columns).
 // WALK: which tiles, and what becomes of the rows (kWalkMod on the tensor-core
 // paths: QMODE 1 or 2, also for one query).
+// A walk of 64 dims keeps to 128 registers (four warps per quarter of an SM
+// instead of three): its consumers wait on latency, and more of them hide it.
+template <typename T, int D, int WALK>
+constexpr int max_threads() {
+  return D == 64 && sizeof(T) == 2 && WALK != kWalkAll ? 512 : 32 * (kMaxGroupHeads + kProducers);
+}
 template <typename T, int D, int GMAX, int QMODE, bool KV8 = false, int WALK = kWalkAll>
-__global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
+__global__ void __launch_bounds__(max_threads<T, D, WALK>(), 1)
     pa_decode_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1907,7 +2173,9 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
   // QMODE 2 splits each KV head's (query, head) columns over p.split warps,
   // 8 columns each (up to 32 columns: four warps).
   const int kSplit = QMODE == 2 ? p.split : 1;
-  const int NCW = Hg * kSplit;  // consumer warps; warps NCW .. NCW + kProducers - 1 produce
+  constexpr bool kRows = QMODE == 2 && WALK != kWalkAll;  // 16 columns per warp, as rows
+  const int NCW = Hg * kSplit;  // consumer warps; warps NCW .. NCW + producers - 1 produce
+  const int producers = WALK == kWalkAll ? kProducers : nwarps - NCW;
   constexpr bool kMmaPath = (sizeof(T) == 2);  // tensor-core consumers, swizzled stages
   const Layout L = make_layout(p.stages, p.q_slots, p.q_bytes, p.stage_bytes, kMmaPath);
   long long* misc = reinterpret_cast<long long*>(smem + L.misc);  // [0,32) scratch, [32..] results
@@ -2101,7 +2369,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
       }
       const int flags = (new_seq ? kSegBegin : 0) | ((x == b - 1 || j == ns - 1) ? kSegEnd : 0) |
                         ((slot + 1) << 2) | (seg_slot0 << 4);
-      const bool mine = kProducers == 1 || static_cast<int>((x - a) % kProducers) == pw;
+      const bool mine = static_cast<int>((x - a) % (WALK == kWalkAll ? kProducers : producers)) == pw;
       if (new_seq && mine) {
         if (!mbar_wait_warp(qempty_bar(qi), qph ^ 1u, p.wait_limit_ns)) {
           timed_out();
@@ -2217,7 +2485,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
   } else {
     // ---------------- consumers ----------------
     const int w = warp / kSplit;  // KV head within the group
-    const int col_base = (warp % kSplit) * 8;
+    const int col_base = (warp % kSplit) * (kRows ? 16 : 8);
     const int kv_head = hg * Hg + w;
     int st = 0, qi = 0;
     uint32_t ph = 0, qph = 0;
@@ -2226,9 +2494,14 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
     using Mma = typename std::conditional<
         KV8, MmaConsumerF8<D, (QMODE > 0), kMod>,
         typename std::conditional<QMODE == 0, MmaConsumer<D>, MmaConsumerMQ<D, 1, kMod>>::type>::type;
-    typename std::conditional<kMma, Mma, SimtConsumer<D, GMAX, kMod>>::type cons;
-    if constexpr (KV8) cons.setup(p.lines, w * D / 16, lane);
-    if constexpr (kMod && kMma) cons.mc.setup(p, kv_head, col_base + 2 * (lane & 3));
+    using Columns = typename std::conditional<kRows, RowsConsumer<D, KV8, kMod>, Mma>::type;
+    typename std::conditional<kMma, Columns, SimtConsumer<D, GMAX, kMod>>::type cons;
+    if constexpr (kRows) {
+      cons.setup(p, kv_head, col_base, w, lane);
+    } else {
+      if constexpr (KV8) cons.setup(p.lines, w * D / 16, lane);
+      if constexpr (kMod && kMma) cons.mc.setup(p, kv_head, col_base + 2 * (lane & 3));
+    }
     // FP8 consumers, and bf16 ones that split a KV head's columns over
     // several warps, take two stages at a time when both hold the same
     // segment (tile pairing: tile2), if the ring has four or more stages.
@@ -2236,6 +2509,10 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
     // bf16 multi-query with one warp per KV head (2 KiB rows, a 3-stage ring
     // for the common shapes) are HBM-bound and keep the ring for copies.
     constexpr bool kPair = kMma && (KV8 || QMODE == 2);
+    // Rows of a tile to attend: the walk's mask, or the first nvalid.
+    auto tile_mask = [](int nvalid) -> uint32_t {
+      return kMod ? (uint32_t)nvalid : nvalid < kTile ? (1u << nvalid) - 1u : 0xffffu;
+    };
     for (long long x = a; x < b; ++x) {
       if (!mbar_wait_warp(full_bar(st), ph, p.wait_limit_ns)) {
         timed_out();
@@ -2247,7 +2524,9 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
           timed_out();
           break;
         }
-        if constexpr (QMODE == 0)
+        if constexpr (kRows)
+          cons.begin_segment(p, smem + L.qring + qi * q_slot_bytes, w, lane);
+        else if constexpr (QMODE == 0)
           cons.begin_segment(smem + L.qring + qi * q_slot_bytes, w, G, lane);
         else if constexpr (KV8)
           cons.begin_segment(smem + L.qring + qi * q_slot_bytes, w, G, lane, p.num_queries, Hg, col_base);
@@ -2300,14 +2579,13 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
                 append_new_rows<D>(p, me, stage_rows + st2 * kTile, kv_head, w, k_half2, v_half2, lane);
             }
           }
-          const ModTile mo0{(uint32_t)mt.nvalid, mt.tok0, mt.ctx, mt.newfirst};
-          const ModTile mo1{(uint32_t)me.nvalid, me.tok0, me.ctx, me.newfirst};
-          if constexpr (kMod && KV8)
+          const ModTile mo0{tile_mask(mt.nvalid), mt.tok0, mt.ctx, mt.newfirst};
+          const ModTile mo1{tile_mask(me.nvalid), me.tok0, me.ctx, me.newfirst};
+          if constexpr (kRows)
+            cons.template tiles<2>(p, {k_half, k_half2}, {v_half, v_half2}, uh, {mo0, mo1}, lane);
+          else if constexpr (kMod && KV8)
             cons.tile2(k_half, v_half, k_half2, v_half2, 0, p.scale_log2, lane, mt.tok0, mt.ctx, G,
                        p.num_queries, &p, mo0, mo1);
-          else if constexpr (kMod)
-            cons.tile2(k_half, v_half, k_half2, v_half2, p.lines, uh, 0, mt.tok0, mt.ctx, G, p.num_queries,
-                       p.scale_log2, lane, &p, mo0, mo1);
           else if constexpr (KV8 && QMODE > 0)
             cons.tile2(k_half, v_half, k_half2, v_half2, me.nvalid, p.scale_log2, lane, mt.tok0, mt.ctx, G,
                        p.num_queries);
@@ -2321,13 +2599,12 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
           ++x;
         }
       }
-      const ModTile mo{(uint32_t)mt.nvalid, mt.tok0, mt.ctx, mt.newfirst};
+      const ModTile mo{tile_mask(mt.nvalid), mt.tok0, mt.ctx, mt.newfirst};
       if (paired) {
+      } else if constexpr (kRows) {
+        cons.template tiles<1>(p, {k_half}, {v_half}, uh, {mo}, lane);
       } else if constexpr (kMod && KV8) {
         cons.tile(k_half, v_half, 0, p.scale_log2, lane, mt.tok0, mt.ctx, G, p.num_queries, &p, mo);
-      } else if constexpr (kMod && kMma && QMODE == 2) {
-        cons.tile_hoisted(k_half, v_half, p.lines, uh, 0, mt.tok0, mt.ctx, G, p.num_queries, p.scale_log2, lane,
-                          &p, mo);
       } else if constexpr (kMod && kMma) {
         cons.tile(k_half, v_half, p.lines, uh, 0, mt.tok0, mt.ctx, G, p.num_queries, p.scale_log2, lane, &p, mo);
       } else if constexpr (kMod) {
@@ -2366,7 +2643,7 @@ __global__ void __launch_bounds__(32 * (kMaxGroupHeads + kProducers), 1)
         // Split-column kernels sit at the register cap: writing the state here
         // (the next segment's begin_segment rewrites it anyway) frees its
         // registers for the merge above.
-        if constexpr (QMODE == 2) cons.clear();
+        if constexpr (QMODE == 2 && !kRows) cons.clear();
       }
       if (++st == NS) {
         st = 0;

@@ -14,7 +14,7 @@
 namespace pa {
 
 struct Plan {
-  int Hg, HG, R, stages, q_slots, split;
+  int Hg, HG, R, stages, q_slots, split, producers;
   uint32_t row_bytes, pitch, q_bytes, stage_bytes, smem;
   uint32_t lines, box_rows, box_bytes;  // tensor-core paths (see DecodeParams)
   size_t ws_ml, ws_o, ws_partials, ws_counters, ws_total;
@@ -56,7 +56,7 @@ int launch_typed(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t 
     if (dev >= 0 && dev < kTrackedDevices) configured[dev].store(true, std::memory_order_release);
   }
   cudaError_t e =
-      launch_pdl(kern, dim3(pl.R * pl.HG), dim3(32 * (pl.Hg * pl.split + kProducers)), pl.smem, stream, prm);
+      launch_pdl(kern, dim3(pl.R * pl.HG), dim3(32 * (pl.Hg * pl.split + pl.producers)), pl.smem, stream, prm);
   if (e != cudaSuccess) return cuda_fail(e, "launch pa_decode_kernel");
   return PA_OK;
 }
