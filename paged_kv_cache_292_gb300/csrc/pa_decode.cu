@@ -24,17 +24,23 @@ namespace pa {
 // ---------------------------------------------------------------------------
 // Of the shapes whose staged rows fit, the one with the most consumer warps per SM;
 // among equals the most KV heads per CTA (the longest copies).  An SM holds 12
-// warps at 168 registers a thread, 16 at the 128 that 64-dim walks keep to.  One
+// warps at 168 registers a thread, 16 at 128 (max_threads).  One
 // producer warp for few consumers: every warp of the other kind hides latency.
 WalkShape walk_shape(int num_heads, int num_kv_heads, int head_size, int num_queries, int elt) {
   const int columns = (num_heads / num_kv_heads) * num_queries;
   const int split = elt == 4 || columns <= 8 ? 1 : (columns + 15) / 16;
-  const int warps = head_size == 64 && elt != 4 ? 16 : 12;
+  const int warps = elt != 4 && (head_size == 64 || columns <= 8) ? 16 : 12;
   WalkShape best{num_kv_heads, split, 1, 1, head_size * elt};
   int most = 0;
   for (int hg = 1; hg * split <= kMaxGroupHeads; ++hg) {
     const int row = hg * head_size * elt, consumers = hg * split;
-    if (num_kv_heads % hg != 0 || row > kMaxRowBytes || (elt != 4 && row % kLine != 0)) continue;
+    // Consumers that take two tiles a pass need a ring of four: rows of at most 1 KiB.
+    if (row > (columns > 8 && elt != 4 ? kMaxRowBytes / 2 : kMaxRowBytes)) continue;
+    if (num_kv_heads % hg != 0 || (elt != 4 && row % kLine != 0)) continue;
+    if (row == kMaxRowBytes && columns <= 8) {  // HBM-bound as they are: the longest copies
+      best = WalkShape{num_kv_heads / hg, split, kProducers, 1, row};
+      break;
+    }
     const int producers = consumers >= 6 ? kProducers : 1;
     int per_sm = warps / (consumers + producers);
     if (per_sm < 1) per_sm = 1;
@@ -161,8 +167,9 @@ int make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int 
   const int pref[][2] = {{6, 2}, {5, 2}, {4, 2}, {3, 2}, {3, 1}, {2, 2}, {2, 1}};
   for (; per_sm > 0 && pl->stages == 0; --per_sm) {
     // An SM has 228 KiB, of which each of its CTAs takes 1 KiB besides its own.
-    const int room = per_sm > 1 ? (228 << 10) / per_sm - 1024 : dev.max_smem_optin;
-    const int least = per_sm > 1 ? 4 : 0;  // fewer CTAs rather than a shorter ring
+    int room = per_sm > 1 ? (228 << 10) / per_sm - 1024 : dev.max_smem_optin;
+    if (walk && !mma) room -= kFp32Buffers;
+    const int least = per_sm > 1 ? (mma ? 4 : 3) : 0;  // fewer CTAs rather than a shorter ring
     for (auto& c : pref) {
       const Layout L = make_layout(c[0], c[1], pl->q_bytes, pl->stage_bytes, mma);
       if ((int)L.total <= room && c[0] >= least) {

@@ -77,6 +77,7 @@ constexpr int kRowSkew = 16;       // fp32 stages: bytes between staged rows bey
 constexpr uint32_t kLine = 128;    // tensor-core stages: bytes per swizzled line
 constexpr int kMaxRowBytes = 2048;  // bytes of one staged token row (K or V)
 constexpr int kMaxRanges = 4096;    // bounds the partial-result scratch
+constexpr int kFp32Buffers = 9216;  // static shared memory of the fp32 walk with modified scores
 
 enum : int { kSegBegin = 1, kSegEnd = 2 };
 
@@ -1576,37 +1577,51 @@ struct RowsConsumer {
   __device__ __forceinline__ void tiles(const DecodeParams& p, const uint32_t (&kh)[N], const uint32_t (&vh)[N], int uh,
                                         const ModTile (&mo)[N], int lane) {
     const int t2 = 2 * (lane & 3);
-    float s[N][8];
+    // Scores: the tiles' chains interleave (k-steps outside), two per tile.
+    float s[N][8], c[N][2][4];  // c: tokens 0-7, 8-15
 #pragma unroll
-    for (int tt = 0; tt < N; ++tt) {
-      float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // tokens 0-7, 8-15
-      if constexpr (KV8) {
-        const uint32_t ka = kh[tt] + lane_off;
+    for (int tt = 0; tt < N; ++tt)
 #pragma unroll
-        for (int j = 0; j < KS / 2; ++j) {
-          uint32_t kr[4];
-          ldmatrix_x4(kr, ka ^ ((uint32_t)(j & 3) << 5));
+      for (int i = 0; i < 4; ++i) c[tt][0][i] = c[tt][1][i] = 0.f;
+    if constexpr (KV8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // k-step 2j + i / 2, tokens 8 (i % 2) ..
+      for (int j = 0; j < KS / 2; ++j) {
+        uint32_t kr[N][4];
+#pragma unroll
+        for (int tt = 0; tt < N; ++tt) ldmatrix_x4(kr[tt], (kh[tt] + lane_off) ^ ((uint32_t)(j & 3) << 5));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // k-step 2j + i / 2, tokens 8 (i % 2) ..
+#pragma unroll
+          for (int tt = 0; tt < N; ++tt) {
             uint32_t b0, b1;
-            e4m3x4_to_f16x2x2(kr[i], b0, b1);
-            mma_f16_16816(c[i & 1], qf[2 * j + (i >> 1)], b0, b1);
+            e4m3x4_to_f16x2x2(kr[tt][i], b0, b1);
+            mma_f16_16816(c[tt][i & 1], qf[2 * j + (i >> 1)], b0, b1);
           }
-        }
-      } else {
+      }
+    } else {
+      uint32_t ka[N][NC];
+#pragma unroll
+      for (int tt = 0; tt < N; ++tt) {
         const RowPtr<NC> kp(kh[tt], (lane & 7) + ((lane >> 4) & 1) * 8, uh + ((lane >> 3) & 1), p.lines);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t b[4];
-          ldmatrix_x4(b, kp.at(ks));
-          mma_bf16_16816(c[0], qf[ks], b[0], b[1]);
-          mma_bf16_16816(c[1], qf[ks], b[2], b[3]);
-        }
+        for (int i = 0; i < NC; ++i) ka[tt][i] = kp.a[i];
       }
 #pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int tt = 0; tt < N; ++tt) {
+          uint32_t b[4];
+          ldmatrix_x4(b, ka[tt][ks >> 2] ^ ((uint32_t)(ks & 3) << 5));
+          mma_bf16_16816(c[tt][0], qf[ks], b[0], b[1]);
+          mma_bf16_16816(c[tt][1], qf[ks], b[2], b[3]);
+        }
+    }
+#pragma unroll
+    for (int tt = 0; tt < N; ++tt) {
+#pragma unroll
       for (int i = 0; i < 2; ++i) {
-        s[tt][2 * i] = c[i][0], s[tt][2 * i + 1] = c[i][1];
-        s[tt][4 + 2 * i] = c[i][2], s[tt][5 + 2 * i] = c[i][3];
+        s[tt][2 * i] = c[tt][i][0], s[tt][2 * i + 1] = c[tt][i][1];
+        s[tt][4 + 2 * i] = c[tt][i][2], s[tt][5 + 2 * i] = c[tt][i][3];
       }
       row_scores<MOD>(p, mc, mo[tt], t2, s[tt]);
     }
@@ -1748,8 +1763,7 @@ struct RowsConsumer {
 
 // fp32 CUDA-core consumer.  Lane l owns head dims [l*DC, l*DC+DC) of every
 // query head; after the butterfly reduction lane l holds the score of token l/2.
-// MOD: modified scores (one query, at position ctx - 1; a row is seen or not).
-template <int D, int GMAX, bool MOD = false>
+template <int D, int GMAX>
 struct SimtConsumer {
   static constexpr int DC = D / 32;
   float qv[GMAX][DC];
@@ -1773,8 +1787,7 @@ struct SimtConsumer {
 
   __device__ __forceinline__ void tile(const unsigned char* k_base, const unsigned char* v_base,
                                        uint32_t pitch, int nvalid, float scale_log2, int G,
-                                       int lane, const DecodeParams* mod = nullptr,
-                                       const ModTile& mo = ModTile(), int kv_head = 0) {
+                                       int lane) {
     const int my_tok = lane >> 1;
 #pragma unroll
     for (int h = 0; h < GMAX; ++h) {
@@ -1817,17 +1830,8 @@ struct SimtConsumer {
         sc = mine + __shfl_xor_sync(0xffffffffu, give, 2);
       }
       sc += __shfl_xor_sync(0xffffffffu, sc, 1);
-      if constexpr (MOD) {
-        // fp32 outputs keep the cap's full precision: tanhf, not the SFU form.
-        sc = mod->cap_out != 0.f ? mod->cap_out * tanhf(sc * mod->cap_in) : sc * scale_log2;
-        if (mod->slopes != nullptr)
-          sc -= 1.4426950408889634f * __ldg(mod->slopes + kv_head * G + h) *
-                fabsf(static_cast<float>(mo.ctx - 1 - mo.tok0 - my_tok));
-        if (!((mo.vis >> my_tok) & 1u)) sc = -INFINITY;
-      } else {
-        sc *= scale_log2;
-        if (my_tok >= nvalid) sc = -INFINITY;
-      }
+      sc *= scale_log2;
+      if (my_tok >= nvalid) sc = -INFINITY;
       float mx = sc;
 #pragma unroll
       for (int o = 2; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -1839,8 +1843,7 @@ struct SimtConsumer {
       l[h] = l[h] * alpha + pw;
 #pragma unroll
       for (int i = 0; i < DC; ++i) acc[h][i] *= alpha;
-      for (int t = 0; t < (MOD ? kTile : nvalid); ++t) {
-        if (MOD && !((mo.vis >> t) & 1u)) continue;
+      for (int t = 0; t < nvalid; ++t) {
         const float pt = __shfl_sync(0xffffffffu, pw, 2 * t);
         const float* vr = reinterpret_cast<const float*>(v_base + t * pitch) + lane * DC;
 #pragma unroll
@@ -1874,6 +1877,153 @@ struct SimtConsumer {
           p.part_ml[base * 2 + 1] = lt;
         }
       }
+    }
+  }
+};
+
+// fp32 consumer with modified scores (one query, at position ctx - 1).  Scores:
+// lanes 2t and 2t + 1 take one half of token t's dims each, for all G heads of the
+// group, so a K value is read from shared memory once; the queries are read
+// there too, as broadcasts.  Of a token's finished scores the even lane keeps the
+// even heads and the odd lane the odd ones: cap, bias, maximum, exponential.
+// Output: lane l owns dims [l * D / 32, (l + 1) * D / 32) of all heads, the weights
+// come back through a small buffer.  Products run two to an instruction.
+template <int D, int GMAX>
+struct Fp32ModConsumer {
+  static constexpr int DC = D / 32, DP = DC / 2;  // dims per lane, as pairs
+  static constexpr int GH = (GMAX + 1) / 2;       // heads a lane keeps
+  uint64_t acc[GMAX][DP];
+  float m[GH], l[GH], slope[GH];
+  const unsigned char* q;  // the segment's queries of this KV head: [G][D]
+
+  __device__ __forceinline__ void setup(const DecodeParams& p, int kv_head, int lane) {
+#pragma unroll
+    for (int i = 0; i < GH; ++i) {
+      const int h = 2 * i + (lane & 1);
+      slope[i] = p.slopes != nullptr && h < p.group
+                     ? 1.4426950408889634f * __ldg(p.slopes + kv_head * p.group + h) : 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void begin_segment(const unsigned char* qslot, int w, int G) {
+    q = qslot + (size_t)w * G * D * 4;
+#pragma unroll
+    for (int h = 0; h < GMAX; ++h)
+#pragma unroll
+      for (int i = 0; i < DP; ++i) acc[h][i] = 0ull;
+#pragma unroll
+    for (int i = 0; i < GH; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+  }
+
+  // weights: this warp's [kTile + 1][GMAX] pairs (each weight twice, then the
+  // factors of the accumulators).
+  __device__ __forceinline__ void tile(const DecodeParams& p, const unsigned char* k_base, const unsigned char* v_base,
+                                       const ModTile& mo, float2* weights, int lane) {
+    const int G = p.group, t = lane >> 1, odd = lane & 1;
+    // Scores: dims [odd * D / 2, (odd + 1) * D / 2) of token t.
+    uint64_t s2[GMAX];
+#pragma unroll
+    for (int h = 0; h < GMAX; ++h) s2[h] = 0ull;
+    const unsigned char* kr = k_base + t * p.pitch + odd * (D * 2);
+    const unsigned char* qr = q + odd * (D * 2);
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      const int c = i ^ (4 * odd);  // the two halves in different banks
+      const ulonglong2 kv = *reinterpret_cast<const ulonglong2*>(kr + 16 * c);
+#pragma unroll
+      for (int h = 0; h < GMAX; ++h) {
+        if (h < G) {
+          const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(qr + h * (D * 4) + 16 * c);
+          s2[h] = fma_pair(kv.x, qv.x, s2[h]);
+          s2[h] = fma_pair(kv.y, qv.y, s2[h]);
+        }
+      }
+    }
+    const bool seen = (mo.vis >> t) & 1u;
+    const float dist = fabsf(static_cast<float>(mo.ctx - 1 - mo.tok0 - t));
+#pragma unroll
+    for (int i = 0; i < GH; ++i) {
+      // This lane's half of heads 2i and 2i + 1: give the other lane its head's.
+      float a, b, e = 0.f, f = 0.f;
+      unpair(s2[2 * i], a, b);
+      if (2 * i + 1 < GMAX) unpair(s2[2 * i + 1 < GMAX ? 2 * i + 1 : 0], e, f);
+      const float even = a + b, odds = e + f;
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? even : odds, 1);
+      float sc = (odd ? odds : even) + other;
+      // fp32 outputs keep the cap's full precision: tanhf, not the SFU form.
+      sc = p.cap_out != 0.f ? p.cap_out * tanhf(sc * p.cap_in) : sc * p.scale_log2;
+      sc -= slope[i] * dist;
+      if (!seen) sc = -INFINITY;
+      float mx = sc;
+#pragma unroll
+      for (int o2 = 2; o2 < 32; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
+      const float mn = fmaxf(m[i], mx);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float alpha = ex2_ftz(m[i] - ref), w = ex2_ftz(sc - ref);
+      m[i] = mn;
+      l[i] = l[i] * alpha + w;
+      const int h = 2 * i + odd;
+      if (h < GMAX) {
+        weights[t * GMAX + h] = make_float2(w, w);
+        if (t == 0) weights[kTile * GMAX + h] = make_float2(alpha, alpha);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < GMAX; ++h) {
+      if (h < G) {
+        const uint64_t f = *reinterpret_cast<const uint64_t*>(weights + kTile * GMAX + h);
+#pragma unroll
+        for (int i = 0; i < DP; ++i) acc[h][i] = mul_pair(acc[h][i], f);
+      }
+    }
+#pragma unroll 4
+    for (int tt = 0; tt < kTile; ++tt) {
+      if (!((mo.vis >> tt) & 1u)) continue;  // its V row may be non-finite
+      const unsigned char* vr = v_base + tt * p.pitch + lane * DC * 4;
+      uint64_t v[DP];
+      if constexpr (DP == 2) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(vr);
+        v[0] = x.x, v[1] = x.y;
+      } else {
+        v[0] = *reinterpret_cast<const uint64_t*>(vr);
+      }
+#pragma unroll
+      for (int h = 0; h < GMAX; ++h) {
+        if (h < G) {
+          const uint64_t w = *reinterpret_cast<const uint64_t*>(weights + tt * GMAX + h);
+#pragma unroll
+          for (int i = 0; i < DP; ++i) acc[h][i] = fma_pair(v[i], w, acc[h][i]);
+        }
+      }
+    }
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ void finish(const DecodeParams& p, int seq, int kv_head, int slot, int r, int lane) {
+    const int G = p.group, H = p.num_heads;
+#pragma unroll
+    for (int h = 0; h < GMAX; ++h) {
+      float lt = l[h / 2];
+#pragma unroll
+      for (int o2 = 2; o2 < 32; o2 <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o2);
+      lt = __shfl_sync(0xffffffffu, lt, h & 1);
+      const float mt = __shfl_sync(0xffffffffu, m[h / 2], h & 1);
+      if (h >= G) continue;
+      const int qh = kv_head * G + h;
+      const size_t base = slot < 0 ? (size_t)seq * H + qh : ((size_t)r * 2 + slot) * H + qh;
+      const float f = slot < 0 ? 1.f / lt : 1.f;  // a sequence with tiles has a seen token
+      float* o = (slot < 0 ? reinterpret_cast<float*>(p.out) : p.part_o) + base * D + lane * DC;
+#pragma unroll
+      for (int i = 0; i < DP; ++i) {
+        float a, b;
+        unpair(acc[h][i], a, b);
+        *reinterpret_cast<float2*>(o + 2 * i) = make_float2(a * f, b * f);
+      }
+      if (slot >= 0 && lane == 0) *reinterpret_cast<float2*>(p.part_ml + base * 2) = make_float2(mt, lt);
     }
   }
 };
@@ -2155,14 +2305,16 @@ __device__ __forceinline__ void append_new_rows_fp8(const DecodeParams& p, const
 // up to 32 columns).
 // WALK: which tiles, and what becomes of the rows (kWalkMod on the tensor-core
 // paths: QMODE 1 or 2, also for one query).
-// A walk of 64 dims keeps to 128 registers (four warps per quarter of an SM
-// instead of three): its consumers wait on latency, and more of them hide it.
-template <typename T, int D, int WALK>
+// Walks other than kWalkAll keep to 128 registers where they can (four warps per
+// quarter of an SM instead of three): their consumers wait on latency, and more of
+// them hide it.  Rows of 128 dims need more.
+template <typename T, int D, int QMODE, int WALK>
 constexpr int max_threads() {
-  return D == 64 && sizeof(T) == 2 && WALK != kWalkAll ? 512 : 32 * (kMaxGroupHeads + kProducers);
+  const bool fits = sizeof(T) == 2 && WALK != kWalkAll && (D == 64 || QMODE < 2);
+  return fits ? 512 : 32 * (kMaxGroupHeads + kProducers);
 }
 template <typename T, int D, int GMAX, int QMODE, bool KV8 = false, int WALK = kWalkAll>
-__global__ void __launch_bounds__(max_threads<T, D, WALK>(), 1)
+__global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
     pa_decode_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -2502,7 +2654,16 @@ __global__ void __launch_bounds__(max_threads<T, D, WALK>(), 1)
         KV8, MmaConsumerF8<D, (QMODE > 0), kMod>,
         typename std::conditional<QMODE == 0, MmaConsumer<D>, MmaConsumerMQ<D, 1, kMod>>::type>::type;
     using Columns = typename std::conditional<kRows, RowsConsumer<D, KV8, kMod>, Mma>::type;
-    typename std::conditional<kMma, Columns, SimtConsumer<D, GMAX, kMod>>::type cons;
+    using Simt = typename std::conditional<kMod, Fp32ModConsumer<D, GMAX>, SimtConsumer<D, GMAX>>::type;
+    constexpr bool kFp32Mod = kMod && !kMma;
+    typename std::conditional<kMma, Columns, Simt>::type cons;
+    float2* weights = nullptr;
+    if constexpr (kFp32Mod) {
+      __shared__ float2 weight_buffers[kMaxGroupHeads][(kTile + 1) * GMAX];
+      static_assert(sizeof(weight_buffers) <= kFp32Buffers, "the host plan leaves room for them");
+      weights = weight_buffers[warp];
+      cons.setup(p, kv_head, lane);
+    }
     if constexpr (kRows) {
       cons.setup(p, kv_head, col_base, w, lane);
     } else {
@@ -2531,7 +2692,9 @@ __global__ void __launch_bounds__(max_threads<T, D, WALK>(), 1)
           timed_out();
           break;
         }
-        if constexpr (kRows)
+        if constexpr (kFp32Mod)
+          cons.begin_segment(smem + L.qring + qi * q_slot_bytes, w, G);
+        else if constexpr (kRows)
           cons.begin_segment(p, smem + L.qring + qi * q_slot_bytes, w, lane);
         else if constexpr (QMODE == 0)
           cons.begin_segment(smem + L.qring + qi * q_slot_bytes, w, G, lane);
@@ -2540,11 +2703,13 @@ __global__ void __launch_bounds__(max_threads<T, D, WALK>(), 1)
         else
           cons.begin_segment(smem + L.qring + qi * q_slot_bytes, w, G, p.num_queries, Hg, lane,
                              col_base);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qempty_bar(qi));
-        if (++qi == NQ) {
-          qi = 0;
-          qph ^= 1u;
+        if constexpr (!kFp32Mod) {  // that one reads the queries in place, until the segment ends
+          __syncwarp();
+          if (lane == 0) mbar_arrive(qempty_bar(qi));
+          if (++qi == NQ) {
+            qi = 0;
+            qph ^= 1u;
+          }
         }
       }
       constexpr int kKVBytes = KV8 ? 1 : (int)sizeof(T);
@@ -2616,7 +2781,7 @@ __global__ void __launch_bounds__(max_threads<T, D, WALK>(), 1)
         cons.tile(k_half, v_half, p.lines, uh, 0, mt.tok0, mt.ctx, G, p.num_queries, p.scale_log2, lane, &p, mo);
       } else if constexpr (kMod) {
         const unsigned char* kb = smem + L.stage + st * p.stage_bytes + w * D * sizeof(T);
-        cons.tile(kb, kb + kTile * p.pitch, p.pitch, 0, p.scale_log2, G, lane, &p, mo, kv_head);
+        cons.tile(p, kb, kb + kTile * p.pitch, mo, weights, lane);
       } else if constexpr (KV8 && QMODE > 0) {
         cons.tile(k_half, v_half, mt.nvalid, p.scale_log2, lane, mt.tok0, mt.ctx, G, p.num_queries);
       } else if constexpr (KV8) {
@@ -2639,6 +2804,13 @@ __global__ void __launch_bounds__(max_threads<T, D, WALK>(), 1)
         if (paired) mbar_arrive(empty_bar(st_last));
       }
       if (me.flags & kSegEnd) {
+        if constexpr (kFp32Mod) {
+          if (lane == 0) mbar_arrive(qempty_bar(qi));
+          if (++qi == NQ) {
+            qi = 0;
+            qph ^= 1u;
+          }
+        }
         const int slot = ((me.flags >> 2) & 3) - 1;
         if constexpr (WALK == kWalkRest)
           cons.template finish<true>(p, me.seq, kv_head, slot, r, lane);

@@ -81,9 +81,11 @@ int launch_walk(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t s
                 bool kv_fp8) {
   const bool wide = prm.group * prm.num_queries > 8;  // two to four warps per KV head
   if (f32) {
-    if (head_size == 64)
-      return prm.group <= 2 ? launch_typed<float, 64, 2, 0, false, kWalkMod>(prm, pl, dev, stream)
+    if (head_size == 64) {
+      if (prm.group <= 2) return launch_typed<float, 64, 2, 0, false, kWalkMod>(prm, pl, dev, stream);
+      return prm.group <= 4 ? launch_typed<float, 64, 4, 0, false, kWalkMod>(prm, pl, dev, stream)
                             : launch_typed<float, 64, 8, 0, false, kWalkMod>(prm, pl, dev, stream);
+    }
     if (prm.group <= 2) return launch_typed<float, 128, 2, 0, false, kWalkMod>(prm, pl, dev, stream);
     return prm.group <= 4 ? launch_typed<float, 128, 4, 0, false, kWalkMod>(prm, pl, dev, stream)
                           : launch_typed<float, 128, 8, 0, false, kWalkMod>(prm, pl, dev, stream);

@@ -50,8 +50,9 @@ int launch_typed(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t 
     DeviceInfo info{};
     int rc = current_device_info(&info);
     if (rc != PA_OK) return rc;
+    const int fixed = WALK == kWalkMod && sizeof(T) == 4 ? kFp32Buffers : 0;  // its static shared memory
     cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, info.max_smem_optin);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, info.max_smem_optin - fixed);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode smem)");
     if (dev >= 0 && dev < kTrackedDevices) configured[dev].store(true, std::memory_order_release);
   }

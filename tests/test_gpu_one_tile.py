@@ -46,3 +46,25 @@ def test_decode(heads, kv_heads, head_size, dtype, num_ranges):
                          num_ranges=num_ranges)
     torch.cuda.synchronize()
     assert_close(out, oracle_decode(w), dtype, "one-tile sequences")
+
+
+@pytest.mark.parametrize("heads, kv_heads, head_size", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("num_ranges", [0, 1])
+def test_decode_mod(heads, kv_heads, head_size, dtype, num_ranges):
+    """The same through the walk with modified scores (a cap far above the scores changes nothing)."""
+    w, g = _batch(heads, kv_heads, head_size, dtype)
+    out = binding.decode_mod(g["q"], g["k_cache"], g["v_cache"], g["block_tables"], g["context_lens"], w.scale,
+                             num_ranges=num_ranges, window=4096)
+    torch.cuda.synchronize()
+    assert_close(out, oracle_decode(w), dtype, "one-tile sequences")
+
+
+@pytest.mark.parametrize("heads, kv_heads, head_size", SHAPES)
+def test_decode_prefix_of_nothing(heads, kv_heads, head_size):
+    """The walk behind a shared prefix, here of no tokens."""
+    w, g = _batch(heads, kv_heads, head_size, "bf16")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    out = binding.decode_prefix(g["q"], g["k_cache"], g["v_cache"], none, g["block_tables"], g["context_lens"], w.scale)
+    torch.cuda.synchronize()
+    assert_close(out, oracle_decode(w), "bf16", "one-tile sequences")
