@@ -249,18 +249,18 @@ struct SeqWalk {
 
 // SMs for the prefix kernel of `units` units (pa_prefix_work.h) beside a walk of
 // `tiles` tiles by `groups` CTAs each, in proportion to the SM time of either: a
-// unit takes about 0.7 us (D = 128: 128 x 128 x 128 x 4 flops), a tile about 0.35
-// us + 0.18 us per KiB of K row, or 0.65 us with several warps per KV head, and a
+// unit takes about 0.9 us (D = 128: 128 x 128 x 128 x 4 flops), a tile about 0.35
+// us + 0.18 us per KiB of K row, or 0.8 us with more than 8 columns per KV head, and a
 // sequence another 0.8 us (its queries, its row).  The walk is bound by HBM from about 80 SMs on.
 __device__ __forceinline__ int prefix_share(float units, long long tiles, int seqs, int groups, float tile_us,
                                             int head_size, int sm_count) {
   if (tiles == 0) return sm_count;
-  const float a = units * (head_size == 128 ? 0.7f : 0.5f), b = (tiles * tile_us + seqs * 0.8f) * groups;
+  const float a = units * (head_size == 128 ? 0.9f : 0.6f), b = (tiles * tile_us + seqs * 0.8f) * groups;
   const int n = __float2int_rn(sm_count * (a / (a + b)));
   return max(1, min(n, sm_count - groups));
 }
 __device__ __forceinline__ float walk_tile_us(uint32_t row_bytes, int columns) {
-  return columns > 8 ? 0.65f : 0.35f + 0.18f / 1024.f * row_bytes;
+  return columns > 8 ? 0.8f : 0.35f + 0.18f / 1024.f * row_bytes;
 }
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {

@@ -71,6 +71,12 @@ struct PrefixParams {
   long long stall_tile;  // tests of the bounded waits: item * tiles + tile whose copies are withheld
 };
 
+// Work of the list for prefix_share: its units, and what a segment costs besides
+// (queries in, pipeline up and down, partials out), about five units.
+__host__ __device__ __forceinline__ float prefix_cost(const PrefixWork& w) {
+  return static_cast<float>(w.total()) + 5.f * (w.items() + 0.25f * w.ctas);
+}
+
 template <int D>
 struct PrefixLayout {
   static constexpr int kPanels = D / 64;
@@ -161,7 +167,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
     __syncthreads();
     walk = 0;
     for (int i = 0; i < kPrefixThreads / 32; ++i) walk += sums[i];
-    wk.ctas = min(wk.ctas, prefix_share(static_cast<float>(wk.total()), walk, p.num_seqs, p.walk_groups,
+    wk.ctas = min(wk.ctas, prefix_share(prefix_cost(wk), walk, p.num_seqs, p.walk_groups,
                                         walk_tile_us(p.walk_row_bytes, p.group * p.num_queries), D, p.sm_count));
   }
   const int cta = blockIdx.x;
@@ -538,10 +544,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
 }
 
 // ---------------------------------------------------------------------------
-// Join: a warp per output row adds the row's partials by log-sum-exp: those of
-// the prefix, when its sequence shares it, and those of the rest.  The maxima and
+// Join: kWarps warps per output row add the row's partials by log-sum-exp: those
+// of the prefix, when its sequence shares it, and those of the rest.  The maxima and
 // sums of up to 32 partials of either kind are read at once, one per lane; what
-// bounds it is the chain of dependent loads, so the lists go side by side.
+// bounds it is the chain of dependent loads, so the lists go side by side, and few
+// rows, whose lists are long, get all 8 warps of a CTA.
 // ---------------------------------------------------------------------------
 struct JoinParams {
   __nv_bfloat16* out;
@@ -559,12 +566,12 @@ struct JoinParams {
   int num_queries, num_heads, group, prefix_tokens, max_tokens;
 };
 
-template <int D>
+template <int D, int kWarps>
 __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ JoinParams p) {
-  constexpr int kLanes = D / 4;  // lanes that hold four dims
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
+  constexpr int kLanes = D / 4;  // lanes that hold four dims (the others repeat them)
+  const int lane = threadIdx.x & 31, dims = lane % kLanes, warp = threadIdx.x >> 5, part = warp % kWarps;
+  const int row = blockIdx.x * (8 / kWarps) + warp / kWarps;
+  if (row >= p.rows) return;  // (all warps of a row alike)
   const int token = row / p.num_heads, h = row - token * p.num_heads;
   const int seq = token / p.num_queries, kv = h / p.group;
   const int r = token * p.group + (h - kv * p.group);  // row of the KV head
@@ -593,13 +600,13 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
   };
   auto part_at = [&](int k) -> int { return (c0 + (two ? k : k >> 1) + item) * 2 + (two ? in_pair >> 7 : k & 1); };
   float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 0; k0 < max(nr, np); k0 += 32) {
+  for (int k0 = 32 * part; k0 < max(nr, np); k0 += 32 * kWarps) {
     const int k = k0 + lane;
     float2 a = make_float2(-INFINITY, 0.f), b = a;
     if (k < nr) a = __ldcg(reinterpret_cast<const float2*>(ml_r) + rest_at(k));
     if (k < np) b = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)part_at(k) * kPrefixRows + (in_pair & 127));
-    if (!(a.y > 0.f)) a = make_float2(-INFINITY, a.y == 0.f ? 0.f : a.y);  // no token seen: no weight (NaN stays)
-    if (!(b.y > 0.f)) b = make_float2(-INFINITY, b.y == 0.f ? 0.f : b.y);
+    if (a.y == 0.f) a.x = -INFINITY;  // no token seen: no weight
+    if (b.y == 0.f) b.x = -INFINITY;
     float top = fmaxf(a.x, b.x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -607,32 +614,50 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
     const float keep = ex2_ftz(m - ref);
     const float wa = ex2_ftz(a.x - ref), wb = ex2_ftz(b.x - ref);
     m = mn;
-    float lw = (a.y != 0.f ? wa * a.y : 0.f) + (b.y != 0.f ? wb * b.y : 0.f);
+    float lw = wa * a.y + wb * b.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
     l = l * keep + lw;
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] *= keep;
+    // The loads are made whatever the weight, so that several are in flight; a
+    // partial without weight may hold anything.
+    auto add = [&](float w, const float4& o) {
+      if (w != 0.f) {
+        acc[0] = fmaf(w, o.x, acc[0]), acc[1] = fmaf(w, o.y, acc[1]);
+        acc[2] = fmaf(w, o.z, acc[2]), acc[3] = fmaf(w, o.w, acc[3]);
+      }
+    };
     const int here_r = min(32, nr - k0), here_p = min(32, np - k0);
-#pragma unroll 4
-    for (int i = 0; i < here_r; ++i) {
-      const float w = __shfl_sync(0xffffffffu, wa, i);
-      if (w != 0.f && lane < kLanes) {
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(o_r + rest_at(k0 + i) * D) + lane);
-        acc[0] = fmaf(w, o.x, acc[0]), acc[1] = fmaf(w, o.y, acc[1]);
-        acc[2] = fmaf(w, o.z, acc[2]), acc[3] = fmaf(w, o.w, acc[3]);
-      }
-    }
-#pragma unroll 4
-    for (int i = 0; i < here_p; ++i) {
-      const float w = __shfl_sync(0xffffffffu, wb, i);
-      // A partial without weight may hold anything.
-      if (w != 0.f && lane < kLanes) {
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o) +
-                                ((size_t)part_at(k0 + i) * (D / 4) + lane) * kPrefixRows + (in_pair & 127));
-        acc[0] = fmaf(w, o.x, acc[0]), acc[1] = fmaf(w, o.y, acc[1]);
-        acc[2] = fmaf(w, o.z, acc[2]), acc[3] = fmaf(w, o.w, acc[3]);
-      }
+#pragma unroll 8
+    for (int i = 0; i < here_r; ++i)
+      add(__shfl_sync(0xffffffffu, wa, i), __ldcg(reinterpret_cast<const float4*>(o_r + rest_at(k0 + i) * D) + dims));
+#pragma unroll 8
+    for (int i = 0; i < here_p; ++i)
+      add(__shfl_sync(0xffffffffu, wb, i),
+          __ldcg(reinterpret_cast<const float4*>(p.part_o) +
+                 ((size_t)part_at(k0 + i) * (D / 4) + dims) * kPrefixRows + (in_pair & 127)));
+  }
+  if constexpr (kWarps > 1) {
+    __shared__ float parts[kWarps][6][32];
+    parts[part][4][lane] = m;
+    parts[part][5][lane] = l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) parts[part][i][lane] = acc[i];
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, parts[w][4][lane]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ex2_ftz(parts[w][4][lane] - ref);
+      l = fmaf(f, parts[w][5][lane], l);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, parts[w][i][lane], acc[i]);
     }
   }
   if (lane < kLanes) {
@@ -844,7 +869,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   ex.prefix_tokens = prefix_tokens;
   ex.rest_ml = reinterpret_cast<float*>(ws + sc.rest_ml);
   ex.rest_o = reinterpret_cast<float*>(ws + sc.rest_o);
-  ex.prefix_units = num_prefix_blocks > 0 ? (float)prm.work.total() : 0.f;
+  ex.prefix_units = num_prefix_blocks > 0 ? prefix_cost(prm.work) : 0.f;
   rc = decode_impl_q(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries, num_heads,
                      num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, stream, dtype,
                      num_physical_blocks, ws + sc.walk, walk_bytes, 0, error_flag, false, 1.f, 1.f, nullptr, nullptr,
@@ -868,8 +893,15 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   jp.group = group;
   jp.prefix_tokens = prefix_tokens;
   jp.max_tokens = max_blocks_per_seq * block_size;
-  const dim3 grid((unsigned)((jp.rows + 7) / 8));
-  const cudaError_t e = head_size == 64 ? launch_pdl(pa_prefix_join<64>, grid, dim3(256), 0, st, jp)
-                                        : launch_pdl(pa_prefix_join<128>, grid, dim3(256), 0, st, jp);
+  // Fewer rows than the SMs hold warps for: a CTA each.
+  const bool few = jp.rows <= 4 * dev.sm_count;
+  const dim3 grid((unsigned)(few ? jp.rows : (jp.rows + 7) / 8));
+  cudaError_t e;
+  if (few)
+    e = head_size == 64 ? launch_pdl(pa_prefix_join<64, 8>, grid, dim3(256), 0, st, jp)
+                        : launch_pdl(pa_prefix_join<128, 8>, grid, dim3(256), 0, st, jp);
+  else
+    e = head_size == 64 ? launch_pdl(pa_prefix_join<64, 1>, grid, dim3(256), 0, st, jp)
+                        : launch_pdl(pa_prefix_join<128, 1>, grid, dim3(256), 0, st, jp);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefix_join");
 }
