@@ -256,8 +256,9 @@ __device__ __forceinline__ int prefix_share(float units, long long tiles, int se
                                             int head_size, int sm_count) {
   if (tiles == 0) return sm_count;
   const float a = units * (head_size == 128 ? 0.9f : 0.6f), b = (tiles * tile_us + seqs * 0.8f) * groups;
-  const int n = __float2int_rn(sm_count * (a / (a + b)));
-  return max(1, min(n, sm_count - groups));
+  // The walk's part in whole ranges (one CTA per group of KV heads each).
+  const int walk = (__float2int_ru(sm_count * (b / (a + b))) + groups - 1) / groups * groups;
+  return max(1, sm_count - max(walk, groups));
 }
 __device__ __forceinline__ float walk_tile_us(uint32_t row_bytes, int columns) {
   return columns > 8 ? 0.8f : 0.35f + 0.18f / 1024.f * row_bytes;
