@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int64_t ua = wk.cta_start(cta), ub = wk.cta_start(cta + 1);
+  const uint32_t ua = wk.cta_start(cta), ub = wk.cta_start(cta + 1);
   const int first_item = wk.item_of(ua);
 
   if (warp < kSoftmaxWarps)
@@ -842,6 +842,9 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
     prm.part_ml = reinterpret_cast<float*>(ws + sc.part_ml);
     prm.part_o = reinterpret_cast<float*>(ws + sc.part_o);
     prm.work = make_prefix_work(rows, num_kv_heads, prefix_tokens, dev.sm_count);
+    if (prm.work.ctas == 0)
+      return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %lld query rows over %d prefix tokens", (long long)rows,
+                  prefix_tokens);
     const WalkShape shape = walk_shape(num_heads, num_kv_heads, head_size, num_queries, 2);
     prm.item_ctas = reinterpret_cast<int2*>(ws + sc.item_ctas);
     prm.context_lens = context_lens;

@@ -20,9 +20,9 @@ static int check(int64_t rows, int kv_heads, int prefix, int max_ctas, int take)
   std::vector<int> owner((size_t)w.items() * w.tiles, -1);
   std::set<int> slots;
   std::map<int, std::set<int>> segments;  // item -> CTAs
-  int64_t before = 0;
+  uint32_t before = 0;
   for (int c = 0; c < w.ctas; ++c) {
-    const int64_t a = w.cta_start(c), b = w.cta_start(c + 1);
+    const uint32_t a = w.cta_start(c), b = w.cta_start(c + 1);
     if (a != before) return 5;
     before = b;
     const int first = w.item_of(a);
@@ -55,6 +55,9 @@ static int check(int64_t rows, int kv_heads, int prefix, int max_ctas, int take)
 }
 
 int main() {
+  // Lists too long for 32-bit units are told apart.
+  if (pa::make_prefix_work(1 << 24, 8, 1 << 20, 152).ctas != 0) return 1;
+  if (pa::make_prefix_work(1 << 16, 8, 1 << 20, 152).ctas != 152) return 1;
   for (int64_t rows : {1, 5, 127, 128, 129, 255, 256, 257, 384, 385, 640, 1024, 4001})
     for (int heads : {1, 2, 3, 8, 16})
       for (int prefix : {8, 120, 128, 136, 1000, 4096, 20000})
