@@ -467,6 +467,9 @@ int pa_decode_fp8_mq_append(void* out, const void* query, const void* k_new, con
  * wait_limit_us microseconds (0: the default of 2 s).  The stage meant for
  * that tile is never filled, the waits on it run out, and the kernel returns
  * after letting the copies it had started land (again within the limit).
+ * (pa_decode_prefix: its prefix kernel, whose tiles of 128 prefix tokens are
+ * counted per KV head and per 256 query rows of it, one after another;
+ * pa_decode_mod: the tiles its walk takes.)
  * That call's output is unspecified, and its scratch (pa_decode_ws) must be
  * zero-filled again before reuse.  The setting is used by one launch and then
  * cleared; tile = -1 clears it.  Returns PA_OK, or PA_ERR_INVALID_ARG for

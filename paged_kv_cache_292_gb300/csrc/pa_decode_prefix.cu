@@ -586,9 +586,9 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
   const int2 ctas = prefix ? __ldcg(p.item_ctas + item) : make_int2(0, -1);
   // Prefix partials: every CTA between the first and the last tile's has one (a
   // range holds two units or more), with a single row tile one per group.
-  const int c0 = ctas.x;
-  const int np =
-      prefix && c >= p.prefix_tokens + p.num_queries - 1 ? (ctas.y - ctas.x + 1) * (two ? 1 : 2) : 0;
+  // (After a timeout of the prefix kernel the table may hold anything: stay inside.)
+  const int c0 = max(ctas.x, 0), c1 = min(ctas.y, p.work.ctas - 1);
+  const int np = prefix && c >= p.prefix_tokens + p.num_queries - 1 ? max(c1 - c0 + 1, 0) * (two ? 1 : 2) : 0;
   // Partials of the rest: none, the walk's finished row, or one per range.
   const bool whole = cut.w == kCutWhole;
   const int nr = cut.w == kCutEmpty ? 0 : whole ? 1 : cut.y - cut.x + 1;
