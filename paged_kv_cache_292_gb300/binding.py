@@ -586,23 +586,18 @@ def _used_on(stream, *ts):
             t.record_stream(stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _call_on(index, fn, *args):
     """One library call with the tensors' device current."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args)
     else:
         with torch.cuda.device(index):
             rc = fn(*args)
     if rc != PA_OK:
         _check(rc)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _size(t):
-    return 0 if t is None else t.numel() * t.element_size()
 
 
 def pa_tables_step(block_tables, context_lens_out, seq_starts, slot_mapping, free_blocks, free_count_out,
@@ -642,9 +637,11 @@ def tables_step(block_tables, context_lens, new_lens, free_blocks, free_count, b
         raise ValueError("context_lens_out, free_count_out and seq_starts must have S, 1 and S + 1 entries")
     _call_on(index, load().pa_tables_step, block_tables.data_ptr(), context_lens_out.data_ptr(),
              seq_starts.data_ptr(), slot_mapping.data_ptr(), free_blocks.data_ptr(), free_count_out.data_ptr(),
-             context_lens.data_ptr(), new_lens.data_ptr(), free_count.data_ptr(), _at(prefix_table),
+             context_lens.data_ptr(), new_lens.data_ptr(), free_count.data_ptr(),
+             None if prefix_table is None else prefix_table.data_ptr(),
              0 if prefix_table is None else prefix_table.numel(), S, MB, block_size, free_blocks.numel(),
-             slot_mapping.numel(), _stream_on(stream, index), _at(error_flag))
+             slot_mapping.numel(), _stream_on(stream, index),
+             None if error_flag is None else error_flag.data_ptr())
     return context_lens_out, free_count_out, seq_starts
 
 
@@ -678,75 +675,105 @@ def pa_decode_mod_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads,
                                                    kv_dtype, num_ranges))
 
 
-def _step_shapes(index, query, k_cache, v_cache, block_tables, context_lens, out, pool_dtype):
-    """(S, Q, H, D, NB, bs, Hk, MB) of a step over paged pools, query [S, H, D] or [S, Q, H, D]."""
-    _on(index, query.dtype, "query and out", query, out)
-    _on(index, pool_dtype, "k_cache and v_cache", k_cache, v_cache)
-    _on(index, torch.int32, "block_tables and context_lens", block_tables, context_lens)
+def _step(query, k_cache, v_cache, block_tables, context_lens, out, pool_dtype):
+    """(device index, S, Q, H, D, NB, bs, Hk, MB) of a step over paged pools, query [S, H, D] or [S, Q, H, D]."""
+    index = query.get_device()
+    if index < 0 or k_cache.get_device() != index or v_cache.get_device() != index or \
+            block_tables.get_device() != index or context_lens.get_device() != index or not (
+                query.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and block_tables.is_contiguous() and context_lens.is_contiguous()):
+        raise ValueError("tensors must be contiguous CUDA tensors on one device")
+    if k_cache.dtype is not pool_dtype or v_cache.dtype is not pool_dtype:
+        raise ValueError(f"k_cache and v_cache must be {pool_dtype}, got {k_cache.dtype} and {v_cache.dtype}")
+    if block_tables.dtype is not torch.int32 or context_lens.dtype is not torch.int32:
+        raise ValueError("block_tables and context_lens must be torch.int32")
     shape = query.shape
-    if len(shape) == 4:
-        S, Q, H, D = shape
-    else:
+    if len(shape) == 3:
         (S, H, D), Q = shape, 1
+    else:
+        S, Q, H, D = shape
     pool = k_cache.shape
     NB, bs, Hk, Dk = pool
     SB, MB = block_tables.shape
-    if Dk != D or v_cache.shape != pool or SB != S or context_lens.numel() != S or (
-            out is not None and out.shape != shape):
-        raise ValueError("shapes of query, pools, block_tables, context_lens and out do not go together")
-    return S, Q, H, D, NB, bs, Hk, MB
+    if Dk != D or v_cache.shape != pool or SB != S or context_lens.numel() != S:
+        raise ValueError("shapes of query, pools, block_tables and context_lens do not go together")
+    if out is not None:
+        _on(index, query.dtype, "out", out)
+        if out.shape != shape:
+            raise ValueError("out must have query's shape")
+    return index, S, Q, H, D, NB, bs, Hk, MB
 
 
-def _decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, scales, out, stream, softcap,
-                alibi_slopes, window, first_tokens, prefix_lens, num_ranges, workspace, error_flag, check_block_ids):
-    index, dtype = _device_of(query), query.dtype
-    if scales and dtype is not torch.bfloat16:
-        raise ValueError(f"query must be {torch.bfloat16}, got {dtype}")
-    S, Q, H, D, NB, bs, Hk, MB = _step_shapes(index, query, k_cache, v_cache, block_tables, context_lens, out,
-                                              torch.uint8 if scales else dtype)
+def _mod_pointers(index, S, H, alibi_slopes, first_tokens, prefix_lens):
+    """Addresses of the optional per-head and per-sequence arrays."""
+    slopes = first = prefix = None
     if alibi_slopes is not None:
         _on(index, torch.float32, "alibi_slopes", alibi_slopes)
         if alibi_slopes.numel() != H:
             raise ValueError("alibi_slopes must have one entry per query head")
-    if first_tokens is not None or prefix_lens is not None:
-        _on(index, torch.int32, "first_tokens and prefix_lens", first_tokens, prefix_lens)
-        if any(t is not None and t.numel() != S for t in (first_tokens, prefix_lens)):
-            raise ValueError("first_tokens and prefix_lens must have one entry per sequence")
-    if error_flag is not None:
-        _on(index, torch.int32, "error_flag", error_flag)
+        slopes = alibi_slopes.data_ptr()
+    if first_tokens is not None:
+        _on(index, torch.int32, "first_tokens", first_tokens)
+        if first_tokens.numel() != S:
+            raise ValueError("first_tokens must have one entry per sequence")
+        first = first_tokens.data_ptr()
+    if prefix_lens is not None:
+        _on(index, torch.int32, "prefix_lens", prefix_lens)
+        if prefix_lens.numel() != S:
+            raise ValueError("prefix_lens must have one entry per sequence")
+        prefix = prefix_lens.data_ptr()
+    return slopes, first, prefix
+
+
+def _scratch_pointers(index, workspace, error_flag):
+    """(address and bytes of the workspace, address of the error word)."""
+    ws, ws_bytes, err = None, 0, None
     if workspace is not None:
         _on(index, workspace.dtype, "workspace", workspace)
-    raw = _stream_on(stream, index)
-    if out is None:
-        out = torch.empty_like(query)
-        _used_on(stream, out)
-    tensors = (out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-               context_lens.data_ptr(), S, Q, H, Hk, D, bs, MB, scale)
-    mods = (softcap, _at(alibi_slopes), window, _at(first_tokens), _at(prefix_lens), raw)
-    rest = (NB if check_block_ids else 0, _at(workspace), _size(workspace), num_ranges, _at(error_flag))
-    if scales:
-        _call_on(index, load().pa_decode_fp8_mod, *tensors, *scales, *mods, *rest)
-    else:
-        _call_on(index, load().pa_decode_mod, *tensors, *mods, dtype_code(dtype), *rest)
-    return out
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if error_flag is not None:
+        _on(index, torch.int32, "error_flag", error_flag)
+        err = error_flag.data_ptr()
+    return ws, ws_bytes, err
 
 
 def decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, out=None, stream=None, *, softcap=0.0,
                alibi_slopes=None, window=0, first_tokens=None, prefix_lens=None, num_ranges=0, workspace=None,
                error_flag=None, check_block_ids=False):
     """Decode with capped, biased and masked scores (as in ``pa_decode_mod``); query and out [S, H, D] or [S, Q, H, D]."""
-    return _decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, None, out, stream, softcap,
-                       alibi_slopes, window, first_tokens, prefix_lens, num_ranges, workspace, error_flag,
-                       check_block_ids)
+    dtype = query.dtype
+    index, S, Q, H, D, NB, bs, Hk, MB = _step(query, k_cache, v_cache, block_tables, context_lens, out, dtype)
+    code = dtype_code(dtype)
+    slopes, first, prefix = _mod_pointers(index, S, H, alibi_slopes, first_tokens, prefix_lens)
+    ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
+    raw = _stream_on(stream, index)
+    if out is None:
+        out = torch.empty_like(query)
+        _used_on(stream, out)
+    _call_on(index, load().pa_decode_mod, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+             block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H, Hk, D, bs, MB, scale, softcap, slopes, window,
+             first, prefix, raw, code, NB if check_block_ids else 0, ws, ws_bytes, num_ranges, err)
+    return out
 
 
 def decode_fp8_mod(query, k_cache, v_cache, block_tables, context_lens, scale, k_scale, v_scale, out=None,
                    stream=None, *, softcap=0.0, alibi_slopes=None, window=0, first_tokens=None, prefix_lens=None,
                    num_ranges=0, workspace=None, error_flag=None, check_block_ids=False):
     """``decode_mod`` over uint8 E4M3 pools (as in ``pa_decode_fp8_mod``)."""
-    return _decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, (k_scale, v_scale), out, stream,
-                       softcap, alibi_slopes, window, first_tokens, prefix_lens, num_ranges, workspace, error_flag,
-                       check_block_ids)
+    if query.dtype is not torch.bfloat16:
+        raise ValueError(f"query must be {torch.bfloat16}, got {query.dtype}")
+    index, S, Q, H, D, NB, bs, Hk, MB = _step(query, k_cache, v_cache, block_tables, context_lens, out, torch.uint8)
+    slopes, first, prefix = _mod_pointers(index, S, H, alibi_slopes, first_tokens, prefix_lens)
+    ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
+    raw = _stream_on(stream, index)
+    if out is None:
+        out = torch.empty_like(query)
+        _used_on(stream, out)
+    _call_on(index, load().pa_decode_fp8_mod, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
+             v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H, Hk, D, bs, MB, scale,
+             k_scale, v_scale, softcap, slopes, window, first, prefix, raw, NB if check_block_ids else 0, ws, ws_bytes,
+             num_ranges, err)
+    return out
 
 
 def pa_decode_prefix(out, query, k_cache, v_cache, prefix_table, block_tables, context_lens, num_seqs, num_queries,
@@ -769,17 +796,16 @@ def decode_prefix(query, k_cache, v_cache, prefix_table, block_tables, context_l
                   workspace=None, error_flag=None, check_block_ids=False):
     """Decode of a batch that shares the prefix in the blocks ``prefix_table[NP]``, attended once for all (as in
     ``pa_decode_prefix``); query and out [S, H, D] or [S, Q, H, D]."""
-    index, dtype = _device_of(query), query.dtype
-    S, Q, H, D, NB, bs, Hk, MB = _step_shapes(index, query, k_cache, v_cache, block_tables, context_lens, out, dtype)
-    _on(index, torch.int32, "prefix_table and error_flag", prefix_table, error_flag)
-    if workspace is not None:
-        _on(index, workspace.dtype, "workspace", workspace)
+    dtype = query.dtype
+    index, S, Q, H, D, NB, bs, Hk, MB = _step(query, k_cache, v_cache, block_tables, context_lens, out, dtype)
+    code = dtype_code(dtype)
+    _on(index, torch.int32, "prefix_table", prefix_table)
+    ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
     raw = _stream_on(stream, index)
     if out is None:
         out = torch.empty_like(query)
         _used_on(stream, out)
     _call_on(index, load().pa_decode_prefix, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), prefix_table.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H,
-             Hk, D, bs, prefix_table.numel(), MB, scale, raw, dtype_code(dtype), NB if check_block_ids else 0,
-             _at(workspace), _size(workspace), _at(error_flag))
+             Hk, D, bs, prefix_table.numel(), MB, scale, raw, code, NB if check_block_ids else 0, ws, ws_bytes, err)
     return out

@@ -377,6 +377,8 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   int32_t* counters = nullptr;
   const bool clear_tickets = workspace == nullptr && fixed_scratch != nullptr;
   if (extras != nullptr) {
+    if ((long long)num_seqs * num_queries * num_heads > 1 << 30)
+      return fail(PA_ERR_UNSUPPORTED, "pa_decode: %d sequences of %d rows", num_seqs, num_queries * num_heads);
     const size_t need = pl.ws_partials + sizeof(int4) * (size_t)num_seqs;
     if (workspace == nullptr) {
       rc = kept_scratch(need, stream, &workspace);

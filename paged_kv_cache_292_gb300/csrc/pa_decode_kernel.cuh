@@ -249,13 +249,14 @@ struct SeqWalk {
 
 // SMs for the prefix kernel of `units` units (pa_prefix_work.h) beside a walk of
 // `tiles` tiles by `groups` CTAs each, in proportion to the SM time of either: a
-// unit takes about 0.9 us (D = 128: 128 x 128 x 128 x 4 flops), a tile about 0.35
+// unit takes about 0.9 us (D = 128: 128 x 128 x 128 x 4 flops; D = 64: 0.78, where the
+// softmax sets the pace), a tile about 0.35
 // us + 0.18 us per KiB of K row, or 0.8 us with more than 8 columns per KV head, and a
 // sequence another 0.8 us (its queries, its row).  The walk is bound by HBM from about 80 SMs on.
 __device__ __forceinline__ int prefix_share(float units, long long tiles, int seqs, int groups, float tile_us,
                                             int head_size, int sm_count) {
   if (tiles == 0) return sm_count;
-  const float a = units * (head_size == 128 ? 0.9f : 0.6f), b = (tiles * tile_us + seqs * 0.8f) * groups;
+  const float a = units * (head_size == 128 ? 0.9f : 0.78f), b = (tiles * tile_us + seqs * 0.8f) * groups;
   // The walk's part in whole ranges (one CTA per group of KV heads each).
   const int walk = (__float2int_ru(sm_count * (b / (a + b))) + groups - 1) / groups * groups;
   return max(1, sm_count - max(walk, groups));
@@ -2168,9 +2169,10 @@ struct MergedRow {
   float o[DL];
 };
 
+// With several warps per row, warp `part` of `parts` takes every parts-th 32 of them.
 template <int D>
 __device__ __forceinline__ MergedRow<D / 32> merge_row(const float* part_ml, const float* part_o, const int4& cut,
-                                                       int seq_rows, int in_seq, int lane) {
+                                                       int seq_rows, int in_seq, int lane, int part, int parts) {
   constexpr int DL = D / 32;
   MergedRow<DL> r;
   r.m = -INFINITY;
@@ -2179,7 +2181,7 @@ __device__ __forceinline__ MergedRow<D / 32> merge_row(const float* part_ml, con
   for (int i = 0; i < DL; ++i) r.o[i] = 0.f;
   // Range rr left its partial in slot 0, the first range in slot cut.z.
   auto at = [&](int rr) { return ((size_t)rr * 2 + (rr == cut.x ? cut.z : 0)) * seq_rows + in_seq; };
-  for (int r0 = cut.x; r0 <= cut.y; r0 += 32) {
+  for (int r0 = cut.x + 32 * part; r0 <= cut.y; r0 += 32 * parts) {
     const int rr = r0 + lane;
     const float2 ml = rr <= cut.y ? __ldcg(reinterpret_cast<const float2*>(part_ml) + at(rr))
                                   : make_float2(-INFINITY, 0.f);
@@ -2353,6 +2355,12 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
   // Never more ranges than tiles, so no range is empty and a cut sequence
   // has exactly r1 - r0 + 1 partials.
   long long Reff = total < R ? total : R;
+  if constexpr (WALK == kWalkMod) {
+    // More ranges than SMs only where each gets eight tiles or more: a range costs
+    // its start-up and a partial of every row it cuts.
+    Reff = min(Reff, max(static_cast<long long>(p.sm_count / HG), total / 8));
+    Reff = max(Reff, min(1ll, total));
+  }
   if constexpr (WALK == kWalkRest) {
     // The SMs the prefix kernel leaves.
     if (p.beside) {

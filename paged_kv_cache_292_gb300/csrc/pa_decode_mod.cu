@@ -29,25 +29,49 @@ struct MergeParams {
   const int4* cuts;
   const float* part_ml;
   const float* part_o;
-  long long rows;    // num_seqs * seq_rows
+  int rows;          // num_seqs * seq_rows
   int seq_rows;      // num_queries * num_heads
   float v_scale;
 };
 
-template <typename T, int D>
+// WARPS warps per row: few rows, whose sequences are cut over many ranges, get all
+// 8 of a CTA.
+template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(256) pa_merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int DL = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
+  const int row = blockIdx.x * (8 / WARPS) + warp / WARPS;
+  if (row >= p.rows) return;  // (all warps of a row alike)
   griddep_wait();
   griddep_launch_dependents();
-  const int s = static_cast<int>(row / p.seq_rows), in_seq = static_cast<int>(row - (long long)s * p.seq_rows);
+  const int s = row / p.seq_rows, in_seq = row - s * p.seq_rows;
   const int4 cut = __ldcg(p.cuts + s);
   if (cut.w != kCutMerge) return;
-  const MergedRow<DL> m = merge_row<D>(p.part_ml, p.part_o, cut, p.seq_rows, in_seq, lane);
+  MergedRow<DL> m = merge_row<D>(p.part_ml, p.part_o, cut, p.seq_rows, in_seq, lane, part, WARPS);
+  if constexpr (WARPS > 1) {
+    __shared__ float parts[WARPS][DL + 2][32];
+    parts[part][DL][lane] = m.m;
+    parts[part][DL + 1][lane] = m.l;
+#pragma unroll
+    for (int i = 0; i < DL; ++i) parts[part][i][lane] = m.o[i];
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) m.m = fmaxf(m.m, parts[w][DL][lane]);
+    const float ref = m.m == -INFINITY ? 0.f : m.m;
+    m.l = 0.f;
+#pragma unroll
+    for (int i = 0; i < DL; ++i) m.o[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = ex2_ftz(parts[w][DL][lane] - ref);
+      m.l = fmaf(f, parts[w][DL + 1][lane], m.l);
+#pragma unroll
+      for (int i = 0; i < DL; ++i) m.o[i] = fmaf(f, parts[w][i][lane], m.o[i]);
+    }
+  }
   const float inv = m.l > 0.f ? p.v_scale / m.l : 0.f;
-  T* out = static_cast<T*>(p.out) + row * D + lane * DL;
+  T* out = static_cast<T*>(p.out) + (size_t)row * D + lane * DL;
 #pragma unroll
   for (int i = 0; i < DL; ++i) out[i] = T(m.o[i] * inv);
 }
@@ -55,9 +79,11 @@ __global__ void __launch_bounds__(256) pa_merge_kernel(const __grid_constant__ M
 template <typename T, int D>
 int launch_merge(const DecodeParams& prm, cudaStream_t stream) {
   MergeParams mp{prm.out, prm.cuts, prm.part_ml, prm.part_o, 0, prm.num_queries * prm.num_heads, prm.v_scale};
-  mp.rows = (long long)prm.num_seqs * mp.seq_rows;
+  mp.rows = prm.num_seqs * mp.seq_rows;
+  const bool few = mp.rows <= 4 * prm.sm_count;
   const cudaError_t e =
-      launch_pdl(pa_merge_kernel<T, D>, dim3((unsigned)((mp.rows + 7) / 8)), dim3(256), 0, stream, mp);
+      few ? launch_pdl(pa_merge_kernel<T, D, 8>, dim3(mp.rows), dim3(256), 0, stream, mp)
+          : launch_pdl(pa_merge_kernel<T, D, 1>, dim3((mp.rows + 7) / 8), dim3(256), 0, stream, mp);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_merge_kernel");
 }
 
