@@ -2169,7 +2169,7 @@ struct MergedRow {
   float o[DL];
 };
 
-// With several warps per row, warp `part` of `parts` takes every parts-th 32 of them.
+// With several warps per row, warp `part` of `parts` takes every parts-th partial.
 template <int D>
 __device__ __forceinline__ MergedRow<D / 32> merge_row(const float* part_ml, const float* part_o, const int4& cut,
                                                        int seq_rows, int in_seq, int lane, int part, int parts) {
@@ -2181,8 +2181,8 @@ __device__ __forceinline__ MergedRow<D / 32> merge_row(const float* part_ml, con
   for (int i = 0; i < DL; ++i) r.o[i] = 0.f;
   // Range rr left its partial in slot 0, the first range in slot cut.z.
   auto at = [&](int rr) { return ((size_t)rr * 2 + (rr == cut.x ? cut.z : 0)) * seq_rows + in_seq; };
-  for (int r0 = cut.x + 32 * part; r0 <= cut.y; r0 += 32 * parts) {
-    const int rr = r0 + lane;
+  for (int r0 = cut.x + part; r0 <= cut.y; r0 += 32 * parts) {
+    const int rr = r0 + lane * parts;
     const float2 ml = rr <= cut.y ? __ldcg(reinterpret_cast<const float2*>(part_ml) + at(rr))
                                   : make_float2(-INFINITY, 0.f);
     float top = ml.x;
@@ -2197,11 +2197,11 @@ __device__ __forceinline__ MergedRow<D / 32> merge_row(const float* part_ml, con
     r.l = r.l * keep + l;
 #pragma unroll
     for (int i = 0; i < DL; ++i) r.o[i] *= keep;
-    const int n = min(32, cut.y - r0 + 1);
+    const int n = min(32, (cut.y - r0) / parts + 1);
 #pragma unroll 8
     for (int k = 0; k < n; ++k) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float* po = part_o + at(r0 + k) * D + lane * DL;
+      const float* po = part_o + at(r0 + k * parts) * D + lane * DL;
       if constexpr (DL == 4) {
         const float4 v = __ldcg(reinterpret_cast<const float4*>(po));
         r.o[0] = fmaf(wk, v.x, r.o[0]), r.o[1] = fmaf(wk, v.y, r.o[1]);

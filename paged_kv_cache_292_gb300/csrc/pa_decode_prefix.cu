@@ -600,11 +600,25 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
   };
   auto part_at = [&](int k) -> int { return (c0 + (two ? k : k >> 1) + item) * 2 + (two ? in_pair >> 7 : k & 1); };
   float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 32 * part; k0 < max(nr, np); k0 += 32 * kWarps) {
-    const int k = k0 + lane;
+  // Partial k of either list belongs to the row's warp k % kWarps; lane j holds the
+  // statistics of its j-th.
+  auto o_of_part = [&](int k) {
+    return __ldcg(reinterpret_cast<const float4*>(p.part_o) +
+                  ((size_t)part_at(k) * (D / 4) + dims) * kPrefixRows + (in_pair & 127));
+  };
+  auto o_of_rest = [&](int k) { return __ldcg(reinterpret_cast<const float4*>(o_r + rest_at(k) * D) + dims); };
+  constexpr int kAhead = 8;  // O parts loaded beside the statistics, whatever their weights
+  for (int k0 = part; k0 < max(nr, np); k0 += 32 * kWarps) {
+    const int k = k0 + lane * kWarps;
+    const int here_r = min(32, (nr - k0 + kWarps - 1) / kWarps), here_p = min(32, (np - k0 + kWarps - 1) / kWarps);
     float2 a = make_float2(-INFINITY, 0.f), b = a;
     if (k < nr) a = __ldcg(reinterpret_cast<const float2*>(ml_r) + rest_at(k));
     if (k < np) b = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)part_at(k) * kPrefixRows + (in_pair & 127));
+    float4 first_r = make_float4(0.f, 0.f, 0.f, 0.f), first_p[kAhead];
+    if (here_r > 0) first_r = o_of_rest(k0);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < here_p) first_p[i] = o_of_part(k0 + i * kWarps);
     if (a.y == 0.f) a.x = -INFINITY;  // no token seen: no weight
     if (b.y == 0.f) b.x = -INFINITY;
     float top = fmaxf(a.x, b.x);
@@ -620,44 +634,43 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
     l = l * keep + lw;
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] *= keep;
-    // The loads are made whatever the weight, so that several are in flight; a
-    // partial without weight may hold anything.
+    // A partial without weight may hold anything.
     auto add = [&](float w, const float4& o) {
       if (w != 0.f) {
         acc[0] = fmaf(w, o.x, acc[0]), acc[1] = fmaf(w, o.y, acc[1]);
         acc[2] = fmaf(w, o.z, acc[2]), acc[3] = fmaf(w, o.w, acc[3]);
       }
     };
-    const int here_r = min(32, nr - k0), here_p = min(32, np - k0);
+    if (here_r > 0) add(__shfl_sync(0xffffffffu, wa, 0), first_r);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < here_p) add(__shfl_sync(0xffffffffu, wb, i), first_p[i]);
 #pragma unroll 8
-    for (int i = 0; i < here_r; ++i)
-      add(__shfl_sync(0xffffffffu, wa, i), __ldcg(reinterpret_cast<const float4*>(o_r + rest_at(k0 + i) * D) + dims));
+    for (int i = 1; i < here_r; ++i) add(__shfl_sync(0xffffffffu, wa, i), o_of_rest(k0 + i * kWarps));
 #pragma unroll 8
-    for (int i = 0; i < here_p; ++i)
-      add(__shfl_sync(0xffffffffu, wb, i),
-          __ldcg(reinterpret_cast<const float4*>(p.part_o) +
-                 ((size_t)part_at(k0 + i) * (D / 4) + dims) * kPrefixRows + (in_pair & 127)));
+    for (int i = kAhead; i < here_p; ++i) add(__shfl_sync(0xffffffffu, wb, i), o_of_part(k0 + i * kWarps));
   }
   if constexpr (kWarps > 1) {
-    __shared__ float parts[kWarps][6][32];
-    parts[part][4][lane] = m;
-    parts[part][5][lane] = l;
+    __shared__ float parts[8][6][32];
+    float(*mine)[6][32] = parts + (warp - part);  // the row's warps
+    mine[part][4][lane] = m;
+    mine[part][5][lane] = l;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) parts[part][i][lane] = acc[i];
-    __syncthreads();
+    for (int i = 0; i < 4; ++i) mine[part][i][lane] = acc[i];
+    named_barrier_sync(1 + warp / kWarps, 32 * kWarps);
     if (part != 0) return;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, parts[w][4][lane]);
+    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, mine[w][4][lane]);
     const float ref = m == -INFINITY ? 0.f : m;
     l = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2_ftz(parts[w][4][lane] - ref);
-      l = fmaf(f, parts[w][5][lane], l);
+      const float f = ex2_ftz(mine[w][4][lane] - ref);
+      l = fmaf(f, mine[w][5][lane], l);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, parts[w][i][lane], acc[i]);
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, mine[w][i][lane], acc[i]);
     }
   }
   if (lane < kLanes) {
@@ -896,15 +909,17 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   jp.group = group;
   jp.prefix_tokens = prefix_tokens;
   jp.max_tokens = max_blocks_per_seq * block_size;
-  // Fewer rows than the SMs hold warps for: a CTA each.
-  const bool few = jp.rows <= 4 * dev.sm_count;
-  const dim3 grid((unsigned)(few ? jp.rows : (jp.rows + 7) / 8));
+  // The fewer the rows, the longer their lists and the more warps there are for each.
+  const int warps = jp.rows <= 4 * dev.sm_count ? 8 : jp.rows <= 16 * dev.sm_count ? 2 : 1;
+  const dim3 grid((unsigned)((jp.rows + 8 / warps - 1) / (8 / warps)));
   cudaError_t e;
-  if (few)
-    e = head_size == 64 ? launch_pdl(pa_prefix_join<64, 8>, grid, dim3(256), 0, st, jp)
-                        : launch_pdl(pa_prefix_join<128, 8>, grid, dim3(256), 0, st, jp);
+  if (head_size == 64)
+    e = warps == 8   ? launch_pdl(pa_prefix_join<64, 8>, grid, dim3(256), 0, st, jp)
+        : warps == 2 ? launch_pdl(pa_prefix_join<64, 2>, grid, dim3(256), 0, st, jp)
+                     : launch_pdl(pa_prefix_join<64, 1>, grid, dim3(256), 0, st, jp);
   else
-    e = head_size == 64 ? launch_pdl(pa_prefix_join<64, 1>, grid, dim3(256), 0, st, jp)
-                        : launch_pdl(pa_prefix_join<128, 1>, grid, dim3(256), 0, st, jp);
+    e = warps == 8   ? launch_pdl(pa_prefix_join<128, 8>, grid, dim3(256), 0, st, jp)
+        : warps == 2 ? launch_pdl(pa_prefix_join<128, 2>, grid, dim3(256), 0, st, jp)
+                     : launch_pdl(pa_prefix_join<128, 1>, grid, dim3(256), 0, st, jp);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefix_join");
 }
