@@ -302,8 +302,10 @@ size_t pa_decode_mod_workspace_size(int num_seqs, int num_queries, int num_heads
  * num_prefix_blocks <= max_blocks_per_seq; (num_heads / num_kv_heads) *
  * num_queries <= 32.  num_physical_blocks > 0 checks the prefix's block ids
  * too; tokens of a bad one count as zeros.
- * The softmax weights of the prefix enter its second product rounded to bf16
- * (relative error <= 2^-8 each; sums and statistics stay fp32).
+ * With more than 128 query rows per KV head (num_seqs * num_queries * group) the
+ * softmax weights of the prefix enter its second product rounded to bf16
+ * (relative error <= 2^-8 each), with fewer to about 2^-16; sums and statistics
+ * stay fp32.
  * workspace    256-byte aligned device scratch of at least
  *              pa_decode_prefix_workspace_size(...) bytes, of any content; NULL:
  *              the library's own, refused while `stream` is being captured

@@ -22,8 +22,8 @@
 // With two row tiles each group has one and both use every K/V tile; with a
 // single row tile the groups take alternate K/V tiles and leave a partial
 // each.  While one group exponentiates, the tensor core works for the other.
-// Tensor memory: S0, S1 (128 columns each; the weights overwrite the first 64),
-// O0, O1 (D columns each).
+// Tensor memory: S0, S1 (128 columns each; the weights overwrite the first 64,
+// their second parts, if any, the other 64), O0, O1 (D columns each).
 #include "pa_launch.cuh"
 
 #include <cmath>
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
   const uint32_t ua = wk.cta_start(cta), ub = wk.cta_start(cta + 1);
   const int first_item = wk.item_of(ua);
+  const bool fine = wk.pairs == 1 && wk.last_weight == 1;  // weights in two parts
 
   if (warp < kSoftmaxWarps)
     registers_up<kSoftmaxRegisters>();
@@ -318,22 +319,39 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
         const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), neg2 = pair(neg, neg);
         uint64_t sum[2] = {0ull, 0ull};
+        // The weights enter the product as bf16: half a step, 2^-8 at most, both
+        // signs alike; the sum keeps them in fp32.  Where one row tile is all
+        // (fine), and the copies set the pace, their remainders follow as a second
+        // bf16 part (2^-16 together) in the columns behind.
+        auto weights = [&](int e, int i) -> uint32_t {  // two of them, kept in s for their remainders
+          float a, b;
+          unpair(fma_pair(pair(s[e], s[e + 1]), scale2, neg2), a, b);
+          s[e] = ex2_ftz(a);
+          s[e + 1] = ex2_ftz(b);
+          sum[i & 1] = add_pair(sum[i & 1], pair(s[e], s[e + 1]));
+          return pack_bf16x2(s[e], s[e + 1]);
+        };
+        if (!fine) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t hi[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int e = 32 * c + 2 * i;
-            float a, b;
-            unpair(fma_pair(pair(s[e], s[e + 1]), scale2, neg2), a, b);
-            a = ex2_ftz(a);
-            b = ex2_ftz(b);
-            sum[i & 1] = add_pair(sum[i & 1], pair(a, b));
-            // The weights enter the product as bf16: half a step (2^-8 at most,
-            // both signs alike); the sum keeps them in fp32.
-            pk[i] = pack_bf16x2(a, b);
+            for (int i = 0; i < 16; ++i) hi[i] = weights(32 * c + 2 * i, i);
+            tmem_store16(s_addr + 32u * half + 16u * c, hi);
           }
-          tmem_store16(s_addr + 32u * half + 16u * c, pk);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int e = 8 * c + 2 * i;
+              hi[i] = weights(e, i);
+              lo[i] = pack_bf16x2(s[e] - bf16_lo(hi[i]), s[e + 1] - bf16_hi(hi[i]));
+            }
+            tmem_store4(s_addr + 32u * half + 4u * c, hi);
+            tmem_store4(s_addr + 64u + 32u * half + 4u * c, lo);
+          }
         }
         {
           float a, b;
@@ -509,6 +527,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
             for (int kk = 0; kk < kPrefixTokens / 16; ++kk)
               mma_ts(tmem + 256u + (uint32_t)D * w, tmem + 128u * w + 8u * kk, b + ((kk * 2048u) >> 4), kValues,
                      kk > 0 || x >= t0 + (two ? 1 : 2));
+            if (fine) {  // the weights' second part
+#pragma unroll
+              for (int kk = 0; kk < kPrefixTokens / 16; ++kk)
+                mma_ts(tmem + 256u + (uint32_t)D * w, tmem + 128u * w + 64u + 8u * kk, b + ((kk * 2048u) >> 4), kValues,
+                       true);
+            }
           }
           __syncwarp();
           if (more) {
