@@ -27,7 +27,6 @@
 #include "pa_launch.cuh"
 
 #include <cmath>
-#include <cstring>
 
 #include "pa_decode_impl.h"
 #include "pa_prefix_work.h"
@@ -742,52 +741,21 @@ int count_items(int num_seqs, int num_queries, int num_heads, int num_kv_heads) 
   return (int)(pairs * num_kv_heads);
 }
 
-// The pools' tensor maps.  A map is a pure function of the fields of its key, so
-// the last few are kept per thread and a step over the same pools skips the
-// driver's encoder.
-struct MapKey {
-  const void* k;
-  const void* v;
-  uint64_t rows;
-  int num_kv_heads, head_size, box_rows;
-};
-struct KeptMaps {
-  MapKey key;
-  CUtensorMap tm_k, tm_v;
-};
-constexpr int kKeptMaps = 4;
-thread_local KeptMaps g_maps[kKeptMaps];
-thread_local int g_maps_used = 0, g_maps_next = 0;
-
-int make_maps(PrefixParams* prm, const MapKey& key) {
-  for (int i = 0; i < g_maps_used; ++i) {
-    const MapKey& o = g_maps[i].key;
-    if (o.k == key.k && o.v == key.v && o.rows == key.rows && o.num_kv_heads == key.num_kv_heads &&
-        o.head_size == key.head_size && o.box_rows == key.box_rows) {
-      prm->tm_k = g_maps[i].tm_k;
-      prm->tm_v = g_maps[i].tm_v;
-      return PA_OK;
-    }
-  }
+// The pools' tensor maps, encoded for every call (about 0.1 us each).
+int make_maps(PrefixParams* prm, const void* k, const void* v, uint64_t pool_rows, int num_kv_heads, int head_size) {
   const EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return fail(PA_ERR_CUDA, "pa_decode_prefix: the driver has no cuTensorMapEncodeTiled");
-  const cuuint64_t row = (cuuint64_t)key.num_kv_heads * key.head_size;
-  const cuuint64_t dims[3] = {64, row / 64, key.rows}, strides[2] = {128, row * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)key.box_rows}, estride[3] = {1, 1, 1};
+  const cuuint64_t row = (cuuint64_t)num_kv_heads * head_size;
+  const cuuint64_t dims[3] = {64, row / 64, pool_rows}, strides[2] = {128, row * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)prm->box_rows}, estride[3] = {1, 1, 1};
   for (int i = 0; i < 2; ++i) {
     const CUresult r = enc(i ? &prm->tm_v : &prm->tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                           const_cast<void*>(i ? key.v : key.k), dims, strides, box, estride,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           const_cast<void*>(i ? v : k), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
       return fail(PA_ERR_CUDA, "pa_decode_prefix: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
   }
-  KeptMaps& m = g_maps[g_maps_next];
-  m.key = key;
-  m.tm_k = prm->tm_k;
-  m.tm_v = prm->tm_v;
-  g_maps_next = (g_maps_next + 1) % kKeptMaps;
-  if (g_maps_used < kKeptMaps) ++g_maps_used;
   return PA_OK;
 }
 
@@ -871,7 +839,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
                   (unsigned long long)pool_rows);
     prm.box_rows = block_size & -block_size;
     if (prm.box_rows > kPrefixTokens) prm.box_rows = kPrefixTokens;
-    rc = make_maps(&prm, MapKey{k_cache, v_cache, pool_rows, num_kv_heads, head_size, prm.box_rows});
+    rc = make_maps(&prm, k_cache, v_cache, pool_rows, num_kv_heads, head_size);
     if (rc != PA_OK) return rc;
     prm.q = static_cast<const __nv_bfloat16*>(query);
     prm.table = prefix_table;
