@@ -235,7 +235,7 @@ int pa_decode_mq_append(void* out, const void* query, const void* k_new, const v
  *   t < prefix_lens[s]   or   ( t <= pos  and  (window == 0 or pos - t < window) )
  *
  * softcap      >= 0, finite (tanh cap of the scores; 0: none)
- * alibi_slopes [num_heads] float or NULL (any finite values)
+ * alibi_slopes [num_heads] float or NULL (finite, also times a distance)
  * window       >= 0: tokens a query sees back, its own included (0: all)
  * first_tokens [num_seqs] int32 or NULL: first token a sequence's queries see
  *              (the start of their document); below 0 counts as 0
@@ -252,10 +252,13 @@ int pa_decode_mq_append(void* out, const void* query, const void* k_new, const v
  * Types: PA_F32 (num_queries == 1) or PA_BF16; (num_heads / num_kv_heads) *
  * num_queries <= 32.
  * workspace    256-byte aligned device scratch of at least
- *              pa_decode_mod_workspace_size(...) bytes, of any content; NULL: the
- *              library's own, refused while `stream` is being captured
- *              (PA_ERR_INVALID_ARG).  Two calls that may overlap in time need
- *              scratch of their own.
+ *              pa_decode_mod_workspace_size(...) bytes, of any content; two calls
+ *              that may overlap in time must not share it.  NULL: the library's
+ *              own, one buffer per stream, refused while `stream` is being
+ *              captured (PA_ERR_INVALID_ARG).  It is allocated at a stream's first
+ *              call and when a batch outgrows it; those calls, and a first call
+ *              on a ninth stream, which takes over the buffer used longest ago,
+ *              may wait for the device.
  * Other arguments as in pa_decode_mq.  The call makes two launches: the walk, and
  * a merge of the sequences that range boundaries cut.
  *
@@ -307,10 +310,8 @@ size_t pa_decode_mod_workspace_size(int num_seqs, int num_queries, int num_heads
  * (relative error <= 2^-8 each), with fewer to about 2^-16; sums and statistics
  * stay fp32.
  * workspace    256-byte aligned device scratch of at least
- *              pa_decode_prefix_workspace_size(...) bytes, of any content; NULL:
- *              the library's own, refused while `stream` is being captured
- *              (PA_ERR_INVALID_ARG).  Two calls that may overlap in time need
- *              scratch of their own.
+ *              pa_decode_prefix_workspace_size(...) bytes; or NULL: as in
+ *              pa_decode_mod
  * Other arguments as in pa_decode_mq.  The call makes up to three launches.
  */
 int pa_decode_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,

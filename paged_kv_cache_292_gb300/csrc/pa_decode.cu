@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <type_traits>
@@ -463,8 +464,12 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
     const double log2e = 1.4426950408889634;
     const double per_cap = extras->softcap > 0.f ? (double)scale * k_scale / extras->softcap : 0.0;
     // The tensor-core consumers take tanh from a power of two, fp32 calls tanhf.
-    prm.cap_in = (float)(dtype == PA_F32 ? per_cap : 2.0 * log2e * per_cap);
-    prm.cap_out = (float)(extras->softcap * log2e);
+    // Caps at the ends of fp32's range keep finite factors: any score reaches the
+    // smallest caps, none gets near the largest.
+    const double cap_in = dtype == PA_F32 ? per_cap : 2.0 * log2e * per_cap, most = FLT_MAX;
+    prm.cap_in = (float)(cap_in > most ? most : cap_in < -most ? -most : cap_in);
+    const double cap_out = extras->softcap * log2e;
+    prm.cap_out = (float)(cap_out > most ? most : cap_out);
     prm.slopes = extras->alibi_slopes;
     prm.first_tokens = extras->first_tokens;
     prm.prefix_lens = extras->prefix_lens;

@@ -25,8 +25,16 @@ void* g_ws_ptr[kMaxDevices] = {nullptr};
 size_t g_ws_bytes[kMaxDevices] = {0};
 void* g_cnt_ptr[kMaxDevices] = {nullptr};
 size_t g_cnt_bytes[kMaxDevices] = {0};
-void* g_kept_ptr[kMaxDevices] = {nullptr};  // kept_scratch
-size_t g_kept_bytes[kMaxDevices] = {0};
+// kept_scratch: a buffer for each of the streams that called last.
+struct KeptScratch {
+  unsigned long long stream;  // its id, which no other stream of the process ever gets
+  unsigned long long used;    // 0: free
+  void* ptr;
+  size_t bytes;
+};
+constexpr int kKeptStreams = 8;
+KeptScratch g_kept[kMaxDevices][kKeptStreams];
+unsigned long long g_kept_calls = 0;
 }  // namespace
 
 int fail(int code, const char* fmt, ...) {
@@ -138,20 +146,40 @@ int kept_scratch(size_t bytes, void* stream, void** ptr) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
   if (status != cudaStreamCaptureStatusNone)
     return fail(PA_ERR_INVALID_ARG, "a captured call needs a workspace of the caller's");
+  unsigned long long id = 0;
+  e = cudaStreamGetId(static_cast<cudaStream_t>(stream), &id);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetId");
   int dev = 0;
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   std::lock_guard<std::mutex> lock(g_mutex);
-  if (g_kept_bytes[dev] < bytes) {
-    size_t want = (size_t)16 << 20;
-    while (want < bytes) want *= 2;
-    void* p = nullptr;
-    e = cudaMalloc(&p, want);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(scratch)");
-    g_kept_ptr[dev] = p;
-    g_kept_bytes[dev] = want;
+  KeptScratch* mine = &g_kept[dev][0];  // the stream's, or the one not used for longest
+  for (KeptScratch& k : g_kept[dev]) {
+    if (k.used != 0 && k.stream == id) {
+      mine = &k;
+      break;
+    }
+    if (k.used < mine->used) mine = &k;
   }
-  *ptr = g_kept_ptr[dev];
+  const bool other = mine->used != 0 && mine->stream != id;
+  if (mine->bytes < bytes || other) {
+    if (mine->used != 0) {  // calls that use the buffer may still run
+      e = cudaDeviceSynchronize();
+      if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize(scratch)");
+    }
+    if (mine->bytes < bytes) {
+      size_t want = (size_t)16 << 20;
+      while (want < bytes) want *= 2;
+      if (mine->used != 0) (void)cudaFree(mine->ptr);
+      *mine = KeptScratch{};
+      e = cudaMalloc(&mine->ptr, want);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(scratch)");
+      mine->bytes = want;
+    }
+    mine->stream = id;
+  }
+  mine->used = ++g_kept_calls;
+  *ptr = mine->ptr;
   return PA_OK;
 }
 

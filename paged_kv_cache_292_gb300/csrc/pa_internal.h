@@ -41,10 +41,12 @@ int library_workspace(size_t bytes, void** ptr);
 int library_counters(size_t bytes, int32_t** ptr);
 
 // Library-owned scratch of the operators beyond plain decode: at least `bytes`
-// of any content.  Apart from the two buffers above, and never freed: a buffer
-// that got too small stays allocated (sizes double, so all of them together are
-// below twice the largest).  Refused while `stream` is being captured, where a
-// graph would keep the address beyond this call: captured calls bring their own.
+// of any content, a buffer for each stream, so that calls on two streams do not
+// meet in one.  The buffers of the last eight streams are kept; a stream beyond
+// them takes over the buffer used longest ago, and a batch that outgrows its buffer
+// replaces it (sizes double): both wait for the device.  Refused while `stream` is being
+// captured, where a graph would keep the address beyond this call: captured calls
+// bring their own.
 int kept_scratch(size_t bytes, void* stream, void** ptr);
 
 // Writes the new rows of a multi-query appending call into the pools (token

@@ -250,3 +250,30 @@ def test_python_layer_refuses_mismatched_arguments():
                   (q, k, v, tables.long(), lens), (q.float(), k, v, tables, lens), (q[:, ::2], k, v, tables, lens)):
         with pytest.raises(ValueError):
             binding.decode_mod(*other, scale)
+
+
+@pytest.mark.parametrize("cap", [1e-40, 1e-3, 40.0, 1e3, 1e6, 1e20, 3e38])
+@pytest.mark.parametrize("dtype, Q", [("bf16", 1), ("bf16", 4), ("bf16", 5), ("fp8", 1), ("fp8", 5), ("f32", 1)])
+def test_caps_of_every_size(cap, dtype, Q):
+    """The smallest caps make all scores alike, the largest change none.  Caps up to 64 add 2^-22 of the cap,
+    larger ones 2^-19 of a score at most, or where it is below an eighth of the cap 2^-23 of it."""
+    Batch(dtype, [1, 70, 300], Q, softcap=cap).check(f"cap {cap} {dtype} Q={Q}")
+
+
+@pytest.mark.parametrize("dtype, Q", [("bf16", 1), ("fp8", 5), ("f32", 1)])
+def test_calls_on_many_streams_at_once(dtype, Q):
+    """The library's scratch is one buffer per stream: calls that overlap do not meet in it, also beyond the
+    number of streams it keeps buffers for."""
+    parts = [Batch(dtype, ctx, Q, seed=i, window=w) for i, (ctx, w) in enumerate([([3000, 9], 0), ([1500, 2000], 700)])]
+    calls = [(x, *x.gpu()) for x in parts]
+    wants = [x.call(args, kw) for x, args, kw in calls]
+    streams = [torch.cuda.Stream() for _ in range(11)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for j in range(4):
+            got += [(i, x.call(args, kw, stream=st)) for k, st in enumerate(streams[:2 if j < 3 else 11])
+                    for i, (x, args, kw) in enumerate(calls) if i == (j + k) % 2]
+        torch.cuda.synchronize()
+        for i, out in got:
+            assert torch.equal(out, wants[i])
