@@ -2368,12 +2368,6 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
   // Never more ranges than tiles, so no range is empty and a cut sequence
   // has exactly r1 - r0 + 1 partials.
   long long Reff = total < R ? total : R;
-  if constexpr (WALK == kWalkMod) {
-    // More ranges than SMs only where each gets eight tiles or more: a range costs
-    // its start-up and a partial of every row it cuts.
-    Reff = min(Reff, max(static_cast<long long>(p.sm_count / HG), total / 8));
-    Reff = max(Reff, min(1ll, total));
-  }
   if constexpr (WALK == kWalkRest) {
     // The SMs the prefix kernel leaves.
     if (p.beside) {

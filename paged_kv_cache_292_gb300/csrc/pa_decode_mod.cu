@@ -80,7 +80,7 @@ template <typename T, int D>
 int launch_merge(const DecodeParams& prm, cudaStream_t stream) {
   MergeParams mp{prm.out, prm.cuts, prm.part_ml, prm.part_o, 0, prm.num_queries * prm.num_heads, prm.v_scale};
   mp.rows = prm.num_seqs * mp.seq_rows;
-  const bool few = mp.rows <= 4 * prm.sm_count;
+  const bool few = mp.rows <= 8 * prm.sm_count;
   const cudaError_t e =
       few ? launch_pdl(pa_merge_kernel<T, D, 8>, dim3(mp.rows), dim3(256), 0, stream, mp)
           : launch_pdl(pa_merge_kernel<T, D, 1>, dim3((mp.rows + 7) / 8), dim3(256), 0, stream, mp);

@@ -27,8 +27,15 @@
 namespace pa {
 namespace {
 
-// Small steps take CTAs whose few warps synchronise quickly, large ones as many
-// threads as an SM's share of slots keeps busy.
+// Few sequences and slots take CTAs of few warps, which start and synchronise
+// quickly, many as many threads as an SM holds.  Device time with 256 / 1024 threads:
+//   64 sequences, a slot each             3.5 / 5.4 us
+//   1024 sequences, a slot each           5.3 / 6.8
+//   517 sequences, 25 k slots             6.6 / 8.2
+//   256 sequences, 100 k slots            6.0 / 5.9
+//   512 sequences, 250 k slots           10.2 / 7.2
+//   4096 sequences, a slot each          18.2 / 9.8
+//   4096 sequences, 0.5 M slots          29.7 / 13.8
 constexpr int kSmallThreads = 256, kLargeThreads = 1024;
 constexpr int kTablesMaxSeqs = 12288;  // four int32 per sequence in shared memory
 
@@ -90,10 +97,7 @@ __device__ __forceinline__ int owner_of(const int* ends, int n, int x) {
   return lo;
 }
 
-// RUN: consecutive slots a thread writes.  Prompt chunks mostly lie in one block of
-// one sequence, which a run searches and looks up once; with more threads than
-// slots a thread per slot has the shorter chain of loads.
-template <int THREADS, int RUN>
+template <int THREADS>
 __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ long long scratch[3][32], reduce[2][32];
@@ -243,70 +247,42 @@ __global__ void __launch_bounds__(THREADS) pa_tables_kernel(const TablesParams p
     *p.free_count_out = top - (int)total_need;
   }
   // One list of work for all threads, each entry a chain of searches and loads of
-  // its own: the slots in runs, the taken blocks into the tables, the returned ones
-  // onto the free list.
-  const long long runs = ((long long)p.max_tokens + RUN - 1) / RUN, takes = runs + total_need, all = takes + n_back;
-  const bool wide = (reinterpret_cast<uintptr_t>(p.slot_mapping) & 15u) == 0;
+  // its own: the slots, the taken blocks into the tables, the returned ones onto
+  // the free list.  (Four slots a thread, which mostly share their block: 4096
+  // sequences with 0.5 M slots 16.3 us, one a thread 13.8.)
+  const long long slots = p.max_tokens, takes = slots + total_need, all = takes + n_back;
   for (long long entry = gtid; entry < all; entry += gthreads) {
     if (entry >= takes) {
       const int k = static_cast<int>(entry - takes), s = owner_of(back_end, S, k);
       p.free_blocks[count + k] = p.block_tables[(size_t)s * p.max_blocks + np + k - (s ? back_end[s - 1] : 0)];
       continue;
     }
-    if (entry >= runs) {
-      const int k = static_cast<int>(entry - runs), s = owner_of(need_end, S, k);
+    if (entry >= slots) {
+      const int k = static_cast<int>(entry - slots), s = owner_of(need_end, S, k);
       const int j = blocks_for(base_of[s]) + k - (s ? need_end[s - 1] : 0);
       p.block_tables[(size_t)s * p.max_blocks + j] = free_block(top - 1 - k);
       continue;
     }
-    const long long i0 = entry * RUN;
-    long long slot[RUN];
-    int s = -1, end = 0, pos = 0, held = 0, need0 = 0, row_block = -1;
-    long long first = 0;  // slot of the current block's token 0
-#pragma unroll
-    for (int k = 0; k < RUN; ++k) {
-      const long long i = i0 + k;
-      slot[k] = -1;
-      if (i < total_grow) {
-        if (i >= end) {  // another sequence
-          s = owner_of(grow_end, S, static_cast<int>(i));
-          end = grow_end[s];
-          pos = base_of[s] + static_cast<int>(i) - (s ? grow_end[s - 1] : 0);
-          held = blocks_for(base_of[s]);
-          need0 = s ? need_end[s - 1] : 0;
-          row_block = -1;
-        }
-        const int j = block_of(pos);
-        if (j != row_block) {
-          row_block = j;
-          const int b = j < held ? p.block_tables[(size_t)s * p.max_blocks + j]
-                                 : free_block(top - 1 - (need0 + j - held));
-          first = (long long)b * bs;
-        }
-        slot[k] = first + (pos - j * bs);
-        ++pos;
-      }
+    const int i = static_cast<int>(entry);
+    long long slot = -1;
+    if (i < total_grow) {
+      const int s = owner_of(grow_end, S, i), base = base_of[s];
+      const int pos = base + i - (s ? grow_end[s - 1] : 0), j = block_of(pos), held = blocks_for(base);
+      const int b = j < held ? p.block_tables[(size_t)s * p.max_blocks + j]
+                             : free_block(top - 1 - ((s ? need_end[s - 1] : 0) + j - held));
+      slot = (long long)b * bs + (pos - j * bs);
     }
-    int64_t* dst = p.slot_mapping + i0;
-    if (RUN > 1 && wide && i0 + RUN <= p.max_tokens) {
-#pragma unroll
-      for (int k = 0; k + 1 < RUN; k += 2)
-        *reinterpret_cast<longlong2*>(dst + k) = make_longlong2(slot[k], slot[k + 1]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < RUN; ++k)
-        if (i0 + k < p.max_tokens) dst[k] = slot[k];
-    }
+    p.slot_mapping[i] = slot;
   }
 }
 
-template <int THREADS, int RUN>
+template <int THREADS>
 int launch_tables(const TablesParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
   static RaisedDevices raised;
-  const int rc = raise_smem_limit(reinterpret_cast<const void*>(pa_tables_kernel<THREADS, RUN>), 16 * kTablesMaxSeqs,
+  const int rc = raise_smem_limit(reinterpret_cast<const void*>(pa_tables_kernel<THREADS>), 16 * kTablesMaxSeqs,
                                   dev.device, &raised);
   if (rc != PA_OK) return rc;
-  const long long work = (long long)prm.max_tokens / RUN + prm.num_seqs;
+  const long long work = (long long)prm.max_tokens + prm.num_seqs;
   const long long want = (work + THREADS - 1) / THREADS;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(want < dev.sm_count ? want : dev.sm_count));
@@ -318,7 +294,7 @@ int launch_tables(const TablesParams& prm, const DeviceInfo& dev, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, pa_tables_kernel<THREADS, RUN>, prm);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, pa_tables_kernel<THREADS>, prm);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_tables_kernel");
 }
 
@@ -382,7 +358,6 @@ extern "C" int pa_tables_step(int32_t* block_tables, int32_t* context_lens_out, 
                    num_seqs, num_prefix_blocks, max_blocks_per_seq, block_size, num_physical_blocks, max_tokens};
   const size_t smem = 16 * S;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (num_seqs <= 1024 && max_tokens <= 4096) return launch_tables<kSmallThreads, 1>(prm, dev, st);
-  if (max_tokens <= dev.sm_count * kLargeThreads) return launch_tables<kLargeThreads, 1>(prm, dev, st);
-  return launch_tables<kLargeThreads, 4>(prm, dev, st);
+  const bool small = num_seqs <= 1024 && max_tokens <= 2 * dev.sm_count * kSmallThreads;
+  return small ? launch_tables<kSmallThreads>(prm, dev, st) : launch_tables<kLargeThreads>(prm, dev, st);
 }
