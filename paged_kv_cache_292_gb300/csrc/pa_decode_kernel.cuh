@@ -1526,7 +1526,10 @@ struct MmaConsumerF8 {
 // Q K^T with Q as the A operand, and the weights are A again for O[16 x D] += P V
 // straight from the score registers.  Against 8 columns per warp (S^T = K Q^T) it
 // reads, and for FP8 pools widens, every K and V fragment once for 16 rows, needs
-// two shuffles per reduction instead of three and no transpose of P.
+// two shuffles per reduction instead of three and no transpose of P: 48 sequences x
+// 4 queries over FP8 pools 75 -> 57 us, 96 x 3 over 64 dims 99 -> 66.  What bounds it is
+// instruction issue and its latencies (10 to 15 warps per SM, 35 to 46% of issue
+// slots); one tile a pass gives 98 and 74 us, four 85 and 110 (registers spill).
 //   bf16: P as a high and a low bf16 part (about 2^-16).  FP8 pools: codes widened
 //   to f16, head dims inside a 16-wide k-step in the order 4t .. 4t + 3 per lane
 //   (see MmaConsumerF8), P rounded to f16.
@@ -1900,7 +1903,9 @@ struct SimtConsumer {
 // there too, as broadcasts.  Of a token's finished scores the even lane keeps the
 // even heads and the odd lane the odd ones: cap, bias, maximum, exponential.
 // Output: lane l owns dims [l * D / 32, (l + 1) * D / 32) of all heads, the weights
-// come back through a small buffer.  Products run two to an instruction.
+// come back through a small buffer.  Products run two to an instruction.  Bound by
+// shared-memory reads and products: 3 sequences of 3k to 9k tokens, 8 query heads of 128
+// per KV head, 149 us with every head's K read apart, 47 us so (11 us of HBM time).
 template <int D, int GMAX>
 struct Fp32ModConsumer {
   static constexpr int DC = D / 32, DP = DC / 2;  // dims per lane, as pairs
@@ -2323,7 +2328,8 @@ __device__ __forceinline__ void append_new_rows_fp8(const DecodeParams& p, const
 // paths: QMODE 1 or 2, also for one query).
 // Walks other than kWalkAll keep to 128 registers where they can (four warps per
 // quarter of an SM instead of three): their consumers wait on latency, and more of
-// them hide it.  Rows of 128 dims need more.
+// them hide it.  Rows of 128 dims need more: FP8 pools, 48 sequences x 4 queries take 74 us
+// at 128 registers, with spills, and 56 at 168.
 template <typename T, int D, int QMODE, int WALK>
 constexpr int max_threads() {
   const bool fits = sizeof(T) == 2 && WALK != kWalkAll && (D == 64 || QMODE < 2);

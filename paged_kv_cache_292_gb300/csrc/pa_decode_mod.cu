@@ -10,6 +10,12 @@
 // equal ranges.  Inside a tile, rows nobody sees are neither copied (whole boxes)
 // nor used (their scores are -inf and their V entries zeroed in registers).
 //
+// Measured (HBM copies run at 6.77 TB/s): 64 sequences of up to 32k tokens, cap and a
+// window of 4096, 848 MB in 134 us (6.3 TB/s); 4 sequences of 32k with slopes, 1.02 GB in
+// 153 us (6.6 TB/s).  Beyond 8 columns per KV head the tiles' arithmetic takes over:
+// FP8 pools, 48 sequences x 4 queries, 195 MB in 57 us (3.4 TB/s); 96 sequences x 3
+// queries of 64 dims, 186 MB in 66 us (2.8 TB/s).
+//
 // Sequences cut by range boundaries leave partials, which a second kernel merges,
 // a warp per output row.  (In plain decode the last warp to finish a KV head
 // merges all its rows; with 32 columns per KV head and sequences cut over tens of
@@ -35,7 +41,8 @@ struct MergeParams {
 };
 
 // WARPS warps per row: few rows, whose sequences are cut over many ranges, get all
-// 8 of a CTA.
+// 8 of a CTA.  One / eight warps, whole call: 64 rows (2 sequences of 8k) 47.7 / 17.4 us,
+// 1024 rows 38.6 / 36.7, 2048 rows 134.0 / 135.3, 6144 rows 56.7 / 66.7.
 template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(256) pa_merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int DL = D / 32;

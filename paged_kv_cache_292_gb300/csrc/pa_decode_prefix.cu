@@ -24,6 +24,16 @@
 // each.  While one group exponentiates, the tensor core works for the other.
 // Tensor memory: S0, S1 (128 columns each; the weights overwrite the first 64,
 // their second parts, if any, the other 64), O0, O1 (D columns each).
+//
+// What bounds it: with two row tiles the products.  A K/V tile pair of two row tiles
+// (16.8 MFLOP at D = 128) takes 1.82 us, its four products alone 1.47, and at the rate
+// of a large library product (1.88 PFLOP/s over 152 SMs) they would take 1.36; the rest
+// is softmax that the tensor core waits for.  With one row tile the copies bound it.
+// Around that stand about 25 us: start-up 9, uneven ends 5, the join 3 to 7.  Measured,
+// whole calls: 64 sequences on 4k shared tokens 39 us (152 MB, 22 us of HBM time), 9 x 4
+// queries on 32k 73 us (39 GFLOP, 21 us), 256 on 16k 203 us (1.14 GB, 168 us: the
+// tokens behind the prefix).  One thread per row instead of two: 54 us for 64 on 4k.
+// Blocks of 8 tokens take about a quarter longer than blocks of 16 or more (smaller boxes).
 #include "pa_launch.cuh"
 
 #include <cmath>
@@ -194,7 +204,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
   const uint32_t ua = wk.cta_start(cta), ub = wk.cta_start(cta + 1);
   const int first_item = wk.item_of(ua);
-  const bool fine = wk.pairs == 1 && wk.last_weight == 1;  // weights in two parts
+  // Weights in two bf16 parts where one row tile is all: 32 sequences on 8k 31.2 -> 33.2
+  // us; with two row tiles the further products would cost 9x4 queries on 32k 74 -> 87.
+  const bool fine = wk.pairs == 1 && wk.last_weight == 1;
 
   if (warp < kSoftmaxWarps)
     registers_up<kSoftmaxRegisters>();
@@ -261,6 +273,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
         if (lane == 0) mbar_arrive(q_full);
       }
       const int step = two ? 1 : 2;
+      // A warp without a row of the batch only takes part in the barriers: its rows' weights
+      // may be anything, they reach nothing but its rows of O, which nobody reads.
+      // (3 sequences on 8k 21.0 -> 18.8 us, 9x4 queries on 32k 74.4 -> 72.7.)
+      const bool rows_here = row0 + (two ? w * kPrefixRows : 0) + 32 * (warp & 3) < p.rows;
       float m = -INFINITY, l = 0.f;
       bool alive = true;
       for (int x = t0 + (two ? 0 : w); x < t1; x += step) {
@@ -270,6 +286,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
         }
         s_phase ^= 1u;
         tc_fence_after();
+        if (!rows_here) {
+          float none;
+          if (!exchange(0.f, &none)) {
+            alive = false;
+            break;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(w));
+          continue;
+        }
         float s[64];
         tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[0]), s_addr + 64u * half);
         tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[32]), s_addr + 64u * half + 32u);
@@ -374,12 +401,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
         break;
       }
       const size_t at = ((size_t)(cta + item) * 2 + w) * kPrefixRows + row;
-      if (half == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m * p.scale_log2, l + theirs);
+      if (rows_here && half == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m * p.scale_log2, l + theirs);
       if (tid == 0) {
         if (t0 == 0) p.item_ctas[item].x = cta;
         if (t1 == wk.tiles) p.item_ctas[item].y = cta;
       }
-      if (t0 + (two ? 0 : w) < t1) {  // this group had a tile
+      if (rows_here && t0 + (two ? 0 : w) < t1) {  // this group had a tile
         float4* dst = reinterpret_cast<float4*>(p.part_o) + (at - row) * (D / 4) + (D / 8) * half * kPrefixRows + row;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
@@ -902,6 +929,9 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   jp.prefix_tokens = prefix_tokens;
   jp.max_tokens = max_blocks_per_seq * block_size;
   // The fewer the rows, the longer their lists and the more warps there are for each.
+  // One / two / eight warps a row, whole call: 96 rows (3 sequences on 8k) 32.2 / 24.6 /
+  // 21.0 us, 1024 rows 37.2 / 33.3 / 36.7, 2048 rows 38.7 / 39.1 / 48.0, 4096 rows
+  // 39.8 / 42.0 / 61.4.
   const int warps = jp.rows <= 4 * dev.sm_count ? 8 : jp.rows <= 16 * dev.sm_count ? 2 : 1;
   const dim3 grid((unsigned)((jp.rows + 8 / warps - 1) / (8 / warps)));
   cudaError_t e;

@@ -13,7 +13,10 @@
 // sequence whose interval of grow holds i.
 //
 // What bounds it is latency: a step reads and writes a few bytes per sequence
-// and 8 bytes per slot.  So it is one launch: every CTA redoes the three sums
+// and 8 bytes per slot.  Measured on the device: 3.5 us for 64 sequences with a
+// token each (an empty kernel takes 2 to 3), 6.6 for 517 with prompt chunks, 13.5 for
+// 4096 with 0.5 M slots (4.7 MB, 0.7 us of HBM time; 10 us of it are the sums over 4096
+// sequences, which every CTA redoes because waiting for another's costs as much).  So it is one launch: every CTA redoes the three sums
 // over all sequences in shared memory (no CTA waits for another) and then
 // takes its share of each output.  A taken block that was returned in the same
 // step is read from the table row that returned it, so no CTA reads what
