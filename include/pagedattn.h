@@ -313,6 +313,11 @@ size_t pa_decode_mod_workspace_size(int num_seqs, int num_queries, int num_heads
  *              pa_decode_prefix_workspace_size(...) bytes; or NULL: as in
  *              pa_decode_mod
  * Other arguments as in pa_decode_mq.  The call makes up to three launches.
+ *
+ * pa_decode_fp8_prefix - the same over FP8 pools: keys, values and the query's
+ * rounding as in pa_decode_fp8_mq, query and out bf16.  The softmax weights of
+ * the prefix enter its second product rounded to f16 (relative error <= 2^-11
+ * each).  head_size 64 with an odd num_kv_heads is PA_ERR_UNSUPPORTED.
  */
 int pa_decode_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,
                      const int32_t* prefix_table, const int32_t* block_tables,
@@ -322,7 +327,15 @@ int pa_decode_prefix(void* out, const void* query, const void* k_cache, const vo
                      int num_physical_blocks, void* workspace, size_t workspace_bytes,
                      int32_t* error_flag);
 
-/* Scratch bytes pa_decode_prefix needs on the current device (0 for invalid sizes). */
+int pa_decode_fp8_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,
+                         const int32_t* prefix_table, const int32_t* block_tables,
+                         const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
+                         int num_kv_heads, int head_size, int block_size, int num_prefix_blocks,
+                         int max_blocks_per_seq, float scale, float k_scale, float v_scale, void* stream,
+                         int num_physical_blocks, void* workspace, size_t workspace_bytes,
+                         int32_t* error_flag);
+
+/* Scratch bytes pa_decode_prefix or pa_decode_fp8_prefix needs on the current device (0 for invalid sizes). */
 size_t pa_decode_prefix_workspace_size(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
                                        int head_size);
 

@@ -123,6 +123,11 @@ _SIGS = {
         _I,
         [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _I, _I, _P, _SZ, _P],
     ),
+    "pa_decode_fp8_prefix": (
+        _I,
+        [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+         _P, _I, _P, _SZ, _P],
+    ),
     "pa_decode_prefix_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "pa_tables_step": (_I, [_P] * 10 + [_I] * 6 + [_P, _P]),
     "pa_version": (_I, []),
@@ -788,6 +793,17 @@ def pa_decode_prefix(out, query, k_cache, v_cache, prefix_table, block_tables, c
                                    _ptr(error_flag)))
 
 
+def pa_decode_fp8_prefix(out, query, k_cache, v_cache, prefix_table, block_tables, context_lens, num_seqs, num_queries,
+                         num_heads, num_kv_heads, head_size, block_size, num_prefix_blocks, max_blocks_per_seq, scale,
+                         k_scale, v_scale, stream=None, num_physical_blocks=0, workspace=None, workspace_bytes=0,
+                         error_flag=None):
+    _check(load().pa_decode_fp8_prefix(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_table),
+                                       _ptr(block_tables), _ptr(context_lens), num_seqs, num_queries, num_heads,
+                                       num_kv_heads, head_size, block_size, num_prefix_blocks, max_blocks_per_seq,
+                                       scale, k_scale, v_scale, _stream(stream), num_physical_blocks, _ptr(workspace),
+                                       workspace_bytes, _ptr(error_flag)))
+
+
 def pa_decode_prefix_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads, head_size) -> int:
     return int(load().pa_decode_prefix_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads, head_size))
 
@@ -808,4 +824,23 @@ def decode_prefix(query, k_cache, v_cache, prefix_table, block_tables, context_l
     _call_on(index, load().pa_decode_prefix, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), prefix_table.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H,
              Hk, D, bs, prefix_table.numel(), MB, scale, raw, code, NB if check_block_ids else 0, ws, ws_bytes, err)
+    return out
+
+
+def decode_fp8_prefix(query, k_cache, v_cache, prefix_table, block_tables, context_lens, scale, k_scale, v_scale,
+                      out=None, stream=None, *, workspace=None, error_flag=None, check_block_ids=False):
+    """``decode_prefix`` over uint8 E4M3 pools (as in ``pa_decode_fp8_prefix``)."""
+    if query.dtype is not torch.bfloat16:
+        raise ValueError(f"query must be {torch.bfloat16}, got {query.dtype}")
+    index, S, Q, H, D, NB, bs, Hk, MB = _step(query, k_cache, v_cache, block_tables, context_lens, out, torch.uint8)
+    _on(index, torch.int32, "prefix_table", prefix_table)
+    ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
+    raw = _stream_on(stream, index)
+    if out is None:
+        out = torch.empty_like(query)
+        _used_on(stream, out)
+    _call_on(index, load().pa_decode_fp8_prefix, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
+             v_cache.data_ptr(), prefix_table.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H,
+             Hk, D, bs, prefix_table.numel(), MB, scale, k_scale, v_scale, raw, NB if check_block_ids else 0, ws,
+             ws_bytes, err)
     return out

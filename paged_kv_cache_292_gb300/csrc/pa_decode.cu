@@ -501,7 +501,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   }
   if (extras != nullptr)
     return extras->walk == kWalkMod ? launch_mod(prm, pl, dev.device, st, head_size, dtype == PA_F32, kv_fp8)
-                                    : launch_rest(prm, pl, dev.device, st, head_size);
+                                    : launch_rest(prm, pl, dev.device, st, head_size, kv_fp8);
   if (dtype == PA_BF16) {
     return head_size == 64 ? launch_dtype<__nv_bfloat16, 64>(prm, pl, dev.device, st, kv_fp8)
                            : launch_dtype<__nv_bfloat16, 128>(prm, pl, dev.device, st, kv_fp8);

@@ -1449,6 +1449,7 @@ struct MmaConsumerF8 {
   // Output row pairs: acc[mt][0] / [2] are dims dd / dd+1 of column a,
   // [1] / [3] of column b.  Output rows are [seq][query][head]; partial rows
   // are [query][head] (one query: [head]).
+  template <bool REST = false>
   __device__ __forceinline__ void finish(const DecodeParams& p, int seq, int kv_head, int slot,
                                          int r, int lane) {
     float la = l_a, lb = l_b;
@@ -1500,7 +1501,7 @@ struct MmaConsumerF8 {
         }
         const int row = qi * H + kv_head * G + gh;
         const float l = half ? lb : la, m = half ? m_b : m_a;
-        if (slot < 0) {
+        if (!REST && slot < 0) {
           __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + ((size_t)seq * Q * H + row) * D;
           // A query with no keys (several queries, short context) gives zeros.
           const float inv = (!MQ || l > 0.f) ? p.v_scale / l : 0.f;
@@ -1509,12 +1510,14 @@ struct MmaConsumerF8 {
             *reinterpret_cast<uint32_t*>(out + mt * 16 + 2 * g) =
                 pack_bf16x2(acc[mt][half] * inv, acc[mt][2 + half] * inv);
         } else {
-          const size_t base = ((size_t)r * 2 + slot) * Q * H + row;
-          float* po = p.part_o + base * D;
+          const bool whole = REST && slot < 0;
+          const size_t base = (whole ? (size_t)seq : (size_t)r * 2 + slot) * Q * H + row;
+          float* po = (whole ? p.rest_o : p.part_o) + base * D;
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt)
             *reinterpret_cast<float2*>(po + mt * 16 + 2 * g) = make_float2(acc[mt][half], acc[mt][2 + half]);
-          if (g == 0) *reinterpret_cast<float2*>(p.part_ml + base * 2) = make_float2(m, l);
+          if (g == 0)
+            *reinterpret_cast<float2*>((whole ? p.rest_ml : p.part_ml) + base * 2) = make_float2(m, l);
         }
       }
     }

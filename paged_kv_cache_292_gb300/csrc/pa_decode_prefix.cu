@@ -17,8 +17,11 @@
 //                   weights go back there as bf16
 //   warp 16         loads K and V tiles by TMA: boxes of gcd(block_size, 128)
 //                   token rows x 64 elements, into 128-byte swizzled panels
+//                   (FP8 pools: the codes as they are, into a ring of their own)
 //   warp 17         issues the products (tcgen05.mma, one thread): S from Q and K in
 //                   shared memory, O from the weights in tensor memory and V
+//   warps 18, 19    FP8 pools: widen the codes to f16 into the panels; queries and
+//                   weights are f16 then, too (2^-11)
 // With two row tiles each group has one and both use every K/V tile; with a
 // single row tile the groups take alternate K/V tiles and leave a partial
 // each.  While one group exponentiates, the tensor core works for the other.
@@ -50,14 +53,14 @@ constexpr int kPrefixThreads = 640;
 // holds 64 scores, the fifth warpgroup issues copies and products.
 // 4 * 128 * 104 + 128 * 64 = 640 * 96.
 constexpr int kSoftmaxRegisters = 104, kIssueRegisters = 64;
-constexpr int kSoftmaxWarps = 16, kLoadWarp = 16, kProductWarp = 17;
+constexpr int kSoftmaxWarps = 16, kLoadWarp = 16, kProductWarp = 17, kWidenWarp = 18, kWidenWarps = 2;
 constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
 // A running maximum is kept until a tile exceeds it by this factor (log2): until
 // then weights are at most 2^8, which bf16 and the fp32 sums hold as well as 1.
 constexpr float kSlack = 8.f;
 
 struct PrefixParams {
-  CUtensorMap tm_k, tm_v;  // (64 elements, chunk of 64 within a token row, token row)
+  CUtensorMap tm_k, tm_v;  // (64 elements, chunk of 64 within a token row, token row); FP8: (D, KV head, token row)
   const __nv_bfloat16* q;
   const int32_t* table;
   int32_t* error_flag;
@@ -86,15 +89,18 @@ __host__ __device__ __forceinline__ float prefix_cost(const PrefixWork& w) {
   return static_cast<float>(w.total()) + 5.f * (w.items() + 0.25f * w.ctas);
 }
 
-template <int D>
+template <int D, bool F8>
 struct PrefixLayout {
   static constexpr int kPanels = D / 64;
   static constexpr uint32_t kTileBytes = kPanels * kPanel;  // a Q, K or V tile
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 64 ? 8 : F8 ? 3 : 5;
+  static constexpr int kRawStages = F8 ? (D == 64 ? 8 : 4) : 0;  // tiles of codes
+  static constexpr uint32_t kRawBytes = kTileBytes / 2;
   static constexpr uint32_t kExchange = 1024;  // [2 groups][2 halves][128] floats; barriers before it
   static constexpr uint32_t kQ = 3 * 1024;
   static constexpr uint32_t kRing = kQ + 2 * kTileBytes;
-  static constexpr uint32_t kBytes = kRing + kStages * kTileBytes;
+  static constexpr uint32_t kRaw = kRing + kStages * kTileBytes;
+  static constexpr uint32_t kBytes = kRaw + kRawStages * kRawBytes;
 };
 
 // mbar_wait that also gives up when another warp has.
@@ -131,10 +137,10 @@ struct Ring {
   }
 };
 
-template <int D>
+template <int D, bool F8>
 __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __grid_constant__ PrefixParams p) {
-  using L = PrefixLayout<D>;
-  constexpr int NS = L::kStages;
+  using L = PrefixLayout<D, F8>;
+  constexpr int NS = L::kStages, NR = L::kRawStages;
   extern __shared__ __align__(1024) unsigned char smem[];  // swizzled panels start on 1 KiB boundaries
   const uint32_t base = smem_addr(smem);
   if ((base & 1023u) != 0) {  // cannot be: the array asks for it
@@ -151,6 +157,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   auto o_full = [&](int w) { return bars + 8u * (2 * NS + 5 + w); };
   const uint32_t drained = bars + 8u * (2 * NS + 7);
   auto exchanged = [&](int w) { return bars + 8u * (2 * NS + 8 + w); };
+  auto raw_full = [&](int i) { return bars + 8u * (2 * NS + 10 + i); };
+  auto raw_empty = [&](int i) { return bars + 8u * (2 * NS + 10 + NR + i); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 512);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + 516);
   auto timed_out = [&]() {
@@ -183,8 +191,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   if (cta >= wk.ctas) return;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full(i), 1);
+      mbar_init(full(i), F8 ? kWidenWarps : 1);
       mbar_init(empty(i), 1);
+    }
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(raw_full(i), 1);
+      mbar_init(raw_empty(i), kWidenWarps);
     }
     mbar_init(q_full, kSoftmaxWarps);
     for (int w = 0; w < 2; ++w) {
@@ -206,7 +218,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   const int first_item = wk.item_of(ua);
   // Weights in two bf16 parts where one row tile is all: 32 sequences on 8k 31.2 -> 33.2
   // us; with two row tiles the further products would cost 9x4 queries on 32k 74 -> 87.
-  const bool fine = wk.pairs == 1 && wk.last_weight == 1;
+  const bool fine = !F8 && wk.pairs == 1 && wk.last_weight == 1;
 
   if (warp < kSoftmaxWarps)
     registers_up<kSoftmaxRegisters>();
@@ -264,6 +276,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
             v[i].y = (v[i].y & p.q_keep) ^ p.q_flip;
             v[i].z = (v[i].z & p.q_keep) ^ p.q_flip;
             v[i].w = (v[i].w & p.q_keep) ^ p.q_flip;
+            if constexpr (F8) {
+              v[i].x = pack_f16x2(bf16_lo(v[i].x), bf16_hi(v[i].x));
+              v[i].y = pack_f16x2(bf16_lo(v[i].y), bf16_hi(v[i].y));
+              v[i].z = pack_f16x2(bf16_lo(v[i].z), bf16_hi(v[i].z));
+              v[i].w = pack_f16x2(bf16_lo(v[i].w), bf16_hi(v[i].w));
+            }
             *reinterpret_cast<uint4*>(dst + (u >> 3) * kPanel + (((u & 7) ^ (row & 7)) << 4)) = v[i];
           }
         }
@@ -355,7 +373,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
           s[e] = ex2_ftz(a);
           s[e + 1] = ex2_ftz(b);
           sum[i & 1] = add_pair(sum[i & 1], pair(s[e], s[e + 1]));
-          return pack_bf16x2(s[e], s[e + 1]);
+          return F8 ? pack_f16x2(s[e], s[e + 1]) : pack_bf16x2(s[e], s[e + 1]);
         };
         if (!fine) {
 #pragma unroll
@@ -426,10 +444,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
       prefetch_tensormap(&p.tm_k);
       prefetch_tensormap(&p.tm_v);
     }
+    // Stages the copies land in: panels, or the codes of FP8 pools.
+    constexpr int kCopyStages = F8 ? NR : NS, kBoxPanels = F8 ? 1 : L::kPanels;
+    constexpr uint32_t kCopyBytes = F8 ? L::kRawBytes : L::kTileBytes, kCopyRing = F8 ? L::kRaw : L::kRing;
+    auto landed = [&](int i) { return F8 ? raw_full(i) : full(i); };
+    auto taken = [&](int i) { return F8 ? raw_empty(i) : empty(i); };
     const int boxes = kPrefixTokens / p.box_rows;
-    const int box = lane / L::kPanels, panel = lane % L::kPanels;
+    const int box = lane / kBoxPanels, panel = lane % kBoxPanels;
     const bool mine = box < boxes;
-    const uint32_t dst0 = panel * kPanel + box * p.box_rows * 128u;
+    const uint32_t dst0 = panel * kPanel + box * p.box_rows * (F8 ? (uint32_t)D : 128u);
     Ring ring;
     uint32_t armed = 0, armed_phase = 0;  // stages armed, with the parity of their last phase
     bool alive = true;
@@ -449,21 +472,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
         return phys * p.block_size + (tok - blk * p.block_size);
       };
       auto load = [&](const void* tmap, int row, bool withhold) -> bool {
-        if (!wait_or_abort(empty(ring.i), ring.phase ^ 1u, p.wait_limit_ns, abort_flag)) {
+        if (!wait_or_abort(taken(ring.i), ring.phase ^ 1u, p.wait_limit_ns, abort_flag)) {
           timed_out();
           return false;
         }
         if (!withhold) {
-          if (lane == 0) mbar_arrive_expect_tx(full(ring.i), L::kTileBytes);
+          if (lane == 0) mbar_arrive_expect_tx(landed(ring.i), kCopyBytes);
           __syncwarp();
           // A chunk beyond the row's last is outside the tensor: zeros, without a read.
           if (mine)
-            tma_load_3d(base + L::kRing + ring.i * L::kTileBytes + dst0, tmap, 0,
-                        (row < 0 ? wk.kv_heads : head) * L::kPanels + panel, row < 0 ? 0 : row, full(ring.i));
+            tma_load_3d(base + kCopyRing + ring.i * kCopyBytes + dst0, tmap, 0,
+                        (row < 0 ? wk.kv_heads : head) * kBoxPanels + panel, row < 0 ? 0 : row, landed(ring.i));
           armed |= 1u << ring.i;
           armed_phase = (armed_phase & ~(1u << ring.i)) | (ring.phase << ring.i);
         }
-        ring.next(NS);
+        ring.next(kCopyStages);
         return true;
       };
       const int ahead = wk.weight(item) == 2 ? 1 : 2;  // K tiles ahead of the V tile
@@ -485,12 +508,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
     if (*abort_flag != 0) {
       // Copies that were started may still be landing: wait for them (again
       // bounded) before the CTA's shared memory goes.
-      for (int i = 0; i < NS; ++i)
-        if ((armed >> i) & 1u) (void)mbar_wait(full(i), (armed_phase >> i) & 1u, p.wait_limit_ns);
+      for (int i = 0; i < kCopyStages; ++i)
+        if ((armed >> i) & 1u) (void)mbar_wait(landed(i), (armed_phase >> i) & 1u, p.wait_limit_ns);
     }
   } else if (warp == kProductWarp) {
     // ---------------- products ----------------
-    constexpr uint32_t kScores = bf16_product(128, 128, false), kValues = bf16_product(128, D, true);
+    constexpr uint32_t kScores = product(!F8, 128, 128, false), kValues = product(!F8, 128, D, true);
     Ring ring;
     uint32_t q_phase = 0, p_phase[2] = {0u, 0u};
     bool alive = true;
@@ -586,8 +609,47 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
     tc_fence_after();
     tmem_free(tmem, 512);
     return;
+  } else if (F8) {
+    // ---------------- codes to f16 ----------------
+    // Tiles come in the order of the copies and leave in that of the products,
+    // which is the same.  A thread takes 8 codes, a 16-byte unit of a panel row; units
+    // of a row lie side by side in a warp, so neither side has bank conflicts.
+    constexpr int kThreads = 32 * kWidenWarps, kUnits = D / 8, kSteps = kPrefixTokens * kUnits / kThreads;
+    const int t = (warp - kWidenWarp) * 32 + lane, row0 = t / kUnits, unit = t % kUnits;
+    Ring ring, raw;
+    bool alive = true;
+    for (int item = first_item; alive && item < wk.items() && wk.item_start(item) < ub; ++item) {
+      const int tiles = 2 * (wk.tile_at(item, ub) - wk.tile_at(item, ua));  // K and V
+      for (int x = 0; x < tiles; ++x) {
+        alive = wait_or_abort(raw_full(raw.i), raw.phase, p.wait_limit_ns, abort_flag) &&
+                wait_or_abort(empty(ring.i), ring.phase ^ 1u, p.wait_limit_ns, abort_flag);
+        if (!alive) {
+          timed_out();
+          break;
+        }
+        const unsigned char* src = smem + L::kRaw + raw.i * L::kRawBytes + 8 * t;
+        unsigned char* dst = smem + L::kRing + ring.i * L::kTileBytes + (unit >> 3) * kPanel + row0 * 128;
+#pragma unroll 8
+        for (int i = 0; i < kSteps; ++i) {
+          const int r = i * (kThreads / kUnits);  // rows from row0
+          const uint2 codes = *reinterpret_cast<const uint2*>(src + 8 * kThreads * i);
+          uint4 v;
+          e4m3x4_to_f16x2x2(codes.x, v.x, v.y);
+          e4m3x4_to_f16x2x2(codes.y, v.z, v.w);
+          *reinterpret_cast<uint4*>(dst + r * 128 + (((unit & 7) ^ ((row0 + r) & 7)) << 4)) = v;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full(ring.i));
+          mbar_arrive(raw_empty(raw.i));
+        }
+        ring.next(NS);
+        raw.next(NR);
+      }
+    }
   }
-  if (warp < kSoftmaxWarps || warp > kProductWarp) {  // (the last two warps only fill their warpgroup)
+  if (warp < kSoftmaxWarps || warp > kProductWarp) {  // (bf16: the last two warps only fill their warpgroup)
     tc_fence_before();
     named_barrier_sync(1, kPrefixThreads);
   }
@@ -614,6 +676,7 @@ struct JoinParams {
   PrefixWork work;
   int rows;  // num_seqs * num_queries * num_heads
   int num_queries, num_heads, group, prefix_tokens, max_tokens;
+  float v_scale;
 };
 
 template <int D, int kWarps>
@@ -724,7 +787,7 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
     }
   }
   if (lane < kLanes) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : p.v_scale / l;
     *reinterpret_cast<uint2*>(p.out + (size_t)row * D + 4 * lane) =
         make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   }
@@ -769,32 +832,42 @@ int count_items(int num_seqs, int num_queries, int num_heads, int num_kv_heads) 
 }
 
 // The pools' tensor maps, encoded for every call (about 0.1 us each).
-int make_maps(PrefixParams* prm, const void* k, const void* v, uint64_t pool_rows, int num_kv_heads, int head_size) {
+int make_maps(PrefixParams* prm, const void* k, const void* v, uint64_t pool_rows, int num_kv_heads, int head_size,
+              bool kv_fp8) {
   const EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return fail(PA_ERR_CUDA, "pa_decode_prefix: the driver has no cuTensorMapEncodeTiled");
   const cuuint64_t row = (cuuint64_t)num_kv_heads * head_size;
-  const cuuint64_t dims[3] = {64, row / 64, pool_rows}, strides[2] = {128, row * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)prm->box_rows}, estride[3] = {1, 1, 1};
+  const cuuint64_t chunk = kv_fp8 ? head_size : 64, elt = kv_fp8 ? 1 : 2;
+  const cuuint64_t dims[3] = {chunk, row / chunk, pool_rows}, strides[2] = {chunk * elt, row * elt};
+  const cuuint32_t box[3] = {(cuuint32_t)chunk, 1, (cuuint32_t)prm->box_rows}, estride[3] = {1, 1, 1};
   for (int i = 0; i < 2; ++i) {
-    const CUresult r = enc(i ? &prm->tm_v : &prm->tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+    const CUresult r = enc(i ? &prm->tm_v : &prm->tm_k,
+                           kv_fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                            const_cast<void*>(i ? v : k), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           kv_fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
       return fail(PA_ERR_CUDA, "pa_decode_prefix: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
   }
   return PA_OK;
 }
 
-template <int D>
+template <int D, bool F8>
 int launch_prefix(const PrefixParams& prm, int device, cudaStream_t stream) {
   static RaisedDevices raised;
-  const int rc = raise_smem_limit(reinterpret_cast<const void*>(pa_prefix_kernel<D>), PrefixLayout<D>::kBytes, device,
-                                  &raised);
+  constexpr int kBytes = PrefixLayout<D, F8>::kBytes;
+  const int rc = raise_smem_limit(reinterpret_cast<const void*>(pa_prefix_kernel<D, F8>), kBytes, device, &raised);
   if (rc != PA_OK) return rc;
-  const cudaError_t e = launch_pdl(pa_prefix_kernel<D>, dim3(prm.work.ctas), dim3(kPrefixThreads),
-                                   PrefixLayout<D>::kBytes, stream, prm);
+  const cudaError_t e =
+      launch_pdl(pa_prefix_kernel<D, F8>, dim3(prm.work.ctas), dim3(kPrefixThreads), kBytes, stream, prm);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefix_kernel");
+}
+
+// Scratch of the walk behind the prefix, whatever the pool's type.
+size_t rest_bytes(int num_seqs, int num_queries, int num_heads, int num_kv_heads, int head_size) {
+  const size_t bf16 = walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 2);
+  const size_t fp8 = walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 1);
+  return bf16 > fp8 ? bf16 : fp8;
 }
 
 }  // namespace
@@ -803,40 +876,41 @@ int launch_prefix(const PrefixParams& prm, int device, cudaStream_t stream) {
 extern "C" size_t pa_decode_prefix_workspace_size(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
                                                   int head_size) {
   using namespace pa;
-  const size_t walk = walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 2);
+  const size_t walk = rest_bytes(num_seqs, num_queries, num_heads, num_kv_heads, head_size);
   DeviceInfo dev{};
   if (walk == 0 || current_device_info(&dev) != PA_OK) return 0;
   const int items = count_items(num_seqs, num_queries, num_heads, num_kv_heads);
   return prefix_scratch(num_seqs, num_queries, num_heads, head_size, dev.sm_count + items, items, walk).total;
 }
 
-extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,
-                                const int32_t* prefix_table, const int32_t* block_tables,
-                                const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
-                                int num_kv_heads, int head_size, int block_size, int num_prefix_blocks,
-                                int max_blocks_per_seq, float scale, void* stream, int dtype,
-                                int num_physical_blocks, void* workspace, size_t workspace_bytes,
-                                int32_t* error_flag) {
-  using namespace pa;
-  clear_error();
+namespace pa {
+namespace {
+
+int prefix_impl(void* out, const void* query, const void* k_cache, const void* v_cache, const int32_t* prefix_table,
+                const int32_t* block_tables, const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
+                int num_kv_heads, int head_size, int block_size, int num_prefix_blocks, int max_blocks_per_seq,
+                float scale, void* stream, int num_physical_blocks, void* workspace, size_t workspace_bytes,
+                int32_t* error_flag, bool kv_fp8, float k_scale, float v_scale) {
   if (num_prefix_blocks < 0 || (num_prefix_blocks > 0 && prefix_table == nullptr))
     return fail(PA_ERR_INVALID_ARG, "pa_decode_prefix: %d prefix blocks without a table", num_prefix_blocks);
   if (num_prefix_blocks > max_blocks_per_seq)
     return fail(PA_ERR_INVALID_ARG, "pa_decode_prefix: prefix of %d blocks in tables of %d", num_prefix_blocks,
                 max_blocks_per_seq);
   if (!aligned(prefix_table, 4)) return fail(PA_ERR_INVALID_ARG, "pa_decode_prefix: misaligned prefix_table");
-  if (dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: bf16 only");
   if (block_size > 0 && block_size % 8 != 0)
     return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: block_size %d is not a multiple of 8", block_size);
   int rc = decode_validate(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries,
-                           num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, dtype,
+                           num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, PA_BF16,
                            num_physical_blocks);
   if (rc != PA_OK) return rc;
+  if (kv_fp8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale <= 0.f || v_scale <= 0.f))
+    return fail(PA_ERR_INVALID_ARG, "pa_decode_fp8_prefix: scales must be finite and positive");
+  if (kv_fp8 && num_kv_heads * head_size % 128 != 0)  // as every decode over FP8 pools
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_fp8_prefix: head_size 64 needs an even number of KV heads");
   DeviceInfo dev{};
   rc = current_device_info(&dev);
   if (rc != PA_OK) return rc;
-  const size_t walk_bytes =
-      walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 2);
+  const size_t walk_bytes = rest_bytes(num_seqs, num_queries, num_heads, num_kv_heads, head_size);
   const int64_t rows = (int64_t)num_seqs * num_queries * (num_heads / num_kv_heads);
   if (rows * num_kv_heads > 1 << 30)
     return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %lld output rows", (long long)(rows * num_kv_heads));
@@ -866,7 +940,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
                   (unsigned long long)pool_rows);
     prm.box_rows = block_size & -block_size;
     if (prm.box_rows > kPrefixTokens) prm.box_rows = kPrefixTokens;
-    rc = make_maps(&prm, k_cache, v_cache, pool_rows, num_kv_heads, head_size);
+    rc = make_maps(&prm, k_cache, v_cache, pool_rows, num_kv_heads, head_size, kv_fp8);
     if (rc != PA_OK) return rc;
     prm.q = static_cast<const __nv_bfloat16*>(query);
     prm.table = prefix_table;
@@ -877,7 +951,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
     if (prm.work.ctas == 0)
       return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %lld query rows over %d prefix tokens", (long long)rows,
                   prefix_tokens);
-    const WalkShape shape = walk_shape(num_heads, num_kv_heads, head_size, num_queries, 2);
+    const WalkShape shape = walk_shape(num_heads, num_kv_heads, head_size, num_queries, kv_fp8 ? 1 : 2);
     prm.item_ctas = reinterpret_cast<int2*>(ws + sc.item_ctas);
     prm.context_lens = context_lens;
     prm.num_seqs = num_seqs;
@@ -892,11 +966,15 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
     prm.block_size = block_size;
     prm.prefix_tokens = prefix_tokens;
     prm.num_physical_blocks = num_physical_blocks;
-    prm.scale_log2 = scale != 0.f ? (float)(std::fabs((double)scale) * 1.4426950408889634) : 1.f;
+    prm.scale_log2 = scale != 0.f ? (float)(std::fabs((double)scale) * k_scale * 1.4426950408889634) : 1.f;
     prm.q_keep = scale != 0.f ? 0xffffffffu : 0u;
     prm.q_flip = scale < 0.f ? 0x80008000u : 0u;
     take_wait_test(&prm.stall_tile, &prm.wait_limit_ns);
-    rc = head_size == 64 ? launch_prefix<64>(prm, dev.device, st) : launch_prefix<128>(prm, dev.device, st);
+    if (kv_fp8)
+      rc = head_size == 64 ? launch_prefix<64, true>(prm, dev.device, st) : launch_prefix<128, true>(prm, dev.device, st);
+    else
+      rc = head_size == 64 ? launch_prefix<64, false>(prm, dev.device, st)
+                           : launch_prefix<128, false>(prm, dev.device, st);
     if (rc != PA_OK) return rc;
   }
   DecodeExtras ex{};
@@ -906,9 +984,9 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   ex.rest_o = reinterpret_cast<float*>(ws + sc.rest_o);
   ex.prefix_units = num_prefix_blocks > 0 ? prefix_cost(prm.work) : 0.f;
   rc = decode_impl_q(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_queries, num_heads,
-                     num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, stream, dtype,
-                     num_physical_blocks, ws + sc.walk, walk_bytes, 0, error_flag, false, 1.f, 1.f, nullptr, nullptr,
-                     nullptr, &ex);
+                     num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, stream, PA_BF16,
+                     num_physical_blocks, ws + sc.walk, walk_bytes, 0, error_flag, kv_fp8, k_scale, v_scale, nullptr,
+                     nullptr, nullptr, &ex);
   if (rc != PA_OK) return rc;
   JoinParams jp{};
   jp.out = static_cast<__nv_bfloat16*>(out);
@@ -928,6 +1006,7 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
   jp.group = group;
   jp.prefix_tokens = prefix_tokens;
   jp.max_tokens = max_blocks_per_seq * block_size;
+  jp.v_scale = v_scale;
   // The fewer the rows, the longer their lists and the more warps there are for each.
   // One / two / eight warps a row, whole call: 96 rows (3 sequences on 8k) 32.2 / 24.6 /
   // 21.0 us, 1024 rows 37.2 / 33.3 / 36.7, 2048 rows 38.7 / 39.1 / 48.0, 4096 rows
@@ -944,4 +1023,36 @@ extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cach
         : warps == 2 ? launch_pdl(pa_prefix_join<128, 2>, grid, dim3(256), 0, st, jp)
                      : launch_pdl(pa_prefix_join<128, 1>, grid, dim3(256), 0, st, jp);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefix_join");
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" int pa_decode_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,
+                                const int32_t* prefix_table, const int32_t* block_tables,
+                                const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
+                                int num_kv_heads, int head_size, int block_size, int num_prefix_blocks,
+                                int max_blocks_per_seq, float scale, void* stream, int dtype,
+                                int num_physical_blocks, void* workspace, size_t workspace_bytes,
+                                int32_t* error_flag) {
+  pa::clear_error();
+  if (dtype != PA_BF16) return pa::fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: bf16 only (FP8: pa_decode_fp8_prefix)");
+  return pa::prefix_impl(out, query, k_cache, v_cache, prefix_table, block_tables, context_lens, num_seqs,
+                         num_queries, num_heads, num_kv_heads, head_size, block_size, num_prefix_blocks,
+                         max_blocks_per_seq, scale, stream, num_physical_blocks, workspace, workspace_bytes, error_flag,
+                         false, 1.f, 1.f);
+}
+
+extern "C" int pa_decode_fp8_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,
+                                    const int32_t* prefix_table, const int32_t* block_tables,
+                                    const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
+                                    int num_kv_heads, int head_size, int block_size, int num_prefix_blocks,
+                                    int max_blocks_per_seq, float scale, float k_scale, float v_scale, void* stream,
+                                    int num_physical_blocks, void* workspace, size_t workspace_bytes,
+                                    int32_t* error_flag) {
+  pa::clear_error();
+  return pa::prefix_impl(out, query, k_cache, v_cache, prefix_table, block_tables, context_lens, num_seqs,
+                         num_queries, num_heads, num_kv_heads, head_size, block_size, num_prefix_blocks,
+                         max_blocks_per_seq, scale, stream, num_physical_blocks, workspace, workspace_bytes, error_flag,
+                         true, k_scale, v_scale);
 }

@@ -69,6 +69,6 @@ EncodeTiledFn encode_tiled_fn();
 // The kernel variants of the other translation units.
 int launch_mod(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool f32,
                bool kv_fp8);
-int launch_rest(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size);
+int launch_rest(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool kv_fp8);
 
 }  // namespace pa

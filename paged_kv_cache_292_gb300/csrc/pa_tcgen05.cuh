@@ -86,29 +86,29 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t panel) 
          (1ull << 46) | (2ull << 61);
 }
 
-// bf16 x bf16 -> fp32, A K-major, M x N.
-__host__ __device__ constexpr uint32_t bf16_product(int m, int n, bool b_mn_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+// bf16 x bf16 (or f16 x f16) -> fp32, A K-major, M x N.
+__host__ __device__ constexpr uint32_t product(bool bf16, int m, int n, bool b_mn_major) {
+  return (1u << 4) | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
 }
 
 // D[tmem] (+)= A[smem] * B[smem], 16 elements of K.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t product, bool accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(product), "r"((uint32_t)accumulate)
+      "l"(a), "l"(b), "r"(what), "r"((uint32_t)accumulate)
       : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem].
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t product, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(product), "r"((uint32_t)accumulate)
+      "r"(a), "l"(b), "r"(what), "r"((uint32_t)accumulate)
       : "memory");
 }
 

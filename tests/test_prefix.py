@@ -76,3 +76,28 @@ def test_work_decomposition_host_check(tmp_path):
     out = subprocess.run([str(exe)], capture_output=True, text=True)
     assert out.returncode == 0, out.stdout + out.stderr
     assert out.stdout.startswith("ok")
+
+
+def _fp8_args(**kw):
+    a = dict(zip(("out query k_cache v_cache prefix_table block_tables context_lens num_seqs num_queries num_heads "
+                  "num_kv_heads head_size block_size num_prefix_blocks max_blocks_per_seq scale").split(), _args()))
+    a.update(k_scale=0.5, v_scale=2.0, stream=0, num_physical_blocks=0, workspace=None, workspace_bytes=0,
+             error_flag=None)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw, code", [
+    *[({name: None}, INVALID) for name in ("out", "query", "k_cache", "v_cache", "prefix_table", "block_tables",
+                                           "context_lens")],
+    *[({name: bad}, INVALID) for name in ("k_scale", "v_scale") for bad in (0.0, -1.0, float("nan"), float("inf"))],
+    (dict(num_prefix_blocks=5), INVALID),
+    (dict(block_size=12), UNSUPPORTED),
+    (dict(num_queries=33), UNSUPPORTED),
+    (dict(num_heads=3, num_kv_heads=3, head_size=64), UNSUPPORTED),
+    (dict(head_size=96), UNSUPPORTED),
+    (dict(k_cache=24), INVALID),
+])
+def test_fp8_rejects_bad_arguments_on_host(lib, kw, code):
+    assert lib.pa_decode_fp8_prefix(*_fp8_args(**kw)) == code
+    assert lib.pa_last_error().decode()
