@@ -250,13 +250,16 @@ struct SeqWalk {
 // SMs for the prefix kernel of `units` units (pa_prefix_work.h) beside a walk of
 // `tiles` tiles by `groups` CTAs each, in proportion to the SM time of either: a
 // unit takes about 0.9 us (D = 128: 128 x 128 x 128 x 4 flops; D = 64: 0.78, where the
-// softmax sets the pace), a tile about 0.35
-// us + 0.18 us per KiB of K row, or 0.8 us with more than 8 columns per KV head, and a
-// sequence another 0.8 us (its queries, its row).  The walk is bound by HBM from about 80 SMs on.
+// softmax sets the pace), a tile about 0.35 us + 0.18 us per KiB of K row, or 0.8 us with
+// more than 8 columns per KV head, and a sequence another 0.8 us per 4096 elements of
+// its query and output rows (0.8 to 2.4).  The walk is bound by HBM from about 80 SMs on.
+//   256 sequences of 64 heads with a tile each behind 32k tokens: 253 us, with 0.8 us
+// for any sequence 359 (the walk came last); of 32 heads on 16k: 83, with 1.6 us 86.
 __device__ __forceinline__ int prefix_share(float units, long long tiles, int seqs, int groups, float tile_us,
-                                            int head_size, int sm_count) {
+                                            int row_elements, int head_size, int sm_count) {
   if (tiles == 0) return sm_count;
-  const float a = units * (head_size == 128 ? 0.9f : 0.78f), b = (tiles * tile_us + seqs * 0.8f) * groups;
+  const float seq_us = 0.8f * fminf(fmaxf(row_elements * (1.f / 4096.f), 1.f), 3.f);
+  const float a = units * (head_size == 128 ? 0.9f : 0.78f), b = (tiles * tile_us + seqs * seq_us) * groups;
   // The walk's part in whole ranges (one CTA per group of KV heads each).
   const int walk = (__float2int_ru(sm_count * (b / (a + b))) + groups - 1) / groups * groups;
   return max(1, sm_count - max(walk, groups));
@@ -2380,8 +2383,9 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
   if constexpr (WALK == kWalkRest) {
     // The SMs the prefix kernel leaves.
     if (p.beside) {
-      const int left = p.sm_count - prefix_share(p.prefix_units, total, S, HG, walk_tile_us(p.row_bytes, p.group * p.num_queries), D,
-                                                  p.sm_count);
+      const int left = p.sm_count - prefix_share(p.prefix_units, total, S, HG,
+                                                 walk_tile_us(p.row_bytes, p.group * p.num_queries),
+                                                 p.num_queries * p.num_heads * D, D, p.sm_count);
       const long long most = static_cast<long long>(left) * R / p.sm_count;
       Reff = min(Reff, max(most, 1ll));
     }

@@ -173,3 +173,31 @@ def test_python_layer_refuses_mismatched_arguments():
                 (q, k, v, prefix.cpu(), tables, lens)):
         with pytest.raises(ValueError):
             binding.decode_fp8_prefix(*bad, scale, b.ks, VS)
+
+
+@pytest.mark.parametrize("D, S", [(64, 5), (128, 70)])
+def test_every_code(D, S):
+    """All finite codes in K and V, subnormal ones among them, and pools of subnormal codes alone."""
+    for codes in (np.setdiff1d(np.arange(256), (0x7F, 0xFF)), np.r_[0:8, 0x80:0x88]):
+        b = Batch(20, [3 + s % 40 for s in range(S)], 1, 8, 2, D, seed=7)
+        rng = np.random.default_rng(9)
+        for x in (b.k, b.v):
+            real = x.numpy() != 0x7F
+            x.numpy()[real] = rng.choice(codes, int(real.sum()))
+        b.ks, b.scale = (0.0005, 0.1) if len(codes) > 16 else (2.0, 1.0)
+        b.check("codes")
+
+
+def test_nan_codes_stay_nan():
+    """A NaN in a token that is seen reaches the rows that see it: a V entry its dimension, a K row all of them."""
+    for D in (64, 128):
+        b = Batch(20, [3, 50, -300], 1, 8, 2, D)
+        out = b.check("clean")
+        b.v[int(b.prefix[13]), 5, 1, 9] = 0x7F
+        got = b.call(b.gpu())
+        hit = torch.zeros_like(got, dtype=torch.bool)
+        hit[:2, 4:, 9] = True
+        assert torch.equal(torch.isnan(got), hit) and torch.equal(got[~hit], out[~hit])
+        b.k[int(b.prefix[2]), 0, 0, 3] = 0xFF
+        got = b.call(b.gpu())
+        assert torch.isnan(got[:2, :4]).all() and not torch.isnan(got[2]).any()
