@@ -201,3 +201,17 @@ def test_nan_codes_stay_nan():
         b.k[int(b.prefix[2]), 0, 0, 3] = 0xFF
         got = b.call(b.gpu())
         assert torch.isnan(got[:2, :4]).all() and not torch.isnan(got[2]).any()
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls of both pool types overlap, each stream with scratch of its own."""
+    b, plain = Batch(40, np.arange(60) % 30 + 1, 1, 8, 2, 128), bf16.Batch(30, [5, 60], 4, 16, 2, 64)
+    args, other = b.gpu(), plain.gpu()
+    want, want_plain = b.call(args), binding.decode_prefix(*other)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [(b.call(args, stream=streams[i % 2]), binding.decode_prefix(*other, stream=streams[1 - i % 2]))
+           for i in range(12)]
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert torch.equal(x, want) and torch.equal(y, want_plain)
