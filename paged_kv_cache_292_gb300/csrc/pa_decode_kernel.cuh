@@ -2551,18 +2551,16 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
       const int flags = (new_seq ? kSegBegin : 0) | ((x == b - 1 || j == ns - 1) ? kSegEnd : 0) |
                         ((slot + 1) << 2) | (seg_slot0 << 4);
       const bool mine = static_cast<int>((x - a) % (WALK == kWalkAll ? kProducers : producers)) == pw;
-      // With one query slot every producer waits for it at every sequence, not only
-      // the one that fills it: a producer that skipped a sequence could be two
-      // phases ahead of the slot's barrier at the next one, where the parity of
-      // an older phase looks like the one it waits for.  (With two slots it is at
-      // most one phase ahead on either.)
-      if (new_seq && (mine || NQ == 1)) {
+      // One producer fills all query slots, whoever takes the sequence's first tile:
+      // it sees every phase of a slot's barrier, so that the parity it waits for is
+      // never an older or a later phase's.  (Had the owner of the first tile filled it, a
+      // producer that skipped sequences of few tiles could be two phases ahead at its
+      // next own one; one that waited without filling could come a phase too late.)
+      if (new_seq && pw == 0) {
         if (!mbar_wait_warp(qempty_bar(qi), qph ^ 1u, p.wait_limit_ns)) {
           timed_out();
           break;
         }
-      }
-      if (new_seq && mine) {
         if (lane == 0) {
           const uint32_t qb = qfull_bar(qi);
           mbar_arrive_expect_tx(qb, p.q_bytes);
