@@ -93,10 +93,13 @@ size_t workspace_layout(int num_seqs, int num_heads, int num_kv_heads, int head_
 
 // KV heads one CTA stages per token row: the largest divisor of num_kv_heads
 // that is at most `max_heads` (8 with one consumer warp per KV head, 4 with
-// two) and keeps the row within 2 KiB, so three stages fit in shared memory.
+// two), keeps the row within 2 KiB, so three stages fit in shared memory, and
+// makes it whole 128-byte lines (FP8 pools of 64 dims: an even number of heads).
 int heads_per_cta(int num_kv_heads, int head_size, int elt, int max_heads = kMaxGroupHeads) {
-  for (int h = max_heads; h > 1; --h)
-    if (num_kv_heads % h == 0 && h * head_size * elt <= kMaxRowBytes) return h;
+  for (int h = max_heads; h > 1; --h) {
+    const int row = h * head_size * elt;
+    if (num_kv_heads % h == 0 && row <= kMaxRowBytes && row % (int)kLine == 0) return h;
+  }
   return 1;
 }
 
