@@ -69,6 +69,39 @@ EncodeTiledFn encode_tiled_fn() {
   return fn;
 }
 
+// A tensor map that goes on where the memory ends is not safe even if every box lies in
+// the pool: random multi-query calls over maps of 2^31 rows, kept from call to call by
+// the pools' addresses, ended with an illegal address about once in 2000, with maps that
+// end with the pools none of 86000 did.
+uint64_t rows_of_pools(const void* k, const void* v, uint64_t row_bytes) {
+  static const PFN_cuPointerGetAttributes_v7000 attributes_of = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &f, 7000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<PFN_cuPointerGetAttributes_v7000>(f);
+  }();
+  uint64_t rows = 1ull << 31;
+  for (const void* p : {k, v}) {
+    CUdeviceptr start = 0;
+    size_t size = 0;
+    CUpointer_attribute what[2] = {CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+    void* out[2] = {&start, &size};
+    const CUdeviceptr at = reinterpret_cast<CUdeviceptr>(p);
+    if (attributes_of == nullptr || attributes_of(2, what, out, at) != CUDA_SUCCESS) size = 0;
+    const uint64_t mine = rows_behind(start, size, at, row_bytes);
+    if (mine == 0) {
+      fail(PA_ERR_INVALID_ARG, "pa_decode: the driver does not know the pools' memory; num_physical_blocks is needed");
+      return 0;
+    }
+    if (mine < rows) rows = mine;
+  }
+  return rows;
+}
+
 namespace {
 
 // Scratch layout: partial (m, l) and O at the start, then the merge tickets
@@ -236,49 +269,23 @@ int validate(const void* out, const void* query, const void* k_cache, const void
 // 128-byte chunk, chunk within a head group's row, head group, token row)
 // with strides (1, 128, group row bytes, token row bytes).  A box is
 // (128, lines, 1, box_rows); its lines past the group's row are outside the
-// tensor, so they arrive zero-filled without touching memory.
-//
-// Encoded maps of the last few pools this thread decoded over.  A map is a
-// pure function of the pool's address, extents, strides and box, which form
-// the key, so a hit is exactly what a fresh encode would give; repeated
-// steps over the same pools skip the driver call.
-struct TensorMapCacheEntry {
-  const void* k;
-  const void* v;
-  cuuint64_t dims[4], strides[3];
-  cuuint32_t box[4];
-  CUtensorMap tm_k, tm_v;
-  bool used;
-};
-constexpr int kTensorMapCache = 4;
-thread_local TensorMapCacheEntry g_tmap_cache[kTensorMapCache];
-thread_local int g_tmap_next = 0;
-
+// tensor, so they arrive zero-filled (requests to L2, but no reads of memory).
+// Encoded for every call (about 0.1 us each): nothing is kept by a pool's address.
 int make_tensor_maps(DecodeParams* prm, const Plan& pl, int num_kv_heads, int head_size, int kv_elt,
                      int block_size, int num_physical_blocks) {
   const EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return fail(PA_ERR_CUDA, "pa_decode: the driver has no cuTensorMapEncodeTiled");
-  // Unknown pool size: the row extent only has to cover every valid row, and
-  // no pool that fits in device memory has 2^31 token rows of >= 128 bytes.
-  const uint64_t rows =
-      num_physical_blocks > 0 ? (uint64_t)num_physical_blocks * block_size : (1ull << 31);
+  const uint64_t token_bytes = (uint64_t)num_kv_heads * head_size * kv_elt;
+  const uint64_t rows = num_physical_blocks > 0 ? (uint64_t)num_physical_blocks * block_size
+                                                : rows_of_pools(prm->k_cache, prm->v_cache, token_bytes);
+  if (rows == 0) return PA_ERR_INVALID_ARG;
   if (rows > (1ull << 31))
     return fail(PA_ERR_UNSUPPORTED, "pa_decode: %llu token rows in the pool (at most 2^31)",
                 (unsigned long long)rows);
   const cuuint64_t dims[4] = {kLine, pl.row_bytes / kLine, (cuuint64_t)pl.HG, rows};
-  const cuuint64_t strides[3] = {kLine, pl.row_bytes,
-                                 (cuuint64_t)num_kv_heads * head_size * kv_elt};
+  const cuuint64_t strides[3] = {kLine, pl.row_bytes, token_bytes};
   const cuuint32_t box[4] = {kLine, pl.lines, 1u, pl.box_rows};
   const cuuint32_t estride[4] = {1u, 1u, 1u, 1u};
-  for (int c = 0; c < kTensorMapCache; ++c) {
-    const TensorMapCacheEntry& e = g_tmap_cache[c];
-    if (e.used && e.k == prm->k_cache && e.v == prm->v_cache && memcmp(e.dims, dims, sizeof(dims)) == 0 &&
-        memcmp(e.strides, strides, sizeof(strides)) == 0 && memcmp(e.box, box, sizeof(box)) == 0) {
-      prm->tm_k = e.tm_k;
-      prm->tm_v = e.tm_v;
-      return PA_OK;
-    }
-  }
   for (int i = 0; i < 2; ++i) {
     const CUresult r = enc(i ? &prm->tm_v : &prm->tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                            const_cast<void*>(i ? prm->v_cache : prm->k_cache), dims, strides, box,
@@ -287,16 +294,6 @@ int make_tensor_maps(DecodeParams* prm, const Plan& pl, int num_kv_heads, int he
     if (r != CUDA_SUCCESS)
       return fail(PA_ERR_CUDA, "pa_decode: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
   }
-  TensorMapCacheEntry& e = g_tmap_cache[g_tmap_next];
-  g_tmap_next = (g_tmap_next + 1) % kTensorMapCache;
-  e.k = prm->k_cache;
-  e.v = prm->v_cache;
-  memcpy(e.dims, dims, sizeof(dims));
-  memcpy(e.strides, strides, sizeof(strides));
-  memcpy(e.box, box, sizeof(box));
-  e.tm_k = prm->tm_k;
-  e.tm_v = prm->tm_v;
-  e.used = true;
   return PA_OK;
 }
 

@@ -943,7 +943,10 @@ int prefix_impl(void* out, const void* query, const void* k_cache, const void* v
   const int group = num_heads / num_kv_heads;
   PrefixParams prm{};
   if (num_prefix_blocks > 0) {
-    const uint64_t pool_rows = num_physical_blocks > 0 ? (uint64_t)num_physical_blocks * block_size : 1ull << 31;
+    const uint64_t pool_rows =
+        num_physical_blocks > 0 ? (uint64_t)num_physical_blocks * block_size
+                                : rows_of_pools(k_cache, v_cache, (uint64_t)num_kv_heads * head_size * (kv_fp8 ? 1 : 2));
+    if (pool_rows == 0) return PA_ERR_INVALID_ARG;
     if (pool_rows > 1ull << 31)
       return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %llu token rows in the pool (at most 2^31)",
                   (unsigned long long)pool_rows);

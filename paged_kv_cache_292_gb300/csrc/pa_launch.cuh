@@ -66,6 +66,11 @@ int launch_typed(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t 
 using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
 EncodeTiledFn encode_tiled_fn();
 
+// Token rows for the tensor maps of two pools whose size the caller has not given:
+// those the pools' allocations hold behind the pools' addresses, at most 2^31.  0 with an
+// error recorded if the driver does not know the memory.
+uint64_t rows_of_pools(const void* k, const void* v, uint64_t row_bytes);
+
 // The kernel variants of the other translation units.
 int launch_mod(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool f32,
                bool kv_fp8);

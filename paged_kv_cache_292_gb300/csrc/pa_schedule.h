@@ -65,4 +65,12 @@ PA_HD int partial_slot_of_range(int64_t r, int64_t seq_lo, int64_t total_tiles,
   return (range_start(r, total_tiles, num_ranges) >= seq_lo) ? 0 : 1;
 }
 
+// Whole token rows from address `at` to the end of the allocation [start, start + size)
+// (0 if it does not hold the address), at most 2^31.
+PA_HD uint64_t rows_behind(uint64_t start, uint64_t size, uint64_t at, uint64_t row_bytes) {
+  if (at < start || at - start >= size) return 0;
+  const uint64_t rows = (size - (at - start)) / row_bytes;
+  return rows < (uint64_t(1) << 31) ? rows : uint64_t(1) << 31;
+}
+
 }  // namespace pa

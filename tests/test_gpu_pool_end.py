@@ -1,0 +1,74 @@
+"""Pools that end where their allocation ends, with the last block in use and no pool size given: the tensor maps end
+there too, and the results are those of pools in the middle of an allocation with the size given."""
+
+import pytest
+import torch
+
+from paged_kv_cache_292_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+BYTES = 24 << 20  # an allocation of its own, whole 2 MiB pages
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_cache_292_gb300 import build
+
+    build.build()
+    binding.load()
+
+
+def _pool(shape, dtype, seed, at_end):
+    """A pool of random values as the last bytes of an allocation, or 4 MiB before them."""
+    n = 1
+    for x in shape:
+        n *= x
+    size = n * dtype.itemsize
+    gen = torch.Generator().manual_seed(seed)
+    arena = torch.empty(BYTES, dtype=torch.uint8, device="cuda")
+    end = BYTES - (0 if at_end else 4 << 20)
+    pool = arena[end - size : end].view(dtype).view(shape)
+    if dtype == torch.uint8:
+        pool.copy_(torch.randint(0, 0x70, shape, generator=gen, dtype=torch.uint8))
+    else:
+        pool.copy_(torch.randn(shape, generator=gen))
+    return pool
+
+
+@pytest.mark.parametrize("Hk, D, bs", [(1, 64, 1), (1, 64, 4), (2, 64, 16), (3, 128, 8), (8, 128, 16), (5, 64, 24)])
+@pytest.mark.parametrize("G, Q", [(4, 1), (2, 3), (3, 3), (8, 4)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_last_block_of_the_allocation(Hk, D, bs, G, Q, fp8):
+    if fp8 and D == 64 and Hk % 2:
+        Hk *= 2
+    S, nblk = 3, 7
+    NB = S * nblk
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    gen = torch.Generator().manual_seed(3)
+    table = torch.randperm(NB, generator=gen).to(torch.int32)
+    last = int((table == NB - 1).nonzero())
+    table[last], table[nblk + 3] = int(table[nblk + 3]), NB - 1
+    table = table.view(S, nblk).cuda()
+    lens = torch.tensor([nblk * bs, nblk * bs - bs // 2, max(Q, nblk * bs - 1)], dtype=torch.int32).cuda()
+    q = torch.randn(S, Q, G * Hk, D, generator=gen).to(torch.bfloat16).cuda()
+    scales = (0.5, 2.0) if fp8 else ()
+    prefix = table[0, :2].contiguous()
+    table[:, :2] = prefix  # (the rows' own first blocks go unused)
+    outs = []
+    for at_end in (True, False):
+        k, v = (_pool((NB, bs, Hk, D), dtype, seed, at_end) for seed in (1, 2))
+        args = (q, k, v, table, lens, D**-0.5, *scales)
+        kw = dict(check_block_ids=not at_end)
+        out = [(binding.decode_fp8_multi if fp8 else binding.decode_multi)(*args, **kw)]
+        out.append((binding.decode_fp8_mod if fp8 else binding.decode_mod)(*args, window=5 * bs, **kw))
+        if bs % 8 == 0:
+            fn = binding.decode_fp8_prefix if fp8 else binding.decode_prefix
+            out.append(fn(q, k, v, prefix, table, lens, D**-0.5, *scales, **kw))
+        torch.cuda.synchronize()
+        outs.append(out)
+    for a, b in zip(*outs):
+        assert torch.isfinite(a.float()).all()
+        assert torch.equal(a, b)

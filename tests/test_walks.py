@@ -1,0 +1,20 @@
+"""Index arithmetic that the kernels and the host share, checked on the host."""
+
+import os
+import subprocess
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def host_check(tmp_path, name):
+    """Build tests/host/<name>.cpp against the kernels' headers as plain C++ and run it."""
+    exe = tmp_path / name
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I" + os.path.join(ROOT, "paged_kv_cache_292_gb300", "csrc"),
+                    os.path.join(ROOT, "tests", "host", name + ".cpp"), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert out.returncode == 0, out.stdout + out.stderr
+    assert out.stdout.startswith("ok")
+
+
+def test_rows_of_an_allocation(tmp_path):
+    host_check(tmp_path, "rows_check")
