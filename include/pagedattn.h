@@ -70,6 +70,7 @@ extern "C" {
 #define PA_DEVERR_CONTEXT_LEN 2 /* context length < 0 or > max_blocks_per_seq*block_size (clamped) */
 #define PA_DEVERR_SLOT 4        /* slot_mapping entry >= num_physical_blocks*block_size (skipped) */
 #define PA_DEVERR_TIMEOUT 8     /* a pipeline wait exceeded its limit; the kernel returned early */
+#define PA_DEVERR_STATE 32      /* a kernel found its own bookkeeping wrong, used none of it and returned early (16: pa_tables.h) */
 
 /*
  * pa_decode - paged decode attention, one query token per sequence.

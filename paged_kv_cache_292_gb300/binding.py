@@ -32,6 +32,7 @@ PA_DEVERR_CONTEXT_LEN = 2
 PA_DEVERR_SLOT = 4
 PA_DEVERR_TIMEOUT = 8
 PA_DEVERR_NO_BLOCKS = 16
+PA_DEVERR_STATE = 32
 PA_TABLES_RELEASE = -1
 
 INCLUDE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")

@@ -456,6 +456,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   if (extras != nullptr) {
     prm.sm_count = dev.sm_count;
     prm.cuts = reinterpret_cast<int4*>(ws + pl.ws_partials);
+    extras->ranges = pl.R;
     extras->cuts = prm.cuts;
     extras->part_ml = prm.part_ml;
     extras->part_o = prm.part_o;

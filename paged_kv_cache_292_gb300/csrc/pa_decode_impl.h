@@ -22,6 +22,7 @@ struct DecodeExtras {
   float* rest_ml = nullptr;
   float* rest_o = nullptr;
   // Set by the call, inside its scratch: how sequences were cut, and the partials.
+  int ranges = 0;
   int4* cuts = nullptr;
   const float* part_ml = nullptr;
   const float* part_o = nullptr;

@@ -81,23 +81,11 @@ constexpr int kFp32Buffers = 9216;  // static shared memory of the fp32 walk wit
 
 enum : int { kSegBegin = 1, kSegEnd = 2 };
 
-// Which tiles of a sequence a kernel walks, and what becomes of its rows.
-enum : int {
-  kWalkAll = 0,   // every token, plain scores, output rows
-  kWalkMod = 1,   // the tiles some query sees, modified scores, output rows
-  kWalkRest = 2,  // the tokens behind a shared prefix, plain scores, (m, l, O) rows
-};
-constexpr int kNoWindow = 1 << 30;  // longer than any context
-
-// SeqCut, what the walks other than kWalkAll leave per sequence: (first range,
-// last range, slot of the first range's partial, state).
-enum : int { kCutEmpty = 0, kCutWhole = 1, kCutMerge = 2 };
-
 struct StageMeta {
   int seq;     // sequence index
   int tok0;    // first token of the tile within the sequence
   int nvalid;  // valid tokens in the tile (1..16); kWalkMod: bit mask of the rows some query sees
-  int flags;   // kSegBegin | kSegEnd | (output slot + 1) << 2 | (slot of range r0) << 4
+  int flags;   // kSegBegin | kSegEnd | (output slot + 1) << 2 | (slot of range r0) << 4 | tile_tag
   int r0, r1;  // first and last range touching the sequence (cut sequences only)
   int ctx;     // the sequence's context length (causal limits of several queries)
   int newfirst;  // appending calls: first tile row holding one of the step's new
@@ -207,43 +195,20 @@ __device__ __forceinline__ int clamp_context(const DecodeParams& p, int s, bool 
   return c;
 }
 
-// The tiles one sequence contributes.  kWalkMod: `nh` tiles from token h0 (the
-// prefix every query sees), then the tiles from token t0 (what the window
-// leaves, from the first query's); kWalkRest: tiles from token t0.  A token is
-// seen by some query if it is in [first, pre) or in [max(first, lo), c).
+// Sequence s as the walk takes it (SeqSpan).
 template <int WALK>
-struct SeqWalk {
-  int c = 0, n = 0;
-  int nh = 0, h0 = 0, t0 = 0, first = 0, pre = 0, lo = 0;
-
+struct SeqWalk : SeqSpan<WALK> {
   __device__ __forceinline__ SeqWalk() {}
   __device__ __forceinline__ SeqWalk(const DecodeParams& p, int s, bool report_it) {
-    c = clamp_context(p, s, report_it);
+    const int context = clamp_context(p, s, report_it);
     if constexpr (WALK == kWalkAll) {
-      n = tiles_of(c);
+      this->all(context);
     } else if constexpr (WALK == kWalkRest) {
-      t0 = c >= p.prefix_tokens + p.num_queries - 1 ? p.prefix_tokens : 0;
-      n = tiles_of(c - t0);
+      this->rest(context, p.prefix_tokens, p.num_queries);
     } else {
-      first = p.first_tokens != nullptr ? max(0, __ldg(p.first_tokens + s)) : 0;
-      pre = p.prefix_lens != nullptr ? max(0, min(c, __ldg(p.prefix_lens + s))) : 0;
-      // The first query that exists sees back to its position - window + 1.
-      lo = max(max(first, pre), max(0, c - p.num_queries) - p.window + 1);
-      if (first < c) {
-        h0 = first & ~(kTile - 1);
-        nh = pre > first ? tiles_of(pre - h0) : 0;
-        t0 = max(lo & ~(kTile - 1), nh > 0 ? h0 + nh * kTile : 0);
-        n = nh + (c > t0 ? tiles_of(c - t0) : 0);
-      }
+      this->seen(context, p.first_tokens != nullptr ? __ldg(p.first_tokens + s) : 0,
+                 p.prefix_lens != nullptr ? __ldg(p.prefix_lens + s) : 0, p.num_queries, p.window);
     }
-  }
-  __device__ __forceinline__ int token(int j) const {
-    if constexpr (WALK == kWalkAll) return j * kTile;
-    if constexpr (WALK == kWalkRest) return t0 + j * kTile;
-    return j < nh ? h0 + j * kTile : t0 + (j - nh) * kTile;
-  }
-  __device__ __forceinline__ bool sees(int tok) const {  // kWalkMod
-    return tok < c && tok >= first && (tok < pre || tok >= lo);
   }
 };
 
@@ -2440,6 +2405,14 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
       *abort_flag = 1;
     }
   };
+  // A stage or a walk is not where it should be: say so and leave instead of
+  // taking a sequence or range from it as an index into global memory.
+  auto lost = [&]() {
+    if (lane == 0) {
+      report(p.error_flag, PA_DEVERR_STATE);
+      *abort_flag = 1;
+    }
+  };
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full_bar(i), 1);
@@ -2509,7 +2482,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
     auto table_entry = [&](int idx) -> int { return idx < nblk ? __ldg(bt_row + idx) : -1; };
     for (long long x = a; x < b; ++x) {
       bool new_seq = (x == a);
-      while (x >= ps + ns) {
+      while (x >= ps + ns && s < S) {
         ps += ns;
         ++s;
         sw = sw_next;
@@ -2518,6 +2491,10 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
         sw_next = SeqWalk<WALK>();
         if (s + 1 < S) sw_next = SeqWalk<WALK>(p, s + 1, false);
         new_seq = true;
+      }
+      if (s >= S) {
+        lost();
+        break;
       }
       const int j = static_cast<int>(x - ps);
       const int tok0 = sw.token(j);
@@ -2549,7 +2526,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
         nxt = table_entry(cb + 32 + lane);
       }
       const int flags = (new_seq ? kSegBegin : 0) | ((x == b - 1 || j == ns - 1) ? kSegEnd : 0) |
-                        ((slot + 1) << 2) | (seg_slot0 << 4);
+                        ((slot + 1) << 2) | (seg_slot0 << 4) | tile_tag(x);
       const bool mine = static_cast<int>((x - a) % (WALK == kWalkAll ? kProducers : producers)) == pw;
       // One producer fills all query slots, whoever takes the sequence's first tile:
       // it sees every phase of a slot's barrier, so that the parity it waits for is
@@ -2714,6 +2691,10 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
         break;
       }
       const StageMeta mt = meta[st];
+      if (!tag_matches(mt.flags, x) || static_cast<unsigned>(mt.seq) >= static_cast<unsigned>(S)) {
+        lost();
+        break;
+      }
       if (mt.flags & kSegBegin) {
         if (!mbar_wait_warp(qfull_bar(qi), qph, p.wait_limit_ns)) {
           timed_out();
@@ -2768,6 +2749,10 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
             break;
           }
           me = meta[st2];
+          if (!tag_matches(me.flags, x + 1) || me.seq != mt.seq) {
+            lost();
+            break;
+          }
           const uint32_t k_half2 = stages + st2 * p.stage_bytes;
           const uint32_t v_half2 = k_half2 + kTile * p.lines * kLine;
           if constexpr (QMODE < 2 && WALK == kWalkAll) {
@@ -2839,6 +2824,10 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
           }
         }
         const int slot = ((me.flags >> 2) & 3) - 1;
+        if (slot > 1 || (WALK == kWalkAll && slot >= 0 && (me.r0 < 0 || me.r0 > r || me.r1 < r || me.r1 >= R))) {
+          lost();
+          break;
+        }
         if constexpr (WALK == kWalkRest)
           cons.template finish<true>(p, me.seq, kv_head, slot, r, lane);
         else

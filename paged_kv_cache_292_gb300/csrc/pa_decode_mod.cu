@@ -35,6 +35,8 @@ struct MergeParams {
   const int4* cuts;
   const float* part_ml;
   const float* part_o;
+  int32_t* error_flag;
+  int ranges;
   int rows;          // num_seqs * seq_rows
   int seq_rows;      // num_queries * num_heads
   float v_scale;
@@ -54,6 +56,10 @@ __global__ void __launch_bounds__(256) pa_merge_kernel(const __grid_constant__ M
   const int s = row / p.seq_rows, in_seq = row - s * p.seq_rows;
   const int4 cut = __ldcg(p.cuts + s);
   if (cut.w != kCutMerge) return;
+  if (!cut_holds(cut.x, cut.y, cut.z, cut.w, p.ranges)) {
+    if (lane == 0) report(p.error_flag, PA_DEVERR_STATE);
+    return;
+  }
   MergedRow<DL> m = merge_row<D>(p.part_ml, p.part_o, cut, p.seq_rows, in_seq, lane, part, WARPS);
   if constexpr (WARPS > 1) {
     __shared__ float parts[WARPS][DL + 2][32];
@@ -85,7 +91,8 @@ __global__ void __launch_bounds__(256) pa_merge_kernel(const __grid_constant__ M
 
 template <typename T, int D>
 int launch_merge(const DecodeParams& prm, cudaStream_t stream) {
-  MergeParams mp{prm.out, prm.cuts, prm.part_ml, prm.part_o, 0, prm.num_queries * prm.num_heads, prm.v_scale};
+  MergeParams mp{prm.out, prm.cuts, prm.part_ml, prm.part_o, prm.error_flag, prm.num_ranges, 0,
+                 prm.num_queries * prm.num_heads, prm.v_scale};
   mp.rows = prm.num_seqs * mp.seq_rows;
   const bool few = mp.rows <= 8 * prm.sm_count;
   const cudaError_t e =

@@ -683,6 +683,8 @@ struct JoinParams {
   const float* walk_o;
   const int2* item_ctas;
   PrefixWork work;
+  int32_t* error_flag;
+  int walk_ranges;
   int rows;  // num_seqs * num_queries * num_heads
   int num_queries, num_heads, group, prefix_tokens, max_tokens;
   float v_scale;
@@ -709,11 +711,12 @@ __global__ void __launch_bounds__(256) pa_prefix_join(const __grid_constant__ Jo
   // Prefix partials: every CTA between the first and the last tile's has one (a
   // range holds two units or more), with a single row tile one per group.
   // (After a timeout of the prefix kernel the table may hold anything: stay inside.)
-  const int c0 = max(ctas.x, 0), c1 = min(ctas.y, p.work.ctas - 1);
+  const int c0 = max(0, min(ctas.x, p.work.ctas)), c1 = max(-1, min(ctas.y, p.work.ctas - 1));
   const int np = prefix && c >= p.prefix_tokens + p.num_queries - 1 ? max(c1 - c0 + 1, 0) * (two ? 1 : 2) : 0;
   // Partials of the rest: none, the walk's finished row, or one per range.
-  const bool whole = cut.w == kCutWhole;
-  const int nr = cut.w == kCutEmpty ? 0 : whole ? 1 : cut.y - cut.x + 1;
+  const bool whole = cut.w == kCutWhole, holds = cut_holds(cut.x, cut.y, cut.z, cut.w, p.walk_ranges);
+  if (!holds && lane == 0) report(p.error_flag, PA_DEVERR_STATE);
+  const int nr = !holds || cut.w == kCutEmpty ? 0 : whole ? 1 : cut.y - cut.x + 1;
   const float* ml_r = whole ? p.rest_ml : p.walk_ml;
   const float* o_r = whole ? p.rest_o : p.walk_o;
   const int seq_rows = p.num_queries * p.num_heads, in_seq = row - seq * seq_rows;
@@ -1012,6 +1015,8 @@ int prefix_impl(void* out, const void* query, const void* k_cache, const void* v
   jp.walk_o = ex.part_o;
   jp.item_ctas = prm.item_ctas;
   jp.work = prm.work;
+  jp.error_flag = error_flag;
+  jp.walk_ranges = ex.ranges;
   jp.rows = num_seqs * num_queries * num_heads;
   jp.num_queries = num_queries;
   jp.num_heads = num_heads;

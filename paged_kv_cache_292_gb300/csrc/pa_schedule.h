@@ -73,4 +73,72 @@ PA_HD uint64_t rows_behind(uint64_t start, uint64_t size, uint64_t at, uint64_t 
   return rows < (uint64_t(1) << 31) ? rows : uint64_t(1) << 31;
 }
 
+// Which tiles of a sequence a kernel walks, and what becomes of its rows.
+enum : int {
+  kWalkAll = 0,   // every token, plain scores, output rows
+  kWalkMod = 1,   // the tiles some query sees, modified scores, output rows
+  kWalkRest = 2,  // the tokens behind a shared prefix, plain scores, (m, l, O) rows
+};
+constexpr int kNoWindow = 1 << 30;  // longer than any context
+
+// The tiles a sequence of c tokens contributes.  kWalkMod: `nh` tiles from token
+// h0 (the prefix every query sees), then the tiles from token t0 (what the window
+// leaves, from the first query's); kWalkRest: tiles from token t0.  A token is
+// seen by some query if it is in [first, pre) or in [max(first, lo), c).
+template <int WALK>
+struct SeqSpan {
+  int c = 0, n = 0;
+  int nh = 0, h0 = 0, t0 = 0, first = 0, pre = 0, lo = 0;
+
+  PA_HD static int smaller(int a, int b) { return a < b ? a : b; }
+  PA_HD static int larger(int a, int b) { return a > b ? a : b; }
+
+  PA_HD void all(int context) {
+    c = context;
+    n = tiles_of(c);
+  }
+  PA_HD void rest(int context, int prefix_tokens, int num_queries) {
+    c = context;
+    t0 = c >= prefix_tokens + num_queries - 1 ? prefix_tokens : 0;
+    n = tiles_of(c - t0);
+  }
+  PA_HD void seen(int context, int first_token, int prefix_len, int num_queries, int window) {
+    c = context;
+    first = larger(0, first_token);
+    pre = larger(0, smaller(c, prefix_len));
+    // The first query that exists sees back to its position - window + 1.
+    lo = larger(larger(first, pre), larger(0, c - num_queries) - window + 1);
+    if (first < c) {
+      h0 = first & ~(kTile - 1);
+      nh = pre > first ? tiles_of(pre - h0) : 0;
+      t0 = larger(lo & ~(kTile - 1), nh > 0 ? h0 + nh * kTile : 0);
+      n = nh + (c > t0 ? tiles_of(c - t0) : 0);
+    }
+  }
+  PA_HD int token(int j) const {
+    if (WALK == kWalkAll) return j * kTile;
+    if (WALK == kWalkRest) return t0 + j * kTile;
+    return j < nh ? h0 + j * kTile : t0 + (j - nh) * kTile;
+  }
+  PA_HD bool sees(int tok) const {  // kWalkMod
+    return tok < c && tok >= first && (tok < pre || tok >= lo);
+  }
+};
+
+// SeqCut, what the walks other than kWalkAll leave per sequence: (first range,
+// last range, slot of the first range's partial, state).
+enum : int { kCutEmpty = 0, kCutWhole = 1, kCutMerge = 2 };
+
+// Whether the cut of a sequence names partials of `ranges` ranges.  The kernels that
+// add the partials ask before they use one as an index.
+PA_HD bool cut_holds(int first, int last, int slot, int state, int ranges) {
+  return state == kCutEmpty || state == kCutWhole ||
+         (state == kCutMerge && first >= 0 && first <= last && last < ranges && (slot == 0 || slot == 1));
+}
+
+// The tile's place in the flat list, beside the 8 bits of flags of its stage: a
+// consumer takes a stage only if it holds the tile that the consumer is at.
+PA_HD int tile_tag(int64_t x) { return static_cast<int>(static_cast<uint32_t>(x) << 8); }
+PA_HD bool tag_matches(int flags, int64_t x) { return (static_cast<uint32_t>(flags) & ~0xffu) == static_cast<uint32_t>(tile_tag(x)); }
+
 }  // namespace pa

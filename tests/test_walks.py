@@ -18,3 +18,9 @@ def host_check(tmp_path, name):
 
 def test_rows_of_an_allocation(tmp_path):
     host_check(tmp_path, "rows_check")
+
+
+def test_walks_partials_and_cuts(tmp_path):
+    """Tiles, partial slots and cuts of every walk, range by range, and the checks that the kernels make before they
+    use a stage's sequence or a sequence's cut as an index."""
+    host_check(tmp_path, "walk_check")
