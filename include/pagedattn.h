@@ -18,7 +18,12 @@
  *   - Every tensor pointer is DEVICE memory owned by the caller, dense and
  *     row-major in the shape given.  The library never frees or keeps it.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Calls
- *     are asynchronous on that stream and never synchronise the host.
+ *     are asynchronous on that stream and never synchronise the host, except
+ *     where the library's own scratch is allocated, grown or taken over (a
+ *     NULL workspace: see pa_decode and pa_decode_mod).
+ *   - Calls may be made from several host threads at once, also on one stream
+ *     and without a workspace: the library's scratch is held from a call's
+ *     lookup until its last launch is queued.
  *   - The return value is PA_OK (0) or a negative PA_ERR_* code; on error
  *     nothing was launched and pa_last_error() describes the cause.
  *   - `dtype` is PA_F32 or PA_BF16 and applies to query, out, the pools and

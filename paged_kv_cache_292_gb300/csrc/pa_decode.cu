@@ -377,13 +377,14 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
                  num_queries, elt, block_size, extras != nullptr);
   if (rc != PA_OK) return rc;
   int32_t* counters = nullptr;
+  ScratchHold hold;  // scratch of the library's own, until the launches are queued
   const bool clear_tickets = workspace == nullptr && fixed_scratch != nullptr;
   if (extras != nullptr) {
     if ((long long)num_seqs * num_queries * num_heads > 1 << 30)
       return fail(PA_ERR_UNSUPPORTED, "pa_decode: %d sequences of %d rows", num_seqs, num_queries * num_heads);
     const size_t need = pl.ws_partials + sizeof(int4) * (size_t)num_seqs;
     if (workspace == nullptr) {
-      rc = kept_scratch(need, stream, &workspace);
+      rc = hold.of_stream(need, stream, &workspace);
       if (rc != PA_OK) return rc;
     } else if (workspace_bytes < need) {
       return fail(PA_ERR_WORKSPACE, "pa_decode: workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -397,9 +398,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   }
   if (extras != nullptr) {
   } else if (workspace == nullptr) {
-    rc = library_workspace(pl.ws_partials, &workspace);
-    if (rc != PA_OK) return rc;
-    rc = library_counters(pl.ws_counters, &counters);
+    rc = hold.plain(pl.ws_partials, pl.ws_counters, &workspace, &counters);
     if (rc != PA_OK) return rc;
   } else {
     if (workspace_bytes < pl.ws_total)

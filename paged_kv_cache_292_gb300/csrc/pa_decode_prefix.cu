@@ -929,9 +929,9 @@ int prefix_impl(void* out, const void* query, const void* k_cache, const void* v
   const int items = count_items(num_seqs, num_queries, num_heads, num_kv_heads);
   const PrefixScratch sc =
       prefix_scratch(num_seqs, num_queries, num_heads, head_size, dev.sm_count + items, items, walk_bytes);
-  const bool own = workspace == nullptr;
-  if (own) {
-    rc = kept_scratch(sc.total, stream, &workspace);
+  ScratchHold hold;  // scratch of the library's own, until the launches are queued
+  if (workspace == nullptr) {
+    rc = hold.of_stream(sc.total, stream, &workspace);
     if (rc != PA_OK) return rc;
   } else {
     if (workspace_bytes < sc.total)

@@ -18,14 +18,15 @@ thread_local long long g_stall_tile = -1;
 thread_local unsigned int g_stall_limit_us = 0;
 
 constexpr int kMaxDevices = 64;
-std::mutex g_mutex;
+std::mutex g_mutex;          // g_info
+std::mutex g_scratch_mutex;  // what follows, held by a ScratchHold
 DeviceInfo g_info[kMaxDevices];
 bool g_info_valid[kMaxDevices] = {false};
 void* g_ws_ptr[kMaxDevices] = {nullptr};
 size_t g_ws_bytes[kMaxDevices] = {0};
 void* g_cnt_ptr[kMaxDevices] = {nullptr};
 size_t g_cnt_bytes[kMaxDevices] = {0};
-// kept_scratch: a buffer for each of the streams that called last.
+// ScratchHold::of_stream: a buffer for each of the streams that called last.
 struct KeptScratch {
   unsigned long long stream;  // its id, which no other stream of the process ever gets
   unsigned long long used;    // 0: free
@@ -77,11 +78,11 @@ int current_device_info(DeviceInfo* info) {
   return PA_OK;
 }
 
-int library_workspace(size_t bytes, void** ptr) {
+int ScratchHold::plain(size_t bytes, size_t counter_bytes, void** ptr, int32_t** counters) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  std::lock_guard<std::mutex> lock(g_mutex);
+  lock_ = std::unique_lock<std::mutex>(g_scratch_mutex);
   if (g_ws_bytes[dev] < bytes) {
     if (g_ws_ptr[dev] != nullptr) {
       e = cudaFree(g_ws_ptr[dev]);
@@ -97,23 +98,14 @@ int library_workspace(size_t bytes, void** ptr) {
     }
     g_ws_bytes[dev] = want;
   }
-  *ptr = g_ws_ptr[dev];
-  return PA_OK;
-}
-
-int library_counters(size_t bytes, int32_t** ptr) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  std::lock_guard<std::mutex> lock(g_mutex);
-  if (g_cnt_bytes[dev] < bytes) {
+  if (g_cnt_bytes[dev] < counter_bytes) {
     if (g_cnt_ptr[dev] != nullptr) {
       e = cudaFree(g_cnt_ptr[dev]);
       g_cnt_ptr[dev] = nullptr;
       g_cnt_bytes[dev] = 0;
       if (e != cudaSuccess) return cuda_fail(e, "cudaFree(tickets)");
     }
-    const size_t want = align_up(bytes < 65536 ? 65536 : bytes, 65536);
+    const size_t want = align_up(counter_bytes < 65536 ? 65536 : counter_bytes, 65536);
     void* p = nullptr;
     e = cudaMalloc(&p, want);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(tickets)");
@@ -127,7 +119,8 @@ int library_counters(size_t bytes, int32_t** ptr) {
     g_cnt_ptr[dev] = p;
     g_cnt_bytes[dev] = want;
   }
-  *ptr = static_cast<int32_t*>(g_cnt_ptr[dev]);
+  *ptr = g_ws_ptr[dev];
+  *counters = static_cast<int32_t*>(g_cnt_ptr[dev]);
   return PA_OK;
 }
 
@@ -140,7 +133,7 @@ int raise_smem_limit(const void* kernel, int bytes, int device, RaisedDevices* r
   return PA_OK;
 }
 
-int kept_scratch(size_t bytes, void* stream, void** ptr) {
+int ScratchHold::of_stream(size_t bytes, void* stream, void** ptr) {
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &status);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
@@ -152,7 +145,7 @@ int kept_scratch(size_t bytes, void* stream, void** ptr) {
   int dev = 0;
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  std::lock_guard<std::mutex> lock(g_mutex);
+  lock_ = std::unique_lock<std::mutex>(g_scratch_mutex);
   KeptScratch* mine = &g_kept[dev][0];  // the stream's, or the one not used for longest
   for (KeptScratch& k : g_kept[dev]) {
     if (k.used != 0 && k.stream == id) {

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 namespace pa {
 
@@ -32,22 +33,28 @@ struct DeviceInfo {
 // Properties of the current device (cached per device; no synchronisation).
 int current_device_info(DeviceInfo* info);
 
-// Library-owned scratch for the current device, grown to at least `bytes`.
-// Growing frees the old buffer (cudaFree synchronises the device).
-int library_workspace(size_t bytes, void** ptr);
+// The scratch of the library's own, held by a call from its lookup until its last
+// launch is queued: until then no other thread grows, frees or takes over what the
+// call is about to use, and the launches of two calls on one buffer do not mix.  (A
+// call that then waits for the device waits for this one's work, too.)
+class ScratchHold {
+ public:
+  // Plain decode, current device: scratch grown to at least `bytes`, and a
+  // zero-filled buffer of merge tickets (zero-filled again when it grows).
+  // Growing frees the old buffer (cudaFree synchronises the device).
+  int plain(size_t bytes, size_t counter_bytes, void** ptr, int32_t** counters);
 
-// Library-owned, zero-filled merge-ticket buffer for the current device, grown
-// to at least `bytes` (zero-filled again when it grows).
-int library_counters(size_t bytes, int32_t** ptr);
+  // The operators beyond plain decode: at least `bytes` of any content, a buffer for
+  // each stream, so that calls on two streams do not meet in one.  The buffers of the
+  // last eight streams are kept; a stream beyond them takes over the buffer used
+  // longest ago, and a batch that outgrows its buffer replaces it (sizes double):
+  // both wait for the device.  Refused while `stream` is being captured, where a
+  // graph would keep the address beyond this call: captured calls bring their own.
+  int of_stream(size_t bytes, void* stream, void** ptr);
 
-// Library-owned scratch of the operators beyond plain decode: at least `bytes`
-// of any content, a buffer for each stream, so that calls on two streams do not
-// meet in one.  The buffers of the last eight streams are kept; a stream beyond
-// them takes over the buffer used longest ago, and a batch that outgrows its buffer
-// replaces it (sizes double): both wait for the device.  Refused while `stream` is being
-// captured, where a graph would keep the address beyond this call: captured calls
-// bring their own.
-int kept_scratch(size_t bytes, void* stream, void** ptr);
+ private:
+  std::unique_lock<std::mutex> lock_;
+};
 
 // Writes the new rows of a multi-query appending call into the pools (token
 // i of sequence s at position context_lens[s] - num_queries + i), as its own
