@@ -24,8 +24,9 @@
  *   - Calls may be made from several host threads at once, also on one stream
  *     and without a workspace: the library's scratch is held from a call's
  *     lookup until its last launch is queued.
- *   - The return value is PA_OK (0) or a negative PA_ERR_* code; on error
- *     nothing was launched and pa_last_error() describes the cause.
+ *   - The return value is PA_OK (0) or a negative PA_ERR_* code, whose cause
+ *     pa_last_error() describes; on error nothing was launched (PA_ERR_CUDA
+ *     from a launch itself: nothing after that launch).
  *   - `dtype` is PA_F32 or PA_BF16 and applies to query, out, the pools and
  *     the new K/V rows alike.  Arithmetic is fp32 in every case.
  *   - Query head h reads KV head h / (num_heads / num_kv_heads).
@@ -493,8 +494,8 @@ int pa_decode_fp8_mq_append(void* out, const void* query, const void* k_new, con
  * that tile is never filled, the waits on it run out, and the kernel returns
  * after letting the copies it had started land (again within the limit).
  * (pa_decode_prefix: its prefix kernel, whose tiles of 128 prefix tokens are
- * counted per KV head and per 256 query rows of it, one after another;
- * pa_decode_mod: the tiles its walk takes.)
+ * counted per KV head and per 256 query rows of it, one after another, and behind
+ * them the tiles of the walk behind the prefix; pa_decode_mod: the tiles its walk takes.)
  * That call's output is unspecified, and its scratch (pa_decode_ws) must be
  * zero-filled again before reuse.  The setting is used by one launch and then
  * cleared; tile = -1 clears it.  Returns PA_OK, or PA_ERR_INVALID_ARG for

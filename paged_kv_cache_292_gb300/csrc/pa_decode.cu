@@ -488,7 +488,14 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
         cudaMemsetAsync(counters, 0, sizeof(int32_t) * (size_t)num_seqs * num_kv_heads, st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(merge tickets)");
   }
-  take_wait_test(&prm.stall_tile, &prm.wait_limit_ns);
+  if (extras != nullptr && extras->walk == kWalkRest) {
+    rc = extras->before(extras, extras->context);
+    if (rc != PA_OK) return rc;
+    prm.stall_tile = extras->stall_tile;
+    prm.wait_limit_ns = extras->wait_limit_ns;
+  } else {
+    take_wait_test(&prm.stall_tile, &prm.wait_limit_ns);
+  }
   if (k_new != nullptr && pl.split >= 2) {
     // Several consumer warps per KV head: the rows are written by their own
     // kernel, chained ahead of the decode, which then only reads them.

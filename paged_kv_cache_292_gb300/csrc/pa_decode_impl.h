@@ -21,6 +21,12 @@ struct DecodeExtras {
   float prefix_units = 0.f;  // work of the prefix kernel launched just before (0: none)
   float* rest_ml = nullptr;
   float* rest_o = nullptr;
+  // kWalkRest: queues what goes before the walk, once nothing but a launch can fail
+  // any more, and sets the walk's settings of pa_test_stall_copy.
+  int (*before)(DecodeExtras* self, void* context) = nullptr;
+  void* context = nullptr;
+  long long stall_tile = -1;
+  unsigned long long wait_limit_ns = 0;
   // Set by the call, inside its scratch: how sequences were cut, and the partials.
   int ranges = 0;
   int4* cuts = nullptr;

@@ -41,6 +41,7 @@
 #include "pa_launch.cuh"
 
 #include <cmath>
+#include <utility>
 
 #include "pa_decode_impl.h"
 #include "pa_prefix_work.h"
@@ -898,6 +899,37 @@ extern "C" size_t pa_decode_prefix_workspace_size(int num_seqs, int num_queries,
 namespace pa {
 namespace {
 
+// What goes before the walk: the prefix kernel, if there is a prefix.
+struct PrefixLaunch {
+  PrefixParams* prm;
+  int head_size;
+  bool kv_fp8;
+  int device;
+  cudaStream_t stream;
+
+  static int run(DecodeExtras* ex, void* context) {
+    const PrefixLaunch& l = *static_cast<PrefixLaunch*>(context);
+    // The stalled tile of a test: the prefix kernel's tiles come first, then the walk's.
+    take_wait_test(&ex->stall_tile, &ex->wait_limit_ns);
+    l.prm->stall_tile = -1;
+    l.prm->wait_limit_ns = kWaitLimitNs;
+    const PrefixWork& w = l.prm->work;
+    const long long tiles = w.tiles > 0 ? (long long)w.items() * w.tiles : 0;
+    if (ex->stall_tile >= tiles) {
+      ex->stall_tile -= tiles;
+    } else if (ex->stall_tile >= 0) {
+      std::swap(ex->stall_tile, l.prm->stall_tile);
+      std::swap(ex->wait_limit_ns, l.prm->wait_limit_ns);
+    }
+    if (tiles == 0) return PA_OK;
+    if (l.kv_fp8)
+      return l.head_size == 64 ? launch_prefix<64, true>(*l.prm, l.device, l.stream)
+                               : launch_prefix<128, true>(*l.prm, l.device, l.stream);
+    return l.head_size == 64 ? launch_prefix<64, false>(*l.prm, l.device, l.stream)
+                             : launch_prefix<128, false>(*l.prm, l.device, l.stream);
+  }
+};
+
 int prefix_impl(void* out, const void* query, const void* k_cache, const void* v_cache, const int32_t* prefix_table,
                 const int32_t* block_tables, const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
                 int num_kv_heads, int head_size, int block_size, int num_prefix_blocks, int max_blocks_per_seq,
@@ -984,16 +1016,12 @@ int prefix_impl(void* out, const void* query, const void* k_cache, const void* v
     prm.scale_log2 = scale != 0.f ? (float)(std::fabs((double)scale) * k_scale * 1.4426950408889634) : 1.f;
     prm.q_keep = scale != 0.f ? 0xffffffffu : 0u;
     prm.q_flip = scale < 0.f ? 0x80008000u : 0u;
-    take_wait_test(&prm.stall_tile, &prm.wait_limit_ns);
-    if (kv_fp8)
-      rc = head_size == 64 ? launch_prefix<64, true>(prm, dev.device, st) : launch_prefix<128, true>(prm, dev.device, st);
-    else
-      rc = head_size == 64 ? launch_prefix<64, false>(prm, dev.device, st)
-                           : launch_prefix<128, false>(prm, dev.device, st);
-    if (rc != PA_OK) return rc;
   }
   DecodeExtras ex{};
   ex.walk = kWalkRest;
+  PrefixLaunch first{&prm, head_size, kv_fp8, dev.device, st};
+  ex.before = PrefixLaunch::run;
+  ex.context = &first;
   ex.prefix_tokens = prefix_tokens;
   ex.rest_ml = reinterpret_cast<float*>(ws + sc.rest_ml);
   ex.rest_o = reinterpret_cast<float*>(ws + sc.rest_o);
