@@ -326,8 +326,9 @@ size_t pa_decode_mod_workspace_size(int num_seqs, int num_queries, int num_heads
  *
  * pa_decode_fp8_prefix - the same over FP8 pools: keys, values and the query's
  * rounding as in pa_decode_fp8_mq, query and out bf16.  The softmax weights of
- * the prefix enter its second product rounded to f16 (relative error <= 2^-11
- * each).  head_size 64 with an odd num_kv_heads is PA_ERR_UNSUPPORTED.
+ * the prefix enter its second product rounded to f16: off by at most 2^-11 of
+ * themselves or 2^-32 of the largest, whichever is more.  head_size 64 with an
+ * odd num_kv_heads is PA_ERR_UNSUPPORTED.
  */
 int pa_decode_prefix(void* out, const void* query, const void* k_cache, const void* v_cache,
                      const int32_t* prefix_table, const int32_t* block_tables,
@@ -418,8 +419,10 @@ int pa_decode_static(void* out, const void* query, const void* k_cache, const vo
  * k = e4m3(code) * k_scale and values v = e4m3(code) * v_scale.  Each token
  * moves half the bytes of a bf16 pool.  Scratch as pa_decode_workspace_size.
  * The query is rounded to f16 on the way into the tensor cores (exact for
- * |q| in [2^-14, 65504]).  head_size 64 with an odd num_kv_heads is
- * PA_ERR_UNSUPPORTED (a KV-head group's FP8 row must be whole 128-byte lines).
+ * |q| in [2^-14, 65504]), and so are the softmax weights: off by at most 2^-11
+ * of themselves or 2^-39 of the largest, whichever is more.  head_size 64 with
+ * an odd num_kv_heads is PA_ERR_UNSUPPORTED (a KV-head group's FP8 row must be
+ * whole 128-byte lines).
  */
 int pa_write_cache_fp8(const void* k_new, const void* v_new, const int64_t* slot_mapping,
                        void* k_cache, void* v_cache, int num_tokens, int num_kv_heads, int head_size,

@@ -1072,6 +1072,12 @@ struct MmaConsumerMQ {
   }
 };
 
+// FP8 pools: weights go into the f16 product times 2^kF16Up, up to 2^14 of f16's 65504.
+// Relative to the largest they then keep 11 bits down to 2^-28 and vanish below
+// 2^-39 (as they are, below 2^-25: 128 k tokens 2^-25 below one token's weight are
+// 0.4% of the output).  The sums carry the same factor, which the stored maxima take out.
+constexpr float kF16Up = 14.f;
+
 // Consumer for an FP8 (E4M3) pool with bf16 queries and outputs.  Codes are
 // widened to f16 in registers (exact) and both products run on f16 MMAs.
 // Shared-memory reads use ldmatrix on 16-bit units (two codes each):
@@ -1220,13 +1226,14 @@ struct MmaConsumerF8 {
     const float base_a = (mn_a == -INFINITY) ? 0.f : mn_a;
     const float base_b = (mn_b == -INFINITY) ? 0.f : mn_b;
     const float alpha_a = ex2_ftz(m_a - base_a), alpha_b = ex2_ftz(m_b - base_b);
+    const float up_a = base_a - kF16Up, up_b = base_b - kF16Up;
     m_a = mn_a;
     m_b = mn_b;
-    const float p0 = ex2_ftz(s0 - base_a), p1 = ex2_ftz(s1 - base_b);
-    const float p2 = ex2_ftz(s2 - base_a), p3 = ex2_ftz(s3 - base_b);
+    const float p0 = ex2_ftz(s0 - up_a), p1 = ex2_ftz(s1 - up_b);
+    const float p2 = ex2_ftz(s2 - up_a), p3 = ex2_ftz(s3 - up_b);
     // Weights enter the f16 MMA rounded to f16 (relative error <= 2^-11,
-    // half an ulp of the 10-bit fraction), well inside the bf16 output's own
-    // rounding; the running sum keeps them in fp32.
+    // half an ulp of the 10-bit fraction; kF16Up), well inside the bf16 output's
+    // own rounding; the running sum keeps them in fp32.
     const uint32_t p_top = pack_f16x2(p0, p1), p_bot = pack_f16x2(p2, p3);
     l_a = l_a * alpha_a + p0 + p2;
     l_b = l_b * alpha_b + p1 + p3;
@@ -1348,15 +1355,16 @@ struct MmaConsumerF8 {
     const float base_a = (mn_a == -INFINITY) ? 0.f : mn_a;
     const float base_b = (mn_b == -INFINITY) ? 0.f : mn_b;
     const float alpha_a = ex2_ftz(m_a - base_a), alpha_b = ex2_ftz(m_b - base_b);
+    const float up_a = base_a - kF16Up, up_b = base_b - kF16Up;
     m_a = mn_a;
     m_b = mn_b;
     float pw[2][4];
 #pragma unroll
     for (int tt = 0; tt < 2; ++tt) {
-      pw[tt][0] = ex2_ftz(sc[tt][0] - base_a);
-      pw[tt][1] = ex2_ftz(sc[tt][1] - base_b);
-      pw[tt][2] = ex2_ftz(sc[tt][2] - base_a);
-      pw[tt][3] = ex2_ftz(sc[tt][3] - base_b);
+      pw[tt][0] = ex2_ftz(sc[tt][0] - up_a);
+      pw[tt][1] = ex2_ftz(sc[tt][1] - up_b);
+      pw[tt][2] = ex2_ftz(sc[tt][2] - up_a);
+      pw[tt][3] = ex2_ftz(sc[tt][3] - up_b);
     }
     l_a = l_a * alpha_a + ((pw[0][0] + pw[0][2]) + (pw[1][0] + pw[1][2]));
     l_b = l_b * alpha_b + ((pw[0][1] + pw[0][3]) + (pw[1][1] + pw[1][3]));
@@ -1453,8 +1461,8 @@ struct MmaConsumerF8 {
         }
         if (g == 0) {
           float* pm = p.part_ml + base * 2;
-          if (ha < G) *reinterpret_cast<float2*>(pm + (size_t)qa * 2) = make_float2(m_a, la);
-          if (hb < G) *reinterpret_cast<float2*>(pm + (size_t)qb_ * 2) = make_float2(m_b, lb);
+          if (ha < G) *reinterpret_cast<float2*>(pm + (size_t)qa * 2) = make_float2(m_a - kF16Up, la);
+          if (hb < G) *reinterpret_cast<float2*>(pm + (size_t)qb_ * 2) = make_float2(m_b - kF16Up, lb);
         }
       }
     } else {
@@ -1468,7 +1476,7 @@ struct MmaConsumerF8 {
           gh = n % G;
         }
         const int row = qi * H + kv_head * G + gh;
-        const float l = half ? lb : la, m = half ? m_b : m_a;
+        const float l = half ? lb : la, m = (half ? m_b : m_a) - kF16Up;
         if (!REST && slot < 0) {
           __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + ((size_t)seq * Q * H + row) * D;
           // A query with no keys (several queries, short context) gives zeros.
@@ -1627,12 +1635,13 @@ struct RowsConsumer {
       const float base = mn == -INFINITY ? 0.f : mn;
       alpha[half] = ex2_ftz(m[half] - base);
       m[half] = mn;
+      const float up = KV8 ? base - kF16Up : base;
       float sum = 0.f;
 #pragma unroll
       for (int tt = 0; tt < N; ++tt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[tt][4 * half + i] = ex2_ftz(s[tt][4 * half + i] - base);
+          s[tt][4 * half + i] = ex2_ftz(s[tt][4 * half + i] - up);
           sum += s[tt][4 * half + i];
         }
       l[half] = l[half] * alpha[half] + sum;
@@ -1742,7 +1751,7 @@ struct RowsConsumer {
           }
         }
         if (t == 0)
-          *reinterpret_cast<float2*>((whole ? p.rest_ml : p.part_ml) + at * 2) = make_float2(m[half], sum);
+          *reinterpret_cast<float2*>((whole ? p.rest_ml : p.part_ml) + at * 2) = make_float2(KV8 ? m[half] - kF16Up : m[half], sum);
       }
     }
   }

@@ -60,6 +60,9 @@ constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
 // A running maximum is kept until a tile exceeds it by this factor (log2): until
 // then weights are at most 2^8, which bf16 and the fp32 sums hold as well as 1.
 constexpr float kSlack = 8.f;
+// FP8 pools: the weights are f16, whose upper range they use: up to 2^15 with the slack.
+// They keep 11 bits down to 2^-21 of the running maximum's and vanish below 2^-32.
+constexpr float kWeightUp = 7.f;
 
 struct PrefixParams {
   CUtensorMap tm_k, tm_v;  // (64 elements, chunk of 64 within a token row, token row); FP8: (D, KV head, token row)
@@ -231,6 +234,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
   if (warp < kSoftmaxWarps) {
     // ---------------- softmax ----------------
     const int w = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
+    constexpr float kUp = F8 ? kWeightUp : 0.f;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the TMEM lanes
     const uint32_t s_addr = tmem + lanes + 128u * w, o_addr = tmem + lanes + 256u + (uint32_t)D * w + (D / 2) * half;
     float* mine = reinterpret_cast<float*>(smem + L::kExchange) + (w * 2 + half) * 128 + row;
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
             }
           }
         }
-        const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
+        const float neg = m == -INFINITY ? 0.f : kUp - m * p.scale_log2;
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), neg2 = pair(neg, neg);
         uint64_t sum[2] = {0ull, 0ull};
         // The weights enter the product as bf16: half a step, 2^-8 at most, both
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __gr
         break;
       }
       const size_t at = ((size_t)(cta + item) * 2 + w) * kPrefixRows + row;
-      if (rows_here && half == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m * p.scale_log2, l + theirs);
+      if (rows_here && half == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m * p.scale_log2 - kUp, l + theirs);
       if (tid == 0) {
         if (t0 == 0) p.item_ctas[item].x = cta;
         if (t1 == wk.tiles) p.item_ctas[item].y = cta;
