@@ -16,43 +16,10 @@
 #include "pa_decode_kernel.cuh"
 #include "pa_internal.h"
 #include "pa_launch.cuh"
+#include "pa_plan.h"
 #include "pa_schedule.h"
 
 namespace pa {
-
-// ---------------------------------------------------------------------------
-// Host side
-// ---------------------------------------------------------------------------
-// Of the shapes whose staged rows fit, the one with the most consumer warps per SM;
-// among equals the most KV heads per CTA (the longest copies).  An SM holds 12
-// warps at 168 registers a thread, 16 at 128 (max_threads).  One
-// producer warp for few consumers: every warp of the other kind hides latency.
-// (96 sequences x 3 queries of 6 x 64 dims: three CTAs per SM 66 us, one 162.)
-WalkShape walk_shape(int num_heads, int num_kv_heads, int head_size, int num_queries, int elt) {
-  const int columns = (num_heads / num_kv_heads) * num_queries;
-  const int split = elt == 4 || columns <= 8 ? 1 : (columns + 15) / 16;
-  const int warps = elt != 4 && (head_size == 64 || columns <= 8) ? 16 : 12;
-  WalkShape best{num_kv_heads, split, 1, 1, head_size * elt};
-  int most = 0;
-  for (int hg = 1; hg * split <= kMaxGroupHeads; ++hg) {
-    const int row = hg * head_size * elt, consumers = hg * split;
-    // Consumers that take two tiles a pass need a ring of four: rows of at most 1 KiB.
-    if (row > (columns > 8 && elt != 4 ? kMaxRowBytes / 2 : kMaxRowBytes)) continue;
-    if (num_kv_heads % hg != 0 || (elt != 4 && row % kLine != 0)) continue;
-    if (row == kMaxRowBytes && columns <= 8) {  // HBM-bound as they are: the longest copies
-      best = WalkShape{num_kv_heads / hg, split, kProducers, 1, row};
-      break;
-    }
-    const int producers = consumers >= 6 ? kProducers : 1;
-    int per_sm = warps / (consumers + producers);
-    if (per_sm < 1) per_sm = 1;
-    if (consumers * per_sm >= most) {
-      most = consumers * per_sm;
-      best = WalkShape{num_kv_heads / hg, split, producers, per_sm, row};
-    }
-  }
-  return best;
-}
 
 EncodeTiledFn encode_tiled_fn() {
   static const EncodeTiledFn fn = [] {
@@ -103,134 +70,6 @@ uint64_t rows_of_pools(const void* k, const void* v, uint64_t row_bytes) {
 }
 
 namespace {
-
-// Scratch layout: partial (m, l) and O at the start, then the merge tickets
-// (num_seqs * num_kv_heads int32).  In a caller's buffer the tickets occupy
-// its last bytes (rounded down to 256), so that buffers reused across batch
-// shapes keep tickets and partials apart.
-size_t workspace_layout(int num_seqs, int num_heads, int num_kv_heads, int head_size, int R,
-                        Plan* pl, int num_queries = 1) {
-  num_heads *= num_queries;  // partial rows are (query, head) pairs
-  const size_t ml = align_up(sizeof(float) * (size_t)R * 2 * num_heads * 2, 256);
-  const size_t o = align_up(sizeof(float) * (size_t)R * 2 * num_heads * head_size, 256);
-  const size_t cnt = align_up(sizeof(int32_t) * (size_t)num_seqs * num_kv_heads, 256);
-  if (pl) {
-    pl->ws_ml = 0;
-    pl->ws_o = ml;
-    pl->ws_partials = ml + o;
-    pl->ws_counters = cnt;
-    pl->ws_total = ml + o + cnt;
-  }
-  return ml + o + cnt;
-}
-
-// KV heads one CTA stages per token row: the largest divisor of num_kv_heads
-// that is at most `max_heads` (8 with one consumer warp per KV head, 4 with
-// two), keeps the row within 2 KiB, so three stages fit in shared memory, and
-// makes it whole 128-byte lines (FP8 pools of 64 dims: an even number of heads).
-int heads_per_cta(int num_kv_heads, int head_size, int elt, int max_heads = kMaxGroupHeads) {
-  for (int h = max_heads; h > 1; --h) {
-    const int row = h * head_size * elt;
-    if (num_kv_heads % h == 0 && row <= kMaxRowBytes && row % (int)kLine == 0) return h;
-  }
-  return 1;
-}
-
-// Consumer warps per KV head: one 8-wide MMA tile of (query, head) columns
-// per warp, so ceil(columns / 8) (at most 4: 32 columns).
-int column_split(int group, int num_queries) { return (group * num_queries + 7) / 8; }
-
-int default_ranges(const DeviceInfo& dev, int HG) {
-  const int r = dev.sm_count / HG;
-  return r < 1 ? 1 : r;
-}
-
-int gcd_int(int a, int b) {
-  while (b != 0) {
-    const int t = a % b;
-    a = b;
-    b = t;
-  }
-  return a;
-}
-
-// elt: bytes of a pool element; q_elt: bytes of a query element (bf16 queries
-// select the tensor-core consumers, whose stages are swizzled tensor boxes).
-// walk: the CTA shape of the walks other than kWalkAll (walk_shape), several
-// ranges per SM where they fit.
-int make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int elt,
-              int num_ranges, const DeviceInfo& dev, Plan* pl, int num_queries = 1,
-              int q_elt = 0, int block_size = 16, bool walk = false) {
-  if (q_elt == 0) q_elt = elt;
-  const int G = num_heads / num_kv_heads;
-  const bool mma = q_elt == 2;
-  pl->split = column_split(G, num_queries);
-  pl->Hg = heads_per_cta(num_kv_heads, head_size, elt, kMaxGroupHeads / pl->split);
-  pl->producers = kProducers;
-  int per_sm = 1;
-  if (walk) {
-    const WalkShape w = walk_shape(num_heads, num_kv_heads, head_size, num_queries, elt);
-    pl->split = w.split;
-    pl->Hg = num_kv_heads / w.groups;
-    pl->producers = w.producers;
-    per_sm = w.per_sm;
-  }
-  pl->HG = num_kv_heads / pl->Hg;
-  pl->row_bytes = (uint32_t)(pl->Hg * head_size * elt);
-  pl->q_bytes = (uint32_t)(num_queries * pl->Hg * G * head_size * q_elt);
-  pl->lines = pl->box_rows = pl->box_bytes = 0;
-  if (mma) {
-    if (pl->row_bytes % kLine != 0)
-      return fail(PA_ERR_UNSUPPORTED,
-                  "pa_decode: %d KV heads x %d dims make %u-byte rows, not whole 128-byte lines",
-                  pl->Hg, head_size, pl->row_bytes);
-    // A tensor copy moves box_rows = gcd(block_size, 16) rows (they share a
-    // block) and must land on a 1 KiB boundary under the 128-byte swizzle, so
-    // box_rows * lines is a multiple of 8: lines is a multiple of `step`.  An
-    // odd multiple spreads consecutive rows over the most bank groups.
-    const uint32_t chunks = pl->row_bytes / kLine;
-    const int br = gcd_int(block_size, kTile);
-    const uint32_t step = 8u / (uint32_t)gcd_int(br, 8);
-    uint32_t lines = (chunks + step - 1) / step * step;
-    if ((lines / step) % 2 == 0) lines += step;
-    pl->lines = lines;
-    pl->box_rows = (uint32_t)br;
-    pl->box_bytes = (uint32_t)br * lines * kLine;
-    pl->pitch = lines * kLine;
-  } else {
-    pl->pitch = pl->row_bytes + kRowSkew;
-  }
-  pl->stage_bytes = 2u * kTile * pl->pitch;
-  pl->stages = 0;
-  const int pref[][2] = {{6, 2}, {5, 2}, {4, 2}, {3, 2}, {3, 1}, {2, 2}, {2, 1}};
-  for (; per_sm > 0 && pl->stages == 0; --per_sm) {
-    // An SM has 228 KiB, of which each of its CTAs takes 1 KiB besides its own.
-    int room = per_sm > 1 ? (228 << 10) / per_sm - 1024 : dev.max_smem_optin;
-    if (walk && !mma) room -= kFp32Buffers;
-    const int least = per_sm > 1 ? (mma ? 4 : 3) : 0;  // fewer CTAs rather than a shorter ring
-    for (auto& c : pref) {
-      const Layout L = make_layout(c[0], c[1], pl->q_bytes, pl->stage_bytes, mma);
-      if ((int)L.total <= room && c[0] >= least) {
-        pl->stages = c[0];
-        pl->q_slots = c[1];
-        pl->smem = L.total;
-        pl->R = num_ranges > 0 ? num_ranges : default_ranges(dev, pl->HG) * per_sm;
-        break;
-      }
-    }
-  }
-  if (pl->stages == 0)
-    return fail(PA_ERR_UNSUPPORTED, "decode stages (%u bytes each) do not fit in %d bytes of shared memory",
-                pl->stage_bytes, dev.max_smem_optin);
-  // Consumers that take two tiles per pass (FP8 pools; bf16 with a KV head's
-  // columns split over several warps) hold two stages at once: they need four
-  // or more.  Their rows are at most 1 KiB, so every shape they accept has.
-  const bool pairs = mma && (elt == 1 || G * num_queries > 8);
-  if (pairs && pl->stages < 4)
-    return fail(PA_ERR_UNSUPPORTED, "decode: %d stages of %u bytes, four needed", pl->stages, pl->stage_bytes);
-  workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, pl->R, pl, num_queries);
-  return PA_OK;
-}
 
 int validate(const void* out, const void* query, const void* k_cache, const void* v_cache,
              const int32_t* block_tables, const int32_t* context_lens, int num_seqs, int num_heads,
@@ -373,8 +212,8 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   if (rc != PA_OK) return rc;
   const int elt = dtype == PA_F32 ? 4 : 2;
   Plan pl{};
-  rc = make_plan(num_seqs, num_heads, num_kv_heads, head_size, kv_fp8 ? 1 : elt, num_ranges, dev, &pl,
-                 num_queries, elt, block_size, extras != nullptr);
+  const PlanShape shape{num_heads, num_kv_heads, head_size, num_queries, kv_fp8 ? 1 : elt, elt, block_size};
+  rc = make_plan(shape, num_seqs, num_ranges, dev, extras != nullptr, &pl);
   if (rc != PA_OK) return rc;
   int32_t* counters = nullptr;
   ScratchHold hold;  // scratch of the library's own, until the launches are queued
@@ -382,7 +221,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   if (extras != nullptr) {
     if ((long long)num_seqs * num_queries * num_heads > 1 << 30)
       return fail(PA_ERR_UNSUPPORTED, "pa_decode: %d sequences of %d rows", num_seqs, num_queries * num_heads);
-    const size_t need = pl.ws_partials + sizeof(int4) * (size_t)num_seqs;
+    const size_t need = walk_bytes(num_seqs, num_heads, num_kv_heads, head_size, pl.R, num_queries);
     if (workspace == nullptr) {
       rc = hold.of_stream(need, stream, &workspace);
       if (rc != PA_OK) return rc;
@@ -548,20 +387,17 @@ size_t decode_workspace_size_q(int num_seqs, int num_heads, int num_kv_heads, in
 }
 
 size_t walk_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size, int num_ranges,
-                           int num_queries, int elt) {
+                           int num_queries, int elt, bool any_block) {
   if (num_queries < 1 || num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
       num_ranges < 0 || num_heads % num_kv_heads != 0)
     return 0;
-  int R = num_ranges;
-  if (R == 0) {
-    DeviceInfo dev{};
-    if (current_device_info(&dev) != PA_OK) return 0;
-    const WalkShape w = walk_shape(num_heads, num_kv_heads, head_size, num_queries, elt);
-    R = default_ranges(dev, w.groups) * w.per_sm;
-  }
-  Plan pl{};
-  workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, R, &pl, num_queries);
-  return pl.ws_partials + sizeof(int4) * (size_t)num_seqs;
+  if (num_ranges > 0) return walk_bytes(num_seqs, num_heads, num_kv_heads, head_size, num_ranges, num_queries);
+  DeviceInfo dev{};
+  if (current_device_info(&dev) != PA_OK) return 0;
+  const PlanShape shape{num_heads, num_kv_heads, head_size, num_queries, elt, elt == 4 ? 4 : 2, kTile};
+  const size_t need = walk_workspace(shape, num_seqs, dev, any_block);
+  clear_error();  // (plans of other block sizes)
+  return need;
 }
 
 size_t decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,

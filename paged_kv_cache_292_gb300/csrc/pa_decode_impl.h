@@ -34,17 +34,10 @@ struct DecodeExtras {
   const float* part_o = nullptr;
 };
 
-// Shape of a walk's CTAs: KV-head groups, consumer warps per KV head, producer
-// warps, CTAs per SM, bytes of a staged K row.
-struct WalkShape {
-  int groups, split, producers, per_sm, row_bytes;
-};
-WalkShape walk_shape(int num_heads, int num_kv_heads, int head_size, int num_queries, int elt);
-
 // Scratch of a call with extras (num_ranges 0: the default; elt: bytes of a pool
-// element).  0 for invalid sizes.
+// element; any_block: not only for blocks that are multiples of 8).  0 for invalid sizes.
 size_t walk_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size, int num_ranges,
-                           int num_queries, int elt);
+                           int num_queries, int elt, bool any_block = true);
 
 // The argument checks every decode call makes.
 int decode_validate(const void* out, const void* query, const void* k_cache, const void* v_cache,

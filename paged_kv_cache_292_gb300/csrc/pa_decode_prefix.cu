@@ -882,8 +882,8 @@ int launch_prefix(const PrefixParams& prm, int device, cudaStream_t stream) {
 
 // Scratch of the walk behind the prefix, whatever the pool's type.
 size_t rest_bytes(int num_seqs, int num_queries, int num_heads, int num_kv_heads, int head_size) {
-  const size_t bf16 = walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 2);
-  const size_t fp8 = walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 1);
+  const size_t bf16 = walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 2, false);
+  const size_t fp8 = walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, 0, num_queries, 1, false);
   return bf16 > fp8 ? bf16 : fp8;
 }
 
@@ -1002,14 +1002,17 @@ int prefix_impl(void* out, const void* query, const void* k_cache, const void* v
     if (prm.work.ctas == 0)
       return fail(PA_ERR_UNSUPPORTED, "pa_decode_prefix: %lld query rows over %d prefix tokens", (long long)rows,
                   prefix_tokens);
-    const WalkShape shape = walk_shape(num_heads, num_kv_heads, head_size, num_queries, kv_fp8 ? 1 : 2);
+    Plan walk{};
+    rc = make_plan(PlanShape{num_heads, num_kv_heads, head_size, num_queries, kv_fp8 ? 1 : 2, 2, block_size}, num_seqs, 0,
+                   dev, true, &walk);
+    if (rc != PA_OK) return rc;
     prm.item_ctas = reinterpret_cast<int2*>(ws + sc.item_ctas);
     prm.context_lens = context_lens;
     prm.num_seqs = num_seqs;
     prm.num_queries = num_queries;
     prm.max_tokens = max_blocks_per_seq * block_size;
-    prm.walk_groups = shape.groups;
-    prm.walk_row_bytes = shape.row_bytes;
+    prm.walk_groups = walk.HG;
+    prm.walk_row_bytes = (int)walk.row_bytes;
     prm.sm_count = dev.sm_count;
     prm.rows = (int)rows;
     prm.group = group;

@@ -10,15 +10,9 @@
 
 #include "pa_decode_kernel.cuh"
 #include "pa_internal.h"
+#include "pa_plan.h"
 
 namespace pa {
-
-struct Plan {
-  int Hg, HG, R, stages, q_slots, split, producers;
-  uint32_t row_bytes, pitch, q_bytes, stage_bytes, smem;
-  uint32_t lines, box_rows, box_bytes;  // tensor-core paths (see DecodeParams)
-  size_t ws_ml, ws_o, ws_partials, ws_counters, ws_total;
-};
 
 // Launch with programmatic stream serialisation: the kernel may become
 // resident while its predecessor on the stream finishes; it calls

@@ -36,3 +36,15 @@ def test_scratch_of_the_librarys_own_under_threads(tmp_path):
     out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert out.returncode == 0, out.stdout + out.stderr
     assert out.stdout.startswith("ok")
+
+
+def test_plans_of_every_batch_shape(tmp_path):
+    """No shape that the entry points take is refused for its launch plan, and every plan fits the SM."""
+    exe = tmp_path / "plan_check"
+    here = os.path.join(ROOT, "tests", "host")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I" + os.path.join(here, "fake"),
+                    "-I" + os.path.join(ROOT, "paged_kv_cache_292_gb300", "csrc"), os.path.join(here, "plan_check.cpp"),
+                    "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert out.returncode == 0, out.stdout + out.stderr
+    assert out.stdout.startswith("ok")
