@@ -90,8 +90,13 @@ struct SeqSpan {
   int c = 0, n = 0;
   int nh = 0, h0 = 0, t0 = 0, first = 0, pre = 0, lo = 0;
 
+#if defined(__CUDA_ARCH__)
+  PA_HD static int smaller(int a, int b) { return min(a, b); }
+  PA_HD static int larger(int a, int b) { return max(a, b); }
+#else
   PA_HD static int smaller(int a, int b) { return a < b ? a : b; }
   PA_HD static int larger(int a, int b) { return a > b ? a : b; }
+#endif
 
   PA_HD void all(int context) {
     c = context;
@@ -137,7 +142,8 @@ PA_HD bool cut_holds(int first, int last, int slot, int state, int ranges) {
 }
 
 // The tile's place in the flat list, beside the 8 bits of flags of its stage: a
-// consumer takes a stage only if it holds the tile that the consumer is at.
+// consumer writes rows for a stage's sequence only if it holds the tile that the
+// consumer is at.
 PA_HD int tile_tag(int64_t x) { return static_cast<int>(static_cast<uint32_t>(x) << 8); }
 PA_HD bool tag_matches(int flags, int64_t x) { return (static_cast<uint32_t>(flags) & ~0xffu) == static_cast<uint32_t>(tile_tag(x)); }
 
