@@ -141,7 +141,9 @@ int pa_decode_ws(void* out, const void* query, const void* k_cache, const void* 
  *                      against it on the device (PA_DEVERR_BLOCK_ID); 0: unchecked
  *                      (bf16 and FP8 pools must then lie in memory that the driver
  *                      knows the extent of: rows beyond the allocation read as
- *                      zeros; PA_ERR_INVALID_ARG if it does not).
+ *                      zeros; PA_ERR_INVALID_ARG if it does not).  Give the size of
+ *                      pools in a reserved address range that is mapped in part:
+ *                      the extent known there is the whole range.
  * workspace            NULL: library-owned scratch (may allocate, see pa_decode).
  * num_ranges           0: one token range per SM (the default).  > 0: split the
  *                      flattened batch into exactly this many ranges (1 = a

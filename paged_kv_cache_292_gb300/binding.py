@@ -200,6 +200,11 @@ def dtype_code(dtype: torch.dtype) -> int:
 
 
 # ---- one-to-one entry points -------------------------------------------------
+#
+# The functions without the prefix pa_ take the pools' size from their shape and always
+# give it to the library, so that tensor maps end with the pools and a block id
+# outside them is skipped and reported (error_flag), never followed;
+# check_block_ids=True says no more than that.
 
 
 def pa_decode(out, query, k_cache, v_cache, block_tables, context_lens, num_seqs, num_heads, num_kv_heads,
@@ -268,7 +273,7 @@ def decode_multi(query, k_cache, v_cache, block_tables, context_lens, scale, out
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     pa_decode_mq(out, query, k_cache, v_cache, block_tables, context_lens, S, Q, H, Hk, D, bs,
                  block_tables.shape[1], float(scale), stream, dtype_code(query.dtype),
-                 NB if check_block_ids else 0, workspace, ws_bytes, num_ranges, error_flag)
+                 NB, workspace, ws_bytes, num_ranges, error_flag)
     return out
 
 
@@ -335,7 +340,7 @@ def decode_append(query, k_new, v_new, k_cache, v_cache, block_tables, context_l
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     pa_decode_append(out, query, k_new, v_new, k_cache, v_cache, block_tables, context_lens, S, H, Hk, D, bs,
                      block_tables.shape[1], float(scale), stream, dtype_code(query.dtype),
-                     NB if check_block_ids else 0, workspace, ws_bytes, num_ranges, error_flag)
+                     NB, workspace, ws_bytes, num_ranges, error_flag)
     return out
 
 
@@ -364,7 +369,7 @@ def decode_multi_append(query, k_new, v_new, k_cache, v_cache, block_tables, con
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     pa_decode_mq_append(out, query, k_new, v_new, k_cache, v_cache, block_tables, context_lens, S, Q, H, Hk, D,
                         bs, block_tables.shape[1], float(scale), stream, dtype_code(query.dtype),
-                        NB if check_block_ids else 0, workspace, ws_bytes, num_ranges, error_flag)
+                        NB, workspace, ws_bytes, num_ranges, error_flag)
     return out
 
 
@@ -381,7 +386,7 @@ def decode_fp8_append(query, k_new, v_new, k_cache, v_cache, block_tables, conte
     _check(load().pa_decode_fp8_append(_ptr(out), _ptr(query), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
                                        _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), S, H, Hk, D, bs,
                                        block_tables.shape[1], float(scale), float(k_scale), float(v_scale),
-                                       _stream(stream), NB if check_block_ids else 0, _ptr(workspace), ws_bytes,
+                                       _stream(stream), NB, _ptr(workspace), ws_bytes,
                                        num_ranges, _ptr(error_flag)))
     return out
 
@@ -397,7 +402,7 @@ def decode(query, k_cache, v_cache, block_tables, context_lens, scale, out=None,
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     pa_decode_ex(out, query, k_cache, v_cache, block_tables, context_lens, S, H, Hk, D, bs,
                  block_tables.shape[1], float(scale), stream, dtype_code(query.dtype),
-                 NB if check_block_ids else 0, workspace, ws_bytes, num_ranges, error_flag)
+                 NB, workspace, ws_bytes, num_ranges, error_flag)
     return out
 
 
@@ -510,7 +515,7 @@ def decode_fp8(query, k_cache, v_cache, block_tables, context_lens, scale, k_sca
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().pa_decode_fp8(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                 _ptr(context_lens), S, H, Hk, D, bs, block_tables.shape[1], float(scale),
-                                float(k_scale), float(v_scale), _stream(stream), NB if check_block_ids else 0,
+                                float(k_scale), float(v_scale), _stream(stream), NB,
                                 _ptr(workspace), ws_bytes, num_ranges, _ptr(error_flag)))
     return out
 
@@ -526,7 +531,7 @@ def decode_fp8_multi(query, k_cache, v_cache, block_tables, context_lens, scale,
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().pa_decode_fp8_mq(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                    _ptr(context_lens), S, Q, H, Hk, D, bs, block_tables.shape[1], float(scale),
-                                   float(k_scale), float(v_scale), _stream(stream), NB if check_block_ids else 0,
+                                   float(k_scale), float(v_scale), _stream(stream), NB,
                                    _ptr(workspace), ws_bytes, num_ranges, _ptr(error_flag)))
     return out
 
@@ -544,7 +549,7 @@ def decode_fp8_multi_append(query, k_new, v_new, k_cache, v_cache, block_tables,
     _check(load().pa_decode_fp8_mq_append(_ptr(out), _ptr(query), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
                                           _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), S, Q, H, Hk, D, bs,
                                           block_tables.shape[1], float(scale), float(k_scale), float(v_scale),
-                                          _stream(stream), NB if check_block_ids else 0, _ptr(workspace), ws_bytes,
+                                          _stream(stream), NB, _ptr(workspace), ws_bytes,
                                           num_ranges, _ptr(error_flag)))
     return out
 
@@ -758,7 +763,7 @@ def decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, out=N
         _used_on(stream, out)
     _call_on(index, load().pa_decode_mod, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
              block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H, Hk, D, bs, MB, scale, softcap, slopes, window,
-             first, prefix, raw, code, NB if check_block_ids else 0, ws, ws_bytes, num_ranges, err)
+             first, prefix, raw, code, NB, ws, ws_bytes, num_ranges, err)
     return out
 
 
@@ -777,7 +782,7 @@ def decode_fp8_mod(query, k_cache, v_cache, block_tables, context_lens, scale, k
         _used_on(stream, out)
     _call_on(index, load().pa_decode_fp8_mod, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H, Hk, D, bs, MB, scale,
-             k_scale, v_scale, softcap, slopes, window, first, prefix, raw, NB if check_block_ids else 0, ws, ws_bytes,
+             k_scale, v_scale, softcap, slopes, window, first, prefix, raw, NB, ws, ws_bytes,
              num_ranges, err)
     return out
 
@@ -824,7 +829,7 @@ def decode_prefix(query, k_cache, v_cache, prefix_table, block_tables, context_l
         _used_on(stream, out)
     _call_on(index, load().pa_decode_prefix, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), prefix_table.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H,
-             Hk, D, bs, prefix_table.numel(), MB, scale, raw, code, NB if check_block_ids else 0, ws, ws_bytes, err)
+             Hk, D, bs, prefix_table.numel(), MB, scale, raw, code, NB, ws, ws_bytes, err)
     return out
 
 
@@ -842,6 +847,6 @@ def decode_fp8_prefix(query, k_cache, v_cache, prefix_table, block_tables, conte
         _used_on(stream, out)
     _call_on(index, load().pa_decode_fp8_prefix, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), prefix_table.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H,
-             Hk, D, bs, prefix_table.numel(), MB, scale, k_scale, v_scale, raw, NB if check_block_ids else 0, ws,
+             Hk, D, bs, prefix_table.numel(), MB, scale, k_scale, v_scale, raw, NB, ws,
              ws_bytes, err)
     return out

@@ -60,13 +60,24 @@ def test_last_block_of_the_allocation(Hk, D, bs, G, Q, fp8):
     outs = []
     for at_end in (True, False):
         k, v = (_pool((NB, bs, Hk, D), dtype, seed, at_end) for seed in (1, 2))
-        args = (q, k, v, table, lens, D**-0.5, *scales)
-        kw = dict(check_block_ids=not at_end)
-        out = [(binding.decode_fp8_multi if fp8 else binding.decode_multi)(*args, **kw)]
-        out.append((binding.decode_fp8_mod if fp8 else binding.decode_mod)(*args, window=5 * bs, **kw))
+        sizes = (S, Q, G * Hk, Hk, D, bs)
+        NBs = 0 if at_end else NB  # no size given: the maps end with the allocation
+        lib, stream = binding.load(), torch.cuda.current_stream().cuda_stream
+        p = lambda x: x.data_ptr()  # noqa: E731
+
+        def run(name, tables, mid, tail):
+            out = torch.full_like(q, float("nan"))
+            dtype_arg = () if fp8 else (binding.PA_BF16,)
+            rc = getattr(lib, ("pa_decode_fp8_" if fp8 else "pa_decode_") + name)(
+                p(out), p(q), p(k), p(v), *(p(t) for t in tables), *sizes, *mid[0], nblk, D**-0.5, *scales, *mid[1],
+                stream, *dtype_arg, NBs, None, 0, *tail)
+            assert rc == binding.PA_OK, lib.pa_last_error()
+            return out
+
+        out = [run("mq", (table, lens), ((), ()), (0, None)),
+               run("mod", (table, lens), ((), (0.0, None, 5 * bs, None, None)), (0, None))]
         if bs % 8 == 0:
-            fn = binding.decode_fp8_prefix if fp8 else binding.decode_prefix
-            out.append(fn(q, k, v, prefix, table, lens, D**-0.5, *scales, **kw))
+            out.append(run("prefix", (prefix, table, lens), ((2,), ()), (None,)))
         torch.cuda.synchronize()
         outs.append(out)
     for a, b in zip(*outs):
