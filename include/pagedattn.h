@@ -105,7 +105,8 @@ extern "C" {
  * device; use pa_decode_ws to supply the scratch and never allocate).  That
  * buffer is shared by every call on the device: calls that may run at the
  * same time on different streams must use pa_decode_ws with scratch of their
- * own.
+ * own, and so must a graph that may run beside other calls.  (The buffer a
+ * captured call has taken is not freed when a larger batch needs another.)
  */
 int pa_decode(void* out, const void* query, const void* k_cache, const void* v_cache,
               const int32_t* block_tables, const int32_t* context_lens, int num_seqs,

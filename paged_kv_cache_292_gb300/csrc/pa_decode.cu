@@ -237,7 +237,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   }
   if (extras != nullptr) {
   } else if (workspace == nullptr) {
-    rc = hold.plain(pl.ws_partials, pl.ws_counters, &workspace, &counters);
+    rc = hold.plain(pl.ws_partials, pl.ws_counters, stream, &workspace, &counters);
     if (rc != PA_OK) return rc;
   } else {
     if (workspace_bytes < pl.ws_total)

@@ -26,6 +26,7 @@ void* g_ws_ptr[kMaxDevices] = {nullptr};
 size_t g_ws_bytes[kMaxDevices] = {0};
 void* g_cnt_ptr[kMaxDevices] = {nullptr};
 size_t g_cnt_bytes[kMaxDevices] = {0};
+bool g_ws_in_graph[kMaxDevices] = {false}, g_cnt_in_graph[kMaxDevices] = {false};
 // ScratchHold::of_stream: a buffer for each of the streams that called last.
 struct KeptScratch {
   unsigned long long stream;  // its id, which no other stream of the process ever gets
@@ -78,16 +79,20 @@ int current_device_info(DeviceInfo* info) {
   return PA_OK;
 }
 
-int ScratchHold::plain(size_t bytes, size_t counter_bytes, void** ptr, int32_t** counters) {
+int ScratchHold::plain(size_t bytes, size_t counter_bytes, void* stream, void** ptr, int32_t** counters) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &status);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
   lock_ = std::unique_lock<std::mutex>(g_scratch_mutex);
   if (g_ws_bytes[dev] < bytes) {
     if (g_ws_ptr[dev] != nullptr) {
-      e = cudaFree(g_ws_ptr[dev]);
+      e = g_ws_in_graph[dev] ? cudaSuccess : cudaFree(g_ws_ptr[dev]);
       g_ws_ptr[dev] = nullptr;
       g_ws_bytes[dev] = 0;
+      g_ws_in_graph[dev] = false;
       if (e != cudaSuccess) return cuda_fail(e, "cudaFree(workspace)");
     }
     const size_t want = align_up(bytes < (1u << 20) ? (1u << 20) : bytes, 1u << 20);
@@ -100,9 +105,10 @@ int ScratchHold::plain(size_t bytes, size_t counter_bytes, void** ptr, int32_t**
   }
   if (g_cnt_bytes[dev] < counter_bytes) {
     if (g_cnt_ptr[dev] != nullptr) {
-      e = cudaFree(g_cnt_ptr[dev]);
+      e = g_cnt_in_graph[dev] ? cudaSuccess : cudaFree(g_cnt_ptr[dev]);
       g_cnt_ptr[dev] = nullptr;
       g_cnt_bytes[dev] = 0;
+      g_cnt_in_graph[dev] = false;
       if (e != cudaSuccess) return cuda_fail(e, "cudaFree(tickets)");
     }
     const size_t want = align_up(counter_bytes < 65536 ? 65536 : counter_bytes, 65536);
@@ -119,6 +125,7 @@ int ScratchHold::plain(size_t bytes, size_t counter_bytes, void** ptr, int32_t**
     g_cnt_ptr[dev] = p;
     g_cnt_bytes[dev] = want;
   }
+  if (status != cudaStreamCaptureStatusNone) g_ws_in_graph[dev] = g_cnt_in_graph[dev] = true;
   *ptr = g_ws_ptr[dev];
   *counters = static_cast<int32_t*>(g_cnt_ptr[dev]);
   return PA_OK;

@@ -41,8 +41,9 @@ class ScratchHold {
  public:
   // Plain decode, current device: scratch grown to at least `bytes`, and a
   // zero-filled buffer of merge tickets (zero-filled again when it grows).
-  // Growing frees the old buffer (cudaFree synchronises the device).
-  int plain(size_t bytes, size_t counter_bytes, void** ptr, int32_t** counters);
+  // Growing frees the old buffers (cudaFree synchronises the device), unless a call
+  // under capture has taken them: a graph keeps their address.
+  int plain(size_t bytes, size_t counter_bytes, void* stream, void** ptr, int32_t** counters);
 
   // The operators beyond plain decode: at least `bytes` of any content, a buffer for
   // each stream, so that calls on two streams do not meet in one.  The buffers of the

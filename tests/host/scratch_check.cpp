@@ -68,7 +68,7 @@ static void call(int id, unsigned long long stream, size_t bytes, bool plain) {
   pa::ScratchHold hold;
   void* p = nullptr;
   int32_t* tickets = nullptr;
-  const int rc = plain ? hold.plain(bytes, 1024, &p, &tickets) : hold.of_stream(bytes, (void*)stream, &p);
+  const int rc = plain ? hold.plain(bytes, 1024, (void*)stream, &p, &tickets) : hold.of_stream(bytes, (void*)stream, &p);
   if (rc != 0) return fault("no scratch");
   for (int launch = 0; launch < 3; ++launch) {
     {
@@ -105,6 +105,25 @@ int main() {
     pa::ScratchHold hold;
     void* p = nullptr;
     if (hold.of_stream(64, (void*)99, &p) == 0) fault("given to a stream under capture");
+  }
+  {  // what a captured call has taken stays, however the scratch grows
+    void *p = nullptr, *q = nullptr;
+    int32_t *tickets = nullptr, *more = nullptr;
+    {
+      pa::ScratchHold hold;
+      hold.plain(1000, 1000, (void*)99, &p, &tickets);
+    }
+    {
+      pa::ScratchHold hold;
+      hold.plain((size_t)1 << 30, (size_t)1 << 20, (void*)7, &q, &more);
+    }
+    if (p == q || tickets == more) fault("not grown");
+    if (memory.count(p) == 0 || memory.count(tickets) == 0) fault("freed under a graph");
+    {
+      pa::ScratchHold hold;
+      hold.plain((size_t)2 << 30, (size_t)2 << 20, (void*)7, &p, &tickets);
+    }
+    if (memory.count(q) != 0 || memory.count(more) != 0) fault("kept without a graph");
   }
   if (faults) return 1;
   printf("ok, %d times synchronised\n", (int)syncs);
