@@ -185,6 +185,23 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+def _made_for(stream, device, make):
+    """``make()``, a tensor that a call on ``stream`` is to write: from that stream's memory, to which nothing still
+    queued on the current stream writes, and in use on the current stream, whose work reads it, when it is freed."""
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    if stream.cuda_stream == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(current)
+    return t
+
+
 def _check(rc: int) -> None:
     if rc != PA_OK:
         msg = load().pa_last_error()
@@ -269,7 +286,7 @@ def decode_multi(query, k_cache, v_cache, block_tables, context_lens, scale, out
     S, Q, H, D = query.shape
     NB, bs, Hk, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(query)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     pa_decode_mq(out, query, k_cache, v_cache, block_tables, context_lens, S, Q, H, Hk, D, bs,
                  block_tables.shape[1], float(scale), stream, dtype_code(query.dtype),
@@ -336,7 +353,7 @@ def decode_append(query, k_new, v_new, k_cache, v_cache, block_tables, context_l
     S, H, D = query.shape
     NB, bs, Hk, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(query)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     pa_decode_append(out, query, k_new, v_new, k_cache, v_cache, block_tables, context_lens, S, H, Hk, D, bs,
                      block_tables.shape[1], float(scale), stream, dtype_code(query.dtype),
@@ -365,7 +382,7 @@ def decode_multi_append(query, k_new, v_new, k_cache, v_cache, block_tables, con
     S, Q, H, D = query.shape
     NB, bs, Hk, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(query)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     pa_decode_mq_append(out, query, k_new, v_new, k_cache, v_cache, block_tables, context_lens, S, Q, H, Hk, D,
                         bs, block_tables.shape[1], float(scale), stream, dtype_code(query.dtype),
@@ -381,7 +398,7 @@ def decode_fp8_append(query, k_new, v_new, k_cache, v_cache, block_tables, conte
     S, H, D = query.shape
     NB, bs, Hk, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(query)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().pa_decode_fp8_append(_ptr(out), _ptr(query), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
                                        _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), S, H, Hk, D, bs,
@@ -398,7 +415,7 @@ def decode(query, k_cache, v_cache, block_tables, context_lens, scale, out=None,
     S, H, D = query.shape
     NB, bs, Hk, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(query)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     pa_decode_ex(out, query, k_cache, v_cache, block_tables, context_lens, S, H, Hk, D, bs,
                  block_tables.shape[1], float(scale), stream, dtype_code(query.dtype),
@@ -511,7 +528,7 @@ def decode_fp8(query, k_cache, v_cache, block_tables, context_lens, scale, k_sca
     S, H, D = query.shape
     NB, bs, Hk, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(query)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().pa_decode_fp8(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                 _ptr(context_lens), S, H, Hk, D, bs, block_tables.shape[1], float(scale),
@@ -527,7 +544,7 @@ def decode_fp8_multi(query, k_cache, v_cache, block_tables, context_lens, scale,
     S, Q, H, D = query.shape
     NB, bs, Hk, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(query)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().pa_decode_fp8_mq(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                    _ptr(context_lens), S, Q, H, Hk, D, bs, block_tables.shape[1], float(scale),
@@ -544,7 +561,7 @@ def decode_fp8_multi_append(query, k_new, v_new, k_cache, v_cache, block_tables,
     S, Q, H, D = query.shape
     NB, bs, Hk, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(query)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().pa_decode_fp8_mq_append(_ptr(out), _ptr(query), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
                                           _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), S, Q, H, Hk, D, bs,
@@ -590,13 +607,6 @@ def _stream_on(stream, index):
     return int(stream)
 
 
-def _used_on(stream, *ts):
-    """Tensors made here for a call on another stream than the allocating one outlive that call."""
-    if isinstance(stream, torch.cuda.Stream):
-        for t in ts:
-            t.record_stream(stream)
-
-
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
@@ -636,14 +646,11 @@ def tables_step(block_tables, context_lens, new_lens, free_blocks, free_count, b
     if context_lens.numel() != S or new_lens.numel() != S or free_count.numel() != 1:
         raise ValueError("context_lens and new_lens must have one entry per table row, free_count one entry")
     if context_lens_out is None:
-        context_lens_out = context_lens.new_empty(S)
-        _used_on(stream, context_lens_out)
+        context_lens_out = _made_for(stream, context_lens.device, lambda: context_lens.new_empty(S))
     if free_count_out is None:
-        free_count_out = context_lens.new_empty(1)
-        _used_on(stream, free_count_out)
+        free_count_out = _made_for(stream, context_lens.device, lambda: context_lens.new_empty(1))
     if seq_starts is None:
-        seq_starts = context_lens.new_empty(S + 1)
-        _used_on(stream, seq_starts)
+        seq_starts = _made_for(stream, context_lens.device, lambda: context_lens.new_empty(S + 1))
     if context_lens_out.numel() != S or free_count_out.numel() != 1 or seq_starts.numel() != S + 1:
         raise ValueError("context_lens_out, free_count_out and seq_starts must have S, 1 and S + 1 entries")
     _call_on(index, load().pa_tables_step, block_tables.data_ptr(), context_lens_out.data_ptr(),
@@ -759,8 +766,7 @@ def decode_mod(query, k_cache, v_cache, block_tables, context_lens, scale, out=N
     ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
     raw = _stream_on(stream, index)
     if out is None:
-        out = torch.empty_like(query)
-        _used_on(stream, out)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     _call_on(index, load().pa_decode_mod, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
              block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H, Hk, D, bs, MB, scale, softcap, slopes, window,
              first, prefix, raw, code, NB, ws, ws_bytes, num_ranges, err)
@@ -778,8 +784,7 @@ def decode_fp8_mod(query, k_cache, v_cache, block_tables, context_lens, scale, k
     ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
     raw = _stream_on(stream, index)
     if out is None:
-        out = torch.empty_like(query)
-        _used_on(stream, out)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     _call_on(index, load().pa_decode_fp8_mod, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H, Hk, D, bs, MB, scale,
              k_scale, v_scale, softcap, slopes, window, first, prefix, raw, NB, ws, ws_bytes,
@@ -825,8 +830,7 @@ def decode_prefix(query, k_cache, v_cache, prefix_table, block_tables, context_l
     ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
     raw = _stream_on(stream, index)
     if out is None:
-        out = torch.empty_like(query)
-        _used_on(stream, out)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     _call_on(index, load().pa_decode_prefix, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), prefix_table.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H,
              Hk, D, bs, prefix_table.numel(), MB, scale, raw, code, NB, ws, ws_bytes, err)
@@ -843,8 +847,7 @@ def decode_fp8_prefix(query, k_cache, v_cache, prefix_table, block_tables, conte
     ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
     raw = _stream_on(stream, index)
     if out is None:
-        out = torch.empty_like(query)
-        _used_on(stream, out)
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     _call_on(index, load().pa_decode_fp8_prefix, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), prefix_table.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H,
              Hk, D, bs, prefix_table.numel(), MB, scale, k_scale, v_scale, raw, NB, ws,
