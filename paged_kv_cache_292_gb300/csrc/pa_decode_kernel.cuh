@@ -2446,6 +2446,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
     // at the first tile of a segment.
     const int32_t* bt_row = nullptr;
     int nblk = 0, cb = 0, cur = -1, nxt = -1;
+    bool bad_ids = false;  // block ids outside the pool among this lane's
     auto table_entry = [&](int idx) -> int { return idx < nblk ? __ldg(bt_row + idx) : -1; };
     for (long long x = a; x < b; ++x) {
       bool new_seq = (x == a);
@@ -2545,10 +2546,11 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
       // A box is copied if some query sees one of its rows.
       if constexpr (WALK == kWalkMod)
         ok = lead && ((nvalid >> t) & (kMmaPath ? (1 << p.box_rows) - 1 : 1)) != 0;
-      if (ok && p.num_physical_blocks > 0 && (phys < 0 || phys >= p.num_physical_blocks)) {
-        report(p.error_flag, PA_DEVERR_BLOCK_ID);
-        ok = false;
-      }
+      // Reported behind the loop: a branch here would be on the way of every tile's copies.
+      const bool bad =
+          ok && p.num_physical_blocks > 0 && static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_physical_blocks);
+      bad_ids |= bad;
+      ok = ok && !bad;
       // Tensor-core paths: lane t (t a multiple of box_rows) copies tile rows
       // t .. t + box_rows - 1, which lie in one block, as one tensor box; rows
       // past the context in that block come along and are masked by the
@@ -2572,8 +2574,8 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
       const bool stall = x == p.stall_tile;
       if (WALK == kWalkAll && newfirst >= 0 && !is_v && t >= newfirst && t < nvalid) {
         // Pool row of this tile row's new token; a failed block check leaves it unwritten.
-        const bool bad = p.num_physical_blocks > 0 && (phys < 0 || phys >= p.num_physical_blocks);
-        stage_rows[st * kTile + t] = bad ? -1 : row;
+        const bool none = p.num_physical_blocks > 0 && (phys < 0 || phys >= p.num_physical_blocks);
+        stage_rows[st * kTile + t] = none ? -1 : row;
       }
       __syncwarp();
       if (lane == 0 && !stall) {
@@ -2601,6 +2603,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
         ph ^= 1u;
       }
     }
+    if (bad_ids) report(p.error_flag, PA_DEVERR_BLOCK_ID);
     named_barrier_sync(1, nthreads);  // every warp has left its tile loop
     if (*abort_flag != 0 && lane == 0) {
       // A wait ran out, so the loops ended early and copies this warp started
