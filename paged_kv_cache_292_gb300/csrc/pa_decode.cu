@@ -37,9 +37,8 @@ EncodeTiledFn encode_tiled_fn() {
 }
 
 // A tensor map that goes on where the memory ends is not safe even if every box lies in
-// the pool: random multi-query calls over maps of 2^31 rows, kept from call to call by
-// the pools' addresses, ended with an illegal address about once in 2000, with maps that
-// end with the pools none of 86000 did.
+// the pool: random multi-query calls over maps of 2^31 rows ended with an illegal
+// address about once in 2000, with maps that end with the pools none of 86000 did.
 uint64_t rows_of_pools(const void* k, const void* v, uint64_t row_bytes) {
   static const PFN_cuPointerGetAttributes_v7000 attributes_of = [] {
     void* f = nullptr;
@@ -58,7 +57,9 @@ uint64_t rows_of_pools(const void* k, const void* v, uint64_t row_bytes) {
     CUpointer_attribute what[2] = {CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
     void* out[2] = {&start, &size};
     const CUdeviceptr at = reinterpret_cast<CUdeviceptr>(p);
-    if (attributes_of == nullptr || attributes_of(2, what, out, at) != CUDA_SUCCESS) size = 0;
+    const CUresult r = attributes_of == nullptr ? CUDA_ERROR_NOT_FOUND
+                                                : in_context([&] { return attributes_of(2, what, out, at); });
+    if (r != CUDA_SUCCESS) size = 0;
     const uint64_t mine = rows_behind(start, size, at, row_bytes);
     if (mine == 0) {
       fail(PA_ERR_INVALID_ARG, "pa_decode: the driver does not know the pools' memory; num_physical_blocks is needed");
@@ -126,10 +127,12 @@ int make_tensor_maps(DecodeParams* prm, const Plan& pl, int num_kv_heads, int he
   const cuuint32_t box[4] = {kLine, pl.lines, 1u, pl.box_rows};
   const cuuint32_t estride[4] = {1u, 1u, 1u, 1u};
   for (int i = 0; i < 2; ++i) {
-    const CUresult r = enc(i ? &prm->tm_v : &prm->tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
-                           const_cast<void*>(i ? prm->v_cache : prm->k_cache), dims, strides, box,
-                           estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = in_context([&] {
+      return enc(i ? &prm->tm_v : &prm->tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+                 const_cast<void*>(i ? prm->v_cache : prm->k_cache), dims, strides, box,
+                 estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
     if (r != CUDA_SUCCESS)
       return fail(PA_ERR_CUDA, "pa_decode: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
   }

@@ -858,11 +858,13 @@ int make_maps(PrefixParams* prm, const void* k, const void* v, uint64_t pool_row
   const cuuint64_t dims[3] = {chunk, row / chunk, pool_rows}, strides[2] = {chunk * elt, row * elt};
   const cuuint32_t box[3] = {(cuuint32_t)chunk, 1, (cuuint32_t)prm->box_rows}, estride[3] = {1, 1, 1};
   for (int i = 0; i < 2; ++i) {
-    const CUresult r = enc(i ? &prm->tm_v : &prm->tm_k,
-                           kv_fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                           const_cast<void*>(i ? v : k), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           kv_fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = in_context([&] {
+      return enc(i ? &prm->tm_v : &prm->tm_k,
+                 kv_fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                 const_cast<void*>(i ? v : k), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 kv_fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
     if (r != CUDA_SUCCESS)
       return fail(PA_ERR_CUDA, "pa_decode_prefix: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
   }

@@ -60,6 +60,17 @@ int launch_typed(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t 
 using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
 EncodeTiledFn encode_tiled_fn();
 
+// `call()`, a call into the driver; where no context is current, as in a host thread
+// that has made no CUDA call yet, once more with the device's own.
+template <typename Call>
+CUresult in_context(Call call) {
+  const CUresult r = call();
+  int device = 0;
+  if (r != CUDA_ERROR_INVALID_CONTEXT || cudaGetDevice(&device) != cudaSuccess || cudaSetDevice(device) != cudaSuccess)
+    return r;
+  return call();
+}
+
 // Token rows for the tensor maps of two pools whose size the caller has not given:
 // those the pools' allocations hold behind the pools' addresses, at most 2^31.  0 with an
 // error recorded if the driver does not know the memory.

@@ -48,7 +48,7 @@ struct PrefixWork {
     const uint32_t d = unit - start, t = weight(item) == 2 ? (d + 1) / 2 : d;
     return (int)(t < (uint32_t)tiles ? t : tiles);
   }
-  PA_HD int cta_of(int item, int tile) const {
+  PA_HD int cta_of(int item, int tile) const {  // (for the host check of the list)
     return (int)range_of_tile(item_start(item) + (uint32_t)tile * weight(item), total(), ctas);
   }
   PA_HD int slots() const { return ctas + items(); }

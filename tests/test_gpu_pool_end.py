@@ -83,3 +83,48 @@ def test_last_block_of_the_allocation(Hk, D, bs, G, Q, fp8):
     for a, b in zip(*outs):
         assert torch.isfinite(a.float()).all()
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["mq", "mod", "prefix"])
+@pytest.mark.parametrize("sized", [False, True])
+def test_first_call_of_a_thread(name, sized):
+    """A caller's workspace, from a host thread that has made no CUDA call before."""
+    import threading
+
+    S, Q, Hk, G, D, bs, nblk = 2, 1, 2, 4, 64, 16, 5
+    H, NB = G * Hk, S * nblk
+    k, v = (_pool((NB, bs, Hk, D), torch.bfloat16, seed, True) for seed in (1, 2))
+    table = torch.arange(NB, dtype=torch.int32).view(S, nblk)
+    table[1, :2] = table[0, :2].clone()
+    prefix, table = table[0, :2].contiguous().cuda(), table.cuda()
+    lens = torch.full((S,), nblk * bs, dtype=torch.int32).cuda()
+    q = torch.randn(S, Q, H, D).to(torch.bfloat16).cuda()
+    out = torch.full_like(q, float("nan"))
+    if name == "mq":
+        want = binding.decode_multi(q, k, v, table, lens, D**-0.5)
+        need, tables, blocks, mods, tail = (binding.pa_decode_mq_workspace_size(S, Q, H, Hk, D), (table, lens), (), (),
+                                            (0, None))
+    elif name == "mod":
+        want = binding.decode_mod(q, k, v, table, lens, D**-0.5, window=50)
+        need = binding.pa_decode_mod_workspace_size(S, Q, H, Hk, D, binding.PA_BF16)
+        tables, blocks, mods, tail = (table, lens), (), (0.0, None, 50, None, None), (0, None)
+    else:
+        want = binding.decode_prefix(q, k, v, prefix, table, lens, D**-0.5)
+        need = binding.pa_decode_prefix_workspace_size(S, Q, H, Hk, D)
+        tables, blocks, mods, tail = (prefix, table, lens), (2,), (), (None,)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    pointers = [x.data_ptr() for x in (out, q, k, v, *tables)]
+    lib, said = binding.load(), []
+
+    def call():
+        said.append(getattr(lib, "pa_decode_" + name)(*pointers, S, Q, H, Hk, D, bs, *blocks, nblk, D**-0.5, *mods, None,
+                                                      binding.PA_BF16, NB if sized else 0, ws.data_ptr(), need, *tail))
+        said.append(lib.pa_last_error())
+
+    thread = threading.Thread(target=call)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert said[0] == binding.PA_OK, said
+    assert torch.equal(out, want)
