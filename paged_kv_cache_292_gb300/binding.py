@@ -131,6 +131,12 @@ _SIGS = {
     ),
     "pa_decode_prefix_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "pa_tables_step": (_I, [_P] * 10 + [_I] * 6 + [_P, _P]),
+    "pa_prefill": (_I, [_P] * 7 + [_I] * 7 + [ctypes.c_float, _P, _I, _I, _P, _SZ, _P]),
+    "pa_prefill_workspace_size": (_SZ, [_I]),
+    "pa_prefill_int8": (_I, [_P] * 9 + [_I] * 7 + [ctypes.c_float, _P, _I, _P, _SZ, _P]),
+    "pa_decode_int8": (_I, [_P] * 8 + [_I] * 7 + [ctypes.c_float, _P, _I, _P, _SZ, _P]),
+    "pa_write_cache_int8": (_I, [_P] * 7 + [_I] * 5 + [_P, _I, _P]),
+    "pa_read_cache_int8": (_I, [_P] * 9 + [_I] * 7 + [_P, _I, _P]),
     "pa_version": (_I, []),
     "pa_test_stall_copy": (_I, [ctypes.c_longlong, ctypes.c_uint]),
 }
@@ -852,4 +858,179 @@ def decode_fp8_prefix(query, k_cache, v_cache, prefix_table, block_tables, conte
              v_cache.data_ptr(), prefix_table.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H,
              Hk, D, bs, prefix_table.numel(), MB, scale, k_scale, v_scale, raw, NB, ws,
              ws_bytes, err)
+    return out
+
+
+# ---- chunks of new tokens, and the int8 cache -----------------------------------
+
+
+def pa_prefill(out, query, k_cache, v_cache, block_tables, context_lens, seq_starts, num_tokens, num_seqs, num_heads,
+               num_kv_heads, head_size, block_size, max_blocks_per_seq, scale, stream=None, dtype=None,
+               num_physical_blocks=0, workspace=None, workspace_bytes=0, error_flag=None):
+    dtype = dtype_code(query.dtype) if dtype is None else dtype
+    _check(load().pa_prefill(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                             _ptr(context_lens), _ptr(seq_starts), num_tokens, num_seqs, num_heads, num_kv_heads,
+                             head_size, block_size, max_blocks_per_seq, scale, _stream(stream), dtype,
+                             num_physical_blocks, _ptr(workspace), workspace_bytes, _ptr(error_flag)))
+
+
+def pa_prefill_int8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, seq_starts,
+                    num_tokens, num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale,
+                    stream=None, num_physical_blocks=0, workspace=None, workspace_bytes=0, error_flag=None):
+    _check(load().pa_prefill_int8(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+                                  _ptr(v_scales), _ptr(block_tables), _ptr(context_lens), _ptr(seq_starts),
+                                  num_tokens, num_seqs, num_heads, num_kv_heads, head_size, block_size,
+                                  max_blocks_per_seq, scale, _stream(stream), num_physical_blocks, _ptr(workspace),
+                                  workspace_bytes, _ptr(error_flag)))
+
+
+def pa_decode_int8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, num_seqs,
+                   num_queries, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale,
+                   stream=None, num_physical_blocks=0, workspace=None, workspace_bytes=0, error_flag=None):
+    _check(load().pa_decode_int8(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+                                 _ptr(v_scales), _ptr(block_tables), _ptr(context_lens), num_seqs, num_queries,
+                                 num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale,
+                                 _stream(stream), num_physical_blocks, _ptr(workspace), workspace_bytes,
+                                 _ptr(error_flag)))
+
+
+def pa_prefill_workspace_size(head_size) -> int:
+    return int(load().pa_prefill_workspace_size(head_size))
+
+
+def pa_write_cache_int8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scales, num_tokens, num_kv_heads,
+                        head_size, block_size, num_physical_blocks, stream=None, src_dtype=None, error_flag=None):
+    src_dtype = dtype_code(k_new.dtype) if src_dtype is None else src_dtype
+    _check(load().pa_write_cache_int8(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
+                                      _ptr(k_scales), _ptr(v_scales), num_tokens, num_kv_heads, head_size, block_size,
+                                      num_physical_blocks, _stream(stream), src_dtype, _ptr(error_flag)))
+
+
+def pa_read_cache_int8(k_out, v_out, k_cache, v_cache, k_scales, v_scales, block_tables, first_tokens, seq_starts,
+                       num_tokens, num_seqs, num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                       num_physical_blocks, stream=None, dst_dtype=None, error_flag=None):
+    dst_dtype = dtype_code(k_out.dtype) if dst_dtype is None else dst_dtype
+    _check(load().pa_read_cache_int8(_ptr(k_out), _ptr(v_out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+                                     _ptr(v_scales), _ptr(block_tables), _ptr(first_tokens), _ptr(seq_starts),
+                                     num_tokens, num_seqs, num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                                     num_physical_blocks, _stream(stream), dst_dtype, _ptr(error_flag)))
+
+
+def _int8_pools(index, k_cache, v_cache, k_scales, v_scales):
+    """(NB, bs, Hk, D) of int8 pools with their scales."""
+    _on(index, torch.int8, "k_cache and v_cache", k_cache, v_cache)
+    _on(index, torch.float32, "k_scales and v_scales", k_scales, v_scales)
+    NB, bs, Hk, D = k_cache.shape
+    if v_cache.shape != k_cache.shape or k_scales.shape != (NB, Hk, bs) or v_scales.shape != (NB, Hk, bs):
+        raise ValueError("shapes of the pools and their scales (blocks, KV heads, block size) do not go together")
+    return NB, bs, Hk, D
+
+
+def write_cache_int8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scales, stream=None, *,
+                     error_flag=None):
+    """Quantise k_new/v_new[T, Hk, D] (bf16 or f32) into int8 pools at slot_mapping[T] (int64), with a scale for
+    every token and KV head in k_scales/v_scales[NB, Hk, bs] (as in ``pa_write_cache_int8``)."""
+    index = _device_of(k_new)
+    NB, bs, Hk, D = _int8_pools(index, k_cache, v_cache, k_scales, v_scales)
+    code = dtype_code(k_new.dtype)
+    _on(index, k_new.dtype, "k_new and v_new", k_new, v_new)
+    _on(index, torch.int64, "slot_mapping", slot_mapping)
+    _on(index, torch.int32, "error_flag", error_flag)
+    T = slot_mapping.numel()
+    if k_new.shape != (T, Hk, D) or v_new.shape != (T, Hk, D):
+        raise ValueError("k_new and v_new must have a row [Hk, D] for every slot")
+    _call_on(index, load().pa_write_cache_int8, k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(),
+             k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), T, Hk, D, bs, NB,
+             _stream_on(stream, index), code, None if error_flag is None else error_flag.data_ptr())
+
+
+def read_cache_int8(k_cache, v_cache, k_scales, v_scales, block_tables, seq_starts, k_out, v_out, *,
+                    first_tokens=None, stream=None, error_flag=None):
+    """Tokens first_tokens[s] + i of every sequence into rows seq_starts[s] + i of k_out/v_out[T, Hk, D] (bf16 or f32;
+    as in ``pa_read_cache_int8``).  Returns (k_out, v_out)."""
+    index = _device_of(k_cache)
+    NB, bs, Hk, D = _int8_pools(index, k_cache, v_cache, k_scales, v_scales)
+    code = dtype_code(k_out.dtype)
+    _on(index, k_out.dtype, "k_out and v_out", k_out, v_out)
+    _on(index, torch.int32, "tables, lengths and starts", block_tables, seq_starts, first_tokens, error_flag)
+    S, MB = block_tables.shape
+    T = k_out.shape[0]
+    if k_out.shape != (T, Hk, D) or v_out.shape != (T, Hk, D):
+        raise ValueError("k_out and v_out must be [tokens, Hk, D]")
+    if seq_starts.numel() != S + 1 or (first_tokens is not None and first_tokens.numel() != S):
+        raise ValueError("seq_starts must have S + 1 entries, first_tokens S")
+    _call_on(index, load().pa_read_cache_int8, k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(),
+             v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+             None if first_tokens is None else first_tokens.data_ptr(), seq_starts.data_ptr(), T, S, Hk, D, bs, MB, NB,
+             _stream_on(stream, index), code, None if error_flag is None else error_flag.data_ptr())
+    return k_out, v_out
+
+
+def _chunk(query, k_cache, v_cache, block_tables, context_lens, seq_starts, out, pool_dtype):
+    """(device index, T, S, H, D, NB, bs, Hk, MB) of a ragged step over paged pools, query [T, H, D]."""
+    index = _device_of(query)
+    _on(index, query.dtype, "query and out", query, out)
+    _on(index, pool_dtype, "k_cache and v_cache", k_cache, v_cache)
+    _on(index, torch.int32, "tables, lengths and starts", block_tables, context_lens, seq_starts)
+    T, H, D = query.shape
+    NB, bs, Hk, Dk = k_cache.shape
+    S, MB = block_tables.shape
+    if Dk != D or v_cache.shape != k_cache.shape or context_lens.numel() != S or seq_starts.numel() != S + 1:
+        raise ValueError("shapes of query, pools, block_tables, context_lens and seq_starts do not go together")
+    if out is not None and out.shape != query.shape:
+        raise ValueError("out must have query's shape")
+    return index, T, S, H, D, NB, bs, Hk, MB
+
+
+def prefill(query, k_cache, v_cache, block_tables, context_lens, seq_starts, scale, out=None, stream=None, *,
+            workspace=None, error_flag=None):
+    """Causal attention of every sequence's newest tokens, rows seq_starts[s] .. seq_starts[s + 1] - 1 of
+    query[T, H, D], over its paged keys and values (as in ``pa_prefill``).  Returns out[T, H, D], whose rows outside
+    the sequences' are left as they are."""
+    index, T, S, H, D, NB, bs, Hk, MB = _chunk(query, k_cache, v_cache, block_tables, context_lens, seq_starts, out,
+                                               query.dtype)
+    code = dtype_code(query.dtype)
+    ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
+    raw = _stream_on(stream, index)
+    if out is None:
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
+    _call_on(index, load().pa_prefill, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+             block_tables.data_ptr(), context_lens.data_ptr(), seq_starts.data_ptr(), T, S, H, Hk, D, bs, MB, scale,
+             raw, code, NB, ws, ws_bytes, err)
+    return out
+
+
+def prefill_int8(query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, seq_starts, scale, out=None,
+                 stream=None, *, workspace=None, error_flag=None):
+    """``prefill`` over int8 pools with their scales (as in ``pa_prefill_int8``); query and out bf16."""
+    if query.dtype is not torch.bfloat16:
+        raise ValueError(f"query must be {torch.bfloat16}, got {query.dtype}")
+    index, T, S, H, D, NB, bs, Hk, MB = _chunk(query, k_cache, v_cache, block_tables, context_lens, seq_starts, out,
+                                               torch.int8)
+    _int8_pools(index, k_cache, v_cache, k_scales, v_scales)
+    ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
+    raw = _stream_on(stream, index)
+    if out is None:
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
+    _call_on(index, load().pa_prefill_int8, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+             k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+             seq_starts.data_ptr(), T, S, H, Hk, D, bs, MB, scale, raw, NB, ws, ws_bytes, err)
+    return out
+
+
+def decode_int8(query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out=None, stream=None,
+                *, workspace=None, error_flag=None):
+    """One step over int8 pools, the same number of new tokens for every sequence (as in ``pa_decode_int8``); query and
+    out [S, H, D] or [S, Q, H, D], bf16."""
+    if query.dtype is not torch.bfloat16:
+        raise ValueError(f"query must be {torch.bfloat16}, got {query.dtype}")
+    index, S, Q, H, D, NB, bs, Hk, MB = _step(query, k_cache, v_cache, block_tables, context_lens, out, torch.int8)
+    _int8_pools(index, k_cache, v_cache, k_scales, v_scales)
+    ws, ws_bytes, err = _scratch_pointers(index, workspace, error_flag)
+    raw = _stream_on(stream, index)
+    if out is None:
+        out = _made_for(stream, query.device, lambda: torch.empty_like(query))
+    _call_on(index, load().pa_decode_int8, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+             k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H, Hk,
+             D, bs, MB, scale, raw, NB, ws, ws_bytes, err)
     return out

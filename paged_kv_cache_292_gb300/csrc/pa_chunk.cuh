@@ -1,0 +1,329 @@
+// Chunk attention's parts that its kernels share: a call's arguments, the walk of a
+// CTA over its range of the list (pa_chunk_work.h), and the join of what range
+// boundaries cut.
+#pragma once
+
+#include "../../include/pa_int8_cache.h"
+#include "pa_chunk_work.h"
+#include "pa_launch.cuh"
+
+namespace pa {
+
+// A call of any of the entry points.
+struct ChunkCall {
+  void* out;
+  const void* query;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scales;  // int8
+  const float* v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* seq_starts;
+  int num_tokens;
+  int num_queries;  // > 0: tokens of every sequence, instead of seq_starts and num_tokens
+  int num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq;
+  float scale;
+  void* stream;
+  int dtype;
+  bool int8;
+  int num_physical_blocks;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* error_flag;
+};
+
+constexpr int kLeastUnits = 4;  // units of a CTA's range, where there are as many
+
+struct ChunkParams {
+  CUtensorMap tm_k, tm_v;  // (64 elements, chunk of 64 within a token row, token row); int8: (D, KV head, token row)
+  const void* q;
+  void* out;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scales;  // [block][KV head][row of the block]
+  const float* v_scales;
+  const int32_t* tables;
+  const int32_t* context_lens;
+  const int32_t* seq_starts;  // nullptr: num_queries tokens each
+  int32_t* error_flag;
+  float* part_ml;  // [2 * CTAs][256][2]
+  float* part_o;   // [2 * CTAs][2][D / 4][128][4]: a thread's row side by side with its neighbours'
+  int4* cuts;      // [CTAs]: (sequence, head, pair, first tile) in which a CTA's range begins
+  int num_tokens, num_seqs, num_queries, num_heads, kv_heads, group, tile_tokens;
+  int block_size, max_blocks, max_tokens, num_physical_blocks, box_rows;
+  // bf16 and int8: scores are scale_log2 * <(q & q_keep) ^ q_flip, k>: a negative scale changes the
+  // queries' signs and a scale of zero makes them zero, so that scale_log2 > 0
+  // and the largest product is the largest score.
+  float scale_log2;  // (fp32: with its sign)
+  uint32_t q_keep, q_flip;
+  unsigned long long wait_limit_ns;
+  long long stall_unit;  // tests of the bounded waits: unit of the list whose tile's copies are withheld
+};
+
+// fp32 pools (pa_prefill_f32.cu): queues both launches.
+int launch_chunks_f32(const ChunkParams& prm, const DeviceInfo& dev, cudaStream_t stream, int head_size);
+
+// (what follows has internal linkage: every translation unit has its own copy)
+namespace {
+
+// A sequence's rows and lengths, inside the buffers whatever the arrays hold.
+struct ChunkRow {
+  int row0, n, ctx;
+};
+__device__ __forceinline__ ChunkRow chunk_row(const ChunkParams& p, int s, bool report_it) {
+  ChunkRow r;
+  if (p.seq_starts == nullptr) {
+    r.row0 = s * p.num_queries;
+    r.n = p.num_queries;
+  } else {
+    const int a = __ldg(p.seq_starts + s), b = __ldg(p.seq_starts + s + 1);
+    r.row0 = min(max(a, 0), p.num_tokens);
+    const int end = min(max(b, 0), p.num_tokens);
+    r.n = max(end - r.row0, 0);
+    if (report_it && (a != r.row0 || b != end || b < a)) report(p.error_flag, PA_DEVERR_CONTEXT_LEN);
+  }
+  const int c = __ldg(p.context_lens + s);
+  r.ctx = min(max(c, 0), p.max_tokens);
+  if (report_it && c != r.ctx) report(p.error_flag, PA_DEVERR_CONTEXT_LEN);
+  return r;
+}
+
+// The items of a CTA's range, one after another; every role walks them.
+struct ChunkItems {
+  int64_t ua, ub, start;  // the range, and the item's first unit
+  int seq, head, pair;
+  ChunkRow row;
+  ChunkSeq cs;
+  int t0, t1, tiles, weight;
+
+  __device__ __forceinline__ void load(const ChunkParams& p) {
+    row = chunk_row(p, seq, false);
+    cs = ChunkSeq{row.n, row.ctx - row.n, p.tile_tokens};
+  }
+  __device__ __forceinline__ void set() {
+    tiles = cs.tiles(pair);
+    weight = cs.weight(pair);
+    t0 = chunk_tile_at(ua - start, weight, tiles);
+    t1 = chunk_tile_at(ub - start, weight, tiles);
+  }
+  // False behind the range's last item.
+  __device__ __forceinline__ bool next(const ChunkParams& p) {
+    start += (int64_t)tiles * weight;
+    if (start >= ub) return false;
+    if (++pair == cs.pairs()) {
+      pair = 0;
+      if (++head == p.kv_heads) {
+        head = 0;
+        do {
+          if (++seq >= p.num_seqs) return false;
+          load(p);
+        } while (row.n == 0);
+      }
+    }
+    set();
+    return true;
+  }
+  __device__ __forceinline__ bool two() const { return weight == 2; }
+  // First and end of the tiles of softmax group w, `step()` apart.
+  __device__ __forceinline__ int first(int w) const { return t0 + (two() ? 0 : w); }
+  __device__ __forceinline__ int end(int w) const { return two() && w == 0 ? min(t1, cs.tiles_first(pair)) : t1; }
+  __device__ __forceinline__ int step() const { return two() ? 1 : 2; }
+};
+
+// This CTA's range of the list and the item that it begins in, found by all of its threads
+// (`shared`: kThreads / 32 + 4 long long).  False: no range for it.
+template <int kThreads>
+__device__ __forceinline__ bool chunk_begin(const ChunkParams& p, ChunkItems* at, long long* shared) {
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+  long long *sums = shared, *found = shared + kWarps;  // sequence, its first unit; pair, its first unit
+  auto units_of = [&](int s, bool report_it) -> int64_t {
+    if (s >= p.num_seqs) return 0;
+    const ChunkRow r = chunk_row(p, s, report_it);
+    return ChunkSeq{r.n, r.ctx - r.n, p.tile_tokens}.units() * p.kv_heads;
+  };
+  auto block_sum = [&](long long v) -> int64_t {  // of all warps' values; `sums` keeps theirs
+    v = warp_sum_ll(v);
+    __syncthreads();
+    if (lane == 0) sums[warp] = v;
+    __syncthreads();
+    int64_t all = 0;
+    for (int i = 0; i < kWarps; ++i) all += sums[i];
+    return all;
+  };
+  if (tid < 4) found[tid] = -1;
+  int64_t total = 0;
+  for (int b = 0; b < p.num_seqs; b += kThreads) total += block_sum(units_of(b + tid, cta == 0));
+  const int ranges = chunk_ranges(total, gridDim.x, kLeastUnits);
+  bool here = total > 0 && cta < ranges;
+  if (here) {
+    at->ua = range_start(cta, total, ranges);
+    at->ub = range_start(cta + 1, total, ranges);
+    int64_t before = 0;
+    for (int b = 0; b < p.num_seqs; b += kThreads) {
+      const int64_t mine = units_of(b + tid, false);
+      const int64_t incl = warp_incl_scan_ll(mine, lane);
+      const int64_t all = block_sum(mine);
+      int64_t excl = before + incl - mine;
+      for (int i = 0; i < warp; ++i) excl += sums[i];
+      if (mine > 0 && excl <= at->ua && at->ua < excl + mine) {
+        found[0] = b + tid;
+        found[1] = excl;
+      }
+      before += all;
+    }
+    __syncthreads();
+    at->seq = (int)found[0];
+    here = at->seq >= 0;
+  }
+  if (here) {
+    at->load(p);
+    const int64_t per_head = at->cs.units(), in_seq = at->ua - found[1];
+    at->head = (int)(in_seq / per_head);
+    const int64_t in_head = in_seq - at->head * per_head;
+    for (int j = tid; j < at->cs.pairs(); j += kThreads) {
+      const int64_t a = at->cs.before(j);
+      if (a <= in_head && in_head < a + (int64_t)at->cs.tiles(j) * at->cs.weight(j)) {
+        found[2] = j;
+        found[3] = a;
+      }
+    }
+    __syncthreads();
+    at->pair = (int)found[2];
+    at->start = at->ua - in_head + found[3];
+    at->set();
+    here = at->pair >= 0;
+  }
+  if (tid == 0)
+    p.cuts[cta] = here ? make_int4(at->seq, at->head, at->pair, at->t0 < at->tiles ? at->t0 : 0) : make_int4(-1, 0, 0, 0);
+  return here;
+}
+
+// ---------------------------------------------------------------------------
+// Join: the rows of the items that range boundaries cut, by log-sum-exp.  Block
+// (b, y) has the item that CTA b's range begins inside of, if CTA b - 1's does not
+// begin inside of the same one; its rows are shared out among the blocks of b and their warps,
+// with eight warps to a row where there are few.
+// ---------------------------------------------------------------------------
+constexpr int kJoinBlocks = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ ChunkParams p) {
+  constexpr int kLanes = D / 4;  // lanes that hold four dims (the others repeat them)
+  const int lane = threadIdx.x & 31, dims = lane % kLanes, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x + 1, ctas = gridDim.x + 1;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int4 cut = __ldcg(p.cuts + b);
+  if (cut.x < 0 || cut.w == 0) return;  // no such range, or it begins with an item
+  auto same = [&](const int4& o) { return o.x == cut.x && o.y == cut.y && o.z == cut.z && o.w != 0; };
+  if (same(__ldcg(p.cuts + b - 1))) return;
+  int last = b;
+  while (last + 1 < ctas && same(__ldcg(p.cuts + last + 1))) ++last;
+  // (After a timeout of the kernel before the list may hold anything: stay inside.)
+  if (cut.x >= p.num_seqs || cut.y < 0 || cut.y >= p.kv_heads || cut.z < 0) {
+    if (threadIdx.x == 0) report(p.error_flag, PA_DEVERR_STATE);
+    return;
+  }
+  const ChunkRow r = chunk_row(p, cut.x, false);
+  const int first = cut.z * 2 * p.tile_tokens;  // the item's first token
+  const int tokens = min(r.n - first, 2 * p.tile_tokens), parts = last - b + 2;
+  const int rows = tokens * p.group;
+  const int per_row = rows <= 4 * kJoinBlocks ? 8 : 1;  // warps
+  __shared__ float shared_parts[8][6][32];
+  for (int i = blockIdx.y * (8 / per_row) + warp / per_row; i < rows; i += kJoinBlocks * (8 / per_row)) {
+    const int tok = i / p.group, g = i - tok * p.group;
+    const int tile = tok >= p.tile_tokens ? 1 : 0;
+    const int in_tile = (tok - tile * p.tile_tokens) * p.group + g;
+    // Part k: CTA b - 1 + k, the first in its second slot, the others in their first.
+    auto slot = [&](int k) -> size_t { return (size_t)2 * (b - 1 + k) + (k == 0 ? 1 : 0); };
+    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const int w0 = per_row == 8 ? warp : 0;
+    for (int k0 = w0; k0 < parts; k0 += 32 * per_row) {
+      const int k = k0 + lane * per_row, here = min(32, (parts - k0 + per_row - 1) / per_row);
+      float2 a = make_float2(-INFINITY, 0.f);
+      if (k < parts) a = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot(k) * (2 * kChunkRows) + tile * kChunkRows + in_tile);
+      if (a.y == 0.f) a.x = -INFINITY;  // no token seen: no weight
+      float top = a.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+      const float keep = ex2_ftz(m - ref);
+      const float wa = a.y == 0.f ? 0.f : ex2_ftz(a.x - ref);
+      m = mn;
+      float lw = wa * a.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+      l = l * keep + lw;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] *= keep;
+#pragma unroll 8
+      for (int j = 0; j < here; ++j) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o) +
+                                ((slot(k0 + j * per_row) * 2 + tile) * (D / 4) + dims) * kChunkRows + in_tile);
+        const float f = __shfl_sync(0xffffffffu, wa, j);
+        if (f != 0.f) {  // a part without weight may hold anything
+          acc[0] = fmaf(f, o.x, acc[0]), acc[1] = fmaf(f, o.y, acc[1]);
+          acc[2] = fmaf(f, o.z, acc[2]), acc[3] = fmaf(f, o.w, acc[3]);
+        }
+      }
+    }
+    if (per_row == 8) {  // (all warps of the block are here, with one row)
+      __syncthreads();
+      float(*mine)[32] = shared_parts[warp];
+      mine[4][lane] = m;
+      mine[5][lane] = l;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mine[j][lane] = acc[j];
+      __syncthreads();
+      if (warp != 0) continue;
+      for (int w = 1; w < 8; ++w) m = fmaxf(m, shared_parts[w][4][lane]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      l = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = 0.f;
+      for (int w = 0; w < 8; ++w) {
+        const float f = ex2_ftz(shared_parts[w][4][lane] - ref);
+        l = fmaf(f, shared_parts[w][5][lane], l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = fmaf(f, shared_parts[w][j][lane], acc[j]);
+      }
+    }
+    if (lane < kLanes) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const size_t at = ((size_t)(r.row0 + first + tok) * p.num_heads + cut.y * p.group + g) * D + 4 * lane;
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(static_cast<T*>(p.out) + at) =
+            make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+      else
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at) =
+            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    }
+  }
+}
+
+// ---- host side ----
+
+struct ChunkScratch {
+  size_t cuts, part_ml, part_o, total;
+};
+
+ChunkScratch chunk_scratch(int head_size, int sm_count) {
+  ChunkScratch s;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes, 256);
+    return at;
+  };
+  const size_t rows = (size_t)2 * sm_count * 2 * kChunkRows;
+  s.cuts = take(sizeof(int4) * (size_t)sm_count);
+  s.part_ml = take(rows * 8);
+  s.part_o = take(rows * head_size * 4);
+  s.total = o;
+  return s;
+}
+
+}  // namespace
+}  // namespace pa

@@ -108,40 +108,6 @@ struct PrefixLayout {
   static constexpr uint32_t kBytes = kRaw + kRawStages * kRawBytes;
 };
 
-// mbar_wait that also gives up when another warp has.
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, unsigned long long limit,
-                                              const volatile int* abort_flag) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t spin = 1;; ++spin) {
-      if ((ok = mbar_try_wait(bar, parity))) break;
-      if ((spin & 63u) == 0 && (*abort_flag != 0 || global_timer_ns() - t0 > limit)) break;
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-      : "memory");
-}
-
-// Position in the ring of stages.
-struct Ring {
-  int i = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int n) {
-    if (++i == n) {
-      i = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
 template <int D, bool F8>
 __global__ void __launch_bounds__(kPrefixThreads, 1) pa_prefix_kernel(const __grid_constant__ PrefixParams p) {
   using L = PrefixLayout<D, F8>;

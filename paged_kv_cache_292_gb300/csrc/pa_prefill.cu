@@ -1,0 +1,1040 @@
+// Attention of chunks of new tokens over the paged cache (pa_prefill,
+// pa_prefill_int8, pa_decode_int8).
+//
+// The (token, group head) rows of a chunk are the rows of two matrix products
+// per KV head and tile of 128 tokens, S = Q K^T and O += P V with the running
+// statistics of a softmax between them (s in log2 units):
+//
+//   m_r = max_t s_rt, l_r = sum_t 2^(s_rt - m_r), O_r = sum_t 2^(s_rt - m_r) v_t
+//
+// int8 pools: k_t = ks_t * codes, v_t = vs_t * codes.  The codes go through the
+// products as they are (every integer up to 256 is a bf16 number), s_rt is
+// multiplied by ks_t and the weight by vs_t on its way into the second product.
+//
+// One persistent CTA per SM, equal shares of the list of (item, tile) units
+// (pa_chunk_work.h).  Per CTA:
+//   warps 0-7, 8-15 softmax groups 0 and 1: two threads per row, 64 tokens each,
+//                   which exchange their maxima; scores come from tensor memory,
+//                   weights go back there as bf16
+//   warp 16         loads K and V tiles: TMA boxes of gcd(block_size, 128) token
+//                   rows x 64 elements into 128-byte swizzled panels (int8: the
+//                   codes into a ring of their own, the scales beside them);
+//                   blocks that are no multiple of 8: 16-byte asynchronous copies
+//   warp 17         issues the products (tcgen05.mma, one thread)
+//   warps 18, 19    int8: widen the codes into the panels.  bf16: warp 18 zeroes what
+//                   lies behind a context's end in its last V tile (zero weights
+//                   do not cancel the NaN that may lie there)
+// With two row tiles each group has one and both use every K/V tile; with a
+// single row tile the groups take alternate K/V tiles and add their results in
+// the end through tensor memory.  While one group exponentiates, the tensor
+// core works for the other.  Tensor memory: S0, S1 (128 columns each; the weights
+// overwrite the first 64, their second parts, if any, the other 64), O0, O1 (D columns).
+#include "pa_launch.cuh"
+
+#include <cmath>
+#include <utility>
+
+#include "../../include/pa_int8_cache.h"
+#include "pa_chunk.cuh"
+#include "pa_decode_impl.h"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kChunkThreads = 640;
+// Registers per thread: 96 at launch (65536 / 640, rounded down); a softmax thread
+// holds 64 scores, the fifth warpgroup issues copies and products.
+// 4 * 128 * 104 + 128 * 64 = 640 * 96.
+constexpr int kSoftmaxRegisters = 104, kIssueRegisters = 64;
+constexpr int kSoftmaxWarps = 16, kLoadWarp = 16, kProductWarp = 17, kWidenWarp = 18, kWidenWarps = 2;
+constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
+// A running maximum is kept until a tile exceeds it by this factor (log2): until
+// then weights are at most 2^8, which bf16 and the fp32 sums hold as well as 1.
+constexpr float kSlack = 8.f;
+constexpr int kScaleSlots = 4;  // int8: tiles whose scales are in shared memory
+
+template <int D, bool I8>
+struct ChunkLayout {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kTileBytes = kPanels * kPanel;  // a Q, K or V tile
+  static constexpr int kStages = D == 64 ? 8 : I8 ? 3 : 5;
+  static constexpr int kRawStages = I8 ? (D == 64 ? 6 : 3) : 0;  // tiles of codes
+  static constexpr uint32_t kRawBytes = kTileBytes / 2;
+  static constexpr uint32_t kExchange = 1024;  // [2 groups][2 halves][128] floats; barriers before it
+  static constexpr uint32_t kQ = 3 * 1024;
+  static constexpr uint32_t kRing = kQ + 2 * kTileBytes;
+  static constexpr uint32_t kRaw = kRing + kStages * kTileBytes;
+  static constexpr uint32_t kScales = kRaw + kRawStages * kRawBytes;  // [slots][K, V][128] floats
+  static constexpr uint32_t kBytes = kScales + (I8 ? kScaleSlots * 1024 : 0);
+  static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
+};
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Two codes (the low bytes of the halves of x) as bf16 integers: with the sign bit
+// apart, code = (128 + low 7 bits) - (128 or 256), and all three are bf16 numbers of
+// one pattern: 0x4300 is 128, and bit 7 of the fraction's carry makes it 256.
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x) {
+  const uint32_t low = (x & 0x007f007fu) | 0x43004300u, sign = (x & 0x00800080u) | 0x43004300u;
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(low), "r"(sign));
+  return r;
+}
+
+template <int D, bool I8, bool kOdd>
+__global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __grid_constant__ ChunkParams p) {
+  using L = ChunkLayout<D, I8>;
+  constexpr int NS = L::kStages, NR = L::kRawStages;
+  extern __shared__ __align__(1024) unsigned char smem[];  // swizzled panels start on 1 KiB boundaries
+  const uint32_t base = smem_addr(smem);
+  if ((base & 1023u) != 0) {  // cannot be: the array asks for it
+    if (threadIdx.x == 0) report(p.error_flag, PA_DEVERR_STATE);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t bars = base;
+  auto full = [&](int i) { return bars + 8u * i; };
+  auto empty = [&](int i) { return bars + 8u * (NS + i); };
+  auto tail = [&](int i) { return bars + 8u * (2 * NS + i); };  // a V tile whose end must be zeroed has landed
+  const uint32_t q_full = bars + 8u * (3 * NS);
+  auto s_full = [&](int w) { return bars + 8u * (3 * NS + 1 + w); };
+  auto p_full = [&](int w) { return bars + 8u * (3 * NS + 3 + w); };
+  auto o_full = [&](int w) { return bars + 8u * (3 * NS + 5 + w); };
+  const uint32_t drained = bars + 8u * (3 * NS + 7), joined = bars + 8u * (3 * NS + 8);
+  auto exchanged = [&](int w) { return bars + 8u * (3 * NS + 9 + w); };
+  auto sc_full = [&](int i) { return bars + 8u * (3 * NS + 11 + i); };
+  auto sc_empty = [&](int i) { return bars + 8u * (3 * NS + 11 + kScaleSlots + i); };
+  auto raw_full = [&](int i) { return bars + 8u * (3 * NS + 11 + 2 * kScaleSlots + i); };
+  auto raw_empty = [&](int i) { return bars + 8u * (3 * NS + 11 + 2 * kScaleSlots + NR + i); };
+  static_assert(8 * (3 * NS + 11 + 2 * kScaleSlots + 2 * NR) <= 512, "barriers lie before the flags");
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 512);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + 516);
+  auto timed_out = [&]() {
+    if (lane == 0) {
+      report(p.error_flag, PA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  };
+  griddep_wait();
+  griddep_launch_dependents();
+
+  ChunkItems items;
+  if (!chunk_begin<kChunkThreads>(p, &items, reinterpret_cast<long long*>(smem + 640))) return;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full(i), I8 ? kWidenWarps : 1);
+      mbar_init(empty(i), 1);
+      mbar_init(tail(i), 1);
+    }
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(raw_full(i), 1);
+      mbar_init(raw_empty(i), kWidenWarps);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(sc_full(i), 1);
+      mbar_init(sc_empty(i), 1);
+    }
+    mbar_init(q_full, kSoftmaxWarps);
+    mbar_init(joined, kSoftmaxWarps);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(exchanged(w), kSoftmaxWarps / 2);
+      mbar_init(s_full(w), 1);
+      mbar_init(p_full(w), kSoftmaxWarps / 2);
+      mbar_init(o_full(w), 1);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == kProductWarp) tmem_alloc(smem_addr(smem + 516), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < kSoftmaxWarps)
+    registers_up<kSoftmaxRegisters>();
+  else
+    registers_down<kIssueRegisters>();
+
+  if (warp < kSoftmaxWarps) {
+    // ---------------- softmax ----------------
+    const int w = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the TMEM lanes
+    const uint32_t s_addr = tmem + lanes + 128u * w, o_all = tmem + lanes + 256u;
+    const uint32_t o_addr = o_all + (uint32_t)D * w + (D / 2) * half;
+    float* mine = reinterpret_cast<float*>(smem + L::kExchange) + (w * 2 + half) * 128 + row;
+    const float* other = reinterpret_cast<const float*>(smem + L::kExchange) + (w * 2 + (half ^ 1)) * 128 + row;
+    uint32_t s_phase = 0, o_phase = 0, x_phase = 0, j_phase = 0;
+    uint32_t tile_count = 0;  // int8: tiles of the segments before (slot and phase of the scales)
+    // Give the row's other thread `v` and get its value.  (What it gave before has
+    // been read: either the weights of the tile in between, which the tensor core
+    // waits for, or the next queries came after that.)
+    auto exchange = [&](float v, float* got) -> bool {
+      *mine = v;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(exchanged(w));
+      if (!wait_or_abort(exchanged(w), x_phase, p.wait_limit_ns, abort_flag)) return false;
+      x_phase ^= 1u;
+      tc_fence_after();
+      *got = *other;
+      return true;
+    };
+    bool alive = true;
+    for (bool more = true; more; more = items.next(p)) {
+      if (items.t0 >= items.t1) continue;
+      const bool two = items.two();
+      const int rr = row, row_tile = two ? w : 0;
+      const int tok_in = rr / p.group, g = rr - tok_in * p.group;
+      const int token = (2 * items.pair + row_tile) * p.tile_tokens + tok_in;  // of the chunk
+      const bool real = rr < p.tile_tokens * p.group && token < items.cs.n;
+      const size_t at = ((size_t)(items.row.row0 + token) * p.num_heads + items.head * p.group + g) * D;
+      // Tokens that the row sees.
+      const int sees = real ? max(items.cs.old + token + 1, 0) : 0;
+      // The row's queries into the swizzled Q tile: half a row per thread with
+      // two row tiles, a quarter with one.
+      {
+        constexpr int kUnits = D / 8;  // 16-byte units of a row
+        const int n = two ? kUnits / 2 : kUnits / 4, u0 = n * (two ? half : 2 * w + half);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
+        unsigned char* dst = smem + L::kQ + (two ? w * L::kTileBytes : 0) + row * 128;
+        uint4 v[kUnits / 2];
+#pragma unroll
+        for (int i = 0; i < kUnits / 2; ++i)
+          v[i] = real && i < n ? __ldg(src + u0 + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < kUnits / 2; ++i) {
+          if (i < n) {
+            const int u = u0 + i;
+            v[i].x = (v[i].x & p.q_keep) ^ p.q_flip;
+            v[i].y = (v[i].y & p.q_keep) ^ p.q_flip;
+            v[i].z = (v[i].z & p.q_keep) ^ p.q_flip;
+            v[i].w = (v[i].w & p.q_keep) ^ p.q_flip;
+            *reinterpret_cast<uint4*>(dst + (u >> 3) * kPanel + (((u & 7) ^ (row & 7)) << 4)) = v[i];
+          }
+        }
+        async_proxy_fence();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      const int step = items.step(), x0 = items.first(w), x1 = items.end(w);
+      // A warp without a row of the batch only takes part in the barriers: its rows' weights
+      // may be anything, they reach nothing but its rows of O, which nobody reads.
+      const bool rows_here = __any_sync(0xffffffffu, real);
+      // Where one row tile is all the copies set the pace, and the weights go in two parts.
+      const bool fine = !two;
+      float m = -INFINITY, l = 0.f;
+      for (int x = x0; x < x1; x += step) {
+        if (!(alive = wait_or_abort(s_full(w), s_phase, p.wait_limit_ns, abort_flag))) break;
+        s_phase ^= 1u;
+        tc_fence_after();
+        if (!rows_here) {
+          float none;
+          if (!(alive = exchange(0.f, &none))) break;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(w));
+          continue;
+        }
+        const uint32_t nth = tile_count + (uint32_t)(x - items.t0);
+        const float* k_scale = nullptr;
+        if constexpr (I8) {
+          if (!(alive = wait_or_abort(sc_full(nth % kScaleSlots), (nth / kScaleSlots) & 1u, p.wait_limit_ns, abort_flag)))
+            break;
+          k_scale = reinterpret_cast<const float*>(smem + L::kScales + (nth % kScaleSlots) * 1024u) + 64 * half;
+        }
+        float s[64];
+        tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[0]), s_addr + 64u * half);
+        tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[32]), s_addr + 64u * half + 32u);
+        tmem_wait_load();
+        if constexpr (I8) {
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(k_scale + i);
+            s[i] *= k4.x;
+            s[i + 1] *= k4.y;
+            s[i + 2] *= k4.z;
+            s[i + 3] *= k4.w;
+          }
+        }
+        const int nvalid = sees - x * kChunkTokens - 64 * half;
+        const bool masked = nvalid < 64;
+        if (masked) {  // tokens behind the row's own
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i >= nvalid) s[i] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < 60; i += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], s[i + j]), s[i + 4 + j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[60 + j]);
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), theirs;
+        // Behind the exchange both threads of every row have read their scores,
+        // which the weights may now overwrite.
+        if (!(alive = exchange(top, &theirs))) break;
+        top = fmaxf(top, theirs);
+        if (m == -INFINITY) m = top;  // nothing but zero weights so far
+        const bool moves = (top - m) * p.scale_log2 > kSlack;
+        if (__any_sync(0xffffffffu, moves)) {
+          // The products of the group's earlier tiles are done (the scores were
+          // issued behind them), so O can be scaled here, half its columns each.
+          const float f = moves ? ex2_ftz((m - top) * p.scale_log2) : 1.f;
+          if (moves) m = top;
+          l *= f;
+          if (x >= x0 + step) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[16];
+              tmem_load16(o, o_addr + 16u * c);
+              tmem_wait_load();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_store16(o_addr + 16u * c, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
+        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), neg2 = pair(neg, neg);
+        uint64_t sum[2] = {0ull, 0ull};
+        const float* v_scale = k_scale + 128;
+        // The weights enter the product as bf16: half a step, 2^-8 at most, both
+        // signs alike; the sum keeps them in fp32.  Where one row tile is all
+        // (fine) their remainders follow as a second bf16 part (2^-16 together) in
+        // the columns behind.  int8: V's scales go into the weights before the
+        // rounding; a scale behind the row's own token, which may be NaN, does not.
+        auto weights = [&](int e, int i) -> uint32_t {  // two of them, kept in s for their remainders
+          float a, b;
+          unpair(fma_pair(pair(s[e], s[e + 1]), scale2, neg2), a, b);
+          s[e] = ex2_ftz(a);
+          s[e + 1] = ex2_ftz(b);
+          sum[i & 1] = add_pair(sum[i & 1], pair(s[e], s[e + 1]));
+          if constexpr (I8) {
+            const float2 v2 = *reinterpret_cast<const float2*>(v_scale + e);
+            s[e] = masked && e >= nvalid ? 0.f : s[e] * v2.x;
+            s[e + 1] = masked && e + 1 >= nvalid ? 0.f : s[e + 1] * v2.y;
+          }
+          return pack_bf16x2(s[e], s[e + 1]);
+        };
+        if (!fine) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t hi[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) hi[i] = weights(32 * c + 2 * i, i);
+            tmem_store16(s_addr + 32u * half + 16u * c, hi);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int e = 8 * c + 2 * i;
+              hi[i] = weights(e, i);
+              lo[i] = pack_bf16x2(s[e] - bf16_lo(hi[i]), s[e + 1] - bf16_hi(hi[i]));
+            }
+            tmem_store4(s_addr + 32u * half + 4u * c, hi);
+            tmem_store4(s_addr + 64u + 32u * half + 4u * c, lo);
+          }
+        }
+        {
+          float a, b;
+          unpair(add_pair(sum[0], sum[1]), a, b);
+          l += a + b;
+        }
+        tmem_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(w));
+      }
+      tile_count += (uint32_t)(items.t1 - items.t0);
+      if (alive) alive = wait_or_abort(o_full(0), o_phase, p.wait_limit_ns, abort_flag);
+      if (alive) alive = wait_or_abort(o_full(1), o_phase, p.wait_limit_ns, abort_flag);
+      o_phase ^= 1u;
+      tc_fence_after();
+      // Whole items end here; a part of one leaves its sums for the join.
+      const bool whole = items.t0 == 0 && items.t1 == items.tiles;
+      const size_t part = (size_t)2 * blockIdx.x + (items.t0 == 0 ? 1 : 0);
+      float* part_o = p.part_o + (part * 2 + row_tile) * (kChunkRows * D) + 4 * row;  // + dims * 128
+      float2* part_ml = reinterpret_cast<float2*>(p.part_ml) + part * (2 * kChunkRows) + row_tile * kChunkRows + row;
+      if (two) {
+        float theirs = 0.f;
+        if (alive) alive = exchange(l, &theirs);
+        if (!alive) {
+          timed_out();
+          break;
+        }
+        l += theirs;
+        if (!rows_here) continue;
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t o[32];
+          tmem_load32(o, o_addr + 32u * c);
+          tmem_wait_load();
+          if (!real) continue;
+          const int d0 = (D / 2) * half + 32 * c;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (l != 0.f) {
+                v.x = pack_bf16x2(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
+                v.y = pack_bf16x2(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
+                v.z = pack_bf16x2(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
+                v.w = pack_bf16x2(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
+              }
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + d0 + 8 * i) = v;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(part_o + (size_t)(d0 + 4 * i) * kChunkRows) =
+                  make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                              __uint_as_float(o[4 * i + 3]));
+          }
+        }
+        if (real && !whole && half == 0) *part_ml = make_float2(m * p.scale_log2, l);
+      } else {
+        // One row tile: the row's four threads leave (m, l) in tensor memory, where the scores
+        // were, and take a quarter of the dims each from both groups' O.
+        if (alive && rows_here) {
+          uint32_t ml[4] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u};
+          tmem_store4(s_addr + 4u * half, ml);
+          tmem_wait_store();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (alive) {
+          if (lane == 0) mbar_arrive(joined);
+          alive = wait_or_abort(joined, j_phase, p.wait_limit_ns, abort_flag);
+          j_phase ^= 1u;
+          tc_fence_after();
+        }
+        if (!alive) {
+          timed_out();
+          break;
+        }
+        if (!rows_here) continue;
+        uint32_t a[16], b[16];
+        tmem_load16(a, tmem + lanes);
+        tmem_load16(b, tmem + lanes + 128u);
+        tmem_wait_load();
+        const float m0 = __uint_as_float(a[0]), m1 = __uint_as_float(b[0]);
+        const float l0 = __uint_as_float(a[1]) + __uint_as_float(a[5]), l1 = __uint_as_float(b[1]) + __uint_as_float(b[5]);
+        // A group that saw nothing (l == 0) may have anything in O.
+        const float top = fmaxf(l0 != 0.f ? m0 : -INFINITY, l1 != 0.f ? m1 : -INFINITY);
+        const float f0 = l0 != 0.f ? ex2_ftz((m0 - top) * p.scale_log2) : 0.f;
+        const float f1 = l1 != 0.f ? ex2_ftz((m1 - top) * p.scale_log2) : 0.f;
+        const float sum = f0 * l0 + f1 * l1;
+        const float inv = whole ? 1.f / sum : 1.f;
+        const int d0 = (D / 4) * (2 * w + half);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          tmem_load16(a, o_all + d0 + 16u * c);
+          tmem_load16(b, o_all + (uint32_t)D + d0 + 16u * c);
+          tmem_wait_load();
+          if (!real) continue;
+          float o[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = ((l0 != 0.f ? __uint_as_float(a[i]) * f0 : 0.f) + (l1 != 0.f ? __uint_as_float(b[i]) * f1 : 0.f)) *
+                   (sum != 0.f ? inv : 0.f);
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + d0 + 16 * c + 8 * i) =
+                  make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                             pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(part_o + (size_t)(d0 + 16 * c + 4 * i) * kChunkRows) =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (real && !whole && w == 0 && half == 0) *part_ml = make_float2(top * p.scale_log2, sum);
+      }
+    }
+  } else if (warp == kLoadWarp) {
+    // ---------------- loads ----------------
+    if (!kOdd && lane == 0) {
+      prefetch_tensormap(&p.tm_k);
+      prefetch_tensormap(&p.tm_v);
+    }
+    // Stages the copies land in: panels, or the codes of int8 pools.
+    constexpr int kCopyStages = I8 ? NR : NS, kBoxPanels = I8 ? 1 : L::kPanels;
+    constexpr uint32_t kCopyBytes = I8 ? L::kRawBytes : L::kTileBytes, kCopyRing = I8 ? L::kRaw : L::kRing;
+    auto landed = [&](int i) { return I8 ? raw_full(i) : full(i); };
+    auto taken = [&](int i) { return I8 ? raw_empty(i) : empty(i); };
+    const int boxes = kOdd ? 1 : kChunkTokens / p.box_rows;
+    const int box = lane / kBoxPanels, panel = lane % kBoxPanels;
+    const bool mine = box < boxes;
+    const uint32_t dst0 = panel * kPanel + box * p.box_rows * (I8 ? (uint32_t)D : 128u);
+    Ring ring;
+    uint32_t armed = 0, armed_phase = 0;       // stages armed, with the parity of their last phase,
+    uint32_t tailed = 0, tail_phase = 0;       // and those armed as a tail
+    uint32_t scaled = 0, scale_phase = 0;      // slots of scales
+    uint32_t tile_count = 0;
+    int late[2] = {-1, -1};  // kOdd: stages whose copies are issued and not yet told of
+    bool alive = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+      if (wait_or_abort(bar, parity, p.wait_limit_ns, abort_flag)) return true;
+      timed_out();
+      return false;
+    };
+    // kOdd: the copies of stage `st` are complete in every lane.
+    auto tell = [&](int st) {
+      async_proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(landed(st));
+    };
+    auto tell_all = [&]() {
+      copies_wait<0>();
+      if (late[0] >= 0) tell(late[0]);
+      if (late[1] >= 0) tell(late[1]);
+      late[0] = late[1] = -1;
+    };
+    for (bool more = true; alive && more; more = items.next(p)) {
+      if (items.t0 >= items.t1) continue;
+      const int32_t* table = p.tables + (size_t)items.seq * p.max_blocks;
+      const int ctx = items.row.ctx;
+      auto block_of = [&](int tok) -> int {  // -1: none
+        if (tok >= ctx) return -1;
+        const int phys = __ldg(table + tok / p.block_size);
+        if (p.num_physical_blocks > 0 && (phys < 0 || phys >= p.num_physical_blocks)) {
+          report(p.error_flag, PA_DEVERR_BLOCK_ID);
+          return -1;
+        }
+        return phys;
+      };
+      // Token row of this lane's box in tile x, -1 for none (zeros then).
+      auto box_row = [&](int x) -> int {
+        const int tok = x * kChunkTokens + box * p.box_rows;
+        if (!mine || x >= items.t1) return -1;
+        const int phys = block_of(tok);
+        return phys < 0 ? -1 : phys * p.block_size + tok % p.block_size;
+      };
+      // The scales of tile x's tokens.
+      auto load_scales = [&](int x, int row, uint32_t nth) -> bool {
+        const int slot = nth % kScaleSlots;
+        const uint32_t phase = (nth / kScaleSlots) & 1u;
+        if (kOdd && __any_sync(0xffffffffu, !mbar_try_wait(sc_empty(slot), phase ^ 1u))) tell_all();
+        if (!wait(sc_empty(slot), phase ^ 1u)) return false;
+        const uint32_t dst = base + L::kScales + slot * 1024u;
+        if constexpr (kOdd) {
+          for (int i = 0; i < kChunkTokens; i += 32) {
+            const int tok = x * kChunkTokens + i + lane, phys = block_of(tok);
+            const size_t at = ((size_t)max(phys, 0) * p.kv_heads + items.head) * p.block_size + tok % p.block_size;
+            copy_async4(dst + 4u * (i + lane), p.k_scales + at, phys >= 0);
+            copy_async4(dst + 512u + 4u * (i + lane), p.v_scales + at, phys >= 0);
+          }
+          copies_commit();
+          tell_all();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sc_full(slot));
+        } else {
+          const bool real = mine && row >= 0;
+          const uint32_t bytes = 4u * p.box_rows;
+          const unsigned there = __ballot_sync(0xffffffffu, real);
+          if (lane == 0) mbar_arrive_expect_tx(sc_full(slot), 2u * bytes * __popc(there));
+          __syncwarp();
+          if (real) {
+            const int phys = row / p.block_size;
+            const size_t at = ((size_t)phys * p.kv_heads + items.head) * p.block_size + (row - phys * p.block_size);
+            bulk_copy_g2s(dst + bytes * box, p.k_scales + at, bytes, sc_full(slot));
+            bulk_copy_g2s(dst + 512u + bytes * box, p.v_scales + at, bytes, sc_full(slot));
+          }
+          scaled |= 1u << slot;
+          scale_phase = (scale_phase & ~(1u << slot)) | (phase << slot);
+        }
+        return true;
+      };
+      auto load = [&](bool v, int x, int row) -> bool {
+        const bool withhold = p.stall_unit >= 0 && items.start + (int64_t)x * items.weight == p.stall_unit;
+        if constexpr (kOdd) {
+          // What it waits for may wait for these.
+          if (__any_sync(0xffffffffu, !mbar_try_wait(taken(ring.i), ring.phase ^ 1u))) tell_all();
+        }
+        if (!wait(taken(ring.i), ring.phase ^ 1u)) return false;
+        const uint32_t dst = base + kCopyRing + ring.i * kCopyBytes;
+        if (withhold) {
+        } else if constexpr (kOdd) {
+          // 16-byte units of the tile's rows, 32 rows' places at a time.
+          constexpr int kUnits = D * (I8 ? 1 : 2) / 16, kRowsAtOnce = 32 / kUnits;
+          const unsigned char* pool = static_cast<const unsigned char*>(v ? p.v_cache : p.k_cache);
+          const int unit = lane % kUnits;
+          for (int r0 = 0; r0 < kChunkTokens; r0 += 32) {
+            const int tok = x * kChunkTokens + r0 + lane, phys = block_of(tok);
+            const int place = phys < 0 ? -1 : phys * p.block_size + tok % p.block_size;
+#pragma unroll 4
+            for (int i = 0; i < 32; i += kRowsAtOnce) {
+              const int r = i + lane / kUnits, from = __shfl_sync(0xffffffffu, place, r);
+              const int rr = r0 + r;
+              const uint32_t to = I8 ? (uint32_t)(rr * D + unit * 16)
+                                     : (uint32_t)((unit >> 3) * kPanel + rr * 128 + (((unit & 7) ^ (rr & 7)) << 4));
+              copy_async16(dst + to, pool + ((size_t)max(from, 0) * p.kv_heads + items.head) * (16 * kUnits) + unit * 16,
+                           from >= 0);
+            }
+          }
+          copies_commit();
+          if (late[1] >= 0) {  // the copies before the last two are complete
+            copies_wait<2>();
+            tell(late[1]);
+          }
+          late[1] = late[0];
+          late[0] = ring.i;
+        } else {
+          // The rows behind the context's end in its last box are zeroed before V is used.
+          const bool ends = !I8 && v && ctx % p.box_rows != 0 && x == (ctx - 1) / kChunkTokens;
+          const uint32_t bar = ends ? tail(ring.i) : landed(ring.i);
+          if (lane == 0) mbar_arrive_expect_tx(bar, kCopyBytes);
+          __syncwarp();
+          // A chunk beyond the row's last is outside the tensor: zeros, without a read.
+          if (mine)
+            tma_load_3d(dst + dst0, v ? &p.tm_v : &p.tm_k, 0, (row < 0 ? p.kv_heads : items.head) * kBoxPanels + panel,
+                        row < 0 ? 0 : row, bar);
+          if (ends) {
+            tail_phase = (tail_phase & ~(1u << ring.i)) | (((tailed >> ring.i) & 1u ? ~tail_phase & (1u << ring.i) : 0u));
+            tailed |= 1u << ring.i;
+            armed &= ~(1u << ring.i);
+          } else {
+            armed |= 1u << ring.i;
+            armed_phase = (armed_phase & ~(1u << ring.i)) | (ring.phase << ring.i);
+          }
+        }
+        ring.next(kCopyStages);
+        return true;
+      };
+      const int ahead = items.two() ? 1 : 2;  // K tiles ahead of the V tile
+      const int t0 = items.t0, t1 = items.t1;
+      auto load_k = [&](int x, int row) -> bool {
+        if (I8 && !load_scales(x, row, tile_count + (uint32_t)(x - t0))) return false;
+        return load(false, x, row);
+      };
+      int row_v = 0, row_v1 = 0, row_k = 0;
+      if constexpr (!kOdd) {
+        row_v = box_row(t0);
+        row_v1 = box_row(t0 + 1);
+      }
+      alive = load_k(t0, row_v);
+      if (alive && ahead == 2 && t0 + 1 < t1) alive = load_k(t0 + 1, row_v1);
+      if constexpr (!kOdd) row_k = ahead == 2 ? box_row(t0 + 2) : row_v1;
+      for (int x = t0; alive && x < t1; ++x) {
+        const int row_next = kOdd ? 0 : box_row(x + ahead + 1);
+        alive = load(true, x, row_v);
+        if (alive && x + ahead < t1) alive = load_k(x + ahead, row_k);
+        row_v = row_v1;
+        row_v1 = ahead == 2 ? row_k : row_next;
+        row_k = row_next;
+      }
+      tile_count += (uint32_t)(t1 - t0);
+    }
+    if constexpr (kOdd) tell_all();
+    named_barrier_sync(1, kChunkThreads);
+    if (!kOdd && *abort_flag != 0) {
+      // Copies that were started may still be landing: wait for them (again
+      // bounded) before the CTA's shared memory goes.
+      for (int i = 0; i < kCopyStages; ++i) {
+        if ((armed >> i) & 1u) (void)mbar_wait(landed(i), (armed_phase >> i) & 1u, p.wait_limit_ns);
+        if ((tailed >> i) & 1u) (void)mbar_wait(tail(i), (tail_phase >> i) & 1u, p.wait_limit_ns);
+      }
+      for (int i = 0; i < kScaleSlots; ++i)
+        if ((scaled >> i) & 1u) (void)mbar_wait(sc_full(i), (scale_phase >> i) & 1u, p.wait_limit_ns);
+    }
+  } else if (warp == kProductWarp) {
+    // ---------------- products ----------------
+    constexpr uint32_t kScores = product(true, 128, 128, false), kValues = product(true, 128, D, true);
+    Ring ring;
+    uint32_t q_phase = 0, p_phase[2] = {0u, 0u}, tile_count = 0;
+    bool alive = true;
+    const uint64_t q_op = smem_operand(base + L::kQ, kPanel);
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+      if (wait_or_abort(bar, parity, p.wait_limit_ns, abort_flag)) return true;
+      timed_out();
+      return false;
+    };
+    for (bool rest = true; alive && rest; rest = items.next(p)) {
+      const int t0 = items.t0, t1 = items.t1;
+      if (t0 >= t1) continue;
+      const bool two = items.two();
+      const int ahead = two ? 1 : 2, end0 = items.end(0);
+      // Whether group w has tile x.
+      auto has = [&](int w, int x) { return w != 0 || x < end0; };
+      // S of group w from the K tile in stage `st`.
+      auto scores = [&](int w, int st) {
+        if (lane == 0) {
+          const uint64_t a = q_op + (two ? (w * L::kTileBytes) >> 4 : 0u);
+          const uint64_t b = smem_operand(base + L::kRing + st * L::kTileBytes, kPanel);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * kPanel + (k & 3) * 32u) >> 4;
+            mma_ss(tmem + 128u * w, a + off, b + off, kScores, k > 0);
+          }
+          mma_commit(s_full(w));
+        }
+        __syncwarp();
+      };
+      auto release = [&](int st) {
+        if (lane == 0) mma_commit(empty(st));
+        __syncwarp();
+      };
+      if (!(alive = wait(q_full, q_phase))) break;
+      q_phase ^= 1u;
+      tc_fence_after();
+      // The first K tiles.
+      for (int x = t0; x < t0 + ahead && x < t1; ++x) {
+        if (!(alive = wait(full(ring.i), ring.phase))) break;
+        tc_fence_after();
+        if (!two || has(0, x)) scores(two ? 0 : x - t0, ring.i);
+        if (two) scores(1, ring.i);
+        release(ring.i);
+        ring.next(NS);
+      }
+      for (int x = t0; alive && x < t1; ++x) {
+        const Ring v = ring;
+        ring.next(NS);
+        const Ring k = ring;
+        const bool more = x + ahead < t1;
+        if (more) ring.next(NS);
+        for (int j = 0; j < (two ? 2 : 1); ++j) {
+          const int w = two ? j : (x - t0) & 1;
+          if (j == 0 && !(alive = wait(full(v.i), v.phase))) break;
+          if (!two || has(w, x)) {
+            if (!(alive = wait(p_full(w), p_phase[w]))) break;
+            p_phase[w] ^= 1u;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint64_t b = smem_operand(base + L::kRing + v.i * L::kTileBytes, kPanel);
+#pragma unroll
+              for (int kk = 0; kk < kChunkTokens / 16; ++kk)
+                mma_ts(tmem + 256u + (uint32_t)D * w, tmem + 128u * w + 8u * kk, b + ((kk * 2048u) >> 4), kValues,
+                       kk > 0 || x >= t0 + (two ? 1 : 2));
+              if (!two) {  // the weights' second part
+#pragma unroll
+                for (int kk = 0; kk < kChunkTokens / 16; ++kk)
+                  mma_ts(tmem + 256u + (uint32_t)D * w, tmem + 128u * w + 64u + 8u * kk, b + ((kk * 2048u) >> 4), kValues,
+                         true);
+              }
+            }
+            __syncwarp();
+          }
+          if (more) {
+            if (j == 0 && !(alive = wait(full(k.i), k.phase))) break;
+            tc_fence_after();
+            if (!two || has(w, x + 1)) scores(w, k.i);
+          }
+        }
+        if (!alive) break;
+        release(v.i);
+        if (more) release(k.i);
+        if (I8) {  // the softmax is done with the tile's scales
+          if (lane == 0) mbar_arrive(sc_empty((tile_count + (uint32_t)(x - t0)) % kScaleSlots));
+          __syncwarp();
+        }
+      }
+      if (!alive) break;
+      tile_count += (uint32_t)(t1 - t0);
+      if (lane == 0) {
+        mma_commit(o_full(0));
+        mma_commit(o_full(1));
+      }
+      __syncwarp();
+    }
+    // Everything issued is done before tensor memory is freed.
+    if (lane == 0) mma_commit(drained);
+    __syncwarp();
+    (void)mbar_wait_warp(drained, 0, p.wait_limit_ns);
+    named_barrier_sync(1, kChunkThreads);
+    tc_fence_after();
+    tmem_free(tmem, 512);
+    return;
+  } else if (I8) {
+    // ---------------- codes to bf16 ----------------
+    // Tiles come in the order of the copies and leave in that of the products,
+    // which is the same.  A thread takes 8 codes, a 16-byte unit of a panel row; units
+    // of a row lie side by side in a warp, so neither side has bank conflicts.
+    constexpr int kThreads = 32 * kWidenWarps, kUnits = D / 8, kSteps = kChunkTokens * kUnits / kThreads;
+    const int t = (warp - kWidenWarp) * 32 + lane, row0 = t / kUnits, unit = t % kUnits;
+    Ring ring, raw;
+    bool alive = true;
+    for (bool more = true; alive && more; more = items.next(p)) {
+      const int tiles = 2 * (items.t1 - items.t0);  // K and V
+      for (int x = 0; x < tiles; ++x) {
+        alive = wait_or_abort(raw_full(raw.i), raw.phase, p.wait_limit_ns, abort_flag) &&
+                wait_or_abort(empty(ring.i), ring.phase ^ 1u, p.wait_limit_ns, abort_flag);
+        if (!alive) {
+          timed_out();
+          break;
+        }
+        const unsigned char* src = smem + L::kRaw + raw.i * L::kRawBytes + 8 * t;
+        unsigned char* dst = smem + L::kRing + ring.i * L::kTileBytes + (unit >> 3) * kPanel + row0 * 128;
+        constexpr int kBatch = 8;  // loads of a batch go before its stores
+        for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
+          uint2 codes[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) codes[i] = *reinterpret_cast<const uint2*>(src + 8 * kThreads * (i0 + i));
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = (i0 + i) * (kThreads / kUnits);  // rows from row0
+            uint4 v;
+            v.x = codes_to_bf16x2(__byte_perm(codes[i].x, 0u, 0x4140));
+            v.y = codes_to_bf16x2(__byte_perm(codes[i].x, 0u, 0x4342));
+            v.z = codes_to_bf16x2(__byte_perm(codes[i].y, 0u, 0x4140));
+            v.w = codes_to_bf16x2(__byte_perm(codes[i].y, 0u, 0x4342));
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((unit & 7) ^ ((row0 + r) & 7)) << 4)) = v;
+          }
+        }
+        async_proxy_fence();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full(ring.i));
+          mbar_arrive(raw_empty(raw.i));
+        }
+        ring.next(NS);
+        raw.next(NR);
+      }
+    }
+  } else if (!kOdd && warp == kWidenWarp) {
+    // ---------------- the end of a context ----------------
+    uint32_t at = 0, phases = 0;  // loads of the segments before; parity per stage
+    bool alive = true;
+    for (bool more = true; alive && more; more = items.next(p)) {
+      if (items.t0 >= items.t1) continue;
+      at += 2u * (uint32_t)(items.t1 - items.t0);
+      const int ctx = items.row.ctx, x = items.t1 - 1;
+      if (ctx % p.box_rows == 0 || x != (ctx - 1) / kChunkTokens) continue;
+      const int st = (int)((at - 1) % NS);  // the segment's last load
+      if (!(alive = wait_or_abort(tail(st), (phases >> st) & 1u, p.wait_limit_ns, abort_flag))) {
+        timed_out();
+        break;
+      }
+      phases ^= 1u << st;
+      const int r0 = ctx - x * kChunkTokens, rows = p.box_rows - r0 % p.box_rows;
+      for (int i = lane; i < rows * (D / 8); i += 32) {
+        const int r = r0 + i / (D / 8), u = i % (D / 8);  // whole rows: the swizzle only moves units within one
+        *reinterpret_cast<uint4*>(smem + L::kRing + st * L::kTileBytes + (u >> 3) * kPanel + r * 128 + (u & 7) * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+      }
+      async_proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(st));
+    }
+  }
+  if (warp < kSoftmaxWarps || warp > kProductWarp) {
+    tc_fence_before();
+    named_barrier_sync(1, kChunkThreads);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// The pools' tensor maps, encoded for every call (about 0.1 us each).
+int make_maps(ChunkParams* prm, uint64_t pool_rows, int head_size, bool int8) {
+  const EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr) return fail(PA_ERR_CUDA, "pa_prefill: the driver has no cuTensorMapEncodeTiled");
+  const cuuint64_t row = (cuuint64_t)prm->kv_heads * head_size;
+  const cuuint64_t chunk = int8 ? head_size : 64, elt = int8 ? 1 : 2;
+  const cuuint64_t dims[3] = {chunk, row / chunk, pool_rows}, strides[2] = {chunk * elt, row * elt};
+  const cuuint32_t box[3] = {(cuuint32_t)chunk, 1, (cuuint32_t)prm->box_rows}, estride[3] = {1, 1, 1};
+  for (int i = 0; i < 2; ++i) {
+    const CUresult r = in_context([&] {
+      return enc(i ? &prm->tm_v : &prm->tm_k, int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                 const_cast<void*>(i ? prm->v_cache : prm->k_cache), dims, strides, box, estride,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, int8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
+    if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "pa_prefill: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  }
+  return PA_OK;
+}
+
+template <int D, bool I8, bool kOdd>
+int launch_chunks(const ChunkParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
+  static RaisedDevices raised;
+  constexpr int kBytes = ChunkLayout<D, I8>::kBytes;
+  const auto kernel = pa_prefill_kernel<D, I8, kOdd>;
+  const int rc = raise_smem_limit(reinterpret_cast<const void*>(kernel), kBytes, dev.device, &raised);
+  if (rc != PA_OK) return rc;
+  cudaError_t e = launch_pdl(kernel, dim3(dev.sm_count), dim3(kChunkThreads), kBytes, stream, prm);
+  if (e != cudaSuccess) return cuda_fail(e, "launch pa_prefill_kernel");
+  if (dev.sm_count > 1)
+    e = launch_pdl(pa_prefill_join<__nv_bfloat16, D>, dim3(dev.sm_count - 1, kJoinBlocks), dim3(256), 0, stream, prm);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "launch pa_prefill_join");
+}
+
+}  // namespace
+
+int prefill_impl(const ChunkCall& c) {
+  const bool none = c.num_queries == 0 && c.num_tokens == 0;  // whose query and out may be null
+  int rc = decode_validate(none ? c.k_cache : c.out, none ? c.k_cache : c.query, c.k_cache, c.v_cache, c.block_tables, c.context_lens, c.num_seqs, 1,
+                           c.num_heads, c.num_kv_heads, c.head_size, c.block_size, c.max_blocks_per_seq, c.scale,
+                           c.int8 ? PA_BF16 : c.dtype, c.num_physical_blocks);
+  if (rc != PA_OK) return rc;
+  if (c.num_queries == 0 && (c.seq_starts == nullptr || !aligned(c.seq_starts, 4)))
+    return fail(PA_ERR_INVALID_ARG, "pa_prefill: seq_starts is null or misaligned");
+  if (c.num_tokens < 0 || c.num_queries < 0)
+    return fail(PA_ERR_INVALID_ARG, "pa_prefill: %d tokens, %d queries", c.num_tokens, c.num_queries);
+  const long long tokens = c.num_queries > 0 ? (long long)c.num_seqs * c.num_queries : c.num_tokens;
+  if (tokens * c.num_heads > 0x7fffffffll)
+    return fail(PA_ERR_UNSUPPORTED, "pa_prefill: %lld tokens of %d heads", tokens, c.num_heads);
+  if (c.int8) {
+    if (c.k_scales == nullptr || c.v_scales == nullptr) return fail(PA_ERR_INVALID_ARG, "pa_prefill_int8: null scales");
+    if (!aligned(c.k_scales, 16) || !aligned(c.v_scales, 16))
+      return fail(PA_ERR_INVALID_ARG, "pa_prefill_int8: scales must be 16-byte aligned");
+    if (c.num_physical_blocks <= 0)
+      return fail(PA_ERR_INVALID_ARG, "pa_prefill_int8: num_physical_blocks %d", c.num_physical_blocks);
+  }
+  if (tokens == 0) return PA_OK;
+  DeviceInfo dev{};
+  rc = current_device_info(&dev);
+  if (rc != PA_OK) return rc;
+  const bool f32 = !c.int8 && c.dtype == PA_F32;
+  const ChunkScratch sc = chunk_scratch(c.head_size, dev.sm_count);
+  ChunkParams prm{};
+  prm.k_cache = c.k_cache;
+  prm.v_cache = c.v_cache;
+  prm.kv_heads = c.num_kv_heads;
+  prm.box_rows = c.block_size & -c.block_size;
+  if (prm.box_rows > kChunkTokens) prm.box_rows = kChunkTokens;
+  const uint64_t pool_rows =
+      c.num_physical_blocks > 0
+          ? (uint64_t)c.num_physical_blocks * c.block_size
+          : rows_of_pools(c.k_cache, c.v_cache, (uint64_t)c.num_kv_heads * c.head_size * (f32 ? 4 : 2));
+  if (pool_rows == 0) return PA_ERR_INVALID_ARG;
+  if (pool_rows > 1ull << 31)
+    return fail(PA_ERR_UNSUPPORTED, "pa_prefill: %llu token rows in the pool (at most 2^31)", (unsigned long long)pool_rows);
+  const bool odd = prm.box_rows < 8;
+  if (!odd && !f32) {
+    rc = make_maps(&prm, pool_rows, c.head_size, c.int8);
+    if (rc != PA_OK) return rc;
+  }
+  ScratchHold hold;  // scratch of the library's own, until the launches are queued
+  void* workspace = c.workspace;
+  if (workspace == nullptr) {
+    rc = hold.of_stream(sc.total, c.stream, &workspace);
+    if (rc != PA_OK) return rc;
+  } else if (c.workspace_bytes < sc.total) {
+    return fail(PA_ERR_WORKSPACE, "pa_prefill: workspace of %zu bytes, %zu needed", c.workspace_bytes, sc.total);
+  } else if (!aligned(workspace, 256)) {
+    return fail(PA_ERR_INVALID_ARG, "pa_prefill: workspace not 256-byte aligned");
+  }
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  prm.q = c.query;
+  prm.out = c.out;
+  prm.k_scales = c.k_scales;
+  prm.v_scales = c.v_scales;
+  prm.tables = c.block_tables;
+  prm.context_lens = c.context_lens;
+  prm.seq_starts = c.num_queries > 0 ? nullptr : c.seq_starts;
+  prm.error_flag = c.error_flag;
+  prm.cuts = reinterpret_cast<int4*>(ws + sc.cuts);
+  prm.part_ml = reinterpret_cast<float*>(ws + sc.part_ml);
+  prm.part_o = reinterpret_cast<float*>(ws + sc.part_o);
+  prm.num_tokens = (int)tokens;
+  prm.num_seqs = c.num_seqs;
+  prm.num_queries = c.num_queries;
+  prm.num_heads = c.num_heads;
+  prm.group = c.num_heads / c.num_kv_heads;
+  prm.tile_tokens = (f32 ? kChunkRowsF32 : kChunkRows) / prm.group;
+  prm.block_size = c.block_size;
+  prm.max_blocks = c.max_blocks_per_seq;
+  prm.max_tokens = c.max_blocks_per_seq * c.block_size;
+  prm.num_physical_blocks = (int)(pool_rows / c.block_size);  // what the rows that the driver knows of hold
+  prm.scale_log2 = c.scale != 0.f ? (float)(std::fabs((double)c.scale) * 1.4426950408889634) : 1.f;
+  prm.q_keep = c.scale != 0.f ? 0xffffffffu : 0u;
+  prm.q_flip = c.scale < 0.f ? 0x80008000u : 0u;
+  cudaStream_t st = static_cast<cudaStream_t>(c.stream);
+  if (f32) {
+    prm.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
+    return launch_chunks_f32(prm, dev, st, c.head_size);
+  }
+  take_wait_test(&prm.stall_unit, &prm.wait_limit_ns);
+  if (c.head_size == 64) {
+    if (c.int8) return odd ? launch_chunks<64, true, true>(prm, dev, st) : launch_chunks<64, true, false>(prm, dev, st);
+    return odd ? launch_chunks<64, false, true>(prm, dev, st) : launch_chunks<64, false, false>(prm, dev, st);
+  }
+  if (c.int8) return odd ? launch_chunks<128, true, true>(prm, dev, st) : launch_chunks<128, true, false>(prm, dev, st);
+  return odd ? launch_chunks<128, false, true>(prm, dev, st) : launch_chunks<128, false, false>(prm, dev, st);
+}
+
+}  // namespace pa
+
+extern "C" size_t pa_prefill_workspace_size(int head_size) {
+  using namespace pa;
+  DeviceInfo dev{};
+  if ((head_size != 64 && head_size != 128) || current_device_info(&dev) != PA_OK) return 0;
+  return chunk_scratch(head_size, dev.sm_count).total;
+}
+
+extern "C" int pa_prefill(void* out, const void* query, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, const int32_t* context_lens, const int32_t* seq_starts,
+                          int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_size, int block_size,
+                          int max_blocks_per_seq, float scale, void* stream, int dtype, int num_physical_blocks,
+                          void* workspace, size_t workspace_bytes, int32_t* error_flag) {
+  pa::clear_error();
+  pa::ChunkCall c{};
+  c.out = out, c.query = query, c.k_cache = k_cache, c.v_cache = v_cache;
+  c.block_tables = block_tables, c.context_lens = context_lens, c.seq_starts = seq_starts;
+  c.num_tokens = num_tokens, c.num_seqs = num_seqs, c.num_heads = num_heads, c.num_kv_heads = num_kv_heads;
+  c.head_size = head_size, c.block_size = block_size, c.max_blocks_per_seq = max_blocks_per_seq;
+  c.scale = scale, c.stream = stream, c.dtype = dtype, c.num_physical_blocks = num_physical_blocks;
+  c.workspace = workspace, c.workspace_bytes = workspace_bytes, c.error_flag = error_flag;
+  return pa::prefill_impl(c);
+}
+
+extern "C" int pa_prefill_int8(void* out, const void* query, const void* k_cache, const void* v_cache,
+                               const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                               const int32_t* context_lens, const int32_t* seq_starts, int num_tokens, int num_seqs,
+                               int num_heads, int num_kv_heads, int head_size, int block_size, int max_blocks_per_seq,
+                               float scale, void* stream, int num_physical_blocks, void* workspace,
+                               size_t workspace_bytes, int32_t* error_flag) {
+  pa::clear_error();
+  pa::ChunkCall c{};
+  c.int8 = true, c.k_scales = k_scales, c.v_scales = v_scales;
+  c.out = out, c.query = query, c.k_cache = k_cache, c.v_cache = v_cache;
+  c.block_tables = block_tables, c.context_lens = context_lens, c.seq_starts = seq_starts;
+  c.num_tokens = num_tokens, c.num_seqs = num_seqs, c.num_heads = num_heads, c.num_kv_heads = num_kv_heads;
+  c.head_size = head_size, c.block_size = block_size, c.max_blocks_per_seq = max_blocks_per_seq;
+  c.scale = scale, c.stream = stream, c.dtype = PA_BF16, c.num_physical_blocks = num_physical_blocks;
+  c.workspace = workspace, c.workspace_bytes = workspace_bytes, c.error_flag = error_flag;
+  return pa::prefill_impl(c);
+}
+
+extern "C" int pa_decode_int8(void* out, const void* query, const void* k_cache, const void* v_cache,
+                              const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                              const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
+                              int num_kv_heads, int head_size, int block_size, int max_blocks_per_seq, float scale,
+                              void* stream, int num_physical_blocks, void* workspace, size_t workspace_bytes,
+                              int32_t* error_flag) {
+  pa::clear_error();
+  if (num_queries < 1) return pa::fail(PA_ERR_INVALID_ARG, "pa_decode_int8: num_queries %d < 1", num_queries);
+  pa::ChunkCall c{};
+  c.int8 = true, c.k_scales = k_scales, c.v_scales = v_scales;
+  c.out = out, c.query = query, c.k_cache = k_cache, c.v_cache = v_cache;
+  c.block_tables = block_tables, c.context_lens = context_lens;
+  c.num_queries = num_queries, c.num_seqs = num_seqs, c.num_heads = num_heads, c.num_kv_heads = num_kv_heads;
+  c.head_size = head_size, c.block_size = block_size, c.max_blocks_per_seq = max_blocks_per_seq;
+  c.scale = scale, c.stream = stream, c.dtype = PA_BF16, c.num_physical_blocks = num_physical_blocks;
+  c.workspace = workspace, c.workspace_bytes = workspace_bytes, c.error_flag = error_flag;
+  return pa::prefill_impl(c);
+}
