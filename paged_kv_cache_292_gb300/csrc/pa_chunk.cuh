@@ -33,9 +33,8 @@ struct ChunkCall {
   int32_t* error_flag;
 };
 
-constexpr int kLeastUnits = 4;  // units of a CTA's range, where there are as many
-
 struct ChunkParams {
+  CUtensorMap tm_q;        // (element, head, token)
   CUtensorMap tm_k, tm_v;  // (64 elements, chunk of 64 within a token row, token row); int8: (D, KV head, token row)
   const void* q;
   void* out;
@@ -49,14 +48,14 @@ struct ChunkParams {
   int32_t* error_flag;
   float* part_ml;  // [2 * CTAs][256][2]
   float* part_o;   // [2 * CTAs][2][D / 4][128][4]: a thread's row side by side with its neighbours'
-  int4* cuts;      // [CTAs]: (sequence, head, pair, first tile) in which a CTA's range begins
+  // [CTAs][2]: the item in which a CTA's range begins, (sequence, head, pair, first tile), and its
+  // (first row of the token buffer, tokens, 0, 0).
+  int4* cuts;
   int num_tokens, num_seqs, num_queries, num_heads, kv_heads, group, tile_tokens;
   int block_size, max_blocks, max_tokens, num_physical_blocks, box_rows;
-  // bf16 and int8: scores are scale_log2 * <(q & q_keep) ^ q_flip, k>: a negative scale changes the
-  // queries' signs and a scale of zero makes them zero, so that scale_log2 > 0
-  // and the largest product is the largest score.
-  float scale_log2;  // (fp32: with its sign)
-  uint32_t q_keep, q_flip;
+  // Scores are scale_log2 * sign * <q, k> with scale_log2 > 0, so that the largest product
+  // (times sign) is the largest score; fp32: scale_log2 has the sign.
+  float scale_log2, sign;
   unsigned long long wait_limit_ns;
   long long stall_unit;  // tests of the bounded waits: unit of the list whose tile's copies are withheld
 };
@@ -109,7 +108,7 @@ struct ChunkItems {
   }
   // False behind the range's last item.
   __device__ __forceinline__ bool next(const ChunkParams& p) {
-    start += (int64_t)tiles * weight;
+    start += kItemUnits + (int64_t)tiles * weight;
     if (start >= ub) return false;
     if (++pair == cs.pairs()) {
       pair = 0;
@@ -125,10 +124,6 @@ struct ChunkItems {
     return true;
   }
   __device__ __forceinline__ bool two() const { return weight == 2; }
-  // First and end of the tiles of softmax group w, `step()` apart.
-  __device__ __forceinline__ int first(int w) const { return t0 + (two() ? 0 : w); }
-  __device__ __forceinline__ int end(int w) const { return two() && w == 0 ? min(t1, cs.tiles_first(pair)) : t1; }
-  __device__ __forceinline__ int step() const { return two() ? 1 : 2; }
 };
 
 // This CTA's range of the list and the item that it begins in, found by all of its threads
@@ -153,16 +148,16 @@ __device__ __forceinline__ bool chunk_begin(const ChunkParams& p, ChunkItems* at
     return all;
   };
   if (tid < 4) found[tid] = -1;
-  int64_t total = 0;
-  for (int b = 0; b < p.num_seqs; b += kThreads) total += block_sum(units_of(b + tid, cta == 0));
-  const int ranges = chunk_ranges(total, gridDim.x, kLeastUnits);
+  int64_t total = 0, units = 0;  // `units`: of this thread's sequence, where each has one at most
+  for (int b = 0; b < p.num_seqs; b += kThreads) total += block_sum(units = units_of(b + tid, cta == 0));
+  const int ranges = chunk_ranges(total, gridDim.x);
   bool here = total > 0 && cta < ranges;
   if (here) {
     at->ua = range_start(cta, total, ranges);
     at->ub = range_start(cta + 1, total, ranges);
     int64_t before = 0;
     for (int b = 0; b < p.num_seqs; b += kThreads) {
-      const int64_t mine = units_of(b + tid, false);
+      const int64_t mine = p.num_seqs <= kThreads ? units : units_of(b + tid, false);
       const int64_t incl = warp_incl_scan_ll(mine, lane);
       const int64_t all = block_sum(mine);
       int64_t excl = before + incl - mine;
@@ -184,7 +179,7 @@ __device__ __forceinline__ bool chunk_begin(const ChunkParams& p, ChunkItems* at
     const int64_t in_head = in_seq - at->head * per_head;
     for (int j = tid; j < at->cs.pairs(); j += kThreads) {
       const int64_t a = at->cs.before(j);
-      if (a <= in_head && in_head < a + (int64_t)at->cs.tiles(j) * at->cs.weight(j)) {
+      if (a <= in_head && in_head < a + at->cs.item_units(j)) {
         found[2] = j;
         found[3] = a;
       }
@@ -195,8 +190,16 @@ __device__ __forceinline__ bool chunk_begin(const ChunkParams& p, ChunkItems* at
     at->set();
     here = at->pair >= 0;
   }
-  if (tid == 0)
-    p.cuts[cta] = here ? make_int4(at->seq, at->head, at->pair, at->t0 < at->tiles ? at->t0 : 0) : make_int4(-1, 0, 0, 0);
+  if (tid == 0) {
+    int4 item = make_int4(-1, 0, 0, 0), rows = make_int4(0, 0, 0, 0);
+    if (here) {
+      const int first = at->pair * 2 * p.tile_tokens;
+      item = make_int4(at->seq, at->head, at->pair, at->t0 < at->tiles ? at->t0 : 0);
+      rows = make_int4(at->row.row0 + first, min(at->row.n - first, 2 * p.tile_tokens), 0, 0);
+    }
+    p.cuts[2 * cta] = item;
+    p.cuts[2 * cta + 1] = rows;
+  }
   return here;
 }
 
@@ -206,7 +209,7 @@ __device__ __forceinline__ bool chunk_begin(const ChunkParams& p, ChunkItems* at
 // begin inside of the same one; its rows are shared out among the blocks of b and their warps,
 // with eight warps to a row where there are few.
 // ---------------------------------------------------------------------------
-constexpr int kJoinBlocks = 4;
+constexpr int kJoinBlocks = 16;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ ChunkParams p) {
@@ -215,22 +218,26 @@ __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ C
   const int b = blockIdx.x + 1, ctas = gridDim.x + 1;
   griddep_wait();
   griddep_launch_dependents();
-  const int4 cut = __ldcg(p.cuts + b);
+  const int4 cut = __ldcg(p.cuts + 2 * b), before = __ldcg(p.cuts + 2 * b - 2), item = __ldcg(p.cuts + 2 * b + 1);
   if (cut.x < 0 || cut.w == 0) return;  // no such range, or it begins with an item
   auto same = [&](const int4& o) { return o.x == cut.x && o.y == cut.y && o.z == cut.z && o.w != 0; };
-  if (same(__ldcg(p.cuts + b - 1))) return;
-  int last = b;
-  while (last + 1 < ctas && same(__ldcg(p.cuts + last + 1))) ++last;
+  if (same(before)) return;
+  int parts = 2;  // CTA b - 1's, b's and those behind that begin in the item, too
+  for (int i = b + 1;; i += 32) {
+    const bool more = i + lane < ctas && same(__ldcg(p.cuts + 2 * min(i + lane, ctas - 1)));
+    const unsigned run = __ballot_sync(0xffffffffu, more);
+    parts += __ffs(~run) == 0 ? 32 : __ffs(~run) - 1;
+    if (run != 0xffffffffu) break;
+  }
   // (After a timeout of the kernel before the list may hold anything: stay inside.)
-  if (cut.x >= p.num_seqs || cut.y < 0 || cut.y >= p.kv_heads || cut.z < 0) {
+  const int tokens = item.y;
+  if (cut.y < 0 || cut.y >= p.kv_heads || item.x < 0 || tokens < 0 || tokens > 2 * p.tile_tokens ||
+      item.x + tokens > p.num_tokens) {
     if (threadIdx.x == 0) report(p.error_flag, PA_DEVERR_STATE);
     return;
   }
-  const ChunkRow r = chunk_row(p, cut.x, false);
-  const int first = cut.z * 2 * p.tile_tokens;  // the item's first token
-  const int tokens = min(r.n - first, 2 * p.tile_tokens), parts = last - b + 2;
   const int rows = tokens * p.group;
-  const int per_row = rows <= 4 * kJoinBlocks ? 8 : 1;  // warps
+  const int per_row = rows <= kJoinBlocks ? 8 : 1;  // warps
   __shared__ float shared_parts[8][6][32];
   for (int i = blockIdx.y * (8 / per_row) + warp / per_row; i < rows; i += kJoinBlocks * (8 / per_row)) {
     const int tok = i / p.group, g = i - tok * p.group;
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ C
     }
     if (lane < kLanes) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const size_t at = ((size_t)(r.row0 + first + tok) * p.num_heads + cut.y * p.group + g) * D + 4 * lane;
+      const size_t at = ((size_t)(item.x + tok) * p.num_heads + cut.y * p.group + g) * D + 4 * lane;
       if constexpr (sizeof(T) == 4)
         *reinterpret_cast<float4*>(static_cast<T*>(p.out) + at) =
             make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
@@ -318,7 +325,7 @@ ChunkScratch chunk_scratch(int head_size, int sm_count) {
     return at;
   };
   const size_t rows = (size_t)2 * sm_count * 2 * kChunkRows;
-  s.cuts = take(sizeof(int4) * (size_t)sm_count);
+  s.cuts = take(sizeof(int4) * (size_t)(2 * sm_count));
   s.part_ml = take(rows * 8);
   s.part_o = take(rows * head_size * 4);
   s.total = o;

@@ -7,8 +7,8 @@
 // last row sees.  A tile of an item with two row tiles costs two units, one
 // of an item with a single row tile (a chunk's last pair, where its tokens do not
 // fill it) one.  All items' units (sequence, head, pair, tile) form one list, cut
-// into equal ranges of two units or more, one per CTA; a tile belongs to the range
-// of its first unit.  So every CTA gets the same work whatever the batch.  A
+// into equal ranges, one per CTA; a tile belongs to the range of its first unit.  Before its
+// first tile an item has a few units for what it costs besides.  So every CTA gets the same work whatever the batch.  A
 // range cuts at most two items: the one that it begins in (partial slot 0) and the one
 // that it ends in (slot 1).
 #pragma once
@@ -19,23 +19,26 @@ namespace pa {
 
 constexpr int kChunkRows = 128;    // query rows per tile (M of the products)
 constexpr int kChunkTokens = 128;  // tokens per tile
+constexpr int kItemUnits = 4;      // what an item costs besides its tiles (queries in, pipeline up and down, rows out)
+constexpr int kLeastUnits = kItemUnits + 4;  // of a range, where there are as many (kItemUnits + 2 at least)
 constexpr int kChunkRowsF32 = 64;  // query rows per tile over fp32 pools
 
-// sum over i = 0 .. n - 1 of floor((a * i + b) / m), for a, b >= 0, m > 0: the
+// sum over i = 0 .. n - 1 of floor((a * i + b) / 128), for a, b >= 0, n < 2^24: the
 // quotients of a and b leave a sum over a smaller triangle, whose axes then change
 // places (Euclid's steps; Graham, Knuth, Patashnik, Concrete Mathematics, 3.5).
-PA_HD int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t sum = 0;
-  while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const int64_t top = a * n + b;
-    n = top / m;
-    b = top % m;
-    const int64_t t = m;
-    m = a;
-    a = t;
+PA_HD int64_t floor_sum_128(int64_t n, int64_t a, int64_t b) {
+  int64_t sum = n * (n - 1) / 2 * (a >> 7) + n * (b >> 7);
+  uint32_t x = (uint32_t)a & 127u, m = 128u, y = (uint32_t)b & 127u, k = (uint32_t)n;
+  while (x != 0u && k != 0u) {
+    const uint32_t top = x * k + y;  // below 2^31
+    k = top / m;
+    y = top % m;
+    const uint32_t t = m;
+    m = x;
+    x = t;
+    sum += (int64_t)k * (k - 1) / 2 * (x / m) + (int64_t)k * (y / m);
+    x %= m;
+    y %= m;
   }
   return sum;
 }
@@ -56,6 +59,7 @@ struct ChunkSeq {
   // Tiles of the pair's first row tile.
   PA_HD int tiles_first(int pair) const { return tiles_for((2 * pair + 1) * tile_tokens); }
   PA_HD int weight(int pair) const { return n - 2 * pair * tile_tokens > tile_tokens ? 2 : 1; }
+  PA_HD int64_t item_units(int pair) const { return kItemUnits + (int64_t)tiles(pair) * weight(pair); }
   // Units of the pairs before `pair` (0 .. pairs()) of one head.
   PA_HD int64_t before(int pair) const {
     const int full = smaller(pair, pairs() - 1);  // pairs that the chunk fills
@@ -65,25 +69,25 @@ struct ChunkSeq {
       int64_t ones = (int64_t)kChunkTokens - old;  // pairs of one tile come first
       ones = ones < step ? 0 : ones / step;
       if (ones > full) ones = full;
-      units = 2 * (ones + floor_sum(full - ones, kChunkTokens, step, old + (ones + 1) * step + kChunkTokens - 1));
+      units = (int64_t)full * kItemUnits + 2 * (ones + floor_sum_128(full - ones, step, old + (ones + 1) * step + kChunkTokens - 1));
     }
-    if (pair > full) units += (int64_t)tiles(pair - 1) * weight(pair - 1);
+    if (pair > full) units += item_units(pair - 1);
     return units;
   }
   PA_HD int64_t units() const { return n > 0 ? before(pairs()) : 0; }
 };
 
-// First tile of an item that begins at unit 0 whose first unit is at or behind `unit`.
+// First tile of an item that begins at unit 0 whose first unit is at or behind `unit`
+// (the item's own units go before its first tile's).
 PA_HD int chunk_tile_at(int64_t unit, int weight, int tiles) {
   if (unit <= 0) return 0;
-  const int64_t t = weight == 2 ? (unit + 1) / 2 : unit;
-  return t < tiles ? (int)t : tiles;
+  const int64_t u = unit > kItemUnits ? unit - kItemUnits : 0, t = weight == 2 ? (u + 1) / 2 : u;
+  return t < 1 ? 1 : t < tiles ? (int)t : tiles;
 }
 
-// Ranges for a list of `total` units: two units at least, so that each holds a
-// tile's first unit.
-PA_HD int chunk_ranges(int64_t total, int most, int least_units) {
-  const int64_t r = total / least_units;
+// Ranges for a list of `total` units: so long that each holds a tile's first unit.
+PA_HD int chunk_ranges(int64_t total, int most) {
+  const int64_t r = total / kLeastUnits;
   return r < 1 ? 1 : r < most ? (int)r : most;
 }
 

@@ -16,11 +16,11 @@
 //   warps 0-7, 8-15 softmax groups 0 and 1: two threads per row, 64 tokens each,
 //                   which exchange their maxima; scores come from tensor memory,
 //                   weights go back there as bf16
-//   warp 16         loads K and V tiles: TMA boxes of gcd(block_size, 128) token
+//   warp 16         walks the list, and loads K and V tiles: TMA boxes of gcd(block_size, 128) token
 //                   rows x 64 elements into 128-byte swizzled panels (int8: the
 //                   codes into a ring of their own, the scales beside them);
 //                   blocks that are no multiple of 8: 16-byte asynchronous copies
-//   warp 17         issues the products (tcgen05.mma, one thread)
+//   warp 17         loads an item's queries (TMA), issues the products (tcgen05.mma, one thread)
 //   warps 18, 19    int8: widen the codes into the panels.  bf16: warp 18 zeroes what
 //                   lies behind a context's end in its last V tile (zero weights
 //                   do not cancel the NaN that may lie there)
@@ -53,6 +53,21 @@ constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
 // then weights are at most 2^8, which bf16 and the fp32 sums hold as well as 1.
 constexpr float kSlack = 8.f;
 constexpr int kScaleSlots = 4;  // int8: tiles whose scales are in shared memory
+constexpr int kItemSlots = 4;   // items that the loads may be ahead
+
+// An item as the other warps need it; the load warp, which walks the list, puts it into a ring.
+struct ChunkItem {
+  int row;      // first row of the token buffer
+  int tokens;   // of the item; 0: the range has no more items
+  int sees;     // tokens that the first of them sees (0 or less: none)
+  int head;
+  int t0, t1;   // tiles of this CTA,
+  int end0;     // and where those of the first row tile end
+  int flags;
+  int ctx, pad[3];
+  __device__ __forceinline__ bool two() const { return flags & 1; }    // row tiles
+  __device__ __forceinline__ bool whole() const { return flags & 2; }  // no other CTA has a tile
+};
 
 template <int D, bool I8>
 struct ChunkLayout {
@@ -118,9 +133,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
   auto sc_empty = [&](int i) { return bars + 8u * (3 * NS + 11 + kScaleSlots + i); };
   auto raw_full = [&](int i) { return bars + 8u * (3 * NS + 11 + 2 * kScaleSlots + i); };
   auto raw_empty = [&](int i) { return bars + 8u * (3 * NS + 11 + 2 * kScaleSlots + NR + i); };
-  static_assert(8 * (3 * NS + 11 + 2 * kScaleSlots + 2 * NR) <= 512, "barriers lie before the flags");
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 512);
-  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + 516);
+  constexpr int kItemBars = 3 * NS + 11 + 2 * kScaleSlots + 2 * NR;
+  auto item_full = [&](int i) { return bars + 8u * (kItemBars + i); };
+  auto item_empty = [&](int i) { return bars + 8u * (kItemBars + kItemSlots + i); };
+  const uint32_t q_empty = bars + 8u * (kItemBars + 2 * kItemSlots);
+  static_assert(8 * (kItemBars + 2 * kItemSlots + 1) <= 560, "barriers lie before the flags");
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 560);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + 564);
   auto timed_out = [&]() {
     if (lane == 0) {
       report(p.error_flag, PA_DEVERR_TIMEOUT);
@@ -130,8 +149,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
   griddep_wait();
   griddep_launch_dependents();
 
+  ChunkItem* ring_items = reinterpret_cast<ChunkItem*>(smem + 576);  // 48 bytes each
   ChunkItems items;
-  if (!chunk_begin<kChunkThreads>(p, &items, reinterpret_cast<long long*>(smem + 640))) return;
+  if (!chunk_begin<kChunkThreads>(p, &items, reinterpret_cast<long long*>(smem + 768))) return;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full(i), I8 ? kWidenWarps : 1);
@@ -146,7 +166,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
       mbar_init(sc_full(i), 1);
       mbar_init(sc_empty(i), 1);
     }
-    mbar_init(q_full, kSoftmaxWarps);
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(item_full(i), 1);
+      mbar_init(item_empty(i), kSoftmaxWarps + 1 + (I8 ? kWidenWarps : kOdd ? 0 : 1));
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, kSoftmaxWarps);
     mbar_init(joined, kSoftmaxWarps);
     for (int w = 0; w < 2; ++w) {
       mbar_init(exchanged(w), kSoftmaxWarps / 2);
@@ -158,7 +183,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
     *abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == kProductWarp) tmem_alloc(smem_addr(smem + 516), 512);
+  // The next item of the ring, and the release of it (by every warp that takes them).
+  Ring at_item;
+  auto take_item = [&](ChunkItem* it) -> bool {  // false: no more, or a wait ran out
+    if (!wait_or_abort(item_full(at_item.i), at_item.phase, p.wait_limit_ns, abort_flag)) {
+      timed_out();
+      return false;
+    }
+    const int4* from = reinterpret_cast<const int4*>(ring_items + at_item.i);
+    const int4 a = from[0], b = from[1];
+    it->row = a.x, it->tokens = a.y, it->sees = a.z, it->head = a.w;
+    it->t0 = b.x, it->t1 = b.y, it->end0 = b.z, it->flags = b.w;
+    it->ctx = ring_items[at_item.i].ctx;
+    return it->tokens > 0;
+  };
+  auto leave_item = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_empty(at_item.i));
+    at_item.next(kItemSlots);
+  };
+  if (warp == kProductWarp) tmem_alloc(smem_addr(smem + 564), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -194,44 +238,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
       return true;
     };
     bool alive = true;
-    for (bool more = true; more; more = items.next(p)) {
-      if (items.t0 >= items.t1) continue;
-      const bool two = items.two();
-      const int rr = row, row_tile = two ? w : 0;
-      const int tok_in = rr / p.group, g = rr - tok_in * p.group;
-      const int token = (2 * items.pair + row_tile) * p.tile_tokens + tok_in;  // of the chunk
-      const bool real = rr < p.tile_tokens * p.group && token < items.cs.n;
-      const size_t at = ((size_t)(items.row.row0 + token) * p.num_heads + items.head * p.group + g) * D;
+    const int tok_in = row / p.group;
+    ChunkItem it;
+    for (; take_item(&it); leave_item()) {
+      const bool two = it.two();
+      const int row_tile = two ? w : 0;
+      const int token = row_tile * p.tile_tokens + tok_in;  // of the item
+      const bool real = tok_in < p.tile_tokens && token < it.tokens;
       // Tokens that the row sees.
-      const int sees = real ? max(items.cs.old + token + 1, 0) : 0;
-      // The row's queries into the swizzled Q tile: half a row per thread with
-      // two row tiles, a quarter with one.
-      {
-        constexpr int kUnits = D / 8;  // 16-byte units of a row
-        const int n = two ? kUnits / 2 : kUnits / 4, u0 = n * (two ? half : 2 * w + half);
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
-        unsigned char* dst = smem + L::kQ + (two ? w * L::kTileBytes : 0) + row * 128;
-        uint4 v[kUnits / 2];
-#pragma unroll
-        for (int i = 0; i < kUnits / 2; ++i)
-          v[i] = real && i < n ? __ldg(src + u0 + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < kUnits / 2; ++i) {
-          if (i < n) {
-            const int u = u0 + i;
-            v[i].x = (v[i].x & p.q_keep) ^ p.q_flip;
-            v[i].y = (v[i].y & p.q_keep) ^ p.q_flip;
-            v[i].z = (v[i].z & p.q_keep) ^ p.q_flip;
-            v[i].w = (v[i].w & p.q_keep) ^ p.q_flip;
-            *reinterpret_cast<uint4*>(dst + (u >> 3) * kPanel + (((u & 7) ^ (row & 7)) << 4)) = v[i];
-          }
-        }
-        async_proxy_fence();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-      }
-      const int step = items.step(), x0 = items.first(w), x1 = items.end(w);
+      const int sees = real ? max(it.sees + token, 0) : 0;
+      const int step = two ? 1 : 2, x0 = it.t0 + (two ? 0 : w), x1 = w == 0 ? it.end0 : it.t1;
       // A warp without a row of the batch only takes part in the barriers: its rows' weights
       // may be anything, they reach nothing but its rows of O, which nobody reads.
       const bool rows_here = __any_sync(0xffffffffu, real);
@@ -250,7 +266,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
           if (lane == 0) mbar_arrive(p_full(w));
           continue;
         }
-        const uint32_t nth = tile_count + (uint32_t)(x - items.t0);
+        const uint32_t nth = tile_count + (uint32_t)(x - it.t0);
         const float* k_scale = nullptr;
         if constexpr (I8) {
           if (!(alive = wait_or_abort(sc_full(nth % kScaleSlots), (nth / kScaleSlots) & 1u, p.wait_limit_ns, abort_flag)))
@@ -261,6 +277,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[0]), s_addr + 64u * half);
         tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[32]), s_addr + 64u * half + 32u);
         tmem_wait_load();
+        if (p.sign != 1.f) {  // a negative scale (or zero)
+#pragma unroll
+          for (int i = 0; i < 64; ++i) s[i] *= p.sign;
+        }
         if constexpr (I8) {
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
@@ -364,16 +384,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(w));
       }
-      tile_count += (uint32_t)(items.t1 - items.t0);
+      tile_count += (uint32_t)(it.t1 - it.t0);
       if (alive) alive = wait_or_abort(o_full(0), o_phase, p.wait_limit_ns, abort_flag);
       if (alive) alive = wait_or_abort(o_full(1), o_phase, p.wait_limit_ns, abort_flag);
       o_phase ^= 1u;
       tc_fence_after();
-      // Whole items end here; a part of one leaves its sums for the join.
-      const bool whole = items.t0 == 0 && items.t1 == items.tiles;
-      const size_t part = (size_t)2 * blockIdx.x + (items.t0 == 0 ? 1 : 0);
+      // Whole items end here: a row's thread puts its part into the Q tile, which nobody
+      // reads any more, and the warp writes its rows out side by side (a thread of a row
+      // each would touch 32 lines with every store).  A part of an item leaves its sums for the join.
+      const bool whole = it.whole();
+      const size_t part = (size_t)2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
       float* part_o = p.part_o + (part * 2 + row_tile) * (kChunkRows * D) + 4 * row;  // + dims * 128
       float2* part_ml = reinterpret_cast<float2*>(p.part_ml) + part * (2 * kChunkRows) + row_tile * kChunkRows + row;
+      unsigned char* staged = smem + L::kQ + (two ? w * L::kTileBytes : 0);
+      const int row0 = row & ~31;  // the warp's first row
+      auto stage = [&](int d0, const float (&o)[16]) {  // 16 dims of this row
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int u = d0 / 8 + i;
+          *reinterpret_cast<uint4*>(staged + (u >> 3) * kPanel + row * 128 + (((u & 7) ^ (row & 7)) << 4)) =
+              make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                         pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+        }
+      };
+      auto write_out = [&](int d0, int dims) {  // the warp's rows, dims d0 .. d0 + dims - 1 (32 or 64; 16 to 64)
+        __syncwarp();
+        const int units = dims / 8, per = 32 / units;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+#pragma unroll 4
+        for (int r = row0 + lane / units; r < row0 + 32; r += per) {
+          const int u = d0 / 8 + lane % units, t = r / p.group, tok = row_tile * p.tile_tokens + t;
+          if (t < p.tile_tokens && tok < it.tokens)
+            *reinterpret_cast<uint4*>(out + ((size_t)(it.row + tok) * p.num_heads + it.head * p.group + (r - t * p.group)) * D +
+                                      8 * u) =
+                *reinterpret_cast<const uint4*>(staged + (u >> 3) * kPanel + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+        }
+      };
       if (two) {
         float theirs = 0.f;
         if (alive) alive = exchange(l, &theirs);
@@ -382,36 +428,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
           break;
         }
         l += theirs;
-        if (!rows_here) continue;
-        const float inv = 1.f / l;
+        if (rows_here) {
+          const float inv = 1.f / l;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t o[32];
-          tmem_load32(o, o_addr + 32u * c);
-          tmem_wait_load();
-          if (!real) continue;
-          const int d0 = (D / 2) * half + 32 * c;
-          if (whole) {
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[16];
+            tmem_load16(o, o_addr + 16u * c);
+            tmem_wait_load();
+            const int d0 = (D / 2) * half + 16 * c;
+            if (whole) {
+              float f[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (l != 0.f) {
-                v.x = pack_bf16x2(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
-                v.y = pack_bf16x2(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
-                v.z = pack_bf16x2(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
-                v.w = pack_bf16x2(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
-              }
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + d0 + 8 * i) = v;
+              for (int i = 0; i < 16; ++i) f[i] = l != 0.f ? __uint_as_float(o[i]) * inv : 0.f;
+              stage(d0, f);
+            } else if (real) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(part_o + (size_t)(d0 + 4 * i) * kChunkRows) =
+                    make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                __uint_as_float(o[4 * i + 3]));
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(part_o + (size_t)(d0 + 4 * i) * kChunkRows) =
-                  make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                              __uint_as_float(o[4 * i + 3]));
           }
+          if (whole)
+            write_out((D / 2) * half, D / 2);
+          else if (real && half == 0)
+            *part_ml = make_float2(m * p.scale_log2, l);
         }
-        if (real && !whole && half == 0) *part_ml = make_float2(m * p.scale_log2, l);
       } else {
         // One row tile: the row's four threads leave (m, l) in tensor memory, where the scores
         // were, and take a quarter of the dims each from both groups' O.
@@ -432,46 +474,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
           timed_out();
           break;
         }
-        if (!rows_here) continue;
-        uint32_t a[16], b[16];
-        tmem_load16(a, tmem + lanes);
-        tmem_load16(b, tmem + lanes + 128u);
-        tmem_wait_load();
-        const float m0 = __uint_as_float(a[0]), m1 = __uint_as_float(b[0]);
-        const float l0 = __uint_as_float(a[1]) + __uint_as_float(a[5]), l1 = __uint_as_float(b[1]) + __uint_as_float(b[5]);
-        // A group that saw nothing (l == 0) may have anything in O.
-        const float top = fmaxf(l0 != 0.f ? m0 : -INFINITY, l1 != 0.f ? m1 : -INFINITY);
-        const float f0 = l0 != 0.f ? ex2_ftz((m0 - top) * p.scale_log2) : 0.f;
-        const float f1 = l1 != 0.f ? ex2_ftz((m1 - top) * p.scale_log2) : 0.f;
-        const float sum = f0 * l0 + f1 * l1;
-        const float inv = whole ? 1.f / sum : 1.f;
-        const int d0 = (D / 4) * (2 * w + half);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          tmem_load16(a, o_all + d0 + 16u * c);
-          tmem_load16(b, o_all + (uint32_t)D + d0 + 16u * c);
+        if (rows_here) {
+          uint32_t a[16], b[16];
+          tmem_load16(a, tmem + lanes);
+          tmem_load16(b, tmem + lanes + 128u);
           tmem_wait_load();
-          if (!real) continue;
-          float o[16];
+          const float m0 = __uint_as_float(a[0]), m1 = __uint_as_float(b[0]);
+          const float l0 = __uint_as_float(a[1]) + __uint_as_float(a[5]), l1 = __uint_as_float(b[1]) + __uint_as_float(b[5]);
+          // A group that saw nothing (l == 0) may have anything in O.
+          const float top = fmaxf(l0 != 0.f ? m0 : -INFINITY, l1 != 0.f ? m1 : -INFINITY);
+          const float f0 = l0 != 0.f ? ex2_ftz((m0 - top) * p.scale_log2) : 0.f;
+          const float f1 = l1 != 0.f ? ex2_ftz((m1 - top) * p.scale_log2) : 0.f;
+          const float sum = f0 * l0 + f1 * l1;
+          const float inv = sum == 0.f ? 0.f : whole ? 1.f / sum : 1.f;
+          const int d0 = (D / 4) * (2 * w + half);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            o[i] = ((l0 != 0.f ? __uint_as_float(a[i]) * f0 : 0.f) + (l1 != 0.f ? __uint_as_float(b[i]) * f1 : 0.f)) *
-                   (sum != 0.f ? inv : 0.f);
-          if (whole) {
+          for (int c = 0; c < D / 64; ++c) {
+            tmem_load16(a, o_all + d0 + 16u * c);
+            tmem_load16(b, o_all + (uint32_t)D + d0 + 16u * c);
+            tmem_wait_load();
+            float o[16];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + d0 + 16 * c + 8 * i) =
-                  make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                             pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-          } else {
+            for (int i = 0; i < 16; ++i)
+              o[i] = ((l0 != 0.f ? __uint_as_float(a[i]) * f0 : 0.f) + (l1 != 0.f ? __uint_as_float(b[i]) * f1 : 0.f)) * inv;
+            if (whole) {
+              stage(d0 + 16 * c, o);
+            } else if (real) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4*>(part_o + (size_t)(d0 + 16 * c + 4 * i) * kChunkRows) =
-                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(part_o + (size_t)(d0 + 16 * c + 4 * i) * kChunkRows) =
+                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
           }
+          if (whole)
+            write_out(d0, D / 4);
+          else if (real && w == 0 && half == 0)
+            *part_ml = make_float2(top * p.scale_log2, sum);
         }
-        if (real && !whole && w == 0 && half == 0) *part_ml = make_float2(top * p.scale_log2, sum);
       }
+      // The Q tile is free for the next item's queries (which copies write).
+      async_proxy_fence();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty);
     }
   } else if (warp == kLoadWarp) {
     // ---------------- loads ----------------
@@ -514,6 +559,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
     };
     for (bool more = true; alive && more; more = items.next(p)) {
       if (items.t0 >= items.t1) continue;
+      if (!(alive = wait(item_empty(at_item.i), at_item.phase ^ 1u))) break;
+      if (lane == 0) {
+        const int first = items.pair * 2 * p.tile_tokens;
+        int4* to = reinterpret_cast<int4*>(ring_items + at_item.i);
+        to[0] = make_int4(items.row.row0 + first, min(items.cs.n - first, 2 * p.tile_tokens), items.cs.old + first + 1,
+                          items.head);
+        to[1] = make_int4(items.t0, items.t1, items.two() ? min(items.t1, items.cs.tiles_first(items.pair)) : items.t1,
+                          (items.two() ? 1 : 0) | (items.t0 == 0 && items.t1 == items.tiles ? 2 : 0));
+        ring_items[at_item.i].ctx = items.row.ctx;
+        mbar_arrive(item_full(at_item.i));
+      }
+      __syncwarp();
+      at_item.next(kItemSlots);
       const int32_t* table = p.tables + (size_t)items.seq * p.max_blocks;
       const int ctx = items.row.ctx;
       auto block_of = [&](int tok) -> int {  // -1: none
@@ -568,7 +626,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         return true;
       };
       auto load = [&](bool v, int x, int row) -> bool {
-        const bool withhold = p.stall_unit >= 0 && items.start + (int64_t)x * items.weight == p.stall_unit;
+        const bool withhold = p.stall_unit >= 0 && items.start + kItemUnits + (int64_t)x * items.weight == p.stall_unit;
         if constexpr (kOdd) {
           // What it waits for may wait for these.
           if (__any_sync(0xffffffffu, !mbar_try_wait(taken(ring.i), ring.phase ^ 1u))) tell_all();
@@ -648,6 +706,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
       tile_count += (uint32_t)(t1 - t0);
     }
     if constexpr (kOdd) tell_all();
+    if (alive && wait(item_empty(at_item.i), at_item.phase ^ 1u)) {
+      if (lane == 0) {
+        ring_items[at_item.i].tokens = 0;  // no more
+        mbar_arrive(item_full(at_item.i));
+      }
+      __syncwarp();
+    }
     named_barrier_sync(1, kChunkThreads);
     if (!kOdd && *abort_flag != 0) {
       // Copies that were started may still be landing: wait for them (again
@@ -671,11 +736,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
       timed_out();
       return false;
     };
-    for (bool rest = true; alive && rest; rest = items.next(p)) {
-      const int t0 = items.t0, t1 = items.t1;
-      if (t0 >= t1) continue;
-      const bool two = items.two();
-      const int ahead = two ? 1 : 2, end0 = items.end(0);
+    if (lane == 0) prefetch_tensormap(&p.tm_q);
+    ChunkItem it;
+    bool first = true;
+    for (; alive && take_item(&it); leave_item()) {
+      const int t0 = it.t0, t1 = it.t1;
+      const bool two = it.two();
+      const int ahead = two ? 1 : 2, end0 = it.end0;
+      // The queries: (token, group head) rows of a row tile are one box.
+      if (!first && !(alive = wait(q_empty, q_phase ^ 1u))) break;
+      first = false;
+      if (lane == 0) {
+        const uint32_t bytes = 128u * p.group * p.tile_tokens;
+        mbar_arrive_expect_tx(q_full, (two ? 2u : 1u) * L::kPanels * bytes);
+        for (int w = 0; w < (two ? 2 : 1); ++w)
+          for (int c = 0; c < L::kPanels; ++c)
+            tma_load_3d(base + L::kQ + w * L::kTileBytes + c * kPanel, &p.tm_q, 64 * c, it.head * p.group,
+                        it.row + w * p.tile_tokens, q_full);
+      }
+      __syncwarp();
       // Whether group w has tile x.
       auto has = [&](int w, int x) { return w != 0 || x < end0; };
       // S of group w from the K tile in stage `st`.
@@ -775,8 +854,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
     const int t = (warp - kWidenWarp) * 32 + lane, row0 = t / kUnits, unit = t % kUnits;
     Ring ring, raw;
     bool alive = true;
-    for (bool more = true; alive && more; more = items.next(p)) {
-      const int tiles = 2 * (items.t1 - items.t0);  // K and V
+    ChunkItem it;
+    for (; alive && take_item(&it); leave_item()) {
+      const int tiles = 2 * (it.t1 - it.t0);  // K and V
       for (int x = 0; x < tiles; ++x) {
         alive = wait_or_abort(raw_full(raw.i), raw.phase, p.wait_limit_ns, abort_flag) &&
                 wait_or_abort(empty(ring.i), ring.phase ^ 1u, p.wait_limit_ns, abort_flag);
@@ -816,10 +896,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
     // ---------------- the end of a context ----------------
     uint32_t at = 0, phases = 0;  // loads of the segments before; parity per stage
     bool alive = true;
-    for (bool more = true; alive && more; more = items.next(p)) {
-      if (items.t0 >= items.t1) continue;
-      at += 2u * (uint32_t)(items.t1 - items.t0);
-      const int ctx = items.row.ctx, x = items.t1 - 1;
+    ChunkItem it;
+    for (; alive && take_item(&it); leave_item()) {
+      at += 2u * (uint32_t)(it.t1 - it.t0);
+      const int ctx = it.ctx, x = it.t1 - 1;
       if (ctx % p.box_rows == 0 || x != (ctx - 1) / kChunkTokens) continue;
       const int st = (int)((at - 1) % NS);  // the segment's last load
       if (!(alive = wait_or_abort(tail(st), (phases >> st) & 1u, p.wait_limit_ns, abort_flag))) {
@@ -848,24 +928,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
 // Host side
 // ---------------------------------------------------------------------------
 
-// The pools' tensor maps, encoded for every call (about 0.1 us each).
-int make_maps(ChunkParams* prm, uint64_t pool_rows, int head_size, bool int8) {
+// Tensor maps, encoded for every call (about 0.1 us each): queries (element, head, token) in
+// boxes of a row tile's tokens, and the pools.
+int make_maps(ChunkParams* prm, uint64_t pool_rows, int head_size, bool int8, bool pools) {
   const EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return fail(PA_ERR_CUDA, "pa_prefill: the driver has no cuTensorMapEncodeTiled");
+  auto encode = [&](CUtensorMap* map, const void* at, bool bytes, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                    const cuuint32_t (&box)[3]) -> int {
+    const cuuint32_t estride[3] = {1, 1, 1};
+    const CUresult r = in_context([&] {
+      return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(at), dims,
+                 strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
+    return r == CUDA_SUCCESS ? PA_OK : fail(PA_ERR_CUDA, "pa_prefill: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  };
+  const cuuint64_t d = head_size;
+  int rc = encode(&prm->tm_q, prm->q, false, {d, (cuuint64_t)prm->num_heads, (cuuint64_t)prm->num_tokens},
+                  {2 * d, 2 * d * prm->num_heads}, {64, (cuuint32_t)prm->group, (cuuint32_t)prm->tile_tokens});
   const cuuint64_t row = (cuuint64_t)prm->kv_heads * head_size;
   const cuuint64_t chunk = int8 ? head_size : 64, elt = int8 ? 1 : 2;
-  const cuuint64_t dims[3] = {chunk, row / chunk, pool_rows}, strides[2] = {chunk * elt, row * elt};
-  const cuuint32_t box[3] = {(cuuint32_t)chunk, 1, (cuuint32_t)prm->box_rows}, estride[3] = {1, 1, 1};
-  for (int i = 0; i < 2; ++i) {
-    const CUresult r = in_context([&] {
-      return enc(i ? &prm->tm_v : &prm->tm_k, int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                 const_cast<void*>(i ? prm->v_cache : prm->k_cache), dims, strides, box, estride,
-                 CU_TENSOR_MAP_INTERLEAVE_NONE, int8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    });
-    if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "pa_prefill: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
-  }
-  return PA_OK;
+  for (int i = 0; i < 2 && pools && rc == PA_OK; ++i)
+    rc = encode(i ? &prm->tm_v : &prm->tm_k, i ? prm->v_cache : prm->k_cache, int8, {chunk, row / chunk, (cuuint64_t)pool_rows},
+                {chunk * elt, row * elt}, {(cuuint32_t)chunk, 1, (cuuint32_t)prm->box_rows});
+  return rc;
 }
 
 template <int D, bool I8, bool kOdd>
@@ -924,10 +1011,6 @@ int prefill_impl(const ChunkCall& c) {
   if (pool_rows > 1ull << 31)
     return fail(PA_ERR_UNSUPPORTED, "pa_prefill: %llu token rows in the pool (at most 2^31)", (unsigned long long)pool_rows);
   const bool odd = prm.box_rows < 8;
-  if (!odd && !f32) {
-    rc = make_maps(&prm, pool_rows, c.head_size, c.int8);
-    if (rc != PA_OK) return rc;
-  }
   ScratchHold hold;  // scratch of the library's own, until the launches are queued
   void* workspace = c.workspace;
   if (workspace == nullptr) {
@@ -961,13 +1044,14 @@ int prefill_impl(const ChunkCall& c) {
   prm.max_tokens = c.max_blocks_per_seq * c.block_size;
   prm.num_physical_blocks = (int)(pool_rows / c.block_size);  // what the rows that the driver knows of hold
   prm.scale_log2 = c.scale != 0.f ? (float)(std::fabs((double)c.scale) * 1.4426950408889634) : 1.f;
-  prm.q_keep = c.scale != 0.f ? 0xffffffffu : 0u;
-  prm.q_flip = c.scale < 0.f ? 0x80008000u : 0u;
+  prm.sign = c.scale > 0.f ? 1.f : c.scale < 0.f ? -1.f : 0.f;
   cudaStream_t st = static_cast<cudaStream_t>(c.stream);
   if (f32) {
     prm.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
     return launch_chunks_f32(prm, dev, st, c.head_size);
   }
+  rc = make_maps(&prm, pool_rows, c.head_size, c.int8, !odd);
+  if (rc != PA_OK) return rc;
   take_wait_test(&prm.stall_unit, &prm.wait_limit_ns);
   if (c.head_size == 64) {
     if (c.int8) return odd ? launch_chunks<64, true, true>(prm, dev, st) : launch_chunks<64, true, false>(prm, dev, st);

@@ -20,12 +20,12 @@ static int64_t slow_units(const pa::ChunkSeq& c, int pairs) {
     const int keys = c.old + last;
     const int tiles = keys <= 128 ? 1 : (keys + 127) / 128;
     const int rows = last - j * 2 * c.tile_tokens;
-    u += (int64_t)tiles * (rows > c.tile_tokens ? 2 : 1);
+    u += pa::kItemUnits + (int64_t)tiles * (rows > c.tile_tokens ? 2 : 1);
   }
   return u;
 }
 
-static int check(const std::vector<pa::ChunkSeq>& seqs, int heads, int most, int least) {
+static int check(const std::vector<pa::ChunkSeq>& seqs, int heads, int most) {
   std::vector<Item> items;
   int64_t total = 0;
   for (int s = 0; s < (int)seqs.size(); ++s) {
@@ -40,13 +40,13 @@ static int check(const std::vector<pa::ChunkSeq>& seqs, int heads, int most, int
     for (int h = 0; h < heads; ++h)
       for (int j = 0; j < c.pairs(); ++j) {
         items.push_back({s, h, j, c.tiles(j), c.weight(j), total});
-        total += (int64_t)c.tiles(j) * c.weight(j);
+        total += c.item_units(j);
         if (c.tiles_first(j) > c.tiles(j)) return 4;
       }
   }
   if (total == 0) return 0;
-  const int ranges = pa::chunk_ranges(total, most, least);
-  if (ranges < 1 || ranges > most || (ranges > 1 && total / ranges < 2)) return 5;
+  const int ranges = pa::chunk_ranges(total, most);
+  if (ranges < 1 || ranges > most || (ranges > 1 && total / ranges < pa::kItemUnits + 2)) return 5;
   std::vector<int> first_tile(ranges, 0), first_item(ranges, -1);
   std::vector<std::vector<int>> owner(items.size());
   for (size_t i = 0; i < items.size(); ++i) owner[i].assign(items[i].tiles, -1);
@@ -55,7 +55,7 @@ static int check(const std::vector<pa::ChunkSeq>& seqs, int heads, int most, int
     int cut_begin = 0, cut_end = 0;
     for (size_t i = 0; i < items.size(); ++i) {
       const Item& it = items[i];
-      const int64_t end = it.start + (int64_t)it.tiles * it.weight;
+      const int64_t end = it.start + pa::kItemUnits + (int64_t)it.tiles * it.weight;
       if (end <= a || it.start >= b) continue;
       const int t0 = pa::chunk_tile_at(a - it.start, it.weight, it.tiles);
       const int t1 = pa::chunk_tile_at(b - it.start, it.weight, it.tiles);
@@ -107,7 +107,7 @@ int main() {
       c.old = context - c.n;
       c.tile_tokens = rows / group;
     }
-    const int rc = check(seqs, heads, rng() % 2 ? 152 : upto(1, 400), rng() % 2 ? 4 : 2);
+    const int rc = check(seqs, heads, rng() % 2 ? 152 : upto(1, 400));
     if (rc) {
       printf("trial %d: %d\n", trial, rc);
       return 1;
