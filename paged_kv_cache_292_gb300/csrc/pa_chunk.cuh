@@ -35,7 +35,7 @@ struct ChunkCall {
 
 struct ChunkParams {
   CUtensorMap tm_q;        // (element, head, token)
-  CUtensorMap tm_k, tm_v;  // (64 elements, chunk of 64 within a token row, token row); int8: (D, KV head, token row)
+  CUtensorMap tm_k, tm_v;  // (element of a panel, row of 8, panel, group of 8 token rows, KV head); int8: (D, KV head, token row)
   const void* q;
   void* out;
   const void* k_cache;
@@ -204,12 +204,13 @@ __device__ __forceinline__ bool chunk_begin(const ChunkParams& p, ChunkItems* at
 }
 
 // ---------------------------------------------------------------------------
-// Join: the rows of the items that range boundaries cut, by log-sum-exp.  Block
-// (b, y) has the item that CTA b's range begins inside of, if CTA b - 1's does not
-// begin inside of the same one; its rows are shared out among the blocks of b and their warps,
-// with eight warps to a row where there are few.
+// Join: the rows of the items that range boundaries cut, by log-sum-exp.  The blocks of
+// b have the item that CTA b's range begins inside of, if CTA b - 1's does not begin
+// inside of the same one.  With many rows (and few parts: the list is long, then) a warp
+// takes 32 of them, a lane each, and a slice of the dims, so that its loads lie side by side; with
+// few rows (and perhaps many parts) eight warps share a row, and a lane has four dims.
 // ---------------------------------------------------------------------------
-constexpr int kJoinBlocks = 16;
+constexpr int kJoinBlocks = 4, kSlice = 32;  // dims of a warp where there are many rows
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ ChunkParams p) {
@@ -237,20 +238,66 @@ __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ C
     return;
   }
   const int rows = tokens * p.group;
-  const int per_row = rows <= kJoinBlocks ? 8 : 1;  // warps
+  // Part k: CTA b - 1 + k, the first in its second slot, the others in their first.
+  auto slot = [&](int k) -> size_t { return (size_t)2 * (b - 1 + k) + (k == 0 ? 1 : 0); };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  const float4* po = reinterpret_cast<const float4*>(p.part_o);
+  if (rows > 8 * kJoinBlocks) {
+    constexpr int kSlices = D / kSlice;
+    for (int i = blockIdx.y * 8 + warp; i < 2 * (kChunkRows / 32) * kSlices; i += 8 * kJoinBlocks) {
+      const int d0 = (i % kSlices) * kSlice, r = (i / kSlices) * 32 + lane, tile = r / kChunkRows, in_tile = r % kChunkRows;
+      const int t = in_tile / p.group, tok = tile * p.tile_tokens + t;
+      const bool real = t < p.tile_tokens && tok < tokens;
+      if (!__any_sync(0xffffffffu, real)) continue;
+      float m = -INFINITY, l = 0.f, acc[kSlice];
+#pragma unroll
+      for (int e = 0; e < kSlice; ++e) acc[e] = 0.f;
+      if (!real) continue;  // (nothing below is for the whole warp)
+      for (int k = 0; k < parts; ++k) {
+        const float2 a = __ldcg(ml + slot(k) * (2 * kChunkRows) + r);
+        float4 o[kSlice / 4];
+#pragma unroll
+        for (int e = 0; e < kSlice / 4; ++e)
+          o[e] = __ldcg(po + ((slot(k) * 2 + tile) * (D / 4) + d0 / 4 + e) * kChunkRows + in_tile);
+        if (a.y == 0.f) continue;  // no token seen: O may be anything
+        const float mn = fmaxf(m, a.x), keep = ex2_ftz(m - mn), f = ex2_ftz(a.x - mn);
+        m = mn;
+        l = fmaf(l, keep, f * a.y);
+#pragma unroll
+        for (int e = 0; e < kSlice / 4; ++e) {
+          acc[4 * e] = fmaf(acc[4 * e], keep, f * o[e].x);
+          acc[4 * e + 1] = fmaf(acc[4 * e + 1], keep, f * o[e].y);
+          acc[4 * e + 2] = fmaf(acc[4 * e + 2], keep, f * o[e].z);
+          acc[4 * e + 3] = fmaf(acc[4 * e + 3], keep, f * o[e].w);
+        }
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int e = 0; e < kSlice; ++e) acc[e] *= inv;
+      T* out = static_cast<T*>(p.out) +
+               ((size_t)(item.x + tok) * p.num_heads + cut.y * p.group + (in_tile - t * p.group)) * D + d0;
+#pragma unroll
+      for (int e = 0; e < kSlice; e += 16 / (int)sizeof(T)) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4*>(out + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        else
+          *reinterpret_cast<uint4*>(out + e) =
+              make_uint4(pack_bf16x2(acc[e], acc[e + 1]), pack_bf16x2(acc[e + 2], acc[e + 3]),
+                         pack_bf16x2(acc[e + 4], acc[e + 5]), pack_bf16x2(acc[e + 6], acc[e + 7]));
+      }
+    }
+    return;
+  }
   __shared__ float shared_parts[8][6][32];
-  for (int i = blockIdx.y * (8 / per_row) + warp / per_row; i < rows; i += kJoinBlocks * (8 / per_row)) {
+  for (int i = blockIdx.y; i < rows; i += kJoinBlocks) {
     const int tok = i / p.group, g = i - tok * p.group;
     const int tile = tok >= p.tile_tokens ? 1 : 0;
     const int in_tile = (tok - tile * p.tile_tokens) * p.group + g;
-    // Part k: CTA b - 1 + k, the first in its second slot, the others in their first.
-    auto slot = [&](int k) -> size_t { return (size_t)2 * (b - 1 + k) + (k == 0 ? 1 : 0); };
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const int w0 = per_row == 8 ? warp : 0;
-    for (int k0 = w0; k0 < parts; k0 += 32 * per_row) {
-      const int k = k0 + lane * per_row, here = min(32, (parts - k0 + per_row - 1) / per_row);
+    for (int k0 = warp; k0 < parts; k0 += 32 * 8) {
+      const int k = k0 + lane * 8, here = min(32, (parts - k0 + 7) / 8);
       float2 a = make_float2(-INFINITY, 0.f);
-      if (k < parts) a = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot(k) * (2 * kChunkRows) + tile * kChunkRows + in_tile);
+      if (k < parts) a = __ldcg(ml + slot(k) * (2 * kChunkRows) + tile * kChunkRows + in_tile);
       if (a.y == 0.f) a.x = -INFINITY;  // no token seen: no weight
       float top = a.x;
 #pragma unroll
@@ -267,8 +314,7 @@ __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ C
       for (int j = 0; j < 4; ++j) acc[j] *= keep;
 #pragma unroll 8
       for (int j = 0; j < here; ++j) {
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o) +
-                                ((slot(k0 + j * per_row) * 2 + tile) * (D / 4) + dims) * kChunkRows + in_tile);
+        const float4 o = __ldcg(po + ((slot(k0 + j * 8) * 2 + tile) * (D / 4) + dims) * kChunkRows + in_tile);
         const float f = __shfl_sync(0xffffffffu, wa, j);
         if (f != 0.f) {  // a part without weight may hold anything
           acc[0] = fmaf(f, o.x, acc[0]), acc[1] = fmaf(f, o.y, acc[1]);
@@ -276,26 +322,24 @@ __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ C
         }
       }
     }
-    if (per_row == 8) {  // (all warps of the block are here, with one row)
-      __syncthreads();
-      float(*mine)[32] = shared_parts[warp];
-      mine[4][lane] = m;
-      mine[5][lane] = l;
+    __syncthreads();
+    float(*mine)[32] = shared_parts[warp];
+    mine[4][lane] = m;
+    mine[5][lane] = l;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mine[j][lane] = acc[j];
-      __syncthreads();
-      if (warp != 0) continue;
-      for (int w = 1; w < 8; ++w) m = fmaxf(m, shared_parts[w][4][lane]);
-      const float ref = m == -INFINITY ? 0.f : m;
-      l = 0.f;
+    for (int j = 0; j < 4; ++j) mine[j][lane] = acc[j];
+    __syncthreads();
+    if (warp != 0) continue;
+    for (int w = 1; w < 8; ++w) m = fmaxf(m, shared_parts[w][4][lane]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    l = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = 0.f;
-      for (int w = 0; w < 8; ++w) {
-        const float f = ex2_ftz(shared_parts[w][4][lane] - ref);
-        l = fmaf(f, shared_parts[w][5][lane], l);
+    for (int j = 0; j < 4; ++j) acc[j] = 0.f;
+    for (int w = 0; w < 8; ++w) {
+      const float f = ex2_ftz(shared_parts[w][4][lane] - ref);
+      l = fmaf(f, shared_parts[w][5][lane], l);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = fmaf(f, shared_parts[w][j][lane], acc[j]);
-      }
+      for (int j = 0; j < 4; ++j) acc[j] = fmaf(f, shared_parts[w][j][lane], acc[j]);
     }
     if (lane < kLanes) {
       const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -120,15 +120,20 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
 }
 
-// mbar_wait that also gives up when another warp has.
+// mbar_wait that also gives up when another warp has.  The timer is read only once a
+// wait has come to nothing many times: reading it takes longer than most waits.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, unsigned long long limit,
                                               const volatile int* abort_flag) {
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) {
-    const uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     for (uint32_t spin = 1;; ++spin) {
       if ((ok = mbar_try_wait(bar, parity))) break;
-      if ((spin & 63u) == 0 && (*abort_flag != 0 || global_timer_ns() - t0 > limit)) break;
+      if ((spin & 63u) == 0) {
+        const uint64_t now = global_timer_ns();
+        if (spin == 64u) t0 = now;
+        if (*abort_flag != 0 || now - t0 > limit) break;
+      }
     }
   }
   return __all_sync(0xffffffffu, ok);
@@ -180,6 +185,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
       : "memory");
 }
 

@@ -13,22 +13,22 @@
 //
 // One persistent CTA per SM, equal shares of the list of (item, tile) units
 // (pa_chunk_work.h).  Per CTA:
-//   warps 0-7, 8-15 softmax groups 0 and 1: two threads per row, 64 tokens each,
-//                   which exchange their maxima; scores come from tensor memory,
-//                   weights go back there as bf16
-//   warp 16         walks the list, and loads K and V tiles: TMA boxes of gcd(block_size, 128) token
-//                   rows x 64 elements into 128-byte swizzled panels (int8: the
+//   warps 0-3, 4-7  softmax groups 0 and 1: a thread per row, 64 tokens a step; scores
+//                   come from tensor memory, weights go back there as bf16
+//   warp 8          walks the list, and loads K and V tiles: TMA boxes of gcd(block_size, 128)
+//                   token rows x 64 elements into 128-byte swizzled panels (int8: the
 //                   codes into a ring of their own, the scales beside them);
 //                   blocks that are no multiple of 8: 16-byte asynchronous copies
-//   warp 17         loads an item's queries (TMA), issues the products (tcgen05.mma, one thread)
-//   warps 18, 19    int8: widen the codes into the panels.  bf16: warp 18 zeroes what
-//                   lies behind a context's end in its last V tile (zero weights
-//                   do not cancel the NaN that may lie there)
+//   warp 9          loads an item's queries (TMA), issues the products (tcgen05.mma, one thread)
+//   warp 10         bf16: zeroes what lies behind a context's end in its last V tile (zero
+//                   weights do not cancel the NaN that may lie there)
+//   warps 12-15     int8: widen the codes into the panels
 // With two row tiles each group has one and both use every K/V tile; with a
 // single row tile the groups take alternate K/V tiles and add their results in
-// the end through tensor memory.  While one group exponentiates, the tensor
-// core works for the other.  Tensor memory: S0, S1 (128 columns each; the weights
-// overwrite the first 64, their second parts, if any, the other 64), O0, O1 (D columns).
+// the end through tensor memory.  A group has two score buffers of 64 tokens: while
+// it exponentiates one, the tensor core fills the other, so that neither waits for the
+// other's step.  Tensor memory: the buffers (2 x 64 columns a group; the weights overwrite
+// the first 32 of one, their second parts, if any, the other 32), O0, O1 (D columns).
 #include "pa_launch.cuh"
 
 #include <cmath>
@@ -42,12 +42,20 @@
 namespace pa {
 namespace {
 
-constexpr int kChunkThreads = 640;
-// Registers per thread: 96 at launch (65536 / 640, rounded down); a softmax thread
-// holds 64 scores, the fifth warpgroup issues copies and products.
-// 4 * 128 * 104 + 128 * 64 = 640 * 96.
-constexpr int kSoftmaxRegisters = 104, kIssueRegisters = 64;
-constexpr int kSoftmaxWarps = 16, kLoadWarp = 16, kProductWarp = 17, kWidenWarp = 18, kWidenWarps = 2;
+// Registers per thread at launch: 168 of 384 threads, 128 of 512 (int8); a softmax thread
+// holds 64 scores and 32 weights.  256 * 200 + 128 * 104 = 384 * 168, 256 * 176 + 256 * 80 = 512 * 128.
+template <bool I8>
+struct ChunkWarps {
+  static constexpr int kThreads = I8 ? 512 : 384;
+  static constexpr int kSoftmaxRegisters = I8 ? 176 : 200, kIssueRegisters = I8 ? 80 : 104;
+};
+// Place of 16-byte unit u of token row r in a K or V tile.
+template <int D>
+__device__ __forceinline__ uint32_t unit_at(int r, int u) {
+  return (uint32_t)((r >> 3) * (D / 64 * 1024) + (u >> 3) * 1024 + (r & 7) * 128 + (((u & 7) ^ (r & 7)) << 4));
+}
+constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kProductWarp = 9, kTailWarp = 10, kWidenWarp = 12, kWidenWarps = 4;
+constexpr int kHalf = 64;  // tokens of a softmax step
 constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
 // A running maximum is kept until a tile exceeds it by this factor (log2): until
 // then weights are at most 2^8, which bf16 and the fp32 sums hold as well as 1.
@@ -61,10 +69,10 @@ struct ChunkItem {
   int tokens;   // of the item; 0: the range has no more items
   int sees;     // tokens that the first of them sees (0 or less: none)
   int head;
-  int t0, t1;   // tiles of this CTA,
-  int end0;     // and where those of the first row tile end
+  int t0, t1;   // tiles of this CTA
+  int ends[2];  // where the steps (halves of tiles) of either group's row tile end
   int flags;
-  int ctx, pad[3];
+  int ctx, pad[2];
   __device__ __forceinline__ bool two() const { return flags & 1; }    // row tiles
   __device__ __forceinline__ bool whole() const { return flags & 2; }  // no other CTA has a tile
 };
@@ -73,11 +81,13 @@ template <int D, bool I8>
 struct ChunkLayout {
   static constexpr int kPanels = D / 64;
   static constexpr uint32_t kTileBytes = kPanels * kPanel;  // a Q, K or V tile
+  // K and V tiles: groups of 8 token rows, a group's panels of 1 KiB side by side, so that
+  // the rows of a block come as one copy.  (Q: panels of 128 rows.)
+  static constexpr uint32_t kGroup = kPanels * 1024;
   static constexpr int kStages = D == 64 ? 8 : I8 ? 3 : 5;
   static constexpr int kRawStages = I8 ? (D == 64 ? 6 : 3) : 0;  // tiles of codes
   static constexpr uint32_t kRawBytes = kTileBytes / 2;
-  static constexpr uint32_t kExchange = 1024;  // [2 groups][2 halves][128] floats; barriers before it
-  static constexpr uint32_t kQ = 3 * 1024;
+  static constexpr uint32_t kQ = 1024;  // barriers and items before it
   static constexpr uint32_t kRing = kQ + 2 * kTileBytes;
   static constexpr uint32_t kRaw = kRing + kStages * kTileBytes;
   static constexpr uint32_t kScales = kRaw + kRawStages * kRawBytes;  // [slots][K, V][128] floats
@@ -109,9 +119,9 @@ __device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x) {
 }
 
 template <int D, bool I8, bool kOdd>
-__global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel(const __grid_constant__ ChunkParams p) {
   using L = ChunkLayout<D, I8>;
-  constexpr int NS = L::kStages, NR = L::kRawStages;
+  constexpr int NS = L::kStages, NR = L::kRawStages, kChunkThreads = ChunkWarps<I8>::kThreads;
   extern __shared__ __align__(1024) unsigned char smem[];  // swizzled panels start on 1 KiB boundaries
   const uint32_t base = smem_addr(smem);
   if ((base & 1023u) != 0) {  // cannot be: the array asks for it
@@ -123,21 +133,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
   auto full = [&](int i) { return bars + 8u * i; };
   auto empty = [&](int i) { return bars + 8u * (NS + i); };
   auto tail = [&](int i) { return bars + 8u * (2 * NS + i); };  // a V tile whose end must be zeroed has landed
-  const uint32_t q_full = bars + 8u * (3 * NS);
-  auto s_full = [&](int w) { return bars + 8u * (3 * NS + 1 + w); };
-  auto p_full = [&](int w) { return bars + 8u * (3 * NS + 3 + w); };
-  auto o_full = [&](int w) { return bars + 8u * (3 * NS + 5 + w); };
-  const uint32_t drained = bars + 8u * (3 * NS + 7), joined = bars + 8u * (3 * NS + 8);
-  auto exchanged = [&](int w) { return bars + 8u * (3 * NS + 9 + w); };
-  auto sc_full = [&](int i) { return bars + 8u * (3 * NS + 11 + i); };
-  auto sc_empty = [&](int i) { return bars + 8u * (3 * NS + 11 + kScaleSlots + i); };
-  auto raw_full = [&](int i) { return bars + 8u * (3 * NS + 11 + 2 * kScaleSlots + i); };
-  auto raw_empty = [&](int i) { return bars + 8u * (3 * NS + 11 + 2 * kScaleSlots + NR + i); };
-  constexpr int kItemBars = 3 * NS + 11 + 2 * kScaleSlots + 2 * NR;
+  auto s_full = [&](int w, int b) { return bars + 8u * (3 * NS + 2 * w + b); };
+  auto p_full = [&](int w, int b) { return bars + 8u * (3 * NS + 4 + 2 * w + b); };
+  auto o_step = [&](int w) { return bars + 8u * (3 * NS + 8 + w); };  // a step's product has been added
+  const uint32_t q_full = bars + 8u * (3 * NS + 10), q_empty = bars + 8u * (3 * NS + 11);
+  const uint32_t o_full = bars + 8u * (3 * NS + 12), joined = bars + 8u * (3 * NS + 13);
+  const uint32_t drained = bars + 8u * (3 * NS + 14);
+  auto sc_full = [&](int i) { return bars + 8u * (3 * NS + 15 + i); };
+  auto sc_empty = [&](int i) { return bars + 8u * (3 * NS + 15 + kScaleSlots + i); };
+  constexpr int kItemBars = 3 * NS + 15 + 2 * kScaleSlots;
   auto item_full = [&](int i) { return bars + 8u * (kItemBars + i); };
   auto item_empty = [&](int i) { return bars + 8u * (kItemBars + kItemSlots + i); };
-  const uint32_t q_empty = bars + 8u * (kItemBars + 2 * kItemSlots);
-  static_assert(8 * (kItemBars + 2 * kItemSlots + 1) <= 560, "barriers lie before the flags");
+  auto raw_full = [&](int i) { return bars + 8u * (kItemBars + 2 * kItemSlots + i); };
+  auto raw_empty = [&](int i) { return bars + 8u * (kItemBars + 2 * kItemSlots + NR + i); };
+  static_assert(8 * (kItemBars + 2 * kItemSlots + 2 * NR) <= 560, "barriers lie before the flags");
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 560);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + 564);
   auto timed_out = [&]() {
@@ -172,13 +181,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, kSoftmaxWarps);
+    mbar_init(o_full, 1);
     mbar_init(joined, kSoftmaxWarps);
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(exchanged(w), kSoftmaxWarps / 2);
-      mbar_init(s_full(w), 1);
-      mbar_init(p_full(w), kSoftmaxWarps / 2);
-      mbar_init(o_full(w), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full(i >> 1, i & 1), 1);
+      mbar_init(p_full(i >> 1, i & 1), kSoftmaxWarps / 2);
     }
+    mbar_init(o_step(0), 1);
+    mbar_init(o_step(1), 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     mbar_init_fence();
@@ -191,10 +201,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
       return false;
     }
     const int4* from = reinterpret_cast<const int4*>(ring_items + at_item.i);
-    const int4 a = from[0], b = from[1];
+    const int4 a = from[0], b = from[1], c = from[2];
     it->row = a.x, it->tokens = a.y, it->sees = a.z, it->head = a.w;
-    it->t0 = b.x, it->t1 = b.y, it->end0 = b.z, it->flags = b.w;
-    it->ctx = ring_items[at_item.i].ctx;
+    it->t0 = b.x, it->t1 = b.y, it->ends[0] = b.z, it->ends[1] = b.w;
+    it->flags = c.x, it->ctx = c.y;
     return it->tokens > 0;
   };
   auto leave_item = [&]() {
@@ -209,34 +219,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
 
   if (warp < kSoftmaxWarps)
-    registers_up<kSoftmaxRegisters>();
+    registers_up<ChunkWarps<I8>::kSoftmaxRegisters>();
   else
-    registers_down<kIssueRegisters>();
+    registers_down<ChunkWarps<I8>::kIssueRegisters>();
 
   if (warp < kSoftmaxWarps) {
     // ---------------- softmax ----------------
-    const int w = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
+    const int w = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the TMEM lanes
-    const uint32_t s_addr = tmem + lanes + 128u * w, o_all = tmem + lanes + 256u;
-    const uint32_t o_addr = o_all + (uint32_t)D * w + (D / 2) * half;
-    float* mine = reinterpret_cast<float*>(smem + L::kExchange) + (w * 2 + half) * 128 + row;
-    const float* other = reinterpret_cast<const float*>(smem + L::kExchange) + (w * 2 + (half ^ 1)) * 128 + row;
-    uint32_t s_phase = 0, o_phase = 0, x_phase = 0, j_phase = 0;
-    uint32_t tile_count = 0;  // int8: tiles of the segments before (slot and phase of the scales)
-    // Give the row's other thread `v` and get its value.  (What it gave before has
-    // been read: either the weights of the tile in between, which the tensor core
-    // waits for, or the next queries came after that.)
-    auto exchange = [&](float v, float* got) -> bool {
-      *mine = v;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(exchanged(w));
-      if (!wait_or_abort(exchanged(w), x_phase, p.wait_limit_ns, abort_flag)) return false;
-      x_phase ^= 1u;
-      tc_fence_after();
-      *got = *other;
-      return true;
-    };
+    const uint32_t s_all = tmem + lanes, o_all = s_all + 256u, o_addr = o_all + (uint32_t)D * w;
+    uint32_t steps = 0;       // of this group so far: buffer steps & 1, its phase (steps >> 1) & 1
+    uint32_t tile_count = 0;  // int8: tiles of the items before (slot and phase of the scales)
+    uint32_t o_phase = 0, j_phase = 0;
     bool alive = true;
     const int tok_in = row / p.group;
     ChunkItem it;
@@ -247,35 +241,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
       const bool real = tok_in < p.tile_tokens && token < it.tokens;
       // Tokens that the row sees.
       const int sees = real ? max(it.sees + token, 0) : 0;
-      const int step = two ? 1 : 2, x0 = it.t0 + (two ? 0 : w), x1 = w == 0 ? it.end0 : it.t1;
+      const int tile_step = two ? 1 : 2, first = 2 * (it.t0 + (two ? 0 : w)), end = w == 0 ? it.ends[0] : it.ends[1];
       // A warp without a row of the batch only takes part in the barriers: its rows' weights
       // may be anything, they reach nothing but its rows of O, which nobody reads.
       const bool rows_here = __any_sync(0xffffffffu, real);
       // Where one row tile is all the copies set the pace, and the weights go in two parts.
       const bool fine = !two;
       float m = -INFINITY, l = 0.f;
-      for (int x = x0; x < x1; x += step) {
-        if (!(alive = wait_or_abort(s_full(w), s_phase, p.wait_limit_ns, abort_flag))) break;
-        s_phase ^= 1u;
+      for (int j = first; j < end; j += (j & 1) ? 2 * tile_step - 1 : 1, ++steps) {
+        const uint32_t buffer = steps & 1u, s_addr = s_all + 128u * w + 64u * buffer;
+        if (!(alive = wait_or_abort(s_full(w, buffer), (steps >> 1) & 1u, p.wait_limit_ns, abort_flag))) break;
         tc_fence_after();
         if (!rows_here) {
-          float none;
-          if (!(alive = exchange(0.f, &none))) break;
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(w));
+          if (lane == 0) mbar_arrive(p_full(w, buffer));
           continue;
         }
-        const uint32_t nth = tile_count + (uint32_t)(x - it.t0);
         const float* k_scale = nullptr;
         if constexpr (I8) {
+          const uint32_t nth = tile_count + (uint32_t)((j >> 1) - it.t0);
           if (!(alive = wait_or_abort(sc_full(nth % kScaleSlots), (nth / kScaleSlots) & 1u, p.wait_limit_ns, abort_flag)))
             break;
-          k_scale = reinterpret_cast<const float*>(smem + L::kScales + (nth % kScaleSlots) * 1024u) + 64 * half;
+          k_scale = reinterpret_cast<const float*>(smem + L::kScales + (nth % kScaleSlots) * 1024u) + kHalf * (j & 1);
         }
         float s[64];
-        tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[0]), s_addr + 64u * half);
-        tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[32]), s_addr + 64u * half + 32u);
+        tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[0]), s_addr);
+        tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&s[32]), s_addr + 32u);
         tmem_wait_load();
         if (p.sign != 1.f) {  // a negative scale (or zero)
 #pragma unroll
@@ -291,7 +283,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
             s[i + 3] *= k4.w;
           }
         }
-        const int nvalid = sees - x * kChunkTokens - 64 * half;
+        const int nvalid = sees - j * kHalf;
         const bool masked = nvalid < 64;
         if (masked) {  // tokens behind the row's own
 #pragma unroll
@@ -302,25 +294,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
 #pragma unroll
         for (int i = 4; i < 60; i += 8)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], s[i + j]), s[i + 4 + j]);
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[i + k]), s[i + 4 + k]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[60 + j]);
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), theirs;
-        // Behind the exchange both threads of every row have read their scores,
-        // which the weights may now overwrite.
-        if (!(alive = exchange(top, &theirs))) break;
-        top = fmaxf(top, theirs);
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[60 + k]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (m == -INFINITY) m = top;  // nothing but zero weights so far
         const bool moves = (top - m) * p.scale_log2 > kSlack;
         if (__any_sync(0xffffffffu, moves)) {
-          // The products of the group's earlier tiles are done (the scores were
-          // issued behind them), so O can be scaled here, half its columns each.
           const float f = moves ? ex2_ftz((m - top) * p.scale_log2) : 1.f;
           if (moves) m = top;
           l *= f;
-          if (x >= x0 + step) {
+          if (j != first) {  // O holds the steps before, once the last of them is added
+            if (!(alive = wait_or_abort(o_step(w), (steps - 1) & 1u, p.wait_limit_ns, abort_flag))) break;
+            tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
               tmem_load16(o, o_addr + 16u * c);
               tmem_wait_load();
@@ -358,20 +346,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
             uint32_t hi[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) hi[i] = weights(32 * c + 2 * i, i);
-            tmem_store16(s_addr + 32u * half + 16u * c, hi);
+            tmem_store16(s_addr + 16u * c, hi);
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t hi[4], lo[4];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = 8 * c + 2 * i;
+            for (int i = 0; i < 16; ++i) {
+              const int e = 32 * c + 2 * i;
               hi[i] = weights(e, i);
               lo[i] = pack_bf16x2(s[e] - bf16_lo(hi[i]), s[e + 1] - bf16_hi(hi[i]));
             }
-            tmem_store4(s_addr + 32u * half + 4u * c, hi);
-            tmem_store4(s_addr + 64u + 32u * half + 4u * c, lo);
+            tmem_store16(s_addr + 16u * c, hi);
+            tmem_store16(s_addr + 32u + 16u * c, lo);
           }
         }
         {
@@ -382,11 +370,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         tmem_wait_store();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(w));
+        if (lane == 0) mbar_arrive(p_full(w, buffer));
       }
       tile_count += (uint32_t)(it.t1 - it.t0);
-      if (alive) alive = wait_or_abort(o_full(0), o_phase, p.wait_limit_ns, abort_flag);
-      if (alive) alive = wait_or_abort(o_full(1), o_phase, p.wait_limit_ns, abort_flag);
+      if (alive) alive = wait_or_abort(o_full, o_phase, p.wait_limit_ns, abort_flag);
       o_phase ^= 1u;
       tc_fence_after();
       // Whole items end here: a row's thread puts its part into the Q tile, which nobody
@@ -407,7 +394,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
         }
       };
-      auto write_out = [&](int d0, int dims) {  // the warp's rows, dims d0 .. d0 + dims - 1 (32 or 64; 16 to 64)
+      auto write_out = [&](int d0, int dims) {  // the warp's rows, dims d0 .. d0 + dims - 1 (32 to 128)
         __syncwarp();
         const int units = dims / 8, per = 32 / units;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
@@ -421,45 +408,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         }
       };
       if (two) {
-        float theirs = 0.f;
-        if (alive) alive = exchange(l, &theirs);
         if (!alive) {
           timed_out();
           break;
         }
-        l += theirs;
         if (rows_here) {
           const float inv = 1.f / l;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 16; ++c) {
             uint32_t o[16];
             tmem_load16(o, o_addr + 16u * c);
             tmem_wait_load();
-            const int d0 = (D / 2) * half + 16 * c;
             if (whole) {
               float f[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) f[i] = l != 0.f ? __uint_as_float(o[i]) * inv : 0.f;
-              stage(d0, f);
+              stage(16 * c, f);
             } else if (real) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(part_o + (size_t)(d0 + 4 * i) * kChunkRows) =
+                *reinterpret_cast<float4*>(part_o + (size_t)(16 * c + 4 * i) * kChunkRows) =
                     make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
                                 __uint_as_float(o[4 * i + 3]));
             }
           }
           if (whole)
-            write_out((D / 2) * half, D / 2);
-          else if (real && half == 0)
+            write_out(0, D);
+          else if (real)
             *part_ml = make_float2(m * p.scale_log2, l);
         }
       } else {
-        // One row tile: the row's four threads leave (m, l) in tensor memory, where the scores
-        // were, and take a quarter of the dims each from both groups' O.
+        // One row tile: the row's two threads leave (m, l) in tensor memory, where the scores
+        // were, and take half of the dims each from both groups' O.
         if (alive && rows_here) {
           uint32_t ml[4] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u};
-          tmem_store4(s_addr + 4u * half, ml);
+          tmem_store4(s_all + 128u * w, ml);
           tmem_wait_store();
         }
         tc_fence_before();
@@ -476,20 +459,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         }
         if (rows_here) {
           uint32_t a[16], b[16];
-          tmem_load16(a, tmem + lanes);
-          tmem_load16(b, tmem + lanes + 128u);
+          tmem_load16(a, s_all);
+          tmem_load16(b, s_all + 128u);
           tmem_wait_load();
           const float m0 = __uint_as_float(a[0]), m1 = __uint_as_float(b[0]);
-          const float l0 = __uint_as_float(a[1]) + __uint_as_float(a[5]), l1 = __uint_as_float(b[1]) + __uint_as_float(b[5]);
+          const float l0 = __uint_as_float(a[1]), l1 = __uint_as_float(b[1]);
           // A group that saw nothing (l == 0) may have anything in O.
           const float top = fmaxf(l0 != 0.f ? m0 : -INFINITY, l1 != 0.f ? m1 : -INFINITY);
           const float f0 = l0 != 0.f ? ex2_ftz((m0 - top) * p.scale_log2) : 0.f;
           const float f1 = l1 != 0.f ? ex2_ftz((m1 - top) * p.scale_log2) : 0.f;
           const float sum = f0 * l0 + f1 * l1;
           const float inv = sum == 0.f ? 0.f : whole ? 1.f / sum : 1.f;
-          const int d0 = (D / 4) * (2 * w + half);
+          const int d0 = (D / 2) * w;
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
+          for (int c = 0; c < D / 32; ++c) {
             tmem_load16(a, o_all + d0 + 16u * c);
             tmem_load16(b, o_all + (uint32_t)D + d0 + 16u * c);
             tmem_wait_load();
@@ -507,8 +490,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
             }
           }
           if (whole)
-            write_out(d0, D / 4);
-          else if (real && w == 0 && half == 0)
+            write_out(d0, D / 2);
+          else if (real && w == 0)
             *part_ml = make_float2(top * p.scale_log2, sum);
         }
       }
@@ -525,14 +508,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
       prefetch_tensormap(&p.tm_v);
     }
     // Stages the copies land in: panels, or the codes of int8 pools.
-    constexpr int kCopyStages = I8 ? NR : NS, kBoxPanels = I8 ? 1 : L::kPanels;
+    constexpr int kCopyStages = I8 ? NR : NS;
     constexpr uint32_t kCopyBytes = I8 ? L::kRawBytes : L::kTileBytes, kCopyRing = I8 ? L::kRaw : L::kRing;
     auto landed = [&](int i) { return I8 ? raw_full(i) : full(i); };
     auto taken = [&](int i) { return I8 ? raw_empty(i) : empty(i); };
     const int boxes = kOdd ? 1 : kChunkTokens / p.box_rows;
-    const int box = lane / kBoxPanels, panel = lane % kBoxPanels;
+    const int box = lane;
     const bool mine = box < boxes;
-    const uint32_t dst0 = panel * kPanel + box * p.box_rows * (I8 ? (uint32_t)D : 128u);
+    const uint32_t dst0 = box * p.box_rows * (I8 ? (uint32_t)D : 2u * D);
+    // Block sizes that are powers of two take shifts instead of divisions.
+    const int bs_shift = (p.block_size & (p.block_size - 1)) == 0 ? __ffs(p.block_size) - 1 : -1;
+    auto block_index = [&](int tok) { return bs_shift >= 0 ? tok >> bs_shift : tok / p.block_size; };
     Ring ring;
     uint32_t armed = 0, armed_phase = 0;       // stages armed, with the parity of their last phase,
     uint32_t tailed = 0, tail_phase = 0;       // and those armed as a tail
@@ -565,30 +551,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         int4* to = reinterpret_cast<int4*>(ring_items + at_item.i);
         to[0] = make_int4(items.row.row0 + first, min(items.cs.n - first, 2 * p.tile_tokens), items.cs.old + first + 1,
                           items.head);
-        to[1] = make_int4(items.t0, items.t1, items.two() ? min(items.t1, items.cs.tiles_first(items.pair)) : items.t1,
-                          (items.two() ? 1 : 0) | (items.t0 == 0 && items.t1 == items.tiles ? 2 : 0));
-        ring_items[at_item.i].ctx = items.row.ctx;
+        // Steps that the rows up to a token see, one at least.
+        auto steps_for = [&](int tokens) {
+          const int keys = items.cs.old + min(items.cs.n, tokens);
+          return min(2 * items.t1, keys > kHalf ? (keys + kHalf - 1) / kHalf : 1);
+        };
+        const int end1 = steps_for(first + 2 * p.tile_tokens);
+        to[1] = make_int4(items.t0, items.t1, items.two() ? steps_for(first + p.tile_tokens) : end1, end1);
+        to[2] = make_int4((items.two() ? 1 : 0) | (items.t0 == 0 && items.t1 == items.tiles ? 2 : 0), items.row.ctx, 0, 0);
         mbar_arrive(item_full(at_item.i));
       }
       __syncwarp();
       at_item.next(kItemSlots);
       const int32_t* table = p.tables + (size_t)items.seq * p.max_blocks;
       const int ctx = items.row.ctx;
-      auto block_of = [&](int tok) -> int {  // -1: none
-        if (tok >= ctx) return -1;
-        const int phys = __ldg(table + tok / p.block_size);
-        if (p.num_physical_blocks > 0 && (phys < 0 || phys >= p.num_physical_blocks)) {
-          report(p.error_flag, PA_DEVERR_BLOCK_ID);
-          return -1;
-        }
-        return phys;
+      // The block of a token, -1: none (behind the context, or no block of the pool).
+      auto entry_of = [&](int tok) -> int { return tok < ctx ? __ldg(table + block_index(tok)) : -1; };
+      auto checked = [&](int phys, int tok) -> int {
+        if (tok >= ctx || (phys >= 0 && phys < p.num_physical_blocks)) return phys;
+        report(p.error_flag, PA_DEVERR_BLOCK_ID);
+        return -1;
       };
+      auto block_of = [&](int tok) -> int { return checked(entry_of(tok), tok); };
+      // The entry of this lane's box in tile x is read well before it is looked at.
+      auto box_entry = [&](int x) -> int { return mine && x < items.t1 ? entry_of(x * kChunkTokens + box * p.box_rows) : -1; };
       // Token row of this lane's box in tile x, -1 for none (zeros then).
-      auto box_row = [&](int x) -> int {
+      auto box_row = [&](int x, int entry) -> int {
         const int tok = x * kChunkTokens + box * p.box_rows;
         if (!mine || x >= items.t1) return -1;
-        const int phys = block_of(tok);
-        return phys < 0 ? -1 : phys * p.block_size + tok % p.block_size;
+        const int phys = checked(entry, tok);
+        return phys < 0 ? -1 : phys * p.block_size + (tok - block_index(tok) * p.block_size);
       };
       // The scales of tile x's tokens.
       auto load_scales = [&](int x, int row, uint32_t nth) -> bool {
@@ -600,7 +592,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         if constexpr (kOdd) {
           for (int i = 0; i < kChunkTokens; i += 32) {
             const int tok = x * kChunkTokens + i + lane, phys = block_of(tok);
-            const size_t at = ((size_t)max(phys, 0) * p.kv_heads + items.head) * p.block_size + tok % p.block_size;
+            const size_t at =
+                ((size_t)max(phys, 0) * p.kv_heads + items.head) * p.block_size + (tok - block_index(tok) * p.block_size);
             copy_async4(dst + 4u * (i + lane), p.k_scales + at, phys >= 0);
             copy_async4(dst + 512u + 4u * (i + lane), p.v_scales + at, phys >= 0);
           }
@@ -615,7 +608,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
           if (lane == 0) mbar_arrive_expect_tx(sc_full(slot), 2u * bytes * __popc(there));
           __syncwarp();
           if (real) {
-            const int phys = row / p.block_size;
+            const int phys = block_index(row);
             const size_t at = ((size_t)phys * p.kv_heads + items.head) * p.block_size + (row - phys * p.block_size);
             bulk_copy_g2s(dst + bytes * box, p.k_scales + at, bytes, sc_full(slot));
             bulk_copy_g2s(dst + 512u + bytes * box, p.v_scales + at, bytes, sc_full(slot));
@@ -641,13 +634,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
           const int unit = lane % kUnits;
           for (int r0 = 0; r0 < kChunkTokens; r0 += 32) {
             const int tok = x * kChunkTokens + r0 + lane, phys = block_of(tok);
-            const int place = phys < 0 ? -1 : phys * p.block_size + tok % p.block_size;
+            const int place = phys < 0 ? -1 : phys * p.block_size + (tok - block_index(tok) * p.block_size);
 #pragma unroll 4
             for (int i = 0; i < 32; i += kRowsAtOnce) {
               const int r = i + lane / kUnits, from = __shfl_sync(0xffffffffu, place, r);
               const int rr = r0 + r;
-              const uint32_t to = I8 ? (uint32_t)(rr * D + unit * 16)
-                                     : (uint32_t)((unit >> 3) * kPanel + rr * 128 + (((unit & 7) ^ (rr & 7)) << 4));
+              const uint32_t to = I8 ? (uint32_t)(rr * D + unit * 16) : unit_at<D>(rr, unit);
               copy_async16(dst + to, pool + ((size_t)max(from, 0) * p.kv_heads + items.head) * (16 * kUnits) + unit * 16,
                            from >= 0);
             }
@@ -665,10 +657,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
           const uint32_t bar = ends ? tail(ring.i) : landed(ring.i);
           if (lane == 0) mbar_arrive_expect_tx(bar, kCopyBytes);
           __syncwarp();
-          // A chunk beyond the row's last is outside the tensor: zeros, without a read.
-          if (mine)
-            tma_load_3d(dst + dst0, v ? &p.tm_v : &p.tm_k, 0, (row < 0 ? p.kv_heads : items.head) * kBoxPanels + panel,
-                        row < 0 ? 0 : row, bar);
+          // A head beyond the last is outside the tensor: zeros, without a read.
+          if (mine) {
+            const void* map = v ? &p.tm_v : &p.tm_k;
+            const int head = row < 0 ? p.kv_heads : items.head, at = row < 0 ? 0 : row;
+            if constexpr (I8)
+              tma_load_3d(dst + dst0, map, 0, head, at, bar);
+            else
+              tma_load_5d(dst + dst0, map, 0, 0, 0, at >> 3, head, bar);
+          }
           if (ends) {
             tail_phase = (tail_phase & ~(1u << ring.i)) | (((tailed >> ring.i) & 1u ? ~tail_phase & (1u << ring.i) : 0u));
             tailed |= 1u << ring.i;
@@ -687,21 +684,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         if (I8 && !load_scales(x, row, tile_count + (uint32_t)(x - t0))) return false;
         return load(false, x, row);
       };
-      int row_v = 0, row_v1 = 0, row_k = 0;
+      // Rows of this lane's box in the V tile to come and (one row tile) the one behind it; K's next.
+      int row_v = -1, row_v1 = -1, row_k = -1, entry = -1;
       if constexpr (!kOdd) {
-        row_v = box_row(t0);
-        row_v1 = box_row(t0 + 1);
+        const int e0 = box_entry(t0), e1 = box_entry(t0 + 1);
+        entry = box_entry(t0 + 2);
+        row_v = box_row(t0, e0);
+        row_v1 = box_row(t0 + 1, e1);
       }
       alive = load_k(t0, row_v);
       if (alive && ahead == 2 && t0 + 1 < t1) alive = load_k(t0 + 1, row_v1);
-      if constexpr (!kOdd) row_k = ahead == 2 ? box_row(t0 + 2) : row_v1;
       for (int x = t0; alive && x < t1; ++x) {
-        const int row_next = kOdd ? 0 : box_row(x + ahead + 1);
+        int row_next = -1;  // of tile x + 2
+        if constexpr (!kOdd) {
+          row_next = box_row(x + 2, entry);
+          entry = box_entry(x + 3);
+        }
+        row_k = ahead == 2 ? row_next : row_v1;
         alive = load(true, x, row_v);
         if (alive && x + ahead < t1) alive = load_k(x + ahead, row_k);
         row_v = row_v1;
-        row_v1 = ahead == 2 ? row_k : row_next;
-        row_k = row_next;
+        row_v1 = row_next;
       }
       tile_count += (uint32_t)(t1 - t0);
     }
@@ -726,13 +729,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
     }
   } else if (warp == kProductWarp) {
     // ---------------- products ----------------
-    constexpr uint32_t kScores = product(true, 128, 128, false), kValues = product(true, 128, D, true);
+    constexpr uint32_t kScores = product(true, 128, kHalf, false), kValues = product(true, 128, D, true);
     Ring ring;
-    uint32_t q_phase = 0, p_phase[2] = {0u, 0u}, tile_count = 0;
+    uint32_t q_phase = 0, tile_count = 0;
+    uint32_t scores_taken[2] = {0u, 0u}, values_taken[2] = {0u, 0u};  // steps of either group
     bool alive = true;
-    const uint64_t q_op = smem_operand(base + L::kQ, kPanel);
+    const uint32_t q_op = smem_operand_low(base + L::kQ, kPanel), elected = elect_one();
+    constexpr uint32_t kQHigh = smem_operand_high(1024), kTileHigh = smem_operand_high(L::kGroup);
+    constexpr uint32_t kHalfBytes = kHalf / 8 * L::kGroup;
+    // Read by every lane, the same in all of them.
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t tm = (uint32_t)uniform((int)tmem);
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-      if (wait_or_abort(bar, parity, p.wait_limit_ns, abort_flag)) return true;
+      if (wait_or_abort(bar, parity, p.wait_limit_ns, abort_flag)) {
+        tc_fence_after();
+        return true;
+      }
       timed_out();
       return false;
     };
@@ -740,9 +752,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
     ChunkItem it;
     bool first = true;
     for (; alive && take_item(&it); leave_item()) {
-      const int t0 = it.t0, t1 = it.t1;
-      const bool two = it.two();
-      const int ahead = two ? 1 : 2, end0 = it.end0;
+      const int t0 = uniform(it.t0), t1 = uniform(it.t1), end0 = uniform(it.ends[0]), end1 = uniform(it.ends[1]);
+      const bool two = uniform(it.flags) & 1;
       // The queries: (token, group head) rows of a row tile are one box.
       if (!first && !(alive = wait(q_empty, q_phase ^ 1u))) break;
       first = false;
@@ -755,97 +766,122 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
                         it.row + w * p.tile_tokens, q_full);
       }
       __syncwarp();
-      // Whether group w has tile x.
-      auto has = [&](int w, int x) { return w != 0 || x < end0; };
-      // S of group w from the K tile in stage `st`.
-      auto scores = [&](int w, int st) {
-        if (lane == 0) {
-          const uint64_t a = q_op + (two ? (w * L::kTileBytes) >> 4 : 0u);
-          const uint64_t b = smem_operand(base + L::kRing + st * L::kTileBytes, kPanel);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k >> 2) * kPanel + (k & 3) * 32u) >> 4;
-            mma_ss(tmem + 128u * w, a + off, b + off, kScores, k > 0);
-          }
-          mma_commit(s_full(w));
-        }
-        __syncwarp();
-      };
-      auto release = [&](int st) {
-        if (lane == 0) mma_commit(empty(st));
-        __syncwarp();
-      };
+      auto release = [&](int st) { mma_commit_warp(empty(st), elected); };
       if (!(alive = wait(q_full, q_phase))) break;
       q_phase ^= 1u;
-      tc_fence_after();
-      // The first K tiles.
-      for (int x = t0; x < t0 + ahead && x < t1; ++x) {
-        if (!(alive = wait(full(ring.i), ring.phase))) break;
-        tc_fence_after();
-        if (!two || has(0, x)) scores(two ? 0 : x - t0, ring.i);
-        if (two) scores(1, ring.i);
-        release(ring.i);
-        ring.next(NS);
-      }
-      for (int x = t0; alive && x < t1; ++x) {
-        const Ring v = ring;
-        ring.next(NS);
-        const Ring k = ring;
-        const bool more = x + ahead < t1;
-        if (more) ring.next(NS);
-        for (int j = 0; j < (two ? 2 : 1); ++j) {
-          const int w = two ? j : (x - t0) & 1;
-          if (j == 0 && !(alive = wait(full(v.i), v.phase))) break;
-          if (!two || has(w, x)) {
-            if (!(alive = wait(p_full(w), p_phase[w]))) break;
-            p_phase[w] ^= 1u;
-            tc_fence_after();
-            if (lane == 0) {
-              const uint64_t b = smem_operand(base + L::kRing + v.i * L::kTileBytes, kPanel);
+      // What follows is written out for both kinds of items, and once more for tiles in whose place
+      // nothing ends: one warp issues everything, and its branches take as long as the products.
+      auto item_of = [&](auto two_tag) -> bool {
+        constexpr bool kTwo = decltype(two_tag)::value;
+        constexpr int kStep = kTwo ? 1 : 2;
+        auto end = [&](int w) { return w == 0 ? end0 : end1; };
+        // The scores of half h of the K tile in stage `st`, for group w.
+        auto scores = [&](auto w_tag, int st, int h) {
+          constexpr int w = decltype(w_tag)::value;
+          const uint32_t buffer = scores_taken[w]++ & 1u;
+          const uint32_t a = q_op + (kTwo && w == 1 ? L::kTileBytes >> 4 : 0u);
+          const uint32_t b = smem_operand_low(base + L::kRing + st * L::kTileBytes + h * kHalfBytes, 1024u);
+          const uint32_t to = tm + 128u * w + 64u * buffer;
 #pragma unroll
-              for (int kk = 0; kk < kChunkTokens / 16; ++kk)
-                mma_ts(tmem + 256u + (uint32_t)D * w, tmem + 128u * w + 8u * kk, b + ((kk * 2048u) >> 4), kValues,
-                       kk > 0 || x >= t0 + (two ? 1 : 2));
-              if (!two) {  // the weights' second part
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss_warp(to, a + (((k >> 2) * kPanel + (k & 3) * 32u) >> 4), kQHigh,
+                        b + (((k >> 2) * 1024u + (k & 3) * 32u) >> 4), kTileHigh, kScores, k > 0, elected);
+          mma_commit_warp(s_full(w, buffer), elected);
+        };
+        // Adds the group's weights times half h of the V tile in stage `st`.
+        auto values = [&](auto w_tag, int st, int h, bool accumulate) -> bool {
+          constexpr int w = decltype(w_tag)::value;
+          const uint32_t n = values_taken[w]++, buffer = n & 1u;
+          if (!wait(p_full(w, buffer), (n >> 1) & 1u)) return false;
+          const uint32_t b = smem_operand_low(base + L::kRing + st * L::kTileBytes + h * kHalfBytes, 1024u);
+          const uint32_t o = tm + 256u + (uint32_t)D * w, weights = tm + 128u * w + 64u * buffer;
 #pragma unroll
-                for (int kk = 0; kk < kChunkTokens / 16; ++kk)
-                  mma_ts(tmem + 256u + (uint32_t)D * w, tmem + 128u * w + 64u + 8u * kk, b + ((kk * 2048u) >> 4), kValues,
-                         true);
-              }
+          for (int kk = 0; kk < kHalf / 16; ++kk)
+            mma_ts_warp(o, weights + 8u * kk, b + ((kk * 2 * L::kGroup) >> 4), kTileHigh, kValues, kk > 0 || accumulate,
+                        elected);
+          if constexpr (!kTwo) {  // the weights' second part
+#pragma unroll
+            for (int kk = 0; kk < kHalf / 16; ++kk)
+              mma_ts_warp(o, weights + 32u + 8u * kk, b + ((kk * 2 * L::kGroup) >> 4), kTileHigh, kValues, true, elected);
+          }
+          mma_commit_warp(o_step(w), elected);
+          return true;
+        };
+        using W0 = std::integral_constant<int, 0>;
+        using W1 = std::integral_constant<int, 1>;
+        // The first K tile of either group.
+        for (int i = 0; i < kStep && t0 + i < t1; ++i) {
+          if (!wait(full(ring.i), ring.phase)) return false;
+          for (int h = 0; h < 2; ++h) {
+            if ((kTwo || i == 0) && 2 * (t0 + i) + h < end0) scores(W0{}, ring.i, h);
+            if ((kTwo || i == 1) && 2 * (t0 + i) + h < end1) scores(W1{}, ring.i, h);
+          }
+          release(ring.i);
+          ring.next(NS);
+        }
+        // V of tile x and K of the group's next, in steps of half h and group w: with two row tiles
+        // the groups in turn, both with both tiles; with one a group's steps and then the other's.
+        Ring v, k;
+        auto step = [&](auto w_tag, auto h_tag, auto inner_tag, int x) -> bool {
+          constexpr int w = decltype(w_tag)::value, h = decltype(h_tag)::value;
+          constexpr bool kInner = decltype(inner_tag)::value;  // all of the steps that are asked for exist
+          if (!kInner && x >= t1) return true;
+          const int next = x + kStep;
+          if (h == 0 && (!kTwo || w == 0)) {
+            v = ring;
+            ring.next(NS);
+            k = ring;
+            if (kInner || next < t1) ring.next(NS);
+            if (!wait(full(v.i), v.phase)) return false;
+          }
+          if ((kInner || 2 * x + h < end(w)) && !values(w_tag, v.i, h, x > t0 + (kTwo ? 0 : w) || h > 0)) return false;
+          if (kInner || (next < t1 && 2 * next + h < end(w))) {
+            if (h == 0 && (!kInner || !kTwo || w == 0) && !wait(full(k.i), k.phase)) return false;
+            scores(w_tag, k.i, h);
+          }
+          if (h == 1 && (!kTwo || w == 1)) {
+            release(v.i);
+            if (kInner || next < t1) {
+              // (A tile that no group has a step of is waited for here, before it goes.)
+              if (!kInner && !wait(full(k.i), k.phase)) return false;
+              release(k.i);
             }
-            __syncwarp();
+            if (I8) {  // the softmax is done with the tile's scales
+              if (lane == 0) mbar_arrive(sc_empty((tile_count + (uint32_t)(x - t0)) % kScaleSlots));
+              __syncwarp();
+            }
           }
-          if (more) {
-            if (j == 0 && !(alive = wait(full(k.i), k.phase))) break;
-            tc_fence_after();
-            if (!two || has(w, x + 1)) scores(w, k.i);
-          }
+          return true;
+        };
+        auto steps = [&](auto inner, int x) -> bool {
+          if constexpr (kTwo)
+            return step(W0{}, W0{}, inner, x) && step(W1{}, W0{}, inner, x) && step(W0{}, W1{}, inner, x) &&
+                   step(W1{}, W1{}, inner, x);
+          else
+            return step(W0{}, W0{}, inner, x) && step(W0{}, W1{}, inner, x) && step(W1{}, W0{}, inner, x + 1) &&
+                   step(W1{}, W1{}, inner, x + 1);
+        };
+        const int inner_end = min(end0, end1);  // steps before it exist for both groups
+        for (int x = t0; x < t1; x += kStep) {
+          const int last = x + (kTwo ? 1 : 3);  // tile of the last scores
+          if (!(2 * last + 1 < inner_end ? steps(std::true_type{}, x) : steps(std::false_type{}, x))) return false;
         }
-        if (!alive) break;
-        release(v.i);
-        if (more) release(k.i);
-        if (I8) {  // the softmax is done with the tile's scales
-          if (lane == 0) mbar_arrive(sc_empty((tile_count + (uint32_t)(x - t0)) % kScaleSlots));
-          __syncwarp();
-        }
-      }
+        return true;
+      };
+      alive = two ? item_of(std::true_type{}) : item_of(std::false_type{});
       if (!alive) break;
       tile_count += (uint32_t)(t1 - t0);
-      if (lane == 0) {
-        mma_commit(o_full(0));
-        mma_commit(o_full(1));
-      }
-      __syncwarp();
+      mma_commit_warp(o_full, elected);
     }
     // Everything issued is done before tensor memory is freed.
-    if (lane == 0) mma_commit(drained);
+    mma_commit_warp(drained, elected);
     __syncwarp();
     (void)mbar_wait_warp(drained, 0, p.wait_limit_ns);
     named_barrier_sync(1, kChunkThreads);
     tc_fence_after();
     tmem_free(tmem, 512);
     return;
-  } else if (I8) {
+  } else if (I8 && warp >= kWidenWarp) {
     // ---------------- codes to bf16 ----------------
     // Tiles come in the order of the copies and leave in that of the products,
     // which is the same.  A thread takes 8 codes, a 16-byte unit of a panel row; units
@@ -865,7 +901,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
           break;
         }
         const unsigned char* src = smem + L::kRaw + raw.i * L::kRawBytes + 8 * t;
-        unsigned char* dst = smem + L::kRing + ring.i * L::kTileBytes + (unit >> 3) * kPanel + row0 * 128;
+        unsigned char* dst = smem + L::kRing + ring.i * L::kTileBytes;
         constexpr int kBatch = 8;  // loads of a batch go before its stores
         for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
           uint2 codes[kBatch];
@@ -879,7 +915,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
             v.y = codes_to_bf16x2(__byte_perm(codes[i].x, 0u, 0x4342));
             v.z = codes_to_bf16x2(__byte_perm(codes[i].y, 0u, 0x4140));
             v.w = codes_to_bf16x2(__byte_perm(codes[i].y, 0u, 0x4342));
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((unit & 7) ^ ((row0 + r) & 7)) << 4)) = v;
+            *reinterpret_cast<uint4*>(dst + unit_at<D>(row0 + r, unit)) = v;
           }
         }
         async_proxy_fence();
@@ -892,7 +928,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
         raw.next(NR);
       }
     }
-  } else if (!kOdd && warp == kWidenWarp) {
+  } else if (!I8 && !kOdd && warp == kTailWarp) {
     // ---------------- the end of a context ----------------
     uint32_t at = 0, phases = 0;  // loads of the segments before; parity per stage
     bool alive = true;
@@ -909,16 +945,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
       phases ^= 1u << st;
       const int r0 = ctx - x * kChunkTokens, rows = p.box_rows - r0 % p.box_rows;
       for (int i = lane; i < rows * (D / 8); i += 32) {
-        const int r = r0 + i / (D / 8), u = i % (D / 8);  // whole rows: the swizzle only moves units within one
-        *reinterpret_cast<uint4*>(smem + L::kRing + st * L::kTileBytes + (u >> 3) * kPanel + r * 128 + (u & 7) * 16) =
-            make_uint4(0u, 0u, 0u, 0u);
+        const int r = r0 + i / (D / 8), u = i % (D / 8);
+        *reinterpret_cast<uint4*>(smem + L::kRing + st * L::kTileBytes + unit_at<D>(r, u)) = make_uint4(0u, 0u, 0u, 0u);
       }
       async_proxy_fence();
       __syncwarp();
       if (lane == 0) mbar_arrive(full(st));
     }
   }
-  if (warp < kSoftmaxWarps || warp > kProductWarp) {
+  if (warp != kLoadWarp) {
     tc_fence_before();
     named_barrier_sync(1, kChunkThreads);
   }
@@ -933,25 +968,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) pa_prefill_kernel(const __gr
 int make_maps(ChunkParams* prm, uint64_t pool_rows, int head_size, bool int8, bool pools) {
   const EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return fail(PA_ERR_CUDA, "pa_prefill: the driver has no cuTensorMapEncodeTiled");
-  auto encode = [&](CUtensorMap* map, const void* at, bool bytes, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
-                    const cuuint32_t (&box)[3]) -> int {
-    const cuuint32_t estride[3] = {1, 1, 1};
+  auto encode = [&](CUtensorMap* map, const void* at, bool bytes, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                    const cuuint32_t* box) -> int {
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
     const CUresult r = in_context([&] {
-      return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(at), dims,
-                 strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(at),
+                 dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                  bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     });
     return r == CUDA_SUCCESS ? PA_OK : fail(PA_ERR_CUDA, "pa_prefill: cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
   };
-  const cuuint64_t d = head_size;
-  int rc = encode(&prm->tm_q, prm->q, false, {d, (cuuint64_t)prm->num_heads, (cuuint64_t)prm->num_tokens},
-                  {2 * d, 2 * d * prm->num_heads}, {64, (cuuint32_t)prm->group, (cuuint32_t)prm->tile_tokens});
-  const cuuint64_t row = (cuuint64_t)prm->kv_heads * head_size;
-  const cuuint64_t chunk = int8 ? head_size : 64, elt = int8 ? 1 : 2;
-  for (int i = 0; i < 2 && pools && rc == PA_OK; ++i)
-    rc = encode(i ? &prm->tm_v : &prm->tm_k, i ? prm->v_cache : prm->k_cache, int8, {chunk, row / chunk, (cuuint64_t)pool_rows},
-                {chunk * elt, row * elt}, {(cuuint32_t)chunk, 1, (cuuint32_t)prm->box_rows});
+  const cuuint64_t d = head_size, row = (cuuint64_t)prm->kv_heads * head_size;
+  const cuuint64_t q_dims[3] = {d, (cuuint64_t)prm->num_heads, (cuuint64_t)prm->num_tokens}, q_strides[2] = {2 * d, 2 * d * prm->num_heads};
+  const cuuint32_t q_box[3] = {64, (cuuint32_t)prm->group, (cuuint32_t)prm->tile_tokens};
+  int rc = encode(&prm->tm_q, prm->q, false, 3, q_dims, q_strides, q_box);
+  for (int i = 0; i < 2 && pools && rc == PA_OK; ++i) {
+    CUtensorMap* map = i ? &prm->tm_v : &prm->tm_k;
+    const void* at = i ? prm->v_cache : prm->k_cache;
+    if (int8) {
+      const cuuint64_t dims[3] = {d, (cuuint64_t)prm->kv_heads, (cuuint64_t)pool_rows}, strides[2] = {d, row};
+      const cuuint32_t box[3] = {(cuuint32_t)d, 1, (cuuint32_t)prm->box_rows};
+      rc = encode(map, at, true, 3, dims, strides, box);
+    } else {
+      // (element of a panel, row of 8, panel, group of 8 rows, head): blocks are multiples of 8 rows here.
+      const cuuint64_t dims[5] = {64, 8, d / 64, (cuuint64_t)pool_rows / 8, (cuuint64_t)prm->kv_heads};
+      const cuuint64_t strides[4] = {2 * row, 128, 16 * row, 2 * d};
+      const cuuint32_t box[5] = {64, 8, (cuuint32_t)(d / 64), (cuuint32_t)prm->box_rows / 8, 1};
+      rc = encode(map, at, false, 5, dims, strides, box);
+    }
+  }
   return rc;
 }
 
@@ -962,7 +1008,7 @@ int launch_chunks(const ChunkParams& prm, const DeviceInfo& dev, cudaStream_t st
   const auto kernel = pa_prefill_kernel<D, I8, kOdd>;
   const int rc = raise_smem_limit(reinterpret_cast<const void*>(kernel), kBytes, dev.device, &raised);
   if (rc != PA_OK) return rc;
-  cudaError_t e = launch_pdl(kernel, dim3(dev.sm_count), dim3(kChunkThreads), kBytes, stream, prm);
+  cudaError_t e = launch_pdl(kernel, dim3(dev.sm_count), dim3(ChunkWarps<I8>::kThreads), kBytes, stream, prm);
   if (e != cudaSuccess) return cuda_fail(e, "launch pa_prefill_kernel");
   if (dev.sm_count > 1)
     e = launch_pdl(pa_prefill_join<__nv_bfloat16, D>, dim3(dev.sm_count - 1, kJoinBlocks), dim3(256), 0, stream, prm);

@@ -112,6 +112,53 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
+// The same products issued by a converged warp for its one thread with `elected` set: the
+// operands, warp-uniform, then come from uniform registers.  (Issued inside a branch of that thread
+// they are moved there one by one, which takes longer than the product.)  Shared-memory
+// operands in two words: the lower has the address and the bytes from one 64-element panel
+// to the next, the upper those from one group of 8 rows to the next.
+__device__ __forceinline__ uint32_t smem_operand_low(uint32_t addr, uint32_t panel) {
+  return ((addr & 0x3ffffu) >> 4) | ((panel >> 4) << 16);
+}
+__host__ __device__ constexpr uint32_t smem_operand_high(uint32_t group) { return (group >> 4) | (1u << 14) | (2u << 29); }
+
+__device__ __forceinline__ void mma_ss_warp(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t b_high,
+                                            uint32_t what, bool accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.u32 p, %6, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(what), "r"((uint32_t)accumulate), "r"(elected)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_ts_warp(uint32_t d, uint32_t a, uint32_t b, uint32_t b_high, uint32_t what,
+                                            bool accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_high), "r"(what), "r"((uint32_t)accumulate), "r"(elected)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_warp(uint32_t bar, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(elected)
+      : "memory");
+}
+
+// One of a converged warp's threads.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r;
+}
+
 // One arrival on `bar` when everything this thread has issued to the tensor core is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
