@@ -277,10 +277,8 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(k_scale + i);
-            s[i] *= k4.x;
-            s[i + 1] *= k4.y;
-            s[i + 2] *= k4.z;
-            s[i + 3] *= k4.w;
+            unpair(mul_pair(pair(s[i], s[i + 1]), pair(k4.x, k4.y)), s[i], s[i + 1]);
+            unpair(mul_pair(pair(s[i + 2], s[i + 3]), pair(k4.z, k4.w)), s[i + 2], s[i + 3]);
           }
         }
         const int nvalid = sees - j * kHalf;
@@ -307,7 +305,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
           if (j != first) {  // O holds the steps before, once the last of them is added
             if (!(alive = wait_or_abort(o_step(w), (steps - 1) & 1u, p.wait_limit_ns, abort_flag))) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
               tmem_load16(o, o_addr + 16u * c);
@@ -321,46 +319,48 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), neg2 = pair(neg, neg);
         uint64_t sum[2] = {0ull, 0ull};
-        const float* v_scale = k_scale + 128;
         // The weights enter the product as bf16: half a step, 2^-8 at most, both
         // signs alike; the sum keeps them in fp32.  Where one row tile is all
         // (fine) their remainders follow as a second bf16 part (2^-16 together) in
         // the columns behind.  int8: V's scales go into the weights before the
         // rounding; a scale behind the row's own token, which may be NaN, does not.
-        auto weights = [&](int e, int i) -> uint32_t {  // two of them, kept in s for their remainders
-          float a, b;
-          unpair(fma_pair(pair(s[e], s[e + 1]), scale2, neg2), a, b);
-          s[e] = ex2_ftz(a);
-          s[e + 1] = ex2_ftz(b);
-          sum[i & 1] = add_pair(sum[i & 1], pair(s[e], s[e + 1]));
+        // Half of them at a time, in a loop that stays one: written out, it does not fit the
+        // instruction cache beside the other warps' code.
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t hi[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpair(fma_pair(pair(s[2 * i], s[2 * i + 1]), scale2, neg2), a, b);
+            s[2 * i] = ex2_ftz(a);
+            s[2 * i + 1] = ex2_ftz(b);
+            sum[i & 1] = add_pair(sum[i & 1], pair(s[2 * i], s[2 * i + 1]));
+          }
           if constexpr (I8) {
-            const float2 v2 = *reinterpret_cast<const float2*>(v_scale + e);
-            s[e] = masked && e >= nvalid ? 0.f : s[e] * v2.x;
-            s[e + 1] = masked && e + 1 >= nvalid ? 0.f : s[e + 1] * v2.y;
-          }
-          return pack_bf16x2(s[e], s[e + 1]);
-        };
-        if (!fine) {
+            const float* v_scale = k_scale + 128 + 32 * c;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t hi[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) hi[i] = weights(32 * c + 2 * i, i);
-            tmem_store16(s_addr + 16u * c, hi);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int e = 32 * c + 2 * i;
-              hi[i] = weights(e, i);
-              lo[i] = pack_bf16x2(s[e] - bf16_lo(hi[i]), s[e + 1] - bf16_hi(hi[i]));
+            for (int i = 0; i < 32; i += 4) {
+              const float4 v4 = *reinterpret_cast<const float4*>(v_scale + i);
+              unpair(mul_pair(pair(s[i], s[i + 1]), pair(v4.x, v4.y)), s[i], s[i + 1]);
+              unpair(mul_pair(pair(s[i + 2], s[i + 3]), pair(v4.z, v4.w)), s[i + 2], s[i + 3]);
             }
-            tmem_store16(s_addr + 16u * c, hi);
-            tmem_store16(s_addr + 32u + 16u * c, lo);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i >= nvalid) s[i] = 0.f;
+            }
           }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) hi[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
+          tmem_store16(s_addr + 16u * c, hi);
+          if (fine) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) hi[i] = pack_bf16x2(s[2 * i] - bf16_lo(hi[i]), s[2 * i + 1] - bf16_hi(hi[i]));
+            tmem_store16(s_addr + 32u + 16u * c, hi);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = s[32 + i];
         }
         {
           float a, b;
@@ -398,13 +398,15 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         __syncwarp();
         const int units = dims / 8, per = 32 / units;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-#pragma unroll 4
-        for (int r = row0 + lane / units; r < row0 + 32; r += per) {
-          const int u = d0 / 8 + lane % units, t = r / p.group, tok = row_tile * p.tile_tokens + t;
+        int r = row0 + lane / units, t = r / p.group, g = r - t * p.group;
+        const int u = d0 / 8 + lane % units;
+#pragma unroll 2
+        for (; r < row0 + 32; r += per) {
+          const int tok = row_tile * p.tile_tokens + t;
           if (t < p.tile_tokens && tok < it.tokens)
-            *reinterpret_cast<uint4*>(out + ((size_t)(it.row + tok) * p.num_heads + it.head * p.group + (r - t * p.group)) * D +
-                                      8 * u) =
+            *reinterpret_cast<uint4*>(out + ((size_t)(it.row + tok) * p.num_heads + it.head * p.group + g) * D + 8 * u) =
                 *reinterpret_cast<const uint4*>(staged + (u >> 3) * kPanel + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+          for (g += per; g >= p.group; g -= p.group) ++t;
         }
       };
       if (two) {
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         }
         if (rows_here) {
           const float inv = 1.f / l;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t o[16];
             tmem_load16(o, o_addr + 16u * c);
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
           const float sum = f0 * l0 + f1 * l1;
           const float inv = sum == 0.f ? 0.f : whole ? 1.f / sum : 1.f;
           const int d0 = (D / 2) * w;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             tmem_load16(a, o_all + d0 + 16u * c);
             tmem_load16(b, o_all + (uint32_t)D + d0 + 16u * c);
