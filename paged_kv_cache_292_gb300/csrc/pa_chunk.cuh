@@ -94,7 +94,7 @@ struct ChunkItems {
   int seq, head, pair;
   ChunkRow row;
   ChunkSeq cs;
-  int t0, t1, tiles, weight;
+  int t0, t1, tiles;
 
   __device__ __forceinline__ void load(const ChunkParams& p) {
     row = chunk_row(p, seq, false);
@@ -102,13 +102,12 @@ struct ChunkItems {
   }
   __device__ __forceinline__ void set() {
     tiles = cs.tiles(pair);
-    weight = cs.weight(pair);
-    t0 = chunk_tile_at(ua - start, weight, tiles);
-    t1 = chunk_tile_at(ub - start, weight, tiles);
+    t0 = chunk_tile_at(ua - start, tiles);
+    t1 = chunk_tile_at(ub - start, tiles);
   }
   // False behind the range's last item.
   __device__ __forceinline__ bool next(const ChunkParams& p) {
-    start += kItemUnits + (int64_t)tiles * weight;
+    start += kItemUnits + tiles;
     if (start >= ub) return false;
     if (++pair == cs.pairs()) {
       pair = 0;
@@ -123,7 +122,7 @@ struct ChunkItems {
     set();
     return true;
   }
-  __device__ __forceinline__ bool two() const { return weight == 2; }
+  __device__ __forceinline__ bool two() const { return cs.two(pair); }
 };
 
 // This CTA's range of the list and the item that it begins in, found by all of its threads

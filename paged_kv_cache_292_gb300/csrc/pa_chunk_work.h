@@ -4,13 +4,12 @@
 // A row tile holds the (token, group head) rows of `tile_tokens` = 128 / group
 // (fp32: 64 / group) new tokens of one sequence and KV head, a pair two of them.  An item is one
 // sequence, KV head and pair; it walks the tiles of 128 tokens that the pair's
-// last row sees.  A tile of an item with two row tiles costs two units, one
-// of an item with a single row tile (a chunk's last pair, where its tokens do not
-// fill it) one.  All items' units (sequence, head, pair, tile) form one list, cut
-// into equal ranges, one per CTA; a tile belongs to the range of its first unit.  Before its
-// first tile an item has a few units for what it costs besides.  So every CTA gets the same work whatever the batch.  A
-// range cuts at most two items: the one that it begins in (partial slot 0) and the one
-// that it ends in (slot 1).
+// last row sees, a unit of work each (an item whose second row tile is empty takes
+// nearly as long: its tiles wait for their copies), and has a few units more for what it
+// costs besides.  All items' units (sequence, head, pair, tile) form one list, cut
+// into equal ranges, one per CTA; a tile belongs to the range of its unit.  So
+// every CTA gets the same work whatever the batch.  A range cuts at most two items:
+// the one that it begins in (partial slot 0) and the one that it ends in (slot 1).
 #pragma once
 
 #include "pa_schedule.h"
@@ -19,8 +18,10 @@ namespace pa {
 
 constexpr int kChunkRows = 128;    // query rows per tile (M of the products)
 constexpr int kChunkTokens = 128;  // tokens per tile
-constexpr int kItemUnits = 4;      // what an item costs besides its tiles (queries in, pipeline up and down, rows out)
-constexpr int kLeastUnits = kItemUnits + 4;  // of a range, where there are as many (kItemUnits + 2 at least)
+// What an item costs besides its tiles (queries in, pipeline up and down, rows out), in tiles:
+// about 10,000 clocks to 3,000.
+constexpr int kItemUnits = 3;
+constexpr int kLeastUnits = kItemUnits + 2;  // of a range, where there are as many (kItemUnits + 1 at least)
 constexpr int kChunkRowsF32 = 64;  // query rows per tile over fp32 pools
 
 // sum over i = 0 .. n - 1 of floor((a * i + b) / 128), for a, b >= 0, n < 2^24: the
@@ -58,8 +59,8 @@ struct ChunkSeq {
   PA_HD int tiles(int pair) const { return tiles_for((pair + 1) * 2 * tile_tokens); }
   // Tiles of the pair's first row tile.
   PA_HD int tiles_first(int pair) const { return tiles_for((2 * pair + 1) * tile_tokens); }
-  PA_HD int weight(int pair) const { return n - 2 * pair * tile_tokens > tile_tokens ? 2 : 1; }
-  PA_HD int64_t item_units(int pair) const { return kItemUnits + (int64_t)tiles(pair) * weight(pair); }
+  PA_HD bool two(int pair) const { return n - 2 * pair * tile_tokens > tile_tokens; }  // row tiles
+  PA_HD int64_t item_units(int pair) const { return kItemUnits + tiles(pair); }
   // Units of the pairs before `pair` (0 .. pairs()) of one head.
   PA_HD int64_t before(int pair) const {
     const int full = smaller(pair, pairs() - 1);  // pairs that the chunk fills
@@ -69,7 +70,7 @@ struct ChunkSeq {
       int64_t ones = (int64_t)kChunkTokens - old;  // pairs of one tile come first
       ones = ones < step ? 0 : ones / step;
       if (ones > full) ones = full;
-      units = (int64_t)full * kItemUnits + 2 * (ones + floor_sum_128(full - ones, step, old + (ones + 1) * step + kChunkTokens - 1));
+      units = (int64_t)full * kItemUnits + (ones + floor_sum_128(full - ones, step, old + (ones + 1) * step + kChunkTokens - 1));
     }
     if (pair > full) units += item_units(pair - 1);
     return units;
@@ -77,11 +78,11 @@ struct ChunkSeq {
   PA_HD int64_t units() const { return n > 0 ? before(pairs()) : 0; }
 };
 
-// First tile of an item that begins at unit 0 whose first unit is at or behind `unit`
-// (the item's own units go before its first tile's).
-PA_HD int chunk_tile_at(int64_t unit, int weight, int tiles) {
+// First tile at or behind `unit` of an item that begins at unit 0 (the item's own units
+// go before its first tile's, which belongs to the item's first unit).
+PA_HD int chunk_tile_at(int64_t unit, int tiles) {
   if (unit <= 0) return 0;
-  const int64_t u = unit > kItemUnits ? unit - kItemUnits : 0, t = weight == 2 ? (u + 1) / 2 : u;
+  const int64_t t = unit - kItemUnits;
   return t < 1 ? 1 : t < tiles ? (int)t : tiles;
 }
 

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         // rounding; a scale behind the row's own token, which may be NaN, does not.
         // Half of them at a time, in a loop that stays one: written out, it does not fit the
         // instruction cache beside the other warps' code.
-#pragma unroll 1
+#pragma unroll(I8 ? 1 : 2)
         for (int c = 0; c < 2; ++c) {
           uint32_t hi[16];
 #pragma unroll
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
         int r = row0 + lane / units, t = r / p.group, g = r - t * p.group;
         const int u = d0 / 8 + lane % units;
-#pragma unroll 2
+#pragma unroll 4
         for (; r < row0 + 32; r += per) {
           const int tok = row_tile * p.tile_tokens + t;
           if (t < p.tile_tokens && tok < it.tokens)
@@ -417,21 +417,25 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         if (rows_here) {
           const float inv = 1.f / l;
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_load16(o, o_addr + 16u * c);
+          for (int c = 0; c < D; c += 64) {
+            uint32_t o[64];
+            tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&o[0]), o_addr + c);
+            tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&o[32]), o_addr + c + 32u);
             tmem_wait_load();
             if (whole) {
-              float f[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) f[i] = l != 0.f ? __uint_as_float(o[i]) * inv : 0.f;
-              stage(16 * c, f);
+              for (int d = 0; d < 64; d += 16) {
+                float f[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = l != 0.f ? __uint_as_float(o[d + i]) * inv : 0.f;
+                stage(c + d, f);
+              }
             } else if (real) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(part_o + (size_t)(16 * c + 4 * i) * kChunkRows) =
-                    make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                                __uint_as_float(o[4 * i + 3]));
+              for (int i = 0; i < 64; i += 4)
+                *reinterpret_cast<float4*>(part_o + (size_t)(c + i) * kChunkRows) =
+                    make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                __uint_as_float(o[i + 3]));
             }
           }
           if (whole)
@@ -563,6 +567,10 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         to[2] = make_int4((items.two() ? 1 : 0) | (items.t0 == 0 && items.t1 == items.tiles ? 2 : 0), items.row.ctx, 0, 0);
         mbar_arrive(item_full(at_item.i));
       }
+      // Their queries on the way to L2.
+      if (lane < 2 * L::kPanels && (items.two() || lane < L::kPanels))
+        tma_prefetch_3d(&p.tm_q, 64 * (lane % L::kPanels), items.head * p.group,
+                        items.row.row0 + (2 * items.pair + lane / L::kPanels) * p.tile_tokens);
       __syncwarp();
       at_item.next(kItemSlots);
       const int32_t* table = p.tables + (size_t)items.seq * p.max_blocks;
@@ -621,7 +629,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         return true;
       };
       auto load = [&](bool v, int x, int row) -> bool {
-        const bool withhold = p.stall_unit >= 0 && items.start + kItemUnits + (int64_t)x * items.weight == p.stall_unit;
+        const bool withhold = p.stall_unit >= 0 && items.start + kItemUnits + x == p.stall_unit;
         if constexpr (kOdd) {
           // What it waits for may wait for these.
           if (__any_sync(0xffffffffu, !mbar_try_wait(taken(ring.i), ring.phase ^ 1u))) tell_all();

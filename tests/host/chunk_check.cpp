@@ -9,7 +9,7 @@
 #include "pa_chunk_work.h"
 
 struct Item {
-  int seq, head, pair, tiles, weight;
+  int seq, head, pair, tiles;
   int64_t start;
 };
 
@@ -19,8 +19,7 @@ static int64_t slow_units(const pa::ChunkSeq& c, int pairs) {
     const int last = (j + 1) * 2 * c.tile_tokens < c.n ? (j + 1) * 2 * c.tile_tokens : c.n;
     const int keys = c.old + last;
     const int tiles = keys <= 128 ? 1 : (keys + 127) / 128;
-    const int rows = last - j * 2 * c.tile_tokens;
-    u += pa::kItemUnits + (int64_t)tiles * (rows > c.tile_tokens ? 2 : 1);
+    u += pa::kItemUnits + tiles;
   }
   return u;
 }
@@ -39,14 +38,14 @@ static int check(const std::vector<pa::ChunkSeq>& seqs, int heads, int most) {
     if (c.units() != c.before(c.pairs())) return 3;
     for (int h = 0; h < heads; ++h)
       for (int j = 0; j < c.pairs(); ++j) {
-        items.push_back({s, h, j, c.tiles(j), c.weight(j), total});
+        items.push_back({s, h, j, c.tiles(j), total});
         total += c.item_units(j);
         if (c.tiles_first(j) > c.tiles(j)) return 4;
       }
   }
   if (total == 0) return 0;
   const int ranges = pa::chunk_ranges(total, most);
-  if (ranges < 1 || ranges > most || (ranges > 1 && total / ranges < pa::kItemUnits + 2)) return 5;
+  if (ranges < 1 || ranges > most || (ranges > 1 && total / ranges < pa::kItemUnits + 1)) return 5;
   std::vector<int> first_tile(ranges, 0), first_item(ranges, -1);
   std::vector<std::vector<int>> owner(items.size());
   for (size_t i = 0; i < items.size(); ++i) owner[i].assign(items[i].tiles, -1);
@@ -55,10 +54,10 @@ static int check(const std::vector<pa::ChunkSeq>& seqs, int heads, int most) {
     int cut_begin = 0, cut_end = 0;
     for (size_t i = 0; i < items.size(); ++i) {
       const Item& it = items[i];
-      const int64_t end = it.start + pa::kItemUnits + (int64_t)it.tiles * it.weight;
+      const int64_t end = it.start + pa::kItemUnits + it.tiles;
       if (end <= a || it.start >= b) continue;
-      const int t0 = pa::chunk_tile_at(a - it.start, it.weight, it.tiles);
-      const int t1 = pa::chunk_tile_at(b - it.start, it.weight, it.tiles);
+      const int t0 = pa::chunk_tile_at(a - it.start, it.tiles);
+      const int t1 = pa::chunk_tile_at(b - it.start, it.tiles);
       if (first_item[r] < 0) {
         first_item[r] = (int)i;
         first_tile[r] = t0 < it.tiles ? t0 : 0;
