@@ -76,8 +76,19 @@ int pa_read_cache_int8(void* k_out, void* v_out, const void* k_cache, const void
  * no others.  num_physical_blocks > 0 is required.  Other arguments, scratch
  * and limits as in pa_prefill.
  *
- * pa_decode_int8 - the same with num_queries new tokens for every sequence: query
- * and out [num_seqs, num_queries, num_heads, head_size].
+ * pa_decode_int8 - one decode step over the int8 pools: num_queries new tokens for every
+ * sequence, query and out [num_seqs, num_queries, num_heads, head_size], results as
+ * of pa_prefill_int8.  As in pa_decode_fp8_mq the query is rounded to f16 (exact
+ * for |q| in [2^-14, 65504]) and so are the softmax weights times V's scales: off by
+ * at most 2^-11 of themselves or 2^-38 of the largest weight times the largest scale,
+ * whichever is more.  More than 32
+ * (query, head) columns per KV head, or head_size 64 with an odd num_kv_heads, run as
+ * chunks do (pa_prefill_int8).
+ * workspace    as in pa_decode_ex: at least pa_decode_int8_workspace_size(...) bytes,
+ *              zero-filled before its first use and left so by every call that
+ *              completes; or NULL: the library's own (shapes that run as chunks:
+ *              refused while `stream` is being captured)
+ * num_ranges   as in pa_decode_ex (shapes that run as chunks: without effect)
  */
 int pa_prefill_int8(void* out, const void* query, const void* k_cache, const void* v_cache,
                     const float* k_scales, const float* v_scales, const int32_t* block_tables,
@@ -90,7 +101,11 @@ int pa_decode_int8(void* out, const void* query, const void* k_cache, const void
                    const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
                    int num_kv_heads, int head_size, int block_size, int max_blocks_per_seq, float scale,
                    void* stream, int num_physical_blocks, void* workspace, size_t workspace_bytes,
-                   int32_t* error_flag);
+                   int num_ranges, int32_t* error_flag);
+
+/* Scratch bytes pa_decode_int8 needs on the current device (0 for invalid sizes). */
+size_t pa_decode_int8_workspace_size(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
+                                     int head_size, int num_ranges);
 
 #ifdef __cplusplus
 }

@@ -67,8 +67,8 @@ int pa_prefill(void* out, const void* query, const void* k_cache, const void* v_
                int block_size, int max_blocks_per_seq, float scale, void* stream, int dtype,
                int num_physical_blocks, void* workspace, size_t workspace_bytes, int32_t* error_flag);
 
-/* Scratch bytes pa_prefill, pa_prefill_int8 and pa_decode_int8 need on the current
- * device, whatever the batch (0 for an invalid head_size). */
+/* Scratch bytes pa_prefill and pa_prefill_int8 need on the current device, whatever
+ * the batch (0 for an invalid head_size). */
 size_t pa_prefill_workspace_size(int head_size);
 
 #ifdef __cplusplus

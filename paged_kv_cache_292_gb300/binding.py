@@ -134,7 +134,8 @@ _SIGS = {
     "pa_prefill": (_I, [_P] * 7 + [_I] * 7 + [ctypes.c_float, _P, _I, _I, _P, _SZ, _P]),
     "pa_prefill_workspace_size": (_SZ, [_I]),
     "pa_prefill_int8": (_I, [_P] * 9 + [_I] * 7 + [ctypes.c_float, _P, _I, _P, _SZ, _P]),
-    "pa_decode_int8": (_I, [_P] * 8 + [_I] * 7 + [ctypes.c_float, _P, _I, _P, _SZ, _P]),
+    "pa_decode_int8": (_I, [_P] * 8 + [_I] * 7 + [ctypes.c_float, _P, _I, _P, _SZ, _I, _P]),
+    "pa_decode_int8_workspace_size": (_SZ, [_I] * 6),
     "pa_write_cache_int8": (_I, [_P] * 7 + [_I] * 5 + [_P, _I, _P]),
     "pa_read_cache_int8": (_I, [_P] * 9 + [_I] * 7 + [_P, _I, _P]),
     "pa_version": (_I, []),
@@ -886,12 +887,18 @@ def pa_prefill_int8(out, query, k_cache, v_cache, k_scales, v_scales, block_tabl
 
 def pa_decode_int8(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, num_seqs,
                    num_queries, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale,
-                   stream=None, num_physical_blocks=0, workspace=None, workspace_bytes=0, error_flag=None):
+                   stream=None, num_physical_blocks=0, workspace=None, workspace_bytes=0, num_ranges=0,
+                   error_flag=None):
     _check(load().pa_decode_int8(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
                                  _ptr(v_scales), _ptr(block_tables), _ptr(context_lens), num_seqs, num_queries,
                                  num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, scale,
-                                 _stream(stream), num_physical_blocks, _ptr(workspace), workspace_bytes,
+                                 _stream(stream), num_physical_blocks, _ptr(workspace), workspace_bytes, num_ranges,
                                  _ptr(error_flag)))
+
+
+def pa_decode_int8_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads, head_size, num_ranges=0) -> int:
+    return int(load().pa_decode_int8_workspace_size(num_seqs, num_queries, num_heads, num_kv_heads, head_size,
+                                                    num_ranges))
 
 
 def pa_prefill_workspace_size(head_size) -> int:
@@ -1019,7 +1026,7 @@ def prefill_int8(query, k_cache, v_cache, k_scales, v_scales, block_tables, cont
 
 
 def decode_int8(query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out=None, stream=None,
-                *, workspace=None, error_flag=None):
+                *, num_ranges=0, workspace=None, error_flag=None):
     """One step over int8 pools, the same number of new tokens for every sequence (as in ``pa_decode_int8``); query and
     out [S, H, D] or [S, Q, H, D], bf16."""
     if query.dtype is not torch.bfloat16:
@@ -1032,5 +1039,5 @@ def decode_int8(query, k_cache, v_cache, k_scales, v_scales, block_tables, conte
         out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     _call_on(index, load().pa_decode_int8, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
              k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H, Hk,
-             D, bs, MB, scale, raw, NB, ws, ws_bytes, err)
+             D, bs, MB, scale, raw, NB, ws, ws_bytes, num_ranges, err)
     return out

@@ -31,7 +31,13 @@ struct ChunkCall {
   void* workspace;
   size_t workspace_bytes;
   int32_t* error_flag;
+
+  long long tokens() const { return num_queries > 0 ? (long long)num_seqs * num_queries : num_tokens; }
 };
+
+// The argument checks, and the call itself.
+int prefill_validate(const ChunkCall& c);
+int prefill_impl(const ChunkCall& c);
 
 struct ChunkParams {
   CUtensorMap tm_q;        // (element, head, token)

@@ -192,7 +192,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
                   int num_physical_blocks, void* workspace, size_t workspace_bytes, int num_ranges,
                   int32_t* error_flag, bool kv_fp8, float k_scale,
                   float v_scale, const void* k_new, const void* v_new,
-                  ScratchProvider fixed_scratch, DecodeExtras* extras) {
+                  ScratchProvider fixed_scratch, DecodeExtras* extras, const TokenScales* int8) {
   clear_error();
   if (k_new != nullptr || v_new != nullptr) {
     if (k_new == nullptr || v_new == nullptr)
@@ -215,7 +215,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   if (rc != PA_OK) return rc;
   const int elt = dtype == PA_F32 ? 4 : 2;
   Plan pl{};
-  const PlanShape shape{num_heads, num_kv_heads, head_size, num_queries, kv_fp8 ? 1 : elt, elt, block_size};
+  const PlanShape shape{num_heads, num_kv_heads, head_size, num_queries, kv_fp8 ? 1 : elt, elt, block_size, int8 != nullptr};
   rc = make_plan(shape, num_seqs, num_ranges, dev, extras != nullptr, &pl);
   if (rc != PA_OK) return rc;
   int32_t* counters = nullptr;
@@ -294,6 +294,10 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   prm.k_scale = k_scale;
   prm.k_new = k_new;
   prm.v_new = v_new;
+  if (int8 != nullptr) {
+    prm.k_scales = int8->k;
+    prm.v_scales = int8->v;
+  }
   if (extras != nullptr) {
     prm.sm_count = dev.sm_count;
     prm.cuts = reinterpret_cast<int4*>(ws + pl.ws_partials);
@@ -351,6 +355,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   if (extras != nullptr)
     return extras->walk == kWalkMod ? launch_mod(prm, pl, dev.device, st, head_size, dtype == PA_F32, kv_fp8)
                                     : launch_rest(prm, pl, dev.device, st, head_size, kv_fp8);
+  if (int8 != nullptr) return launch_int8(prm, pl, dev.device, st, head_size);
   if (dtype == PA_BF16) {
     return head_size == 64 ? launch_dtype<__nv_bfloat16, 64>(prm, pl, dev.device, st, kv_fp8)
                            : launch_dtype<__nv_bfloat16, 128>(prm, pl, dev.device, st, kv_fp8);

@@ -34,6 +34,12 @@ struct DecodeExtras {
   const float* part_o = nullptr;
 };
 
+// The scales of int8 pools, [block][KV head][row of the block].
+struct TokenScales {
+  const float* k;
+  const float* v;
+};
+
 // Scratch of a call with extras (num_ranges 0: the default; elt: bytes of a pool
 // element; any_block: not only for blocks that are multiples of 8).  0 for invalid sizes.
 size_t walk_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size, int num_ranges,
@@ -52,6 +58,11 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
                   int num_physical_blocks, void* workspace, size_t workspace_bytes, int num_ranges,
                   int32_t* error_flag, bool kv_fp8 = false, float k_scale = 1.f,
                   float v_scale = 1.f, const void* k_new = nullptr, const void* v_new = nullptr,
-                  ScratchProvider fixed_scratch = nullptr, DecodeExtras* extras = nullptr);
+                  ScratchProvider fixed_scratch = nullptr, DecodeExtras* extras = nullptr,
+                  const TokenScales* int8 = nullptr);  // int8: with kv_fp8, whose pools theirs are like
+
+// Scratch of a plain call (0 for invalid sizes).
+size_t decode_workspace_size_q(int num_seqs, int num_heads, int num_kv_heads, int head_size, int num_ranges,
+                               int num_queries);
 
 }  // namespace pa

@@ -139,6 +139,10 @@ struct DecodeParams {
   float prefix_units;
   float* rest_ml;  // [num_seqs * num_queries * num_heads][2]
   float* rest_o;   // [num_seqs * num_queries * num_heads][D]
+  // int8 pools: a scale for every token and KV head, [block][KV head][row of the block]; in a stage
+  // they lie behind K and V: [K, V][head of the group][16].
+  const float* k_scales;
+  const float* v_scales;
   unsigned long long wait_limit_ns;  // bound of every pipeline wait
   long long stall_tile;  // tests of the bounded waits: flattened tile whose copies are withheld (-1: none)
 };
@@ -1054,7 +1058,11 @@ constexpr float kF16Up = 14.f;
 // MmaConsumerMQ: column n = col0 + (lane / 4) holds (query n / G, head n % G),
 // query qi sits at position ctx - Q + qi and sees tokens up to it.
 // MOD (with MQ): modified scores, as in MmaConsumerMQ.
-template <int D, bool MQ = false, bool MOD = false>
+// I8: int8 pools, whose tokens have scales of their own.  Codes widen to f16 (exact), K's scale
+// multiplies the token's scores and V's its weights in fp32.  f16 does not hold any
+// weight times any scale, so the scales go in as fractions of `unit`, a power of two that
+// no scale so far exceeds; the accumulators count in it and follow it when it grows.
+template <int D, bool MQ = false, bool MOD = false, bool I8 = false>
 struct MmaConsumerF8 {
   static constexpr int KS = D / 16;
   uint32_t qb[KS][2];
@@ -1063,6 +1071,33 @@ struct MmaConsumerF8 {
   uint32_t lane_off = 0;  // this lane's ldmatrix row address within a half-stage (K and V alike)
   int col0 = 0;           // MQ: first (query, head) column of this warp
   ModCols mc;             // MOD
+  float unit = 0.f, per_unit = 0.f;  // I8: the unit and its reciprocal
+  const float* scales = nullptr;     // I8: this head's 16 K scales of a stage; V's are `v_scales_at` behind
+  int v_scales_at = 0;
+
+  __device__ __forceinline__ static void widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    if constexpr (I8)
+      s8x4_to_f16x2x2(codes, lo, hi);
+    else
+      e4m3x4_to_f16x2x2(codes, lo, hi);
+  }
+  // I8: a token's V scale in units (0: the token is not there).
+  __device__ __forceinline__ void take_unit(float most) {
+    if (__any_sync(0xffffffffu, most > unit)) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      // The next power of two (at most 2^127, whose reciprocal is a normal number's; scales
+      // reach 2^128 / 127).
+      const float next = __uint_as_float((__float_as_uint(most) + 0x007fffffu) & 0x7f800000u);
+      const float f = unit * (1.f / next);  // a power of two, or zero where it does not matter any more
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mt][i] *= f;
+      unit = next;
+      per_unit = 1.f / next;
+    }
+  }
 
   // Once per kernel: uh is the head's first 16-byte unit in the group's row.
   __device__ __forceinline__ void setup(uint32_t lines, int uh, int lane) {
@@ -1102,6 +1137,10 @@ struct MmaConsumerF8 {
     }
     m_a = m_b = -INFINITY;
     l_a = l_b = 0.f;
+    if constexpr (I8) {
+      unit = 0x1p-126f;  // (so that its reciprocal is finite, too)
+      per_unit = 0x1p126f;
+    }
   }
 
   // After a segment's finish (and merge) every state register is rewritten
@@ -1143,8 +1182,8 @@ struct MmaConsumerF8 {
     for (int ks = 0; ks < KS; ++ks) {
       const uint32_t top = kr[ks >> 1][2 * (ks & 1)], bot = kr[ks >> 1][2 * (ks & 1) + 1];
       uint32_t a[4];
-      e4m3x4_to_f16x2x2(top, a[0], a[2]);  // token row g: codes 0,1 | codes 2,3
-      e4m3x4_to_f16x2x2(bot, a[1], a[3]);  // token row g+8
+      widen(top, a[0], a[2]);  // token row g: codes 0,1 | codes 2,3
+      widen(bot, a[1], a[3]);  // token row g+8
       mma_f16_16816(cc[ks % NCH], a, qb[ks][0], qb[ks][1]);
     }
 #pragma unroll
@@ -1156,10 +1195,15 @@ struct MmaConsumerF8 {
     if constexpr (MOD) {
       mod_scores(*mod, mc, mo, g, s0, s1, s2, s3);
     } else {
-      s0 *= scale_log2;
-      s1 *= scale_log2;
-      s2 *= scale_log2;
-      s3 *= scale_log2;
+      float f0 = scale_log2, f1 = scale_log2;
+      if constexpr (I8) {
+        f0 *= scales[g];
+        f1 *= scales[g + 8];
+      }
+      s0 *= f0;
+      s1 *= f0;
+      s2 *= f1;
+      s3 *= f1;
       if (g >= nvalid) s0 = s1 = -INFINITY;
       if (g + 8 >= nvalid) s2 = s3 = -INFINITY;
     }
@@ -1192,7 +1236,18 @@ struct MmaConsumerF8 {
     // Weights enter the f16 MMA rounded to f16 (relative error <= 2^-11,
     // half an ulp of the 10-bit fraction; kF16Up), well inside the bf16 output's
     // own rounding; the running sum keeps them in fp32.
-    const uint32_t p_top = pack_f16x2(p0, p1), p_bot = pack_f16x2(p2, p3);
+    float w0 = p0, w1 = p1, w2 = p2, w3 = p3;
+    if constexpr (I8) {
+      const float v0 = g < nvalid ? scales[v_scales_at + g] : 0.f, v1 = g + 8 < nvalid ? scales[v_scales_at + g + 8] : 0.f;
+      take_unit(fmaxf(v0, v1));
+      const float u0 = v0 * per_unit, u1 = v1 * per_unit;
+      // (A token that a query does not see has no weight, whatever its scale.)
+      w0 = MQ && s0 == -INFINITY ? 0.f : p0 * u0;
+      w1 = MQ && s1 == -INFINITY ? 0.f : p1 * u0;
+      w2 = MQ && s2 == -INFINITY ? 0.f : p2 * u1;
+      w3 = MQ && s3 == -INFINITY ? 0.f : p3 * u1;
+    }
+    const uint32_t p_top = pack_f16x2(w0, w1), p_bot = pack_f16x2(w2, w3);
     l_a = l_a * alpha_a + p0 + p2;
     l_b = l_b * alpha_b + p1 + p3;
     const uint32_t pb0 = movmatrix_trans(p_top), pb1 = movmatrix_trans(p_bot);
@@ -1229,8 +1284,8 @@ struct MmaConsumerF8 {
       const uint32_t bot = vr[mt >> 1][2 * (mt & 1) + 1];  // tokens 2t+8, 2t+9
       // One byte permute per register: (dim 2g: tokens 2t, 2t+1 | dim 2g+1: same).
       uint32_t a[4];
-      e4m3x4_to_f16x2x2(__byte_perm(top, 0u, 0x3120), a[0], a[1]);
-      e4m3x4_to_f16x2x2(__byte_perm(bot, 0u, 0x3120), a[2], a[3]);
+      widen(__byte_perm(top, 0u, 0x3120), a[0], a[1]);
+      widen(__byte_perm(bot, 0u, 0x3120), a[2], a[3]);
       mma_f16_16816(acc[mt], a, pb0, pb1);
     }
   }
@@ -1243,7 +1298,8 @@ struct MmaConsumerF8 {
   __device__ __forceinline__ void tile2(uint32_t k_half0, uint32_t v_half0, uint32_t k_half1, uint32_t v_half1,
                                         int nvalid1, float scale_log2, int lane, int tok0 = 0, int ctx = 0,
                                         int G = 1, int Q = 1, const DecodeParams* mod = nullptr,
-                                        const ModTile& mo0 = ModTile(), const ModTile& mo1 = ModTile()) {
+                                        const ModTile& mo0 = ModTile(), const ModTile& mo1 = ModTile(),
+                                        const float* scales1 = nullptr) {
     const uint32_t ka[2] = {k_half0 + lane_off, k_half1 + lane_off};
     const uint32_t va[2] = {v_half0 + lane_off, v_half1 + lane_off};
     uint32_t kr[2][KS / 2][4];
@@ -1264,8 +1320,8 @@ struct MmaConsumerF8 {
       for (int tt = 0; tt < 2; ++tt) {
         const uint32_t top = kr[tt][ks >> 1][2 * (ks & 1)], bot = kr[tt][ks >> 1][2 * (ks & 1) + 1];
         uint32_t a[4];
-        e4m3x4_to_f16x2x2(top, a[0], a[2]);
-        e4m3x4_to_f16x2x2(bot, a[1], a[3]);
+        widen(top, a[0], a[2]);
+        widen(bot, a[1], a[3]);
         mma_f16_16816(cc[tt][ks & 1], a, qb[ks][0], qb[ks][1]);
       }
     uint32_t vr[2][KS / 2][4];
@@ -1280,7 +1336,11 @@ struct MmaConsumerF8 {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         sc[tt][i] = cc[tt][0][i] + cc[tt][1][i];
-        if constexpr (!MOD) sc[tt][i] *= scale_log2;
+        if constexpr (!MOD) {
+          float f = scale_log2;
+          if constexpr (I8) f *= (tt ? scales1 : scales)[g + 8 * (i >> 1)];
+          sc[tt][i] *= f;
+        }
       }
     if constexpr (MOD) {
       mod_scores(*mod, mc, mo0, g, sc[0][0], sc[0][1], sc[0][2], sc[0][3]);
@@ -1326,6 +1386,20 @@ struct MmaConsumerF8 {
     }
     l_a = l_a * alpha_a + ((pw[0][0] + pw[0][2]) + (pw[1][0] + pw[1][2]));
     l_b = l_b * alpha_b + ((pw[0][1] + pw[0][3]) + (pw[1][1] + pw[1][3]));
+    if constexpr (I8) {
+      float u[2][2];
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          u[tt][i] = tt == 0 || g + 8 * i < nvalid1 ? (tt ? scales1 : scales)[v_scales_at + g + 8 * i] : 0.f;
+      take_unit(fmaxf(fmaxf(u[0][0], u[0][1]), fmaxf(u[1][0], u[1][1])));
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          pw[tt][i] = MQ && sc[tt][i] == -INFINITY ? 0.f : pw[tt][i] * (u[tt][i >> 1] * per_unit);
+    }
     uint32_t pb[2][2];
 #pragma unroll
     for (int tt = 0; tt < 2; ++tt) {
@@ -1374,8 +1448,8 @@ struct MmaConsumerF8 {
         const uint32_t top = vr[tt][mt >> 1][2 * (mt & 1)];
         const uint32_t bot = vr[tt][mt >> 1][2 * (mt & 1) + 1];
         uint32_t a[4];
-        e4m3x4_to_f16x2x2(__byte_perm(top, 0u, 0x3120), a[0], a[1]);
-        e4m3x4_to_f16x2x2(__byte_perm(bot, 0u, 0x3120), a[2], a[3]);
+        widen(__byte_perm(top, 0u, 0x3120), a[0], a[1]);
+        widen(__byte_perm(bot, 0u, 0x3120), a[2], a[3]);
         mma_f16_16816(acc[mt], a, pb[tt][0], pb[tt][1]);
       }
   }
@@ -1394,12 +1468,19 @@ struct MmaConsumerF8 {
     }
     const int G = p.group, H = p.num_heads, Q = MQ ? p.num_queries : 1;
     const int g = lane >> 2;
+    const float v_scale = I8 ? 1.f : p.v_scale;
+    if constexpr (I8) {
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mt][i] *= unit;
+    }
     if constexpr (!MQ) {
       const int ha = 2 * (lane & 3), hb = ha + 1;
       const int qa = kv_head * G + ha, qb_ = kv_head * G + hb;
       if (slot < 0) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + (size_t)seq * H * D;
-        const float ia = p.v_scale / la, ib = p.v_scale / lb;
+        const float ia = v_scale / la, ib = v_scale / lb;
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
           const int dd = mt * 16 + 2 * g;
@@ -1438,7 +1519,7 @@ struct MmaConsumerF8 {
         if (!REST && slot < 0) {
           __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + ((size_t)seq * Q * H + row) * D;
           // A query with no keys (several queries, short context) gives zeros.
-          const float inv = (!MQ || l > 0.f) ? p.v_scale / l : 0.f;
+          const float inv = (!MQ || (I8 ? l != 0.f : l > 0.f)) ? v_scale / l : 0.f;
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt)
             *reinterpret_cast<uint32_t*>(out + mt * 16 + 2 * g) =
@@ -2273,7 +2354,7 @@ constexpr int max_threads() {
   const bool fits = sizeof(T) == 2 && WALK != kWalkAll && (D == 64 || QMODE < 2);
   return fits ? 512 : 32 * (kMaxGroupHeads + kProducers);
 }
-template <typename T, int D, int GMAX, int QMODE, bool KV8 = false, int WALK = kWalkAll>
+template <typename T, int D, int GMAX, int QMODE, bool KV8 = false, int WALK = kWalkAll, bool I8 = false>
 __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
     pa_decode_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -2382,7 +2463,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
   };
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full_bar(i), 1);
+      mbar_init(full_bar(i), I8 ? 33 : 1);  // int8: and the lanes' copies of scales
       mbar_init(empty_bar(i), NCW);
     }
     for (int i = 0; i < NQ; ++i) {
@@ -2598,6 +2679,37 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
           bulk_copy_g2s(dst, src, p.row_bytes, full_bar(st));
         }
       }
+      if constexpr (I8) {
+        // The scales of the tile's rows, 4 rows of a block at a time where its size allows.
+        if (!stall) {
+          const uint32_t to = stages + st * p.stage_bytes + 2 * kTile * p.lines * kLine;
+          auto copy_scales = [&](auto rows_tag) {
+            constexpr int kRows = decltype(rows_tag)::value;
+            const int runs = kTile / kRows * Hg;  // of K; then V's
+            for (int i0 = 0; i0 < 2 * runs; i0 += 32) {
+              const int i = i0 + lane, v = i >= runs, j = v ? i - runs : i;
+              const int head = j / (kTile / kRows), t0 = j % (kTile / kRows) * kRows;
+              const int blk = __shfl_sync(0xffffffffu, phys, t0);
+              if (i < 2 * runs) {
+                const bool there = t0 < nvalid && !(p.num_physical_blocks > 0 && static_cast<unsigned>(blk) >=
+                                                                                    static_cast<unsigned>(p.num_physical_blocks));
+                const float* src = (v ? p.v_scales : p.k_scales) +
+                                   ((size_t)(there ? blk : 0) * Hk + hg * Hg + head) * bs + off_of(tok0 + t0);
+                const uint32_t dst = to + 4u * ((v * Hg + head) * kTile + t0);
+                if constexpr (kRows == 4)
+                  copy_async16(dst, src, there);
+                else
+                  copy_async4(dst, src, there);
+              }
+            }
+          };
+          if ((bs & 3) == 0)
+            copy_scales(std::integral_constant<int, 4>{});
+          else
+            copy_scales(std::integral_constant<int, 1>{});
+          copies_arrive(full_bar(st));
+        }
+      }
       if (++st == NS) {
         st = 0;
         ph ^= 1u;
@@ -2625,7 +2737,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
     constexpr bool kMma = (sizeof(T) == 2);
     constexpr bool kMod = WALK == kWalkMod;
     using Mma = typename std::conditional<
-        KV8, MmaConsumerF8<D, (QMODE > 0), kMod>,
+        KV8, MmaConsumerF8<D, (QMODE > 0), kMod, I8>,
         typename std::conditional<QMODE == 0, MmaConsumer<D>, MmaConsumerMQ<D, 1, kMod>>::type>::type;
     using Columns = typename std::conditional<kRows, RowsConsumer<D, KV8, kMod>, Mma>::type;
     using Simt = typename std::conditional<kMod, Fp32ModConsumer<D, GMAX>, SimtConsumer<D, GMAX>>::type;
@@ -2696,7 +2808,15 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
       const uint32_t k_half = stages + st * p.stage_bytes;
       const uint32_t v_half = k_half + kTile * p.lines * kLine;
       const int uh = w * D * kKVBytes / 16;  // this head's first 16-byte unit in the row
-      if constexpr (kMma && QMODE < 2 && WALK == kWalkAll) {
+      auto scales_of = [&](int stage) {  // int8
+        return reinterpret_cast<const float*>(smem + (stages - smem_addr(smem)) + stage * p.stage_bytes +
+                                              2 * kTile * p.lines * kLine) + w * kTile;
+      };
+      if constexpr (I8) {
+        cons.scales = scales_of(st);
+        cons.v_scales_at = Hg * kTile;
+      }
+      if constexpr (kMma && QMODE < 2 && WALK == kWalkAll && !I8) {
         if (mt.newfirst >= 0) {
           if (!in_place(mt, x)) {
             lost();
@@ -2727,7 +2847,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
           me = meta[st2];
           const uint32_t k_half2 = stages + st2 * p.stage_bytes;
           const uint32_t v_half2 = k_half2 + kTile * p.lines * kLine;
-          if constexpr (QMODE < 2 && WALK == kWalkAll) {
+          if constexpr (QMODE < 2 && WALK == kWalkAll && !I8) {
             if (me.newfirst >= 0) {
               if (!in_place(me, x + 1)) {
                 lost();
@@ -2746,6 +2866,9 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
           else if constexpr (kMod && KV8)
             cons.tile2(k_half, v_half, k_half2, v_half2, 0, p.scale_log2, lane, mt.tok0, mt.ctx, G,
                        p.num_queries, &p, mo0, mo1);
+          else if constexpr (I8)
+            cons.tile2(k_half, v_half, k_half2, v_half2, me.nvalid, p.scale_log2, lane, mt.tok0, mt.ctx, G,
+                       p.num_queries, nullptr, ModTile(), ModTile(), scales_of(st2));
           else if constexpr (KV8 && QMODE > 0)
             cons.tile2(k_half, v_half, k_half2, v_half2, me.nvalid, p.scale_log2, lane, mt.tok0, mt.ctx, G,
                        p.num_queries);

@@ -284,6 +284,26 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t codes, uint32_t& lo, 
       : "r"(codes));
 }
 
+// Four int8 codes (byte 0 first) -> two f16x2 registers, as above.  Exact: with the sign
+// bit flipped a code is a byte b, 0x6400 | b is the f16 number 1024 + b, and the code is b - 128.
+__device__ __forceinline__ void s8x4_to_f16x2x2(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  const uint32_t b = codes ^ 0x80808080u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(b, 0x64646464u, 0x4140)), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(b, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
+// 16 (4) bytes from global to shared memory; zeros where `real` is false.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+}
+// One of the arrivals that `bar` counts, when this thread's copies so far are complete.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);

@@ -33,13 +33,13 @@ cudaError_t launch_pdl(Kernel kern, dim3 grid, dim3 block, size_t smem, cudaStre
   return cudaLaunchKernelEx(&cfg, kern, prm);
 }
 
-template <typename T, int D, int GMAX, int QMODE = 0, bool KV8 = false, int WALK = kWalkAll>
+template <typename T, int D, int GMAX, int QMODE = 0, bool KV8 = false, int WALK = kWalkAll, bool I8 = false>
 int launch_typed(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream) {
   // Devices whose shared-memory limit is already raised for this kernel
   // (setting it again is harmless, so concurrent first calls may both set it).
   constexpr int kTrackedDevices = 64;
   static std::atomic<bool> configured[kTrackedDevices];
-  auto kern = pa_decode_kernel<T, D, GMAX, QMODE, KV8, WALK>;
+  auto kern = pa_decode_kernel<T, D, GMAX, QMODE, KV8, WALK, I8>;
   if (dev < 0 || dev >= kTrackedDevices || !configured[dev].load(std::memory_order_acquire)) {
     DeviceInfo info{};
     int rc = current_device_info(&info);
@@ -80,5 +80,6 @@ uint64_t rows_of_pools(const void* k, const void* v, uint64_t row_bytes);
 int launch_mod(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool f32,
                bool kv_fp8);
 int launch_rest(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size, bool kv_fp8);
+int launch_int8(const DecodeParams& prm, const Plan& pl, int dev, cudaStream_t stream, int head_size);
 
 }  // namespace pa

@@ -21,6 +21,7 @@ struct Plan {
 // stages are swizzled tensor boxes).
 struct PlanShape {
   int num_heads, num_kv_heads, head_size, num_queries, elt, q_elt, block_size;
+  bool scaled = false;  // stages hold the tokens' scales, too (int8 pools)
 
   int group() const { return num_heads / num_kv_heads; }
   int columns() const { return group() * num_queries; }
@@ -103,6 +104,7 @@ inline bool plan_rows(const PlanShape& s, int Hg, Plan* pl) {
     pl->pitch = pl->row_bytes + kRowSkew;
   }
   pl->stage_bytes = 2u * kTile * pl->pitch;
+  if (s.scaled) pl->stage_bytes += (uint32_t)align_up(2 * kTile * sizeof(float) * Hg, 1024);  // (stages start on 1 KiB)
   return true;
 }
 

@@ -95,12 +95,6 @@ struct ChunkLayout {
   static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
 };
 
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
-}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
@@ -1027,7 +1021,7 @@ int launch_chunks(const ChunkParams& prm, const DeviceInfo& dev, cudaStream_t st
 
 }  // namespace
 
-int prefill_impl(const ChunkCall& c) {
+int prefill_validate(const ChunkCall& c) {
   const bool none = c.num_queries == 0 && c.num_tokens == 0;  // whose query and out may be null
   int rc = decode_validate(none ? c.k_cache : c.out, none ? c.k_cache : c.query, c.k_cache, c.v_cache, c.block_tables, c.context_lens, c.num_seqs, 1,
                            c.num_heads, c.num_kv_heads, c.head_size, c.block_size, c.max_blocks_per_seq, c.scale,
@@ -1037,7 +1031,7 @@ int prefill_impl(const ChunkCall& c) {
     return fail(PA_ERR_INVALID_ARG, "pa_prefill: seq_starts is null or misaligned");
   if (c.num_tokens < 0 || c.num_queries < 0)
     return fail(PA_ERR_INVALID_ARG, "pa_prefill: %d tokens, %d queries", c.num_tokens, c.num_queries);
-  const long long tokens = c.num_queries > 0 ? (long long)c.num_seqs * c.num_queries : c.num_tokens;
+  const long long tokens = c.tokens();
   if (tokens * c.num_heads > 0x7fffffffll)
     return fail(PA_ERR_UNSUPPORTED, "pa_prefill: %lld tokens of %d heads", tokens, c.num_heads);
   if (c.int8) {
@@ -1047,6 +1041,13 @@ int prefill_impl(const ChunkCall& c) {
     if (c.num_physical_blocks <= 0)
       return fail(PA_ERR_INVALID_ARG, "pa_prefill_int8: num_physical_blocks %d", c.num_physical_blocks);
   }
+  return PA_OK;
+}
+
+int prefill_impl(const ChunkCall& c) {
+  int rc = prefill_validate(c);
+  if (rc != PA_OK) return rc;
+  const long long tokens = c.tokens();
   if (tokens == 0) return PA_OK;
   DeviceInfo dev{};
   rc = current_device_info(&dev);
@@ -1154,25 +1155,6 @@ extern "C" int pa_prefill_int8(void* out, const void* query, const void* k_cache
   c.out = out, c.query = query, c.k_cache = k_cache, c.v_cache = v_cache;
   c.block_tables = block_tables, c.context_lens = context_lens, c.seq_starts = seq_starts;
   c.num_tokens = num_tokens, c.num_seqs = num_seqs, c.num_heads = num_heads, c.num_kv_heads = num_kv_heads;
-  c.head_size = head_size, c.block_size = block_size, c.max_blocks_per_seq = max_blocks_per_seq;
-  c.scale = scale, c.stream = stream, c.dtype = PA_BF16, c.num_physical_blocks = num_physical_blocks;
-  c.workspace = workspace, c.workspace_bytes = workspace_bytes, c.error_flag = error_flag;
-  return pa::prefill_impl(c);
-}
-
-extern "C" int pa_decode_int8(void* out, const void* query, const void* k_cache, const void* v_cache,
-                              const float* k_scales, const float* v_scales, const int32_t* block_tables,
-                              const int32_t* context_lens, int num_seqs, int num_queries, int num_heads,
-                              int num_kv_heads, int head_size, int block_size, int max_blocks_per_seq, float scale,
-                              void* stream, int num_physical_blocks, void* workspace, size_t workspace_bytes,
-                              int32_t* error_flag) {
-  pa::clear_error();
-  if (num_queries < 1) return pa::fail(PA_ERR_INVALID_ARG, "pa_decode_int8: num_queries %d < 1", num_queries);
-  pa::ChunkCall c{};
-  c.int8 = true, c.k_scales = k_scales, c.v_scales = v_scales;
-  c.out = out, c.query = query, c.k_cache = k_cache, c.v_cache = v_cache;
-  c.block_tables = block_tables, c.context_lens = context_lens;
-  c.num_queries = num_queries, c.num_seqs = num_seqs, c.num_heads = num_heads, c.num_kv_heads = num_kv_heads;
   c.head_size = head_size, c.block_size = block_size, c.max_blocks_per_seq = max_blocks_per_seq;
   c.scale = scale, c.stream = stream, c.dtype = PA_BF16, c.num_physical_blocks = num_physical_blocks;
   c.workspace = workspace, c.workspace_bytes = workspace_bytes, c.error_flag = error_flag;

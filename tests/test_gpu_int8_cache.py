@@ -178,7 +178,7 @@ def test_serving_steps_on_the_device():
     slots = torch.empty(S, dtype=torch.int64, device="cuda")
     lens2, count2, starts2 = torch.empty_like(lens), torch.empty_like(count), torch.empty_like(starts)
     out = torch.empty_like(q)
-    space = torch.empty(binding.pa_prefill_workspace_size(D), dtype=torch.uint8, device="cuda")
+    space = torch.zeros(binding.pa_decode_int8_workspace_size(S, 1, H, Hk, D), dtype=torch.uint8, device="cuda")
 
     def step(a, b):
         binding.tables_step(tables, a[0], ones, free, a[1], bs, slots, context_lens_out=b[0], free_count_out=b[1],

@@ -42,7 +42,8 @@ def _prefill_int8(**kw):
 def _decode_int8(**kw):
     a = dict(out=16, query=16, k_cache=16, v_cache=16, k_scales=16, v_scales=16, block_tables=16, context_lens=16,
              num_seqs=1, num_queries=1, num_heads=8, num_kv_heads=8, head_size=128, block_size=16, max_blocks_per_seq=4,
-             scale=0.1, stream=0, num_physical_blocks=8, workspace=None, workspace_bytes=0, error_flag=None)
+             scale=0.1, stream=0, num_physical_blocks=8, workspace=None, workspace_bytes=0,
+             num_ranges=0, error_flag=None)
     a.update(kw)
     return list(a.values())
 
@@ -80,7 +81,8 @@ def test_prefill_int8_rejects(lib, kw, code):
     assert lib.pa_last_error().decode()
 
 
-@pytest.mark.parametrize("kw, code", SHARED + SCALED + [(dict(num_queries=0), INVALID), (dict(num_queries=1 << 29), UNSUPPORTED)])
+@pytest.mark.parametrize("kw, code", SHARED + SCALED + [(dict(num_queries=0), INVALID), (dict(num_queries=1 << 29), UNSUPPORTED),
+                                                         (dict(num_ranges=-1), INVALID), (dict(num_ranges=5000), UNSUPPORTED)])
 def test_decode_int8_rejects(lib, kw, code):
     assert lib.pa_decode_int8(*_decode_int8(**kw)) == code
     assert lib.pa_last_error().decode()
@@ -142,6 +144,8 @@ def test_calls_without_a_token_do_nothing(lib):
 
 def test_workspace_size_of_an_invalid_head_size_is_zero(lib):
     assert binding.pa_prefill_workspace_size(96) == 0
+    for bad in ((0, 1, 8, 8, 128), (1, 0, 8, 8, 128), (1, 1, 9, 8, 128), (1, 1, 8, 0, 128), (1, 1, 8, 8, 96), (1, 1, 8, 8, 128, -1)):
+        assert binding.pa_decode_int8_workspace_size(*bad) == 0
 
 
 def test_python_layer_wants_cuda_tensors():
