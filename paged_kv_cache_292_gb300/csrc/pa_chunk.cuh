@@ -57,7 +57,7 @@ struct ChunkParams {
   // [CTAs][2]: the item in which a CTA's range begins, (sequence, head, pair, first tile), and its
   // (first row of the token buffer, tokens, 0, 0).
   int4* cuts;
-  int num_tokens, num_seqs, num_queries, num_heads, kv_heads, group, tile_tokens;
+  int num_tokens, num_seqs, num_queries, num_heads, kv_heads, group, tile_tokens, item_units;
   int block_size, max_blocks, max_tokens, num_physical_blocks, box_rows;
   // Scores are scale_log2 * sign * <q, k> with scale_log2 > 0, so that the largest product
   // (times sign) is the largest score; fp32: scale_log2 has the sign.
@@ -104,16 +104,16 @@ struct ChunkItems {
 
   __device__ __forceinline__ void load(const ChunkParams& p) {
     row = chunk_row(p, seq, false);
-    cs = ChunkSeq{row.n, row.ctx - row.n, p.tile_tokens};
+    cs = ChunkSeq{row.n, row.ctx - row.n, p.tile_tokens, p.item_units};
   }
   __device__ __forceinline__ void set() {
     tiles = cs.tiles(pair);
-    t0 = chunk_tile_at(ua - start, tiles);
-    t1 = chunk_tile_at(ub - start, tiles);
+    t0 = chunk_tile_at(ua - start, tiles, cs.item);
+    t1 = chunk_tile_at(ub - start, tiles, cs.item);
   }
   // False behind the range's last item.
   __device__ __forceinline__ bool next(const ChunkParams& p) {
-    start += kItemUnits + tiles;
+    start += cs.item + tiles;
     if (start >= ub) return false;
     if (++pair == cs.pairs()) {
       pair = 0;
@@ -132,66 +132,80 @@ struct ChunkItems {
 };
 
 // This CTA's range of the list and the item that it begins in, found by all of its threads
-// (`shared`: kThreads / 32 + 4 long long).  False: no range for it.
+// (`shared`: kThreads / 32 + 8 long long).  False: no range for it.
 template <int kThreads>
 __device__ __forceinline__ bool chunk_begin(const ChunkParams& p, ChunkItems* at, long long* shared) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
-  long long *sums = shared, *found = shared + kWarps;  // sequence, its first unit; pair, its first unit
-  auto units_of = [&](int s, bool report_it) -> int64_t {
-    if (s >= p.num_seqs) return 0;
-    const ChunkRow r = chunk_row(p, s, report_it);
-    return ChunkSeq{r.n, r.ctx - r.n, p.tile_tokens}.units() * p.kv_heads;
-  };
-  auto block_sum = [&](long long v) -> int64_t {  // of all warps' values; `sums` keeps theirs
-    v = warp_sum_ll(v);
+  // The sequence, its first unit and its units per head; (first row, tokens, context); pair, its first unit.
+  long long* found = shared + kWarps;
+  int* found_row = reinterpret_cast<int*>(found + 5);
+  const bool one_each = p.num_seqs <= kThreads;  // a thread has one sequence at most
+  ChunkRow row{0, 0, 0};
+  int64_t units = 0, before = 0;  // of the thread's sequence, per head; of the sequences before it
+  // The units of sequences base .. base + kThreads - 1, and each thread's place among them.
+  auto scan = [&](int base, bool report_it) -> int64_t {
+    units = 0;
+    if (base + tid < p.num_seqs) {
+      row = chunk_row(p, base + tid, report_it);
+      units = ChunkSeq{row.n, row.ctx - row.n, p.tile_tokens, p.item_units}.units();
+    }
+    const int64_t mine = units * p.kv_heads, incl = warp_incl_scan_ll(mine, lane);
     __syncthreads();
-    if (lane == 0) sums[warp] = v;
+    if (lane == 31) shared[warp] = incl;
     __syncthreads();
     int64_t all = 0;
-    for (int i = 0; i < kWarps; ++i) all += sums[i];
+    before = incl - mine;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const int64_t w = shared[i];
+      if (i < warp) before += w;
+      all += w;
+    }
     return all;
   };
-  if (tid < 4) found[tid] = -1;
-  int64_t total = 0, units = 0;  // `units`: of this thread's sequence, where each has one at most
-  for (int b = 0; b < p.num_seqs; b += kThreads) total += block_sum(units = units_of(b + tid, cta == 0));
-  const int ranges = chunk_ranges(total, gridDim.x);
+  if (tid < 5) found[tid] = -1;
+  int64_t total = 0;
+  for (int b = 0; b < p.num_seqs; b += kThreads) total += scan(b, cta == 0);
+  const int ranges = chunk_ranges(total, gridDim.x, p.item_units);
   bool here = total > 0 && cta < ranges;
   if (here) {
     at->ua = range_start(cta, total, ranges);
     at->ub = range_start(cta + 1, total, ranges);
-    int64_t before = 0;
+    int64_t earlier = 0;
     for (int b = 0; b < p.num_seqs; b += kThreads) {
-      const int64_t mine = p.num_seqs <= kThreads ? units : units_of(b + tid, false);
-      const int64_t incl = warp_incl_scan_ll(mine, lane);
-      const int64_t all = block_sum(mine);
-      int64_t excl = before + incl - mine;
-      for (int i = 0; i < warp; ++i) excl += sums[i];
-      if (mine > 0 && excl <= at->ua && at->ua < excl + mine) {
+      const int64_t all = one_each ? total : scan(b, false);
+      const int64_t first = earlier + before;
+      if (units > 0 && first <= at->ua && at->ua < first + units * p.kv_heads) {
         found[0] = b + tid;
-        found[1] = excl;
+        found[1] = first;
+        found[2] = units;
+        found_row[0] = row.row0;
+        found_row[1] = row.n;
+        found_row[2] = row.ctx;
       }
-      before += all;
+      earlier += all;
     }
     __syncthreads();
     at->seq = (int)found[0];
     here = at->seq >= 0;
   }
   if (here) {
-    at->load(p);
-    const int64_t per_head = at->cs.units(), in_seq = at->ua - found[1];
-    at->head = (int)(in_seq / per_head);
+    at->row = ChunkRow{found_row[0], found_row[1], found_row[2]};
+    at->cs = ChunkSeq{at->row.n, at->row.ctx - at->row.n, p.tile_tokens, p.item_units};
+    const int64_t per_head = found[2], in_seq = at->ua - found[1];
+    at->head = ((in_seq | per_head) >> 32) == 0 ? (int)((uint32_t)in_seq / (uint32_t)per_head) : (int)(in_seq / per_head);
     const int64_t in_head = in_seq - at->head * per_head;
     for (int j = tid; j < at->cs.pairs(); j += kThreads) {
       const int64_t a = at->cs.before(j);
       if (a <= in_head && in_head < a + at->cs.item_units(j)) {
-        found[2] = j;
-        found[3] = a;
+        found[3] = j;
+        found[4] = a;
       }
     }
     __syncthreads();
-    at->pair = (int)found[2];
-    at->start = at->ua - in_head + found[3];
+    at->pair = (int)found[3];
+    at->start = at->ua - in_head + found[4];
     at->set();
     here = at->pair >= 0;
   }

@@ -19,9 +19,8 @@ namespace pa {
 constexpr int kChunkRows = 128;    // query rows per tile (M of the products)
 constexpr int kChunkTokens = 128;  // tokens per tile
 // What an item costs besides its tiles (queries in, pipeline up and down, rows out), in tiles:
-// about 10,000 clocks to 3,000.
-constexpr int kItemUnits = 3;
-constexpr int kLeastUnits = kItemUnits + 2;  // of a range, where there are as many (kItemUnits + 1 at least)
+// about 10,000 clocks to 3,000; fp32: a few to 16,000.
+constexpr int kItemUnits = 3, kItemUnitsF32 = 1;
 constexpr int kChunkRowsF32 = 64;  // query rows per tile over fp32 pools
 
 // sum over i = 0 .. n - 1 of floor((a * i + b) / 128), for a, b >= 0, n < 2^24: the
@@ -48,6 +47,7 @@ PA_HD int64_t floor_sum_128(int64_t n, int64_t a, int64_t b) {
 // of the n have no position and see nothing).
 struct ChunkSeq {
   int n, old, tile_tokens;
+  int item;  // units of an item besides its tiles (kItemUnits)
 
   PA_HD static int smaller(int a, int b) { return a < b ? a : b; }
   PA_HD int pairs() const { return (n + 2 * tile_tokens - 1) / (2 * tile_tokens); }
@@ -60,7 +60,7 @@ struct ChunkSeq {
   // Tiles of the pair's first row tile.
   PA_HD int tiles_first(int pair) const { return tiles_for((2 * pair + 1) * tile_tokens); }
   PA_HD bool two(int pair) const { return n - 2 * pair * tile_tokens > tile_tokens; }  // row tiles
-  PA_HD int64_t item_units(int pair) const { return kItemUnits + tiles(pair); }
+  PA_HD int64_t item_units(int pair) const { return item + tiles(pair); }
   // Units of the pairs before `pair` (0 .. pairs()) of one head.
   PA_HD int64_t before(int pair) const {
     const int full = smaller(pair, pairs() - 1);  // pairs that the chunk fills
@@ -70,7 +70,7 @@ struct ChunkSeq {
       int64_t ones = (int64_t)kChunkTokens - old;  // pairs of one tile come first
       ones = ones < step ? 0 : ones / step;
       if (ones > full) ones = full;
-      units = (int64_t)full * kItemUnits + (ones + floor_sum_128(full - ones, step, old + (ones + 1) * step + kChunkTokens - 1));
+      units = (int64_t)full * item + (ones + floor_sum_128(full - ones, step, old + (ones + 1) * step + kChunkTokens - 1));
     }
     if (pair > full) units += item_units(pair - 1);
     return units;
@@ -80,15 +80,15 @@ struct ChunkSeq {
 
 // First tile at or behind `unit` of an item that begins at unit 0 (the item's own units
 // go before its first tile's, which belongs to the item's first unit).
-PA_HD int chunk_tile_at(int64_t unit, int tiles) {
+PA_HD int chunk_tile_at(int64_t unit, int tiles, int item) {
   if (unit <= 0) return 0;
-  const int64_t t = unit - kItemUnits;
+  const int64_t t = unit - item;
   return t < 1 ? 1 : t < tiles ? (int)t : tiles;
 }
 
 // Ranges for a list of `total` units: so long that each holds a tile's first unit.
-PA_HD int chunk_ranges(int64_t total, int most) {
-  const int64_t r = total / kLeastUnits;
+PA_HD int chunk_ranges(int64_t total, int most, int item) {
+  const int64_t r = total / (item + (item > 1 ? 2 : 1));
   return r < 1 ? 1 : r < most ? (int)r : most;
 }
 

@@ -149,12 +149,6 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
       *abort_flag = 1;
     }
   };
-  griddep_wait();
-  griddep_launch_dependents();
-
-  ChunkItem* ring_items = reinterpret_cast<ChunkItem*>(smem + 576);  // 48 bytes each
-  ChunkItems items;
-  if (!chunk_begin<kChunkThreads>(p, &items, reinterpret_cast<long long*>(smem + 768))) return;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full(i), I8 ? kWidenWarps : 1);
@@ -187,6 +181,12 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
     *abort_flag = 0;
     mbar_init_fence();
   }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  ChunkItem* ring_items = reinterpret_cast<ChunkItem*>(smem + 576);  // 48 bytes each
+  ChunkItems items;
+  if (!chunk_begin<kChunkThreads>(p, &items, reinterpret_cast<long long*>(smem + 768))) return;
   // The next item of the ring, and the release of it (by every warp that takes them).
   Ring at_item;
   auto take_item = [&](ChunkItem* it) -> bool {  // false: no more, or a wait ran out
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         return true;
       };
       auto load = [&](bool v, int x, int row) -> bool {
-        const bool withhold = p.stall_unit >= 0 && items.start + kItemUnits + x == p.stall_unit;
+        const bool withhold = p.stall_unit >= 0 && items.start + items.cs.item + x == p.stall_unit;
         if constexpr (kOdd) {
           // What it waits for may wait for these.
           if (__any_sync(0xffffffffu, !mbar_try_wait(taken(ring.i), ring.phase ^ 1u))) tell_all();
@@ -906,7 +906,10 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         }
         const unsigned char* src = smem + L::kRaw + raw.i * L::kRawBytes + 8 * t;
         unsigned char* dst = smem + L::kRing + ring.i * L::kTileBytes;
-        constexpr int kBatch = 8;  // loads of a batch go before its stores
+        // Loads of a batch go before its stores.  (Larger batches do not fit the instruction cache
+        // beside the other warps' code: 4 chunks of int8 prompts 212 us, with 8 a batch 227, with 16 268.)
+        constexpr int kBatch = 4;
+#pragma unroll 1
         for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
           uint2 codes[kBatch];
 #pragma unroll
@@ -1096,6 +1099,7 @@ int prefill_impl(const ChunkCall& c) {
   prm.num_heads = c.num_heads;
   prm.group = c.num_heads / c.num_kv_heads;
   prm.tile_tokens = (f32 ? kChunkRowsF32 : kChunkRows) / prm.group;
+  prm.item_units = f32 ? kItemUnitsF32 : kItemUnits;
   prm.block_size = c.block_size;
   prm.max_blocks = c.max_blocks_per_seq;
   prm.max_tokens = c.max_blocks_per_seq * c.block_size;

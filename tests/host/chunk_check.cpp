@@ -19,12 +19,13 @@ static int64_t slow_units(const pa::ChunkSeq& c, int pairs) {
     const int last = (j + 1) * 2 * c.tile_tokens < c.n ? (j + 1) * 2 * c.tile_tokens : c.n;
     const int keys = c.old + last;
     const int tiles = keys <= 128 ? 1 : (keys + 127) / 128;
-    u += pa::kItemUnits + tiles;
+    u += c.item + tiles;
   }
   return u;
 }
 
 static int check(const std::vector<pa::ChunkSeq>& seqs, int heads, int most) {
+  const int item_units = seqs[0].item;
   std::vector<Item> items;
   int64_t total = 0;
   for (int s = 0; s < (int)seqs.size(); ++s) {
@@ -44,8 +45,8 @@ static int check(const std::vector<pa::ChunkSeq>& seqs, int heads, int most) {
       }
   }
   if (total == 0) return 0;
-  const int ranges = pa::chunk_ranges(total, most);
-  if (ranges < 1 || ranges > most || (ranges > 1 && total / ranges < pa::kItemUnits + 1)) return 5;
+  const int ranges = pa::chunk_ranges(total, most, item_units);
+  if (ranges < 1 || ranges > most || (ranges > 1 && total / ranges < item_units + 1)) return 5;
   std::vector<int> first_tile(ranges, 0), first_item(ranges, -1);
   std::vector<std::vector<int>> owner(items.size());
   for (size_t i = 0; i < items.size(); ++i) owner[i].assign(items[i].tiles, -1);
@@ -54,10 +55,10 @@ static int check(const std::vector<pa::ChunkSeq>& seqs, int heads, int most) {
     int cut_begin = 0, cut_end = 0;
     for (size_t i = 0; i < items.size(); ++i) {
       const Item& it = items[i];
-      const int64_t end = it.start + pa::kItemUnits + it.tiles;
+      const int64_t end = it.start + item_units + it.tiles;
       if (end <= a || it.start >= b) continue;
-      const int t0 = pa::chunk_tile_at(a - it.start, it.tiles);
-      const int t1 = pa::chunk_tile_at(b - it.start, it.tiles);
+      const int t0 = pa::chunk_tile_at(a - it.start, it.tiles, item_units);
+      const int t1 = pa::chunk_tile_at(b - it.start, it.tiles, item_units);
       if (first_item[r] < 0) {
         first_item[r] = (int)i;
         first_tile[r] = t0 < it.tiles ? t0 : 0;
@@ -105,6 +106,7 @@ int main() {
       const int context = rng() % 5 ? c.n + upto(0, ctx) : upto(0, c.n);
       c.old = context - c.n;
       c.tile_tokens = rows / group;
+      c.item = rows == 64 ? pa::kItemUnitsF32 : pa::kItemUnits;
     }
     const int rc = check(seqs, heads, rng() % 2 ? 152 : upto(1, 400));
     if (rc) {
@@ -113,7 +115,7 @@ int main() {
     }
   }
   // Long lists.
-  pa::ChunkSeq c{1 << 20, 1 << 20, 16};
+  pa::ChunkSeq c{1 << 20, 1 << 20, 16, pa::kItemUnits};
   if (c.units() != slow_units(c, c.pairs())) return 1;
   printf("ok\n");
   return 0;
