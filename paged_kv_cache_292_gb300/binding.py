@@ -925,10 +925,17 @@ def pa_read_cache_int8(k_out, v_out, k_cache, v_cache, k_scales, v_scales, block
 
 def _int8_pools(index, k_cache, v_cache, k_scales, v_scales):
     """(NB, bs, Hk, D) of int8 pools with their scales."""
-    _on(index, torch.int8, "k_cache and v_cache", k_cache, v_cache)
-    _on(index, torch.float32, "k_scales and v_scales", k_scales, v_scales)
-    NB, bs, Hk, D = k_cache.shape
-    if v_cache.shape != k_cache.shape or k_scales.shape != (NB, Hk, bs) or v_scales.shape != (NB, Hk, bs):
+    if not (k_cache.dtype is torch.int8 and v_cache.dtype is torch.int8 and k_scales.dtype is torch.float32
+            and v_scales.dtype is torch.float32):
+        raise ValueError("k_cache and v_cache must be torch.int8, k_scales and v_scales torch.float32")
+    if not (k_cache.get_device() == v_cache.get_device() == k_scales.get_device() == v_scales.get_device() == index
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scales.is_contiguous()
+            and v_scales.is_contiguous()):
+        raise ValueError("tensors must be contiguous CUDA tensors on one device")
+    pool = k_cache.shape
+    NB, bs, Hk, D = pool
+    scales = k_scales.shape
+    if v_cache.shape != pool or v_scales.shape != scales or scales != (NB, Hk, bs):
         raise ValueError("shapes of the pools and their scales (blocks, KV heads, block size) do not go together")
     return NB, bs, Hk, D
 
@@ -939,13 +946,18 @@ def write_cache_int8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_s
     every token and KV head in k_scales/v_scales[NB, Hk, bs] (as in ``pa_write_cache_int8``)."""
     index = _device_of(k_new)
     NB, bs, Hk, D = _int8_pools(index, k_cache, v_cache, k_scales, v_scales)
-    code = dtype_code(k_new.dtype)
-    _on(index, k_new.dtype, "k_new and v_new", k_new, v_new)
-    _on(index, torch.int64, "slot_mapping", slot_mapping)
-    _on(index, torch.int32, "error_flag", error_flag)
-    T = slot_mapping.numel()
-    if k_new.shape != (T, Hk, D) or v_new.shape != (T, Hk, D):
+    dtype = k_new.dtype
+    code = dtype_code(dtype)
+    if v_new.dtype is not dtype or slot_mapping.dtype is not torch.int64:
+        raise ValueError("k_new and v_new must have one type, slot_mapping must be torch.int64")
+    if not (v_new.get_device() == slot_mapping.get_device() == index and k_new.is_contiguous()
+            and v_new.is_contiguous() and slot_mapping.is_contiguous()):
+        raise ValueError("tensors must be contiguous CUDA tensors on one device")
+    shape, T = k_new.shape, slot_mapping.numel()
+    if shape != (T, Hk, D) or v_new.shape != shape:
         raise ValueError("k_new and v_new must have a row [Hk, D] for every slot")
+    if error_flag is not None:
+        _on(index, torch.int32, "error_flag", error_flag)
     _call_on(index, load().pa_write_cache_int8, k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(),
              k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), T, Hk, D, bs, NB,
              _stream_on(stream, index), code, None if error_flag is None else error_flag.data_ptr())
@@ -957,19 +969,33 @@ def read_cache_int8(k_cache, v_cache, k_scales, v_scales, block_tables, seq_star
     as in ``pa_read_cache_int8``).  Returns (k_out, v_out)."""
     index = _device_of(k_cache)
     NB, bs, Hk, D = _int8_pools(index, k_cache, v_cache, k_scales, v_scales)
-    code = dtype_code(k_out.dtype)
-    _on(index, k_out.dtype, "k_out and v_out", k_out, v_out)
-    _on(index, torch.int32, "tables, lengths and starts", block_tables, seq_starts, first_tokens, error_flag)
+    dtype = k_out.dtype
+    code = dtype_code(dtype)
+    if v_out.dtype is not dtype or block_tables.dtype is not torch.int32 or seq_starts.dtype is not torch.int32:
+        raise ValueError("k_out and v_out must have one type, block_tables and seq_starts must be torch.int32")
+    if not (k_out.get_device() == v_out.get_device() == block_tables.get_device() == seq_starts.get_device() == index
+            and k_out.is_contiguous() and v_out.is_contiguous() and block_tables.is_contiguous()
+            and seq_starts.is_contiguous()):
+        raise ValueError("tensors must be contiguous CUDA tensors on one device")
     S, MB = block_tables.shape
-    T = k_out.shape[0]
-    if k_out.shape != (T, Hk, D) or v_out.shape != (T, Hk, D):
+    shape = k_out.shape
+    T = shape[0]
+    if shape != (T, Hk, D) or v_out.shape != shape:
         raise ValueError("k_out and v_out must be [tokens, Hk, D]")
-    if seq_starts.numel() != S + 1 or (first_tokens is not None and first_tokens.numel() != S):
-        raise ValueError("seq_starts must have S + 1 entries, first_tokens S")
+    if seq_starts.numel() != S + 1:
+        raise ValueError("seq_starts must have S + 1 entries")
+    first = None
+    if first_tokens is not None:
+        _on(index, torch.int32, "first_tokens", first_tokens)
+        if first_tokens.numel() != S:
+            raise ValueError("first_tokens must have S entries")
+        first = first_tokens.data_ptr()
+    if error_flag is not None:
+        _on(index, torch.int32, "error_flag", error_flag)
     _call_on(index, load().pa_read_cache_int8, k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(),
-             v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-             None if first_tokens is None else first_tokens.data_ptr(), seq_starts.data_ptr(), T, S, Hk, D, bs, MB, NB,
-             _stream_on(stream, index), code, None if error_flag is None else error_flag.data_ptr())
+             v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), first,
+             seq_starts.data_ptr(), T, S, Hk, D, bs, MB, NB, _stream_on(stream, index), code,
+             None if error_flag is None else error_flag.data_ptr())
     return k_out, v_out
 
 

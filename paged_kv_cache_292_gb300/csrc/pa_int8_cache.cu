@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kCacheThreads) pa_write_int8_kernel(const __gr
     if (lane == 0 && blockIdx.y == 0) report(p.error_flag, PA_DEVERR_SLOT);
     return;
   }
-  const long long block = slot / p.block_size;
+  const long long block = slot < (1ll << 32) ? (uint32_t)slot / (uint32_t)p.block_size : slot / p.block_size;
   const int in_block = (int)(slot - block * p.block_size);
   const int first = blockIdx.y * (kCacheSteps * kRowsPerStep) + lane / kRowThreads;
   float x[kCacheSteps][8];
