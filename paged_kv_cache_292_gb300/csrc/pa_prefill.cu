@@ -15,11 +15,11 @@
 // (pa_chunk_work.h).  Per CTA:
 //   warps 0-3, 4-7  softmax groups 0 and 1: a thread per row, 64 tokens a step; scores
 //                   come from tensor memory, weights go back there as bf16
-//   warp 8          walks the list, and loads K and V tiles: TMA boxes of gcd(block_size, 128)
+//   warp 8          walks the list, loads queries (TMA) and K and V tiles: TMA boxes of gcd(block_size, 128)
 //                   token rows x 64 elements into 128-byte swizzled panels (int8: the
 //                   codes into a ring of their own, the scales beside them);
 //                   blocks that are no multiple of 8: 16-byte asynchronous copies
-//   warp 9          loads an item's queries (TMA), issues the products (tcgen05.mma, one thread)
+//   warp 9          issues the products (tcgen05.mma, one thread)
 //   warp 10         bf16: zeroes what lies behind a context's end in its last V tile (zero
 //                   weights do not cancel the NaN that may lie there)
 //   warps 12-15     int8: widen the codes into the panels
@@ -84,14 +84,16 @@ struct ChunkLayout {
   // K and V tiles: groups of 8 token rows, a group's panels of 1 KiB side by side, so that
   // the rows of a block come as one copy.  (Q: panels of 128 rows.)
   static constexpr uint32_t kGroup = kPanels * 1024;
-  static constexpr int kStages = D == 64 ? 8 : I8 ? 3 : 5;
-  static constexpr int kRawStages = I8 ? (D == 64 ? 6 : 3) : 0;  // tiles of codes
+  static constexpr int kStages = D == 64 ? 8 : I8 ? 3 : 4;
+  static constexpr int kRawStages = I8 ? (D == 64 ? 4 : 2) : 0;  // tiles of codes
   static constexpr uint32_t kRawBytes = kTileBytes / 2;
   static constexpr uint32_t kQ = 1024;  // barriers and items before it
   static constexpr uint32_t kRing = kQ + 2 * kTileBytes;
   static constexpr uint32_t kRaw = kRing + kStages * kTileBytes;
   static constexpr uint32_t kScales = kRaw + kRawStages * kRawBytes;  // [slots][K, V][128] floats
-  static constexpr uint32_t kBytes = kScales + (I8 ? kScaleSlots * 1024 : 0);
+  static constexpr uint32_t kOut = kScales + (I8 ? kScaleSlots * 1024 : 0);  // [softmax warp][32 rows][32 dims] bf16
+  static constexpr uint32_t kMl = kOut + kSoftmaxWarps * 2048;               // [group][128] (m, l)
+  static constexpr uint32_t kBytes = kMl + 2048;
   static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
 };
 
@@ -132,10 +134,10 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
   auto o_step = [&](int w) { return bars + 8u * (3 * NS + 8 + w); };  // a step's product has been added
   const uint32_t q_full = bars + 8u * (3 * NS + 10), q_empty = bars + 8u * (3 * NS + 11);
   const uint32_t o_full = bars + 8u * (3 * NS + 12), joined = bars + 8u * (3 * NS + 13);
-  const uint32_t drained = bars + 8u * (3 * NS + 14);
-  auto sc_full = [&](int i) { return bars + 8u * (3 * NS + 15 + i); };
-  auto sc_empty = [&](int i) { return bars + 8u * (3 * NS + 15 + kScaleSlots + i); };
-  constexpr int kItemBars = 3 * NS + 15 + 2 * kScaleSlots;
+  const uint32_t drained = bars + 8u * (3 * NS + 14), o_free = bars + 8u * (3 * NS + 15);
+  auto sc_full = [&](int i) { return bars + 8u * (3 * NS + 16 + i); };
+  auto sc_empty = [&](int i) { return bars + 8u * (3 * NS + 16 + kScaleSlots + i); };
+  constexpr int kItemBars = 3 * NS + 16 + 2 * kScaleSlots;
   auto item_full = [&](int i) { return bars + 8u * (kItemBars + i); };
   auto item_empty = [&](int i) { return bars + 8u * (kItemBars + kItemSlots + i); };
   auto raw_full = [&](int i) { return bars + 8u * (kItemBars + 2 * kItemSlots + i); };
@@ -168,7 +170,8 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
       mbar_init(item_empty(i), kSoftmaxWarps + 1 + (I8 ? kWidenWarps : kOdd ? 0 : 1));
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, kSoftmaxWarps);
+    mbar_init(q_empty, 1);
+    mbar_init(o_free, kSoftmaxWarps);
     mbar_init(o_full, 1);
     mbar_init(joined, kSoftmaxWarps);
     for (int i = 0; i < 4; ++i) {
@@ -370,142 +373,106 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
       if (alive) alive = wait_or_abort(o_full, o_phase, p.wait_limit_ns, abort_flag);
       o_phase ^= 1u;
       tc_fence_after();
-      // Whole items end here: a row's thread puts its part into the Q tile, which nobody
-      // reads any more, and the warp writes its rows out side by side (a thread of a row
-      // each would touch 32 lines with every store).  A part of an item leaves its sums for the join.
+      // Whole items end here: a row's thread puts 32 dims at a time where its warp reads
+      // them again, and the warp writes its rows out side by side (a thread of a row each
+      // would touch 32 lines with every store).  A part of an item leaves its sums for the join.
       const bool whole = it.whole();
       const size_t part = (size_t)2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
       float* part_o = p.part_o + (part * 2 + row_tile) * (kChunkRows * D) + 4 * row;  // + dims * 128
       float2* part_ml = reinterpret_cast<float2*>(p.part_ml) + part * (2 * kChunkRows) + row_tile * kChunkRows + row;
-      unsigned char* staged = smem + L::kQ + (two ? w * L::kTileBytes : 0);
-      const int row0 = row & ~31;  // the warp's first row
-      auto stage = [&](int d0, const float (&o)[16]) {  // 16 dims of this row
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int u = d0 / 8 + i;
-          *reinterpret_cast<uint4*>(staged + (u >> 3) * kPanel + row * 128 + (((u & 7) ^ (row & 7)) << 4)) =
-              make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                         pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-        }
-      };
-      auto write_out = [&](int d0, int dims) {  // the warp's rows, dims d0 .. d0 + dims - 1 (32 to 128)
-        __syncwarp();
-        const int units = dims / 8, per = 32 / units;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-        int r = row0 + lane / units, t = r / p.group, g = r - t * p.group;
-        const int u = d0 / 8 + lane % units;
-#pragma unroll 4
-        for (; r < row0 + 32; r += per) {
-          const int tok = row_tile * p.tile_tokens + t;
-          if (t < p.tile_tokens && tok < it.tokens)
-            *reinterpret_cast<uint4*>(out + ((size_t)(it.row + tok) * p.num_heads + it.head * p.group + g) * D + 8 * u) =
-                *reinterpret_cast<const uint4*>(staged + (u >> 3) * kPanel + r * 128 + (((u & 7) ^ (r & 7)) << 4));
-          for (g += per; g >= p.group; g -= p.group) ++t;
-        }
-      };
-      if (two) {
-        if (!alive) {
-          timed_out();
-          break;
-        }
-        if (rows_here) {
-          const float inv = 1.f / l;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 64) {
-            uint32_t o[64];
-            tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&o[0]), o_addr + c);
-            tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&o[32]), o_addr + c + 32u);
-            tmem_wait_load();
-            if (whole) {
-#pragma unroll
-              for (int d = 0; d < 64; d += 16) {
-                float f[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = l != 0.f ? __uint_as_float(o[d + i]) * inv : 0.f;
-                stage(c + d, f);
-              }
-            } else if (real) {
-#pragma unroll
-              for (int i = 0; i < 64; i += 4)
-                *reinterpret_cast<float4*>(part_o + (size_t)(c + i) * kChunkRows) =
-                    make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
-                                __uint_as_float(o[i + 3]));
-            }
-          }
-          if (whole)
-            write_out(0, D);
-          else if (real)
-            *part_ml = make_float2(m * p.scale_log2, l);
-        }
-      } else {
-        // One row tile: the row's two threads leave (m, l) in tensor memory, where the scores
-        // were, and take half of the dims each from both groups' O.
-        if (alive && rows_here) {
-          uint32_t ml[4] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u};
-          tmem_store4(s_all + 128u * w, ml);
-          tmem_wait_store();
-        }
-        tc_fence_before();
+      float f0 = 1.f, f1 = 0.f;  // factors of this group's O, or of group 0's and group 1's
+      int d0 = 0, d1 = D;
+      float2* ml = reinterpret_cast<float2*>(smem + L::kMl);
+      if (!two) {
+        // One row tile: the row's two threads have a part of its tokens each, and take half of
+        // the dims each from both groups' O.
+        ml[w * kChunkRows + row] = make_float2(m, l);
         __syncwarp();
         if (alive) {
           if (lane == 0) mbar_arrive(joined);
           alive = wait_or_abort(joined, j_phase, p.wait_limit_ns, abort_flag);
           j_phase ^= 1u;
-          tc_fence_after();
         }
-        if (!alive) {
-          timed_out();
-          break;
-        }
-        if (rows_here) {
-          uint32_t a[16], b[16];
-          tmem_load16(a, s_all);
-          tmem_load16(b, s_all + 128u);
-          tmem_wait_load();
-          const float m0 = __uint_as_float(a[0]), m1 = __uint_as_float(b[0]);
-          const float l0 = __uint_as_float(a[1]), l1 = __uint_as_float(b[1]);
-          // A group that saw nothing (l == 0) may have anything in O.
-          const float top = fmaxf(l0 != 0.f ? m0 : -INFINITY, l1 != 0.f ? m1 : -INFINITY);
-          const float f0 = l0 != 0.f ? ex2_ftz((m0 - top) * p.scale_log2) : 0.f;
-          const float f1 = l1 != 0.f ? ex2_ftz((m1 - top) * p.scale_log2) : 0.f;
-          const float sum = f0 * l0 + f1 * l1;
-          const float inv = sum == 0.f ? 0.f : whole ? 1.f / sum : 1.f;
-          const int d0 = (D / 2) * w;
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            tmem_load16(a, o_all + d0 + 16u * c);
-            tmem_load16(b, o_all + (uint32_t)D + d0 + 16u * c);
-            tmem_wait_load();
-            float o[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = ((l0 != 0.f ? __uint_as_float(a[i]) * f0 : 0.f) + (l1 != 0.f ? __uint_as_float(b[i]) * f1 : 0.f)) * inv;
-            if (whole) {
-              stage(d0 + 16 * c, o);
-            } else if (real) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(part_o + (size_t)(d0 + 16 * c + 4 * i) * kChunkRows) =
-                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            }
-          }
-          if (whole)
-            write_out(d0, D / 2);
-          else if (real && w == 0)
-            *part_ml = make_float2(top * p.scale_log2, sum);
-        }
+        const float2 a = ml[row], b = ml[kChunkRows + row];
+        // A group that saw nothing (l == 0) may have anything in O.
+        m = fmaxf(a.y != 0.f ? a.x : -INFINITY, b.y != 0.f ? b.x : -INFINITY);
+        f0 = a.y != 0.f ? ex2_ftz((a.x - m) * p.scale_log2) : 0.f;
+        f1 = b.y != 0.f ? ex2_ftz((b.x - m) * p.scale_log2) : 0.f;
+        l = f0 * a.y + f1 * b.y;
+        d0 = (D / 2) * w;
+        d1 = d0 + D / 2;
       }
-      // The Q tile is free for the next item's queries (which copies write).
-      async_proxy_fence();
+      if (!alive) {
+        timed_out();
+        break;
+      }
+      if (rows_here) {
+        if (whole || l == 0.f) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          f0 *= inv;
+          f1 *= inv;
+        }
+        // The rows that this lane writes: 8 i + lane / 4 of the warp's, by the place of their head.
+        int place[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = (row & ~31) + 8 * i + (lane >> 2), t = r / p.group, tok = row_tile * p.tile_tokens + t;
+          place[i] = t < p.tile_tokens && tok < it.tokens ? (it.row + tok) * p.num_heads + it.head * p.group + (r - t * p.group)
+                                                          : -1;
+        }
+        const uint32_t own = two ? o_addr : o_all;
+        unsigned char* staged = smem + L::kOut + warp * 2048;
+#pragma unroll 1
+        for (int d = d0; d < d1; d += 32) {
+          float o[32];
+          tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&o[0]), own + d);
+          tmem_wait_load();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? o[i] * f0 : 0.f;
+          if (!two) {
+            float more[32];
+            tmem_load32(*reinterpret_cast<uint32_t(*)[32]>(&more[0]), own + (uint32_t)D + d);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] += f1 != 0.f ? more[i] * f1 : 0.f;
+          }
+          if (whole) {
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              *reinterpret_cast<uint4*>(staged + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
+                             pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (lane >> 2), u = lane & 3;
+              if (place[i] >= 0)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)place[i] * D + d + 8 * u) =
+                    *reinterpret_cast<const uint4*>(staged + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+            }
+          } else if (real) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(part_o + (size_t)(d + 4 * i) * kChunkRows) =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (!whole && real && (two || w == 0)) *part_ml = make_float2(m * p.scale_log2, l);
+      }
+      // O, and the places of (m, l), are free for the next item's.
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_empty);
+      if (lane == 0) mbar_arrive(o_free);
     }
   } else if (warp == kLoadWarp) {
     // ---------------- loads ----------------
-    if (!kOdd && lane == 0) {
-      prefetch_tensormap(&p.tm_k);
-      prefetch_tensormap(&p.tm_v);
+    if (lane == 0) {
+      prefetch_tensormap(&p.tm_q);
+      if (!kOdd) {
+        prefetch_tensormap(&p.tm_k);
+        prefetch_tensormap(&p.tm_v);
+      }
     }
     // Stages the copies land in: panels, or the codes of int8 pools.
     constexpr int kCopyStages = I8 ? NR : NS;
@@ -523,6 +490,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
     uint32_t armed = 0, armed_phase = 0;       // stages armed, with the parity of their last phase,
     uint32_t tailed = 0, tail_phase = 0;       // and those armed as a tail
     uint32_t scaled = 0, scale_phase = 0;      // slots of scales
+    uint32_t queries = 0;                      // items whose queries are asked for
     uint32_t tile_count = 0;
     int late[2] = {-1, -1};  // kOdd: stages whose copies are issued and not yet told of
     bool alive = true;
@@ -561,10 +529,6 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         to[2] = make_int4((items.two() ? 1 : 0) | (items.t0 == 0 && items.t1 == items.tiles ? 2 : 0), items.row.ctx, 0, 0);
         mbar_arrive(item_full(at_item.i));
       }
-      // Their queries on the way to L2.
-      if (lane < 2 * L::kPanels && (items.two() || lane < L::kPanels))
-        tma_prefetch_3d(&p.tm_q, 64 * (lane % L::kPanels), items.head * p.group,
-                        items.row.row0 + (2 * items.pair + lane / L::kPanels) * p.tile_tokens);
       __syncwarp();
       at_item.next(kItemSlots);
       const int32_t* table = p.tables + (size_t)items.seq * p.max_blocks;
@@ -698,6 +662,19 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
       }
       alive = load_k(t0, row_v);
       if (alive && ahead == 2 && t0 + 1 < t1) alive = load_k(t0 + 1, row_v1);
+      // The queries, once the item before has all of its scores: (token, group head) rows of a row
+      // tile are one box.
+      if constexpr (kOdd) tell_all();
+      if (!alive || (queries > 0 && !(alive = wait(q_empty, (queries - 1) & 1u)))) break;
+      {
+        const int copies = (items.two() ? 2 : 1) * L::kPanels;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, 128u * p.group * p.tile_tokens * copies);
+        __syncwarp();
+        if (lane < copies)
+          tma_load_3d(base + L::kQ + lane * kPanel, &p.tm_q, 64 * (lane % L::kPanels), items.head * p.group,
+                      items.row.row0 + (2 * items.pair + lane / L::kPanels) * p.tile_tokens, q_full);
+        ++queries;
+      }
       for (int x = t0; alive && x < t1; ++x) {
         int row_next = -1;  // of tile x + 2
         if constexpr (!kOdd) {
@@ -721,9 +698,10 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
       __syncwarp();
     }
     named_barrier_sync(1, kChunkThreads);
-    if (!kOdd && *abort_flag != 0) {
+    if (*abort_flag != 0) {
       // Copies that were started may still be landing: wait for them (again
       // bounded) before the CTA's shared memory goes.
+      if (queries > 0) (void)mbar_wait(q_full, (queries - 1) & 1u, p.wait_limit_ns);
       for (int i = 0; i < kCopyStages; ++i) {
         if ((armed >> i) & 1u) (void)mbar_wait(landed(i), (armed_phase >> i) & 1u, p.wait_limit_ns);
         if ((tailed >> i) & 1u) (void)mbar_wait(tail(i), (tail_phase >> i) & 1u, p.wait_limit_ns);
@@ -735,7 +713,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
     // ---------------- products ----------------
     constexpr uint32_t kScores = product(true, 128, kHalf, false), kValues = product(true, 128, D, true);
     Ring ring;
-    uint32_t q_phase = 0, tile_count = 0;
+    uint32_t tile_count = 0;
     uint32_t scores_taken[2] = {0u, 0u}, values_taken[2] = {0u, 0u};  // steps of either group
     bool alive = true;
     const uint32_t q_op = smem_operand_low(base + L::kQ, kPanel), elected = elect_one();
@@ -752,27 +730,13 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
       timed_out();
       return false;
     };
-    if (lane == 0) prefetch_tensormap(&p.tm_q);
     ChunkItem it;
-    bool first = true;
-    for (; alive && take_item(&it); leave_item()) {
+    uint32_t nth = 0;  // item
+    for (; alive && take_item(&it); leave_item(), ++nth) {
       const int t0 = uniform(it.t0), t1 = uniform(it.t1), end0 = uniform(it.ends[0]), end1 = uniform(it.ends[1]);
       const bool two = uniform(it.flags) & 1;
-      // The queries: (token, group head) rows of a row tile are one box.
-      if (!first && !(alive = wait(q_empty, q_phase ^ 1u))) break;
-      first = false;
-      if (lane == 0) {
-        const uint32_t bytes = 128u * p.group * p.tile_tokens;
-        mbar_arrive_expect_tx(q_full, (two ? 2u : 1u) * L::kPanels * bytes);
-        for (int w = 0; w < (two ? 2 : 1); ++w)
-          for (int c = 0; c < L::kPanels; ++c)
-            tma_load_3d(base + L::kQ + w * L::kTileBytes + c * kPanel, &p.tm_q, 64 * c, it.head * p.group,
-                        it.row + w * p.tile_tokens, q_full);
-      }
-      __syncwarp();
       auto release = [&](int st) { mma_commit_warp(empty(st), elected); };
-      if (!(alive = wait(q_full, q_phase))) break;
-      q_phase ^= 1u;
+      if (!(alive = wait(q_full, nth & 1u))) break;
       // What follows is written out for both kinds of items, and once more for tiles in whose place
       // nothing ends: one warp issues everything, and its branches take as long as the products.
       auto item_of = [&](auto two_tag) -> bool {
@@ -866,7 +830,10 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
                    step(W1{}, W1{}, inner, x + 1);
         };
         const int inner_end = min(end0, end1);  // steps before it exist for both groups
+        // O is the item before's until its rows are out.
+        if (nth > 0 && !wait(o_free, (nth - 1) & 1u)) return false;
         for (int x = t0; x < t1; x += kStep) {
+          if (x + kStep >= t1) mma_commit_warp(q_empty, elected);  // all scores are asked for
           const int last = x + (kTwo ? 1 : 3);  // tile of the last scores
           if (!(2 * last + 1 < inner_end ? steps(std::true_type{}, x) : steps(std::false_type{}, x))) return false;
         }
