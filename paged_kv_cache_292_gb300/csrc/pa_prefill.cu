@@ -778,8 +778,10 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         using W0 = std::integral_constant<int, 0>;
         using W1 = std::integral_constant<int, 1>;
         // The first K tile of either group.
+#pragma unroll 1
         for (int i = 0; i < kStep && t0 + i < t1; ++i) {
           if (!wait(full(ring.i), ring.phase)) return false;
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             if ((kTwo || i == 0) && 2 * (t0 + i) + h < end0) scores(W0{}, ring.i, h);
             if ((kTwo || i == 1) && 2 * (t0 + i) + h < end1) scores(W1{}, ring.i, h);
@@ -790,8 +792,8 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         // V of tile x and K of the group's next, in steps of half h and group w: with two row tiles
         // the groups in turn, both with both tiles; with one a group's steps and then the other's.
         Ring v, k;
-        auto step = [&](auto w_tag, auto h_tag, auto inner_tag, int x) -> bool {
-          constexpr int w = decltype(w_tag)::value, h = decltype(h_tag)::value;
+        auto step = [&](auto w_tag, int h, auto inner_tag, int x) -> bool {
+          constexpr int w = decltype(w_tag)::value;
           constexpr bool kInner = decltype(inner_tag)::value;  // all of the steps that are asked for exist
           if (!kInner && x >= t1) return true;
           const int next = x + kStep;
@@ -822,12 +824,19 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
           return true;
         };
         auto steps = [&](auto inner, int x) -> bool {
-          if constexpr (kTwo)
-            return step(W0{}, W0{}, inner, x) && step(W1{}, W0{}, inner, x) && step(W0{}, W1{}, inner, x) &&
-                   step(W1{}, W1{}, inner, x);
-          else
-            return step(W0{}, W0{}, inner, x) && step(W0{}, W1{}, inner, x) && step(W1{}, W0{}, inner, x + 1) &&
-                   step(W1{}, W1{}, inner, x + 1);
+          if constexpr (kTwo) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+              if (!step(W0{}, h, inner, x) || !step(W1{}, h, inner, x)) return false;
+          } else {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+              if (!step(W0{}, h, inner, x)) return false;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+              if (!step(W1{}, h, inner, x + 1)) return false;
+          }
+          return true;
         };
         const int inner_end = min(end0, end1);  // steps before it exist for both groups
         // O is the item before's until its rows are out.
