@@ -648,44 +648,44 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
       };
       const int ahead = items.two() ? 1 : 2;  // K tiles ahead of the V tile
       const int t0 = items.t0, t1 = items.t1;
-      auto load_k = [&](int x, int row) -> bool {
-        if (I8 && !load_scales(x, row, tile_count + (uint32_t)(x - t0))) return false;
-        return load(false, x, row);
-      };
-      // Rows of this lane's box in the V tile to come and (one row tile) the one behind it; K's next.
-      int row_v = -1, row_v1 = -1, row_k = -1, entry = -1;
-      if constexpr (!kOdd) {
-        const int e0 = box_entry(t0), e1 = box_entry(t0 + 1);
-        entry = box_entry(t0 + 2);
-        row_v = box_row(t0, e0);
-        row_v1 = box_row(t0 + 1, e1);
-      }
-      alive = load_k(t0, row_v);
-      if (alive && ahead == 2 && t0 + 1 < t1) alive = load_k(t0 + 1, row_v1);
-      // The queries, once the item before has all of its scores: (token, group head) rows of a row
-      // tile are one box.
-      if constexpr (kOdd) tell_all();
-      if (!alive || (queries > 0 && !(alive = wait(q_empty, (queries - 1) & 1u)))) break;
-      {
-        const int copies = (items.two() ? 2 : 1) * L::kPanels;
-        if (lane == 0) mbar_arrive_expect_tx(q_full, 128u * p.group * p.tile_tokens * copies);
-        __syncwarp();
-        if (lane < copies)
-          tma_load_3d(base + L::kQ + lane * kPanel, &p.tm_q, 64 * (lane % L::kPanels), items.head * p.group,
-                      items.row.row0 + (2 * items.pair + lane / L::kPanels) * p.tile_tokens, q_full);
-        ++queries;
-      }
-      for (int x = t0; alive && x < t1; ++x) {
-        int row_next = -1;  // of tile x + 2
-        if constexpr (!kOdd) {
-          row_next = box_row(x + 2, entry);
-          entry = box_entry(x + 3);
+      // K of tile kx or V of tile vx, whichever the products take next.  Rows of this lane's box in
+      // the V tiles vx and vx + 1; the table entry of K's next tile is read a tile before.
+      int kx = t0, vx = t0, row_v = -1, row_v1 = -1, entry = kOdd ? -1 : box_entry(t0);
+#pragma unroll 1
+      while (vx < t1) {
+        const bool v = kx >= t1 || kx - vx >= ahead;
+        if (v && vx == t0) {
+          // The queries, once the item before has all of its scores: (token, group head) rows of a row
+          // tile are one box.
+          if constexpr (kOdd) tell_all();
+          if (queries > 0 && !(alive = wait(q_empty, (queries - 1) & 1u))) break;
+          const int copies = (items.two() ? 2 : 1) * L::kPanels;
+          if (lane == 0) mbar_arrive_expect_tx(q_full, 128u * p.group * p.tile_tokens * copies);
+          __syncwarp();
+          if (lane < copies)
+            tma_load_3d(base + L::kQ + lane * kPanel, &p.tm_q, 64 * (lane % L::kPanels), items.head * p.group,
+                        items.row.row0 + (2 * items.pair + lane / L::kPanels) * p.tile_tokens, q_full);
+          ++queries;
         }
-        row_k = ahead == 2 ? row_next : row_v1;
-        alive = load(true, x, row_v);
-        if (alive && x + ahead < t1) alive = load_k(x + ahead, row_k);
-        row_v = row_v1;
-        row_v1 = row_next;
+        int row = row_v;
+        if (!v) {
+          if constexpr (!kOdd) {
+            row = box_row(kx, entry);
+            entry = box_entry(kx + 1);
+          }
+          if (kx == vx)
+            row_v = row;
+          else
+            row_v1 = row;
+          if (I8 && !(alive = load_scales(kx, row, tile_count + (uint32_t)(kx - t0)))) break;
+        }
+        if (!(alive = load(v, v ? vx : kx, row))) break;
+        if (v) {
+          ++vx;
+          row_v = row_v1;
+        } else {
+          ++kx;
+        }
       }
       tile_count += (uint32_t)(t1 - t0);
     }
