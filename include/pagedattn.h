@@ -501,7 +501,9 @@ int pa_decode_fp8_mq_append(void* out, const void* query, const void* k_new, con
  * after letting the copies it had started land (again within the limit).
  * (pa_decode_prefix: its prefix kernel, whose tiles of 128 prefix tokens are
  * counted per KV head and per 256 query rows of it, one after another, and behind
- * them the tiles of the walk behind the prefix; pa_decode_mod: the tiles its walk takes.)
+ * them the tiles of the walk behind the prefix; pa_decode_mod: the tiles its walk takes;
+ * pa_prefill and pa_prefill_int8: tile `tile` of those that each CTA takes, in every CTA;
+ * pa_prefill over fp32 pools has no waits and leaves the setting alone.)
  * That call's output is unspecified, and its scratch (pa_decode_ws) must be
  * zero-filled again before reuse.  The setting is used by one launch and then
  * cleared; tile = -1 clears it.  Returns PA_OK, or PA_ERR_INVALID_ARG for

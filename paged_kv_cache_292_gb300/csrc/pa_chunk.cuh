@@ -63,7 +63,7 @@ struct ChunkParams {
   // (times sign) is the largest score; fp32: scale_log2 has the sign.
   float scale_log2, sign;
   unsigned long long wait_limit_ns;
-  long long stall_unit;  // tests of the bounded waits: unit of the list whose tile's copies are withheld
+  long long stall_tile;  // tests of the bounded waits: tile of every CTA whose copies are withheld (-1: none)
 };
 
 // fp32 pools (pa_prefill_f32.cu): queues both launches.

@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
         return true;
       };
       auto load = [&](bool v, int x, int row) -> bool {
-        const bool withhold = p.stall_unit >= 0 && items.start + items.cs.item + x == p.stall_unit;
+        const bool withhold = p.stall_tile >= 0 && tile_count + (uint32_t)(x - items.t0) == (uint64_t)p.stall_tile;
         if constexpr (kOdd) {
           // What it waits for may wait for these.
           if (__any_sync(0xffffffffu, !mbar_try_wait(taken(ring.i), ring.phase ^ 1u))) tell_all();
@@ -1089,7 +1089,7 @@ int prefill_impl(const ChunkCall& c) {
   }
   rc = make_maps(&prm, pool_rows, c.head_size, c.int8, !odd);
   if (rc != PA_OK) return rc;
-  take_wait_test(&prm.stall_unit, &prm.wait_limit_ns);
+  take_wait_test(&prm.stall_tile, &prm.wait_limit_ns);
   if (c.head_size == 64) {
     if (c.int8) return odd ? launch_chunks<64, true, true>(prm, dev, st) : launch_chunks<64, true, false>(prm, dev, st);
     return odd ? launch_chunks<64, false, true>(prm, dev, st) : launch_chunks<64, false, false>(prm, dev, st);
