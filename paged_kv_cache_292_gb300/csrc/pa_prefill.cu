@@ -97,11 +97,6 @@ struct ChunkLayout {
   static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
 };
 
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Two codes (the low bytes of the halves of x) as bf16 integers: with the sign bit

@@ -41,6 +41,9 @@ __global__ void __launch_bounds__(kF32Threads, 1) pa_prefill_f32_kernel(const __
   if (!chunk_begin<kF32Threads>(p, &items, reinterpret_cast<long long*>(smem))) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   constexpr int kUnits = D / 4;  // 16-byte units of a row
+  constexpr int kRowStep = kF32Threads / kUnits, kCopies = kStep / kRowStep;
+  // Row 8 ty + i in shared memory: a warp's two rows lie side by side, in different banks.
+  auto row_at = [](int ty, int i) { return 16 * i + ty; };
   const float* q = static_cast<const float*>(p.q);
   float* out = static_cast<float*>(p.out);
   // Row i of the item: its token in the chunk (-1: none) and its place in query and out.
@@ -59,7 +62,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) pa_prefill_f32_kernel(const __
       const int r = i / kUnits, u = i % kUnits;
       size_t at;
       const bool real = token_of(r, &at) >= 0;
-      *reinterpret_cast<float4*>(sq + r * L::kPitch + 4 * u) =
+      *reinterpret_cast<float4*>(sq + row_at(r >> 3, r & 7) * L::kPitch + 4 * u) =
           real ? __ldg(reinterpret_cast<const float4*>(q + at) + u) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     int sees[8];
@@ -74,102 +77,138 @@ __global__ void __launch_bounds__(kF32Threads, 1) pa_prefill_f32_kernel(const __
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) acc[i][j] = 0.f;
     }
-    const int end = min(items.t1 * kChunkTokens, ctx);
-    for (int t0 = items.t0 * kChunkTokens; t0 < end; t0 += kStep) {
-      __syncthreads();
-      for (int i = tid; i < kStep * kUnits; i += kF32Threads) {
-        const int r = i / kUnits, u = i % kUnits, tok = t0 + r;
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-        if (tok < ctx) {
-          const int phys = __ldg(table + tok / p.block_size);
-          if (phys < 0 || phys >= p.num_physical_blocks) {
+    bool mine = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      size_t at;
+      mine = mine || token_of(8 * ty + i, &at) >= 0;
+    }
+    const bool rows_here = __any_sync(0xffffffffu, mine);
+    const int begin = items.t0 * kChunkTokens, end = min(items.t1 * kChunkTokens, ctx);
+    // K of a step is copied while the step before multiplies V, V while the scores are
+    // made: a buffer each.  A thread copies unit tid % kUnits of rows tid / kUnits + kRowStep i.
+    int place[kCopies];  // those rows in the pool (-1: none)
+    auto look_up = [&](int t0) {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int tok = t0 + tid / kUnits + kRowStep * i;
+        place[i] = -1;
+        if (tok < end) {
+          const int blk = tok / p.block_size, phys = __ldg(table + blk);
+          if (phys < 0 || phys >= p.num_physical_blocks)
             report(p.error_flag, PA_DEVERR_BLOCK_ID);
-          } else {
-            const size_t at = (((size_t)phys * p.block_size + tok % p.block_size) * p.kv_heads + items.head) * kUnits + u;
-            k = __ldg(static_cast<const float4*>(p.k_cache) + at);
-            v = __ldg(static_cast<const float4*>(p.v_cache) + at);
-          }
+          else
+            place[i] = phys * p.block_size + (tok - blk * p.block_size);
         }
-        *reinterpret_cast<float4*>(sk + r * L::kPitch + 4 * u) = k;
-        *reinterpret_cast<float4*>(sv + r * D + 4 * u) = v;
       }
-      __syncthreads();
-      float s[8][4];
+    };
+    auto copy = [&](const void* pool, float* to, int pitch) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 2
-      for (int u = 0; u < kUnits; ++u) {
-        float4 a[8], b[4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (8 * ty + i) * L::kPitch + 4 * u);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * L::kPitch + 4 * u);
+      for (int i = 0; i < kCopies; ++i)
+        copy_async16(smem_addr(to + (tid / kUnits + kRowStep * i) * pitch + 4 * (tid % kUnits)),
+                     static_cast<const float4*>(pool) + ((size_t)max(place[i], 0) * p.kv_heads + items.head) * kUnits + tid % kUnits,
+                     place[i] >= 0);
+    };
+    if (begin < end) {
+      look_up(begin);
+      copy(p.k_cache, sk, L::kPitch);
+      copies_commit();
+      copy(p.v_cache, sv, D);
+    }
+    copies_commit();
+    for (int t0 = begin; t0 < end; t0 += kStep) {
+      const bool more_steps = t0 + kStep < end;
+      if (more_steps) look_up(t0 + kStep);
+      copies_wait<1>();
+      __syncthreads();  // K is there (and the queries)
+      float keep[8];
+      if (rows_here) {  // (else the warp's 16 rows are none of the chunk's)
+        float s[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-            s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-            s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-            s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
-          }
-      }
-      float keep[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[i][j] = t0 + tx + 16 * j < sees[i] ? s[i][j] * p.scale_log2 : -INFINITY;
-          top = fmaxf(top, s[i][j]);
-        }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float mn = fmaxf(m[i], top), ref = mn == -INFINITY ? 0.f : mn;
-        keep[i] = ex2_ftz(m[i] - ref);
-        m[i] = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float w = ex2_ftz(s[i][j] - ref);
-          sum += w;
-          sp[(8 * ty + i) * L::kPPitch + tx + 16 * j] = w;
-        }
-        l[i] = fmaf(l[i], keep[i], sum);
-      }
-      __syncwarp();  // a row's weights are written and read by the same half warp
-      float part[8][D / 16];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) part[i][j] = 0.f;
+          for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 2
-      for (int t = 0; t < kStep; t += 4) {
-        float4 w[8];
+        for (int u = 0; u < kUnits; ++u) {
+          float4 a[8], b[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const float4*>(sp + (8 * ty + i) * L::kPPitch + t);
+          for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const float4*>(sq + row_at(ty, i) * L::kPitch + 4 * u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+          for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * L::kPitch + 4 * u);
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            const float4 v = *reinterpret_cast<const float4*>(sv + (t + e) * D + 64 * j + 4 * tx);
+          for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float f = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
-              part[i][4 * j] = fmaf(f, v.x, part[i][4 * j]);
-              part[i][4 * j + 1] = fmaf(f, v.y, part[i][4 * j + 1]);
-              part[i][4 * j + 2] = fmaf(f, v.z, part[i][4 * j + 2]);
-              part[i][4 * j + 3] = fmaf(f, v.w, part[i][4 * j + 3]);
+            for (int j = 0; j < 4; ++j) {
+              s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+              s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+              s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+              s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
             }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[i][j] = t0 + tx + 16 * j < sees[i] ? s[i][j] * p.scale_log2 : -INFINITY;
+            top = fmaxf(top, s[i][j]);
           }
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float mn = fmaxf(m[i], top), ref = mn == -INFINITY ? 0.f : mn;
+          keep[i] = ex2_ftz(m[i] - ref);
+          m[i] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float w = ex2_ftz(s[i][j] - ref);
+            sum += w;
+            sp[row_at(ty, i) * L::kPPitch + tx + 16 * j] = w;
+          }
+          l[i] = fmaf(l[i], keep[i], sum);
+        }
       }
+      __syncthreads();  // K is read (and a row's weights are there, which its own half warp reads)
+      if (more_steps) copy(p.k_cache, sk, L::kPitch);
+      copies_commit();
+      copies_wait<1>();
+      __syncthreads();  // V is there
+      if (rows_here) {
+        float part[8][D / 16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) acc[i][j] = fmaf(acc[i][j], keep[i], part[i][j]);
+          for (int j = 0; j < D / 16; ++j) part[i][j] = 0.f;
+#pragma unroll 2
+        for (int t = 0; t < kStep; t += 4) {
+          float4 w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const float4*>(sp + row_at(ty, i) * L::kPPitch + t);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+              const float4 v = *reinterpret_cast<const float4*>(sv + (t + e) * D + 64 * j + 4 * tx);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float f = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
+                part[i][4 * j] = fmaf(f, v.x, part[i][4 * j]);
+                part[i][4 * j + 1] = fmaf(f, v.y, part[i][4 * j + 1]);
+                part[i][4 * j + 2] = fmaf(f, v.z, part[i][4 * j + 2]);
+                part[i][4 * j + 3] = fmaf(f, v.w, part[i][4 * j + 3]);
+              }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) acc[i][j] = fmaf(acc[i][j], keep[i], part[i][j]);
+      }
+      __syncthreads();  // V is read
+      if (more_steps) copy(p.v_cache, sv, D);
+      copies_commit();
     }
+    copies_wait<0>();
     const bool whole = items.t0 == 0 && items.t1 == items.tiles;
     const size_t part = (size_t)2 * blockIdx.x + (items.t0 == 0 ? 1 : 0);
 #pragma unroll
