@@ -29,6 +29,23 @@
 // it exponentiates one, the tensor core fills the other, so that neither waits for the
 // other's step.  Tensor memory: the buffers (2 x 64 columns a group; the weights overwrite
 // the first 32 of one, their second parts, if any, the other 32), O0, O1 (D columns).
+//
+// What bounds it, and what it measured:
+//   long chunks  the tensor core.  4096 tokens on 12,288 others (32 heads on 8, 128 dims):
+//                679 us, 1.42 PFLOP/s of the products that the mask leaves.  A tile and its two row
+//                tiles need 2,050 clocks of it if S has N = 128, but S in halves of 64 tokens reads
+//                its query operand twice as often and takes 1.5 times as long: 2,930 with the
+//                commits, which is what the kernel's tiles take.  N = 128 would need both score
+//                buffers at once, and the softmax and the products would take turns.
+//   short items  what an item costs besides its tiles, about 10,000 clocks: first scores, last product,
+//                rows out, much of it instruction fetches (0.85 stalls for an instruction per issue,
+//                0.53 in long chunks).  7 prompts of 33 to 2,047 tokens: 95 us, 0.68 PFLOP/s; 19
+//                single tokens, 3 chunks of 200 to 256 tokens and 2 idle rows on up to 4,096
+//                others: 76 us, 2.5 TB/s.
+//   few tokens   the chain of a launch: schedule, copies, one tile per CTA, join.  16 on 1k: 19 us.
+//   int8         the softmax warps' issue slots, which the widening warps share: a scale into every score
+//                and one into every weight.  51% of all slots are used.  4 chunks
+//                of 300 to 1,024 tokens on 1k to 7k others and 2 single tokens: 191 us.
 #include "pa_launch.cuh"
 
 #include <cmath>

