@@ -54,7 +54,8 @@ int pa_write_cache_int8(const void* k_new, const void* v_new, const int64_t* slo
  *               code * scale in float32, rounded once to bf16.  Rows before the
  *               first and behind the last sequence's are left as they are.
  * first_tokens  [num_seqs] int32, or NULL: 0
- * seq_starts    [num_seqs + 1] int32, as in pa_prefill
+ * seq_starts    [num_seqs + 1] int32, as in pa_prefill; where entries decrease, a row
+ *               may be left as it is (PA_DEVERR_CONTEXT_LEN)
  * A token outside its sequence's row of the tables (PA_DEVERR_CONTEXT_LEN), or of a
  * block outside the pool (PA_DEVERR_BLOCK_ID; num_physical_blocks > 0 is
  * required), leaves its row as it is.

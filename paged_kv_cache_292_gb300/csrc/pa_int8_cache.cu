@@ -164,9 +164,11 @@ __global__ void __launch_bounds__(kCacheThreads) pa_read_int8_kernel(const __gri
   // The sequence whose rows hold the token: the last that begins at or before it.
   const int s = count_up_to(p.seq_starts, p.num_seqs + 1, token, lane) - 1;
   if (s < 0 || s >= p.num_seqs) return;
-  const long long pos = (long long)token - __ldg(p.seq_starts + s) + (p.first_tokens != nullptr ? __ldg(p.first_tokens + s) : 0);
+  const int from = __ldg(p.seq_starts + s);
+  const long long pos = (long long)token - from + (p.first_tokens != nullptr ? __ldg(p.first_tokens + s) : 0);
   const bool report_it = lane == 0 && blockIdx.y == 0;
-  if (pos < 0 || pos >= (long long)p.max_blocks * p.block_size) {
+  // (Among starts that decrease the search may end at a sequence that does not hold the token.)
+  if (token < from || token >= __ldg(p.seq_starts + s + 1) || pos < 0 || pos >= (long long)p.max_blocks * p.block_size) {
     if (report_it) report(p.error_flag, PA_DEVERR_CONTEXT_LEN);
     return;
   }
@@ -211,7 +213,7 @@ int launch_rows(Kernel kernel, int num_tokens, int kv_heads, int head_size, cons
                 const char* what) {
   const int per_token = kCacheSteps * (32 / (head_size / 8));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((num_tokens + kCacheThreads / 32 - 1) / (kCacheThreads / 32)),
+  cfg.gridDim = dim3((unsigned)((num_tokens - 1) / (kCacheThreads / 32) + 1),
                      (unsigned)((2 * kv_heads + per_token - 1) / per_token));
   cfg.blockDim = dim3(kCacheThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);

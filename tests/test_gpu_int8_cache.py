@@ -139,6 +139,29 @@ def test_read_back_of_what_is_not_there():
                 assert bool((o[:20] == 9.0).all())
 
 
+def test_read_back_with_starts_that_decrease():
+    """A row gets the token of a sequence that holds it, or stays as it is and is reported."""
+    b = Chunks([40, 40, 40], [0, 0, 0], "int8", 2, 2, 64, 8, gap=0)
+    _, k, v, ks, vs, tables, _, _, _ = b.gpu()
+    starts, first = [0, 10, 5, 15], [0, 30, 2]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    outs = [torch.full((15, 2, 64), 9.0, device="cuda") for _ in range(2)]
+    err = torch.zeros(1, **i32)
+    binding.read_cache_int8(k, v, ks, vs, tables, torch.tensor(starts, **i32), *outs, error_flag=err,
+                            first_tokens=torch.tensor(first, **i32))
+    assert int(err) == binding.PA_DEVERR_CONTEXT_LEN
+    for out, values in zip(outs, b.values()):
+        for row in range(15):
+            may = [np.full((2, 64), 9.0)]
+            for s in range(3):
+                if starts[s] <= row < starts[s + 1]:
+                    t = first[s] + row - starts[s]
+                    may.append(values[b.tables[s, t // 8], t % 8].astype(np.float32))
+            got = out[row].cpu().numpy()
+            assert any((got == m).all() for m in may), row
+            assert 5 <= row < 10 or (got != 9.0).any()
+
+
 def test_serving_steps_on_the_device():
     """tables_step -> write_cache_int8 -> prefill_int8 for a prompt, then decode_int8 steps in a captured graph; and the
     same prompt through read_cache_int8 and prefill over the plain rows."""
