@@ -87,8 +87,8 @@ int pa_read_cache_int8(void* k_out, void* v_out, const void* k_cache, const void
  * chunks do (pa_prefill_int8).
  * workspace    as in pa_decode_ex: at least pa_decode_int8_workspace_size(...) bytes,
  *              zero-filled before its first use and left so by every call that
- *              completes; or NULL: the library's own (shapes that run as chunks:
- *              refused while `stream` is being captured)
+ *              completes; or NULL: the library's own, one buffer per stream, as in
+ *              pa_prefill (refused while `stream` is being captured)
  * num_ranges   as in pa_decode_ex (shapes that run as chunks: without effect)
  */
 int pa_prefill_int8(void* out, const void* query, const void* k_cache, const void* v_cache,

@@ -1028,7 +1028,7 @@ def prefill(query, k_cache, v_cache, block_tables, context_lens, seq_starts, sca
     if out is None:
         out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     _call_on(index, load().pa_prefill, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-             block_tables.data_ptr(), context_lens.data_ptr(), seq_starts.data_ptr(), T, S, H, Hk, D, bs, MB, scale,
+             block_tables.data_ptr(), context_lens.data_ptr(), seq_starts.data_ptr(), T, S, H, Hk, D, bs, MB, float(scale),
              raw, code, NB, ws, ws_bytes, err)
     return out
 
@@ -1047,7 +1047,7 @@ def prefill_int8(query, k_cache, v_cache, k_scales, v_scales, block_tables, cont
         out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     _call_on(index, load().pa_prefill_int8, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
              k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-             seq_starts.data_ptr(), T, S, H, Hk, D, bs, MB, scale, raw, NB, ws, ws_bytes, err)
+             seq_starts.data_ptr(), T, S, H, Hk, D, bs, MB, float(scale), raw, NB, ws, ws_bytes, err)
     return out
 
 
@@ -1065,5 +1065,5 @@ def decode_int8(query, k_cache, v_cache, k_scales, v_scales, block_tables, conte
         out = _made_for(stream, query.device, lambda: torch.empty_like(query))
     _call_on(index, load().pa_decode_int8, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
              k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Q, H, Hk,
-             D, bs, MB, scale, raw, NB, ws, ws_bytes, num_ranges, err)
+             D, bs, MB, float(scale), raw, NB, ws, ws_bytes, num_ranges, err)
     return out

@@ -239,6 +239,9 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
     workspace_bytes = pl.ws_total;
   }
   if (extras != nullptr) {
+  } else if (workspace == nullptr && int8 != nullptr) {
+    rc = hold.of_stream(pl.ws_partials, stream, &workspace, pl.ws_counters, &counters);
+    if (rc != PA_OK) return rc;
   } else if (workspace == nullptr) {
     rc = hold.plain(pl.ws_partials, pl.ws_counters, stream, &workspace, &counters);
     if (rc != PA_OK) return rc;

@@ -33,6 +33,8 @@ struct KeptScratch {
   unsigned long long used;    // 0: free
   void* ptr;
   size_t bytes;
+  void* tickets;  // of decode calls, zero between them
+  size_t ticket_bytes;
 };
 constexpr int kKeptStreams = 8;
 KeptScratch g_kept[kMaxDevices][kKeptStreams];
@@ -140,7 +142,7 @@ int raise_smem_limit(const void* kernel, int bytes, int device, RaisedDevices* r
   return PA_OK;
 }
 
-int ScratchHold::of_stream(size_t bytes, void* stream, void** ptr) {
+int ScratchHold::of_stream(size_t bytes, void* stream, void** ptr, size_t ticket_bytes, int32_t** tickets) {
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &status);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
@@ -161,8 +163,8 @@ int ScratchHold::of_stream(size_t bytes, void* stream, void** ptr) {
     }
     if (k.used < mine->used) mine = &k;
   }
-  const bool other = mine->used != 0 && mine->stream != id;
-  if (mine->bytes < bytes || other) {
+  const bool held = mine->used != 0 && mine->stream == id;
+  if (mine->bytes < bytes || mine->ticket_bytes < ticket_bytes || !held) {
     if (mine->used != 0) {  // calls that use the buffer may still run
       e = cudaDeviceSynchronize();
       if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize(scratch)");
@@ -170,16 +172,40 @@ int ScratchHold::of_stream(size_t bytes, void* stream, void** ptr) {
     if (mine->bytes < bytes) {
       size_t want = (size_t)16 << 20;
       while (want < bytes) want *= 2;
-      if (mine->used != 0) (void)cudaFree(mine->ptr);
-      *mine = KeptScratch{};
+      if (mine->ptr != nullptr) (void)cudaFree(mine->ptr);
+      mine->ptr = nullptr;
+      mine->bytes = 0;
+      mine->used = 0;
       e = cudaMalloc(&mine->ptr, want);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(scratch)");
+      if (e != cudaSuccess) {
+        mine->ptr = nullptr;
+        return cuda_fail(e, "cudaMalloc(scratch)");
+      }
       mine->bytes = want;
+    }
+    if (mine->ticket_bytes < ticket_bytes) {
+      const size_t want = align_up(ticket_bytes < 65536 ? 65536 : ticket_bytes, 65536);
+      if (mine->tickets != nullptr) (void)cudaFree(mine->tickets);
+      mine->tickets = nullptr;
+      mine->ticket_bytes = 0;
+      mine->used = 0;
+      void* p = nullptr;
+      e = cudaMalloc(&p, want);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(tickets)");
+      e = cudaMemset(p, 0, want);
+      if (e == cudaSuccess) e = cudaDeviceSynchronize();
+      if (e != cudaSuccess) {
+        cudaFree(p);
+        return cuda_fail(e, "cudaMemset(tickets)");
+      }
+      mine->tickets = p;
+      mine->ticket_bytes = want;
     }
     mine->stream = id;
   }
   mine->used = ++g_kept_calls;
   *ptr = mine->ptr;
+  if (tickets != nullptr) *tickets = static_cast<int32_t*>(mine->tickets);
   return PA_OK;
 }
 

@@ -51,7 +51,8 @@ class ScratchHold {
   // longest ago, and a batch that outgrows its buffer replaces it (sizes double):
   // both wait for the device.  Refused while `stream` is being captured, where a
   // graph would keep the address beyond this call: captured calls bring their own.
-  int of_stream(size_t bytes, void* stream, void** ptr);
+  // `tickets`: a buffer of the stream's for merge tickets, too, zero-filled as plain()'s.
+  int of_stream(size_t bytes, void* stream, void** ptr, size_t ticket_bytes = 0, int32_t** tickets = nullptr);
 
  private:
   std::unique_lock<std::mutex> lock_;
