@@ -45,7 +45,7 @@
 //   few tokens   the chain of a launch: schedule, copies, one tile per CTA, join.  16 on 1k: 19 us.
 //   int8         the softmax warps' issue slots, which the widening warps share: a scale into every score
 //                and one into every weight.  51% of all slots are used.  4 chunks
-//                of 300 to 1,024 tokens on 1k to 7k others and 2 single tokens: 191 us.
+//                of 300 to 1,024 tokens on 1k to 7k others and 2 single tokens: 185 us.
 #include "pa_launch.cuh"
 
 #include <cmath>
@@ -75,8 +75,9 @@ constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kProductWarp = 9, kTailWarp = 10
 constexpr int kHalf = 64;  // tokens of a softmax step
 constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
 // A running maximum is kept until a tile exceeds it by this factor (log2): until
-// then weights are at most 2^8, which bf16 and the fp32 sums hold as well as 1.
-constexpr float kSlack = 8.f;
+// then weights are at most 2^16, which bf16 and the fp32 sums hold as well as 1.  (With 2^8
+// a warp of int8 prompts rescaled in every fourth step: 192 us for 185.)
+constexpr float kSlack = 16.f;
 constexpr int kScaleSlots = 4;  // int8: tiles whose scales are in shared memory
 constexpr int kItemSlots = 4;   // items that the loads may be ahead
 
