@@ -170,9 +170,10 @@ __device__ __forceinline__ bool chunk_begin(const ChunkParams& p, ChunkItems* at
   int64_t total = 0;
   for (int b = 0; b < p.num_seqs; b += kThreads) total += scan(b, cta == 0);
   // A list that leaves CTAs without a range is cut finer: there, an item's costs are paid side by
-  // side.  (16 tokens on 1k: 23.6 -> 19.3 us; batches that fill the SMs take 2 to 20% longer so.)
-  if (at->item_units > 1 && chunk_ranges(total, gridDim.x, at->item_units) < (int)gridDim.x) {
-    at->item_units = 1;
+  // side.  (16 tokens on 1k: 23.6 -> 19.3 us; batches that fill the SMs take 2 to 20% longer so.  fp32, whose
+  // tiles take longest: 3 prompts of up to 200 tokens 44 -> 32; bf16 with nothing for an item, 19 -> 23.)
+  if (at->item_units > 0 && chunk_ranges(total, gridDim.x, at->item_units) < (int)gridDim.x) {
+    at->item_units = at->item_units > 1 ? 1 : 0;
     total = 0;
     for (int b = 0; b < p.num_seqs; b += kThreads) total += scan(b, false);
   }
@@ -232,16 +233,17 @@ __device__ __forceinline__ bool chunk_begin(const ChunkParams& p, ChunkItems* at
 }
 
 // ---------------------------------------------------------------------------
-// Join: the rows of the items that range boundaries cut, by log-sum-exp.  The blocks of
-// b have the item that CTA b's range begins inside of, if CTA b - 1's does not begin
-// inside of the same one.  With many rows (and few parts: the list is long, then) a warp
-// takes 32 of them, a lane each, and a slice of the dims, so that its loads lie side by side; with
-// few rows (and perhaps many parts) eight warps share a row, and a lane has four dims.
+// Join: the rows of the items that range boundaries cut, by log-sum-exp.  kJoinBlocks blocks
+// belong to every boundary, and those of an item's boundaries share its rows.  With many rows
+// a block (and few parts: the list is long, then) a warp takes 32 of them, a lane each, and a slice of
+// the dims, so that its loads lie side by side; with few (and perhaps many parts) eight warps share
+// a row, and a lane has four dims.  (16 tokens on 4k, 17 parts: 43 us with the first boundary's
+// blocks alone, 29 with all.)
 // ---------------------------------------------------------------------------
 constexpr int kJoinBlocks = 4, kSlice = 32;  // dims of a warp where there are many rows
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(256, 4) pa_prefill_join(const __grid_constant__ ChunkParams p) {
   constexpr int kLanes = D / 4;  // lanes that hold four dims (the others repeat them)
   const int lane = threadIdx.x & 31, dims = lane % kLanes, warp = threadIdx.x >> 5;
   const int b = blockIdx.x + 1, ctas = gridDim.x + 1;
@@ -250,14 +252,23 @@ __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ C
   const int4 cut = __ldcg(p.cuts + 2 * b), before = __ldcg(p.cuts + 2 * b - 2), item = __ldcg(p.cuts + 2 * b + 1);
   if (cut.x < 0 || cut.w == 0) return;  // no such range, or it begins with an item
   auto same = [&](const int4& o) { return o.x == cut.x && o.y == cut.y && o.z == cut.z && o.w != 0; };
-  if (same(before)) return;
-  int parts = 2;  // CTA b - 1's, b's and those behind that begin in the item, too
+  // The CTAs whose ranges begin in the item are first .. first + parts - 2.
+  int first = b, parts = 2;
+  if (same(before)) {
+    for (int i = b - 1;; i -= 32) {
+      const unsigned run = __ballot_sync(0xffffffffu, i - lane >= 1 && same(__ldcg(p.cuts + 2 * max(i - lane, 1))));
+      first -= __ffs(~run) == 0 ? 32 : __ffs(~run) - 1;
+      if (run != 0xffffffffu) break;
+    }
+  }
   for (int i = b + 1;; i += 32) {
     const bool more = i + lane < ctas && same(__ldcg(p.cuts + 2 * min(i + lane, ctas - 1)));
     const unsigned run = __ballot_sync(0xffffffffu, more);
     parts += __ffs(~run) == 0 ? 32 : __ffs(~run) - 1;
     if (run != 0xffffffffu) break;
   }
+  parts += b - first;
+  const int blocks = (parts - 1) * kJoinBlocks, block = (b - first) * kJoinBlocks + blockIdx.y;
   // (After a timeout of the kernel before the list may hold anything: stay inside.)
   const int tokens = item.y;
   if (cut.y < 0 || cut.y >= p.kv_heads || item.x < 0 || tokens < 0 || tokens > 2 * p.tile_tokens ||
@@ -266,13 +277,13 @@ __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ C
     return;
   }
   const int rows = tokens * p.group;
-  // Part k: CTA b - 1 + k, the first in its second slot, the others in their first.
-  auto slot = [&](int k) -> size_t { return (size_t)2 * (b - 1 + k) + (k == 0 ? 1 : 0); };
+  // Part k: CTA first - 1 + k, the first in its second slot, the others in their first.
+  auto slot = [&](int k) -> size_t { return (size_t)2 * (first - 1 + k) + (k == 0 ? 1 : 0); };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   const float4* po = reinterpret_cast<const float4*>(p.part_o);
-  if (rows > 8 * kJoinBlocks) {
+  if (rows > 8 * blocks) {
     constexpr int kSlices = D / kSlice;
-    for (int i = blockIdx.y * 8 + warp; i < 2 * (kChunkRows / 32) * kSlices; i += 8 * kJoinBlocks) {
+    for (int i = block * 8 + warp; i < 2 * (kChunkRows / 32) * kSlices; i += 8 * blocks) {
       const int d0 = (i % kSlices) * kSlice, r = (i / kSlices) * 32 + lane, tile = r / kChunkRows, in_tile = r % kChunkRows;
       const int t = in_tile / p.group, tok = tile * p.tile_tokens + t;
       const bool real = t < p.tile_tokens && tok < tokens;
@@ -317,7 +328,7 @@ __global__ void __launch_bounds__(256) pa_prefill_join(const __grid_constant__ C
     return;
   }
   __shared__ float shared_parts[8][6][32];
-  for (int i = blockIdx.y; i < rows; i += kJoinBlocks) {
+  for (int i = block; i < rows; i += blocks) {
     const int tok = i / p.group, g = i - tok * p.group;
     const int tile = tok >= p.tile_tokens ? 1 : 0;
     const int in_tile = (tok - tile * p.tile_tokens) * p.group + g;

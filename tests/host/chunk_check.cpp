@@ -106,7 +106,7 @@ int main() {
       const int context = rng() % 5 ? c.n + upto(0, ctx) : upto(0, c.n);
       c.old = context - c.n;
       c.tile_tokens = rows / group;
-      c.item = trial % 2 ? pa::kItemUnitsF32 : pa::kItemUnits;
+      c.item = trial % 4 == 3 ? 0 : trial % 2 ? pa::kItemUnitsF32 : pa::kItemUnits;
     }
     const int rc = check(seqs, heads, rng() % 2 ? 152 : upto(1, 400));
     if (rc) {
