@@ -125,9 +125,13 @@ size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, i
  * pa_decode_ws - pa_decode with caller-owned scratch (device memory of at
  * least pa_decode_workspace_size(...) bytes, 256-byte aligned).  Never
  * allocates.  The scratch must be zero-filled before its first use; every
- * call that completes leaves it zero-filled again, so it can be reused by the
- * next call on the same stream.  Two calls that overlap in time must not
- * share it.  After a call that reported PA_DEVERR_TIMEOUT, zero it again.
+ * call that completes leaves its first 16 KiB, where the merge tickets are, zero
+ * again, and no decode call writes anything else there.  So it can be reused by the
+ * next call on the same stream, of any shape and any of the pa_decode_ex,
+ * pa_decode_mq, pa_decode_fp8* and pa_decode_int8 forms, whatever workspace_bytes
+ * each of them gives (scratch "of any content", pa_decode_mod's for one, is a
+ * buffer of its own).  Two calls that overlap in time must not share it.
+ * After a call that reported PA_DEVERR_TIMEOUT, zero it again.
  */
 int pa_decode_ws(void* out, const void* query, const void* k_cache, const void* v_cache,
                  const int32_t* block_tables, const int32_t* context_lens, int num_seqs,

@@ -220,7 +220,8 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   if (rc != PA_OK) return rc;
   int32_t* counters = nullptr;
   ScratchHold hold;  // scratch of the library's own, until the launches are queued
-  const bool clear_tickets = workspace == nullptr && fixed_scratch != nullptr;
+  bool clear_tickets = workspace == nullptr && fixed_scratch != nullptr;
+  size_t partials = 0;  // where they begin
   if (extras != nullptr) {
     if ((long long)num_seqs * num_queries * num_heads > 1 << 30)
       return fail(PA_ERR_UNSUPPORTED, "pa_decode: %d sequences of %d rows", num_seqs, num_queries * num_heads);
@@ -240,21 +241,21 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   }
   if (extras != nullptr) {
   } else if (workspace == nullptr && int8 != nullptr) {
-    rc = hold.of_stream(pl.ws_partials, stream, &workspace, pl.ws_counters, &counters);
+    rc = hold.of_stream(pl.ws_partials, stream, &workspace, pl.ws_tickets, &counters);
     if (rc != PA_OK) return rc;
   } else if (workspace == nullptr) {
-    rc = hold.plain(pl.ws_partials, pl.ws_counters, stream, &workspace, &counters);
+    rc = hold.plain(pl.ws_partials, pl.ws_tickets, stream, &workspace, &counters);
     if (rc != PA_OK) return rc;
   } else {
     if (workspace_bytes < pl.ws_total)
       return fail(PA_ERR_WORKSPACE, "pa_decode: workspace of %zu bytes, %zu needed", workspace_bytes,
                   pl.ws_total);
     if (!aligned(workspace, 256)) return fail(PA_ERR_INVALID_ARG, "pa_decode: workspace not 256-byte aligned");
-    const size_t cnt_bytes = sizeof(int32_t) * (size_t)num_seqs * num_kv_heads;
-    counters = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) +
-                                          ((workspace_bytes - cnt_bytes) & ~(size_t)255));
+    counters = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) + pl.ws_late);
+    if (pl.ws_late != 0) clear_tickets = true;
+    partials = kTicketRoom;
   }
-  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  unsigned char* ws = static_cast<unsigned char*>(workspace) + partials;
   DecodeParams prm{};
   prm.out = out;
   prm.q = query;
@@ -333,8 +334,7 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (clear_tickets) {
-    const cudaError_t e =
-        cudaMemsetAsync(counters, 0, sizeof(int32_t) * (size_t)num_seqs * num_kv_heads, st);
+    const cudaError_t e = cudaMemsetAsync(counters, 0, pl.ws_tickets, st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(merge tickets)");
   }
   if (extras != nullptr && extras->walk == kWalkRest) {

@@ -6,6 +6,7 @@
 // the loads' latency and the copies of the scales: DRAM is at 58%, issue slots at 38%.
 #include "pa_chunk.cuh"
 #include "pa_decode_impl.h"
+#include "pa_plan.h"
 
 namespace pa {
 
@@ -31,8 +32,6 @@ bool runs_as_chunks(int num_queries, int num_heads, int num_kv_heads, int head_s
          (long long)num_kv_heads * head_size % kLine != 0;
 }
 
-size_t ticket_bytes(int num_seqs, int num_kv_heads) { return align_up(sizeof(int32_t) * (size_t)num_seqs * num_kv_heads, 256); }
-
 }  // namespace
 }  // namespace pa
 
@@ -44,8 +43,8 @@ extern "C" size_t pa_decode_int8_workspace_size(int num_seqs, int num_queries, i
     return 0;
   if (!runs_as_chunks(num_queries, num_heads, num_kv_heads, head_size))
     return decode_workspace_size_q(num_seqs, num_heads, num_kv_heads, head_size, num_ranges, num_queries);
-  const size_t chunks = pa_prefill_workspace_size(head_size);  // the bytes where other shapes keep their tickets stay as they are
-  return chunks == 0 ? 0 : chunks + ticket_bytes(num_seqs, num_kv_heads);
+  const size_t chunks = pa_prefill_workspace_size(head_size);  // behind the bytes where other shapes keep their tickets
+  return chunks == 0 ? 0 : kTicketRoom + chunks;
 }
 
 extern "C" int pa_decode_int8(void* out, const void* query, const void* k_cache, const void* v_cache,
@@ -69,10 +68,12 @@ extern "C" int pa_decode_int8(void* out, const void* query, const void* k_cache,
   if (rc != PA_OK) return rc;
   if (num_ranges < 0) return fail(PA_ERR_INVALID_ARG, "pa_decode_int8: num_ranges %d", num_ranges);
   if (runs_as_chunks(num_queries, num_heads, num_kv_heads, head_size)) {
-    const size_t tickets = ticket_bytes(num_seqs, num_kv_heads);
-    if (workspace != nullptr && workspace_bytes < tickets)
-      return fail(PA_ERR_WORKSPACE, "pa_decode_int8: workspace of %zu bytes", workspace_bytes);
-    c.workspace = workspace, c.workspace_bytes = workspace != nullptr ? workspace_bytes - tickets : 0;
+    if (workspace != nullptr) {
+      if (workspace_bytes < kTicketRoom)
+        return fail(PA_ERR_WORKSPACE, "pa_decode_int8: workspace of %zu bytes", workspace_bytes);
+      c.workspace = static_cast<unsigned char*>(workspace) + kTicketRoom;
+      c.workspace_bytes = workspace_bytes - kTicketRoom;
+    }
     return prefill_impl(c);
   }
   const TokenScales scales{k_scales, v_scales};

@@ -45,7 +45,7 @@
 //   * A sequence wholly inside the range is written to `out` directly.  A
 //     sequence cut by range boundaries leaves one (m, l, O) partial per range
 //     and KV head; the warp that writes the last of them (an atomic ticket per
-//     sequence and KV head, no waiting) then merges them all by log-sum-exp:
+//     cut sequence and KV head, no waiting) then merges them all by log-sum-exp:
 //     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  The ticket counters
 //     are reset by that warp, so the scratch is left zeroed for the next call.
 //   * Empty sequences get zero output rows (all their query rows) from the
@@ -96,7 +96,7 @@ struct DecodeParams {
   const void* v_cache;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  int32_t* counters;  // [num_seqs][num_kv_heads] merge tickets; zero between calls
+  int32_t* counters;  // [num_ranges - 1][num_kv_heads] merge tickets (of the sequence that a range's end cuts); zero between calls
   float* part_ml;   // [R][2][H][2]: (m in log2 units, l)
   float* part_o;    // [R][2][H][D]: un-normalised weighted V sums
   int32_t* error_flag;
@@ -2103,7 +2103,7 @@ __device__ void arrive_and_merge(const DecodeParams& p, int seq, int kv_head, in
   // Acquire: the warp holding the last ticket fences before the barrier that
   // releases its lanes to read the other partials.
   const int last = arrivals * (r1 - r0 + 1) - 1;
-  int* cnt = p.counters + (size_t)seq * p.num_kv_heads + kv_head;
+  int* cnt = p.counters + (size_t)r0 * p.num_kv_heads + kv_head;
   __syncwarp();
   int ticket = 0;
   if (lane == 0) {
@@ -2923,7 +2923,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
           }
         }
         const int slot = ((me.flags >> 2) & 3) - 1;
-        if (!in_place(me, x) || slot > 1 || (WALK == kWalkAll && slot >= 0 && (me.r0 < 0 || me.r0 > r || me.r1 < r || me.r1 >= R))) {
+        if (!in_place(me, x) || slot > 1 || (WALK == kWalkAll && slot >= 0 && (me.r0 < 0 || me.r0 > r || me.r1 < r || me.r1 >= R || me.r0 == me.r1))) {
           lost();
           break;
         }

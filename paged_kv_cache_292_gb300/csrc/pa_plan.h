@@ -13,7 +13,10 @@ struct Plan {
   int per_sm;  // CTAs per SM
   uint32_t row_bytes, pitch, q_bytes, stage_bytes, smem;
   uint32_t lines, box_rows, box_bytes;  // tensor-core paths (see DecodeParams)
-  size_t ws_ml, ws_o, ws_partials, ws_counters, ws_total;
+  size_t ws_ml, ws_o, ws_partials;  // places of the partials behind their start, and their bytes
+  size_t ws_tickets;                // bytes of the merge tickets
+  size_t ws_late;                   // where in a caller's buffer they are if kTicketRoom does not hold them (else 0)
+  size_t ws_total;                  // bytes of a caller's buffer
 };
 
 // The batch's shape as far as a plan depends on it.  elt: bytes of a pool element;
@@ -28,24 +31,38 @@ struct PlanShape {
   bool mma() const { return q_elt == 2; }
 };
 
-// Scratch layout: partial (m, l) and O at the start, then the merge tickets
-// (num_seqs * num_kv_heads int32).  In a caller's buffer the tickets occupy
-// its last bytes (rounded down to 256), so that buffers reused across batch
-// shapes keep tickets and partials apart.
+// A caller's buffer: the merge tickets in its first kTicketRoom bytes, then partial (m, l)
+// and O.  A ticket belongs to one KV head of the sequence that the end of a range cuts and
+// is found by that range, so that a batch has (R - 1) * num_kv_heads of them however
+// many sequences there are.  Their place depends on nothing else: whatever shapes share a
+// buffer, and whatever size each call gives for it, no partial lies where another call
+// has a ticket.  (By default R * num_kv_heads is at most 8 a CTA: 1,216 on 152 SMs.  More tickets than
+// the room holds, where num_ranges is in the hundreds, lie behind the call's own partials, and
+// are cleared before its launch.)
+// The size is the partials, a ticket for every sequence and KV head, as callers' own formulas have
+// it, and of the room what slot 1 of the last range, in which no sequence ends and nothing
+// is written, does not pay for: with 4,096 query elements a token and more, nothing.
+constexpr size_t kTicketRoom = 16384;
+
 inline size_t workspace_layout(int num_seqs, int num_heads, int num_kv_heads, int head_size, int R, Plan* pl,
                                int num_queries = 1) {
   num_heads *= num_queries;  // partial rows are (query, head) pairs
   const size_t ml = align_up(sizeof(float) * (size_t)R * 2 * num_heads * 2, 256);
   const size_t o = align_up(sizeof(float) * (size_t)R * 2 * num_heads * head_size, 256);
   const size_t cnt = align_up(sizeof(int32_t) * (size_t)num_seqs * num_kv_heads, 256);
+  const size_t tickets = align_up(sizeof(int32_t) * (size_t)(R - 1) * num_kv_heads, 256);
+  const size_t unused = sizeof(float) * (size_t)num_heads * head_size;  // (a multiple of 256)
+  const bool late = tickets > kTicketRoom;
+  const size_t total = ml + o + cnt + (kTicketRoom > unused ? kTicketRoom - unused : 0) + (late ? tickets : 0);
   if (pl) {
     pl->ws_ml = 0;
     pl->ws_o = ml;
     pl->ws_partials = ml + o;
-    pl->ws_counters = cnt;
-    pl->ws_total = ml + o + cnt;
+    pl->ws_tickets = tickets;
+    pl->ws_late = late ? kTicketRoom + ml + o - unused : 0;
+    pl->ws_total = total;
   }
-  return ml + o + cnt;
+  return total;
 }
 
 // KV heads one CTA stages per token row: the largest divisor of num_kv_heads
