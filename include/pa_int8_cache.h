@@ -86,8 +86,8 @@ int pa_read_cache_int8(void* k_out, void* v_out, const void* k_cache, const void
  * (query, head) columns per KV head, or head_size 64 with an odd num_kv_heads, run as
  * chunks do (pa_prefill_int8).
  * workspace    as in pa_decode_ws: at least pa_decode_int8_workspace_size(...) bytes,
- *              zero-filled before its first use and reusable as it is behind every call
- *              that completes, by other shapes, too; or NULL: the library's own, one buffer per stream, as in
+ *              zero-filled before its first use and reusable as it is behind every call,
+ *              by other shapes, too; or NULL: the library's own, one buffer per stream, as in
  *              pa_prefill (refused while `stream` is being captured)
  * num_ranges   as in pa_decode_ex (shapes that run as chunks: without effect)
  */

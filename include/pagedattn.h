@@ -125,13 +125,12 @@ size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, i
  * pa_decode_ws - pa_decode with caller-owned scratch (device memory of at
  * least pa_decode_workspace_size(...) bytes, 256-byte aligned).  Never
  * allocates.  The scratch must be zero-filled before its first use; every
- * call that completes leaves its first 16 KiB, where the merge tickets are, zero
- * again, and no decode call writes anything else there.  So it can be reused by the
+ * call leaves its first 16 KiB, where the merge tickets are, zero again, also one that
+ * reports PA_DEVERR_TIMEOUT, and no decode call writes anything else there.  So it can be reused by the
  * next call on the same stream, of any shape and any of the pa_decode_ex,
  * pa_decode_mq, pa_decode_fp8* and pa_decode_int8 forms, whatever workspace_bytes
  * each of them gives (scratch "of any content", pa_decode_mod's for one, is a
  * buffer of its own).  Two calls that overlap in time must not share it.
- * After a call that reported PA_DEVERR_TIMEOUT, zero it again.
  */
 int pa_decode_ws(void* out, const void* query, const void* k_cache, const void* v_cache,
                  const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
@@ -508,9 +507,8 @@ int pa_decode_fp8_mq_append(void* out, const void* query, const void* k_new, con
  * them the tiles of the walk behind the prefix; pa_decode_mod: the tiles its walk takes;
  * pa_prefill and pa_prefill_int8: tile `tile` of those that each CTA takes, in every CTA;
  * pa_prefill over fp32 pools has no waits and leaves the setting alone.)
- * That call's output is unspecified, and its scratch (pa_decode_ws) must be
- * zero-filled again before reuse.  The setting is used by one launch and then
- * cleared; tile = -1 clears it.  Returns PA_OK, or PA_ERR_INVALID_ARG for
+ * That call's output is unspecified; its scratch is fit for the next call.  The
+ * setting is used by one launch and then cleared; tile = -1 clears it.  Returns PA_OK, or PA_ERR_INVALID_ARG for
  * tile < -1.
  */
 int pa_test_stall_copy(long long tile, unsigned int wait_limit_us);

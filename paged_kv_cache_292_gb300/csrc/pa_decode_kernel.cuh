@@ -40,8 +40,9 @@
 //     (append_new_rows).  Not with several consumer warps per KV head, where
 //     that code slowed the consumers' tile loop: the host then writes the rows
 //     with a separate kernel ahead of the decode.
-//   * Every wait is bounded; a wait that runs out sets PA_DEVERR_TIMEOUT, and
-//     the producers let the copies they started land before the CTA retires.
+//   * Every wait is bounded; a wait that runs out sets PA_DEVERR_TIMEOUT, the
+//     producers let the copies they started land before the CTA retires, and the
+//     consumers take the tickets that they owe (give_up_tickets).
 //   * A sequence wholly inside the range is written to `out` directly.  A
 //     sequence cut by range boundaries leaves one (m, l, O) partial per range
 //     and KV head; the warp that writes the last of them (an atomic ticket per
@@ -2196,6 +2197,40 @@ __device__ void arrive_and_merge(const DecodeParams& p, int seq, int kv_head, in
   if (lane == 0) *cnt = 0;  // leave the counter zeroed for the next call
 }
 
+// A consumer warp that leaves the range [a, b) at tile x, before its end, still takes the
+// tickets of the cut sequences that it has not finished (the range's first one if x is
+// in it, and its last): with them every ticket gets all of its arrivals, and is back
+// at zero when the call is over.  The call's output is unspecified then, as its error flag says.
+template <int WALK>
+__device__ __noinline__ void give_up_tickets(const DecodeParams& p, const long long* found, int r, long long x,
+                                             int kv_head, int lane, int arrivals) {
+  const int s = static_cast<int>(found[0]), S = p.num_seqs;
+  const long long first = found[1], total = found[3], ranges = found[4];
+  const long long a = range_start(r, total, ranges), b = range_start(r + 1, total, ranges);
+  auto take = [&](long long lo, long long hi) {  // of a sequence of tiles lo .. hi - 1
+    if (lane != 0 || segment_slot(a, b, lo, hi) < 0) return;
+    const int r0 = static_cast<int>(range_of_tile(lo, total, ranges));
+    const int r1 = static_cast<int>(range_of_tile(hi - 1, total, ranges));
+    int* cnt = p.counters + (size_t)r0 * p.num_kv_heads + kv_head;
+    if (atomicAdd(cnt, 1) == arrivals * (r1 - r0 + 1) - 1) *cnt = 0;
+  };
+  long long at = first + SeqWalk<WALK>(p, s, false).n;
+  if (x < at) take(first, at);
+  if (at >= b) return;
+  for (int base = s + 1; base < S; base += 32) {
+    const long long n = base + lane < S ? SeqWalk<WALK>(p, base + lane, false).n : 0;
+    const long long hi = at + warp_incl_scan_ll(n, lane);
+    const unsigned holds = __ballot_sync(0xffffffffu, hi - n < b && b <= hi);
+    if (holds != 0) {
+      const int from = __ffs(holds) - 1;
+      const long long last = __shfl_sync(0xffffffffu, hi, from);
+      take(last - __shfl_sync(0xffffffffu, n, from), last);
+      return;
+    }
+    at = __shfl_sync(0xffffffffu, hi, 31);
+  }
+}
+
 // One row of a cut sequence (kCutMerge), its partials added by log-sum-exp by a
 // warp: lane i holds dims [i * D / 32, (i + 1) * D / 32).  The maxima and sums of up
 // to 32 partials are read at once, one per lane, so that the loads of their O
@@ -2471,6 +2506,8 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
       mbar_init(qempty_bar(i), NCW);
     }
     *abort_flag = 0;
+    misc[35] = total;  // (give_up_tickets)
+    misc[36] = Reff;
     mbar_init_fence();
   }
   __syncthreads();
@@ -2773,7 +2810,8 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
     auto tile_mask = [](int nvalid) -> uint32_t {
       return kMod ? (uint32_t)nvalid : nvalid < kTile ? (1u << nvalid) - 1u : 0xffffu;
     };
-    for (long long x = a; x < b; ++x) {
+    long long x = a;
+    for (; x < b; ++x) {
       if (!mbar_wait_warp(full_bar(st), ph, p.wait_limit_ns)) {
         timed_out();
         break;
@@ -2948,6 +2986,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
         ph ^= 1u;
       }
     }
+    if (WALK == kWalkAll && x < b) give_up_tickets<WALK>(p, misc + 32, r, x, kv_head, lane, kSplit);
     named_barrier_sync(1, nthreads);  // lets the producers drain their copies after a timeout
   }
   if (WALK == kWalkRest && p.beside) griddep_wait();

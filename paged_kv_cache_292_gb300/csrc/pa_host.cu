@@ -117,7 +117,7 @@ int ScratchHold::plain(size_t bytes, size_t counter_bytes, void* stream, void** 
     void* p = nullptr;
     e = cudaMalloc(&p, want);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(tickets)");
-    // Merge tickets start at zero; every completed decode leaves them zero.
+    // Merge tickets start at zero; every decode leaves them zero, a timed-out one too.
     e = cudaMemset(p, 0, want);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
