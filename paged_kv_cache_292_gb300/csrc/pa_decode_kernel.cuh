@@ -2197,13 +2197,15 @@ __device__ void arrive_and_merge(const DecodeParams& p, int seq, int kv_head, in
   if (lane == 0) *cnt = 0;  // leave the counter zeroed for the next call
 }
 
-// A consumer warp that leaves the range [a, b) at tile x, before its end, still takes the
-// tickets of the cut sequences that it has not finished (the range's first one if x is
-// in it, and its last): with them every ticket gets all of its arrivals, and is back
-// at zero when the call is over.  The call's output is unspecified then, as its error flag says.
+// A consumer warp that left its range before the end still takes the tickets of the cut
+// sequences that it has not finished (`taken`: bit 0 the range's first one, in slot 0,
+// bit 1 its last, in slot 1): with them every ticket gets all of its arrivals, and is back at
+// zero when the call is over.  The call's output is unspecified then, as its error flag says.
+// (By what the warp left in shared memory: with its place in a register until then 8 int8
+// contexts of 32k took 107.4 us for 106.8.)
 template <int WALK>
-__device__ __noinline__ void give_up_tickets(const DecodeParams& p, const long long* found, int r, long long x,
-                                             int kv_head, int lane, int arrivals) {
+__device__ __forceinline__ void give_up_tickets(const DecodeParams& p, const long long* found, int r, int taken,
+                                                int kv_head, int lane, int arrivals) {
   const int s = static_cast<int>(found[0]), S = p.num_seqs;
   const long long first = found[1], total = found[3], ranges = found[4];
   const long long a = range_start(r, total, ranges), b = range_start(r + 1, total, ranges);
@@ -2215,8 +2217,8 @@ __device__ __noinline__ void give_up_tickets(const DecodeParams& p, const long l
     if (atomicAdd(cnt, 1) == arrivals * (r1 - r0 + 1) - 1) *cnt = 0;
   };
   long long at = first + SeqWalk<WALK>(p, s, false).n;
-  if (x < at) take(first, at);
-  if (at >= b) return;
+  if ((taken & 1) == 0) take(first, at);
+  if (at >= b || (taken & 2) != 0) return;
   for (int base = s + 1; base < S; base += 32) {
     const long long n = base + lane < S ? SeqWalk<WALK>(p, base + lane, false).n : 0;
     const long long hi = at + warp_incl_scan_ll(n, lane);
@@ -2229,6 +2231,14 @@ __device__ __noinline__ void give_up_tickets(const DecodeParams& p, const long l
     }
     at = __shfl_sync(0xffffffffu, hi, 31);
   }
+}
+// As a call, for consumers at the register cap: 64 sequences x 4 queries of 32 heads on 8 take 111.2 us
+// so, 113.4 with it written out; the others are faster without one (2 queries over int8 pools
+// 70.2 for 71.6).
+template <int WALK>
+__device__ __noinline__ void give_up_tickets_call(const DecodeParams& p, const long long* found, int r, int taken,
+                                                  int kv_head, int lane, int arrivals) {
+  give_up_tickets<WALK>(p, found, r, taken, kv_head, lane, arrivals);
 }
 
 // One row of a cut sequence (kCutMerge), its partials added by log-sum-exp by a
@@ -2508,6 +2518,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
     *abort_flag = 0;
     misc[35] = total;  // (give_up_tickets)
     misc[36] = Reff;
+    misc[37] = misc[38] = 0;
     mbar_init_fence();
   }
   __syncthreads();
@@ -2810,8 +2821,7 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
     auto tile_mask = [](int nvalid) -> uint32_t {
       return kMod ? (uint32_t)nvalid : nvalid < kTile ? (1u << nvalid) - 1u : 0xffffu;
     };
-    long long x = a;
-    for (; x < b; ++x) {
+    for (long long x = a; x < b; ++x) {
       if (!mbar_wait_warp(full_bar(st), ph, p.wait_limit_ns)) {
         timed_out();
         break;
@@ -2969,9 +2979,11 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
           cons.template finish<true>(p, me.seq, kv_head, slot, r, lane);
         else
           cons.finish(p, me.seq, kv_head, slot, r, lane);
-        if (WALK == kWalkAll && slot >= 0)
+        if (WALK == kWalkAll && slot >= 0) {
+          if (lane == 0) reinterpret_cast<unsigned char*>(misc + 37)[warp] |= 1u << slot;
           arrive_and_merge<T, D, (QMODE > 0)>(p, me.seq, kv_head, me.r0, me.r1, (me.flags >> 4) & 1, lane,
                                               kSplit);
+        }
         // Split-column kernels sit at the register cap: writing the state here
         // (the next segment's begin_segment rewrites it anyway) frees its
         // registers for the merge above.
@@ -2986,8 +2998,14 @@ __global__ void __launch_bounds__(max_threads<T, D, QMODE, WALK>(), 1)
         ph ^= 1u;
       }
     }
-    if (WALK == kWalkAll && x < b) give_up_tickets<WALK>(p, misc + 32, r, x, kv_head, lane, kSplit);
     named_barrier_sync(1, nthreads);  // lets the producers drain their copies after a timeout
+    if (WALK == kWalkAll && *abort_flag != 0) {
+      const int taken = reinterpret_cast<unsigned char*>(misc + 37)[warp];
+      if constexpr (QMODE == 2)
+        give_up_tickets_call<WALK>(p, misc + 32, r, taken, kv_head, lane, kSplit);
+      else
+        give_up_tickets<WALK>(p, misc + 32, r, taken, kv_head, lane, kSplit);
+    }
   }
   if (WALK == kWalkRest && p.beside) griddep_wait();
   (void)Hk;
