@@ -82,7 +82,8 @@ int pa_read_cache_int8(void* k_out, void* v_out, const void* k_cache, const void
  * of pa_prefill_int8.  As in pa_decode_fp8_mq the query is rounded to f16 (exact
  * for |q| in [2^-14, 65504]) and so are the softmax weights times V's scales: off by
  * at most 2^-11 of themselves or 2^-38 of the largest weight times the largest scale,
- * whichever is more.  More than 32
+ * whichever is more.  A row is finite as long as the sum of its weights (the largest counted as
+ * 1) times |v| is, whatever the values.  More than 32
  * (query, head) columns per KV head, or head_size 64 with an odd num_kv_heads, run as
  * chunks do (pa_prefill_int8).
  * workspace    as in pa_decode_ws: at least pa_decode_int8_workspace_size(...) bytes,

@@ -1471,10 +1471,18 @@ struct MmaConsumerF8 {
     const int g = lane >> 2;
     const float v_scale = I8 ? 1.f : p.v_scale;
     if constexpr (I8) {
+      // The unit may be near the largest number and the weights count 2^14 times: with both a row's
+      // sums and those of its weights 2^14 times smaller (here and in every other partial) a row
+      // stays finite as long as the sum of its weights of at most 1 times |v| does, as over other pools.
+      constexpr float kDown = 0x1p-14f;
+      static_assert(kF16Up == 14.f, "the weights' factor");
+      const float by = unit * kDown;
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[mt][i] *= unit;
+        for (int i = 0; i < 4; ++i) acc[mt][i] *= by;
+      la *= kDown;
+      lb *= kDown;
     }
     if constexpr (!MQ) {
       const int ha = 2 * (lane & 3), hb = ha + 1;

@@ -1,0 +1,60 @@
+"""Values near the largest number: rows whose weighted sum of |v| is finite stay finite and right."""
+
+import pytest
+import torch
+
+from paged_kv_cache_292_gb300 import binding
+
+from chunklib import Chunks
+
+pytestmark = pytest.mark.gpu
+
+LARGEST = 3.3e38
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_cache_292_gb300 import build
+
+    build.build()
+    binding.load()
+
+
+def _enlarge(b, room):
+    """V of an int8 or bf16 batch times a power of two, so that no value exceeds LARGEST / room."""
+    largest = 127 * float(torch.nan_to_num(b.scales[1]).max()) if b.pool == "int8" else float(torch.nan_to_num(b.cache[1]).abs().max())
+    times = 2.0 ** int(torch.tensor(LARGEST / room / largest, dtype=torch.float64).log2().floor())
+    held = b.scales if b.pool == "int8" else b.cache
+    held[1] = (held[1].double() * times).to(held[1].dtype)
+    values = torch.nan_to_num(torch.from_numpy(b.values()[1])).abs().max()
+    assert LARGEST / room / 2 < float(values) <= LARGEST / room
+    return b
+
+
+def _decode(b, Q, **kw):
+    q, k, v, ks, vs, tables, lens, _, scale = b.gpu()
+    S = len(b.ctx)
+    q = q.view(S, Q, b.heads, b.D) if Q > 1 else q.view(S, b.heads, b.D)
+    return binding.decode_int8(q, k, v, ks, vs, tables, lens, scale, **kw).view(-1, b.heads, b.D)
+
+
+@pytest.mark.parametrize("Q", [1, 2, 7])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx, num_ranges", [([20, 300, 1, 64], 1), ([20, 300, 1, 64], 0), ([5000, 33], 0)])
+def test_decode_int8(Q, D, ctx, num_ranges):
+    """Whole rows and merged ones.  (The sum over c tokens of weights of at most 1 times |v| is below c * max |v|.)"""
+    b = Chunks([Q] * len(ctx), [max(c - Q, 0) for c in ctx], "int8", 8, 2, D, gap=0)
+    _enlarge(b, int(b.ctx.max()) + 1)
+    b.compare(_decode(b, Q, num_ranges=num_ranges), "large values")
+
+
+@pytest.mark.parametrize("Q", [1, 3])
+@pytest.mark.parametrize("times", [2.0**-60, 2.0**-90])
+def test_decode_int8_of_small_values(Q, times):
+    b = Chunks([Q] * 3, [40, 17, 3000], "int8", 8, 2, 128, gap=0)
+    b.scales[1] *= times
+    got = _decode(b, Q)
+    want, spread, reach = b.want()
+    b.compare((got.double() / times).to(torch.bfloat16), "small values", (want / times, spread / times, reach))
