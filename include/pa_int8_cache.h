@@ -73,7 +73,8 @@ int pa_read_cache_int8(void* k_out, void* v_out, const void* k_cache, const void
  * pa_prefill_int8 - pa_prefill over the int8 pools; query and out bf16.  Codes
  * enter both products exactly (as bf16 integers), K's scales multiply the scores
  * and V's the weights in fp32, and the products weight * scale are rounded to bf16
- * (at most 2^-8 of themselves).  A token whose scale is NaN makes the rows that see it NaN, and
+ * (at most 2^-8 of themselves, as long as V's scale is above 2^-110: a weight may
+ * enter as 2^-16 of itself, and bf16 ends at 2^-126).  A token whose scale is NaN makes the rows that see it NaN, and
  * no others.  num_physical_blocks > 0 is required.  Other arguments, scratch
  * and limits as in pa_prefill.
  *

@@ -5,7 +5,10 @@
 // per KV head and tile of 128 tokens, S = Q K^T and O += P V with the running
 // statistics of a softmax between them (s in log2 units):
 //
-//   m_r = max_t s_rt, l_r = sum_t 2^(s_rt - m_r), O_r = sum_t 2^(s_rt - m_r) v_t
+//   l_r = sum_t 2^(s_rt - m_r), O_r = sum_t 2^(s_rt - m_r) v_t, out_r = O_r / l_r
+//
+// for any m_r that no s_rt exceeds: here the maximum over the tiles up to some one, plus 16
+// (kSlack), and a later one's where that falls short.
 //
 // int8 pools: k_t = ks_t * codes, v_t = vs_t * codes.  The codes go through the
 // products as they are (every integer up to 256 is a bf16 number), s_rt is
@@ -74,9 +77,10 @@ __device__ __forceinline__ uint32_t unit_at(int r, int u) {
 constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kProductWarp = 9, kTailWarp = 10, kWidenWarp = 12, kWidenWarps = 4;
 constexpr int kHalf = 64;  // tokens of a softmax step
 constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows x 64 bf16
-// A running maximum is kept until a tile exceeds it by this factor (log2): until
-// then weights are at most 2^16, which bf16 and the fp32 sums hold as well as 1.  (With 2^8
-// a warp of int8 prompts rescaled in every fourth step: 192 us for 185.)
+// A running maximum is kept until a tile exceeds it by this factor (log2), and weights count
+// 2^-16 at the maximum, so that none is above 1 meanwhile: no weight times a value, and no sum of
+// them, is larger than by the definition.  bf16 and fp32 hold them as well as 1, down to 2^-110
+// of the maximum's.  (With 2^8 a warp of int8 prompts rescaled in every fourth step: 192 us for 185.)
 constexpr float kSlack = 16.f;
 constexpr int kScaleSlots = 4;  // int8: tiles whose scales are in shared memory
 constexpr int kItemSlots = 4;   // items that the loads may be ahead
@@ -326,7 +330,7 @@ __global__ void __launch_bounds__(ChunkWarps<I8>::kThreads, 1) pa_prefill_kernel
             }
           }
         }
-        const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
+        const float neg = m == -INFINITY ? 0.f : fmaf(-m, p.scale_log2, -kSlack);
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), neg2 = pair(neg, neg);
         uint64_t sum[2] = {0ull, 0ull};
         // The weights enter the product as bf16: half a step, 2^-8 at most, both
