@@ -15,13 +15,15 @@ def lib():
     return binding.load()
 
 
-def test_layout_host_check(tmp_path):
-    """Partials of no shape reach another's merge tickets, and everything stays inside the size handed out."""
+@pytest.mark.parametrize("check", ["workspace_check", "scaled_plan_check"])
+def test_host_check(tmp_path, check):
+    """Partials of no shape reach another's merge tickets, everything stays inside the size handed out; plans over int8
+    pools hold their scales."""
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    exe = tmp_path / "workspace_check"
+    exe = tmp_path / check
     subprocess.run(["g++", "-O2", "-std=c++17", "-I" + os.path.join(root, "paged_kv_cache_292_gb300", "csrc"),
                     "-I" + os.path.join(root, "tests", "host", "fake"),
-                    os.path.join(root, "tests", "host", "workspace_check.cpp"), "-o", str(exe)], check=True)
+                    os.path.join(root, "tests", "host", check + ".cpp"), "-o", str(exe)], check=True)
     out = subprocess.run([str(exe)], capture_output=True, text=True)
     assert out.returncode == 0, out.stdout + out.stderr
     assert out.stdout.startswith("ok")
