@@ -11,11 +11,18 @@
  *   integer, ties to even, decided as in exact arithmetic     value = code * scale
  *
  * A row of zeros has scale 0.  A row that holds an infinity or NaN has scale
- * NaN and codes 0: all of it reads as NaN.
+ * NaN and codes 0: all of it reads as NaN.  (A row with the largest float32 itself
+ * has a scale that was rounded up: code 127 reads as an infinity there.)
  *
  * k_cache, v_cache    int8 [num_physical_blocks, block_size, num_kv_heads, head_size]
  * k_scales, v_scales  float [num_physical_blocks, num_kv_heads, block_size]: a
- *                     block's scales of one head side by side
+ *                     block's scales of one head side by side.  Attention wants them
+ *                     16-byte aligned (PA_ERR_INVALID_ARG), writing and reading back
+ *                     4-byte: allocate them 16-byte aligned.
+ *
+ * Copy-on-write of a forked sequence's block (pa_bm_append): pa_copy_blocks copies
+ * bits, so the pools go through it as PA_BF16 with half the head_size, the scales as
+ * PA_F32 with head_size 1 (block_size * num_kv_heads a multiple of 4 there).
  *
  * Conventions are those of pagedattn.h and pa_prefill.h.
  */
@@ -74,7 +81,7 @@ int pa_read_cache_int8(void* k_out, void* v_out, const void* k_cache, const void
  * enter both products exactly (as bf16 integers), K's scales multiply the scores
  * and V's the weights in fp32, and the products weight * scale are rounded to bf16
  * (at most 2^-8 of themselves, as long as V's scale is above 2^-110: a weight may
- * enter as 2^-16 of itself, and bf16 ends at 2^-126).  A token whose scale is NaN makes the rows that see it NaN, and
+ * enter as 2^-16 of itself, and bf16 ends at 2^-126; rows that pa_prefill carries in two parts: 2^-16).  A token whose scale is NaN makes the rows that see it NaN, and
  * no others.  num_physical_blocks > 0 is required.  Other arguments, scratch
  * and limits as in pa_prefill.
  *
