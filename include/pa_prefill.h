@@ -49,9 +49,12 @@ extern "C" {
  * Types: PA_BF16 or PA_F32.  num_heads / num_kv_heads <= 8, head_size 64 or 128,
  * block_size 1 .. 4096 (multiples of 8 stream fastest), num_tokens *
  * num_heads < 2^31.  bf16: the softmax weights enter the second product rounded to
- * bf16 (at most 2^-8 of themselves), the sums keep them in fp32; weights under 2^-110
- * of a row's largest (fp32 pools: 2^-126) may count as zero.  A row is finite as long
- * as the sum of its weights (the largest counted as 1) times |v| is.
+ * bf16 (at most 2^-8 of themselves), the sums keep them in fp32.  A chunk's tokens go
+ * in tiles of t = 128 / (num_heads / num_kv_heads), two at a time; a tile that is left
+ * alone (all of a chunk of at most t tokens, a decode for one) carries the weights in two
+ * bf16 parts, 2^-16 together.  So a token's rounding depends on the chunk that it comes in.
+ * Weights under 2^-110 of a row's largest (fp32 pools: 2^-126) may count as zero.  A row
+ * is finite as long as the sum of its weights (the largest counted as 1) times |v| is.
  * num_physical_blocks > 0: block ids are checked against it, and tokens of a
  * bad one are unspecified; 0: as in pa_decode_ex.
  * workspace    256-byte aligned device scratch of at least

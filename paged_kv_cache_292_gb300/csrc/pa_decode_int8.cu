@@ -2,8 +2,9 @@
 // f16 and the tokens' scales beside them in every stage; shapes that it does not take run as
 // chunks (pa_prefill.cu).  Integers up to 127 are f16 numbers; scores and weights take the
 // scales in fp32.  64 sequences of 512 to 4,096: 64.5 us (217 as chunks, whose 128 rows one token hardly
-// fills), 4.8 TB/s of codes and scales; 8 of 32k: 106 us (292), 5.1 TB/s.  What bounds it are
-// the loads' latency and the copies of the scales: DRAM is at 58%, issue slots at 38%.
+// fills), 4.8 TB/s of codes and scales; 8 of 32k: 106 us (292), 5.1 TB/s.  DRAM is at 58%
+// and issue slots at 38%: the copies' latency, and start and end of the launch.  Without the
+// scales' copies, 3% of the bytes, 61.7 and 100 us.
 #include "pa_chunk.cuh"
 #include "pa_decode_impl.h"
 #include "pa_plan.h"

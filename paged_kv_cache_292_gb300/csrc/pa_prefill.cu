@@ -38,8 +38,8 @@
 //                679 us, 1.42 PFLOP/s of the products that the mask leaves.  A tile and its two row
 //                tiles need 2,050 clocks of it if S has N = 128, but S in halves of 64 tokens reads
 //                its query operand twice as often and takes 1.5 times as long: 2,930 with the
-//                commits, which is what the kernel's tiles take.  N = 128 would need both score
-//                buffers at once, and the softmax and the products would take turns.
+//                commits, which is what the kernel's tiles take.  (S with N = 128 in one buffer a
+//                group, a group's softmax under the other's products: not tried.)
 //   short items  what an item costs besides its tiles, about 10,000 clocks: first scores, last product,
 //                rows out, much of it instruction fetches (0.85 stalls for an instruction per issue,
 //                0.53 in long chunks).  7 prompts of 33 to 2,047 tokens: 95 us, 0.68 PFLOP/s; 19

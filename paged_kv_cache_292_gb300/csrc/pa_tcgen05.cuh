@@ -112,10 +112,9 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-// The same products issued by a converged warp for its one thread with `elected` set: the
-// operands, warp-uniform, then come from uniform registers.  (Issued inside a branch of that thread
-// they are moved there one by one, which takes longer than the product.)  Shared-memory
-// operands in two words: the lower has the address and the bytes from one 64-element panel
+// The same products issued by a converged warp, with warp-uniform operands, for its one thread
+// with `elected` set.  (Issued inside a branch of that thread every product took about 100
+// clocks.)  Shared-memory operands in two words: the lower has the address and the bytes from one 64-element panel
 // to the next, the upper those from one group of 8 rows to the next.
 __device__ __forceinline__ uint32_t smem_operand_low(uint32_t addr, uint32_t panel) {
   return ((addr & 0x3ffffu) >> 4) | ((panel >> 4) << 16);
