@@ -58,8 +58,9 @@ extern "C" {
  * num_physical_blocks > 0: block ids are checked against it, and tokens of a
  * bad one are unspecified; 0: as in pa_decode_ex.
  * workspace    256-byte aligned device scratch of at least
- *              pa_prefill_workspace_size(...) bytes, of any content; two calls
- *              that may overlap in time must not share it.  NULL: the library's
+ *              pa_prefill_workspace_size(...) bytes, of any content (the first
+ *              16 KiB are left alone: see pa_decode_ws); two calls that may
+ *              overlap in time must not share it.  NULL: the library's
  *              own, one buffer per stream, as in pa_decode_mod (refused while
  *              `stream` is being captured).
  * The call makes two launches: the attention, whose list of (row tile, token

@@ -125,12 +125,12 @@ size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, i
  * pa_decode_ws - pa_decode with caller-owned scratch (device memory of at
  * least pa_decode_workspace_size(...) bytes, 256-byte aligned).  Never
  * allocates.  The scratch must be zero-filled before its first use; every
- * call leaves its first 16 KiB, where the merge tickets are, zero again, also one that
- * reports PA_DEVERR_TIMEOUT, and no decode call writes anything else there.  So it can be reused by the
- * next call on the same stream, of any shape and any of the pa_decode_ex,
- * pa_decode_mq, pa_decode_fp8* and pa_decode_int8 forms, whatever workspace_bytes
- * each of them gives (scratch "of any content", pa_decode_mod's for one, is a
- * buffer of its own).  Two calls that overlap in time must not share it.
+ * call leaves its first 16 KiB, where the merge tickets are, zero again, also one
+ * that reports PA_DEVERR_TIMEOUT, and no call of this library writes anything else
+ * there.  So it can be reused by the next call on the same stream, of any shape and
+ * any entry point (also those that take scratch of any content, pa_decode_mod for
+ * one), whatever workspace_bytes each of them gives.  Two calls that overlap in time
+ * must not share it.
  */
 int pa_decode_ws(void* out, const void* query, const void* k_cache, const void* v_cache,
                  const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
@@ -268,8 +268,9 @@ int pa_decode_mq_append(void* out, const void* query, const void* k_new, const v
  * Types: PA_F32 (num_queries == 1) or PA_BF16; (num_heads / num_kv_heads) *
  * num_queries <= 32.
  * workspace    256-byte aligned device scratch of at least
- *              pa_decode_mod_workspace_size(...) bytes, of any content; two calls
- *              that may overlap in time must not share it.  NULL: the library's
+ *              pa_decode_mod_workspace_size(...) bytes, of any content (the first
+ *              16 KiB are left alone: see pa_decode_ws); two calls that may
+ *              overlap in time must not share it.  NULL: the library's
  *              own, one buffer per stream, refused while `stream` is being
  *              captured (PA_ERR_INVALID_ARG).  It is allocated at a stream's first
  *              call and when a batch outgrows it; those calls, and a first call

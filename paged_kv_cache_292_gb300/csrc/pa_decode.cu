@@ -226,11 +226,13 @@ int decode_impl_q(void* out, const void* query, const void* k_cache, const void*
     if ((long long)num_seqs * num_queries * num_heads > 1 << 30)
       return fail(PA_ERR_UNSUPPORTED, "pa_decode: %d sequences of %d rows", num_seqs, num_queries * num_heads);
     const size_t need = walk_bytes(num_seqs, num_heads, num_kv_heads, head_size, pl.R, num_queries);
+    // (The rest behind a shared prefix gets a part of that call's buffer.)
+    if (extras->walk != kWalkRest && workspace != nullptr) partials = kTicketRoom;
     if (workspace == nullptr) {
       rc = hold.of_stream(need, stream, &workspace);
       if (rc != PA_OK) return rc;
-    } else if (workspace_bytes < need) {
-      return fail(PA_ERR_WORKSPACE, "pa_decode: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    } else if (workspace_bytes < partials + need) {
+      return fail(PA_ERR_WORKSPACE, "pa_decode: workspace of %zu bytes, %zu needed", workspace_bytes, partials + need);
     } else if (!aligned(workspace, 256)) {
       return fail(PA_ERR_INVALID_ARG, "pa_decode: workspace not 256-byte aligned");
     }

@@ -7,7 +7,6 @@
 // scales' copies, 3% of the bytes, 61.7 and 100 us.
 #include "pa_chunk.cuh"
 #include "pa_decode_impl.h"
-#include "pa_plan.h"
 
 namespace pa {
 
@@ -44,8 +43,7 @@ extern "C" size_t pa_decode_int8_workspace_size(int num_seqs, int num_queries, i
     return 0;
   if (!runs_as_chunks(num_queries, num_heads, num_kv_heads, head_size))
     return decode_workspace_size_q(num_seqs, num_heads, num_kv_heads, head_size, num_ranges, num_queries);
-  const size_t chunks = pa_prefill_workspace_size(head_size);  // behind the bytes where other shapes keep their tickets
-  return chunks == 0 ? 0 : kTicketRoom + chunks;
+  return pa_prefill_workspace_size(head_size);
 }
 
 extern "C" int pa_decode_int8(void* out, const void* query, const void* k_cache, const void* v_cache,
@@ -69,12 +67,7 @@ extern "C" int pa_decode_int8(void* out, const void* query, const void* k_cache,
   if (rc != PA_OK) return rc;
   if (num_ranges < 0) return fail(PA_ERR_INVALID_ARG, "pa_decode_int8: num_ranges %d", num_ranges);
   if (runs_as_chunks(num_queries, num_heads, num_kv_heads, head_size)) {
-    if (workspace != nullptr) {
-      if (workspace_bytes < kTicketRoom)
-        return fail(PA_ERR_WORKSPACE, "pa_decode_int8: workspace of %zu bytes", workspace_bytes);
-      c.workspace = static_cast<unsigned char*>(workspace) + kTicketRoom;
-      c.workspace_bytes = workspace_bytes - kTicketRoom;
-    }
+    c.workspace = workspace, c.workspace_bytes = workspace_bytes;
     return prefill_impl(c);
   }
   const TokenScales scales{k_scales, v_scales};

@@ -201,6 +201,7 @@ extern "C" int pa_decode_fp8_mod(void* out, const void* query, const void* k_cac
 extern "C" size_t pa_decode_mod_workspace_size(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
                                                int head_size, int kv_dtype, int num_ranges) {
   if (kv_dtype != PA_F32 && kv_dtype != PA_BF16 && kv_dtype != PA_FP8_E4M3) return 0;
-  return pa::walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, num_ranges, num_queries,
-                                 kv_dtype == PA_F32 ? 4 : kv_dtype == PA_BF16 ? 2 : 1);
+  const size_t walk = pa::walk_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, num_ranges, num_queries,
+                                              kv_dtype == PA_F32 ? 4 : kv_dtype == PA_BF16 ? 2 : 1);
+  return walk == 0 ? 0 : pa::kTicketRoom + walk;
 }

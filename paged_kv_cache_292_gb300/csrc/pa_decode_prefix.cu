@@ -865,7 +865,8 @@ extern "C" size_t pa_decode_prefix_workspace_size(int num_seqs, int num_queries,
   DeviceInfo dev{};
   if (walk == 0 || current_device_info(&dev) != PA_OK) return 0;
   const int items = count_items(num_seqs, num_queries, num_heads, num_kv_heads);
-  return prefix_scratch(num_seqs, num_queries, num_heads, head_size, dev.sm_count + items, items, walk).total;
+  return kTicketRoom +
+         prefix_scratch(num_seqs, num_queries, num_heads, head_size, dev.sm_count + items, items, walk).total;
 }
 
 namespace pa {
@@ -938,11 +939,12 @@ int prefix_impl(void* out, const void* query, const void* k_cache, const void* v
     rc = hold.of_stream(sc.total, stream, &workspace);
     if (rc != PA_OK) return rc;
   } else {
-    if (workspace_bytes < sc.total)
+    if (workspace_bytes < kTicketRoom + sc.total)
       return fail(PA_ERR_WORKSPACE, "pa_decode_prefix: workspace of %zu bytes, %zu needed", workspace_bytes,
-                  sc.total);
+                  kTicketRoom + sc.total);
     if (!aligned(workspace, 256))
       return fail(PA_ERR_INVALID_ARG, "pa_decode_prefix: workspace not 256-byte aligned");
+    workspace = static_cast<unsigned char*>(workspace) + kTicketRoom;
   }
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

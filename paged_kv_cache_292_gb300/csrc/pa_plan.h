@@ -36,9 +36,10 @@ struct PlanShape {
 // is found by that range, so that a batch has (R - 1) * num_kv_heads of them however
 // many sequences there are.  Their place depends on nothing else: whatever shapes share a
 // buffer, and whatever size each call gives for it, no partial lies where another call
-// has a ticket.  (By default R * num_kv_heads is at most 8 a CTA: 1,216 on 152 SMs.  More tickets than
-// the room holds, where num_ranges is in the hundreds, lie behind the call's own partials, and
-// are cleared before its launch.)
+// has a ticket.  Calls whose scratch may hold anything leave the room alone, too, so that
+// one buffer serves every kind of call.  (By default R * num_kv_heads is at most 8 a CTA:
+// 1,216 on 152 SMs.  More tickets than the room holds, where num_ranges is in the hundreds,
+// lie behind the call's own partials, and are cleared before its launch.)
 // The size is the partials, a ticket for every sequence and KV head, as callers' own formulas have
 // it, and of the room what slot 1 of the last range, in which no sequence ends and nothing
 // is written, does not pay for: with 4,096 query elements a token and more, nothing.

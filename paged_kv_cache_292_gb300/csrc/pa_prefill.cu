@@ -1069,10 +1069,13 @@ int prefill_impl(const ChunkCall& c) {
   if (workspace == nullptr) {
     rc = hold.of_stream(sc.total, c.stream, &workspace);
     if (rc != PA_OK) return rc;
-  } else if (c.workspace_bytes < sc.total) {
-    return fail(PA_ERR_WORKSPACE, "pa_prefill: workspace of %zu bytes, %zu needed", c.workspace_bytes, sc.total);
+  } else if (c.workspace_bytes < kTicketRoom + sc.total) {
+    return fail(PA_ERR_WORKSPACE, "pa_prefill: workspace of %zu bytes, %zu needed", c.workspace_bytes,
+                kTicketRoom + sc.total);
   } else if (!aligned(workspace, 256)) {
     return fail(PA_ERR_INVALID_ARG, "pa_prefill: workspace not 256-byte aligned");
+  } else {
+    workspace = static_cast<unsigned char*>(workspace) + kTicketRoom;
   }
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   prm.q = c.query;
@@ -1121,7 +1124,7 @@ extern "C" size_t pa_prefill_workspace_size(int head_size) {
   using namespace pa;
   DeviceInfo dev{};
   if ((head_size != 64 && head_size != 128) || current_device_info(&dev) != PA_OK) return 0;
-  return chunk_scratch(head_size, dev.sm_count).total;
+  return kTicketRoom + chunk_scratch(head_size, dev.sm_count).total;
 }
 
 extern "C" int pa_prefill(void* out, const void* query, const void* k_cache, const void* v_cache,

@@ -100,3 +100,52 @@ def test_many_ranges_in_a_buffer_of_any_content(num_ranges):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(graph_out, want)
+
+
+def _others(b):
+    """(size, call) of what takes scratch of any content, over a bf16 batch's pools."""
+    S, Q, H, Hk, D, _ = b.shape
+    k, v = b.pools
+    starts = torch.arange(S + 1, device="cuda", dtype=torch.int32) * Q
+    scale = D**-0.5
+    codes = [(30 * x).clamp(-127, 127).to(torch.int8) for x in (k, v)]
+    scales = [torch.full((k.shape[0], Hk, k.shape[1]), 1 / 30, device="cuda") for _ in range(2)]
+    fp8 = [x.to(torch.float8_e4m3fn).view(torch.uint8) for x in (k, v)]
+    tables = b.tables.clone()
+    tables[:, :2] = tables[0, :2]
+    rows = b.q.view(S * Q, H, D)
+    chunk, mod = binding.pa_prefill_workspace_size(D), binding.pa_decode_mod_workspace_size
+    prefix = binding.pa_decode_prefix_workspace_size(S, Q, H, Hk, D)
+    return {
+        "prefill": (chunk, lambda ws: binding.prefill(rows, k, v, b.tables, b.lens, starts, scale, workspace=ws)),
+        "prefill f32": (chunk, lambda ws: binding.prefill(rows.float(), k.float(), v.float(), b.tables, b.lens, starts, scale,
+                                                          workspace=ws)),
+        "prefill int8": (chunk, lambda ws: binding.prefill_int8(rows, *codes, *scales, b.tables, b.lens, starts, scale,
+                                                                workspace=ws)),
+        "mod": (mod(S, Q, H, Hk, D, binding.PA_BF16),
+                lambda ws: binding.decode_mod(b.q, k, v, b.tables, b.lens, scale, softcap=20.0, workspace=ws)),
+        "fp8 mod": (mod(S, Q, H, Hk, D, binding.PA_FP8_E4M3),
+                    lambda ws: binding.decode_fp8_mod(b.q, *fp8, b.tables, b.lens, scale, 1.0, 1.0, window=900, workspace=ws)),
+        "prefix": (prefix, lambda ws: binding.decode_prefix(b.q, k, v, tables[0, :2].contiguous(), tables, b.lens, scale,
+                                                            workspace=ws)),
+        "fp8 prefix": (prefix, lambda ws: binding.decode_fp8_prefix(b.q, *fp8, tables[0, :2].contiguous(), tables, b.lens,
+                                                                    scale, 1.0, 1.0, workspace=ws)),
+    }
+
+
+@pytest.mark.parametrize("other", ["prefill", "prefill f32", "prefill int8", "mod", "fp8 mod", "prefix", "fp8 prefix"])
+def test_kinds_of_calls_share_a_buffer(other):
+    """A decode's tickets survive calls whose scratch may hold anything, before and behind it in one buffer."""
+    decodes = [Batch("bf16", 4, 2, 3000, 3100), Batch("int8", 300, 1, 20, 600), Batch("fp8", 3, 4, 500, 4000)]
+    size, call = _others(Batch("bf16", 5, 2, 900, 2000))[other]
+    fresh = lambda n: torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # noqa: E731
+    want = call(fresh(size)).clone()
+    wants = [d.call(torch.zeros(d.size(), dtype=torch.uint8, device="cuda")) for d in decodes]
+    ws = torch.zeros(max(size, *(d.size() for d in decodes)), dtype=torch.uint8, device="cuda")
+    for slices in (False, True):
+        for d, w in zip(decodes, wants):
+            assert torch.equal(call(ws[:size] if slices else ws), want)
+            assert torch.equal(d.call(ws[: d.size()] if slices else ws), w)
+    with pytest.raises(binding.PagedAttnError) as e:
+        call(ws[: size // 64 // 256 * 256])
+    assert e.value.code == binding.PA_ERR_WORKSPACE
